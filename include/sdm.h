@@ -396,6 +396,73 @@ int sdm_product_key_topk_backward(const int64_t *lin, const void *grad_val, long
                                   const int *factors, int F, int k, int dtype, float *grad_raw,
                                   void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The gated delta rule: the write/read's recurrence with dense keys. Every token decays the whole
+ * Dk x Dv state of its head by one factor, retrieves with its key, delta-writes its value and
+ * reads with its query:
+ *     d = exp(g) S;  r = v - d^T k;  S = d + beta k r^T;  o = scale S^T q
+ * (the token loop of memory_ops.py's SDMWriteRead docstring with W = R = Dk, every slot selected
+ * and one log-decay a token.)
+ *   B  sequences, T  tokens (both may be 0), H  value heads, Hk  key heads (H a multiple of Hk:
+ *   value head h reads key head h / (H / Hk)), Dk, Dv  head widths, multiples of 16, Dk up to 128
+ *   and Dv up to 512; dtype SDM_F32 or SDM_BF16 of q, k, v, the readings and their gradients; the
+ *   state and the gates are float32. Strides are in elements, for (sequence, token, head); the
+ *   last dimension is contiguous. Strides of q, k, v and the gradient must be multiples of 16
+ *   bytes, their addresses 16-byte aligned; a stride of 0 (a broadcast input) is fine.
+ *
+ *   state        [B, H, Dk, Dv] float32, advanced in place
+ *   q, k         [B, T, Hk, Dk]
+ *   v            [B, T, H, Dv]
+ *   log_decay    [B, T, H] float32; below -110 (and -inf) the state is forgotten whole
+ *   beta         [B, T, H] float32
+ *   valid_tokens [B] int32, or NULL: all T. Tokens past it change nothing and none of their inputs
+ *                is used; their readings (and gradients) are 0. Clamped to [0, T].
+ *   readings     [B, T, H, Dv] contiguous, written whole
+ *   workspace    sdm_gated_delta_workspace_bytes(shape) bytes, 256-byte aligned
+ * Deterministic. Products run on the tensor cores with the float32 operands (the state, the
+ * corrections, the chunk's inverse) split into bfloat16 terms that keep float32's accuracy.
+ * Each call returns SDM_OK once queued on stream, or a negative sdm_status (nothing queued).
+ * --------------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t B, T, H, Hk, Dk, Dv;
+    int32_t dtype;
+    float scale;
+    int64_t q_stride[3], k_stride[3], v_stride[3], decay_stride[3], beta_stride[3];
+    int64_t grad_stride[3];   /* of grad_readings; the forward ignores it */
+} sdm_delta_shape;
+
+/* Workspace of sdm_gated_delta and sdm_gated_delta_save; 0 for a refused shape. */
+size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape);
+
+int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, const void *k,
+                    const void *v, const float *log_decay, const float *beta,
+                    const int32_t *valid_tokens, void *readings, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Layer norm over rows of n columns (1..16384), float32 arithmetic, y rounded once:
+ *     y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   x       device rows of n contiguous elements, x_stride >= 0 elements apart; dtype SDM_F32 or
+ *           SDM_BF16; any alignment (rows that 16-byte pieces divide are the fast ones)
+ *   weight, bias  [n] of weight_dtype (SDM_F32, or dtype), each may be NULL (1 and 0)
+ *   y       [rows, n] contiguous, dtype; may be x itself when x_stride is n
+ *   stats   [rows, 2] float32 (mean, rstd) for the backward, or NULL; 8-byte aligned
+ * rows may be 0. Deterministic. */
+int sdm_layer_norm(const void *x, long long rows, int n, long long x_stride, const void *weight,
+                   const void *bias, int weight_dtype, float eps, int dtype, void *y, float *stats,
+                   void *stream);
+
+/* Its backward. grad: rows of n elements of dtype, grad_stride apart; stats as the forward stored
+ * them; grad_x [rows, n] contiguous, dtype (may be grad itself when grad_stride is n); grad_weight
+ * and grad_bias [n] float32, summed over the rows in a fixed order, each may be NULL. workspace:
+ * sdm_layer_norm_workspace_bytes(rows, n) bytes, 256-byte aligned (unused when both are NULL). */
+size_t sdm_layer_norm_workspace_bytes(long long rows, int n);
+int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void *x,
+                            long long x_stride, long long rows, int n, const void *weight,
+                            int weight_dtype, const float *stats, int dtype, void *grad_x,
+                            float *grad_weight, float *grad_bias, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Testing aid: the number of polls after which a kernel's bounded wait for its own bulk copies
  * gives up (default 2^22, seconds at most), for calls queued after this one, process-wide;
  * polls < 1 restores the default. A kernel whose wait gives up sets SDM_ERR_TIMEOUT in the

@@ -24,7 +24,8 @@ __all__ = ["FLAG_SNAPSHOT_BF16", "FLAG_SNAPSHOT_FP8", "FLAG_TOKEN_GATE", "FLAG_S
            "sdm_write_read_noalloc", "noalloc_device_status", "profile_write_read", "workspace_bytes",
            "backward_workspace_bytes", "launch_count",
            "phase1_debug", "KERNEL_KINDS", "set_wait_limit", "product_key_topk",
-           "product_key_topk_backward",
+           "product_key_topk_backward", "gated_delta", "layer_norm", "layer_norm_save",
+           "layer_norm_backward",
            "device_status", "SdmError", "Shape", "library", "library_path", "version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +54,12 @@ class Shape(ctypes.Structure):
                 ("S", ctypes.c_int32), ("D", ctypes.c_int32), ("W", ctypes.c_int32),
                 ("R", ctypes.c_int32), ("bank_dtype", ctypes.c_int32),
                 ("slab_steps", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class _DeltaShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "H", "Hk", "Dk", "Dv", "dtype")]
+                + [("scale", ctypes.c_float)]
+                + [(n + "_stride", ctypes.c_int64 * 3) for n in ("q", "k", "v", "decay", "beta", "grad")])
 
 
 class _DeviceStatus(ctypes.Structure):
@@ -120,6 +127,18 @@ def library() -> ctypes.CDLL:
             lib.sdm_product_key_topk_backward.argtypes = [vp, vp, ll, ctypes.POINTER(ctypes.c_int),
                                                           i32, i32, i32, vp, vp]
             lib.sdm_product_key_topk_backward.restype = i32
+            dp = ctypes.POINTER(_DeltaShape)
+            lib.sdm_gated_delta_workspace_bytes.argtypes = [dp]
+            lib.sdm_gated_delta_workspace_bytes.restype = sz
+            lib.sdm_gated_delta.argtypes = [dp] + [vp] * 8 + [vp, sz, vp]
+            lib.sdm_gated_delta.restype = i32
+            lib.sdm_layer_norm.argtypes = [vp, ll, i32, ll, vp, vp, i32, ctypes.c_float, i32, vp, vp, vp]
+            lib.sdm_layer_norm.restype = i32
+            lib.sdm_layer_norm_workspace_bytes.argtypes = [ll, i32]
+            lib.sdm_layer_norm_workspace_bytes.restype = sz
+            lib.sdm_layer_norm_backward.argtypes = [vp, ll, vp, ll, ll, i32, vp, i32, vp, i32, vp,
+                                                    vp, vp, vp, sz, vp]
+            lib.sdm_layer_norm_backward.restype = i32
             lib.sdm_set_wait_limit.argtypes = [ctypes.c_longlong]
             lib.sdm_set_wait_limit.restype = ctypes.c_longlong
             lib.sdm_last_error.argtypes = []
@@ -661,4 +680,209 @@ def bank_sum(x: torch.Tensor, stream=None) -> torch.Tensor:
     with torch.cuda.device(x.device):
         _check(library().sdm_bank_sum(_ptr(x), _ptr(out), B, S, D, _dtype_code(x.dtype),
                                       _stream_ptr(stream)))
+    return out
+
+
+# ------------------------------------------------------------------------------------------
+# the gated delta rule: the write/read's recurrence with dense keys
+# ------------------------------------------------------------------------------------------
+
+def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
+    """A [B, T, heads, width] (or [B, T, heads]) input on the state's device, of any strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the state on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() == 4:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+        es = t.element_size()
+        if t.numel() and (t.data_ptr() % 16 or any(n > 1 and s * es % 16 for n, s in
+                                                   zip(t.shape[:3], t.stride()[:3]))):
+            raise ValueError(f"{name}'s address and strides must be multiples of 16 bytes")
+    return t
+
+
+def _strides(t: Optional[torch.Tensor]):
+    # a dimension of one element is never stepped along: its stride says nothing
+    return ((0, 0, 0) if t is None else
+            tuple(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])))
+
+
+def _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale, grad=None):
+    """Checks the inputs against each other; (shape struct, (B, T, H, Hk, Dk, Dv))."""
+    for t, name, dims in ((q, "q", 4), (k, "k", 4), (v, "v", 4)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if t.dim() != dims:
+            raise ValueError(f"{name} must be [B, T, heads, width]")
+    dev, dt = v.device, v.dtype
+    if dev.type != "cuda":
+        raise ValueError("q, k and v must be CUDA tensors")
+    code = _dtype_code(dt)
+    B, T, Hk, Dk = q.shape
+    H, Dv = v.shape[2:]
+    _rows(q, "q", (B, T, Hk, Dk), dt, dev)
+    _rows(k, "k", (B, T, Hk, Dk), dt, dev)
+    _rows(v, "v", (B, T, H, Dv), dt, dev)
+    _rows(log_decay, "log_decay", (B, T, H), torch.float32, dev)
+    _rows(beta, "beta", (B, T, H), torch.float32, dev)
+    if valid_tokens is not None:
+        _need(valid_tokens, "valid_tokens", (B,), torch.int32, dev)
+    if grad is not None:
+        _rows(grad, "grad_readings", (B, T, H, Dv), dt, dev)
+    if scale is None:
+        scale = Dk ** -0.5 if Dk else 1.0
+    shape = _DeltaShape(B, T, H, Hk, Dk, Dv, code, float(scale))
+    for name, t in (("q", q), ("k", k), ("v", v), ("decay", log_decay), ("beta", beta), ("grad", grad)):
+        getattr(shape, name + "_stride")[:] = _strides(t)
+    return shape, (B, T, H, Hk, Dk, Dv)
+
+
+def _bytes(n: int) -> int:
+    """A size query's answer; 0 is a refusal."""
+    if n == 0:
+        raise SdmError(-1, library().sdm_last_error().decode())
+    return int(n)
+
+
+def _scratch(workspace, nbytes: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                log_decay: torch.Tensor, beta: torch.Tensor,
+                valid_tokens: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
+                readings: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """The gated delta rule over B sequences; returns readings [B, T, H, Dv] and advances ``state``
+    ([B, H, Dk, Dv] float32, contiguous) in place. Per token and head:
+    d = exp(g) S; r = v - d^T k; S = d + beta k r^T; o = scale S^T q.
+
+    q, k [B, T, Hk, Dk] and v [B, T, H, Dv], float32 or bfloat16, any strides that are multiples of
+    16 bytes; H a multiple of Hk (value head h uses key head h // (H // Hk)); Dk (up to 128) and Dv
+    (up to 512) multiples of 16. log_decay, beta [B, T, H] float32. valid_tokens [B] int32 (None:
+    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step."""
+    shape, (B, T, H, Hk, Dk, Dv) = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
+    dev = v.device
+    _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
+    if readings is None:
+        readings = torch.empty((B, T, H, Dv), dtype=v.dtype, device=dev)
+    else:
+        _need(readings, "readings", (B, T, H, Dv), v.dtype, dev)
+    lib = library()
+    workspace = _scratch(workspace, _bytes(lib.sdm_gated_delta_workspace_bytes(ctypes.byref(shape))), dev)
+    with torch.cuda.device(dev):
+        _check(lib.sdm_gated_delta(
+            ctypes.byref(shape), _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+            _ptr(beta), _ptr(valid_tokens), _ptr(readings), _ptr(workspace), workspace.numel(),
+            _stream_ptr(stream)))
+    return readings
+
+
+# ------------------------------------------------------------------------------------------
+# layer norm
+# ------------------------------------------------------------------------------------------
+
+def _norm_rows(x: torch.Tensor, name: str):
+    """(rows, columns, row stride) of x [..., n] as rows of n contiguous elements one stride apart."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if x.device.type != "cuda" or x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name} must be a CUDA tensor of rows, [..., n] with n >= 1")
+    _dtype_code(x.dtype)
+    n = x.shape[-1]
+    rows = x.numel() // n
+    if n > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    step, span = None, 1                       # the leading dimensions have to be one run of rows
+    for size, stride in reversed(list(zip(x.shape[:-1], x.stride()[:-1]))):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * span:
+            raise ValueError(f"{name}'s rows must be one stride apart")
+        span *= size
+    return rows, n, n if step is None or rows == 0 else step
+
+
+def _norm_params(x, weight, bias):
+    n = x.shape[-1]
+    wdt = torch.float32
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            if t.dtype not in (torch.float32, x.dtype):
+                raise TypeError(f"{name} must be float32 or {x.dtype}, got {t.dtype}")
+            _need(t, name, (n,), t.dtype, x.device)
+            wdt = t.dtype
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have one dtype")
+    return _dtype_code(wdt)
+
+
+def _layer_norm(x, weight, bias, eps, out, stats, stream):
+    rows, n, step = _norm_rows(x, "x")
+    wdt = _norm_params(x, weight, bias)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _need(out, "out", x.shape, x.dtype, x.device)
+    with torch.cuda.device(x.device):
+        _check(library().sdm_layer_norm(_ptr(x), rows, n, step, _ptr(weight), _ptr(bias), wdt,
+                                        float(eps), _dtype_code(x.dtype), _ptr(out), _ptr(stats),
+                                        _stream_ptr(stream)))
+    return out
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Layer norm over x's last dimension (1..16384 columns): (x - mean) rstd weight + bias, in
+    float32, rounded once to x's dtype (float32 or bfloat16). weight and bias [n], float32 or x's
+    dtype, each optional. x's rows may be strided; the result is contiguous."""
+    return _layer_norm(x, weight, bias, eps, out, None, stream)
+
+
+def layer_norm_save(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                    bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+                    out: Optional[torch.Tensor] = None, stream=None):
+    """layer_norm that also returns what its backward needs: (y, stats [..., 2] float32)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device)
+    return _layer_norm(x, weight, bias, eps, out, stats, stream), stats
+
+
+def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                        stats: torch.Tensor, *, bias: bool = True, workspace=None,
+                        stream=None) -> Dict[str, torch.Tensor]:
+    """The backward after layer_norm_save: a dict of grad_x (x's dtype) and, where the forward had
+    them, grad_weight and (``bias``) grad_bias, float32 [n], summed over the rows in a fixed order."""
+    rows, n, step = _norm_rows(x, "x")
+    grows, gn, gstep = _norm_rows(grad, "grad")
+    if grad.shape != x.shape or grad.dtype != x.dtype or grad.device != x.device:
+        raise ValueError("grad must have x's shape, dtype and device")
+    wdt = _norm_params(x, weight, None)
+    _need(stats, "stats", tuple(x.shape[:-1]) + (2,), torch.float32, x.device)
+    out = {"grad_x": torch.empty(x.shape, dtype=x.dtype, device=x.device)}
+    if weight is not None:
+        out["grad_weight"] = torch.empty(n, dtype=torch.float32, device=x.device)
+    if bias:
+        out["grad_bias"] = torch.empty(n, dtype=torch.float32, device=x.device)
+    lib = library()
+    workspace = _scratch(workspace, _bytes(lib.sdm_layer_norm_workspace_bytes(rows, n)), x.device)
+    with torch.cuda.device(x.device):
+        _check(lib.sdm_layer_norm_backward(
+            _ptr(grad), gstep, _ptr(x), step, rows, n, _ptr(weight), wdt, _ptr(stats),
+            _dtype_code(x.dtype), _ptr(out["grad_x"]), _ptr(out.get("grad_weight")),
+            _ptr(out.get("grad_bias")), _ptr(workspace), workspace.numel(), _stream_ptr(stream)))
     return out

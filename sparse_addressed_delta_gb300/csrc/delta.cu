@@ -1,0 +1,94 @@
+// C ABI of the gated delta rule (declared and documented in include/sdm.h): argument checks and the
+// launch sequence. Everything is queued on the caller's stream; nothing is allocated and nothing
+// synchronizes.
+#include "delta_internal.cuh"
+
+namespace sdm {
+namespace {
+
+// Checks the shape; fills d. Returns SDM_OK or a refusal (message set).
+int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
+    if (!s) return set_error(SDM_ERR_INVALID, "gated delta: shape is NULL");
+    if (s->B < 0 || s->T < 0)
+        return set_error(SDM_ERR_INVALID, "gated delta: B and T must be >= 0, got %d, %d", s->B, s->T);
+    if (s->H < 1 || s->Hk < 1 || s->H % s->Hk)
+        return set_error(SDM_ERR_INVALID, "gated delta: H must be a multiple of Hk >= 1, got %d, %d",
+                         s->H, s->Hk);
+    if (s->dtype != SDM_F32 && s->dtype != SDM_BF16)
+        return set_error(SDM_ERR_INVALID, "gated delta: dtype must be SDM_F32 or SDM_BF16, got %d",
+                         s->dtype);
+    if (s->Dk < 1 || s->Dv < 1)
+        return set_error(SDM_ERR_INVALID, "gated delta: Dk and Dv must be >= 1, got %d, %d", s->Dk, s->Dv);
+    if (s->Dk % 16 || s->Dk > kDeltaMaxDk || s->Dv % 16 || s->Dv > kDeltaMaxDv)
+        return set_error(SDM_ERR_UNSUPPORTED, "gated delta: Dk (up to %d) and Dv (up to %d) must be "
+                         "multiples of 16, got %d, %d", kDeltaMaxDk, kDeltaMaxDv, s->Dk, s->Dv);
+    if (!(s->scale == s->scale))
+        return set_error(SDM_ERR_INVALID, "gated delta: scale is not a number");
+    d.B = s->B; d.T = s->T; d.H = s->H; d.Hk = s->Hk; d.Dk = s->Dk; d.Dv = s->Dv;
+    d.dtype = s->dtype;
+    d.scale = s->scale;
+    d.C = delta_chunk(s->dtype);
+    d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
+    // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
+    if ((long long)s->B * s->H * d.Nt >= (1LL << 31) || (long long)s->B * s->H * (s->Dv / 16) >= (1LL << 31))
+        return set_error(SDM_ERR_INVALID, "gated delta: B H ceil(T / %d) and B H Dv / 16 must be below 2^31", d.C);
+    const int es = s->dtype == SDM_BF16 ? 2 : 4;
+    for (int i = 0; i < 3; ++i) {
+        d.qs[i] = s->q_stride[i]; d.ks[i] = s->k_stride[i]; d.vs[i] = s->v_stride[i];
+        d.gs[i] = s->decay_stride[i]; d.bs[i] = s->beta_stride[i]; d.os[i] = s->grad_stride[i];
+        if ((d.qs[i] * es) % 16 || (d.ks[i] * es) % 16 || (d.vs[i] * es) % 16 || (d.os[i] * es) % 16)
+            return set_error(SDM_ERR_INVALID, "gated delta: the strides of q, k, v and the gradient "
+                             "must be multiples of 16 bytes");
+        if (d.qs[i] < 0 || d.ks[i] < 0 || d.vs[i] < 0 || d.gs[i] < 0 || d.bs[i] < 0 || d.os[i] < 0)
+            return set_error(SDM_ERR_INVALID, "gated delta: negative stride");
+    }
+    return SDM_OK;
+}
+
+bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
+
+int delta_check_inputs(const void *q, const void *k, const void *v, const float *g,
+                       const float *beta) {
+    if (!q || !k || !v || !g || !beta) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
+    if (off16(q) || off16(k) || off16(v))
+        return set_error(SDM_ERR_INVALID, "gated delta: q, k and v must be 16-byte aligned");
+    return SDM_OK;
+}
+
+int delta_status(cudaError_t e) {
+    if (e == cudaSuccess) return SDM_OK;
+    return set_error(SDM_ERR_CUDA, "gated delta: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" {
+
+size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape) {
+    DeltaDims d;
+    if (delta_check(shape, d) != SDM_OK) return 0;
+    return kAlign;
+}
+
+int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, const void *k,
+                    const void *v, const float *log_decay, const float *beta,
+                    const int32_t *valid_tokens, void *readings, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+    DeltaDims d;
+    int rc = delta_check(shape, d);
+    if (rc != SDM_OK) return rc;
+    if (d.B == 0 || d.T == 0) return SDM_OK;
+    rc = delta_check_inputs(q, k, v, log_decay, beta);
+    if (rc != SDM_OK) return rc;
+    if (!state || !readings) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
+    if (off16(state) || off16(readings))
+        return set_error(SDM_ERR_INVALID, "gated delta: the state and the readings must be 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
+    return delta_status(launch_delta_step(d, in, state, readings, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,168 @@
+// Shared by the gated delta rule's kernels (delta*.cu): sizes, the chunk workspace, bf16 tensor-core
+// fragments and the split of a float into bfloat16 terms.
+#pragma once
+
+#include "sdm_internal.cuh"
+
+namespace sdm {
+
+constexpr int kDeltaMaxDk = 128, kDeltaMaxDv = 512;
+constexpr int kDeltaStepTokens = 16;     // up to this many tokens take the token-by-token kernel
+// A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten
+// whole, and -inf (a hard reset) stays out of the running sums' differences.
+constexpr float kDeltaMinDecay = -110.f;
+
+struct DeltaDims {
+    int B, T, H, Hk, Dk, Dv;
+    int C, Nt;                           // chunk length, chunks a sequence
+    int dtype;
+    float scale;
+    long long qs[3], ks[3], vs[3], gs[3], bs[3], os[3];   // element strides of (b, t, h)
+};
+
+struct DeltaIn {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const int32_t *valid;                // may be null
+};
+
+// bfloat16 operands of the products: planes whose sum is the input (one for bfloat16 inputs, three
+// for float32 inputs, split by launch_delta_split into contiguous [B, T, heads, D])
+struct DeltaPlanes {
+    const __nv_bfloat16 *p;
+    long long plane;                     // elements from one plane to the next
+    long long s[3];                      // element strides of (b, t, h)
+};
+
+// Per chunk and head, written by the chunk-local kernel (k_delta_local) for the scans:
+//   x   [3][C][C] bfloat16 planes of (I + diag(beta) A)^-1
+//   p   [PP][C][C] planes of the decayed scale q k^T
+//   aux [3][C] float: exp(L_t), exp(L_C - L_t), beta_t
+// The plane images are stored as shared memory holds them (16-byte pieces of a row permuted by
+// delta_swz), so the scans copy them as they are. Blocks above the diagonal are never written and
+// never read.
+struct DeltaLocal {
+    unsigned char *x, *p;
+    float *aux;
+};
+
+__host__ __device__ constexpr int delta_chunk(int dtype) { return dtype == SDM_BF16 ? 64 : 32; }
+__host__ __device__ constexpr int delta_p_planes(int dtype) { return dtype == SDM_BF16 ? 2 : 3; }
+
+inline size_t delta_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+inline size_t delta_chunks(const DeltaDims &d) { return (size_t)d.B * d.H * d.Nt; }
+inline size_t delta_x_bytes(const DeltaDims &d) { return (size_t)3 * d.C * d.C * 2; }
+inline size_t delta_p_bytes(const DeltaDims &d) {
+    return (size_t)delta_p_planes(d.dtype) * d.C * d.C * 2;
+}
+
+cudaError_t launch_delta_step(const DeltaDims &d, const DeltaIn &in, float *state, void *o,
+                              cudaStream_t st);
+cudaError_t launch_delta_split(const DeltaDims &d, const void *x, const long long *s, int heads,
+                               int D, __nv_bfloat16 *planes, cudaStream_t st);
+cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
+                               const DeltaPlanes &k, const DeltaLocal &w, cudaStream_t st);
+// snap [B, H, Nt, Dk, Dv] the state at each chunk's start, u [B, H, Nt, C, Dv]; null unless saving
+cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
+                              const DeltaPlanes &k, const DeltaLocal &w, float *state, void *o,
+                              float *snap, float *u, cudaStream_t st);
+
+// ---------------------------------------------------------------------------------------
+// device helpers
+// ---------------------------------------------------------------------------------------
+
+__device__ __forceinline__ int delta_valid(const int32_t *valid, int b, int T) {
+    const int v = valid ? valid[b] : T;
+    return v < 0 ? 0 : (v > T ? T : v);
+}
+
+__device__ __forceinline__ float delta_decay(float g) { return g < kDeltaMinDecay ? kDeltaMinDecay : g; }
+
+// byte offset of 16-byte piece `c` of row `r` in a tile with rows of PITCH bytes: the pieces of 8
+// consecutive rows at one column fall into different banks
+template <int PITCH>
+__device__ __forceinline__ unsigned delta_swz(int r, int c) {
+    if constexpr (PITCH >= 128) return r * PITCH + ((c ^ (r & 7)) << 4);
+    else if constexpr (PITCH == 64) return r * PITCH + ((c ^ ((r >> 1) & 3)) << 4);
+    else return r * PITCH + ((c ^ ((r >> 2) & 1)) << 4);
+}
+
+__device__ __forceinline__ void cp_async16_zfill(unsigned dst, const void *src, bool live) {
+    const int n = live ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(unsigned (&r)[4], unsigned addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Fragments of a tile in shared memory (rows of PITCH bytes, pieces permuted by delta_swz):
+// rows r0.., bfloat16 columns c0.. (multiples of 8). ldmatrix lane i addresses row i % 8 of 8 x 8
+// block i / 8.
+//   frag_rc: blocks (r, c), (r + 8, c), (r, c + 8), (r + 8, c + 8)
+//     plain: an A operand of 16 rows x 16 of K;  transposed: two 8-column B operands with K = rows
+//   frag_cr: blocks (r, c), (r, c + 8), (r + 8, c), (r + 8, c + 8)
+//     plain: two 8-column B operands with N = rows, K = columns; transposed: an A operand, M = columns
+template <int PITCH>
+__device__ __forceinline__ unsigned frag_rc(unsigned base, int r0, int c0, int lane) {
+    return base + delta_swz<PITCH>(r0 + (lane & 15), (c0 >> 3) + (lane >> 4));
+}
+template <int PITCH>
+__device__ __forceinline__ unsigned frag_cr(unsigned base, int r0, int c0, int lane) {
+    return base + delta_swz<PITCH>(r0 + (lane & 7) + ((lane >> 4) << 3), (c0 >> 3) + ((lane >> 3) & 1));
+}
+
+// c += a b, one 16 x 8 x 16 bfloat16 product with float32 sums
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const unsigned (&a)[4], unsigned b0,
+                                         unsigned b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float x0, float x1) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+__device__ __forceinline__ float lo_f32(unsigned h) { return __uint_as_float(h << 16); }
+__device__ __forceinline__ float hi_f32(unsigned h) { return __uint_as_float(h & 0xffff0000u); }
+
+// x0, x1 as sums of N bfloat16 terms each (8 bits a term: three keep float32's 24 bits)
+template <int N>
+__device__ __forceinline__ void split_bf16(float x0, float x1, unsigned (&p)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        p[i] = pack_bf16(x0, x1);
+        if (i + 1 < N) {
+            x0 -= lo_f32(p[i]);
+            x1 -= hi_f32(p[i]);
+        }
+    }
+}
+
+// A operand (K step ks) of the transposed product from accumulators acc[tile][4] whose columns are
+// its K: N planes
+template <int N, int TILES>
+__device__ __forceinline__ void split_frag(const float (&acc)[TILES][4], int ks,
+                                           unsigned (&a)[N][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        unsigned p[N];
+        split_bf16<N>(acc[2 * ks + (i >> 1)][2 * (i & 1)], acc[2 * ks + (i >> 1)][2 * (i & 1) + 1], p);
+#pragma unroll
+        for (int s = 0; s < N; ++s) a[s][i] = p[s];
+    }
+}
+
+}  // namespace sdm

@@ -1,0 +1,493 @@
+// Layer norm over the last dimension, forward and backward: the norm before a memory layer (rows
+// of the model's width) and on its readings (rows of one head's width).
+//   mean = sum(x) / n;  rstd = 1 / sqrt(sum((x - mean)^2) / n + eps);  xhat = (x - mean) rstd
+//   y  = xhat w + b
+//   dx = rstd (w dy - mean(w dy) - xhat mean(w dy xhat));  dw = sum_rows dy xhat;  db = sum_rows dy
+// All arithmetic is float32; y and dx are rounded once. The variance is the sum of squares around
+// the mean, from the row kept in registers: no cancellation, and x is read once.
+//
+// Bound by memory: a row is read once, held in registers and written once. A row belongs to TPR
+// threads (a part of a warp up to 32, else the whole block), each with E elements as whole vectors
+// (16 bytes when the row length, its stride and the pointers allow it, else 4 or one element).
+// Blocks stay resident and walk over the rows with the weights in registers, the next row's loads
+// in flight while the current one is reduced. The backward's column sums stay in the same threads
+// over all the rows of a block (in shared memory above 8192 columns), go to one partial per block,
+// and a second kernel adds the partials in block order: no atomics, so results are reproducible.
+#include "sdm_internal.cuh"
+
+namespace sdm {
+namespace {
+
+constexpr int kNormBlock = 128;        // threads of a block whose rows belong to parts of warps
+constexpr int kNormMaxCols = 16384;
+constexpr int kNormRegCols = 8192;     // backward: column sums in registers up to this width
+constexpr int kNormColThreads = 32, kNormColSlices = 8;
+
+template <int BYTES> struct VecOf;
+template <> struct VecOf<16> { using type = uint4; };
+template <> struct VecOf<4> { using type = unsigned; };
+template <> struct VecOf<2> { using type = unsigned short; };
+
+template <typename T, int VEC>
+using Vec = typename VecOf<VEC * (int)sizeof(T)>::type;
+
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Vec<T, VEC> &r, float *o) {
+    const T *e = reinterpret_cast<const T *>(&r);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = to_f32(e[j]);
+}
+
+// the thread's NV vectors of one row (zero past the row's end, or when the row is not live)
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void load_row(const T *row, bool live, int t, int tpr, int n,
+                                         Vec<T, VEC> (&r)[NV]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        r[i] = Vec<T, VEC>{};
+        if (live && c < n) r[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(row + c));
+    }
+}
+
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_row(T *row, int t, int tpr, int n, const float *v) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        if (c < n) {
+            float o[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) o[j] = v[i * VEC + j];
+            store_vec<T, VEC>(row + c, o);
+        }
+    }
+}
+
+// per-column parameters (float32, or the row's type), `fill` where there are none
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void load_cols(const void *p, bool f32, float fill, int t, int tpr,
+                                          int n, float *o) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const int c = (i * tpr + t) * VEC + j;
+            o[i * VEC + j] = !p || c >= n ? fill
+                             : f32 ? static_cast<const float *>(p)[c]
+                                   : to_f32(static_cast<const T *>(p)[c]);
+        }
+}
+
+// Sums of M values over the threads of one row, returned to all of them. BLOCK: over the block,
+// warps added in warp order (`red` holds 2 * M * 32 floats, its halves used in turn so that one
+// barrier a call is enough).
+template <bool BLOCK, int M>
+__device__ __forceinline__ void row_sum(float (&v)[M], int tpr, float *red, int &turn) {
+    const int width = BLOCK ? 32 : tpr;
+    for (int o = width >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+    if constexpr (BLOCK) {
+        float *r = red + turn * M * 32;
+        turn ^= 1;
+        const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int m = 0; m < M; ++m) r[m * 32 + warp] = v[m];
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            float s = 0.f;
+            for (int w = 0; w < nw; ++w) s += r[m * 32 + w];
+            v[m] = s;
+        }
+    }
+}
+
+template <typename T, int VEC, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
+    k_norm(const T *x, long long xs, long long rows, int n, int tpr, const void *w, const void *b,
+           bool wf32, float eps, T *y, float2 *stats) {
+    constexpr int E = VEC * NV;
+    __shared__ float red[2 * 32];
+    int turn = 0;
+    const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr;
+    const int rpb = BLOCK ? 1 : kNormBlock / tpr;
+    const long long step = (long long)gridDim.x * rpb;
+    float wv[E], bv[E];
+    load_cols<T, VEC, NV>(w, wf32, 1.f, t, tpr, n, wv);
+    load_cols<T, VEC, NV>(b, wf32, 0.f, t, tpr, n, bv);
+    Vec<T, VEC> next[NV];
+    long long base = (long long)blockIdx.x * rpb;
+    load_row<T, VEC, NV>(x + (base + sub) * xs, base + sub < rows, t, tpr, n, next);
+    for (; base < rows; base += step) {
+        const long long row = base + sub;
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) unpack<T, VEC>(next[i], v + i * VEC);
+        load_row<T, VEC, NV>(x + (row + step) * xs, row + step < rows, t, tpr, n, next);
+        float s[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < E; ++j) s[0] += v[j];
+        row_sum<BLOCK, 1>(s, tpr, red, turn);
+        const float mean = s[0] / (float)n;
+        s[0] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * tpr + t) * VEC < n)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float d = v[i * VEC + j] - mean;
+                    v[i * VEC + j] = d;
+                    s[0] = fmaf(d, d, s[0]);
+                }
+        row_sum<BLOCK, 1>(s, tpr, red, turn);
+        const float rstd = 1.f / sqrtf(s[0] / (float)n + eps);
+        if (row < rows) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = fmaf(v[j] * rstd, wv[j], bv[j]);
+            store_row<T, VEC, NV>(y + row * n, t, tpr, n, v);
+            if (stats && t == 0) stats[row] = make_float2(mean, rstd);
+        }
+    }
+}
+
+// part [blocks][2][n]: the block's column sums of dy xhat and of dy
+template <typename T, int VEC, int NV, bool BLOCK, bool WIDE>
+__global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
+    k_norm_bwd(const T *dy, long long ds, const T *x, long long xs, long long rows, int n, int tpr,
+               const void *w, bool wf32, const float2 *stats, T *dx, float *part) {
+    constexpr int E = VEC * NV;
+    extern __shared__ float cols[];          // WIDE: the column sums [2][n]; else see the end
+    __shared__ float red[2 * 2 * 32];
+    int turn = 0;
+    const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr;
+    const int rpb = BLOCK ? 1 : kNormBlock / tpr;
+    const long long step = (long long)gridDim.x * rpb;
+    float wv[WIDE ? 1 : E], aw[WIDE ? 1 : E], ab[WIDE ? 1 : E];
+    if constexpr (WIDE) {
+        for (int c = threadIdx.x; c < 2 * n; c += blockDim.x) cols[c] = 0.f;
+        __syncthreads();
+    } else {
+        load_cols<T, VEC, NV>(w, wf32, 1.f, t, tpr, n, wv);
+#pragma unroll
+        for (int j = 0; j < E; ++j) aw[j] = ab[j] = 0.f;
+    }
+    Vec<T, VEC> nx[NV], ny[NV];
+    float2 ns = make_float2(0.f, 0.f);
+    long long base = (long long)blockIdx.x * rpb;
+    auto fetch = [&](long long row) {
+        const bool live = row < rows;
+        load_row<T, VEC, NV>(x + row * xs, live, t, tpr, n, nx);
+        load_row<T, VEC, NV>(dy + row * ds, live, t, tpr, n, ny);
+        ns = live ? __ldg(stats + row) : make_float2(0.f, 0.f);
+    };
+    fetch(base + sub);
+    for (; base < rows; base += step) {
+        const long long row = base + sub;
+        const float mean = ns.x, rstd = ns.y;
+        float h[E], g[E], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unpack<T, VEC>(nx[i], h + i * VEC);
+            unpack<T, VEC>(ny[i], g + i * VEC);
+        }
+        fetch(row + step);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c0 = (i * tpr + t) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int e = i * VEC + j;
+                // past the row's end x and dy are 0, and dy = 0 keeps the sums clean
+                h[e] = (h[e] - mean) * rstd;
+                if constexpr (WIDE) {
+                    if (c0 + j < n) {
+                        cols[c0 + j] = fmaf(g[e], h[e], cols[c0 + j]);
+                        cols[n + c0 + j] += g[e];
+                        g[e] *= !w ? 1.f : wf32 ? static_cast<const float *>(w)[c0 + j]
+                                                : to_f32(static_cast<const T *>(w)[c0 + j]);
+                    }
+                } else {
+                    aw[e] = fmaf(g[e], h[e], aw[e]);
+                    ab[e] += g[e];
+                    g[e] *= wv[e];
+                }
+                s[0] += g[e];
+                s[1] = fmaf(g[e], h[e], s[1]);
+            }
+        }
+        row_sum<BLOCK, 2>(s, tpr, red, turn);
+        const float c1 = s[0] / (float)n, c2 = s[1] / (float)n;
+        if (row < rows) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) g[j] = rstd * (g[j] - c1 - h[j] * c2);
+            store_row<T, VEC, NV>(dx + row * n, t, tpr, n, g);
+        }
+    }
+    if (!part) return;
+    float *out = part + (size_t)blockIdx.x * 2 * n;
+    if constexpr (WIDE) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * n; c += blockDim.x) out[c] = cols[c];
+    } else {
+        // the block's row groups, added in their order: cols [2][groups][tpr * E]
+        const int wide = tpr * E;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int c = (i * tpr + t) * VEC + j, e = i * VEC + j;
+                if constexpr (BLOCK) {
+                    if (c < n) {
+                        out[c] = aw[e];
+                        out[n + c] = ab[e];
+                    }
+                } else {
+                    cols[sub * wide + c] = aw[e];
+                    cols[(rpb + sub) * wide + c] = ab[e];
+                }
+            }
+        if constexpr (!BLOCK) {
+            __syncthreads();
+            for (int c = threadIdx.x; c < n; c += kNormBlock) {
+                float a = 0.f, d = 0.f;
+                for (int r = 0; r < rpb; ++r) {
+                    a += cols[r * wide + c];
+                    d += cols[(rpb + r) * wide + c];
+                }
+                out[c] = a;
+                out[n + c] = d;
+            }
+        }
+    }
+}
+
+// column sums of the blocks' partials, in a fixed order: kNormColSlices runs of blocks, then them
+__global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
+    k_norm_cols(const float *part, int parts, int n, float *dw, float *db) {
+    __shared__ float sh[kNormColSlices][kNormColThreads];
+    const int tx = threadIdx.x % kNormColThreads, ty = threadIdx.x / kNormColThreads;
+    const int c = blockIdx.x * kNormColThreads + tx;     // over [2][n]
+    float s = 0.f;
+    if (c < 2 * n)
+        for (int p = ty; p < parts; p += kNormColSlices) s += part[(size_t)p * 2 * n + c];
+    sh[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < 2 * n) {
+        for (int k = 1; k < kNormColSlices; ++k) s += sh[k][tx];
+        if (c < n) {
+            if (dw) dw[c] = s;
+        } else if (db) {
+            db[c - n] = s;
+        }
+    }
+}
+
+struct NormGeom {
+    int vec;        // elements per vector
+    int e;          // elements per thread
+    int tpr;        // threads per row
+    bool block;     // a row belongs to a whole block
+    int threads, rpb;
+};
+
+// 16 elements a thread keep enough loads in flight with the weights and sums in registers; the
+// forward (no sums) takes 32 once a block of 128 threads would not cover the row with 16.
+NormGeom norm_geom(int n, int vec, bool backward) {
+    NormGeom g;
+    g.vec = vec;
+    g.e = !backward && n > 16 * kNormBlock ? 32 : 16;
+    const int need = (n + g.e - 1) / g.e;
+    if (need <= 32) {
+        g.tpr = 1;
+        while (g.tpr < need) g.tpr *= 2;
+        g.block = false;
+        g.threads = kNormBlock;
+        g.rpb = kNormBlock / g.tpr;
+    } else {
+        g.tpr = (need + 31) / 32 * 32;
+        g.block = true;
+        g.threads = g.tpr;
+        g.rpb = 1;
+    }
+    return g;
+}
+
+// blocks that fill the card once, at most one per row group
+int norm_blocks(const NormGeom &g, long long rows, bool backward) {
+    const int per_sm = g.threads >= 1024 ? 1 : (backward ? 768 : 1024) / g.threads;
+    const long long most = (long long)kRefSms * (per_sm < 1 ? 1 : per_sm);
+    const long long need = (rows + g.rpb - 1) / g.rpb;
+    return (int)(need < most ? need : most);
+}
+
+// the widest vector that divides the rows, their strides (in elements) and the addresses
+int norm_vec(int es, int n, long long s0, long long s1, const void *a, const void *b,
+             const void *c) {
+    const uintptr_t any = (uintptr_t)a | (uintptr_t)b | (uintptr_t)c | (uintptr_t)((long long)n * es) |
+                          (uintptr_t)(s0 * es) | (uintptr_t)(s1 * es);
+    if (any % 16 == 0) return 16 / es;
+    return any % 4 == 0 ? 4 / es : 1;
+}
+
+int norm_check(const char *what, const void *x, long long rows, int n, long long xs, int wdtype,
+               int dtype) {
+    if (dtype != SDM_F32 && dtype != SDM_BF16)
+        return set_error(SDM_ERR_INVALID, "%s: dtype must be SDM_F32 or SDM_BF16", what);
+    if (wdtype != SDM_F32 && wdtype != dtype)
+        return set_error(SDM_ERR_INVALID, "%s: the weight's dtype must be SDM_F32 or the rows'", what);
+    if (rows < 0 || n < 1 || xs < 0)
+        return set_error(SDM_ERR_INVALID, "%s: rows must be >= 0, columns >= 1 and the row stride "
+                         ">= 0, got %lld, %d, %lld", what, rows, n, xs);
+    if (n > kNormMaxCols)
+        return set_error(SDM_ERR_UNSUPPORTED, "%s: at most %d columns, got %d", what, kNormMaxCols, n);
+    if (rows > 0 && !x) return set_error(SDM_ERR_INVALID, "%s: NULL pointer", what);
+    return SDM_OK;
+}
+
+int norm_status(cudaError_t e) {
+    if (e == cudaSuccess) return SDM_OK;
+    return set_error(SDM_ERR_CUDA, "layer norm: %s", cudaGetErrorString(e));
+}
+
+template <typename T, int VEC, int E>
+void norm_launch(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
+                 const void *b, bool wf32, float eps, T *y, float2 *stats, cudaStream_t st) {
+    const int grid = norm_blocks(g, rows, false);
+    if (g.block)
+        k_norm<T, VEC, E / VEC, true><<<grid, g.threads, 0, st>>>(x, xs, rows, n, g.tpr, w, b, wf32,
+                                                                 eps, y, stats);
+    else
+        k_norm<T, VEC, E / VEC, false><<<grid, g.threads, 0, st>>>(x, xs, rows, n, g.tpr, w, b,
+                                                                  wf32, eps, y, stats);
+}
+
+template <typename T>
+void norm_forward(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
+                  const void *b, bool wf32, float eps, T *y, float2 *stats, cudaStream_t st) {
+    constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
+    auto go = [&](auto vec) {
+        constexpr int VEC = decltype(vec)::value;
+        if (g.e == 32) norm_launch<T, VEC, 32>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
+        else norm_launch<T, VEC, 16>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
+    };
+    if (g.vec == V16) return go(std::integral_constant<int, V16>{});
+    if constexpr (V4 > 1)
+        if (g.vec == V4) return go(std::integral_constant<int, V4>{});
+    go(std::integral_constant<int, 1>{});
+}
+
+template <typename T, int VEC>
+void norm_bwd_launch(const NormGeom &g, int grid, const T *dy, long long ds, const T *x,
+                     long long xs, long long rows, int n, const void *w, bool wf32,
+                     const float2 *stats, T *dx, float *part, cudaStream_t st) {
+    constexpr int NV = 16 / VEC;
+    if (n > kNormRegCols) {
+        auto k = k_norm_bwd<T, VEC, NV, true, true>;
+        const size_t smem = (size_t)2 * n * 4;
+        set_kernel_smem(k, smem);
+        k<<<grid, g.threads, smem, st>>>(dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
+    } else if (g.block) {
+        k_norm_bwd<T, VEC, NV, true, false><<<grid, g.threads, 0, st>>>(
+            dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
+    } else {
+        const size_t smem = (size_t)2 * kNormBlock * 16 * 4;
+        k_norm_bwd<T, VEC, NV, false, false><<<grid, g.threads, smem, st>>>(
+            dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
+    }
+}
+
+template <typename T>
+void norm_backward(const NormGeom &g, int grid, const T *dy, long long ds, const T *x, long long xs,
+                   long long rows, int n, const void *w, bool wf32, const float2 *stats, T *dx,
+                   float *part, cudaStream_t st) {
+    constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
+    if (g.vec == V16)
+        return norm_bwd_launch<T, V16>(g, grid, dy, ds, x, xs, rows, n, w, wf32, stats, dx, part, st);
+    if constexpr (V4 > 1)
+        if (g.vec == V4)
+            return norm_bwd_launch<T, V4>(g, grid, dy, ds, x, xs, rows, n, w, wf32, stats, dx, part, st);
+    norm_bwd_launch<T, 1>(g, grid, dy, ds, x, xs, rows, n, w, wf32, stats, dx, part, st);
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" {
+
+int sdm_layer_norm(const void *x, long long rows, int n, long long x_stride, const void *weight,
+                   const void *bias, int weight_dtype, float eps, int dtype, void *y, float *stats,
+                   void *stream) {
+    const int rc = norm_check("layer norm", x, rows, n, x_stride, weight_dtype, dtype);
+    if (rc != SDM_OK) return rc;
+    if (!(eps >= 0.f)) return set_error(SDM_ERR_INVALID, "layer norm: eps must be >= 0");
+    if (rows == 0) return SDM_OK;
+    if (!y) return set_error(SDM_ERR_INVALID, "layer norm: NULL pointer");
+    const NormGeom g = norm_geom(n, norm_vec(dtype == SDM_BF16 ? 2 : 4, n, x_stride, x_stride, x, y, y), false);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto s2 = reinterpret_cast<float2 *>(stats);
+    const bool wf32 = weight_dtype == SDM_F32;
+    if (dtype == SDM_BF16)
+        norm_forward(g, static_cast<const __nv_bfloat16 *>(x), x_stride, rows, n, weight, bias, wf32,
+                     eps, static_cast<__nv_bfloat16 *>(y), s2, st);
+    else
+        norm_forward(g, static_cast<const float *>(x), x_stride, rows, n, weight, bias, wf32, eps,
+                     static_cast<float *>(y), s2, st);
+    return norm_status(cudaGetLastError());
+}
+
+size_t sdm_layer_norm_workspace_bytes(long long rows, int n) {
+    if (rows < 0 || n < 1 || n > kNormMaxCols) {
+        set_error(SDM_ERR_INVALID, "layer norm: bad sizes %lld, %d", rows, n);
+        return 0;
+    }
+    const NormGeom g = norm_geom(n, 1, true);
+    const size_t blocks = rows ? (size_t)norm_blocks(g, rows, true) : 1;
+    return (blocks * 2 * n * 4 + kAlign - 1) / kAlign * kAlign;
+}
+
+int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void *x,
+                            long long x_stride, long long rows, int n, const void *weight,
+                            int weight_dtype, const float *stats, int dtype, void *grad_x,
+                            float *grad_weight, float *grad_bias, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    int rc = norm_check("layer norm backward", x, rows, n, x_stride, weight_dtype, dtype);
+    if (rc != SDM_OK) return rc;
+    if (grad_stride < 0)
+        return set_error(SDM_ERR_INVALID, "layer norm backward: the gradient's row stride must be "
+                         ">= 0, got %lld", grad_stride);
+    if (rows > 0 && (!grad || !stats || !grad_x))
+        return set_error(SDM_ERR_INVALID, "layer norm backward: NULL pointer");
+    const bool sums = grad_weight || grad_bias;
+    if (sums && (!workspace || workspace_bytes < sdm_layer_norm_workspace_bytes(rows, n) ||
+                 (uintptr_t)workspace % kAlign))
+        return set_error(SDM_ERR_WORKSPACE, "layer norm backward: workspace NULL, too small or not "
+                         "%zu-byte aligned", (size_t)kAlign);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const NormGeom g = norm_geom(
+        n, norm_vec(dtype == SDM_BF16 ? 2 : 4, n, x_stride, grad_stride, x, grad, grad_x), true);
+    const int grid = rows ? norm_blocks(g, rows, true) : 0;
+    float *part = sums ? static_cast<float *>(workspace) : nullptr;
+    auto s2 = reinterpret_cast<const float2 *>(stats);
+    const bool wf32 = weight_dtype == SDM_F32;
+    if (rows > 0) {
+        if (dtype == SDM_BF16)
+            norm_backward(g, grid, static_cast<const __nv_bfloat16 *>(grad), grad_stride,
+                          static_cast<const __nv_bfloat16 *>(x), x_stride, rows, n, weight, wf32, s2,
+                          static_cast<__nv_bfloat16 *>(grad_x), part, st);
+        else
+            norm_backward(g, grid, static_cast<const float *>(grad), grad_stride,
+                          static_cast<const float *>(x), x_stride, rows, n, weight, wf32, s2,
+                          static_cast<float *>(grad_x), part, st);
+    }
+    if (sums)
+        k_norm_cols<<<(2 * n + kNormColThreads - 1) / kNormColThreads, kNormColThreads * kNormColSlices,
+                      0, st>>>(part, grid, n, grad_weight, grad_bias);
+    return norm_status(cudaGetLastError());
+}
+
+}  // extern "C"
