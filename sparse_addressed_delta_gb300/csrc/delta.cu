@@ -60,6 +60,70 @@ int delta_status(cudaError_t e) {
     return set_error(SDM_ERR_CUDA, "gated delta: %s", cudaGetErrorString(e));
 }
 
+bool by_token(const DeltaDims &d) { return d.T <= kDeltaStepTokens; }
+
+// Where the chunk form's buffers lie in a workspace; `bytes` is their end.
+struct DeltaLayout {
+    size_t q, k, x, p, aux, bytes;       // q, k: the planes of float32 inputs
+};
+
+DeltaLayout delta_layout(const DeltaDims &d) {
+    DeltaLayout l{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += delta_up(bytes);
+        return here;
+    };
+    const size_t tok = d.dtype == SDM_F32 ? (size_t)d.B * d.T * d.Hk * d.Dk * 3 * 2 : 0;
+    l.q = take(tok);
+    l.k = take(tok);
+    l.x = take(delta_chunks(d) * delta_x_bytes(d));
+    l.p = take(delta_chunks(d) * delta_p_bytes(d));
+    l.aux = take(delta_chunks(d) * 3 * d.C * 4);
+    l.bytes = at;
+    return l;
+}
+
+DeltaPlanes delta_planes(const DeltaDims &d, const void *x, const long long *s, unsigned char *split) {
+    DeltaPlanes p;
+    if (d.dtype == SDM_BF16) {
+        p.p = static_cast<const __nv_bfloat16 *>(x);
+        p.plane = 0;
+        for (int i = 0; i < 3; ++i) p.s[i] = s[i];
+    } else {
+        p.p = reinterpret_cast<const __nv_bfloat16 *>(split);
+        p.plane = (long long)d.B * d.T * d.Hk * d.Dk;
+        p.s[0] = (long long)d.T * d.Hk * d.Dk;
+        p.s[1] = (long long)d.Hk * d.Dk;
+        p.s[2] = d.Dk;
+    }
+    return p;
+}
+
+// the chunk-local work: planes of float32 keys and queries, X, P and the gates
+cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, unsigned char *ws, DeltaPlanes &q,
+                        DeltaPlanes &k, DeltaLocal &w, cudaStream_t st) {
+    const DeltaLayout l = delta_layout(d);
+    q = delta_planes(d, in.q, d.qs, ws + l.q);
+    k = delta_planes(d, in.k, d.ks, ws + l.k);
+    w = DeltaLocal{ws + l.x, ws + l.p, reinterpret_cast<float *>(ws + l.aux)};
+    if (d.dtype == SDM_F32) {
+        cudaError_t e = launch_delta_split(d, in.q, d.qs, d.Hk, d.Dk, const_cast<__nv_bfloat16 *>(q.p), st);
+        if (e == cudaSuccess)
+            e = launch_delta_split(d, in.k, d.ks, d.Hk, d.Dk, const_cast<__nv_bfloat16 *>(k.p), st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_delta_local(d, in, q, k, w, st);
+}
+
+int delta_check_ws(const void *ws, size_t have, size_t need) {
+    if (!ws || have < need || (uintptr_t)ws % kAlign)
+        return set_error(SDM_ERR_WORKSPACE, "gated delta: workspace NULL, too small (%zu of %zu bytes) "
+                         "or not %zu-byte aligned", have, need, (size_t)kAlign);
+    return SDM_OK;
+}
+
 }  // namespace
 }  // namespace sdm
 
@@ -70,7 +134,7 @@ extern "C" {
 size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
     if (delta_check(shape, d) != SDM_OK) return 0;
-    return kAlign;
+    return by_token(d) ? kAlign : delta_layout(d).bytes + kAlign;
 }
 
 int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, const void *k,
@@ -88,7 +152,15 @@ int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, c
         return set_error(SDM_ERR_INVALID, "gated delta: the state and the readings must be 16-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
-    return delta_status(launch_delta_step(d, in, state, readings, st));
+    if (by_token(d)) return delta_status(launch_delta_step(d, in, state, readings, st));
+    rc = delta_check_ws(workspace, workspace_bytes, delta_layout(d).bytes);
+    if (rc != SDM_OK) return rc;
+    DeltaPlanes qp, kp;
+    DeltaLocal w;
+    cudaError_t e = delta_local(d, in, static_cast<unsigned char *>(workspace), qp, kp, w, st);
+    if (e == cudaSuccess)
+        e = launch_delta_scan(d, in, qp, kp, w, state, readings, nullptr, nullptr, st);
+    return delta_status(e);
 }
 
 }  // extern "C"

@@ -1,0 +1,588 @@
+// The gated delta rule in chunks of C tokens. With S0 the state at a chunk's start, L the running
+// sum of the log-decays inside the chunk (inclusive) and G = e^L:
+//   A[t,s] = k_t . k_s e^{L_t - L_s}  (s < t);   P[t,s] = scale q_t . k_s e^{L_t - L_s}  (s <= t)
+//   X = (I + diag(beta) A)^-1
+//   w = v - G (K S0);   u = X (beta w);   o = scale G (Q S0) + P u;   S1 = G_C S0 + K^T (e^{L_C - L} u)
+// X, P and the gates need no state: k_delta_local computes them for all chunks at once. k_delta_scan
+// then walks over each head's chunks.
+//
+// The scan keeps everything transposed, [Dv] x [tokens or Dk]: a warp owns 16 of the state's columns
+// as the accumulators of m16n8k16 products, and the accumulators of one product are, in place, the A
+// operand of the next (S^T -> (K S)^T -> u^T -> S^T). Columns never mix, so warps share only the
+// loads of K, Q, X and P, and no value crosses a warp in the whole recurrence.
+//
+// Accuracy: K and Q are bfloat16 (or three bfloat16 planes of a float32 input); S, the corrections w
+// and u, and X are float32 and enter products as three bfloat16 terms, the products of terms below
+// 2^-24 of the result left out. The chunk's update of the state is summed by itself and added to the
+// decayed state in float32, outside the tensor cores' accumulation.
+#include "delta_internal.cuh"
+
+namespace sdm {
+namespace {
+
+__device__ __forceinline__ bool plane_pair(int a, int b, int most) { return a + b < most; }
+
+// K or Q planes of a chunk's `nt` live tokens into tiles [KP][C][DKP], zero elsewhere
+template <int KP, int DKP, int C, int THREADS>
+__device__ __forceinline__ void load_tokens(unsigned dst, const DeltaPlanes &x, long long base,
+                                            int Dk, int nt, int tid) {
+    constexpr int PC = DKP / 8;
+    for (int i = tid; i < KP * C * PC; i += THREADS) {
+        const int c = i % PC, r = (i / PC) % C, pl = i / (PC * C);
+        const bool live = r < nt && c * 8 < Dk;
+        const __nv_bfloat16 *src = x.p + pl * x.plane + base + (live ? r * x.s[1] + c * 8 : 0);
+        cp_async16_zfill(dst + pl * (C * DKP * 2) + delta_swz<DKP * 2>(r, c), src, live);
+    }
+}
+
+template <int KP, int DKP, int C>
+struct LocalSmem {
+    static constexpr int TILE = C * DKP * 2, NP = C + 4;
+    static constexpr int Q = KP * TILE, N = 2 * KP * TILE, X = N + C * NP * 4, G = X + C * NP * 4;
+    static constexpr int BYTES = G + 3 * C * 4;
+};
+
+// One block per chunk and head, one warp per 16 tokens. The products K K^T and Q K^T (blocks on and
+// below the diagonal), the decays, then the inverse of I + N, N = diag(beta) A: 16 x 16 diagonal
+// blocks by substitution, a warp each, a lane a column; then warp j goes down block column j,
+// X_ij = -X_ii sum_l N_il X_lj, which needs only its own column and the diagonal blocks.
+template <int KP, int DKP, int C, int PP>
+__global__ void __launch_bounds__(2 * C)
+    k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w) {
+    using L = LocalSmem<KP, DKP, C>;
+    constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = C * 2;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const long long bhn = blockIdx.x;
+    const int n = (int)(bhn % d.Nt);
+    const long long bh = bhn / d.Nt;
+    const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
+    const int t0 = n * C;
+    int nt = delta_valid(in.valid, b, d.T) - t0;
+    if (nt <= 0) return;
+    nt = nt < C ? nt : C;
+    const unsigned sk = smem_u32(smem), sq = sk + L::Q;
+    float *N = reinterpret_cast<float *>(smem + L::N), *X = reinterpret_cast<float *>(smem + L::X);
+    float *hi = reinterpret_cast<float *>(smem + L::G), *lo = hi + C, *be = lo + C;
+
+    load_tokens<KP, DKP, C, THREADS>(sk, k, b * k.s[0] + t0 * k.s[1] + hk * k.s[2], d.Dk, nt, tid);
+    load_tokens<KP, DKP, C, THREADS>(sq, q, b * q.s[0] + t0 * q.s[1] + hk * q.s[2], d.Dk, nt, tid);
+    cp_async_commit();
+    if (warp == 0) {
+        // running sums in double: differences of large sums (resets inside the chunk) stay exact
+        constexpr int PL = C / 32;
+        double run[PL];
+        float bt[PL];
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            const int r = lane * PL + i;
+            const long long t = t0 + r;
+            const bool live = r < nt;
+            s += live ? (double)delta_decay(in.g[b * d.gs[0] + t * d.gs[1] + h * d.gs[2]]) : 0.0;
+            bt[i] = live ? in.beta[b * d.bs[0] + t * d.bs[1] + h * d.bs[2]] : 0.f;
+            run[i] = s;
+        }
+        double before = s;
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2) {
+            const double x = __shfl_up_sync(~0u, before, m);
+            if (lane >= m) before += x;
+        }
+        const double all = __shfl_sync(~0u, before, 31);
+        before -= s;
+        float *aux = w.aux + bhn * 3 * C;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            const int r = lane * PL + i;
+            const double x = before + run[i];
+            hi[r] = (float)x;
+            lo[r] = (float)(x - (double)(float)x);
+            be[r] = bt[i];
+            aux[r] = expf((float)x);
+            aux[C + r] = expf((float)(all - x));
+            aux[2 * C + r] = bt[i];
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+
+    {
+        float kk[C / 8][4] = {}, qk[C / 8][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < DKP / 16; ++ks) {
+            unsigned ak[KP][4], aq[KP][4];
+#pragma unroll
+            for (int p = 0; p < KP; ++p) {
+                ldsm4(ak[p], frag_rc<DKP * 2>(sk + p * L::TILE, 16 * warp, 16 * ks, lane));
+                ldsm4(aq[p], frag_rc<DKP * 2>(sq + p * L::TILE, 16 * warp, 16 * ks, lane));
+            }
+#pragma unroll
+            for (int jj = 0; jj < NB; ++jj) {
+                if (jj > warp) break;
+                unsigned bk[KP][4];
+#pragma unroll
+                for (int p = 0; p < KP; ++p)
+                    ldsm4(bk[p], frag_cr<DKP * 2>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+#pragma unroll
+                for (int x = KP - 1; x >= 0; --x)
+#pragma unroll
+                    for (int y = KP - 1; y >= 0; --y)
+                        if (plane_pair(x, y, KP))
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                mma_bf16(kk[2 * jj + e], ak[x], bk[y][2 * e], bk[y][2 * e + 1]);
+                                mma_bf16(qk[2 * jj + e], aq[x], bk[y][2 * e], bk[y][2 * e + 1]);
+                            }
+            }
+        }
+        unsigned char *pimg = w.p + bhn * (size_t)(PP * C * XP);
+#pragma unroll
+        for (int j = 0; j < C / 8; ++j) {
+            if (j > 2 * warp + 1) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t = 16 * warp + (lane >> 2) + 8 * half;
+                const float bt = be[t];
+                float nn[2], pp[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int s = 8 * j + 2 * (lane & 3) + e;
+                    const float f = s <= t ? expf((hi[t] - hi[s]) + (lo[t] - lo[s])) : 0.f;
+                    nn[e] = s < t ? bt * kk[j][2 * half + e] * f : 0.f;
+                    pp[e] = s <= t ? d.scale * qk[j][2 * half + e] * f : 0.f;
+                }
+                *reinterpret_cast<float2 *>(N + t * NP + 8 * j + 2 * (lane & 3)) = make_float2(nn[0], nn[1]);
+                unsigned pl[PP];
+                split_bf16<PP>(pp[0], pp[1], pl);
+#pragma unroll
+                for (int p = 0; p < PP; ++p)
+                    *reinterpret_cast<unsigned *>(pimg + p * C * XP + delta_swz<XP>(t, j) + 4 * (lane & 3)) = pl[p];
+            }
+        }
+    }
+    __syncwarp();
+    if (lane < 16) {
+        float x[16];
+        const float *D = N + (16 * warp) * NP + 16 * warp;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == lane ? 1.f : 0.f;
+#pragma unroll
+            for (int l = 0; l < i; ++l) s = fmaf(-D[i * NP + l], x[l], s);
+            x[i] = s;
+            X[(16 * warp + i) * NP + 16 * warp + lane] = s;
+        }
+    }
+    __syncthreads();
+    {
+        const int c = lane & 15, r0 = (lane >> 4) * 8, j = warp;
+        for (int i = j + 1; i < NB; ++i) {
+            float acc[8] = {};
+            for (int m = 16 * j; m < 16 * i; m += 4) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = X[(m + e) * NP + 16 * j + c];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float4 a = *reinterpret_cast<const float4 *>(N + (16 * i + r0 + r) * NP + m);
+                    acc[r] = fmaf(a.x, x[0], fmaf(a.y, x[1], fmaf(a.z, x[2], fmaf(a.w, x[3], acc[r]))));
+                }
+            }
+            float *blk = X + (16 * i) * NP + 16 * j;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) blk[(r0 + r) * NP + c] = acc[r];
+            __syncwarp();
+            float out[8] = {};
+#pragma unroll
+            for (int m = 0; m < 16; m += 4) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = blk[(m + e) * NP + c];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float4 a = *reinterpret_cast<const float4 *>(X + (16 * i + r0 + r) * NP + 16 * i + m);
+                    out[r] = fmaf(a.x, x[0], fmaf(a.y, x[1], fmaf(a.z, x[2], fmaf(a.w, x[3], out[r]))));
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < 8; ++r) blk[(r0 + r) * NP + c] = -out[r];
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    unsigned char *ximg = w.x + bhn * (size_t)(3 * C * XP);
+    for (int i = tid; i < C * (C / 8); i += THREADS) {
+        const int r = i / (C / 8), c = i % (C / 8);
+        if (c > 2 * (r >> 4) + 1) continue;
+        unsigned pl[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = *reinterpret_cast<const float2 *>(X + r * NP + 8 * c + 2 * e);
+            split_bf16<3>(x.x, x.y, pl[e]);
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+            *reinterpret_cast<uint4 *>(ximg + p * C * XP + delta_swz<XP>(r, c)) =
+                make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
+    }
+}
+
+template <typename T, int DKP, int NW>
+struct ScanSmem {
+    static constexpr bool BF = sizeof(T) == 2;
+    static constexpr int C = BF ? 64 : 32, KP = BF ? 1 : 3, PP = BF ? 2 : 3;
+    static constexpr int XP = C * 2;                         // row pitch of the X and P planes
+    static constexpr int VP = NW * 16 * (int)sizeof(T);      // row pitch of the value tile
+    static constexpr int TILE = C * DKP * 2;
+    static constexpr int Q = KP * TILE, X = 2 * KP * TILE, P = X + 3 * C * XP, V = P + PP * C * XP;
+    static constexpr int AUX = V + C * VP, STAGE = AUX + 3 * C * 4;
+    static constexpr int BYTES = 2 * STAGE;
+};
+
+// One block per head and NW * 16 of its columns; two stages of chunk inputs, the next chunk's copies
+// in flight while this one is computed. SAVE: also stores S0 and u for the backward.
+template <typename T, int DKP, int NW, bool SAVE>
+__global__ void __launch_bounds__(NW * 32, 1)
+    k_delta_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, float *state,
+                 T *o, float *snap, float *usave) {
+    using L = ScanSmem<T, DKP, NW>;
+    constexpr bool BF = L::BF;
+    constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, THREADS = NW * 32;
+    constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / (int)sizeof(T);
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
+    const int slices = (d.Dv + NW * 16 - 1) / (NW * 16);
+    const int dv_blk = (blockIdx.x % slices) * NW * 16;
+    const long long bh = blockIdx.x / slices;
+    const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
+    const int dv0 = dv_blk + 16 * warp;
+    const bool mine = dv0 < d.Dv;                            // else the warp only helps to load
+    const int ntok = delta_valid(in.valid, b, d.T), nch = (ntok + C - 1) / C;
+    const T *v = static_cast<const T *>(in.v) + b * d.vs[0] + h * d.vs[2] + dv_blk;
+    const long long kbase = b * k.s[0] + hk * k.s[2], qbase = b * q.s[0] + hk * q.s[2];
+    T *out = o + ((long long)b * d.T * d.H + h) * d.Dv;
+    const long long orow = (long long)d.H * d.Dv;
+    const unsigned s0 = smem_u32(smem);
+
+    auto load = [&](int n, int stage) {
+        const unsigned st = s0 + stage * L::STAGE;
+        const long long t0 = (long long)n * C, bhn = bh * d.Nt + n;
+        const int nt = ntok - (int)t0 < C ? ntok - (int)t0 : C;
+        load_tokens<KP, DKP, C, THREADS>(st, k, kbase + t0 * k.s[1], d.Dk, nt, tid);
+        load_tokens<KP, DKP, C, THREADS>(st + L::Q, q, qbase + t0 * q.s[1], d.Dk, nt, tid);
+        const unsigned char *xi = w.x + bhn * (3 * C * XP), *pi = w.p + bhn * (PP * C * XP);
+        for (int i = tid; i < (3 + PP) * C * (C / 8); i += THREADS) {
+            const int c = i % (C / 8), r = (i / (C / 8)) % C, pl = i / (C * (C / 8));
+            if (c > 2 * (r >> 4) + 1) continue;              // above the diagonal blocks
+            const int off = delta_swz<XP>(r, c);
+            const unsigned char *src = pl < 3 ? xi + pl * C * XP + off : pi + (pl - 3) * C * XP + off;
+            cp_async16_zfill(st + L::X + pl * C * XP + off, src, true);
+        }
+        for (int i = tid; i < C * NW * 16 / VE; i += THREADS) {
+            const int c = i % (NW * 16 / VE), r = i / (NW * 16 / VE);
+            const bool live = r < nt && dv_blk + c * VE < d.Dv;
+            cp_async16_zfill(st + L::V + delta_swz<VP>(r, c), live ? v + (t0 + r) * d.vs[1] + c * VE : v, live);
+        }
+        for (int i = tid; i < 3 * C / 4; i += THREADS)
+            cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * 3 * C + 4 * i, true);
+        cp_async_commit();
+    };
+
+    float S[ND][4];
+    float *sp = state + (bh * d.Dk) * d.Dv + dv0;
+#pragma unroll
+    for (int j = 0; j < ND; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int dk = 8 * j + 2 * i4 + (e & 1);
+            S[j][e] = mine && dk < d.Dk ? sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] : 0.f;
+        }
+    if (nch > 0) load(0, 0);
+    for (int n = 0; n < nch; ++n) {
+        if (n + 1 < nch) {
+            load(n + 1, (n + 1) & 1);
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
+        __syncthreads();
+        const int stage = (n & 1) * L::STAGE;
+        const unsigned sk = s0 + stage, sq = sk + L::Q, sx = sk + L::X, spp = sk + L::P, sv = sk + L::V;
+        const float *from = reinterpret_cast<const float *>(smem + stage + L::AUX), *to = from + C, *be = to + C;
+        const int nt = ntok - n * C < C ? ntok - n * C : C;
+        if (mine) {
+            if constexpr (SAVE) {
+                float *dst = snap + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv + dv0;
+#pragma unroll
+                for (int j = 0; j < ND; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int dk = 8 * j + 2 * i4 + (e & 1);
+                        if (dk < d.Dk) dst[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
+                    }
+            }
+            float R[NT][4] = {}, O[NT][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < DKP / 16; ++ks) {          // R = (K S)^T, O = (Q S)^T
+                unsigned a[3][4], bb[KP][C / 16][4];
+                split_frag<3>(S, ks, a);
+#pragma unroll
+                for (int p = 0; p < KP; ++p)
+#pragma unroll
+                    for (int jj = 0; jj < C / 16; ++jj)
+                        ldsm4(bb[p][jj], frag_cr<DKP * 2>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+#pragma unroll
+                for (int x = 2; x >= 0; --x)
+#pragma unroll
+                    for (int p = KP - 1; p >= 0; --p)
+                        if (plane_pair(x, p, 3))
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma_bf16(R[j], a[x], bb[p][j >> 1][2 * (j & 1)], bb[p][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                for (int p = 0; p < KP; ++p)
+#pragma unroll
+                    for (int jj = 0; jj < C / 16; ++jj)
+                        ldsm4(bb[p][jj], frag_cr<DKP * 2>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
+#pragma unroll
+                for (int x = PP - 1; x >= 0; --x)            // bfloat16 readings: two terms (2^-17)
+#pragma unroll
+                    for (int p = KP - 1; p >= 0; --p)
+                        if (plane_pair(x, p, PP))
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma_bf16(O[j], a[x], bb[p][j >> 1][2 * (j & 1)], bb[p][j >> 1][2 * (j & 1) + 1]);
+            }
+            // R <- beta (v - G R), O <- scale G O
+#pragma unroll
+            for (int jj = 0; jj < C / 16; ++jj) {
+                float vv[2][4];
+                if constexpr (BF) {
+                    unsigned r[4];
+                    ldsm4t(r, frag_rc<VP>(sv, 16 * jj, 16 * warp, lane));
+                    vv[0][0] = lo_f32(r[0]); vv[0][1] = hi_f32(r[0]);
+                    vv[1][0] = lo_f32(r[1]); vv[1][1] = hi_f32(r[1]);
+                    vv[0][2] = lo_f32(r[2]); vv[0][3] = hi_f32(r[2]);
+                    vv[1][2] = lo_f32(r[3]); vv[1][3] = hi_f32(r[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = 16 * jj + 8 * (e >> 2) + 2 * i4 + (e & 1);
+                        const int c = 16 * warp + g4 + 8 * ((e >> 1) & 1);
+                        vv[e >> 2][e & 3] = *reinterpret_cast<const float *>(
+                            smem + stage + L::V + delta_swz<VP>(t, c >> 2) + 4 * (c & 3));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 2 * jj + (e >> 2), t = 8 * j + 2 * i4 + (e & 1);
+                    const float f = from[t];
+                    R[j][e & 3] = be[t] * (vv[e >> 2][e & 3] - f * R[j][e & 3]);
+                    O[j][e & 3] *= d.scale * f;
+                }
+            }
+            float U[NT][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < C / 16; ++ks) {            // U = (X (beta w))^T
+                unsigned a[3][4];
+                split_frag<3>(R, ks, a);
+#pragma unroll
+                for (int jj = ks; jj < C / 16; ++jj) {
+                    unsigned bb[3][4];
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) ldsm4(bb[p], frag_cr<XP>(sx + p * C * XP, 16 * jj, 16 * ks, lane));
+#pragma unroll
+                    for (int x = 2; x >= 0; --x)
+#pragma unroll
+                        for (int p = 2; p >= 0; --p)
+                            if (plane_pair(x, p, 3)) {
+                                mma_bf16(U[2 * jj], a[x], bb[p][0], bb[p][1]);
+                                mma_bf16(U[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
+                            }
+                }
+            }
+            if constexpr (SAVE) {
+                float *dst = usave + ((bh * d.Nt + n) * (long long)C) * d.Dv + dv0;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[(size_t)(8 * j + 2 * i4 + (e & 1)) * d.Dv + g4 + 8 * (e >> 1)] = U[j][e];
+            }
+#pragma unroll
+            for (int ks = 0; ks < C / 16; ++ks) {            // O += (P u)^T
+                unsigned a[PP][4];
+                split_frag<PP>(U, ks, a);
+#pragma unroll
+                for (int jj = ks; jj < C / 16; ++jj) {
+                    unsigned bb[PP][4];
+#pragma unroll
+                    for (int p = 0; p < PP; ++p) ldsm4(bb[p], frag_cr<XP>(spp + p * C * XP, 16 * jj, 16 * ks, lane));
+#pragma unroll
+                    for (int x = PP - 1; x >= 0; --x)
+#pragma unroll
+                        for (int p = PP - 1; p >= 0; --p)
+                            if (plane_pair(x, p, PP)) {
+                                mma_bf16(O[2 * jj], a[x], bb[p][0], bb[p][1]);
+                                mma_bf16(O[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
+                            }
+                }
+            }
+            // the readings take the place of the warp's columns of the value tile, then leave as rows
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * j + 2 * i4 + (e & 1), c = 16 * warp + g4 + 8 * (e >> 1);
+                    *reinterpret_cast<T *>(smem + stage + L::V + delta_swz<VP>(t, c / VE) +
+                                           (c % VE) * sizeof(T)) = from_f32<T>(O[j][e]);
+                }
+            __syncwarp();
+            {
+                constexpr int PR = 16 / VE, RP = 32 / PR;    // pieces a row, rows at once
+#pragma unroll
+                for (int r0 = 0; r0 < C; r0 += RP) {
+                    const int r = r0 + lane / PR, c = lane % PR;
+                    const long long t = (long long)n * C + r;
+                    uint4 x = *reinterpret_cast<const uint4 *>(smem + stage + L::V + delta_swz<VP>(r, 16 * warp / VE + c));
+                    if (r >= nt) x = make_uint4(0u, 0u, 0u, 0u);
+                    if (t < d.T) *reinterpret_cast<uint4 *>(out + t * orow + dv0 + c * VE) = x;
+                }
+            }
+            // S <- G_C S + (e^{L_C - L} u)^T K
+            unsigned ua[C / 16][3][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) U[j][e] *= to[8 * j + 2 * i4 + (e & 1)];
+#pragma unroll
+            for (int ks = 0; ks < C / 16; ++ks) split_frag<3>(U, ks, ua[ks]);
+            const float whole = from[C - 1];
+#pragma unroll
+            for (int nn = 0; nn < ND / 2; nn += 2) {
+                float acc[4][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks) {
+                    unsigned bb[KP][2][4];
+#pragma unroll
+                    for (int p = 0; p < KP; ++p)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            ldsm4t(bb[p][m], frag_rc<DKP * 2>(sk + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
+#pragma unroll
+                    for (int x = 2; x >= 0; --x)
+#pragma unroll
+                        for (int p = KP - 1; p >= 0; --p)
+                            if (plane_pair(x, p, 3))
+#pragma unroll
+                                for (int m = 0; m < 4; ++m)
+                                    mma_bf16(acc[m], ua[ks][x], bb[p][m >> 1][2 * (m & 1)], bb[p][m >> 1][2 * (m & 1) + 1]);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[2 * nn + m][e] = fmaf(whole, S[2 * nn + m][e], acc[m][e]);
+            }
+        }
+        __syncthreads();
+    }
+    if (!mine) return;
+    if (nch > 0) {
+#pragma unroll
+        for (int j = 0; j < ND; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dk = 8 * j + 2 * i4 + (e & 1);
+                if (dk < d.Dk) sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
+            }
+    }
+    constexpr int PR = 16 / VE;
+    for (long long t = (long long)nch * C + lane / PR; t < d.T; t += 32 / PR)
+        *reinterpret_cast<uint4 *>(out + t * orow + dv0 + (lane % PR) * VE) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// float32 rows [b, t, h] of D columns -> three contiguous bfloat16 planes [B, T, heads, D]
+__global__ void __launch_bounds__(256) k_delta_split(DeltaDims d, const float *x, long long sb, long long st,
+                                                     long long sh, int heads, int D, __nv_bfloat16 *planes) {
+    const long long all = (long long)d.B * d.T * heads * (D / 4), plane = all * 4;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+        const long long row = i / (D / 4), h = row % heads, bt = row / heads, t = bt % d.T, b = bt / d.T;
+        const int c = (int)(i % (D / 4)) * 4;
+        unsigned p0[3] = {0u, 0u, 0u}, p1[3] = {0u, 0u, 0u};
+        const float4 a = *reinterpret_cast<const float4 *>(x + b * sb + t * st + h * sh + c);
+        split_bf16<3>(a.x, a.y, p0);
+        split_bf16<3>(a.z, a.w, p1);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+            *reinterpret_cast<uint2 *>(planes + p * plane + 4 * i) = make_uint2(p0[p], p1[p]);
+    }
+}
+
+template <typename T, int DKP, int NW, bool SAVE>
+cudaError_t scan_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
+                     const DeltaLocal &w, float *state, T *o, float *snap, float *u, cudaStream_t st) {
+    using L = ScanSmem<T, DKP, NW>;
+    auto kern = k_delta_scan<T, DKP, NW, SAVE>;
+    set_kernel_smem(kern, L::BYTES);
+    const long long slices = (d.Dv + NW * 16 - 1) / (NW * 16);
+    kern<<<(unsigned)((long long)d.B * d.H * slices), NW * 32, L::BYTES, st>>>(d, in, q, k, w, state, o, snap, u);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t scan_any(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
+                     const DeltaLocal &w, float *state, void *o, float *snap, float *u, cudaStream_t st) {
+    T *out = static_cast<T *>(o);
+    // eight warps (two an SM sub-core) share a chunk's loads once there is a block for every SM;
+    // with fewer heads four, so that every warp has a tensor core of its own
+    const bool wide = d.Dv > 64 && (long long)d.B * d.H * ((d.Dv + 127) / 128) >= kRefSms;
+    auto go = [&](auto dkp, auto nw, auto save) {
+        return scan_one<T, decltype(dkp)::value, decltype(nw)::value, decltype(save)::value>(
+            d, in, q, k, w, state, out, snap, u, st);
+    };
+    auto pick = [&](auto dkp, auto nw) {
+        return snap ? go(dkp, nw, std::true_type{}) : go(dkp, nw, std::false_type{});
+    };
+    auto size = [&](auto dkp) {
+        return wide ? pick(dkp, std::integral_constant<int, 8>{}) : pick(dkp, std::integral_constant<int, 4>{});
+    };
+    return d.Dk <= 64 ? size(std::integral_constant<int, 64>{}) : size(std::integral_constant<int, 128>{});
+}
+
+template <int KP, int DKP, int C, int PP>
+cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
+                      const DeltaLocal &w, cudaStream_t st) {
+    auto kern = k_delta_local<KP, DKP, C, PP>;
+    constexpr int bytes = LocalSmem<KP, DKP, C>::BYTES;
+    set_kernel_smem(kern, bytes);
+    kern<<<(unsigned)delta_chunks(d), 2 * C, bytes, st>>>(d, in, q, k, w);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
+                               const DeltaLocal &w, cudaStream_t st) {
+    if (d.dtype == SDM_BF16)
+        return d.Dk <= 64 ? local_one<1, 64, 64, 2>(d, in, q, k, w, st) : local_one<1, 128, 64, 2>(d, in, q, k, w, st);
+    return d.Dk <= 64 ? local_one<3, 64, 32, 3>(d, in, q, k, w, st) : local_one<3, 128, 32, 3>(d, in, q, k, w, st);
+}
+
+cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
+                              const DeltaLocal &w, float *state, void *o, float *snap, float *u, cudaStream_t st) {
+    return d.dtype == SDM_BF16 ? scan_any<__nv_bfloat16>(d, in, q, k, w, state, o, snap, u, st)
+                               : scan_any<float>(d, in, q, k, w, state, o, snap, u, st);
+}
+
+cudaError_t launch_delta_split(const DeltaDims &d, const void *x, const long long *s, int heads, int D,
+                               __nv_bfloat16 *planes, cudaStream_t st) {
+    const long long units = (long long)d.B * d.T * heads * (D / 4), blocks = (units + 255) / 256;
+    k_delta_split<<<(unsigned)(blocks < 8 * kRefSms ? blocks : 8 * kRefSms), 256, 0, st>>>(
+        d, static_cast<const float *>(x), s[0], s[1], s[2], heads, D, planes);
+    return cudaGetLastError();
+}
+
+}  // namespace sdm
