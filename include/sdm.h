@@ -439,6 +439,34 @@ int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, c
                     const int32_t *valid_tokens, void *readings, void *workspace,
                     size_t workspace_bytes, void *stream);
 
+/* The saving forward: sdm_gated_delta, and what the backward needs (the state at the start of every
+ * chunk and the chunks' corrections, float32) in saved: sdm_gated_delta_saved_bytes(shape) bytes,
+ * 256-byte aligned. */
+size_t sdm_gated_delta_saved_bytes(const sdm_delta_shape *shape);
+int sdm_gated_delta_save(const sdm_delta_shape *shape, float *state, const void *q, const void *k,
+                         const void *v, const float *log_decay, const float *beta,
+                         const int32_t *valid_tokens, void *readings, void *saved,
+                         size_t saved_bytes, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The backward after sdm_gated_delta_save with the same shape and inputs (grad_stride now given).
+ *   grad_readings     [B, T, H, Dv] dtype, strided
+ *   grad_final_state  [B, H, Dk, Dv] float32, the gradient of the final state, or NULL (zeros)
+ *   grad_state        [B, H, Dk, Dv] float32, the gradient of the initial state (may be
+ *                     grad_final_state itself)
+ *   grad_q, grad_k    [B, T, Hk, Dk] dtype, heads that share a key head added in float32 in head order
+ *   grad_v            [B, T, H, Dv] dtype
+ *   grad_log_decay, grad_beta  [B, T, H] float32
+ * all contiguous and written whole. workspace: sdm_gated_delta_backward_workspace_bytes(shape) bytes,
+ * 256-byte aligned. */
+size_t sdm_gated_delta_backward_workspace_bytes(const sdm_delta_shape *shape);
+int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const void *k,
+                             const void *v, const float *log_decay, const float *beta,
+                             const int32_t *valid_tokens, const void *saved, size_t saved_bytes,
+                             const void *grad_readings, const float *grad_final_state,
+                             float *grad_state, void *grad_q, void *grad_k, void *grad_v,
+                             float *grad_log_decay, float *grad_beta, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* ---------------------------------------------------------------------------------------
  * Layer norm over rows of n columns (1..16384), float32 arithmetic, y rounded once:
  *     y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)

@@ -24,7 +24,8 @@ __all__ = ["FLAG_SNAPSHOT_BF16", "FLAG_SNAPSHOT_FP8", "FLAG_TOKEN_GATE", "FLAG_S
            "sdm_write_read_noalloc", "noalloc_device_status", "profile_write_read", "workspace_bytes",
            "backward_workspace_bytes", "launch_count",
            "phase1_debug", "KERNEL_KINDS", "set_wait_limit", "product_key_topk",
-           "product_key_topk_backward", "gated_delta", "layer_norm", "layer_norm_save",
+           "product_key_topk_backward", "gated_delta", "gated_delta_save",
+           "gated_delta_backward", "layer_norm", "layer_norm_save",
            "layer_norm_backward",
            "device_status", "SdmError", "Shape", "library", "library_path", "version"]
 
@@ -132,6 +133,14 @@ def library() -> ctypes.CDLL:
             lib.sdm_gated_delta_workspace_bytes.restype = sz
             lib.sdm_gated_delta.argtypes = [dp] + [vp] * 8 + [vp, sz, vp]
             lib.sdm_gated_delta.restype = i32
+            lib.sdm_gated_delta_saved_bytes.argtypes = [dp]
+            lib.sdm_gated_delta_saved_bytes.restype = sz
+            lib.sdm_gated_delta_save.argtypes = [dp] + [vp] * 8 + [vp, sz, vp, sz, vp]
+            lib.sdm_gated_delta_save.restype = i32
+            lib.sdm_gated_delta_backward_workspace_bytes.argtypes = [dp]
+            lib.sdm_gated_delta_backward_workspace_bytes.restype = sz
+            lib.sdm_gated_delta_backward.argtypes = [dp] + [vp] * 6 + [vp, sz] + [vp] * 8 + [vp, sz, vp]
+            lib.sdm_gated_delta_backward.restype = i32
             lib.sdm_layer_norm.argtypes = [vp, ll, i32, ll, vp, vp, i32, ctypes.c_float, i32, vp, vp, vp]
             lib.sdm_layer_norm.restype = i32
             lib.sdm_layer_norm_workspace_bytes.argtypes = [ll, i32]
@@ -786,6 +795,64 @@ def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.
             _ptr(beta), _ptr(valid_tokens), _ptr(readings), _ptr(workspace), workspace.numel(),
             _stream_ptr(stream)))
     return readings
+
+
+def gated_delta_save(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: torch.Tensor, beta: torch.Tensor,
+                     valid_tokens: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
+                     readings=None, saved=None, workspace=None, stream=None):
+    """gated_delta that also keeps what its backward needs: (readings, saved), with ``state``
+    advanced in place. ``saved`` (uint8) holds the state at the start of every chunk of 64 (float32
+    inputs: 32) tokens and the chunks' corrections."""
+    shape, (B, T, H, Hk, Dk, Dv) = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
+    dev = v.device
+    _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
+    if readings is None:
+        readings = torch.empty((B, T, H, Dv), dtype=v.dtype, device=dev)
+    else:
+        _need(readings, "readings", (B, T, H, Dv), v.dtype, dev)
+    lib = library()
+    workspace = _scratch(workspace, _bytes(lib.sdm_gated_delta_workspace_bytes(ctypes.byref(shape))), dev)
+    saved = _scratch(saved, _bytes(lib.sdm_gated_delta_saved_bytes(ctypes.byref(shape))), dev)
+    with torch.cuda.device(dev):
+        _check(lib.sdm_gated_delta_save(
+            ctypes.byref(shape), _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+            _ptr(beta), _ptr(valid_tokens), _ptr(readings), _ptr(saved), saved.numel(),
+            _ptr(workspace), workspace.numel(), _stream_ptr(stream)))
+    return readings, saved
+
+
+def gated_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                         beta: torch.Tensor, valid_tokens: Optional[torch.Tensor],
+                         saved: torch.Tensor, grad_readings: torch.Tensor, *,
+                         grad_state: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                         workspace=None, stream=None) -> Dict[str, torch.Tensor]:
+    """The backward after gated_delta_save (same inputs and scale): a dict of grad_q, grad_k, grad_v
+    (the inputs' dtype; heads that share a key head are summed), grad_log_decay, grad_beta and
+    grad_state (float32; of the initial state). ``grad_state`` [B, H, Dk, Dv] float32: the gradient
+    of the final state (None: zero); it is not changed."""
+    shape, (B, T, H, Hk, Dk, Dv) = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale, grad_readings)
+    dev, dt = v.device, v.dtype
+    if grad_state is not None:
+        _need(grad_state, "grad_state", (B, H, Dk, Dv), torch.float32, dev)
+    lib = library()
+    workspace = _scratch(workspace, _bytes(lib.sdm_gated_delta_backward_workspace_bytes(ctypes.byref(shape))), dev)
+    if not isinstance(saved, torch.Tensor):
+        raise TypeError("saved must be a tensor")
+    _scratch(saved, 0, dev)
+    new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+    out = {"grad_q": torch.empty((B, T, Hk, Dk), dtype=dt, device=dev),
+           "grad_k": torch.empty((B, T, Hk, Dk), dtype=dt, device=dev),
+           "grad_v": torch.empty((B, T, H, Dv), dtype=dt, device=dev),
+           "grad_log_decay": new(B, T, H), "grad_beta": new(B, T, H), "grad_state": new(B, H, Dk, Dv)}
+    with torch.cuda.device(dev):
+        _check(lib.sdm_gated_delta_backward(
+            ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta),
+            _ptr(valid_tokens), _ptr(saved), saved.numel(), _ptr(grad_readings), _ptr(grad_state),
+            _ptr(out["grad_state"]), _ptr(out["grad_q"]), _ptr(out["grad_k"]), _ptr(out["grad_v"]),
+            _ptr(out["grad_log_decay"]), _ptr(out["grad_beta"]), _ptr(workspace),
+            workspace.numel(), _stream_ptr(stream)))
+    return out
 
 
 # ------------------------------------------------------------------------------------------

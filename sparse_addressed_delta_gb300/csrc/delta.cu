@@ -28,6 +28,7 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.dtype = s->dtype;
     d.scale = s->scale;
     d.C = delta_chunk(s->dtype);
+    d.pp = s->dtype == SDM_BF16 ? 2 : 3;
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
     if ((long long)s->B * s->H * d.Nt >= (1LL << 31) || (long long)s->B * s->H * (s->Dv / 16) >= (1LL << 31))
@@ -64,10 +65,12 @@ bool by_token(const DeltaDims &d) { return d.T <= kDeltaStepTokens; }
 
 // Where the chunk form's buffers lie in a workspace; `bytes` is their end.
 struct DeltaLayout {
-    size_t q, k, x, p, aux, bytes;       // q, k: the planes of float32 inputs
+    size_t q, k, x, p, aux;              // q, k: the planes of float32 inputs
+    size_t ends, w, dq, dk;              // the backward's
+    size_t bytes;
 };
 
-DeltaLayout delta_layout(const DeltaDims &d) {
+DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     DeltaLayout l{};
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -78,11 +81,24 @@ DeltaLayout delta_layout(const DeltaDims &d) {
     const size_t tok = d.dtype == SDM_F32 ? (size_t)d.B * d.T * d.Hk * d.Dk * 3 * 2 : 0;
     l.q = take(tok);
     l.k = take(tok);
-    l.x = take(delta_chunks(d) * delta_x_bytes(d));
-    l.p = take(delta_chunks(d) * delta_p_bytes(d));
+    l.x = take(delta_chunks(d) * 3 * delta_plane_bytes(d));
+    l.p = take(delta_chunks(d) * d.pp * delta_plane_bytes(d));
     l.aux = take(delta_chunks(d) * 3 * d.C * 4);
+    if (backward) {
+        l.ends = take(delta_chunks(d) * d.Dk * d.Dv * 4);
+        l.w = take(delta_chunks(d) * d.C * d.Dv * 4);
+        const size_t part = d.H != d.Hk ? (size_t)d.B * d.T * d.H * d.Dk * 4 : 0;
+        l.dq = take(part);
+        l.dk = take(part);
+    }
     l.bytes = at;
     return l;
+}
+
+// what the saving forward keeps: the state at every chunk's start, and u
+size_t delta_saved_snap(const DeltaDims &d) { return delta_up(delta_chunks(d) * d.Dk * d.Dv * 4); }
+size_t delta_saved(const DeltaDims &d) {
+    return delta_saved_snap(d) + delta_up(delta_chunks(d) * d.C * d.Dv * 4);
 }
 
 DeltaPlanes delta_planes(const DeltaDims &d, const void *x, const long long *s, unsigned char *split) {
@@ -102,9 +118,8 @@ DeltaPlanes delta_planes(const DeltaDims &d, const void *x, const long long *s, 
 }
 
 // the chunk-local work: planes of float32 keys and queries, X, P and the gates
-cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, unsigned char *ws, DeltaPlanes &q,
-                        DeltaPlanes &k, DeltaLocal &w, cudaStream_t st) {
-    const DeltaLayout l = delta_layout(d);
+cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaLayout &l, unsigned char *ws,
+                        DeltaPlanes &q, DeltaPlanes &k, DeltaLocal &w, cudaStream_t st) {
     q = delta_planes(d, in.q, d.qs, ws + l.q);
     k = delta_planes(d, in.k, d.ks, ws + l.k);
     w = DeltaLocal{ws + l.x, ws + l.p, reinterpret_cast<float *>(ws + l.aux)};
@@ -117,10 +132,10 @@ cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, unsigned char *ws
     return launch_delta_local(d, in, q, k, w, st);
 }
 
-int delta_check_ws(const void *ws, size_t have, size_t need) {
+int delta_check_ws(const char *what, const void *ws, size_t have, size_t need) {
     if (!ws || have < need || (uintptr_t)ws % kAlign)
-        return set_error(SDM_ERR_WORKSPACE, "gated delta: workspace NULL, too small (%zu of %zu bytes) "
-                         "or not %zu-byte aligned", have, need, (size_t)kAlign);
+        return set_error(SDM_ERR_WORKSPACE, "gated delta: %s NULL, too small (%zu of %zu bytes) "
+                         "or not %zu-byte aligned", what, have, need, (size_t)kAlign);
     return SDM_OK;
 }
 
@@ -129,18 +144,13 @@ int delta_check_ws(const void *ws, size_t have, size_t need) {
 
 using namespace sdm;
 
-extern "C" {
+namespace {
 
-size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape) {
-    DeltaDims d;
-    if (delta_check(shape, d) != SDM_OK) return 0;
-    return by_token(d) ? kAlign : delta_layout(d).bytes + kAlign;
-}
-
-int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, const void *k,
-                    const void *v, const float *log_decay, const float *beta,
-                    const int32_t *valid_tokens, void *readings, void *workspace,
-                    size_t workspace_bytes, void *stream) {
+// sdm_gated_delta and, with `saved`, sdm_gated_delta_save
+int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, const void *k, const void *v,
+                  const float *log_decay, const float *beta, const int32_t *valid_tokens, void *readings,
+                  bool save, void *saved, size_t saved_bytes, void *workspace, size_t workspace_bytes,
+                  void *stream) {
     DeltaDims d;
     int rc = delta_check(shape, d);
     if (rc != SDM_OK) return rc;
@@ -152,14 +162,109 @@ int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, c
         return set_error(SDM_ERR_INVALID, "gated delta: the state and the readings must be 16-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
-    if (by_token(d)) return delta_status(launch_delta_step(d, in, state, readings, st));
-    rc = delta_check_ws(workspace, workspace_bytes, delta_layout(d).bytes);
+    if (!save && by_token(d)) return delta_status(launch_delta_step(d, in, state, readings, st));
+    const DeltaLayout l = delta_layout(d, false);
+    rc = delta_check_ws("workspace", workspace, workspace_bytes, l.bytes);
+    if (rc == SDM_OK && save) rc = delta_check_ws("saved buffer", saved, saved_bytes, delta_saved(d));
     if (rc != SDM_OK) return rc;
     DeltaPlanes qp, kp;
     DeltaLocal w;
-    cudaError_t e = delta_local(d, in, static_cast<unsigned char *>(workspace), qp, kp, w, st);
-    if (e == cudaSuccess)
-        e = launch_delta_scan(d, in, qp, kp, w, state, readings, nullptr, nullptr, st);
+    cudaError_t e = delta_local(d, in, l, static_cast<unsigned char *>(workspace), qp, kp, w, st);
+    float *snap = save ? static_cast<float *>(saved) : nullptr;
+    float *u = save ? reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_snap(d)) : nullptr;
+    if (e == cudaSuccess) e = launch_delta_scan(d, in, qp, kp, w, state, readings, snap, u, st);
+    return delta_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape) {
+    DeltaDims d;
+    if (delta_check(shape, d) != SDM_OK) return 0;
+    return delta_layout(d, false).bytes + kAlign;
+}
+
+int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, const void *k,
+                    const void *v, const float *log_decay, const float *beta,
+                    const int32_t *valid_tokens, void *readings, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+    return delta_forward(shape, state, q, k, v, log_decay, beta, valid_tokens, readings, false, nullptr, 0,
+                         workspace, workspace_bytes, stream);
+}
+
+size_t sdm_gated_delta_saved_bytes(const sdm_delta_shape *shape) {
+    DeltaDims d;
+    if (delta_check(shape, d) != SDM_OK) return 0;
+    return delta_saved(d) + kAlign;
+}
+
+int sdm_gated_delta_save(const sdm_delta_shape *shape, float *state, const void *q, const void *k,
+                         const void *v, const float *log_decay, const float *beta,
+                         const int32_t *valid_tokens, void *readings, void *saved,
+                         size_t saved_bytes, void *workspace, size_t workspace_bytes, void *stream) {
+    return delta_forward(shape, state, q, k, v, log_decay, beta, valid_tokens, readings, true, saved,
+                         saved_bytes, workspace, workspace_bytes, stream);
+}
+
+size_t sdm_gated_delta_backward_workspace_bytes(const sdm_delta_shape *shape) {
+    DeltaDims d;
+    if (delta_check(shape, d) != SDM_OK) return 0;
+    d.pp = 3;
+    return delta_layout(d, true).bytes + kAlign;
+}
+
+int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const void *k, const void *v,
+                             const float *log_decay, const float *beta, const int32_t *valid_tokens,
+                             const void *saved, size_t saved_bytes, const void *grad_readings,
+                             const float *grad_final_state, float *grad_state, void *grad_q, void *grad_k,
+                             void *grad_v, float *grad_log_decay, float *grad_beta, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    DeltaDims d;
+    int rc = delta_check(shape, d);
+    if (rc != SDM_OK) return rc;
+    d.pp = 3;                            // P reaches float32 gradients
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d.B == 0) return SDM_OK;
+    if (!grad_state) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
+    if (d.T == 0) {                      // the final state is the initial one
+        const size_t bytes = (size_t)d.B * d.H * d.Dk * d.Dv * 4;
+        return delta_status(grad_final_state ? cudaMemcpyAsync(grad_state, grad_final_state, bytes, cudaMemcpyDeviceToDevice, st)
+                                             : cudaMemsetAsync(grad_state, 0, bytes, st));
+    }
+    rc = delta_check_inputs(q, k, v, log_decay, beta);
+    if (rc != SDM_OK) return rc;
+    if (!grad_readings || !grad_q || !grad_k || !grad_v || !grad_log_decay || !grad_beta)
+        return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
+    if (off16(grad_readings) || off16(grad_q) || off16(grad_k) || off16(grad_v))
+        return set_error(SDM_ERR_INVALID, "gated delta: the gradients of q, k, v and the readings must be 16-byte aligned");
+    const DeltaLayout l = delta_layout(d, true);
+    rc = delta_check_ws("workspace", workspace, workspace_bytes, l.bytes);
+    if (rc == SDM_OK) rc = delta_check_ws("saved buffer", saved, saved_bytes, delta_saved(d));
+    if (rc != SDM_OK) return rc;
+    auto ws = static_cast<unsigned char *>(workspace);
+    const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
+    DeltaPlanes qp, kp;
+    DeltaLocal w;
+    cudaError_t e = delta_local(d, in, l, ws, qp, kp, w, st);
+    DeltaBack o;
+    o.grad = grad_readings;
+    o.state_in = grad_final_state;
+    o.state_out = grad_state;
+    o.grad_q = grad_q;
+    o.grad_k = grad_k;
+    o.grad_v = grad_v;
+    o.grad_decay = grad_log_decay;
+    o.grad_beta = grad_beta;
+    o.snap = static_cast<const float *>(saved);
+    o.u = reinterpret_cast<const float *>(static_cast<const unsigned char *>(saved) + delta_saved_snap(d));
+    o.ends = reinterpret_cast<float *>(ws + l.ends);
+    o.w = reinterpret_cast<float *>(ws + l.w);
+    o.dq = reinterpret_cast<float *>(ws + l.dq);
+    o.dk = reinterpret_cast<float *>(ws + l.dk);
+    if (e == cudaSuccess) e = launch_delta_back_scan(d, in, qp, kp, w, o, st);
+    if (e == cudaSuccess) e = launch_delta_back_local(d, in, qp, kp, w, o, st);
     return delta_status(e);
 }
 

@@ -20,24 +20,9 @@
 namespace sdm {
 namespace {
 
-__device__ __forceinline__ bool plane_pair(int a, int b, int most) { return a + b < most; }
-
-// K or Q planes of a chunk's `nt` live tokens into tiles [KP][C][DKP], zero elsewhere
-template <int KP, int DKP, int C, int THREADS>
-__device__ __forceinline__ void load_tokens(unsigned dst, const DeltaPlanes &x, long long base,
-                                            int Dk, int nt, int tid) {
-    constexpr int PC = DKP / 8;
-    for (int i = tid; i < KP * C * PC; i += THREADS) {
-        const int c = i % PC, r = (i / PC) % C, pl = i / (PC * C);
-        const bool live = r < nt && c * 8 < Dk;
-        const __nv_bfloat16 *src = x.p + pl * x.plane + base + (live ? r * x.s[1] + c * 8 : 0);
-        cp_async16_zfill(dst + pl * (C * DKP * 2) + delta_swz<DKP * 2>(r, c), src, live);
-    }
-}
-
 template <int KP, int DKP, int C>
 struct LocalSmem {
-    static constexpr int TILE = C * DKP * 2, NP = C + 4;
+    static constexpr int KPITCH = delta_pitch(DKP * 2), TILE = C * KPITCH, NP = C + 4;
     static constexpr int Q = KP * TILE, N = 2 * KP * TILE, X = N + C * NP * 4, G = X + C * NP * 4;
     static constexpr int BYTES = G + 3 * C * 4;
 };
@@ -50,7 +35,7 @@ template <int KP, int DKP, int C, int PP>
 __global__ void __launch_bounds__(2 * C)
     k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w) {
     using L = LocalSmem<KP, DKP, C>;
-    constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = C * 2;
+    constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = delta_pitch(C * 2), KPI = L::KPITCH;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long bhn = blockIdx.x;
@@ -114,8 +99,8 @@ __global__ void __launch_bounds__(2 * C)
             unsigned ak[KP][4], aq[KP][4];
 #pragma unroll
             for (int p = 0; p < KP; ++p) {
-                ldsm4(ak[p], frag_rc<DKP * 2>(sk + p * L::TILE, 16 * warp, 16 * ks, lane));
-                ldsm4(aq[p], frag_rc<DKP * 2>(sq + p * L::TILE, 16 * warp, 16 * ks, lane));
+                ldsm4(ak[p], frag_rc<KPI>(sk + p * L::TILE, 16 * warp, 16 * ks, lane));
+                ldsm4(aq[p], frag_rc<KPI>(sq + p * L::TILE, 16 * warp, 16 * ks, lane));
             }
 #pragma unroll
             for (int jj = 0; jj < NB; ++jj) {
@@ -123,7 +108,7 @@ __global__ void __launch_bounds__(2 * C)
                 unsigned bk[KP][4];
 #pragma unroll
                 for (int p = 0; p < KP; ++p)
-                    ldsm4(bk[p], frag_cr<DKP * 2>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+                    ldsm4(bk[p], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = KP - 1; x >= 0; --x)
 #pragma unroll
@@ -157,7 +142,7 @@ __global__ void __launch_bounds__(2 * C)
                 split_bf16<PP>(pp[0], pp[1], pl);
 #pragma unroll
                 for (int p = 0; p < PP; ++p)
-                    *reinterpret_cast<unsigned *>(pimg + p * C * XP + delta_swz<XP>(t, j) + 4 * (lane & 3)) = pl[p];
+                    *reinterpret_cast<unsigned *>(pimg + p * C * XP + delta_at<XP>(t, j) + 4 * (lane & 3)) = pl[p];
             }
         }
     }
@@ -224,7 +209,7 @@ __global__ void __launch_bounds__(2 * C)
         }
 #pragma unroll
         for (int p = 0; p < 3; ++p)
-            *reinterpret_cast<uint4 *>(ximg + p * C * XP + delta_swz<XP>(r, c)) =
+            *reinterpret_cast<uint4 *>(ximg + p * C * XP + delta_at<XP>(r, c)) =
                 make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
     }
 }
@@ -233,9 +218,9 @@ template <typename T, int DKP, int NW>
 struct ScanSmem {
     static constexpr bool BF = sizeof(T) == 2;
     static constexpr int C = BF ? 64 : 32, KP = BF ? 1 : 3, PP = BF ? 2 : 3;
-    static constexpr int XP = C * 2;                         // row pitch of the X and P planes
-    static constexpr int VP = NW * 16 * (int)sizeof(T);      // row pitch of the value tile
-    static constexpr int TILE = C * DKP * 2;
+    static constexpr int XP = delta_pitch(C * 2);            // row pitch of the X and P planes
+    static constexpr int VP = delta_pitch(NW * 16 * (int)sizeof(T));   // of the value tile
+    static constexpr int KPI = delta_pitch(DKP * 2), TILE = C * KPI;
     static constexpr int Q = KP * TILE, X = 2 * KP * TILE, P = X + 3 * C * XP, V = P + PP * C * XP;
     static constexpr int AUX = V + C * VP, STAGE = AUX + 3 * C * 4;
     static constexpr int BYTES = 2 * STAGE;
@@ -249,7 +234,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                  T *o, float *snap, float *usave) {
     using L = ScanSmem<T, DKP, NW>;
     constexpr bool BF = L::BF;
-    constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, THREADS = NW * 32;
+    constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, KPI = L::KPI, THREADS = NW * 32;
     constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
@@ -272,19 +257,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
         const int nt = ntok - (int)t0 < C ? ntok - (int)t0 : C;
         load_tokens<KP, DKP, C, THREADS>(st, k, kbase + t0 * k.s[1], d.Dk, nt, tid);
         load_tokens<KP, DKP, C, THREADS>(st + L::Q, q, qbase + t0 * q.s[1], d.Dk, nt, tid);
-        const unsigned char *xi = w.x + bhn * (3 * C * XP), *pi = w.p + bhn * (PP * C * XP);
-        for (int i = tid; i < (3 + PP) * C * (C / 8); i += THREADS) {
-            const int c = i % (C / 8), r = (i / (C / 8)) % C, pl = i / (C * (C / 8));
-            if (c > 2 * (r >> 4) + 1) continue;              // above the diagonal blocks
-            const int off = delta_swz<XP>(r, c);
-            const unsigned char *src = pl < 3 ? xi + pl * C * XP + off : pi + (pl - 3) * C * XP + off;
-            cp_async16_zfill(st + L::X + pl * C * XP + off, src, true);
-        }
-        for (int i = tid; i < C * NW * 16 / VE; i += THREADS) {
-            const int c = i % (NW * 16 / VE), r = i / (NW * 16 / VE);
-            const bool live = r < nt && dv_blk + c * VE < d.Dv;
-            cp_async16_zfill(st + L::V + delta_swz<VP>(r, c), live ? v + (t0 + r) * d.vs[1] + c * VE : v, live);
-        }
+        load_planes<3, C, THREADS>(st + L::X, w.x + bhn * (3 * C * XP), tid);
+        load_planes<PP, C, THREADS>(st + L::P, w.p + bhn * (PP * C * XP), tid);
+        load_values<T, NW * 16, C, THREADS>(st + L::V, v + t0 * d.vs[1], d.vs[1], nt, d.Dv - dv_blk, tid);
         for (int i = tid; i < 3 * C / 4; i += THREADS)
             cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * 3 * C + 4 * i, true);
         cp_async_commit();
@@ -332,7 +307,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
                     for (int jj = 0; jj < C / 16; ++jj)
-                        ldsm4(bb[p][jj], frag_cr<DKP * 2>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+                        ldsm4(bb[p][jj], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -345,7 +320,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
                     for (int jj = 0; jj < C / 16; ++jj)
-                        ldsm4(bb[p][jj], frag_cr<DKP * 2>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
+                        ldsm4(bb[p][jj], frag_cr<KPI>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = PP - 1; x >= 0; --x)            // bfloat16 readings: two terms (2^-17)
 #pragma unroll
@@ -372,7 +347,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         const int t = 16 * jj + 8 * (e >> 2) + 2 * i4 + (e & 1);
                         const int c = 16 * warp + g4 + 8 * ((e >> 1) & 1);
                         vv[e >> 2][e & 3] = *reinterpret_cast<const float *>(
-                            smem + stage + L::V + delta_swz<VP>(t, c >> 2) + 4 * (c & 3));
+                            smem + stage + L::V + delta_at<VP>(t, c >> 2) + 4 * (c & 3));
                     }
                 }
 #pragma unroll
@@ -437,7 +412,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 8 * j + 2 * i4 + (e & 1), c = 16 * warp + g4 + 8 * (e >> 1);
-                    *reinterpret_cast<T *>(smem + stage + L::V + delta_swz<VP>(t, c / VE) +
+                    *reinterpret_cast<T *>(smem + stage + L::V + delta_at<VP>(t, c / VE) +
                                            (c % VE) * sizeof(T)) = from_f32<T>(O[j][e]);
                 }
             __syncwarp();
@@ -447,7 +422,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int r0 = 0; r0 < C; r0 += RP) {
                     const int r = r0 + lane / PR, c = lane % PR;
                     const long long t = (long long)n * C + r;
-                    uint4 x = *reinterpret_cast<const uint4 *>(smem + stage + L::V + delta_swz<VP>(r, 16 * warp / VE + c));
+                    uint4 x = *reinterpret_cast<const uint4 *>(smem + stage + L::V + delta_at<VP>(r, 16 * warp / VE + c));
                     if (r >= nt) x = make_uint4(0u, 0u, 0u, 0u);
                     if (t < d.T) *reinterpret_cast<uint4 *>(out + t * orow + dv0 + c * VE) = x;
                 }
@@ -471,7 +446,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     for (int p = 0; p < KP; ++p)
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
-                            ldsm4t(bb[p][m], frag_rc<DKP * 2>(sk + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
+                            ldsm4t(bb[p][m], frag_rc<KPI>(sk + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
 #pragma unroll
                     for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -566,8 +541,10 @@ cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &
 
 cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                                const DeltaLocal &w, cudaStream_t st) {
-    if (d.dtype == SDM_BF16)
+    if (d.dtype == SDM_BF16 && d.pp == 2)
         return d.Dk <= 64 ? local_one<1, 64, 64, 2>(d, in, q, k, w, st) : local_one<1, 128, 64, 2>(d, in, q, k, w, st);
+    if (d.dtype == SDM_BF16)
+        return d.Dk <= 64 ? local_one<1, 64, 64, 3>(d, in, q, k, w, st) : local_one<1, 128, 64, 3>(d, in, q, k, w, st);
     return d.Dk <= 64 ? local_one<3, 64, 32, 3>(d, in, q, k, w, st) : local_one<3, 128, 32, 3>(d, in, q, k, w, st);
 }
 

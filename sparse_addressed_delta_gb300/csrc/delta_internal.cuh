@@ -15,6 +15,7 @@ constexpr float kDeltaMinDecay = -110.f;
 struct DeltaDims {
     int B, T, H, Hk, Dk, Dv;
     int C, Nt;                           // chunk length, chunks a sequence
+    int pp;                              // planes of P: 2 where it only reaches bfloat16 readings
     int dtype;
     float scale;
     long long qs[3], ks[3], vs[3], gs[3], bs[3], os[3];   // element strides of (b, t, h)
@@ -36,25 +37,20 @@ struct DeltaPlanes {
 
 // Per chunk and head, written by the chunk-local kernel (k_delta_local) for the scans:
 //   x   [3][C][C] bfloat16 planes of (I + diag(beta) A)^-1
-//   p   [PP][C][C] planes of the decayed scale q k^T
+//   p   [pp][C][C] planes of the decayed scale q k^T
 //   aux [3][C] float: exp(L_t), exp(L_C - L_t), beta_t
-// The plane images are stored as shared memory holds them (16-byte pieces of a row permuted by
-// delta_swz), so the scans copy them as they are. Blocks above the diagonal are never written and
-// never read.
+// The planes' rows have shared memory's pitch, so the scans copy them as they are. Blocks above the
+// diagonal are never written and never read.
 struct DeltaLocal {
     unsigned char *x, *p;
     float *aux;
 };
 
 __host__ __device__ constexpr int delta_chunk(int dtype) { return dtype == SDM_BF16 ? 64 : 32; }
-__host__ __device__ constexpr int delta_p_planes(int dtype) { return dtype == SDM_BF16 ? 2 : 3; }
 
 inline size_t delta_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 inline size_t delta_chunks(const DeltaDims &d) { return (size_t)d.B * d.H * d.Nt; }
-inline size_t delta_x_bytes(const DeltaDims &d) { return (size_t)3 * d.C * d.C * 2; }
-inline size_t delta_p_bytes(const DeltaDims &d) {
-    return (size_t)delta_p_planes(d.dtype) * d.C * d.C * 2;
-}
+inline size_t delta_plane_bytes(const DeltaDims &d) { return (size_t)d.C * (d.C * 2 + 16); }
 
 cudaError_t launch_delta_step(const DeltaDims &d, const DeltaIn &in, float *state, void *o,
                               cudaStream_t st);
@@ -67,6 +63,26 @@ cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const Delta
                               const DeltaPlanes &k, const DeltaLocal &w, float *state, void *o,
                               float *snap, float *u, cudaStream_t st);
 
+// Outputs of the backward and what its kernels hand on.
+struct DeltaBack {
+    const void *grad;                    // [B, T, H, Dv] (strides os) gradient of the readings
+    const float *state_in;               // [B, H, Dk, Dv] gradient of the final state, or null: 0
+    float *state_out;                    // [B, H, Dk, Dv]
+    void *grad_q, *grad_k, *grad_v;      // contiguous, the inputs' type
+    float *grad_decay, *grad_beta;       // [B, T, H]
+    const float *snap, *u;               // saved by the forward
+    float *ends;                         // [B, H, Nt, Dk, Dv] gradient of each chunk's end state
+    float *w;                            // [B, H, Nt, C, Dv] X^T (gradient of u)
+    float *dq, *dk;                      // [B, T, H, Dk] before shared heads are summed (H > Hk)
+};
+
+cudaError_t launch_delta_back_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
+                                   const DeltaPlanes &k, const DeltaLocal &w, const DeltaBack &o,
+                                   cudaStream_t st);
+cudaError_t launch_delta_back_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
+                                    const DeltaPlanes &k, const DeltaLocal &w, const DeltaBack &o,
+                                    cudaStream_t st);
+
 // ---------------------------------------------------------------------------------------
 // device helpers
 // ---------------------------------------------------------------------------------------
@@ -78,14 +94,12 @@ __device__ __forceinline__ int delta_valid(const int32_t *valid, int b, int T) {
 
 __device__ __forceinline__ float delta_decay(float g) { return g < kDeltaMinDecay ? kDeltaMinDecay : g; }
 
-// byte offset of 16-byte piece `c` of row `r` in a tile with rows of PITCH bytes: the pieces of 8
-// consecutive rows at one column fall into different banks
+// Tiles in shared memory have rows of PITCH bytes, an odd multiple of 16: ldmatrix's eight rows at
+// one column then fall into different banks, and every fragment's address is the lane's own offset
+// plus a constant.
+__host__ __device__ constexpr int delta_pitch(int bytes) { return bytes + 16; }
 template <int PITCH>
-__device__ __forceinline__ unsigned delta_swz(int r, int c) {
-    if constexpr (PITCH >= 128) return r * PITCH + ((c ^ (r & 7)) << 4);
-    else if constexpr (PITCH == 64) return r * PITCH + ((c ^ ((r >> 1) & 3)) << 4);
-    else return r * PITCH + ((c ^ ((r >> 2) & 1)) << 4);
-}
+__device__ __forceinline__ int delta_at(int r, int c) { return r * PITCH + c * 16; }
 
 __device__ __forceinline__ void cp_async16_zfill(unsigned dst, const void *src, bool live) {
     const int n = live ? 16 : 0;
@@ -106,7 +120,7 @@ __device__ __forceinline__ void ldsm4t(unsigned (&r)[4], unsigned addr) {
                  : "memory");
 }
 
-// Fragments of a tile in shared memory (rows of PITCH bytes, pieces permuted by delta_swz):
+// Fragments of a tile in shared memory (rows of PITCH bytes):
 // rows r0.., bfloat16 columns c0.. (multiples of 8). ldmatrix lane i addresses row i % 8 of 8 x 8
 // block i / 8.
 //   frag_rc: blocks (r, c), (r + 8, c), (r, c + 8), (r + 8, c + 8)
@@ -115,11 +129,11 @@ __device__ __forceinline__ void ldsm4t(unsigned (&r)[4], unsigned addr) {
 //     plain: two 8-column B operands with N = rows, K = columns; transposed: an A operand, M = columns
 template <int PITCH>
 __device__ __forceinline__ unsigned frag_rc(unsigned base, int r0, int c0, int lane) {
-    return base + delta_swz<PITCH>(r0 + (lane & 15), (c0 >> 3) + (lane >> 4));
+    return base + delta_at<PITCH>(lane & 15, lane >> 4) + delta_at<PITCH>(r0, c0 >> 3);
 }
 template <int PITCH>
 __device__ __forceinline__ unsigned frag_cr(unsigned base, int r0, int c0, int lane) {
-    return base + delta_swz<PITCH>(r0 + (lane & 7) + ((lane >> 4) << 3), (c0 >> 3) + ((lane >> 3) & 1));
+    return base + delta_at<PITCH>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1) + delta_at<PITCH>(r0, c0 >> 3);
 }
 
 // c += a b, one 16 x 8 x 16 bfloat16 product with float32 sums
@@ -162,6 +176,46 @@ __device__ __forceinline__ void split_frag(const float (&acc)[TILES][4], int ks,
         split_bf16<N>(acc[2 * ks + (i >> 1)][2 * (i & 1)], acc[2 * ks + (i >> 1)][2 * (i & 1) + 1], p);
 #pragma unroll
         for (int s = 0; s < N; ++s) a[s][i] = p[s];
+    }
+}
+
+// whether the product of terms a and b (counted from the largest) is above 2^-8 `most` of the whole
+__device__ __forceinline__ constexpr bool plane_pair(int a, int b, int most) { return a + b < most; }
+
+// K or Q planes of a chunk's `nt` live tokens into tiles [KP][C] of DKP columns, zero elsewhere
+template <int KP, int DKP, int C, int THREADS>
+__device__ __forceinline__ void load_tokens(unsigned dst, const DeltaPlanes &x, long long base,
+                                            int Dk, int nt, int tid) {
+    constexpr int PC = DKP / 8, PITCH = delta_pitch(DKP * 2);
+    for (int i = tid; i < KP * C * PC; i += THREADS) {
+        const int c = i % PC, r = (i / PC) % C, pl = i / (PC * C);
+        const bool live = r < nt && c * 8 < Dk;
+        const __nv_bfloat16 *src = x.p + pl * x.plane + base + (live ? r * x.s[1] + c * 8 : 0);
+        cp_async16_zfill(dst + pl * (C * PITCH) + delta_at<PITCH>(r, c), src, live);
+    }
+}
+
+// PL planes [C][C] of X or P as k_delta_local stored them (blocks on and below the diagonal)
+template <int PL, int C, int THREADS>
+__device__ __forceinline__ void load_planes(unsigned dst, const unsigned char *src, int tid) {
+    constexpr int XP = delta_pitch(C * 2);
+    for (int i = tid; i < PL * C * (C / 8); i += THREADS) {
+        const int c = i % (C / 8), r = (i / (C / 8)) % C, pl = i / (C * (C / 8));
+        if (c > 2 * (r >> 4) + 1) continue;
+        const int off = pl * C * XP + delta_at<XP>(r, c);
+        cp_async16_zfill(dst + off, src + off, true);
+    }
+}
+
+// COLS columns of a [tokens, Dv] tile (values, gradients), zero past the live tokens and columns
+template <typename T, int COLS, int C, int THREADS>
+__device__ __forceinline__ void load_values(unsigned dst, const T *src, long long row, int nt,
+                                            int cols, int tid) {
+    constexpr int VE = 16 / (int)sizeof(T), PC = COLS / VE, PITCH = delta_pitch(COLS * (int)sizeof(T));
+    for (int i = tid; i < C * PC; i += THREADS) {
+        const int c = i % PC, r = i / PC;
+        const bool live = r < nt && c * VE < cols;
+        cp_async16_zfill(dst + delta_at<PITCH>(r, c), live ? src + r * row + c * VE : src, live);
     }
 }
 
