@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Dict, Optional
 
@@ -33,6 +34,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libsdm.so")
 
 SDM_F32, SDM_BF16 = 0, 1
+DELTA_STEP_TOKENS = 16            # gated_delta: up to this many tokens go one by one
 KERNEL_KINDS = ("phase1", "solve", "gather", "dualmm", "dw", "phase2")
 FLAG_PER_STEP_KERNELS = 1
 FLAG_SNAPSHOT_BF16 = 2
@@ -57,12 +59,6 @@ class Shape(ctypes.Structure):
                 ("slab_steps", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
-class _DeltaShape(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "H", "Hk", "Dk", "Dv", "dtype")]
-                + [("scale", ctypes.c_float)]
-                + [(n + "_stride", ctypes.c_int64 * 3) for n in ("q", "k", "v", "decay", "beta", "grad")])
-
-
 class _DeviceStatus(ctypes.Structure):
     _fields_ = [("code", ctypes.c_int32), ("first_bad_token", ctypes.c_int32),
                 ("bad_slots", ctypes.c_int64), ("repeated_write_slots", ctypes.c_int64)]
@@ -75,6 +71,8 @@ _lib = None
 def library() -> ctypes.CDLL:
     """The loaded libsdm.so (built in-tree by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):
@@ -128,18 +126,17 @@ def library() -> ctypes.CDLL:
             lib.sdm_product_key_topk_backward.argtypes = [vp, vp, ll, ctypes.POINTER(ctypes.c_int),
                                                           i32, i32, i32, vp, vp]
             lib.sdm_product_key_topk_backward.restype = i32
-            dp = ctypes.POINTER(_DeltaShape)
-            lib.sdm_gated_delta_workspace_bytes.argtypes = [dp]
+            lib.sdm_gated_delta_workspace_bytes.argtypes = [vp]
             lib.sdm_gated_delta_workspace_bytes.restype = sz
-            lib.sdm_gated_delta.argtypes = [dp] + [vp] * 8 + [vp, sz, vp]
+            lib.sdm_gated_delta.argtypes = [vp] + [vp] * 8 + [vp, sz, vp]
             lib.sdm_gated_delta.restype = i32
-            lib.sdm_gated_delta_saved_bytes.argtypes = [dp]
+            lib.sdm_gated_delta_saved_bytes.argtypes = [vp]
             lib.sdm_gated_delta_saved_bytes.restype = sz
-            lib.sdm_gated_delta_save.argtypes = [dp] + [vp] * 8 + [vp, sz, vp, sz, vp]
+            lib.sdm_gated_delta_save.argtypes = [vp] + [vp] * 8 + [vp, sz, vp, sz, vp]
             lib.sdm_gated_delta_save.restype = i32
-            lib.sdm_gated_delta_backward_workspace_bytes.argtypes = [dp]
+            lib.sdm_gated_delta_backward_workspace_bytes.argtypes = [vp]
             lib.sdm_gated_delta_backward_workspace_bytes.restype = sz
-            lib.sdm_gated_delta_backward.argtypes = [dp] + [vp] * 6 + [vp, sz] + [vp] * 8 + [vp, sz, vp]
+            lib.sdm_gated_delta_backward.argtypes = [vp] + [vp] * 6 + [vp, sz] + [vp] * 8 + [vp, sz, vp]
             lib.sdm_gated_delta_backward.restype = i32
             lib.sdm_layer_norm.argtypes = [vp, ll, i32, ll, vp, vp, i32, ctypes.c_float, i32, vp, vp, vp]
             lib.sdm_layer_norm.restype = i32
@@ -695,61 +692,83 @@ def bank_sum(x: torch.Tensor, stream=None) -> torch.Tensor:
 # ------------------------------------------------------------------------------------------
 # the gated delta rule: the write/read's recurrence with dense keys
 # ------------------------------------------------------------------------------------------
+# A single token's kernel takes a few microseconds, so the checks below read each tensor property
+# once, and the shape goes to the library as packed bytes (include/sdm.h, sdm_delta_shape).
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
-    """A [B, T, heads, width] (or [B, T, heads]) input on the state's device, of any strides."""
+_DELTA_SHAPE = struct.Struct("=7if18q")
+
+
+def _on(stream, fn, *args, **kw):
+    """fn on another stream: its allocations belong to that stream, as its work does."""
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _call(fn, dev: torch.device, *args) -> None:
+    """One library call on dev and its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype, dev, es: int):
+    """(b, t, h) strides of an input [B, T, heads, width] (es: bytes an element) or, with es 0,
+    [B, T, heads], checked; a dimension of one element is never stepped along: stride 0."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the state on {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dim() == 4:
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+    st = t.stride()
+    B, T, H = shape[:3]
+    s = (st[0] if B > 1 else 0, st[1] if T > 1 else 0, st[2] if H > 1 else 0)
+    if es and B and T:
+        if st[3] != 1 and shape[3] > 1:
             raise ValueError(f"{name}'s last dimension must be contiguous")
-        es = t.element_size()
-        if t.numel() and (t.data_ptr() % 16 or any(n > 1 and s * es % 16 for n, s in
-                                                   zip(t.shape[:3], t.stride()[:3]))):
+        if ((s[0] | s[1] | s[2]) * es | t.data_ptr()) & 15:
             raise ValueError(f"{name}'s address and strides must be multiples of 16 bytes")
-    return t
-
-
-def _strides(t: Optional[torch.Tensor]):
-    # a dimension of one element is never stepped along: its stride says nothing
-    return ((0, 0, 0) if t is None else
-            tuple(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])))
+    return s
 
 
 def _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale, grad=None):
-    """Checks the inputs against each other; (shape struct, (B, T, H, Hk, Dk, Dv))."""
-    for t, name, dims in ((q, "q", 4), (k, "k", 4), (v, "v", 4)):
+    """Checks the inputs against each other; (packed shape, (B, T, H, Hk, Dk, Dv), device, dtype)."""
+    for t, name in ((q, "q"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
-        if t.dim() != dims:
+        if t.dim() != 4:
             raise ValueError(f"{name} must be [B, T, heads, width]")
     dev, dt = v.device, v.dtype
     if dev.type != "cuda":
         raise ValueError("q, k and v must be CUDA tensors")
     code = _dtype_code(dt)
-    B, T, Hk, Dk = q.shape
-    H, Dv = v.shape[2:]
-    _rows(q, "q", (B, T, Hk, Dk), dt, dev)
-    _rows(k, "k", (B, T, Hk, Dk), dt, dev)
-    _rows(v, "v", (B, T, H, Dv), dt, dev)
-    _rows(log_decay, "log_decay", (B, T, H), torch.float32, dev)
-    _rows(beta, "beta", (B, T, H), torch.float32, dev)
+    es = 2 if code == SDM_BF16 else 4
+    kshape, vshape = q.shape, v.shape
+    B, T, Hk, Dk = kshape
+    H, Dv = vshape[2], vshape[3]
+    if vshape[0] != B or vshape[1] != T:
+        raise ValueError(f"v must be [{B}, {T}, heads, width], got {tuple(vshape)}")
+    gshape = (B, T, H)
+    f32 = torch.float32
+    strides = (_rows(q, "q", kshape, dt, dev, es) + _rows(k, "k", kshape, dt, dev, es)
+               + _rows(v, "v", vshape, dt, dev, es) + _rows(log_decay, "log_decay", gshape, f32, dev, 0)
+               + _rows(beta, "beta", gshape, f32, dev, 0)
+               + ((0, 0, 0) if grad is None else _rows(grad, "grad_readings", vshape, dt, dev, es)))
     if valid_tokens is not None:
         _need(valid_tokens, "valid_tokens", (B,), torch.int32, dev)
-    if grad is not None:
-        _rows(grad, "grad_readings", (B, T, H, Dv), dt, dev)
     if scale is None:
         scale = Dk ** -0.5 if Dk else 1.0
-    shape = _DeltaShape(B, T, H, Hk, Dk, Dv, code, float(scale))
-    for name, t in (("q", q), ("k", k), ("v", v), ("decay", log_decay), ("beta", beta), ("grad", grad)):
-        getattr(shape, name + "_stride")[:] = _strides(t)
-    return shape, (B, T, H, Hk, Dk, Dv)
+    return (_DELTA_SHAPE.pack(B, T, H, Hk, Dk, Dv, code, scale, *strides), (B, T, H, Hk, Dk, Dv), dev, dt)
 
 
 def _bytes(n: int) -> int:
@@ -759,12 +778,21 @@ def _bytes(n: int) -> int:
     return int(n)
 
 
-def _scratch(workspace, nbytes: int, device) -> torch.Tensor:
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
+def _scratch(t, query, dev, *args):
+    """(tensor, bytes): the caller's buffer, or a new one of the size the library asks for."""
+    if t is None:
+        n = _bytes(query(*args))
+        return torch.empty(n, dtype=torch.uint8, device=dev), n
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError(f"workspaces and saved buffers must be contiguous uint8 tensors on {dev}")
+    return t, t.numel()
+
+
+def _result(t, name, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, shape, dtype, dev)
+    return t
 
 
 def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -779,21 +807,18 @@ def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.
     q, k [B, T, Hk, Dk] and v [B, T, H, Dv], float32 or bfloat16, any strides that are multiples of
     16 bytes; H a multiple of Hk (value head h uses key head h // (H // Hk)); Dk (up to 128) and Dv
     (up to 512) multiples of 16. log_decay, beta [B, T, H] float32. valid_tokens [B] int32 (None:
-    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step."""
-    shape, (B, T, H, Hk, Dk, Dv) = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
-    dev = v.device
+    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step; up to 16 tokens
+    need no workspace. What is allocated here belongs to ``stream`` (None: the current one)."""
+    if stream is not None:
+        return _on(stream, gated_delta, state, q, k, v, log_decay, beta, valid_tokens, scale=scale,
+                   readings=readings, workspace=workspace)
+    shape, (B, T, H, Hk, Dk, Dv), dev, dt = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
-    if readings is None:
-        readings = torch.empty((B, T, H, Dv), dtype=v.dtype, device=dev)
-    else:
-        _need(readings, "readings", (B, T, H, Dv), v.dtype, dev)
+    readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
     lib = library()
-    workspace = _scratch(workspace, _bytes(lib.sdm_gated_delta_workspace_bytes(ctypes.byref(shape))), dev)
-    with torch.cuda.device(dev):
-        _check(lib.sdm_gated_delta(
-            ctypes.byref(shape), _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-            _ptr(beta), _ptr(valid_tokens), _ptr(readings), _ptr(workspace), workspace.numel(),
-            _stream_ptr(stream)))
+    ws, n = (None, 0) if T <= DELTA_STEP_TOKENS else _scratch(workspace, lib.sdm_gated_delta_workspace_bytes, dev, shape)
+    _call(lib.sdm_gated_delta, dev, shape, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), beta.data_ptr(), _at(valid_tokens), readings.data_ptr(), _at(ws), n)
     return readings
 
 
@@ -804,21 +829,17 @@ def gated_delta_save(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     """gated_delta that also keeps what its backward needs: (readings, saved), with ``state``
     advanced in place. ``saved`` (uint8) holds the state at the start of every chunk of 64 (float32
     inputs: 32) tokens and the chunks' corrections."""
-    shape, (B, T, H, Hk, Dk, Dv) = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
-    dev = v.device
+    if stream is not None:
+        return _on(stream, gated_delta_save, state, q, k, v, log_decay, beta, valid_tokens, scale=scale,
+                   readings=readings, saved=saved, workspace=workspace)
+    shape, (B, T, H, Hk, Dk, Dv), dev, dt = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
-    if readings is None:
-        readings = torch.empty((B, T, H, Dv), dtype=v.dtype, device=dev)
-    else:
-        _need(readings, "readings", (B, T, H, Dv), v.dtype, dev)
+    readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
     lib = library()
-    workspace = _scratch(workspace, _bytes(lib.sdm_gated_delta_workspace_bytes(ctypes.byref(shape))), dev)
-    saved = _scratch(saved, _bytes(lib.sdm_gated_delta_saved_bytes(ctypes.byref(shape))), dev)
-    with torch.cuda.device(dev):
-        _check(lib.sdm_gated_delta_save(
-            ctypes.byref(shape), _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-            _ptr(beta), _ptr(valid_tokens), _ptr(readings), _ptr(saved), saved.numel(),
-            _ptr(workspace), workspace.numel(), _stream_ptr(stream)))
+    ws, n = _scratch(workspace, lib.sdm_gated_delta_workspace_bytes, dev, shape)
+    saved, m = _scratch(saved, lib.sdm_gated_delta_saved_bytes, dev, shape)
+    _call(lib.sdm_gated_delta_save, dev, shape, _at(state), _at(q), _at(k), _at(v), _at(log_decay),
+          _at(beta), _at(valid_tokens), _at(readings), _at(saved), m, _at(ws), n)
     return readings, saved
 
 
@@ -831,27 +852,26 @@ def gated_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     (the inputs' dtype; heads that share a key head are summed), grad_log_decay, grad_beta and
     grad_state (float32; of the initial state). ``grad_state`` [B, H, Dk, Dv] float32: the gradient
     of the final state (None: zero); it is not changed."""
-    shape, (B, T, H, Hk, Dk, Dv) = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale, grad_readings)
-    dev, dt = v.device, v.dtype
+    if stream is not None:
+        return _on(stream, gated_delta_backward, q, k, v, log_decay, beta, valid_tokens, saved, grad_readings,
+                   grad_state=grad_state, scale=scale, workspace=workspace)
+    shape, (B, T, H, Hk, Dk, Dv), dev, dt = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale, grad_readings)
     if grad_state is not None:
         _need(grad_state, "grad_state", (B, H, Dk, Dv), torch.float32, dev)
-    lib = library()
-    workspace = _scratch(workspace, _bytes(lib.sdm_gated_delta_backward_workspace_bytes(ctypes.byref(shape))), dev)
-    if not isinstance(saved, torch.Tensor):
+    if saved is None:
         raise TypeError("saved must be a tensor")
-    _scratch(saved, 0, dev)
+    saved, m = _scratch(saved, None, dev)
+    lib = library()
+    ws, n = _scratch(workspace, lib.sdm_gated_delta_backward_workspace_bytes, dev, shape)
     new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
     out = {"grad_q": torch.empty((B, T, Hk, Dk), dtype=dt, device=dev),
            "grad_k": torch.empty((B, T, Hk, Dk), dtype=dt, device=dev),
            "grad_v": torch.empty((B, T, H, Dv), dtype=dt, device=dev),
            "grad_log_decay": new(B, T, H), "grad_beta": new(B, T, H), "grad_state": new(B, H, Dk, Dv)}
-    with torch.cuda.device(dev):
-        _check(lib.sdm_gated_delta_backward(
-            ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta),
-            _ptr(valid_tokens), _ptr(saved), saved.numel(), _ptr(grad_readings), _ptr(grad_state),
-            _ptr(out["grad_state"]), _ptr(out["grad_q"]), _ptr(out["grad_k"]), _ptr(out["grad_v"]),
-            _ptr(out["grad_log_decay"]), _ptr(out["grad_beta"]), _ptr(workspace),
-            workspace.numel(), _stream_ptr(stream)))
+    _call(lib.sdm_gated_delta_backward, dev, shape, _at(q), _at(k), _at(v), _at(log_decay), _at(beta),
+          _at(valid_tokens), _at(saved), m, _at(grad_readings), _at(grad_state), _at(out["grad_state"]),
+          _at(out["grad_q"]), _at(out["grad_k"]), _at(out["grad_v"]), _at(out["grad_log_decay"]),
+          _at(out["grad_beta"]), _at(ws), n)
     return out
 
 
@@ -863,15 +883,18 @@ def _norm_rows(x: torch.Tensor, name: str):
     """(rows, columns, row stride) of x [..., n] as rows of n contiguous elements one stride apart."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if x.device.type != "cuda" or x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if not x.is_cuda or not shape or shape[-1] < 1:
         raise ValueError(f"{name} must be a CUDA tensor of rows, [..., n] with n >= 1")
-    _dtype_code(x.dtype)
-    n = x.shape[-1]
+    n = shape[-1]
     rows = x.numel() // n
-    if n > 1 and x.stride(-1) != 1:
+    if x.is_contiguous():
+        return rows, n, n
+    strides = x.stride()
+    if n > 1 and strides[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     step, span = None, 1                       # the leading dimensions have to be one run of rows
-    for size, stride in reversed(list(zip(x.shape[:-1], x.stride()[:-1]))):
+    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if size == 1:
             continue
         if step is None:
@@ -882,31 +905,27 @@ def _norm_rows(x: torch.Tensor, name: str):
     return rows, n, n if step is None or rows == 0 else step
 
 
-def _norm_params(x, weight, bias):
-    n = x.shape[-1]
+def _norm_params(x, n, weight, bias):
     wdt = torch.float32
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
-            if t.dtype not in (torch.float32, x.dtype):
-                raise TypeError(f"{name} must be float32 or {x.dtype}, got {t.dtype}")
-            _need(t, name, (n,), t.dtype, x.device)
             wdt = t.dtype
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+            if wdt is not torch.float32 and wdt is not x.dtype:
+                raise TypeError(f"{name} must be float32 or {x.dtype}, got {wdt}")
+            _need(t, name, (n,), wdt, x.device)
+    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
         raise TypeError("weight and bias must have one dtype")
     return _dtype_code(wdt)
 
 
-def _layer_norm(x, weight, bias, eps, out, stats, stream):
+def _layer_norm(x, weight, bias, eps, out, stats):
     rows, n, step = _norm_rows(x, "x")
-    wdt = _norm_params(x, weight, bias)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    else:
-        _need(out, "out", x.shape, x.dtype, x.device)
-    with torch.cuda.device(x.device):
-        _check(library().sdm_layer_norm(_ptr(x), rows, n, step, _ptr(weight), _ptr(bias), wdt,
-                                        float(eps), _dtype_code(x.dtype), _ptr(out), _ptr(stats),
-                                        _stream_ptr(stream)))
+    dt, dev = x.dtype, x.device
+    code = _dtype_code(dt)
+    wdt = _norm_params(x, n, weight, bias)
+    out = torch.empty(x.shape, dtype=dt, device=dev) if out is None else _result(out, "out", x.shape, dt, dev)
+    _call(library().sdm_layer_norm, dev, x.data_ptr(), rows, n, step, _at(weight), _at(bias), wdt, eps,
+          code, out.data_ptr(), _at(stats))
     return out
 
 
@@ -915,18 +934,23 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Layer norm over x's last dimension (1..16384 columns): (x - mean) rstd weight + bias, in
     float32, rounded once to x's dtype (float32 or bfloat16). weight and bias [n], float32 or x's
-    dtype, each optional. x's rows may be strided; the result is contiguous."""
-    return _layer_norm(x, weight, bias, eps, out, None, stream)
+    dtype, each optional. x's rows may be strided; the result is contiguous. What is allocated here
+    belongs to ``stream`` (None: the current one)."""
+    if stream is not None:
+        return _on(stream, layer_norm, x, weight, bias, eps=eps, out=out)
+    return _layer_norm(x, weight, bias, eps, out, None)
 
 
 def layer_norm_save(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                     bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
                     out: Optional[torch.Tensor] = None, stream=None):
     """layer_norm that also returns what its backward needs: (y, stats [..., 2] float32)."""
+    if stream is not None:
+        return _on(stream, layer_norm_save, x, weight, bias, eps=eps, out=out)
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")
     stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device)
-    return _layer_norm(x, weight, bias, eps, out, stats, stream), stats
+    return _layer_norm(x, weight, bias, eps, out, stats), stats
 
 
 def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
@@ -934,22 +958,24 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: Optional[to
                         stream=None) -> Dict[str, torch.Tensor]:
     """The backward after layer_norm_save: a dict of grad_x (x's dtype) and, where the forward had
     them, grad_weight and (``bias``) grad_bias, float32 [n], summed over the rows in a fixed order."""
+    if stream is not None:
+        return _on(stream, layer_norm_backward, grad, x, weight, stats, bias=bias, workspace=workspace)
     rows, n, step = _norm_rows(x, "x")
-    grows, gn, gstep = _norm_rows(grad, "grad")
-    if grad.shape != x.shape or grad.dtype != x.dtype or grad.device != x.device:
+    gstep = _norm_rows(grad, "grad")[2]
+    dt, dev = x.dtype, x.device
+    if grad.shape != x.shape or grad.dtype is not dt or grad.device != dev:
         raise ValueError("grad must have x's shape, dtype and device")
-    wdt = _norm_params(x, weight, None)
-    _need(stats, "stats", tuple(x.shape[:-1]) + (2,), torch.float32, x.device)
-    out = {"grad_x": torch.empty(x.shape, dtype=x.dtype, device=x.device)}
+    code = _dtype_code(dt)
+    wdt = _norm_params(x, n, weight, None)
+    _need(stats, "stats", x.shape[:-1] + (2,), torch.float32, dev)
+    out = {"grad_x": torch.empty(x.shape, dtype=dt, device=dev)}
     if weight is not None:
-        out["grad_weight"] = torch.empty(n, dtype=torch.float32, device=x.device)
+        out["grad_weight"] = torch.empty(n, dtype=torch.float32, device=dev)
     if bias:
-        out["grad_bias"] = torch.empty(n, dtype=torch.float32, device=x.device)
+        out["grad_bias"] = torch.empty(n, dtype=torch.float32, device=dev)
     lib = library()
-    workspace = _scratch(workspace, _bytes(lib.sdm_layer_norm_workspace_bytes(rows, n)), x.device)
-    with torch.cuda.device(x.device):
-        _check(lib.sdm_layer_norm_backward(
-            _ptr(grad), gstep, _ptr(x), step, rows, n, _ptr(weight), wdt, _ptr(stats),
-            _dtype_code(x.dtype), _ptr(out["grad_x"]), _ptr(out.get("grad_weight")),
-            _ptr(out.get("grad_bias")), _ptr(workspace), workspace.numel(), _stream_ptr(stream)))
+    ws, nbytes = _scratch(workspace, lib.sdm_layer_norm_workspace_bytes, dev, rows, n)
+    _call(lib.sdm_layer_norm_backward, dev, grad.data_ptr(), gstep, x.data_ptr(), step, rows, n,
+          _at(weight), wdt, stats.data_ptr(), code, out["grad_x"].data_ptr(), _at(out.get("grad_weight")),
+          _at(out.get("grad_bias")), ws.data_ptr(), nbytes)
     return out
