@@ -29,6 +29,8 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.scale = s->scale;
     d.C = delta_chunk(s->dtype);
     d.pp = s->dtype == SDM_BF16 ? 2 : 3;
+    d.tc = s->dtype == SDM_BF16 && s->Dv > 64;
+    d.spin = wait_limit();
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
     if ((long long)s->B * s->H * d.Nt >= (1LL << 31) || (long long)s->B * s->H * (s->Dv / 16) >= (1LL << 31))
@@ -72,7 +74,7 @@ struct DeltaLayout {
 
 DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     DeltaLayout l{};
-    size_t at = 0;
+    size_t at = kAlign;                  // behind the status block
     auto take = [&](size_t bytes) {
         const size_t here = at;
         at += delta_up(bytes);
@@ -122,7 +124,7 @@ cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaLayout
                         DeltaPlanes &q, DeltaPlanes &k, DeltaLocal &w, cudaStream_t st) {
     q = delta_planes(d, in.q, d.qs, ws + l.q);
     k = delta_planes(d, in.k, d.ks, ws + l.k);
-    w = DeltaLocal{ws + l.x, ws + l.p, reinterpret_cast<float *>(ws + l.aux)};
+    w = DeltaLocal{ws + l.x, ws + l.p, reinterpret_cast<float *>(ws + l.aux), reinterpret_cast<DevStatus *>(ws)};
     if (d.dtype == SDM_F32) {
         cudaError_t e = launch_delta_split(d, in.q, d.qs, d.Hk, d.Dk, const_cast<__nv_bfloat16 *>(q.p), st);
         if (e == cudaSuccess)
@@ -172,7 +174,9 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
     cudaError_t e = delta_local(d, in, l, static_cast<unsigned char *>(workspace), qp, kp, w, st);
     float *snap = save ? static_cast<float *>(saved) : nullptr;
     float *u = save ? reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_snap(d)) : nullptr;
-    if (e == cudaSuccess) e = launch_delta_scan(d, in, qp, kp, w, state, readings, snap, u, st);
+    if (e == cudaSuccess)
+        e = d.tc ? launch_delta_scan_tc(d, in, w, state, readings, snap, u, st)
+                 : launch_delta_scan(d, in, qp, kp, w, state, readings, snap, u, st);
     return delta_status(e);
 }
 
@@ -212,6 +216,7 @@ size_t sdm_gated_delta_backward_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
     if (delta_check(shape, d) != SDM_OK) return 0;
     d.pp = 3;
+    d.tc = 0;
     return delta_layout(d, true).bytes + kAlign;
 }
 
@@ -225,6 +230,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     int rc = delta_check(shape, d);
     if (rc != SDM_OK) return rc;
     d.pp = 3;                            // P reaches float32 gradients
+    d.tc = 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d.B == 0) return SDM_OK;
     if (!grad_state) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");

@@ -31,7 +31,7 @@ struct LocalSmem {
 // below the diagonal), the decays, then the inverse of I + N, N = diag(beta) A: 16 x 16 diagonal
 // blocks by substitution, a warp each, a lane a column; then warp j goes down block column j,
 // X_ij = -X_ii sum_l N_il X_lj, which needs only its own column and the diagonal blocks.
-template <int KP, int DKP, int C, int PP>
+template <int KP, int DKP, int C, int PP, bool TC>
 __global__ void __launch_bounds__(2 * C)
     k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w) {
     using L = LocalSmem<KP, DKP, C>;
@@ -39,6 +39,9 @@ __global__ void __launch_bounds__(2 * C)
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long bhn = blockIdx.x;
+    if (bhn == 0 && tid == 0) *w.status = DevStatus{};
+    auto plane_at = [](int r, int c) { return TC ? tc_at(r, c) : delta_at<XP>(r, c); };
+    constexpr int PLANE = C * (TC ? 128 : XP);
     const int n = (int)(bhn % d.Nt);
     const long long bh = bhn / d.Nt;
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(2 * C)
                             }
             }
         }
-        unsigned char *pimg = w.p + bhn * (size_t)(PP * C * XP);
+        unsigned char *pimg = w.p + bhn * (size_t)(PP * PLANE);
 #pragma unroll
         for (int j = 0; j < C / 8; ++j) {
             if (j > 2 * warp + 1) break;
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(2 * C)
                 split_bf16<PP>(pp[0], pp[1], pl);
 #pragma unroll
                 for (int p = 0; p < PP; ++p)
-                    *reinterpret_cast<unsigned *>(pimg + p * C * XP + delta_at<XP>(t, j) + 4 * (lane & 3)) = pl[p];
+                    *reinterpret_cast<unsigned *>(pimg + p * PLANE + plane_at(t, j) + 4 * (lane & 3)) = pl[p];
             }
         }
     }
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(2 * C)
         }
     }
     __syncthreads();
-    unsigned char *ximg = w.x + bhn * (size_t)(3 * C * XP);
+    unsigned char *ximg = w.x + bhn * (size_t)(3 * PLANE);
     for (int i = tid; i < C * (C / 8); i += THREADS) {
         const int r = i / (C / 8), c = i % (C / 8);
         if (c > 2 * (r >> 4) + 1) continue;
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(2 * C)
         }
 #pragma unroll
         for (int p = 0; p < 3; ++p)
-            *reinterpret_cast<uint4 *>(ximg + p * C * XP + delta_at<XP>(r, c)) =
+            *reinterpret_cast<uint4 *>(ximg + p * PLANE + plane_at(r, c)) =
                 make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
     }
 }
@@ -527,10 +530,10 @@ cudaError_t scan_any(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q
     return d.Dk <= 64 ? size(std::integral_constant<int, 64>{}) : size(std::integral_constant<int, 128>{});
 }
 
-template <int KP, int DKP, int C, int PP>
+template <int KP, int DKP, int C, int PP, bool TC = false>
 cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                       const DeltaLocal &w, cudaStream_t st) {
-    auto kern = k_delta_local<KP, DKP, C, PP>;
+    auto kern = k_delta_local<KP, DKP, C, PP, TC>;
     constexpr int bytes = LocalSmem<KP, DKP, C>::BYTES;
     set_kernel_smem(kern, bytes);
     kern<<<(unsigned)delta_chunks(d), 2 * C, bytes, st>>>(d, in, q, k, w);
@@ -541,6 +544,9 @@ cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &
 
 cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                                const DeltaLocal &w, cudaStream_t st) {
+    if (d.tc && d.pp == 2)
+        return d.Dk <= 64 ? local_one<1, 64, 64, 2, true>(d, in, q, k, w, st)
+                          : local_one<1, 128, 64, 2, true>(d, in, q, k, w, st);
     if (d.dtype == SDM_BF16 && d.pp == 2)
         return d.Dk <= 64 ? local_one<1, 64, 64, 2>(d, in, q, k, w, st) : local_one<1, 128, 64, 2>(d, in, q, k, w, st);
     if (d.dtype == SDM_BF16)

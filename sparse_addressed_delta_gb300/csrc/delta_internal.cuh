@@ -17,7 +17,9 @@ struct DeltaDims {
     int C, Nt;                           // chunk length, chunks a sequence
     int pp;                              // planes of P: 2 where it only reaches bfloat16 readings
     int dtype;
+    int tc;                              // 1: the scans run on tcgen05 (planes of X and P in its layout)
     float scale;
+    long long spin;                      // polls before a kernel's wait gives up (sdm_set_wait_limit)
     long long qs[3], ks[3], vs[3], gs[3], bs[3], os[3];   // element strides of (b, t, h)
 };
 
@@ -39,11 +41,13 @@ struct DeltaPlanes {
 //   x   [3][C][C] bfloat16 planes of (I + diag(beta) A)^-1
 //   p   [pp][C][C] planes of the decayed scale q k^T
 //   aux [3][C] float: exp(L_t), exp(L_C - L_t), beta_t
-// The planes' rows have shared memory's pitch, so the scans copy them as they are. Blocks above the
-// diagonal are never written and never read.
+// The planes' rows have shared memory's layout (delta_pitch, or tcgen05's 128-byte rows with permuted
+// pieces, tc_at), so the scans copy them as they are. Blocks above the diagonal are never written and
+// never used. k_delta_local also clears the workspace's status block.
 struct DeltaLocal {
     unsigned char *x, *p;
     float *aux;
+    DevStatus *status;
 };
 
 __host__ __device__ constexpr int delta_chunk(int dtype) { return dtype == SDM_BF16 ? 64 : 32; }
@@ -62,6 +66,9 @@ cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const Delt
 cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                               const DeltaPlanes &k, const DeltaLocal &w, float *state, void *o,
                               float *snap, float *u, cudaStream_t st);
+
+cudaError_t launch_delta_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state,
+                                 void *o, float *snap, float *u, cudaStream_t st);
 
 // Outputs of the backward and what its kernels hand on.
 struct DeltaBack {
@@ -100,6 +107,10 @@ __device__ __forceinline__ float delta_decay(float g) { return g < kDeltaMinDeca
 __host__ __device__ constexpr int delta_pitch(int bytes) { return bytes + 16; }
 template <int PITCH>
 __device__ __forceinline__ int delta_at(int r, int c) { return r * PITCH + c * 16; }
+
+// The tensor core's tiles (tcgen05): rows of 128 bytes (64 bfloat16), 16-byte piece c of row r at piece
+// c ^ (r % 8); tiles start at multiples of 1024 bytes; wider rows are several such tiles.
+__device__ __forceinline__ int tc_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 __device__ __forceinline__ void cp_async16_zfill(unsigned dst, const void *src, bool live) {
     const int n = live ? 16 : 0;
