@@ -20,10 +20,13 @@
 namespace sdm {
 namespace {
 
-template <int KP, int DKP, int C>
+template <int KP, int DKP, int C, bool TC>
 struct LocalSmem {
-    static constexpr int KPITCH = delta_pitch(DKP * 2), TILE = C * KPITCH, NP = C + 4;
-    static constexpr int Q = KP * TILE, N = 2 * KP * TILE, X = N + C * NP * 4, G = X + C * NP * 4;
+    static constexpr int KPITCH = delta_pitch(DKP * 2), TILE = C * KPITCH, NP = C + 4, XP = delta_pitch(C * 2);
+    // K and Q make room for the inverse (and its planes) once their products are taken
+    static constexpr int Q = KP * TILE, X = 0, XPL = C * NP * 4, FIRST = 2 * KP * TILE;
+    static constexpr int SECOND = XPL + (TC ? 2 * C * XP : 0);
+    static constexpr int N = FIRST > SECOND ? FIRST : SECOND, G = N + C * NP * 4;
     static constexpr int BYTES = G + 3 * C * 4;
 };
 
@@ -31,10 +34,12 @@ struct LocalSmem {
 // below the diagonal), the decays, then the inverse of I + N, N = diag(beta) A: 16 x 16 diagonal
 // blocks by substitution, a warp each, a lane a column; then warp j goes down block column j,
 // X_ij = -X_ii sum_l N_il X_lj, which needs only its own column and the diagonal blocks.
+// TC: for the tcgen05 scan, Y = X diag(beta) in the place of X and Z = P Y in the place of P (the product
+// P X from two terms of each, as exact as the bfloat16 readings need).
 template <int KP, int DKP, int C, int PP, bool TC>
 __global__ void __launch_bounds__(2 * C)
     k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w) {
-    using L = LocalSmem<KP, DKP, C>;
+    using L = LocalSmem<KP, DKP, C, TC>;
     constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = delta_pitch(C * 2), KPI = L::KPITCH;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -95,6 +100,7 @@ __global__ void __launch_bounds__(2 * C)
     cp_async_wait<0>();
     __syncthreads();
 
+    float pv[TC ? C / 8 : 1][4];
     {
         float kk[C / 8][4] = {}, qk[C / 8][4] = {};
 #pragma unroll
@@ -141,15 +147,20 @@ __global__ void __launch_bounds__(2 * C)
                     pp[e] = s <= t ? d.scale * qk[j][2 * half + e] * f : 0.f;
                 }
                 *reinterpret_cast<float2 *>(N + t * NP + 8 * j + 2 * (lane & 3)) = make_float2(nn[0], nn[1]);
-                unsigned pl[PP];
-                split_bf16<PP>(pp[0], pp[1], pl);
+                if constexpr (TC) {
+                    pv[j][2 * half] = pp[0];
+                    pv[j][2 * half + 1] = pp[1];
+                } else {
+                    unsigned pl[PP];
+                    split_bf16<PP>(pp[0], pp[1], pl);
 #pragma unroll
-                for (int p = 0; p < PP; ++p)
-                    *reinterpret_cast<unsigned *>(pimg + p * PLANE + plane_at(t, j) + 4 * (lane & 3)) = pl[p];
+                    for (int p = 0; p < PP; ++p)
+                        *reinterpret_cast<unsigned *>(pimg + p * PLANE + plane_at(t, j) + 4 * (lane & 3)) = pl[p];
+                }
             }
         }
     }
-    __syncwarp();
+    __syncthreads();                                             // K and Q are used
     if (lane < 16) {
         float x[16];
         const float *D = N + (16 * warp) * NP + 16 * warp;
@@ -204,16 +215,63 @@ __global__ void __launch_bounds__(2 * C)
     for (int i = tid; i < C * (C / 8); i += THREADS) {
         const int r = i / (C / 8), c = i % (C / 8);
         if (c > 2 * (r >> 4) + 1) continue;
-        unsigned pl[4][3];
+        unsigned pl[4][3], raw[4][2];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 x = *reinterpret_cast<const float2 *>(X + r * NP + 8 * c + 2 * e);
-            split_bf16<3>(x.x, x.y, pl[e]);
+            if constexpr (TC) {
+                split_bf16<2>(x.x, x.y, raw[e]);
+                split_bf16<3>(x.x * be[8 * c + 2 * e], x.y * be[8 * c + 2 * e + 1], pl[e]);
+            } else {
+                split_bf16<3>(x.x, x.y, pl[e]);
+            }
         }
+        if constexpr (TC)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                *reinterpret_cast<uint4 *>(smem + L::XPL + p * C * XP + delta_at<XP>(r, c)) =
+                    make_uint4(raw[0][p], raw[1][p], raw[2][p], raw[3][p]);
 #pragma unroll
         for (int p = 0; p < 3; ++p)
             *reinterpret_cast<uint4 *>(ximg + p * PLANE + plane_at(r, c)) =
                 make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
+    }
+    if constexpr (TC) {
+        __syncthreads();
+        float z[C / 8][4] = {};
+        const unsigned sx = smem_u32(smem) + L::XPL;
+#pragma unroll
+        for (int ks = 0; ks < NB; ++ks) {                         // the accumulators of P are its A operand
+            if (ks > warp) break;
+            unsigned a[2][4];
+            split_frag<2>(pv, ks, a);
+#pragma unroll
+            for (int jj = 0; jj <= ks; ++jj) {
+                unsigned bb[2][4];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma_bf16(z[2 * jj + e], a[1], bb[0][2 * e], bb[0][2 * e + 1]);
+                    mma_bf16(z[2 * jj + e], a[0], bb[1][2 * e], bb[1][2 * e + 1]);
+                    mma_bf16(z[2 * jj + e], a[0], bb[0][2 * e], bb[0][2 * e + 1]);
+                }
+            }
+        }
+        unsigned char *zimg = w.p + bhn * (size_t)(PP * PLANE);
+#pragma unroll
+        for (int j = 0; j < C / 8; ++j) {
+            if (j > 2 * warp + 1) break;
+            const float2 bt = *reinterpret_cast<const float2 *>(be + 8 * j + 2 * (lane & 3));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                unsigned pl[PP];
+                split_bf16<PP>(z[j][2 * half] * bt.x, z[j][2 * half + 1] * bt.y, pl);
+#pragma unroll
+                for (int p = 0; p < PP; ++p)
+                    *reinterpret_cast<unsigned *>(zimg + p * PLANE + plane_at(16 * warp + (lane >> 2) + 8 * half, j) + 4 * (lane & 3)) = pl[p];
+            }
+        }
     }
 }
 
@@ -534,7 +592,7 @@ template <int KP, int DKP, int C, int PP, bool TC = false>
 cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                       const DeltaLocal &w, cudaStream_t st) {
     auto kern = k_delta_local<KP, DKP, C, PP, TC>;
-    constexpr int bytes = LocalSmem<KP, DKP, C>::BYTES;
+    constexpr int bytes = LocalSmem<KP, DKP, C, TC>::BYTES;
     set_kernel_smem(kern, bytes);
     kern<<<(unsigned)delta_chunks(d), 2 * C, bytes, st>>>(d, in, q, k, w);
     return cudaGetLastError();

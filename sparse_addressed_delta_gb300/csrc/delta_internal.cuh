@@ -39,7 +39,8 @@ struct DeltaPlanes {
 
 // Per chunk and head, written by the chunk-local kernel (k_delta_local) for the scans:
 //   x   [3][C][C] bfloat16 planes of (I + diag(beta) A)^-1
-//   p   [pp][C][C] planes of the decayed scale q k^T
+//   p   [pp][C][C] planes of P, the decayed scale q k^T
+//   (for the tcgen05 scan: x holds Y = X diag(beta), p holds Z = P Y)
 //   aux [3][C] float: exp(L_t), exp(L_C - L_t), beta_t
 // The planes' rows have shared memory's layout (delta_pitch, or tcgen05's 128-byte rows with permuted
 // pieces, tc_at), so the scans copy them as they are. Blocks above the diagonal are never written and

@@ -22,67 +22,100 @@ __device__ __forceinline__ uint64_t tc_n_major(uint32_t addr, uint32_t next) {
 }
 
 // instruction descriptor: bfloat16 x bfloat16 -> float32, M = 128, N columns
-template <bool N_MAJOR>
+template <bool B_N_MAJOR, bool A_M_MAJOR = false>
 __device__ __forceinline__ constexpr uint32_t tc_idesc(int n) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (N_MAJOR ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
-           ((uint32_t)(128 >> 4) << 24);
+    return (1u << 4) | (1u << 7) | (1u << 10) | (A_M_MAJOR ? 1u << 15 : 0u) | (B_N_MAJOR ? 1u << 16 : 0u) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// d [128 lanes x N] (+)= a [128 lanes x 16, two bfloat16 a column] b
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+// The products are issued by one lane (`one`: elected once) of a converged warp whose operands are
+// uniform: they then stay in uniform registers, and a product issues in 14 cycles; issued from a branch
+// that only one lane takes, each one costs 48 whatever its size (measured with M = 128; N = 64 runs in 33).
+__device__ __forceinline__ uint32_t tc_elect() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one;
+}
+// d [128 lanes x N] (+)= a [128 lanes x 16, two bfloat16 a column of tensor memory] b
+__device__ __forceinline__ void tc_mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(one)
+        : "memory");
+}
+// the same with both operands in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(one)
         : "memory");
 }
 
-__device__ __forceinline__ void tc_commit_to(unsigned long long *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void tc_commit_to(uint32_t one, unsigned long long *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+        "r"(one)
+        : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 columns of the warp's 32 lanes
-__device__ __forceinline__ void tc_load32(uint32_t addr, float (&v)[32]) {
+// 16 columns of the warp's 32 lanes
+__device__ __forceinline__ void tc_load16(uint32_t addr, float (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];\n"
         "tcgen05.wait::ld.sync.aligned;"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
           "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
-          "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
-          "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+          "=f"(v[14]), "=f"(v[15])
         : "r"(addr)
         : "memory");
 }
-// 16 columns of the warp's 32 lanes
-__device__ __forceinline__ void tc_store16(uint32_t addr, const unsigned (&v)[16]) {
+// 16 columns of 16 lanes from `addr` on and of the 16 behind them, in the fragments of 8 x 8 blocks: for
+// half l and 8 columns c, v[l][4 c ..] is (lane / 4, 2 (lane % 4)), its right neighbour, and both of row + 8
+__device__ __forceinline__ void tc_load_frag16(uint32_t addr, float (&v)[2][8]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0][0]), "=f"(v[0][1]), "=f"(v[0][2]), "=f"(v[0][3]), "=f"(v[0][4]), "=f"(v[0][5]),
+          "=f"(v[0][6]), "=f"(v[0][7]), "=f"(v[1][0]), "=f"(v[1][1]), "=f"(v[1][2]), "=f"(v[1][3]),
+          "=f"(v[1][4]), "=f"(v[1][5]), "=f"(v[1][6]), "=f"(v[1][7])
+        : "r"(addr), "r"(addr + (16u << 16))
         : "memory");
 }
+__device__ __forceinline__ void tc_store8(uint32_t addr, const unsigned (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 
-// 32 floats as N bfloat16 planes of 16 packed columns, plane p at addr + p * step
+// 16 floats as N bfloat16 planes of 8 packed columns, plane p at addr + p * step
 template <int N>
-__device__ __forceinline__ void tc_store_planes(uint32_t addr, uint32_t step, const float (&x)[32]) {
-    unsigned p[N][16];
+__device__ __forceinline__ void tc_store_planes(uint32_t addr, uint32_t step, const float (&x)[16]) {
+    unsigned p[N][8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
         unsigned s[N];
         split_bf16<N>(x[2 * i], x[2 * i + 1], s);
 #pragma unroll
         for (int m = 0; m < N; ++m) p[m][i] = s[m];
     }
 #pragma unroll
-    for (int m = 0; m < N; ++m) tc_store16(addr + m * step, p[m]);
+    for (int m = 0; m < N; ++m) tc_store8(addr + m * step, p[m]);
+}
+
+// four 8 x 8 blocks of bfloat16 fragments stored transposed: lane 8 b + r gives the address of row r (a
+// column of block b)
+__device__ __forceinline__ void stsm4t(unsigned addr, const unsigned (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 // Waits for a phase of `bar`, at most `limit` polls; gives up at once when another thread of the
