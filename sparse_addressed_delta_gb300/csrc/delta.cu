@@ -1,7 +1,7 @@
 // C ABI of the gated delta rule (declared and documented in include/sdm.h): argument checks and the
 // launch sequence. Everything is queued on the caller's stream; nothing is allocated and nothing
 // synchronizes.
-#include "delta_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace sdm {
 namespace {
@@ -29,7 +29,6 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.scale = s->scale;
     d.C = delta_chunk(s->dtype);
     d.pp = s->dtype == SDM_BF16 ? 2 : 3;
-    d.tc = s->dtype == SDM_BF16 && s->Dv > 64;
     d.spin = wait_limit();
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
@@ -45,6 +44,8 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
         if (d.qs[i] < 0 || d.ks[i] < 0 || d.vs[i] < 0 || d.gs[i] < 0 || d.bs[i] < 0 || d.os[i] < 0)
             return set_error(SDM_ERR_INVALID, "gated delta: negative stride");
     }
+    d.tc = s->dtype == SDM_BF16 && s->Dv > 64 && tc_tensor_fits(d.qs, d.B, d.T, d.Hk) &&
+           tc_tensor_fits(d.ks, d.B, d.T, d.Hk) && tc_tensor_fits(d.vs, d.B, d.T, d.H);
     return SDM_OK;
 }
 

@@ -11,38 +11,51 @@
 // in float32 for the whole sequence; the tensor core only ever sums one chunk's update.
 //
 // What bounds it: every chunk's chain R -> w -> U -> update -> S, products and the threads' work in
-// turn; the values' products and the readings run in its gaps.
+// turn. The chain runs in two halves, one behind the other: half the warps own the chunk's first 32
+// tokens and the first half of Dk, the others the rest. The triangular products let the first tokens'
+// U finish before the second tokens' w is there, the update's products start with the first tokens,
+// and the first half of the new S enters the next chunk's R while the second is being made. The values'
+// products and the readings run in the gaps.
 //
-// Warps 0..15 compute (lanes 32 (warp % 4).., column quarter warp / 4), warp 16 issues the products,
-// warps 17..20 copy (a thread a 16-byte column, so that its addresses only step). Two stages of chunk inputs. Every wait is bounded: one that gives up sets
-// SDM_ERR_TIMEOUT in the status block, and the block leaves after its copies and products in flight.
+// Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the tokens and of Dk), warp 16 issues
+// the products, warp 17 loads, warp 18 stores the readings; K, Q, V and the readings move as tensor
+// copies. Two stages of chunk inputs, two buffers of readings. Every wait is bounded: one that gives up
+// sets SDM_ERR_TIMEOUT in the status block, and the block leaves after its copies and products in flight.
 #include "tcgen05.cuh"
 
 namespace sdm {
 namespace {
 
 constexpr int kTcC = 64;
-constexpr int kTcWarps = 16, kTcCopy = 128, kTcThreads = 32 * kTcWarps + 32 + kTcCopy;
+constexpr int kTcWarps = 16, kTcThreads = 32 * (kTcWarps + 3);
 
 template <int DKP>
 struct TcScan {
     static constexpr int TILE = kTcC * 128;                        // 64 columns of a token tile
     static constexpr int K = 0, Q = K + DKP / 64 * TILE, Y = Q + DKP / 64 * TILE, Z = Y + 3 * TILE;
     static constexpr int V = Z + 2 * TILE, STAGE = V + 2 * TILE;
-    static constexpr int AUX = 2 * STAGE, BARS = AUX + 2 * 512, BYTES = BARS + 256 + 1024;
+    static constexpr int O = 2 * STAGE, AUX = O + 2 * 2 * TILE,   // readings: two buffers like V's
+                          BARS = AUX + 2 * 512, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    // Tensor memory columns: planes of S (once they are used: of the decayed U), planes of w (then the
-    // update), R (then S^T Q^T), U, the readings' rest
-    static constexpr int SP = 0, UP = 3 * (DKP / 2), R = UP + 128, U = R + 64, O = U + 64;
-    static_assert(O + 64 <= 512, "tensor memory");
+    // Tensor memory columns: planes of S, planes of w (then the update), R (then S^T Q^T), U (then, in
+    // each quarter's own 16 columns, two planes of the decayed U), the readings' rest. The decayed U's
+    // third plane takes the second half of S's third, which only R reads.
+    static constexpr int SP = 0, UP = 3 * (DKP / 2), R = UP + 128, U = R + 64, OA = U + 64;
+    static constexpr int LO = DKP == 128 ? SP + 160 : OA + 64;
+    static_assert((DKP == 128 ? OA + 64 : LO + 32) <= 512, "tensor memory");
 };
 
-enum { B_FULL = 0, B_EMPTY = 2, B_S = 4, B_W, B_U, B_READ, B_R, B_O1, B_UACC, B_O2, B_UPD, B_DRAIN, B_BULK, B_COUNT = B_BULK + 2 };
+enum {
+    B_FULL = 0, B_EMPTY = 2, B_OUT = 4, B_OFREE = 6,               // [stage]
+    B_S = 8, B_W = 10, B_U = 12, B_R = 14, B_UACC = 16, B_UPD = 18, // [half]
+    B_READ = 20, B_O1, B_O2, B_DRAIN, B_BULK, B_COUNT = B_BULK + 2
+};
 
 template <int DKP, bool SAVE>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    k_delta_scan_tc(DeltaDims d, DeltaIn in, DeltaLocal w, float *state, __nv_bfloat16 *o, float *snap,
-                    float *usave) {
+    k_delta_scan_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, DeltaDims d,
+                    DeltaIn in, DeltaLocal w, float *state, __nv_bfloat16 *o, float *snap, float *usave) {
     using L = TcScan<DKP>;
     constexpr int C = kTcC, HD = DKP / 4;                          // columns of S a thread
     extern __shared__ unsigned char raw[];
@@ -58,11 +71,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar + B_FULL + i, kTcCopy);
+            mbar_init(bar + B_FULL + i, 32);
             mbar_init(bar + B_EMPTY + i, kTcWarps + 1);
+            mbar_init(bar + B_OUT + i, kTcWarps);
+            mbar_init(bar + B_OFREE + i, 1);
         }
-        for (int i = B_S; i <= B_READ; ++i) mbar_init(bar + i, kTcWarps);
-        for (int i = B_R; i < B_COUNT; ++i) mbar_init(bar + i, 1);
+        for (int i = B_S; i < B_R; ++i) mbar_init(bar + i, kTcWarps / 2);
+        for (int i = B_R; i < B_COUNT; ++i) mbar_init(bar + i, i == B_READ ? kTcWarps : 1);
         *dead = 0;
         fence_mbar_init();
     }
@@ -77,7 +92,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp < kTcWarps) {
         // ---- the lanes' threads
-        const int part = warp >> 2, lane0 = 32 * (warp & 3), dv = dv_blk + lane0 + lane;
+        const int part = warp >> 2, half = part >> 1, lane0 = 32 * (warp & 3), dv = dv_blk + lane0 + lane;
         const bool mine = dv < d.Dv;
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
         const int dk0 = part * HD;
@@ -87,11 +102,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < HD; ++i) S[i] = mine && dk0 + i < d.Dk ? sp[(size_t)i * d.Dv] : 0.f;
         }
-        auto keep_state = [&](float *dst) {
+        // columns [i0, i1) of S as rows of a [Dk, Dv] state
+        auto keep_state = [&](float *dst, int i0, int i1) {
             dst += (size_t)dk0 * d.Dv + dv;
 #pragma unroll
             for (int i = 0; i < HD; ++i)
-                if (mine && dk0 + i < d.Dk) dst[(size_t)i * d.Dv] = S[i];
+                if (i >= i0 && i < i1 && mine && dk0 + i < d.Dk) dst[(size_t)i * d.Dv] = S[i];
         };
         auto planes_of_s = [&] {
 #pragma unroll
@@ -99,8 +115,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = S[c + i];
-                tc_store_planes<3>(at + L::SP + (dk0 + c) / 2, DKP / 2, x);
+                const uint32_t dst = at + L::SP + (dk0 + c) / 2;
+                tc_store_planes(dst, dst + DKP / 2, dst + DKP, x);
             }
+            tc_wait_st();
         };
         auto arrive = [&](int which) {
             tc_fence_before();
@@ -109,68 +127,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         if (nch > 0) {
             planes_of_s();
-            tc_wait_st();
-            arrive(B_S);
+            arrive(B_S + half);
         }
-        // the readings' 8 x 8 blocks in the value tile: block b of a store is 8 columns of dv (b % 2) and
+        // the readings' 8 x 8 blocks in the row buffer: block b of a store is 8 columns of dv (b % 2) and
         // 8 tokens (b / 2), a lane's row one token
         const int orow = 16 * part + 8 * (lane >> 4) + (lane & 7), ocol = (lane0 >> 3) + ((lane >> 3) & 1);
         for (int n = 0; n < nch; ++n) {
             const unsigned par = n & 1;
-            if (SAVE) keep_state(snap + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv);
+            float *keep = snap + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv;
             if (!tc_warp_wait(bar + B_FULL + par, (n >> 1) & 1, dead, d.spin)) break;
             const float *aux = reinterpret_cast<const float *>(smem + L::AUX + 512 * par);
             const float *from = aux + 16 * part, *to = aux + C + 16 * part;
             const float whole = aux[C - 1];
-            float x[16], y[2][8];
-            if (!tc_warp_wait(bar + B_R, par, dead, d.spin)) break;
+            float x[16];
+            if (!tc_warp_wait(bar + B_R + half, par, dead, d.spin)) break;
             tc_fence_after();
             tc_load16(at + L::R + 16 * part, x);
-            arrive(B_READ);
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] *= -from[i];
-            tc_store_planes<3>(at + L::UP + 8 * part, C / 2, x);
-            tc_wait_st();
-            arrive(B_W);
-            if (!tc_warp_wait(bar + B_O1, par, dead, d.spin)) break;
-            tc_fence_after();
-            tc_load_frag16(at + L::R + 16 * part, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = d.scale * from[8 * (i >> 2) + 2 * (lane & 3) + (i & 1)];
-                y[0][i] *= f;
-                y[1][i] *= f;
+            {
+                const uint32_t dst = at + L::UP + 8 * part;
+                tc_store_planes(dst, dst + C / 2, dst + C, x);
             }
-            if (!tc_warp_wait(bar + B_UACC, par, dead, d.spin)) break;
+            tc_wait_st();
+            arrive(B_W + half);
+            if (SAVE) keep_state(keep, 0, HD / 2);                 // in the products' time
+            if (!tc_warp_wait(bar + B_UACC + half, par, dead, d.spin)) break;
             tc_fence_after();
             tc_load16(at + L::U + 16 * part, x);
+            float *udst = usave + ((bh * d.Nt + n) * (long long)C + 16 * part) * d.Dv + dv;
             if (SAVE && mine) {
-                float *dst = usave + ((bh * d.Nt + n) * (long long)C + 16 * part) * d.Dv + dv;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) dst[(size_t)i * d.Dv] = x[i];
+                for (int i = 0; i < 16; ++i) udst[(size_t)i * d.Dv] = x[i];
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] *= to[i];
-            tc_store_planes<3>(at + L::SP + 8 * part, C / 2, x);
-            tc_wait_st();
-            arrive(B_U);
-            // the readings, in the values' place; the copying warps store them as rows
-            if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;
-            tc_fence_after();
             {
-                float z[2][8];
-                tc_load_frag16(at + L::O + 16 * part, z);
-                unsigned char *vt = smem + par * L::STAGE + L::V;
-#pragma unroll
-                for (int l = 0; l < 2; ++l) {
-                    unsigned r[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r[i] = pack_bf16(y[l][2 * i] + z[l][2 * i], y[l][2 * i + 1] + z[l][2 * i + 1]);
-                    const int c = ocol + 2 * l;
-                    stsm4t(smem_u32(vt) + (c >> 3) * L::TILE + tc_at(orow, c & 7), r);
-                }
+                const uint32_t dst = at + L::U + 16 * part;
+                tc_store_planes(dst, dst + 8, at + L::LO + 8 * part, x);
             }
-            if (!tc_warp_wait(bar + B_UPD, par, dead, d.spin)) break;
+            tc_wait_st();
+            arrive(B_U + half);
+            if (SAVE) keep_state(keep, HD / 2, HD);
+            // the readings, in a buffer that warp 18 stores; 0 past the valid tokens
+            if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;
+            if (!tc_warp_wait(bar + B_O1, par, dead, d.spin)) break;
+            if (n >= 2 && !tc_warp_wait(bar + B_OFREE + par, ((n >> 1) - 1) & 1, dead, d.spin)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {                          // 16 lanes of dv
+                float y[8], z[8];
+                tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::R + 16 * part, at + ((uint32_t)(16 * l) << 16) + L::OA + 16 * part, y, z);
+                unsigned r[4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int t = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                    z[i] = n * C + 16 * part + t < ntok ? fmaf(d.scale * from[t], y[i], z[i]) : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[2 * i], z[2 * i + 1]);
+                const int c = ocol + 2 * l;
+                stsm4t(smem_u32(smem) + L::O + (2 * par + (c >> 3)) * L::TILE + tc_at(orow, c & 7), r);
+            }
+            fence_proxy_async_smem();
+            arrive(B_READ);
+            if (lane == 0) mbar_arrive(bar + B_OUT + par);
+            if (!tc_warp_wait(bar + B_UPD + half, par, dead, d.spin)) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
@@ -179,160 +201,173 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int i = 0; i < 16; ++i) S[c + i] = fmaf(whole, S[c + i], x[i]);
             }
             if (n + 1 < nch) planes_of_s();
-            tc_wait_st();
-            arrive(B_S);
+            arrive(B_S + half);
             if (lane == 0) mbar_arrive(bar + B_EMPTY + par);
         }
-        if (nch > 0 && !*dead) keep_state(state + bh * d.Dk * (long long)d.Dv);
+        if (nch > 0 && !*dead) keep_state(state + bh * d.Dk * (long long)d.Dv, 0, HD);
     } else if (warp == kTcWarps) {
         // ---- the products
-        {
-            const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
-            for (int n = 0; n < nch; ++n) {
-                const unsigned par = n & 1;
-                const uint32_t st = base + par * L::STAGE;
-                const uint64_t kd = tc_k_major(st + L::K), qd = tc_k_major(st + L::Q), yd = tc_k_major(st + L::Y),
-                               zd = tc_k_major(st + L::Z), kn = tc_n_major(st + L::K, L::TILE), vm = tc_n_major(st + L::V, L::TILE);
-                // lower triangular B: K step ks reaches the columns from 16 ks on. A descriptor's address
-                // counts 16 bytes.
-                auto tri_ts = [&](uint32_t dst, uint32_t a, uint64_t tile) {
+        const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
+        for (int n = 0; n < nch; ++n) {
+            const unsigned par = n & 1;
+            const uint32_t st = base + par * L::STAGE;
+            // a descriptor's address counts 16 bytes
+            const uint64_t kd = tc_k_major(st + L::K), qd = tc_k_major(st + L::Q), yd = tc_k_major(st + L::Y),
+                           zd = tc_k_major(st + L::Z), kn = tc_n_major(st + L::K, L::TILE), vm = tc_n_major(st + L::V, L::TILE);
+            // lower triangular B: K step ks reaches the columns from 16 ks on
+            auto tri = [&](uint32_t dst, uint32_t a, uint64_t tile, int ks) {
+                tc_mma_ts(one, tu + dst + 16 * ks, tu + a + 8 * ks, tile + (16 * ks * 128 + 32 * ks) / 16, tc_idesc<false>(C - 16 * ks), true);
+            };
+            auto tri_v = [&](uint32_t dst, uint64_t tile, bool first) {
 #pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks)
-                        tc_mma_ts(one, tu + dst + 16 * ks, tu + a + 8 * ks, tile + (16 * ks * 128 + 32 * ks) / 16, tc_idesc<false>(C - 16 * ks), true);
-                };
-                auto tri_ss = [&](uint32_t dst, uint64_t tile, bool first) {
+                for (int ks = 0; ks < C / 16; ++ks)
+                    tc_mma_ss(one, tu + dst + 16 * ks, vm + 2048 * ks / 16, tile + (16 * ks * 128 + 32 * ks) / 16,
+                              tc_idesc<false, true>(C - 16 * ks), !first || ks > 0);
+            };
+            // 16 tokens' or more rows of a [tokens][DKP] tile against the planes of S
+            auto rows = [&](uint32_t dst, uint64_t tile, int t0, int tokens, int p, int ks, bool add) {
+                tc_mma_ts(one, tu + dst + t0, tu + L::SP + p * (DKP / 2) + 8 * ks, tile + (t0 * 128 + (ks >> 2) * L::TILE + 32 * (ks & 3)) / 16,
+                          tc_idesc<false>(tokens), add);
+            };
+            auto update = [&](int ks, int hd) {                    // half hd of Dk, or (Dk 64) all of it at once
+                constexpr int N = DKP == 128 ? 64 : DKP;
 #pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks)
-                        tc_mma_ss(one, tu + dst + 16 * ks, vm + 2048 * ks / 16, tile + (16 * ks * 128 + 32 * ks) / 16,
-                                  tc_idesc<false, true>(C - 16 * ks), !first || ks > 0);
-                };
-                if (!tc_warp_wait(bar + B_FULL + par, (n >> 1) & 1, dead, d.spin)) break;
-                if (!tc_warp_wait(bar + B_S, par, dead, d.spin)) break;
-                tc_fence_after();
+                for (int p = 2; p >= 0; --p)
+                    tc_mma_ts(one, tu + L::UP + 64 * hd, tu + (p < 2 ? L::U + 16 * ks + 8 * p : L::LO + 8 * ks),
+                              kn + (2048 * ks + hd * L::TILE) / 16, tc_idesc<true>(N), p < 2 || ks > 0);
+            };
+            if (!tc_warp_wait(bar + B_FULL + par, (n >> 1) & 1, dead, d.spin)) break;
+            if (n > 0 && !tc_warp_wait(bar + B_READ, par ^ 1, dead, d.spin)) break;
+            if (!tc_warp_wait(bar + B_S, par, dead, d.spin)) break;
+            tc_fence_after();
+            constexpr int KS = DKP / 16;
+#pragma unroll
+            for (int p = 2; p >= 0; --p)
+#pragma unroll
+                for (int ks = 0; ks < KS / 2; ++ks) rows(L::R, kd, 0, C, p, ks, p < 2 || ks > 0);
+            if (!tc_warp_wait(bar + B_S + 1, par, dead, d.spin)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
                 for (int p = 2; p >= 0; --p)
 #pragma unroll
-                    for (int ks = 0; ks < DKP / 16; ++ks)
-                        tc_mma_ts(one, tu + L::R, tu + L::SP + p * (DKP / 2) + 8 * ks, kd + ((ks >> 2) * L::TILE + 32 * (ks & 3)) / 16,
-                                  tc_idesc<false>(C), p < 2 || ks > 0);
-                tc_commit_to(one, bar + B_R);
+                    for (int ks = KS / 2; ks < KS; ++ks) rows(L::R, kd, 32 * hf, 32, p, ks, true);
+                tc_commit_to(one, bar + B_R + hf);
+            }
 #pragma unroll
-                for (int p = 2; p >= 0; --p) tri_ss(L::U, yd + p * L::TILE / 16, p == 2);
+            for (int p = 2; p >= 0; --p) tri_v(L::U, yd + p * L::TILE / 16, p == 2);
 #pragma unroll
-                for (int p = 1; p >= 0; --p) tri_ss(L::O, zd + p * L::TILE / 16, p == 1);
-                if (!tc_warp_wait(bar + B_READ, par, dead, d.spin)) break;
-                tc_fence_after();
+            for (int p = 1; p >= 0; --p) tri_v(L::OA, zd + p * L::TILE / 16, p == 1);
+            bool ok = true;
 #pragma unroll
-                for (int p = 1; p >= 0; --p)
-#pragma unroll
-                    for (int ks = 0; ks < DKP / 16; ++ks)
-                        tc_mma_ts(one, tu + L::R, tu + L::SP + p * (DKP / 2) + 8 * ks, qd + ((ks >> 2) * L::TILE + 32 * (ks & 3)) / 16,
-                                  tc_idesc<false>(C), p < 1 || ks > 0);
-                tc_commit_to(one, bar + B_O1);
-                if (!tc_warp_wait(bar + B_W, par, dead, d.spin)) break;
+            for (int hf = 0; hf < 2; ++hf) {
+                ok = ok && tc_warp_wait(bar + B_W + hf, par, dead, d.spin);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int a = 2; a >= 0; --a)
 #pragma unroll
-                    for (int p = 2 - a; p >= 0; --p) tri_ts(L::U, L::UP + a * (C / 2), yd + p * L::TILE / 16);
-                tc_commit_to(one, bar + B_UACC);
-#pragma unroll
-                for (int a = 1; a >= 0; --a)
-#pragma unroll
-                    for (int p = 1 - a; p >= 0; --p) tri_ts(L::O, L::UP + a * (C / 2), zd + p * L::TILE / 16);
-                tc_commit_to(one, bar + B_O2);
-                if (!tc_warp_wait(bar + B_U, par, dead, d.spin)) break;
-                if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;      // w's planes make room for the update
-                tc_fence_after();
-#pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks)
-                        tc_mma_ts(one, tu + L::UP, tu + L::SP + p * (C / 2) + 8 * ks, kn + 2048 * ks / 16, tc_idesc<true>(DKP), p < 2 || ks > 0);
-                tc_commit_to(one, bar + B_UPD);
-                tc_commit_to(one, bar + B_EMPTY + par);
+                    for (int p = 2 - a; p >= 0; --p) {
+                        tri(L::U, L::UP + a * (C / 2), yd + p * L::TILE / 16, 2 * hf);
+                        tri(L::U, L::UP + a * (C / 2), yd + p * L::TILE / 16, 2 * hf + 1);
+                    }
+                tc_commit_to(one, bar + B_UACC + hf);
             }
+            if (!ok) break;
+#pragma unroll
+            for (int a = 1; a >= 0; --a)
+#pragma unroll
+                for (int p = 1 - a; p >= 0; --p)
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks) tri(L::OA, L::UP + a * (C / 2), zd + p * L::TILE / 16, ks);
+            tc_commit_to(one, bar + B_O2);
+#pragma unroll
+            for (int p = 1; p >= 0; --p)                           // R is used: S^T Q^T in its place
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) rows(L::R, qd, 0, C, p, ks, p < 1 || ks > 0);
+            tc_commit_to(one, bar + B_O1);
+            if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;      // w's planes make room for the update
+            if (!tc_warp_wait(bar + B_U, par, dead, d.spin)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int hd = 0; hd < DKP / 64; ++hd) {
+                update(0, hd);
+                update(1, hd);
+            }
+            if (!tc_warp_wait(bar + B_U + 1, par, dead, d.spin)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int hd = 0; hd < DKP / 64; ++hd) {
+                update(2, hd);
+                update(3, hd);
+                tc_commit_to(one, bar + B_UPD + hd);
+            }
+            if (DKP == 64) tc_commit_to(one, bar + B_UPD + 1);
+            tc_commit_to(one, bar + B_EMPTY + par);
         }
         __syncwarp();
-    } else {
-        // ---- the copies
-        const int ct = tid - 32 * (kTcWarps + 1);
-        // a thread copies 16-byte piece ck of K's and Q's rows rk + RK i, and piece c of V's rows r + 8 i
-        constexpr int PC = DKP / 8, RK = kTcCopy / PC;
-        const int ck = ct % PC, rk = ct / PC, c = ct & 15, r = ct >> 4;
-        const int koff = (ck >> 3) * L::TILE + tc_at(rk, ck & 7), voff = L::V + (c >> 3) * L::TILE + tc_at(r, c & 7);
-        const int pieces = d.Dv - dv_blk < 128 ? (d.Dv - dv_blk) / 8 : 16;
-        const bool kin = ck * 8 < d.Dk, vin = c < pieces;
-        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(in.k) + b * d.ks[0] + hk * d.ks[2];
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(in.q) + b * d.qs[0] + hk * d.qs[2];
-        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(in.v) + b * d.vs[0] + h * d.vs[2] + dv_blk;
-        const long long orow = (long long)d.H * d.Dv;
-        __nv_bfloat16 *out = o + (((long long)b * d.T + r) * d.H + h) * d.Dv + dv_blk + c * 8;
-        bool good = true;                                          // this thread's waits so far
-        // The readings of chunk n, once its stage is done with (rows past the valid tokens are 0). Returns
-        // whether all copying threads' waits have succeeded: they leave together.
-        auto store = [&](int n) {
-            good = good && tc_wait(bar + B_EMPTY + (n & 1), (n >> 1) & 1, dead, d.spin);
-            const unsigned char *src = smem + (n & 1) * L::STAGE + voff;
-            const int t0 = n * C + r;
-            if (good && vin) {
-                __nv_bfloat16 *dst = out + (long long)n * C * orow;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint4 x = *reinterpret_cast<const uint4 *>(src + 1024 * i);
-                    if (t0 + 8 * i >= ntok) x = make_uint4(0u, 0u, 0u, 0u);
-                    if (t0 + 8 * i < d.T) *reinterpret_cast<uint4 *>(dst + 8 * i * orow) = x;
-                }
-            }
-            // also: every thread's reads, before any copy into the stage
-            int all;
-            asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n"
-                         " selp.b32 %0, 1, 0, q;\n}" : "=r"(all) : "r"((int)good), "n"(kTcCopy) : "memory");
-            return all != 0;
-        };
-        bool ok = true;
+    } else if (warp == kTcWarps + 1) {
+        // ---- the chunks' inputs
         for (int n = 0; n < nch; ++n) {
-            const int s = n & 1;
+            const int s = n & 1, t0 = n * C, nt = ntok - t0 < C ? ntok - t0 : C;
             unsigned char *st = smem + s * L::STAGE;
-            const uint32_t sa = smem_u32(st);
-            if (n >= 2 && !(ok = store(n - 2))) break;
-            const long long t0 = (long long)n * C, bhn = bh * d.Nt + n;
-            const int nt = ntok - (int)t0 < C ? ntok - (int)t0 : C;
-            if (ct == 0) {
-                mbar_arrive_expect_tx(bar + B_BULK + s, 5 * L::TILE + 2 * C * 4);
-                bulk_g2s(st + L::Y, w.x + bhn * (3 * L::TILE), 3 * L::TILE, bar + B_BULK + s);
-                bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, bar + B_BULK + s);
-                bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * 3 * C, 2 * C * 4, bar + B_BULK + s);
+            const long long bhn = bh * d.Nt + n;
+            unsigned long long *full = bar + B_BULK + s;
+            if (n >= 2 && !tc_warp_wait(bar + B_EMPTY + s, ((n >> 1) - 1) & 1, dead, d.spin)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full, L::STAGE + 2 * C * 4);
+                for (int c = 0; c < DKP / 64; ++c) {
+                    tc_tensor_load(st + L::K + c * L::TILE, &mk, 64 * c, hk, t0, b, full);
+                    tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, hk, t0, b, full);
+                }
+                for (int c = 0; c < 2; ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, h, t0, b, full);
+                bulk_g2s(st + L::Y, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
+                bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, full);
+                bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * 3 * C, 2 * C * 4, full);
             }
-            const __nv_bfloat16 *kp = k + (t0 + rk) * d.ks[1] + ck * 8, *qp = q + (t0 + rk) * d.qs[1] + ck * 8;
-#pragma unroll
-            for (int i = 0; i < C / RK; ++i) {
-                const bool live = kin && rk + RK * i < nt;
-                cp_async16_zfill(sa + L::K + koff + RK * 128 * i, live ? kp + RK * i * d.ks[1] : k, live);
-                cp_async16_zfill(sa + L::Q + koff + RK * 128 * i, live ? qp + RK * i * d.qs[1] : q, live);
+            __syncwarp();
+            if (!tc_warp_wait(full, (n >> 1) & 1, dead, d.spin)) {
+                mbar_wait_bounded(full, (n >> 1) & 1);             // nothing in flight behind a give-up
+                break;
             }
-            const __nv_bfloat16 *vp = v + (t0 + r) * d.vs[1] + c * 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool live = vin && r + 8 * i < nt;
-                cp_async16_zfill(sa + voff + 1024 * i, live ? vp + 8 * i * d.vs[1] : v, live);
+            if (nt < C) {                                          // what lies past the valid tokens is not used
+                const int rows = C - nt;
+                for (int i = lane; i < rows * 8; i += 32) {
+                    const int off = tc_at(nt + (i >> 3), i & 7);
+                    for (int c = 0; c < DKP / 64; ++c) {
+                        *reinterpret_cast<uint4 *>(st + L::K + c * L::TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(st + L::Q + c * L::TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4 *>(st + L::V + c * L::TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
             }
-            cp_async_commit();
-            cp_async_wait<0>();
-            if (ct == 0 && !tc_wait(bar + B_BULK + s, (n >> 1) & 1, dead, d.spin)) {
-                mbar_wait_bounded(bar + B_BULK + s, (n >> 1) & 1);    // nothing in flight behind a give-up
-                good = false;
-            }
-            fence_proxy_async_smem();                              // the tiles, before the tensor core reads them
             mbar_arrive(bar + B_FULL + s);
         }
-        for (int n = nch > 2 ? nch - 2 : 0; ok && n < nch; ++n) ok = store(n);
-        if (vin)
-            for (long long t = (long long)nch * C; t + r < d.T; t += 8) *reinterpret_cast<uint4 *>(out + t * orow) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        // ---- the readings
+        for (int n = 0; n < nch; ++n) {
+            if (!tc_warp_wait(bar + B_OUT + (n & 1), (n >> 1) & 1, dead, d.spin)) break;
+            if (lane == 0) {
+                for (int c = 0; c < 2; ++c)
+                    if (dv_blk + 64 * c < d.Dv)
+                        tc_tensor_store(&mo, dv_blk + 64 * c, h, n * C, b, smem + L::O + (2 * (n & 1) + c) * L::TILE);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                mbar_arrive(bar + B_OFREE + (n & 1));
+            }
+            __syncwarp();
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        const int cols = d.Dv - dv_blk < 128 ? d.Dv - dv_blk : 128;
+        __nv_bfloat16 *out = o + ((long long)b * d.T * d.H + h) * d.Dv + dv_blk;
+        for (long long t = (long long)nch * C + (lane >> 4); t < d.T; t += 2)
+            if ((lane & 15) * 8 < cols) *reinterpret_cast<uint4 *>(out + t * d.H * d.Dv + (lane & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
     if (*dead) {
-        // the products issued so far are waited for (the copies were, by their own thread)
+        // the products issued so far are waited for (the copies were, by their own warps)
         if (tid == 32 * kTcWarps) {
             tc_commit_to(1, bar + B_DRAIN);
             mbar_wait_bounded(bar + B_DRAIN, 0);
@@ -348,14 +383,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 template <int DKP, bool SAVE>
 cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o, float *snap,
                     float *u, cudaStream_t st) {
+    const long long os[3] = {(long long)d.T * d.H * d.Dv, (long long)d.H * d.Dv, d.Dv};
+    CUtensorMap mq, mk, mv, mo;
+    cudaError_t e = tc_tensor_map(&mq, in.q, d.qs, d.B, d.T, d.Hk, d.Dk);
+    if (e == cudaSuccess) e = tc_tensor_map(&mk, in.k, d.ks, d.B, d.T, d.Hk, d.Dk);
+    if (e == cudaSuccess) e = tc_tensor_map(&mv, in.v, d.vs, d.B, d.T, d.H, d.Dv);
+    if (e == cudaSuccess) e = tc_tensor_map(&mo, o, os, d.B, d.T, d.H, d.Dv);
+    if (e != cudaSuccess) return e;
     auto kern = k_delta_scan_tc<DKP, SAVE>;
     set_kernel_smem(kern, TcScan<DKP>::BYTES);
     kern<<<(unsigned)((long long)d.B * d.H * ((d.Dv + 127) / 128)), kTcThreads, TcScan<DKP>::BYTES, st>>>(
-        d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, u);
+        mq, mk, mv, mo, d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, u);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *s, int B, int T, int heads, int D) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        cudaDriverEntryPointQueryResult found;
+        void *fn = nullptr;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn) : nullptr;
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dim[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
+    // a dimension of one element is never stepped along: any stride will do
+    auto bytes = [](long long stride, int n) { return (cuuint64_t)(n > 1 ? stride * 2 : 16); };
+    const cuuint64_t str[3] = {bytes(s[2], heads), bytes(s[1], T), bytes(s[0], B)};
+    const cuuint32_t box[4] = {64, 1, 64, 1}, one[4] = {1, 1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dim, str, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 cudaError_t launch_delta_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o,
                                  float *snap, float *u, cudaStream_t st) {

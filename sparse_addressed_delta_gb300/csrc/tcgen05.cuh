@@ -3,6 +3,9 @@
 // memory with the 128-byte swizzle.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "delta_internal.cuh"
 
 namespace sdm {
@@ -76,17 +79,16 @@ __device__ __forceinline__ void tc_load16(uint32_t addr, float (&v)[16]) {
         : "r"(addr)
         : "memory");
 }
-// 16 columns of 16 lanes from `addr` on and of the 16 behind them, in the fragments of 8 x 8 blocks: for
-// half l and 8 columns c, v[l][4 c ..] is (lane / 4, 2 (lane % 4)), its right neighbour, and both of row + 8
-__device__ __forceinline__ void tc_load_frag16(uint32_t addr, float (&v)[2][8]) {
+// 16 columns of 16 lanes at each of two addresses, in the fragments of 8 x 8 blocks: for 8 columns c,
+// v[4 c ..] is (lane / 4, 2 (lane % 4)), its right neighbour, and both of row + 8
+__device__ __forceinline__ void tc_load_frag16(uint32_t a, uint32_t b, float (&v)[8], float (&u)[8]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
         "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0][0]), "=f"(v[0][1]), "=f"(v[0][2]), "=f"(v[0][3]), "=f"(v[0][4]), "=f"(v[0][5]),
-          "=f"(v[0][6]), "=f"(v[0][7]), "=f"(v[1][0]), "=f"(v[1][1]), "=f"(v[1][2]), "=f"(v[1][3]),
-          "=f"(v[1][4]), "=f"(v[1][5]), "=f"(v[1][6]), "=f"(v[1][7])
-        : "r"(addr), "r"(addr + (16u << 16))
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]), "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7])
+        : "r"(a), "r"(b)
         : "memory");
 }
 __device__ __forceinline__ void tc_store8(uint32_t addr, const unsigned (&v)[8]) {
@@ -95,9 +97,9 @@ __device__ __forceinline__ void tc_store8(uint32_t addr, const unsigned (&v)[8])
                  : "memory");
 }
 
-// 16 floats as N bfloat16 planes of 8 packed columns, plane p at addr + p * step
-template <int N>
-__device__ __forceinline__ void tc_store_planes(uint32_t addr, uint32_t step, const float (&x)[16]) {
+// 16 floats as three bfloat16 planes of 8 packed columns
+__device__ __forceinline__ void tc_store_planes(uint32_t hi, uint32_t mid, uint32_t lo, const float (&x)[16]) {
+    constexpr int N = 3;
     unsigned p[N][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -106,8 +108,33 @@ __device__ __forceinline__ void tc_store_planes(uint32_t addr, uint32_t step, co
 #pragma unroll
         for (int m = 0; m < N; ++m) p[m][i] = s[m];
     }
-#pragma unroll
-    for (int m = 0; m < N; ++m) tc_store8(addr + m * step, p[m]);
+    tc_store8(hi, p[0]);
+    tc_store8(mid, p[1]);
+    tc_store8(lo, p[2]);
+}
+
+// Tensor copies of 64 tokens x 64 columns of one head of a [B, T, heads, D] bfloat16 tensor, between
+// global memory and a tile as tc_at lays it out. Loads are 0, stores are left out, past T and D.
+cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *strides, int B, int T, int heads, int D);
+// whether such a map can describe the tensor (a broadcast dimension has no stride to give)
+inline bool tc_tensor_fits(const long long *s, int B, int T, int heads) {
+    const int n[3] = {B, T, heads};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] == 0 || s[i] * 2 >= (1LL << 40))) return false;
+    return true;
+}
+__device__ __forceinline__ void tc_tensor_load(void *dst, const CUtensorMap *m, int col, int head, int token, int seq,
+                                               unsigned long long *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(m), "r"(col), "r"(head), "r"(token), "r"(seq), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tc_tensor_store(const CUtensorMap *m, int col, int head, int token, int seq, const void *src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(m),
+                 "r"(col), "r"(head), "r"(token), "r"(seq), "r"(smem_u32(src))
+                 : "memory");
 }
 
 // four 8 x 8 blocks of bfloat16 fragments stored transposed: lane 8 b + r gives the address of row r (a
