@@ -29,6 +29,7 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.scale = s->scale;
     d.C = delta_chunk(s->dtype);
     d.pp = s->dtype == SDM_BF16 ? 2 : 3;
+    d.back = 0;
     d.spin = wait_limit();
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
@@ -98,8 +99,10 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     return l;
 }
 
-// what the saving forward keeps: the state at every chunk's start, and u
-size_t delta_saved_snap(const DeltaDims &d) { return delta_up(delta_chunks(d) * d.Dk * d.Dv * 4); }
+// what the saving forward keeps: the state at every chunk's start and at the end, and r
+size_t delta_saved_snap(const DeltaDims &d) {
+    return delta_up((delta_chunks(d) + (size_t)d.B * d.H) * d.Dk * d.Dv * 4);
+}
 size_t delta_saved(const DeltaDims &d) {
     return delta_saved_snap(d) + delta_up(delta_chunks(d) * d.C * d.Dv * 4);
 }
@@ -174,10 +177,10 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
     DeltaLocal w;
     cudaError_t e = delta_local(d, in, l, static_cast<unsigned char *>(workspace), qp, kp, w, st);
     float *snap = save ? static_cast<float *>(saved) : nullptr;
-    float *u = save ? reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_snap(d)) : nullptr;
+    float *r = save ? reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_snap(d)) : nullptr;
     if (e == cudaSuccess)
-        e = d.tc ? launch_delta_scan_tc(d, in, w, state, readings, snap, u, st)
-                 : launch_delta_scan(d, in, qp, kp, w, state, readings, snap, u, st);
+        e = d.tc ? launch_delta_scan_tc(d, in, w, state, readings, snap, r, st)
+                 : launch_delta_scan(d, in, qp, kp, w, state, readings, snap, r, st);
     return delta_status(e);
 }
 
@@ -217,6 +220,7 @@ size_t sdm_gated_delta_backward_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
     if (delta_check(shape, d) != SDM_OK) return 0;
     d.pp = 3;
+    d.back = 1;
     d.tc = 0;
     return delta_layout(d, true).bytes + kAlign;
 }
@@ -231,6 +235,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     int rc = delta_check(shape, d);
     if (rc != SDM_OK) return rc;
     d.pp = 3;                            // P reaches float32 gradients
+    d.back = 1;
     d.tc = 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d.B == 0) return SDM_OK;
@@ -265,7 +270,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     o.grad_decay = grad_log_decay;
     o.grad_beta = grad_beta;
     o.snap = static_cast<const float *>(saved);
-    o.u = reinterpret_cast<const float *>(static_cast<const unsigned char *>(saved) + delta_saved_snap(d));
+    o.r = reinterpret_cast<const float *>(static_cast<const unsigned char *>(saved) + delta_saved_snap(d));
     o.ends = reinterpret_cast<float *>(ws + l.ends);
     o.w = reinterpret_cast<float *>(ws + l.w);
     o.dq = reinterpret_cast<float *>(ws + l.dq);

@@ -4,15 +4,19 @@
 //   D0 = G_C D1 + (scale G Q)^T dO - K^T (beta G dw)
 // is a recurrence over the chunks from the last to the first (k_delta_back_scan), the forward scan's
 // mirror image: a warp owns 16 columns, and accumulators pass from product to product as A operands.
-// Everything else needs only a chunk's own S0, u (saved by the forward), D1 and dw (left by the scan),
-// and runs for all chunks at once (k_delta_back_local):
-//   E = dw u^T, dA = -beta E (s < t);   dP = dO u^T (s <= t);   a = dA e^{L_t - L_s}, p = scale dP e^{L_t - L_s}
+// (X = (I + diag(beta) A)^-1 here.) Everything else needs only a chunk's own S0, r and end state S1 (saved
+// by the forward), D1 and dw (left by the scan), and runs for all chunks at once (k_delta_back_local):
+//   a[t,s] = -beta_t beta_s <dw_t, r_s> e^{L_t - L_s}  (s < t)
+//   p[t,s] = scale beta_s <dO_t, r_s> e^{L_t - L_s}    (s <= t)
 //   dq = p K + scale G (dO S0^T)
-//   dk = p^T Q + (a + a^T) K - beta G (dw S0^T) + e^{L_C - L} (u D1^T)
-//   dbeta_t = <dw_t, v_t> - G_t <k_t, dw_t S0^T> - sum_s E[t,s] A[t,s]
-//   dL from a, p (rows minus columns), from the three products with the states (row products with q and
-//   k) and from G_C <S0, D1>;  dg = the suffix sums of dL.
-// The gates' gradients are float32: every product that reaches them keeps float32's accuracy.
+//   dk = p^T Q + (a + a^T) K - beta G (dw S0^T) + e^{L_C - L} beta (r D1^T)
+//   dbeta_t = <dw_t, r_t>
+// The log-decays need no products of their own. Scaling the state before token t scales what is read and
+// undoes what is written, so dg_t = <S_{t-1}, dS_{t-1}> changes from token to token by
+//   dg_t = dg_{t+1} + <o_t, dO_t> - <v_t, dv_t>
+// and within a chunk it is <S1, D1> plus suffix sums; <o_t, dO_t> is the row sum of p * (q k^T) plus
+// <q_t, scale G dO_t S0^T>. Products that reach the gates' float32 gradients keep float32's accuracy; with
+// bfloat16 inputs the others take two terms of each operand (2^-17), as exact as their results need.
 #include "delta_internal.cuh"
 
 namespace sdm {
@@ -276,36 +280,41 @@ __global__ void __launch_bounds__(NW * 32, 1)
         *reinterpret_cast<uint4 *>(gv + t * orow + dv0 + (lane % PR) * VE) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-constexpr int kBackThreads = 256, kBackCols = 64;     // columns of the state at a time
+constexpr int kBackCols = 128;                        // columns of the state at a time
 
 template <typename T, int DKP>
 struct BackLocalSmem {
     static constexpr bool BF = sizeof(T) == 2;
-    static constexpr int C = BF ? 64 : 32, KP = BF ? 1 : 3, GP = BF ? 2 : 3;
+    static constexpr int C = BF ? 64 : 32, NB = C / 16;
+    static constexpr int KP = BF ? 1 : 3;             // planes of q, k and dO
+    static constexpr int PL = BF ? 2 : 3;             // terms of products that reach only the inputs' type
+    static constexpr int NWK = DKP / 16, WARPS = NWK * NB < 16 ? NWK * NB : 16;
     static constexpr int KPI = delta_pitch(DKP * 2), TILE = C * KPI;
-    static constexpr int VPI = delta_pitch(kBackCols * 2), VT = C * VPI;   // planes of dO, dw and u
+    static constexpr int VPI = delta_pitch(kBackCols * 2), VT = C * VPI;   // planes of dO, dw and r
     static constexpr int GPI = delta_pitch(C * 2), GT = C * GPI;           // planes of p and a
-    static constexpr int NB = C / 16;
-    static constexpr int Q = KP * TILE, O = 2 * KP * TILE, W = O + KP * VT, U = W + 3 * VT;
-    static constexpr int P = U + 3 * VT, A = P + GP * GT, F = A + GP * GT;
-    // floats: hi, lo, from, to, beta [C]; <dw, v> [C]; row and column sums of z and row sums of E A
-    // [NB][C]; row products [8 warps][3][C]; <S0, D1> [8]
-    static constexpr int FLOATS = 6 * C + 3 * NB * C + 8 * 3 * C + 8;
+    static constexpr int Q = KP * TILE, O = 2 * KP * TILE, W = O + KP * VT, R = W + PL * VT;
+    static constexpr int P = R + 3 * VT, A = P + PL * GT, F = A + PL * GT;
+    // floats: hi, lo, from, to, beta, <dw, v>, <dw, r> [C]; row sums of p * qk [NB][C]; row products with
+    // q [NWK][C]; <S1, D1> [WARPS]
+    static constexpr int FLOATS = 7 * C + NB * C + NWK * C + WARPS;
     static constexpr int BYTES = F + FLOATS * 4;
+    static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
-// One block of eight warps per chunk and head. For the products with the states a warp owns 16 of
-// the Dk columns (with Dk up to 64, half of the tokens too) and reads its rows of S0 and D1 straight
-// into fragments; the C x C products are split into 16 x 16 blocks.
+// One block per chunk and head. For the products with the states a warp owns 16 of the Dk columns and a
+// part of the tokens, and reads its rows of S0 and D1 straight into fragments, one step ahead; the C x C
+// products are split into 16 x 16 blocks, a warp each.
+// What bounds it: the m16n8k16 products, about 7600 a chunk and head at Dk = Dv = 128 (8 cycles each on
+// one of four tensor cores).
 template <typename T, int DKP>
-__global__ void __launch_bounds__(kBackThreads, 1)
+__global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     k_delta_back_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal lw, DeltaBack o) {
     using L = BackLocalSmem<T, DKP>;
     constexpr bool BF = L::BF;
-    constexpr int C = L::C, KP = L::KP, GP = L::GP, NB = L::NB, KPI = L::KPI, VPI = L::VPI, GPI = L::GPI;
-    constexpr int NWK = DKP / 16, MS = 8 / NWK, MT = NB / MS;     // warps over Dk, over tokens; token tiles
-    constexpr int BLOCKS = NB * (NB + 1) / 2, BPW = (BLOCKS + 7) / 8;
-    static_assert(MT >= 1, "token tiles");
+    constexpr int C = L::C, KP = L::KP, PL = L::PL, NB = L::NB, KPI = L::KPI, VPI = L::VPI, GPI = L::GPI;
+    constexpr int THREADS = L::WARPS * 32, NWK = L::NWK, MS = L::WARPS / NWK, MT = NB / MS;
+    constexpr int BLOCKS = NB * (NB + 1) / 2;
+    static_assert(MT >= 1 && BLOCKS <= L::WARPS, "tokens and blocks");
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
     const long long bhn = blockIdx.x;
@@ -331,29 +340,28 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     };
     float *gdec = o.grad_decay + ((long long)b * d.T + t0) * d.H + h, *gbeta = o.grad_beta + ((long long)b * d.T + t0) * d.H + h;
     if (nt == 0) {
-        for (int i = tid; i < rows * (d.Dk / 2); i += kBackThreads) {
+        for (int i = tid; i < rows * (d.Dk / 2); i += THREADS) {
             store2(false, i / (d.Dk / 2), 2 * (i % (d.Dk / 2)), 0.f, 0.f);
             store2(true, i / (d.Dk / 2), 2 * (i % (d.Dk / 2)), 0.f, 0.f);
         }
-        for (int r = tid; r < rows; r += kBackThreads) gdec[(long long)r * d.H] = gbeta[(long long)r * d.H] = 0.f;
+        for (int r = tid; r < rows; r += THREADS) gdec[(long long)r * d.H] = gbeta[(long long)r * d.H] = 0.f;
         return;
     }
-    const unsigned sk = smem_u32(smem), sq = sk + L::Q, so = sk + L::O, sw = sk + L::W, su = sk + L::U;
+    const unsigned sk = smem_u32(smem), sq = sk + L::Q, so = sk + L::O, sw = sk + L::W, sr = sk + L::R;
     float *hi = reinterpret_cast<float *>(smem + L::F), *lo = hi + C, *from = lo + C, *to = from + C, *be = to + C;
-    float *dwv = be + C, *zrow = dwv + C, *zcol = zrow + NB * C, *erow = zcol + NB * C, *dots = erow + NB * C;
-    float *ends = dots + 8 * 3 * C;
+    float *dwv = be + C, *dwr = dwv + C, *zrow = dwr + C, *dots = zrow + NB * C, *ends = dots + NWK * C;
 
-    load_tokens<KP, DKP, C, kBackThreads>(sk, k, b * k.s[0] + t0 * k.s[1] + hk * k.s[2], d.Dk, nt, tid);
-    load_tokens<KP, DKP, C, kBackThreads>(sq, q, b * q.s[0] + t0 * q.s[1] + hk * q.s[2], d.Dk, nt, tid);
+    load_tokens<KP, DKP, C, THREADS>(sk, k, b * k.s[0] + t0 * k.s[1] + hk * k.s[2], d.Dk, nt, tid);
+    load_tokens<KP, DKP, C, THREADS>(sq, q, b * q.s[0] + t0 * q.s[1] + hk * q.s[2], d.Dk, nt, tid);
     cp_async_commit();
     if (warp == 0) {
         const float *aux = lw.aux + bhn * 3 * C;
         double s = 0.0;
-        constexpr int PL = C / 32;
-        double run[PL];
+        constexpr int TL = C / 32;
+        double run[TL];
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int r = lane * PL + i;
+        for (int i = 0; i < TL; ++i) {
+            const int r = lane * TL + i;
             if (r < nt) s += (double)delta_decay(in.g[b * d.gs[0] + (long long)(t0 + r) * d.gs[1] + h * d.gs[2]]);
             run[i] = s;
             from[r] = aux[r];
@@ -368,188 +376,196 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         }
         before -= s;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
+        for (int i = 0; i < TL; ++i) {
             const double x = before + run[i];
-            hi[lane * PL + i] = (float)x;
-            lo[lane * PL + i] = (float)(x - (double)(float)x);
+            hi[lane * TL + i] = (float)x;
+            lo[lane * TL + i] = (float)(x - (double)(float)x);
         }
     }
-    for (int i = tid; i < C; i += kBackThreads) dwv[i] = 0.f;
+    for (int i = tid; i < 2 * C; i += THREADS) dwv[i] = 0.f;      // and dwr behind it
 
     const T *grad = static_cast<const T *>(o.grad) + b * d.os[0] + t0 * d.os[1] + h * d.os[2];
     const T *val = static_cast<const T *>(in.v) + b * d.vs[0] + t0 * d.vs[1] + h * d.vs[2];
-    const float *wp = o.w + bhn * C * (long long)d.Dv, *up = o.u + bhn * C * (long long)d.Dv;
+    const float *wp = o.w + bhn * C * (long long)d.Dv, *rp = o.r + bhn * C * (long long)d.Dv;
     const int dk0 = 16 * (warp % NWK), m0 = (warp / NWK) * MT;    // this warp's Dk columns and token tiles
-    const float *s0p = o.snap + (bhn * d.Dk) * (long long)d.Dv, *d1p = o.ends + (bhn * d.Dk) * (long long)d.Dv;
-    float G1[MT][2][4] = {}, G2[MT][2][4] = {}, G3[MT][2][4] = {}, E[BPW][2][4] = {}, DP[BPW][2][4] = {};
-    float inner = 0.f;
+    const long long cells = (long long)d.Dk * d.Dv;
+    const float *s0p = o.snap + (bh * (d.Nt + 1) + n) * cells, *d1p = o.ends + bhn * cells;
+    {
+        const float4 *x = reinterpret_cast<const float4 *>(s0p + cells), *y = reinterpret_cast<const float4 *>(d1p);
+        float s = 0.f;
+#pragma unroll 4
+        for (int i = tid; i < (int)(cells / 4); i += THREADS) {
+            const float4 u = __ldg(x + i), v = __ldg(y + i);
+            s = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, s))));
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
+        if (lane == 0) ends[warp] = s;
+    }
+    // 16 x 16 block (bi, bj) of the C x C products, on or below the diagonal
+    const bool block = warp < BLOCKS;
+    const int bi = warp < 1 ? 0 : warp < 3 ? 1 : warp < 6 ? 2 : 3, bj = warp - bi * (bi + 1) / 2;
+    float G1[MT][2][4] = {}, G2[MT][2][4] = {}, G3[MT][2][4] = {}, E[2][4] = {}, DP[2][4] = {};
     for (int c0 = 0; c0 < d.Dv; c0 += kBackCols) {
         __syncthreads();
-        // dO, dw and u of this column tile as planes; <dw, v>
-        for (int i = tid; i < C * (kBackCols / 8); i += kBackThreads) {
+        // dO, dw and r of this column tile as planes; <dw, v> and <dw, r>
+        for (int i = tid; i < C * (kBackCols / 8); i += THREADS) {
             const int r = i / (kBackCols / 8), c = i % (kBackCols / 8), col = c0 + 8 * c;
             const bool live = r < nt && col < d.Dv;
             float g[8] = {}, x[8] = {}, u[8] = {}, v[8] = {};
             if (live) {
                 load_vec<T, 8, true>(grad + r * d.os[1] + col, g);
                 load_vec<float, 8, true>(wp + (long long)r * d.Dv + col, x);
-                load_vec<float, 8, true>(up + (long long)r * d.Dv + col, u);
+                load_vec<float, 8, true>(rp + (long long)r * d.Dv + col, u);
                 load_vec<T, 8, true>(val + r * d.vs[1] + col, v);
             }
-            float s = 0.f;
+            float s = 0.f, z = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(x[e], v[e], s);
+            for (int e = 0; e < 8; ++e) {
+                s = fmaf(x[e], v[e], s);
+                z = fmaf(x[e], u[e], z);
+            }
 #pragma unroll
-            for (int m = 1; m < kBackCols / 8; m *= 2) s += __shfl_xor_sync(~0u, s, m);
-            if (c == 0) dwv[r] += s;
+            for (int m = 1; m < kBackCols / 8; m *= 2) {
+                s += __shfl_xor_sync(~0u, s, m);
+                z += __shfl_xor_sync(~0u, z, m);
+            }
+            if (c == 0) {
+                dwv[r] += s;
+                dwr[r] += z;
+            }
             auto put = [&](unsigned char *dst, const float (&y)[8], auto planes) {
-                constexpr int PL = decltype(planes)::value;
-                unsigned p[4][PL];
+                constexpr int N = decltype(planes)::value;
+                unsigned p[4][N];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) split_bf16<PL>(y[2 * e], y[2 * e + 1], p[e]);
+                for (int e = 0; e < 4; ++e) split_bf16<N>(y[2 * e], y[2 * e + 1], p[e]);
 #pragma unroll
-                for (int m = 0; m < PL; ++m)
+                for (int m = 0; m < N; ++m)
                     *reinterpret_cast<uint4 *>(dst + m * L::VT + delta_at<VPI>(r, c)) = make_uint4(p[0][m], p[1][m], p[2][m], p[3][m]);
             };
             put(smem + L::O, g, std::integral_constant<int, KP>{});
-            put(smem + L::W, x, std::integral_constant<int, 3>{});
-            put(smem + L::U, u, std::integral_constant<int, 3>{});
+            put(smem + L::W, x, std::integral_constant<int, PL>{});
+            put(smem + L::R, u, std::integral_constant<int, 3>{});
         }
-        cp_async_wait<0>();
-        __syncthreads();
-        // E += dw u^T, dP += dO u^T, 16 x 16 blocks on and below the diagonal
-#pragma unroll
-        for (int x = 0; x < BPW; ++x) {
-            const int idx = warp + 8 * x;
-            if (idx >= BLOCKS) break;
-            const int bi = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, bj = idx - bi * (bi + 1) / 2;
-#pragma unroll
-            for (int ks = 0; ks < kBackCols / 16; ++ks) {
-                unsigned aw[3][4], ao[KP][4], bu[3][4];
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    ldsm4(aw[p], frag_rc<VPI>(sw + p * L::VT, 16 * bi, 16 * ks, lane));
-                    ldsm4(bu[p], frag_cr<VPI>(su + p * L::VT, 16 * bj, 16 * ks, lane));
-                }
-#pragma unroll
-                for (int p = 0; p < KP; ++p) ldsm4(ao[p], frag_rc<VPI>(so + p * L::VT, 16 * bi, 16 * ks, lane));
-#pragma unroll
-                for (int s = 2; s >= 0; --s)
-#pragma unroll
-                    for (int p = 2; p >= 0; --p)
-                        if (plane_pair(s, p, 3))
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                mma_bf16(E[x][e], aw[s], bu[p][2 * e], bu[p][2 * e + 1]);
-                                if (s < KP) mma_bf16(DP[x][e], ao[s < KP ? s : 0], bu[p][2 * e], bu[p][2 * e + 1]);
-                            }
-            }
-        }
-        // products with the states over this column tile
         const int rest = d.Dv - c0 < kBackCols ? d.Dv - c0 : kBackCols;
-        for (int ks = 0; ks < rest / 16; ++ks) {
-            unsigned bs[2][2][3], be1[2][2][3];                   // [8-column tile][k half][plane]
+        // this lane's two rows of the states: columns 2 i4 and 8 + 2 i4 of each 16
+        float2 xs[2][2], ys[2][2];
+        auto fetch = [&](int ks) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const int row = dk0 + 8 * e + g4;
                     const long long at = (long long)row * d.Dv + c0 + 16 * ks + 8 * m + 2 * i4;
-                    float2 x = make_float2(0.f, 0.f), y = x;
-                    if (row < d.Dk) {
-                        x = __ldg(reinterpret_cast<const float2 *>(s0p + at));
-                        y = __ldg(reinterpret_cast<const float2 *>(d1p + at));
-                    }
-                    inner = fmaf(x.x, y.x, fmaf(x.y, y.y, inner));
-                    split_bf16<3>(x.x, x.y, bs[e][m]);
-                    split_bf16<3>(y.x, y.y, be1[e][m]);
+                    const bool live = row < d.Dk && 16 * ks < rest;
+                    xs[e][m] = live ? __ldg(reinterpret_cast<const float2 *>(s0p + at)) : make_float2(0.f, 0.f);
+                    ys[e][m] = live ? __ldg(reinterpret_cast<const float2 *>(d1p + at)) : make_float2(0.f, 0.f);
                 }
+        };
+        fetch(0);
+        cp_async_wait<0>();
+        __syncthreads();
+        // E += dw r^T, dP += dO r^T
+        if (block) {
+#pragma unroll 2
+            for (int ks = 0; ks < rest / 16; ++ks) {
+                unsigned aw[PL][4], ao[KP][4], br[3][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                unsigned ao[KP][4], aw[3][4], au[3][4];
+                for (int p = 0; p < PL; ++p) ldsm4(aw[p], frag_rc<VPI>(sw + p * L::VT, 16 * bi, 16 * ks, lane));
 #pragma unroll
-                for (int p = 0; p < KP; ++p) ldsm4(ao[p], frag_rc<VPI>(so + p * L::VT, 16 * (m0 + mt), 16 * ks, lane));
+                for (int p = 0; p < 3; ++p) ldsm4(br[p], frag_cr<VPI>(sr + p * L::VT, 16 * bj, 16 * ks, lane));
 #pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    ldsm4(aw[p], frag_rc<VPI>(sw + p * L::VT, 16 * (m0 + mt), 16 * ks, lane));
-                    ldsm4(au[p], frag_rc<VPI>(su + p * L::VT, 16 * (m0 + mt), 16 * ks, lane));
-                }
+                for (int p = 0; p < KP; ++p) ldsm4(ao[p], frag_rc<VPI>(so + p * L::VT, 16 * bi, 16 * ks, lane));
 #pragma unroll
                 for (int s = 2; s >= 0; --s)
 #pragma unroll
                     for (int p = 2; p >= 0; --p)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (s < PL && plane_pair(s, p, PL)) mma_bf16(E[e], aw[s < PL ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
+                            if (s < KP && plane_pair(s, p, 3)) mma_bf16(DP[e], ao[s < KP ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
+                        }
+            }
+        }
+        // products with the states over this column tile
+        for (int ks = 0; ks < rest / 16; ++ks) {
+            unsigned bs[2][2][3], bd[2][2][PL];                   // [8-column tile][k half][plane]
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    split_bf16<3>(xs[e][m].x, xs[e][m].y, bs[e][m]);
+                    split_bf16<PL>(ys[e][m].x, ys[e][m].y, bd[e][m]);
+                }
+            fetch(ks + 1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                unsigned a[3][4];
+                const int r0 = 16 * (m0 + mt);
+#pragma unroll
+                for (int p = 0; p < KP; ++p) ldsm4(a[p], frag_rc<VPI>(so + p * L::VT, r0, 16 * ks, lane));
+#pragma unroll
+                for (int s = KP - 1; s >= 0; --s)
+#pragma unroll
+                    for (int p = 2; p >= 0; --p)
                         if (plane_pair(s, p, 3))
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                if (s < KP) mma_bf16(G1[mt][e], ao[s < KP ? s : 0], bs[e][0][p], bs[e][1][p]);
-                                mma_bf16(G2[mt][e], aw[s], bs[e][0][p], bs[e][1][p]);
-                                mma_bf16(G3[mt][e], au[s], be1[e][0][p], be1[e][1][p]);
-                            }
+                            for (int e = 0; e < 2; ++e) mma_bf16(G1[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
+#pragma unroll
+                for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<VPI>(sw + p * L::VT, r0, 16 * ks, lane));
+#pragma unroll
+                for (int s = PL - 1; s >= 0; --s)
+#pragma unroll
+                    for (int p = PL - 1; p >= 0; --p)
+                        if (plane_pair(s, p, PL))
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) mma_bf16(G2[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
+#pragma unroll
+                for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<VPI>(sr + p * L::VT, r0, 16 * ks, lane));
+#pragma unroll
+                for (int s = PL - 1; s >= 0; --s)
+#pragma unroll
+                    for (int p = PL - 1; p >= 0; --p)
+                        if (plane_pair(s, p, PL))
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) mma_bf16(G3[mt][e], a[s], bd[e][0][p], bd[e][1][p]);
             }
         }
     }
-    // row products with q and k over this warp's columns, then the three terms in place
-    auto tile2 = [&](int base, int r, int c) {                    // two neighbouring elements
-        float2 x = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int p = KP - 1; p >= 0; --p) {
-            const unsigned y = *reinterpret_cast<const unsigned *>(smem + base + p * L::TILE + r * KPI + 2 * c);
-            x.x += lo_f32(y);
-            x.y += hi_f32(y);
-        }
-        return x;
-    };
+    // the terms of dq and dk in place, and the row products with q over this warp's columns
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = 16 * (m0 + mt) + g4 + 8 * half;
-            float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-            const float f = from[r], f1 = f * d.scale, f2 = -be[r] * f, f3 = to[r];
+            float s1 = 0.f;
+            const float f = from[r], f1 = f * d.scale, f2 = -be[r] * f, f3 = to[r] * be[r];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int c = dk0 + 8 * e + 2 * i4;
-                const float2 qq = tile2(L::Q, r, c), kk = tile2(0, r, c);
                 float *a = &G1[mt][e][2 * half], *x = &G2[mt][e][2 * half], *y = &G3[mt][e][2 * half];
-                a[0] *= f1; a[1] *= f1;
-                y[0] *= f3; y[1] *= f3;
-                s1 = fmaf(qq.x, a[0], fmaf(qq.y, a[1], s1));
-                s2 = fmaf(kk.x, x[0], fmaf(kk.y, x[1], s2));
-                s3 = fmaf(kk.x, y[0], fmaf(kk.y, y[1], s3));
-                x[0] = fmaf(f2, x[0], y[0]);                      // both terms of dk
-                x[1] = fmaf(f2, x[1], y[1]);
-            }
+                a[0] *= f1;
+                a[1] *= f1;
 #pragma unroll
-            for (int m = 1; m < 4; m *= 2) {
-                s1 += __shfl_xor_sync(~0u, s1, m);
-                s2 += __shfl_xor_sync(~0u, s2, m);
-                s3 += __shfl_xor_sync(~0u, s3, m);
+                for (int p = KP - 1; p >= 0; --p) {
+                    const unsigned qq = *reinterpret_cast<const unsigned *>(smem + L::Q + p * L::TILE + r * KPI + 2 * c);
+                    s1 = fmaf(lo_f32(qq), a[0], fmaf(hi_f32(qq), a[1], s1));
+                }
+                x[0] = fmaf(f2, x[0], f3 * y[0]);
+                x[1] = fmaf(f2, x[1], f3 * y[1]);
             }
-            if (i4 == 0) {
-                float *p = dots + (warp % NWK) * 3 * C + r;
-                p[0] = s1;
-                p[C] = s2;
-                p[2 * C] = s3;
-            }
+            s1 += __shfl_xor_sync(~0u, s1, 1);
+            s1 += __shfl_xor_sync(~0u, s1, 2);
+            if (i4 == 0) dots[(warp % NWK) * C + r] = s1;
         }
-    if (warp / NWK == 0) {                                        // warps that share columns agree
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) inner += __shfl_xor_sync(~0u, inner, m);
-        if (lane == 0) ends[warp] = inner;
-    }
-    // the C x C blocks: A and P again, then a, p, and what goes into the gates
-#pragma unroll
-    for (int x = 0; x < BPW; ++x) {
-        const int idx = warp + 8 * x;
-        if (idx >= BLOCKS) break;
-        const int bi = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, bj = idx - bi * (bi + 1) / 2;
-        float kk[2][4] = {}, qk[2][4] = {};
+    // the C x C blocks: q k^T again, then a, p and the row sums of p * (q k^T)
+    if (block) {
+        float qk[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < DKP / 16; ++ks) {
-            unsigned ak[KP][4], aq[KP][4], bk[KP][4];
+            unsigned aq[KP][4], bk[KP][4];
 #pragma unroll
             for (int p = 0; p < KP; ++p) {
-                ldsm4(ak[p], frag_rc<KPI>(sk + p * L::TILE, 16 * bi, 16 * ks, lane));
                 ldsm4(aq[p], frag_rc<KPI>(sq + p * L::TILE, 16 * bi, 16 * ks, lane));
                 ldsm4(bk[p], frag_cr<KPI>(sk + p * L::TILE, 16 * bj, 16 * ks, lane));
             }
@@ -559,63 +575,71 @@ __global__ void __launch_bounds__(kBackThreads, 1)
                 for (int p = KP - 1; p >= 0; --p)
                     if (plane_pair(s, p, KP))
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            mma_bf16(kk[e], ak[s], bk[p][2 * e], bk[p][2 * e + 1]);
-                            mma_bf16(qk[e], aq[s], bk[p][2 * e], bk[p][2 * e + 1]);
-                        }
+                        for (int e = 0; e < 2; ++e) mma_bf16(qk[e], aq[s], bk[p][2 * e], bk[p][2 * e + 1]);
         }
-        float col[2][2] = {};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int t = 16 * bi + g4 + 8 * half;
-            float zr = 0.f, er = 0.f;
+            float zr = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float pa[2], aa[2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const int s = 16 * bj + 8 * e + 2 * i4 + m, i = 2 * half + m;
-                    const float f = s <= t ? expf((hi[t] - hi[s]) + (lo[t] - lo[s])) : 0.f;
-                    const float A = s < t ? kk[e][i] * f : 0.f, Pq = s <= t ? d.scale * (qk[e][i] * f) : 0.f;
-                    const float da = s < t ? -be[t] * E[x][e][i] : 0.f, dp = s <= t ? DP[x][e][i] : 0.f;
-                    const float z = fmaf(da, A, dp * Pq);
-                    er = s < t ? fmaf(E[x][e][i], A, er) : er;
-                    zr += z;
-                    col[e][m] += z;
-                    aa[m] = da * f;
-                    pa[m] = d.scale * (dp * f);
+                    const float f = s <= t ? expf((hi[t] - hi[s]) + (lo[t] - lo[s])) * be[s] : 0.f;
+                    pa[m] = s <= t ? d.scale * (DP[e][i] * f) : 0.f;
+                    aa[m] = s < t ? -be[t] * (E[e][i] * f) : 0.f;
+                    zr = s <= t ? fmaf(pa[m], qk[e][i], zr) : zr;
                 }
-                unsigned pl[GP];
+                unsigned pl[PL];
                 const int at = t * GPI + 2 * (16 * bj + 8 * e + 2 * i4);
-                split_bf16<GP>(pa[0], pa[1], pl);
+                split_bf16<PL>(pa[0], pa[1], pl);
 #pragma unroll
-                for (int p = 0; p < GP; ++p) *reinterpret_cast<unsigned *>(smem + L::P + p * L::GT + at) = pl[p];
-                split_bf16<GP>(aa[0], aa[1], pl);
+                for (int p = 0; p < PL; ++p) *reinterpret_cast<unsigned *>(smem + L::P + p * L::GT + at) = pl[p];
+                split_bf16<PL>(aa[0], aa[1], pl);
 #pragma unroll
-                for (int p = 0; p < GP; ++p) *reinterpret_cast<unsigned *>(smem + L::A + p * L::GT + at) = pl[p];
+                for (int p = 0; p < PL; ++p) *reinterpret_cast<unsigned *>(smem + L::A + p * L::GT + at) = pl[p];
             }
-#pragma unroll
-            for (int m = 1; m < 4; m *= 2) {
-                zr += __shfl_xor_sync(~0u, zr, m);
-                er += __shfl_xor_sync(~0u, er, m);
-            }
-            if (i4 == 0) {
-                zrow[bj * C + t] = zr;
-                erow[bj * C + t] = er;
-            }
+            zr += __shfl_xor_sync(~0u, zr, 1);
+            zr += __shfl_xor_sync(~0u, zr, 2);
+            if (i4 == 0) zrow[bj * C + t] = zr;
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                float c = col[e][m];
-                c += __shfl_xor_sync(~0u, c, 4);
-                c += __shfl_xor_sync(~0u, c, 8);
-                c += __shfl_xor_sync(~0u, c, 16);
-                if (g4 == 0) zcol[bi * C + 16 * bj + 8 * e + 2 * i4 + m] = c;
-            }
     }
     __syncthreads();
+    if (warp == L::WARPS - 1) {
+        constexpr int TL = C / 32;
+        double suf[TL], rev = 0.0;
+#pragma unroll
+        for (int i = TL - 1; i >= 0; --i) {
+            const int r = lane * TL + i;
+            float z = 0.f, x = 0.f;
+#pragma unroll
+            for (int p = 0; p < NB; ++p)
+                if (16 * p <= r) z += zrow[p * C + r];
+#pragma unroll
+            for (int p = 0; p < NWK; ++p) x += dots[p * C + r];
+            rev += (double)(z + x) - (double)be[r] * (double)dwv[r];
+            suf[i] = rev;
+        }
+        double after = rev;
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2) {
+            const double y = __shfl_down_sync(~0u, after, m);
+            if (lane + m < 32) after += y;
+        }
+        after -= rev;
+#pragma unroll
+        for (int p = 0; p < L::WARPS; ++p) after += (double)ends[p];
+#pragma unroll
+        for (int i = 0; i < TL; ++i) {
+            const int r = lane * TL + i;
+            if (r < rows) {
+                gdec[(long long)r * d.H] = r < nt ? (float)(after + suf[i]) : 0.f;
+                gbeta[(long long)r * d.H] = r < nt ? dwr[r] : 0.f;
+            }
+        }
+    }
     // dq += p K;  dk += p^T Q + (a + a^T) K
     const unsigned gp = sk + L::P, ga = sk + L::A;
 #pragma unroll
@@ -629,30 +653,30 @@ __global__ void __launch_bounds__(kBackThreads, 1)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int m = m0 + mt;
-            auto add = [&](float (&acc)[2][4], const unsigned (&a)[GP][4], const unsigned (&bb)[KP][4]) {
+            auto add = [&](float (&acc)[2][4], const unsigned (&a)[PL][4], const unsigned (&bb)[KP][4]) {
 #pragma unroll
-                for (int s = GP - 1; s >= 0; --s)
+                for (int s = PL - 1; s >= 0; --s)
 #pragma unroll
                     for (int p = KP - 1; p >= 0; --p)
-                        if (plane_pair(s, p, GP))
+                        if (plane_pair(s, p, PL))
 #pragma unroll
                             for (int e = 0; e < 2; ++e) mma_bf16(acc[e], a[s], bb[p][2 * e], bb[p][2 * e + 1]);
             };
-            unsigned a[GP][4];
+            unsigned a[PL][4];
             if (ks <= m) {
 #pragma unroll
-                for (int p = 0; p < GP; ++p) ldsm4(a[p], frag_rc<GPI>(gp + p * L::GT, 16 * m, 16 * ks, lane));
+                for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<GPI>(gp + p * L::GT, 16 * m, 16 * ks, lane));
                 add(G1[mt], a, bk);
 #pragma unroll
-                for (int p = 0; p < GP; ++p) ldsm4(a[p], frag_rc<GPI>(ga + p * L::GT, 16 * m, 16 * ks, lane));
+                for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<GPI>(ga + p * L::GT, 16 * m, 16 * ks, lane));
                 add(G2[mt], a, bk);
             }
             if (ks >= m) {
 #pragma unroll
-                for (int p = 0; p < GP; ++p) ldsm4t(a[p], frag_cr<GPI>(gp + p * L::GT, 16 * ks, 16 * m, lane));
+                for (int p = 0; p < PL; ++p) ldsm4t(a[p], frag_cr<GPI>(gp + p * L::GT, 16 * ks, 16 * m, lane));
                 add(G2[mt], a, bq);
 #pragma unroll
-                for (int p = 0; p < GP; ++p) ldsm4t(a[p], frag_cr<GPI>(ga + p * L::GT, 16 * ks, 16 * m, lane));
+                for (int p = 0; p < PL; ++p) ldsm4t(a[p], frag_cr<GPI>(ga + p * L::GT, 16 * ks, 16 * m, lane));
                 add(G2[mt], a, bk);
             }
         }
@@ -672,61 +696,6 @@ __global__ void __launch_bounds__(kBackThreads, 1)
                 store2(true, r, c, live ? G2[mt][e][2 * half] : 0.f, live ? G2[mt][e][2 * half + 1] : 0.f);
             }
         }
-    if (warp == 0) {
-        // dg_t = sum_{t' >= t} (rows - columns + products) + sum_{t' < t} (products with D1) + G_C <S0, D1>
-        constexpr int PL = C / 32;
-        double suf[PL], pre[PL], run = 0.0, rev = 0.0;
-        float dbeta[PL];
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int r = lane * PL + i;
-            float zr = 0.f, zc = 0.f, er = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
-#pragma unroll
-            for (int p = 0; p < NB; ++p) {
-                if (16 * p <= r) {
-                    zr += zrow[p * C + r];
-                    er += erow[p * C + r];
-                }
-                if (16 * p + 15 >= r) zc += zcol[p * C + r];
-            }
-#pragma unroll
-            for (int p = 0; p < NWK; ++p) {
-                x1 += dots[(p * 3) * C + r];
-                x2 += dots[(p * 3 + 1) * C + r];
-                x3 += dots[(p * 3 + 2) * C + r];
-            }
-            dbeta[i] = dwv[r] - from[r] * x2 - er;
-            pre[i] = run;                                         // of this lane's earlier tokens
-            run += (double)x3;
-            suf[i] = (double)((zr - zc) + (x1 - be[r] * from[r] * x2));
-        }
-#pragma unroll
-        for (int i = PL - 1; i >= 0; --i) {
-            rev += suf[i];
-            suf[i] = rev;
-        }
-        double before = run, after = rev;
-#pragma unroll
-        for (int m = 1; m < 32; m *= 2) {
-            const double x = __shfl_up_sync(~0u, before, m), y = __shfl_down_sync(~0u, after, m);
-            if (lane >= m) before += x;
-            if (lane + m < 32) after += y;
-        }
-        before -= run;
-        after -= rev;
-        double whole = 0.0;
-#pragma unroll
-        for (int p = 0; p < NWK; ++p) whole += (double)ends[p];
-        whole *= (double)from[C - 1];
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int r = lane * PL + i;
-            if (r < rows) {
-                gdec[(long long)r * d.H] = r < nt ? (float)(after + suf[i] + before + pre[i] + whole) : 0.f;
-                gbeta[(long long)r * d.H] = r < nt ? dbeta[i] : 0.f;
-            }
-        }
-    }
 }
 
 // value heads that share a key head: their parts added in head order
@@ -762,7 +731,7 @@ cudaError_t back_local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPla
     auto kern = k_delta_back_local<T, DKP>;
     constexpr int bytes = BackLocalSmem<T, DKP>::BYTES;
     set_kernel_smem(kern, bytes);
-    kern<<<(unsigned)delta_chunks(d), kBackThreads, bytes, st>>>(d, in, q, k, w, o);
+    kern<<<(unsigned)delta_chunks(d), BackLocalSmem<T, DKP>::WARPS * 32, bytes, st>>>(d, in, q, k, w, o);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || d.H == d.Hk) return e;
     const long long rows = (long long)d.B * d.T, units = rows * d.Hk * (d.Dk / 4), blocks = (units + 255) / 256;

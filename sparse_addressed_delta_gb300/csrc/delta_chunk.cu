@@ -1,9 +1,9 @@
 // The gated delta rule in chunks of C tokens. With S0 the state at a chunk's start, L the running
 // sum of the log-decays inside the chunk (inclusive) and G = e^L:
 //   A[t,s] = k_t . k_s e^{L_t - L_s}  (s < t);   P[t,s] = scale q_t . k_s e^{L_t - L_s}  (s <= t)
-//   X = (I + diag(beta) A)^-1
-//   w = v - G (K S0);   u = X (beta w);   o = scale G (Q S0) + P u;   S1 = G_C S0 + K^T (e^{L_C - L} u)
-// X, P and the gates need no state: k_delta_local computes them for all chunks at once. k_delta_scan
+//   X = (I + A diag(beta))^-1;   r = X (v - G (K S0)), what each value lacks;   u = beta r
+//   o = scale G (Q S0) + P u;    S1 = G_C S0 + K^T (e^{L_C - L} u)
+// X, P diag(beta) and the gates need no state: k_delta_local computes them for all chunks at once. k_delta_scan
 // then walks over each head's chunks.
 //
 // The scan keeps everything transposed, [Dv] x [tokens or Dk]: a warp owns 16 of the state's columns
@@ -20,50 +20,93 @@
 namespace sdm {
 namespace {
 
+constexpr int kLocalHeads = 4;          // value heads of one key head a block takes at most
+
 template <int KP, int DKP, int C, bool TC>
 struct LocalSmem {
     static constexpr int KPITCH = delta_pitch(DKP * 2), TILE = C * KPITCH, NP = C + 4, XP = delta_pitch(C * 2);
-    // K and Q make room for the inverse (and its planes) once their products are taken
+    // K and Q make room for the inverse (and two of its planes) once their products are taken
     static constexpr int Q = KP * TILE, X = 0, XPL = C * NP * 4, FIRST = 2 * KP * TILE;
     static constexpr int SECOND = XPL + (TC ? 2 * C * XP : 0);
     static constexpr int N = FIRST > SECOND ? FIRST : SECOND, G = N + C * NP * 4;
-    static constexpr int BYTES = G + 3 * C * 4;
+    static constexpr int BYTES = G + kLocalHeads * 3 * C * 4;
 };
 
-// One block per chunk and head, one warp per 16 tokens. The products K K^T and Q K^T (blocks on and
-// below the diagonal), the decays, then the inverse of I + N, N = diag(beta) A: 16 x 16 diagonal
-// blocks by substitution, a warp each, a lane a column; then warp j goes down block column j,
-// X_ij = -X_ii sum_l N_il X_lj, which needs only its own column and the diagonal blocks.
-// TC: for the tcgen05 scan, Y = X diag(beta) in the place of X and Z = P Y in the place of P (the product
-// P X from two terms of each, as exact as the bfloat16 readings need).
-template <int KP, int DKP, int C, int PP, bool TC>
-__global__ void __launch_bounds__(2 * C)
-    k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w) {
+// acc[i][e] += sum over m of A[row0 + i][m0 + m] B[m0 + m][col + e], m < M (a multiple of 4); both in
+// shared memory with rows of NP floats
+template <int ROWS, int NP>
+__device__ __forceinline__ void tile_product(float (&acc)[ROWS][2], const float *A, const float *B, int M) {
+    for (int m = 0; m < M; m += 4) {
+        float2 x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float2 *>(B + (m + e) * NP);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const float4 a = *reinterpret_cast<const float4 *>(A + i * NP + m);
+            acc[i][0] = fmaf(a.x, x[0].x, fmaf(a.y, x[1].x, fmaf(a.z, x[2].x, fmaf(a.w, x[3].x, acc[i][0]))));
+            acc[i][1] = fmaf(a.x, x[0].y, fmaf(a.y, x[1].y, fmaf(a.z, x[2].y, fmaf(a.w, x[3].y, acc[i][1]))));
+        }
+    }
+}
+
+// X[lo.., c0..] = -X[lo.., lo..] N[lo.., c0..] X[c0.., c0..] for blocks of HALF rows and columns whose
+// diagonal blocks are inverted: a warp takes 8 of the columns, which are its own in both products, so
+// it needs no other warp. `part`: which 8.
+template <int HALF, int NP>
+__device__ __forceinline__ void merge_columns(const float *N, float *X, int c0, int part, int lane) {
+    constexpr int ROWS = HALF / 8;                     // a lane: ROWS rows x 2 columns
+    const int lo = c0 + HALF, col = c0 + 8 * part + 2 * (lane & 3), row = lo + ROWS * (lane >> 2);
+    const int first = 8 * part / 16 * 16;              // the right factor is 0 above its diagonal blocks
+    float acc[ROWS][2] = {};
+    tile_product<ROWS, NP>(acc, N + row * NP + c0 + first, X + (c0 + first) * NP + col, HALF - first);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) *reinterpret_cast<float2 *>(X + (row + i) * NP + col) = make_float2(acc[i][0], acc[i][1]);
+    __syncwarp();
+    float out[ROWS][2] = {};
+    const int upto = (row - lo) / 16 * 16 + 16;        // and the left one
+    tile_product<ROWS, NP>(out, X + row * NP + lo, X + lo * NP + col, upto);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) *reinterpret_cast<float2 *>(X + (row + i) * NP + col) = make_float2(-out[i][0], -out[i][1]);
+}
+
+// One block per chunk and up to kLocalHeads value heads that share a key head, one warp per 16 tokens.
+// The products K K^T and Q K^T (blocks on and below the diagonal) are taken once for all of them and
+// stay in registers. For each head: the decays, then the inverse of I + N, N = A diag(beta) (BACK:
+// diag(beta) A): 16 x 16 diagonal blocks by substitution, a warp each, a lane a column, then merged
+// in pairs, -X_2 N X_1, with the columns spread over the warps.
+// TC: for the tcgen05 scan, Z = P X in the place of P (from two terms of each, as exact as the bfloat16
+// readings need).
+// What bounds it: issue. At C = 64 the merges take about 40 % of its instructions, the planes 25 %.
+template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
+__global__ void __launch_bounds__(2 * C, C == 64 ? 4 : 1)
+    k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, int heads) {
     using L = LocalSmem<KP, DKP, C, TC>;
     constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = delta_pitch(C * 2), KPI = L::KPITCH;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long bhn = blockIdx.x;
-    if (bhn == 0 && tid == 0) *w.status = DevStatus{};
+    if (blockIdx.x == 0 && tid == 0) *w.status = DevStatus{};
     auto plane_at = [](int r, int c) { return TC ? tc_at(r, c) : delta_at<XP>(r, c); };
     constexpr int PLANE = C * (TC ? 128 : XP);
-    const int n = (int)(bhn % d.Nt);
-    const long long bh = bhn / d.Nt;
-    const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
+    const int n = (int)(blockIdx.x % d.Nt);
+    const long long bg = blockIdx.x / d.Nt;                        // sequence and group of heads
+    const int groups = d.H / heads, b = (int)(bg / groups), h0 = (int)(bg % groups) * heads, hk = h0 / (d.H / d.Hk);
     const int t0 = n * C;
     int nt = delta_valid(in.valid, b, d.T) - t0;
     if (nt <= 0) return;
     nt = nt < C ? nt : C;
     const unsigned sk = smem_u32(smem), sq = sk + L::Q;
     float *N = reinterpret_cast<float *>(smem + L::N), *X = reinterpret_cast<float *>(smem + L::X);
-    float *hi = reinterpret_cast<float *>(smem + L::G), *lo = hi + C, *be = lo + C;
+    float *gates = reinterpret_cast<float *>(smem + L::G);         // [head][hi, lo, beta][C]
 
     load_tokens<KP, DKP, C, THREADS>(sk, k, b * k.s[0] + t0 * k.s[1] + hk * k.s[2], d.Dk, nt, tid);
     load_tokens<KP, DKP, C, THREADS>(sq, q, b * q.s[0] + t0 * q.s[1] + hk * q.s[2], d.Dk, nt, tid);
     cp_async_commit();
-    if (warp == 0) {
+    for (int hh = warp; hh < heads; hh += NB) {
         // running sums in double: differences of large sums (resets inside the chunk) stay exact
         constexpr int PL = C / 32;
+        const int h = h0 + hh;
+        float *hi = gates + hh * 3 * C, *lo = hi + C, *be = lo + C;
         double run[PL];
         float bt[PL];
         double s = 0.0;
@@ -84,7 +127,7 @@ __global__ void __launch_bounds__(2 * C)
         }
         const double all = __shfl_sync(~0u, before, 31);
         before -= s;
-        float *aux = w.aux + bhn * 3 * C;
+        float *aux = w.aux + (((long long)b * d.H + h) * d.Nt + n) * 3 * C;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
             const int r = lane * PL + i;
@@ -93,59 +136,67 @@ __global__ void __launch_bounds__(2 * C)
             lo[r] = (float)(x - (double)(float)x);
             be[r] = bt[i];
             aux[r] = expf((float)x);
-            aux[C + r] = expf((float)(all - x));
+            aux[C + r] = expf((float)(all - x)) * (BACK ? 1.f : bt[i]);
             aux[2 * C + r] = bt[i];
         }
     }
     cp_async_wait<0>();
     __syncthreads();
 
-    float pv[TC ? C / 8 : 1][4];
-    {
-        float kk[C / 8][4] = {}, qk[C / 8][4] = {};
+    float kk[C / 8][4] = {}, qk[C / 8][4] = {};
 #pragma unroll
-        for (int ks = 0; ks < DKP / 16; ++ks) {
-            unsigned ak[KP][4], aq[KP][4];
+    for (int ks = 0; ks < DKP / 16; ++ks) {
+        unsigned ak[KP][4], aq[KP][4];
 #pragma unroll
-            for (int p = 0; p < KP; ++p) {
-                ldsm4(ak[p], frag_rc<KPI>(sk + p * L::TILE, 16 * warp, 16 * ks, lane));
-                ldsm4(aq[p], frag_rc<KPI>(sq + p * L::TILE, 16 * warp, 16 * ks, lane));
-            }
-#pragma unroll
-            for (int jj = 0; jj < NB; ++jj) {
-                if (jj > warp) break;
-                unsigned bk[KP][4];
-#pragma unroll
-                for (int p = 0; p < KP; ++p)
-                    ldsm4(bk[p], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
-#pragma unroll
-                for (int x = KP - 1; x >= 0; --x)
-#pragma unroll
-                    for (int y = KP - 1; y >= 0; --y)
-                        if (plane_pair(x, y, KP))
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                mma_bf16(kk[2 * jj + e], ak[x], bk[y][2 * e], bk[y][2 * e + 1]);
-                                mma_bf16(qk[2 * jj + e], aq[x], bk[y][2 * e], bk[y][2 * e + 1]);
-                            }
-            }
+        for (int p = 0; p < KP; ++p) {
+            ldsm4(ak[p], frag_rc<KPI>(sk + p * L::TILE, 16 * warp, 16 * ks, lane));
+            ldsm4(aq[p], frag_rc<KPI>(sq + p * L::TILE, 16 * warp, 16 * ks, lane));
         }
+#pragma unroll
+        for (int jj = 0; jj < NB; ++jj) {
+            if (jj > warp) break;
+            unsigned bk[KP][4];
+#pragma unroll
+            for (int p = 0; p < KP; ++p)
+                ldsm4(bk[p], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+#pragma unroll
+            for (int x = KP - 1; x >= 0; --x)
+#pragma unroll
+                for (int y = KP - 1; y >= 0; --y)
+                    if (plane_pair(x, y, KP))
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            mma_bf16(kk[2 * jj + e], ak[x], bk[y][2 * e], bk[y][2 * e + 1]);
+                            mma_bf16(qk[2 * jj + e], aq[x], bk[y][2 * e], bk[y][2 * e + 1]);
+                        }
+        }
+    }
+    __syncthreads();                                               // K and Q are used
+    for (int hh = 0; hh < heads; ++hh) {
+        const long long bhn = ((long long)b * d.H + h0 + hh) * d.Nt + n;
+        const float *hi = gates + hh * 3 * C, *lo = hi + C, *be = lo + C;
         unsigned char *pimg = w.p + bhn * (size_t)(PP * PLANE);
+        // P of a forward carries the corrections' beta: u = beta r
+        auto p_pair = [&](int j, int half, float (&pp)[2], float (&nn)[2]) {
+            const int t = 16 * warp + (lane >> 2) + 8 * half;
+            const float ht = hi[t], lt = lo[t], bt = be[t];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int s = 8 * j + 2 * (lane & 3) + e;
+                const float f = s <= t ? expf((ht - hi[s]) + (lt - lo[s])) : 0.f, bs = be[s];
+                nn[e] = s < t ? kk[j][2 * half + e] * f * (BACK ? bt : bs) : 0.f;
+                pp[e] = s <= t ? d.scale * qk[j][2 * half + e] * f * (BACK ? 1.f : bs) : 0.f;
+            }
+        };
+        float pv[TC ? C / 8 : 1][4];
 #pragma unroll
         for (int j = 0; j < C / 8; ++j) {
             if (j > 2 * warp + 1) break;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int t = 16 * warp + (lane >> 2) + 8 * half;
-                const float bt = be[t];
                 float nn[2], pp[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int s = 8 * j + 2 * (lane & 3) + e;
-                    const float f = s <= t ? expf((hi[t] - hi[s]) + (lo[t] - lo[s])) : 0.f;
-                    nn[e] = s < t ? bt * kk[j][2 * half + e] * f : 0.f;
-                    pp[e] = s <= t ? d.scale * qk[j][2 * half + e] * f : 0.f;
-                }
+                p_pair(j, half, pp, nn);
                 *reinterpret_cast<float2 *>(N + t * NP + 8 * j + 2 * (lane & 3)) = make_float2(nn[0], nn[1]);
                 if constexpr (TC) {
                     pv[j][2 * half] = pp[0];
@@ -159,119 +210,86 @@ __global__ void __launch_bounds__(2 * C)
                 }
             }
         }
-    }
-    __syncthreads();                                             // K and Q are used
-    if (lane < 16) {
-        float x[16];
-        const float *D = N + (16 * warp) * NP + 16 * warp;
+        __syncwarp();
+        if (lane < 16) {
+            float x[16];
+            const float *D = N + (16 * warp) * NP + 16 * warp;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == lane ? 1.f : 0.f;
+            for (int i = 0; i < 16; ++i) {
+                float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-            for (int l = 0; l < i; ++l) s = fmaf(-D[i * NP + l], x[l], s);
-            x[i] = s;
-            X[(16 * warp + i) * NP + 16 * warp + lane] = s;
-        }
-    }
-    __syncthreads();
-    {
-        const int c = lane & 15, r0 = (lane >> 4) * 8, j = warp;
-        for (int i = j + 1; i < NB; ++i) {
-            float acc[8] = {};
-            for (int m = 16 * j; m < 16 * i; m += 4) {
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = X[(m + e) * NP + 16 * j + c];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float4 a = *reinterpret_cast<const float4 *>(N + (16 * i + r0 + r) * NP + m);
-                    acc[r] = fmaf(a.x, x[0], fmaf(a.y, x[1], fmaf(a.z, x[2], fmaf(a.w, x[3], acc[r]))));
+                for (int l = 0; l < i; l += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(D + i * NP + l);
+                    s0 = fmaf(-a.x, x[l], s0);
+                    if (l + 1 < i) s1 = fmaf(-a.y, x[l + 1], s1);
+                    if (l + 2 < i) s0 = fmaf(-a.z, x[l + 2], s0);
+                    if (l + 3 < i) s1 = fmaf(-a.w, x[l + 3], s1);
                 }
+                x[i] = s0 + s1;
+                X[(16 * warp + i) * NP + 16 * warp + lane] = x[i];
             }
-            float *blk = X + (16 * i) * NP + 16 * j;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) blk[(r0 + r) * NP + c] = acc[r];
-            __syncwarp();
-            float out[8] = {};
-#pragma unroll
-            for (int m = 0; m < 16; m += 4) {
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = blk[(m + e) * NP + c];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float4 a = *reinterpret_cast<const float4 *>(X + (16 * i + r0 + r) * NP + 16 * i + m);
-                    out[r] = fmaf(a.x, x[0], fmaf(a.y, x[1], fmaf(a.z, x[2], fmaf(a.w, x[3], out[r]))));
-                }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int r = 0; r < 8; ++r) blk[(r0 + r) * NP + c] = -out[r];
-            __syncwarp();
         }
-    }
-    __syncthreads();
-    unsigned char *ximg = w.x + bhn * (size_t)(3 * PLANE);
-    for (int i = tid; i < C * (C / 8); i += THREADS) {
-        const int r = i / (C / 8), c = i % (C / 8);
-        if (c > 2 * (r >> 4) + 1) continue;
-        unsigned pl[4][3], raw[4][2];
+        __syncthreads();
+        // 16 -> 32: each pair's 16 columns over two warps; 32 -> 64: the 32 columns over four
+        merge_columns<16, NP>(N, X, 32 * (warp >> 1), warp & 1, lane);
+        __syncthreads();
+        if constexpr (C == 64) {
+            merge_columns<32, NP>(N, X, 0, warp, lane);
+            __syncthreads();
+        }
+        unsigned char *ximg = w.x + bhn * (size_t)(3 * PLANE);
+        for (int i = tid; i < C * (C / 8); i += THREADS) {
+            const int r = i / (C / 8), c = i % (C / 8);
+            if (c > 2 * (r >> 4) + 1) continue;
+            unsigned pl[4][3];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 x = *reinterpret_cast<const float2 *>(X + r * NP + 8 * c + 2 * e);
-            if constexpr (TC) {
-                split_bf16<2>(x.x, x.y, raw[e]);
-                split_bf16<3>(x.x * be[8 * c + 2 * e], x.y * be[8 * c + 2 * e + 1], pl[e]);
-            } else {
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = *reinterpret_cast<const float2 *>(X + r * NP + 8 * c + 2 * e);
                 split_bf16<3>(x.x, x.y, pl[e]);
             }
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const uint4 y = make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
+                *reinterpret_cast<uint4 *>(ximg + p * PLANE + plane_at(r, c)) = y;
+                if (TC && p < 2) *reinterpret_cast<uint4 *>(smem + L::XPL + p * C * XP + delta_at<XP>(r, c)) = y;
+            }
         }
-        if constexpr (TC)
+        if constexpr (TC) {
+            __syncthreads();
+            float z[C / 8][4] = {};
+            const unsigned sx = smem_u32(smem) + L::XPL;
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                *reinterpret_cast<uint4 *>(smem + L::XPL + p * C * XP + delta_at<XP>(r, c)) =
-                    make_uint4(raw[0][p], raw[1][p], raw[2][p], raw[3][p]);
+            for (int ks = 0; ks < NB; ++ks) {                      // the accumulators of P are its A operand
+                if (ks > warp) break;
+                unsigned a[2][4];
+                split_frag<2>(pv, ks, a);
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-            *reinterpret_cast<uint4 *>(ximg + p * PLANE + plane_at(r, c)) =
-                make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
-    }
-    if constexpr (TC) {
-        __syncthreads();
-        float z[C / 8][4] = {};
-        const unsigned sx = smem_u32(smem) + L::XPL;
+                for (int jj = 0; jj <= ks; ++jj) {
+                    unsigned bb[2][4];
 #pragma unroll
-        for (int ks = 0; ks < NB; ++ks) {                         // the accumulators of P are its A operand
-            if (ks > warp) break;
-            unsigned a[2][4];
-            split_frag<2>(pv, ks, a);
+                    for (int p = 0; p < 2; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
 #pragma unroll
-            for (int jj = 0; jj <= ks; ++jj) {
-                unsigned bb[2][4];
+                    for (int e = 0; e < 2; ++e) {
+                        mma_bf16(z[2 * jj + e], a[1], bb[0][2 * e], bb[0][2 * e + 1]);
+                        mma_bf16(z[2 * jj + e], a[0], bb[1][2 * e], bb[1][2 * e + 1]);
+                        mma_bf16(z[2 * jj + e], a[0], bb[0][2 * e], bb[0][2 * e + 1]);
+                    }
+                }
+            }
 #pragma unroll
-                for (int p = 0; p < 2; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
+            for (int j = 0; j < C / 8; ++j) {
+                if (j > 2 * warp + 1) break;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mma_bf16(z[2 * jj + e], a[1], bb[0][2 * e], bb[0][2 * e + 1]);
-                    mma_bf16(z[2 * jj + e], a[0], bb[1][2 * e], bb[1][2 * e + 1]);
-                    mma_bf16(z[2 * jj + e], a[0], bb[0][2 * e], bb[0][2 * e + 1]);
+                for (int half = 0; half < 2; ++half) {
+                    unsigned pl[PP];
+                    split_bf16<PP>(z[j][2 * half], z[j][2 * half + 1], pl);
+#pragma unroll
+                    for (int p = 0; p < PP; ++p)
+                        *reinterpret_cast<unsigned *>(pimg + p * PLANE + plane_at(16 * warp + (lane >> 2) + 8 * half, j) + 4 * (lane & 3)) = pl[p];
                 }
             }
         }
-        unsigned char *zimg = w.p + bhn * (size_t)(PP * PLANE);
-#pragma unroll
-        for (int j = 0; j < C / 8; ++j) {
-            if (j > 2 * warp + 1) break;
-            const float2 bt = *reinterpret_cast<const float2 *>(be + 8 * j + 2 * (lane & 3));
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                unsigned pl[PP];
-                split_bf16<PP>(z[j][2 * half] * bt.x, z[j][2 * half + 1] * bt.y, pl);
-#pragma unroll
-                for (int p = 0; p < PP; ++p)
-                    *reinterpret_cast<unsigned *>(zimg + p * PLANE + plane_at(16 * warp + (lane >> 2) + 8 * half, j) + 4 * (lane & 3)) = pl[p];
-            }
-        }
+        if (hh + 1 < heads) __syncthreads();                       // X and N for the next head
     }
 }
 
@@ -292,7 +310,7 @@ struct ScanSmem {
 template <typename T, int DKP, int NW, bool SAVE>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_delta_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, float *state,
-                 T *o, float *snap, float *usave) {
+                 T *o, float *snap, float *rsave) {
     using L = ScanSmem<T, DKP, NW>;
     constexpr bool BF = L::BF;
     constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, KPI = L::KPI, THREADS = NW * 32;
@@ -335,6 +353,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
             const int dk = 8 * j + 2 * i4 + (e & 1);
             S[j][e] = mine && dk < d.Dk ? sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] : 0.f;
         }
+    auto store_state = [&](float *dst) {
+#pragma unroll
+        for (int j = 0; j < ND; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dk = 8 * j + 2 * i4 + (e & 1);
+                if (dk < d.Dk) dst[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
+            }
+    };
     if (nch > 0) load(0, 0);
     for (int n = 0; n < nch; ++n) {
         if (n + 1 < nch) {
@@ -346,19 +373,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
         __syncthreads();
         const int stage = (n & 1) * L::STAGE;
         const unsigned sk = s0 + stage, sq = sk + L::Q, sx = sk + L::X, spp = sk + L::P, sv = sk + L::V;
-        const float *from = reinterpret_cast<const float *>(smem + stage + L::AUX), *to = from + C, *be = to + C;
+        const float *from = reinterpret_cast<const float *>(smem + stage + L::AUX), *to = from + C;
         const int nt = ntok - n * C < C ? ntok - n * C : C;
         if (mine) {
-            if constexpr (SAVE) {
-                float *dst = snap + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv + dv0;
-#pragma unroll
-                for (int j = 0; j < ND; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int dk = 8 * j + 2 * i4 + (e & 1);
-                        if (dk < d.Dk) dst[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
-                    }
-            }
+            if constexpr (SAVE) store_state(snap + ((bh * (d.Nt + 1) + n) * (long long)d.Dk) * d.Dv + dv0);
             float R[NT][4] = {}, O[NT][4] = {};
 #pragma unroll
             for (int ks = 0; ks < DKP / 16; ++ks) {          // R = (K S)^T, O = (Q S)^T
@@ -391,7 +409,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                             for (int j = 0; j < NT; ++j)
                                 mma_bf16(O[j], a[x], bb[p][j >> 1][2 * (j & 1)], bb[p][j >> 1][2 * (j & 1) + 1]);
             }
-            // R <- beta (v - G R), O <- scale G O
+            // R <- v - G R, O <- scale G O
 #pragma unroll
             for (int jj = 0; jj < C / 16; ++jj) {
                 float vv[2][4];
@@ -415,13 +433,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int e = 0; e < 8; ++e) {
                     const int j = 2 * jj + (e >> 2), t = 8 * j + 2 * i4 + (e & 1);
                     const float f = from[t];
-                    R[j][e & 3] = be[t] * (vv[e >> 2][e & 3] - f * R[j][e & 3]);
+                    R[j][e & 3] = vv[e >> 2][e & 3] - f * R[j][e & 3];
                     O[j][e & 3] *= d.scale * f;
                 }
             }
             float U[NT][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {            // U = (X (beta w))^T
+            for (int ks = 0; ks < C / 16; ++ks) {            // U = r^T = (X (v - G K S))^T
                 unsigned a[3][4];
                 split_frag<3>(R, ks, a);
 #pragma unroll
@@ -440,7 +458,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 }
             }
             if constexpr (SAVE) {
-                float *dst = usave + ((bh * d.Nt + n) * (long long)C) * d.Dv + dv0;
+                float *dst = rsave + ((bh * d.Nt + n) * (long long)C) * d.Dv + dv0;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -448,7 +466,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         dst[(size_t)(8 * j + 2 * i4 + (e & 1)) * d.Dv + g4 + 8 * (e >> 1)] = U[j][e];
             }
 #pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {            // O += (P u)^T
+            for (int ks = 0; ks < C / 16; ++ks) {            // O += (P diag(beta) r)^T
                 unsigned a[PP][4];
                 split_frag<PP>(U, ks, a);
 #pragma unroll
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     if (t < d.T) *reinterpret_cast<uint4 *>(out + t * orow + dv0 + c * VE) = x;
                 }
             }
-            // S <- G_C S + (e^{L_C - L} u)^T K
+            // S <- G_C S + (e^{L_C - L} beta r)^T K
             unsigned ua[C / 16][3][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -526,15 +544,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
         __syncthreads();
     }
     if (!mine) return;
-    if (nch > 0) {
-#pragma unroll
-        for (int j = 0; j < ND; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int dk = 8 * j + 2 * i4 + (e & 1);
-                if (dk < d.Dk) sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
-            }
-    }
+    if (nch > 0) store_state(sp);
+    if (SAVE) store_state(snap + ((bh * (d.Nt + 1) + nch) * (long long)d.Dk) * d.Dv + dv0);
     constexpr int PR = 16 / VE;
     for (long long t = (long long)nch * C + lane / PR; t < d.T; t += 32 / PR)
         *reinterpret_cast<uint4 *>(out + t * orow + dv0 + (lane % PR) * VE) = make_uint4(0u, 0u, 0u, 0u);
@@ -559,25 +570,25 @@ __global__ void __launch_bounds__(256) k_delta_split(DeltaDims d, const float *x
 
 template <typename T, int DKP, int NW, bool SAVE>
 cudaError_t scan_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
-                     const DeltaLocal &w, float *state, T *o, float *snap, float *u, cudaStream_t st) {
+                     const DeltaLocal &w, float *state, T *o, float *snap, float *r, cudaStream_t st) {
     using L = ScanSmem<T, DKP, NW>;
     auto kern = k_delta_scan<T, DKP, NW, SAVE>;
     set_kernel_smem(kern, L::BYTES);
     const long long slices = (d.Dv + NW * 16 - 1) / (NW * 16);
-    kern<<<(unsigned)((long long)d.B * d.H * slices), NW * 32, L::BYTES, st>>>(d, in, q, k, w, state, o, snap, u);
+    kern<<<(unsigned)((long long)d.B * d.H * slices), NW * 32, L::BYTES, st>>>(d, in, q, k, w, state, o, snap, r);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t scan_any(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
-                     const DeltaLocal &w, float *state, void *o, float *snap, float *u, cudaStream_t st) {
+                     const DeltaLocal &w, float *state, void *o, float *snap, float *r, cudaStream_t st) {
     T *out = static_cast<T *>(o);
     // eight warps (two an SM sub-core) share a chunk's loads once there is a block for every SM;
     // with fewer heads four, so that every warp has a tensor core of its own
     const bool wide = d.Dv > 64 && (long long)d.B * d.H * ((d.Dv + 127) / 128) >= kRefSms;
     auto go = [&](auto dkp, auto nw, auto save) {
         return scan_one<T, decltype(dkp)::value, decltype(nw)::value, decltype(save)::value>(
-            d, in, q, k, w, state, out, snap, u, st);
+            d, in, q, k, w, state, out, snap, r, st);
     };
     auto pick = [&](auto dkp, auto nw) {
         return snap ? go(dkp, nw, std::true_type{}) : go(dkp, nw, std::false_type{});
@@ -588,13 +599,17 @@ cudaError_t scan_any(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q
     return d.Dk <= 64 ? size(std::integral_constant<int, 64>{}) : size(std::integral_constant<int, 128>{});
 }
 
-template <int KP, int DKP, int C, int PP, bool TC = false>
+template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
 cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                       const DeltaLocal &w, cudaStream_t st) {
-    auto kern = k_delta_local<KP, DKP, C, PP, TC>;
+    auto kern = k_delta_local<KP, DKP, C, PP, TC, BACK>;
     constexpr int bytes = LocalSmem<KP, DKP, C, TC>::BYTES;
     set_kernel_smem(kern, bytes);
-    kern<<<(unsigned)delta_chunks(d), 2 * C, bytes, st>>>(d, in, q, k, w);
+    // as many heads of a key head to a block as still leave four blocks for every SM
+    const int group = d.H / d.Hk;
+    int heads = kLocalHeads;
+    while (heads > 1 && (group % heads || delta_chunks(d) / heads < 4 * kRefSms)) --heads;
+    kern<<<(unsigned)(delta_chunks(d) / heads), 2 * C, bytes, st>>>(d, in, q, k, w, heads);
     return cudaGetLastError();
 }
 
@@ -602,20 +617,28 @@ cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &
 
 cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                                const DeltaLocal &w, cudaStream_t st) {
-    if (d.tc && d.pp == 2)
-        return d.Dk <= 64 ? local_one<1, 64, 64, 2, true>(d, in, q, k, w, st)
-                          : local_one<1, 128, 64, 2, true>(d, in, q, k, w, st);
-    if (d.dtype == SDM_BF16 && d.pp == 2)
-        return d.Dk <= 64 ? local_one<1, 64, 64, 2>(d, in, q, k, w, st) : local_one<1, 128, 64, 2>(d, in, q, k, w, st);
-    if (d.dtype == SDM_BF16)
-        return d.Dk <= 64 ? local_one<1, 64, 64, 3>(d, in, q, k, w, st) : local_one<1, 128, 64, 3>(d, in, q, k, w, st);
-    return d.Dk <= 64 ? local_one<3, 64, 32, 3>(d, in, q, k, w, st) : local_one<3, 128, 32, 3>(d, in, q, k, w, st);
+    auto go = [&](auto kp, auto dkp, auto c, auto pp, auto tc, auto back) {
+        return local_one<decltype(kp)::value, decltype(dkp)::value, decltype(c)::value, decltype(pp)::value,
+                         decltype(tc)::value, decltype(back)::value>(d, in, q, k, w, st);
+    };
+    using std::integral_constant;
+    auto size = [&](auto dkp) {
+        const std::true_type yes;
+        const std::false_type no;
+        if (d.dtype == SDM_F32)
+            return d.back ? go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, yes)
+                          : go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, no);
+        if (d.back) return go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, no, yes);
+        return d.tc ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, yes, no)
+                    : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, no, no);
+    };
+    return d.Dk <= 64 ? size(integral_constant<int, 64>{}) : size(integral_constant<int, 128>{});
 }
 
 cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
-                              const DeltaLocal &w, float *state, void *o, float *snap, float *u, cudaStream_t st) {
-    return d.dtype == SDM_BF16 ? scan_any<__nv_bfloat16>(d, in, q, k, w, state, o, snap, u, st)
-                               : scan_any<float>(d, in, q, k, w, state, o, snap, u, st);
+                              const DeltaLocal &w, float *state, void *o, float *snap, float *r, cudaStream_t st) {
+    return d.dtype == SDM_BF16 ? scan_any<__nv_bfloat16>(d, in, q, k, w, state, o, snap, r, st)
+                               : scan_any<float>(d, in, q, k, w, state, o, snap, r, st);
 }
 
 cudaError_t launch_delta_split(const DeltaDims &d, const void *x, const long long *s, int heads, int D,

@@ -16,6 +16,7 @@ struct DeltaDims {
     int B, T, H, Hk, Dk, Dv;
     int C, Nt;                           // chunk length, chunks a sequence
     int pp;                              // planes of P: 2 where it only reaches bfloat16 readings
+    int back;                            // 1: the chunk-local work of a backward
     int dtype;
     int tc;                              // 1: the scans run on tcgen05 (planes of X and P in its layout)
     float scale;
@@ -38,10 +39,10 @@ struct DeltaPlanes {
 };
 
 // Per chunk and head, written by the chunk-local kernel (k_delta_local) for the scans:
-//   x   [3][C][C] bfloat16 planes of (I + diag(beta) A)^-1
-//   p   [pp][C][C] planes of P, the decayed scale q k^T
-//   (for the tcgen05 scan: x holds Y = X diag(beta), p holds Z = P Y)
-//   aux [3][C] float: exp(L_t), exp(L_C - L_t), beta_t
+//   x   [3][C][C] bfloat16 planes of X
+//   p   [pp][C][C] planes of P diag(beta) (for the tcgen05 scan: of P diag(beta) X)
+//   aux [3][C] float: exp(L_t), exp(L_C - L_t) beta_t, beta_t
+// and for a backward: planes of (I + diag(beta) A)^-1 and of P, and exp(L_C - L_t) without beta.
 // The planes' rows have shared memory's layout (delta_pitch, or tcgen05's 128-byte rows with permuted
 // pieces, tc_at), so the scans copy them as they are. Blocks above the diagonal are never written and
 // never used. k_delta_local also clears the workspace's status block.
@@ -63,13 +64,14 @@ cudaError_t launch_delta_split(const DeltaDims &d, const void *x, const long lon
                                int D, __nv_bfloat16 *planes, cudaStream_t st);
 cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                                const DeltaPlanes &k, const DeltaLocal &w, cudaStream_t st);
-// snap [B, H, Nt, Dk, Dv] the state at each chunk's start, u [B, H, Nt, C, Dv]; null unless saving
+// snap [B, H, Nt + 1, Dk, Dv] the state at each chunk's start and, behind the last chunk with tokens, the
+// final one; r [B, H, Nt, C, Dv] what each value lacks; null unless saving
 cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                               const DeltaPlanes &k, const DeltaLocal &w, float *state, void *o,
-                              float *snap, float *u, cudaStream_t st);
+                              float *snap, float *r, cudaStream_t st);
 
 cudaError_t launch_delta_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state,
-                                 void *o, float *snap, float *u, cudaStream_t st);
+                                 void *o, float *snap, float *r, cudaStream_t st);
 
 // Outputs of the backward and what its kernels hand on.
 struct DeltaBack {
@@ -78,7 +80,7 @@ struct DeltaBack {
     float *state_out;                    // [B, H, Dk, Dv]
     void *grad_q, *grad_k, *grad_v;      // contiguous, the inputs' type
     float *grad_decay, *grad_beta;       // [B, T, H]
-    const float *snap, *u;               // saved by the forward
+    const float *snap, *r;               // saved by the forward
     float *ends;                         // [B, H, Nt, Dk, Dv] gradient of each chunk's end state
     float *w;                            // [B, H, Nt, C, Dv] X^T (gradient of u)
     float *dq, *dk;                      // [B, T, H, Dk] before shared heads are summed (H > Hk)

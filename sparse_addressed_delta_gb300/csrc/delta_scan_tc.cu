@@ -1,11 +1,11 @@
 // The gated delta rule's scan over a head's chunks (notation of delta_chunk.cu) on the 5th-generation
 // tensor cores, for bfloat16 inputs. As in the register form everything is transposed: 128 of the
-// state's columns are the 128 lanes of tensor memory. With Y = X diag(beta) and Z = P Y from
-// k_delta_local, a chunk is
-//   R = S^T K^T;  w = -G R;  U = V^T Y^T + w Y^T;  S = G_C S + (e^{L_C - L} U) K
-//   o = scale G (S^T Q^T) + V^T Z^T + w Z^T                 (all transposed; S before the chunk)
+// state's columns are the 128 lanes of tensor memory. With X and Z = P diag(beta) X from k_delta_local,
+// a chunk is
+//   R = S^T K^T;  w = -G R;  U = V^T X^T + w X^T;  S = G_C S + (e^{L_C - L} beta U) K
+//   o = scale G (S^T Q^T) + V^T Z^T + w Z^T      (all transposed; S before the chunk; U is r)
 // S, w and the decayed U are A operands in tensor memory, as bfloat16 planes that their own lanes'
-// threads store; V is an A operand in shared memory; K, Q, Y and Z are B operands there, K in both its
+// threads store; V is an A operand in shared memory; K, Q, X and Z are B operands there, K in both its
 // majors (K S runs over Dk, the state's update over the tokens). Three planes (24 bits) go into R, U
 // and the update, two into the bfloat16 readings. A thread keeps its part of its lane of S in registers
 // in float32 for the whole sequence; the tensor core only ever sums one chunk's update.
@@ -32,7 +32,7 @@ constexpr int kTcWarps = 16, kTcThreads = 32 * (kTcWarps + 3);
 template <int DKP>
 struct TcScan {
     static constexpr int TILE = kTcC * 128;                        // 64 columns of a token tile
-    static constexpr int K = 0, Q = K + DKP / 64 * TILE, Y = Q + DKP / 64 * TILE, Z = Y + 3 * TILE;
+    static constexpr int K = 0, Q = K + DKP / 64 * TILE, X = Q + DKP / 64 * TILE, Z = X + 3 * TILE;
     static constexpr int V = Z + 2 * TILE, STAGE = V + 2 * TILE;
     static constexpr int O = 2 * STAGE, AUX = O + 2 * 2 * TILE,   // readings: two buffers like V's
                           BARS = AUX + 2 * 512, BYTES = BARS + 256 + 1024;
@@ -55,7 +55,7 @@ template <int DKP, bool SAVE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_delta_scan_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, DeltaDims d,
-                    DeltaIn in, DeltaLocal w, float *state, __nv_bfloat16 *o, float *snap, float *usave) {
+                    DeltaIn in, DeltaLocal w, float *state, __nv_bfloat16 *o, float *snap, float *rsave) {
     using L = TcScan<DKP>;
     constexpr int C = kTcC, HD = DKP / 4;                          // columns of S a thread
     extern __shared__ unsigned char raw[];
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int orow = 16 * part + 8 * (lane >> 4) + (lane & 7), ocol = (lane0 >> 3) + ((lane >> 3) & 1);
         for (int n = 0; n < nch; ++n) {
             const unsigned par = n & 1;
-            float *keep = snap + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv;
+            float *keep = snap + ((bh * (d.Nt + 1) + n) * (long long)d.Dk) * d.Dv;
             if (!tc_warp_wait(bar + B_FULL + par, (n >> 1) & 1, dead, d.spin)) break;
             const float *aux = reinterpret_cast<const float *>(smem + L::AUX + 512 * par);
             const float *from = aux + 16 * part, *to = aux + C + 16 * part;
@@ -155,10 +155,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!tc_warp_wait(bar + B_UACC + half, par, dead, d.spin)) break;
             tc_fence_after();
             tc_load16(at + L::U + 16 * part, x);
-            float *udst = usave + ((bh * d.Nt + n) * (long long)C + 16 * part) * d.Dv + dv;
+            float *rdst = rsave + ((bh * d.Nt + n) * (long long)C + 16 * part) * d.Dv + dv;
             if (SAVE && mine) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) udst[(size_t)i * d.Dv] = x[i];
+                for (int i = 0; i < 16; ++i) rdst[(size_t)i * d.Dv] = x[i];
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] *= to[i];
@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (lane == 0) mbar_arrive(bar + B_EMPTY + par);
         }
         if (nch > 0 && !*dead) keep_state(state + bh * d.Dk * (long long)d.Dv, 0, HD);
+        if (SAVE) keep_state(snap + ((bh * (d.Nt + 1) + nch) * (long long)d.Dk) * d.Dv, 0, HD);
     } else if (warp == kTcWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const unsigned par = n & 1;
             const uint32_t st = base + par * L::STAGE;
             // a descriptor's address counts 16 bytes
-            const uint64_t kd = tc_k_major(st + L::K), qd = tc_k_major(st + L::Q), yd = tc_k_major(st + L::Y),
+            const uint64_t kd = tc_k_major(st + L::K), qd = tc_k_major(st + L::Q), xd = tc_k_major(st + L::X),
                            zd = tc_k_major(st + L::Z), kn = tc_n_major(st + L::K, L::TILE), vm = tc_n_major(st + L::V, L::TILE);
             // lower triangular B: K step ks reaches the columns from 16 ks on
             auto tri = [&](uint32_t dst, uint32_t a, uint64_t tile, int ks) {
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_commit_to(one, bar + B_R + hf);
             }
 #pragma unroll
-            for (int p = 2; p >= 0; --p) tri_v(L::U, yd + p * L::TILE / 16, p == 2);
+            for (int p = 2; p >= 0; --p) tri_v(L::U, xd + p * L::TILE / 16, p == 2);
 #pragma unroll
             for (int p = 1; p >= 0; --p) tri_v(L::OA, zd + p * L::TILE / 16, p == 1);
             bool ok = true;
@@ -269,8 +270,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int a = 2; a >= 0; --a)
 #pragma unroll
                     for (int p = 2 - a; p >= 0; --p) {
-                        tri(L::U, L::UP + a * (C / 2), yd + p * L::TILE / 16, 2 * hf);
-                        tri(L::U, L::UP + a * (C / 2), yd + p * L::TILE / 16, 2 * hf + 1);
+                        tri(L::U, L::UP + a * (C / 2), xd + p * L::TILE / 16, 2 * hf);
+                        tri(L::U, L::UP + a * (C / 2), xd + p * L::TILE / 16, 2 * hf + 1);
                     }
                 tc_commit_to(one, bar + B_UACC + hf);
             }
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, hk, t0, b, full);
                 }
                 for (int c = 0; c < 2; ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, h, t0, b, full);
-                bulk_g2s(st + L::Y, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
+                bulk_g2s(st + L::X, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
                 bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, full);
                 bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * 3 * C, 2 * C * 4, full);
             }
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 template <int DKP, bool SAVE>
 cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o, float *snap,
-                    float *u, cudaStream_t st) {
+                    float *r, cudaStream_t st) {
     const long long os[3] = {(long long)d.T * d.H * d.Dv, (long long)d.H * d.Dv, d.Dv};
     CUtensorMap mq, mk, mv, mo;
     cudaError_t e = tc_tensor_map(&mq, in.q, d.qs, d.B, d.T, d.Hk, d.Dk);
@@ -393,7 +394,7 @@ cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, 
     auto kern = k_delta_scan_tc<DKP, SAVE>;
     set_kernel_smem(kern, TcScan<DKP>::BYTES);
     kern<<<(unsigned)((long long)d.B * d.H * ((d.Dv + 127) / 128)), kTcThreads, TcScan<DKP>::BYTES, st>>>(
-        mq, mk, mv, mo, d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, u);
+        mq, mk, mv, mo, d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, r);
     return cudaGetLastError();
 }
 
@@ -418,12 +419,12 @@ cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *s, int
 }
 
 cudaError_t launch_delta_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o,
-                                 float *snap, float *u, cudaStream_t st) {
+                                 float *snap, float *r, cudaStream_t st) {
     if (d.Dk <= 64)
-        return snap ? scan_tc<64, true>(d, in, w, state, o, snap, u, st)
-                    : scan_tc<64, false>(d, in, w, state, o, snap, u, st);
-    return snap ? scan_tc<128, true>(d, in, w, state, o, snap, u, st)
-                : scan_tc<128, false>(d, in, w, state, o, snap, u, st);
+        return snap ? scan_tc<64, true>(d, in, w, state, o, snap, r, st)
+                    : scan_tc<64, false>(d, in, w, state, o, snap, r, st);
+    return snap ? scan_tc<128, true>(d, in, w, state, o, snap, r, st)
+                : scan_tc<128, false>(d, in, w, state, o, snap, r, st);
 }
 
 }  // namespace sdm
