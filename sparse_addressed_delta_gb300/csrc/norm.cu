@@ -9,10 +9,12 @@
 // Bound by memory: a row is read once, held in registers and written once. A row belongs to TPR
 // threads (a part of a warp up to 32, else the whole block), each with E elements as whole vectors
 // (16 bytes when the row length, its stride and the pointers allow it, else 4 or one element).
-// Blocks stay resident and walk over the rows with the weights in registers, the next row's loads
-// in flight while the current one is reduced. The backward's column sums stay in the same threads
-// over all the rows of a block (in shared memory above 8192 columns), go to one partial per block,
-// and a second kernel adds the partials in block order: no atomics, so results are reproducible.
+// Blocks stay resident and walk over the rows with the weights in registers. Every thread copies its
+// own pieces of the next kNormStages - 1 rows into shared memory (cp.async; nobody else reads them, so
+// there is no barrier), which keeps about 100 KB an SM in flight. The backward's column sums stay in
+// the same threads over all the rows of a block (in shared memory above 8192 columns), go to one
+// partial per block, and a second kernel adds the partials in block order: no atomics, so results are
+// reproducible.
 #include "sdm_internal.cuh"
 
 namespace sdm {
@@ -21,7 +23,10 @@ namespace {
 constexpr int kNormBlock = 128;        // threads of a block whose rows belong to parts of warps
 constexpr int kNormMaxCols = 16384;
 constexpr int kNormRegCols = 8192;     // backward: column sums in registers up to this width
-constexpr int kNormColThreads = 32, kNormColSlices = 8;
+constexpr int kNormColThreads = 32, kNormColSlices = 32;
+template <typename T>
+constexpr int kNormStages = sizeof(T) == 2 ? 4 : 3;   // rows in the ring, the one in use among them
+constexpr int kNormRowsBlock = 8;      // backward: at least this many rows a block, for fewer partials
 
 template <int BYTES> struct VecOf;
 template <> struct VecOf<16> { using type = uint4; };
@@ -38,15 +43,56 @@ __device__ __forceinline__ void unpack(const Vec<T, VEC> &r, float *o) {
     for (int j = 0; j < VEC; ++j) o[j] = to_f32(e[j]);
 }
 
-// the thread's NV vectors of one row (zero past the row's end, or when the row is not live)
+// A thread's own pieces of the rows ahead: `stage` holds NV vectors of each of ROWS tensors (and 8 bytes
+// of statistics) at [vector][thread].
+template <typename T, int VEC, int NV, int ROWS, bool STATS>
+struct RowRing {
+    static constexpr int VB = VEC * (int)sizeof(T), ROW = NV * VB, THREAD = ROWS * ROW + (STATS ? 8 : 0);
+    unsigned char *base;               // of the block
+    int t, tpr, n;                     // thread of the row, threads of the row, columns
+
+    __device__ __forceinline__ unsigned char *at(int stage, int vector) const {
+        return base + ((size_t)stage * THREAD) * blockDim.x + ((size_t)vector * blockDim.x + threadIdx.x) * VB;
+    }
+    __device__ __forceinline__ unsigned char *stats_at(int stage) const {
+        return base + ((size_t)stage * THREAD + ROWS * ROW) * blockDim.x + 8 * threadIdx.x;
+    }
+    // row `which` of `stage`; 0 past the row's end, or when the row is not live
+    __device__ __forceinline__ void fetch(int stage, int which, const T *row, bool live) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            const bool in = live && c < n;
+            unsigned char *dst = at(stage, which * NV + i);
+            if constexpr (VB == 16) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(row + (in ? c : 0)), "r"(in ? 16 : 0) : "memory");
+            } else if constexpr (VB == 4) {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(row + (in ? c : 0)), "r"(in ? 4 : 0) : "memory");
+            } else {
+                *reinterpret_cast<T *>(dst) = in ? row[c] : from_f32<T>(0.f);
+            }
+        }
+    }
+    __device__ __forceinline__ void fetch_stats(int stage, const float2 *p, bool live) const {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(stats_at(stage))), "l"(p), "r"(live ? 8 : 0) : "memory");
+    }
+    __device__ __forceinline__ void read(int stage, int which, float *o) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Vec<T, VEC> r = *reinterpret_cast<const Vec<T, VEC> *>(at(stage, which * NV + i));
+            unpack<T, VEC>(r, o + i * VEC);
+        }
+    }
+};
+
+// the thread's pieces of a row (0 past its end), straight to registers
 template <typename T, int VEC, int NV>
-__device__ __forceinline__ void load_row(const T *row, bool live, int t, int tpr, int n,
-                                         Vec<T, VEC> (&r)[NV]) {
+__device__ __forceinline__ void load_row(const T *row, int t, int tpr, int n, float *o) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * VEC;
-        r[i] = Vec<T, VEC>{};
-        if (live && c < n) r[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(row + c));
+        const Vec<T, VEC> r = c < n ? __ldg(reinterpret_cast<const Vec<T, VEC> *>(row + c)) : Vec<T, VEC>{};
+        unpack<T, VEC>(r, o + i * VEC);
     }
 }
 
@@ -79,15 +125,19 @@ __device__ __forceinline__ void load_cols(const void *p, bool f32, float fill, i
         }
 }
 
+template <int M>
+__device__ __forceinline__ void warp_sum(float (&v)[M], int width) {
+    for (int o = width >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+}
+
 // Sums of M values over the threads of one row, returned to all of them. BLOCK: over the block,
 // warps added in warp order (`red` holds 2 * M * 32 floats, its halves used in turn so that one
 // barrier a call is enough).
 template <bool BLOCK, int M>
 __device__ __forceinline__ void row_sum(float (&v)[M], int tpr, float *red, int &turn) {
-    const int width = BLOCK ? 32 : tpr;
-    for (int o = width >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+    warp_sum<M>(v, BLOCK ? 32 : tpr);
     if constexpr (BLOCK) {
         float *r = red + turn * M * 32;
         turn ^= 1;
@@ -109,8 +159,11 @@ template <typename T, int VEC, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
     k_norm(const T *x, long long xs, long long rows, int n, int tpr, const void *w, const void *b,
            bool wf32, float eps, T *y, float2 *stats) {
-    constexpr int E = VEC * NV;
-    __shared__ float red[2 * 32];
+    constexpr int E = VEC * NV, ST = kNormStages<T>;
+    extern __shared__ __align__(16) unsigned char ring_smem[];
+    __shared__ float2 red[2 * 32];
+    __shared__ float counts[32];           // BLOCK: columns of each warp
+    float warp_cols = 0.f;
     int turn = 0;
     const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr;
     const int rpb = BLOCK ? 1 : kNormBlock / tpr;
@@ -118,32 +171,73 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
     float wv[E], bv[E];
     load_cols<T, VEC, NV>(w, wf32, 1.f, t, tpr, n, wv);
     load_cols<T, VEC, NV>(b, wf32, 0.f, t, tpr, n, bv);
-    Vec<T, VEC> next[NV];
-    long long base = (long long)blockIdx.x * rpb;
-    load_row<T, VEC, NV>(x + (base + sub) * xs, base + sub < rows, t, tpr, n, next);
-    for (; base < rows; base += step) {
-        const long long row = base + sub;
-        float v[E];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) unpack<T, VEC>(next[i], v + i * VEC);
-        load_row<T, VEC, NV>(x + (row + step) * xs, row + step < rows, t, tpr, n, next);
-        float s[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < E; ++j) s[0] += v[j];
-        row_sum<BLOCK, 1>(s, tpr, red, turn);
-        const float mean = s[0] / (float)n;
-        s[0] = 0.f;
+    if constexpr (BLOCK) {
+        float c[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if ((i * tpr + t) * VEC < n)
+            if ((i * tpr + t) * VEC < n) c[0] += VEC;
+        warp_sum<1>(c, 32);
+        warp_cols = c[0];                  // at least one: the block has no warp past the row's end
+        if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = warp_cols;
+        __syncthreads();
+    }
+    const RowRing<T, VEC, NV, 1, false> ring{ring_smem, t, tpr, n};
+    long long base = (long long)blockIdx.x * rpb;
+    auto fetch = [&](int stage, long long row) {
+        ring.fetch(stage, 0, x + (row < rows ? row : 0) * xs, row < rows);
+        cp_async_commit();
+    };
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float d = v[i * VEC + j] - mean;
-                    v[i * VEC + j] = d;
-                    s[0] = fmaf(d, d, s[0]);
-                }
-        row_sum<BLOCK, 1>(s, tpr, red, turn);
-        const float rstd = 1.f / sqrtf(s[0] / (float)n + eps);
+    for (int i = 0; i < ST - 1; ++i) fetch(i, base + sub + i * step);
+    for (int stage = 0; base < rows; base += step, stage = (stage + 1) % ST) {
+        const long long row = base + sub;
+        fetch((stage + ST - 1) % ST, row + (ST - 1) * step);
+        cp_async_wait<ST - 1>();
+        float v[E];
+        ring.read(stage, 0, v);
+        float s[1] = {0.f}, mean, m2;
+#pragma unroll
+        for (int j = 0; j < E; ++j) s[0] += v[j];
+        auto around = [&](float c) {                       // this thread's squares around c
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if ((i * tpr + t) * VEC < n)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const float d = v[i * VEC + j] - c;
+                        q = fmaf(d, d, q);
+                    }
+            return q;
+        };
+        warp_sum<1>(s, BLOCK ? 32 : tpr);
+        if constexpr (BLOCK) {
+            // each warp's sum and squares around its own mean; together, the squares around the row's
+            // mean are those and count (mean_w - mean)^2: one barrier a row
+            const float sw = s[0];
+            float q[1] = {around(sw / warp_cols)};
+            warp_sum<1>(q, 32);
+            float2 *r = red + 32 * turn;
+            turn ^= 1;
+            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(sw, q[0]);
+            __syncthreads();
+            float sum = 0.f;
+            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += r[w].x;
+            mean = sum / (float)n;
+            m2 = 0.f;
+            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+                const float c = counts[w], d = r[w].x / c - mean;
+                m2 += fmaf(c * d, d, r[w].y);
+            }
+        } else {
+            mean = s[0] / (float)n;
+            float q[1] = {around(mean)};
+            warp_sum<1>(q, tpr);
+            m2 = q[0];
+        }
+        const float rstd = 1.f / sqrtf(m2 / (float)n + eps);
+#pragma unroll
+        for (int j = 0; j < E; ++j) v[j] -= mean;
         if (row < rows) {
 #pragma unroll
             for (int j = 0; j < E; ++j) v[j] = fmaf(v[j] * rstd, wv[j], bv[j]);
@@ -158,8 +252,11 @@ template <typename T, int VEC, int NV, bool BLOCK, bool WIDE>
 __global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
     k_norm_bwd(const T *dy, long long ds, const T *x, long long xs, long long rows, int n, int tpr,
                const void *w, bool wf32, const float2 *stats, T *dx, float *part) {
-    constexpr int E = VEC * NV;
-    extern __shared__ float cols[];          // WIDE: the column sums [2][n]; else see the end
+    constexpr int E = VEC * NV, ST = kNormStages<T>;
+    extern __shared__ __align__(16) unsigned char ring_smem[];
+    using Ring = RowRing<T, VEC, NV, 2, true>;
+    // WIDE: no ring, the column sums [2][n]; else they take the ring's place at the end
+    float *cols = reinterpret_cast<float *>(ring_smem);
     __shared__ float red[2 * 2 * 32];
     int turn = 0;
     const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr;
@@ -174,26 +271,35 @@ __global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
 #pragma unroll
         for (int j = 0; j < E; ++j) aw[j] = ab[j] = 0.f;
     }
-    Vec<T, VEC> nx[NV], ny[NV];
-    float2 ns = make_float2(0.f, 0.f);
+    const Ring ring{ring_smem, t, tpr, n};
     long long base = (long long)blockIdx.x * rpb;
-    auto fetch = [&](long long row) {
+    auto fetch = [&](int stage, long long row) {
         const bool live = row < rows;
-        load_row<T, VEC, NV>(x + row * xs, live, t, tpr, n, nx);
-        load_row<T, VEC, NV>(dy + row * ds, live, t, tpr, n, ny);
-        ns = live ? __ldg(stats + row) : make_float2(0.f, 0.f);
+        const long long at = live ? row : 0;
+        ring.fetch(stage, 0, x + at * xs, live);
+        ring.fetch(stage, 1, dy + at * ds, live);
+        ring.fetch_stats(stage, stats + at, live);
+        cp_async_commit();
     };
-    fetch(base + sub);
-    for (; base < rows; base += step) {
-        const long long row = base + sub;
-        const float mean = ns.x, rstd = ns.y;
-        float h[E], g[E], s[2] = {0.f, 0.f};
+    if constexpr (!WIDE)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            unpack<T, VEC>(nx[i], h + i * VEC);
-            unpack<T, VEC>(ny[i], g + i * VEC);
+        for (int i = 0; i < ST - 1; ++i) fetch(i, base + sub + i * step);
+    for (int stage = 0; base < rows; base += step, stage = (stage + 1) % ST) {
+        const long long row = base + sub;
+        float2 ns;
+        float h[E], g[E], s[2] = {0.f, 0.f};
+        if constexpr (WIDE) {                              // a row a block: it is live
+            ns = __ldg(stats + row);
+            load_row<T, VEC, NV>(x + row * xs, t, tpr, n, h);
+            load_row<T, VEC, NV>(dy + row * ds, t, tpr, n, g);
+        } else {
+            fetch((stage + ST - 1) % ST, row + (ST - 1) * step);
+            cp_async_wait<ST - 1>();
+            ns = *reinterpret_cast<const float2 *>(ring.stats_at(stage));
+            ring.read(stage, 0, h);
+            ring.read(stage, 1, g);
         }
-        fetch(row + step);
+        const float mean = ns.x, rstd = ns.y;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c0 = (i * tpr + t) * VEC;
@@ -227,9 +333,10 @@ __global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
         }
     }
     if (!part) return;
+    cp_async_wait<0>();
+    __syncthreads();
     float *out = part + (size_t)blockIdx.x * 2 * n;
     if constexpr (WIDE) {
-        __syncthreads();
         for (int c = threadIdx.x; c < 2 * n; c += blockDim.x) out[c] = cols[c];
     } else {
         // the block's row groups, added in their order: cols [2][groups][tpr * E]
@@ -272,7 +379,8 @@ __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
     const int c = blockIdx.x * kNormColThreads + tx;     // over [2][n]
     float s = 0.f;
     if (c < 2 * n)
-        for (int p = ty; p < parts; p += kNormColSlices) s += part[(size_t)p * 2 * n + c];
+#pragma unroll 4
+        for (int p = ty; p < parts; p += kNormColSlices) s += __ldg(part + (size_t)p * 2 * n + c);
     sh[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && c < 2 * n) {
@@ -293,8 +401,8 @@ struct NormGeom {
     int threads, rpb;
 };
 
-// 16 elements a thread keep enough loads in flight with the weights and sums in registers; the
-// forward (no sums) takes 32 once a block of 128 threads would not cover the row with 16.
+// 16 elements a thread leave room for the weights and sums in registers; the forward (no sums) takes 32
+// once 128 threads do not cover the row with 16: fewer threads to a barrier.
 NormGeom norm_geom(int n, int vec, bool backward) {
     NormGeom g;
     g.vec = vec;
@@ -315,11 +423,13 @@ NormGeom norm_geom(int n, int vec, bool backward) {
     return g;
 }
 
-// blocks that fill the card once, at most one per row group
-int norm_blocks(const NormGeom &g, long long rows, bool backward) {
-    const int per_sm = g.threads >= 1024 ? 1 : (backward ? 768 : 1024) / g.threads;
-    const long long most = (long long)kRefSms * (per_sm < 1 ? 1 : per_sm);
-    const long long need = (rows + g.rpb - 1) / g.rpb;
+// blocks of a backward: at most one per row group, and per kNormRowsBlock rows as long as every SM has
+// one; 512 threads an SM (by their registers)
+int norm_back_blocks(const NormGeom &g, long long rows) {
+    const int per_sm = g.threads >= 512 ? 1 : 512 / g.threads;
+    const long long few = rows / kNormRowsBlock > kRefSms ? rows / kNormRowsBlock : kRefSms;
+    const long long need = (rows + g.rpb - 1) / g.rpb, fill = (long long)kRefSms * per_sm;
+    const long long most = fill < few ? fill : few;
     return (int)(need < most ? need : most);
 }
 
@@ -355,13 +465,20 @@ int norm_status(cudaError_t e) {
 template <typename T, int VEC, int E>
 void norm_launch(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
                  const void *b, bool wf32, float eps, T *y, float2 *stats, cudaStream_t st) {
-    const int grid = norm_blocks(g, rows, false);
-    if (g.block)
-        k_norm<T, VEC, E / VEC, true><<<grid, g.threads, 0, st>>>(x, xs, rows, n, g.tpr, w, b, wf32,
-                                                                 eps, y, stats);
-    else
-        k_norm<T, VEC, E / VEC, false><<<grid, g.threads, 0, st>>>(x, xs, rows, n, g.tpr, w, b,
-                                                                  wf32, eps, y, stats);
+    const size_t smem = (size_t)kNormStages<T> * E * sizeof(T) * g.threads;
+    const long long need = (rows + g.rpb - 1) / g.rpb;
+    auto go = [&](auto kern) {
+        set_kernel_smem(kern, smem);
+        // as many blocks as fit the card at once: they walk over the rows, and a second wave of blocks
+        // would leave part of it idle (32768 x 4096 bfloat16: 122 us with one and a half waves)
+        int per_sm = 1;
+        if (need > kRefSms) cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, g.threads, smem);
+        const long long most = (long long)kRefSms * (per_sm > 1 ? per_sm : 1);
+        const unsigned grid = (unsigned)(need < most ? need : most);
+        kern<<<grid, g.threads, smem, st>>>(x, xs, rows, n, g.tpr, w, b, wf32, eps, y, stats);
+    };
+    if (g.block) go(k_norm<T, VEC, E / VEC, true>);
+    else go(k_norm<T, VEC, E / VEC, false>);
 }
 
 template <typename T>
@@ -384,19 +501,15 @@ void norm_bwd_launch(const NormGeom &g, int grid, const T *dy, long long ds, con
                      long long xs, long long rows, int n, const void *w, bool wf32,
                      const float2 *stats, T *dx, float *part, cudaStream_t st) {
     constexpr int NV = 16 / VEC;
-    if (n > kNormRegCols) {
-        auto k = k_norm_bwd<T, VEC, NV, true, true>;
-        const size_t smem = (size_t)2 * n * 4;
-        set_kernel_smem(k, smem);
-        k<<<grid, g.threads, smem, st>>>(dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
-    } else if (g.block) {
-        k_norm_bwd<T, VEC, NV, true, false><<<grid, g.threads, 0, st>>>(
-            dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
-    } else {
-        const size_t smem = (size_t)2 * kNormBlock * 16 * 4;
-        k_norm_bwd<T, VEC, NV, false, false><<<grid, g.threads, smem, st>>>(
-            dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
-    }
+    const size_t ring = (size_t)kNormStages<T> * RowRing<T, VEC, NV, 2, true>::THREAD * g.threads;
+    const size_t sums = (size_t)2 * (n > kNormRegCols ? n : kNormBlock * 16) * 4;
+    auto go = [&](auto kern, size_t smem) {
+        set_kernel_smem(kern, smem);
+        kern<<<grid, g.threads, smem, st>>>(dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
+    };
+    if (n > kNormRegCols) go(k_norm_bwd<T, VEC, NV, true, true>, sums);
+    else if (g.block) go(k_norm_bwd<T, VEC, NV, true, false>, ring);
+    else go(k_norm_bwd<T, VEC, NV, false, false>, ring > sums ? ring : sums);
 }
 
 template <typename T>
@@ -446,7 +559,7 @@ size_t sdm_layer_norm_workspace_bytes(long long rows, int n) {
         return 0;
     }
     const NormGeom g = norm_geom(n, 1, true);
-    const size_t blocks = rows ? (size_t)norm_blocks(g, rows, true) : 1;
+    const size_t blocks = rows ? (size_t)norm_back_blocks(g, rows) : 1;
     return (blocks * 2 * n * 4 + kAlign - 1) / kAlign * kAlign;
 }
 
@@ -470,7 +583,7 @@ int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const NormGeom g = norm_geom(
         n, norm_vec(dtype == SDM_BF16 ? 2 : 4, n, x_stride, grad_stride, x, grad, grad_x), true);
-    const int grid = rows ? norm_blocks(g, rows, true) : 0;
+    const int grid = rows ? norm_back_blocks(g, rows) : 0;
     float *part = sums ? static_cast<float *>(workspace) : nullptr;
     auto s2 = reinterpret_cast<const float2 *>(stats);
     const bool wf32 = weight_dtype == SDM_F32;
