@@ -221,7 +221,6 @@ size_t sdm_gated_delta_backward_workspace_bytes(const sdm_delta_shape *shape) {
     if (delta_check(shape, d) != SDM_OK) return 0;
     d.pp = 3;
     d.back = 1;
-    d.tc = 0;
     return delta_layout(d, true).bytes + kAlign;
 }
 
@@ -236,7 +235,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     if (rc != SDM_OK) return rc;
     d.pp = 3;                            // P reaches float32 gradients
     d.back = 1;
-    d.tc = 0;
+    d.tc = d.tc && tc_tensor_fits(d.os, d.B, d.T, d.H);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d.B == 0) return SDM_OK;
     if (!grad_state) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
@@ -275,7 +274,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     o.w = reinterpret_cast<float *>(ws + l.w);
     o.dq = reinterpret_cast<float *>(ws + l.dq);
     o.dk = reinterpret_cast<float *>(ws + l.dk);
-    if (e == cudaSuccess) e = launch_delta_back_scan(d, in, qp, kp, w, o, st);
+    if (e == cudaSuccess) e = d.tc ? launch_delta_back_scan_tc(d, in, w, o, st) : launch_delta_back_scan(d, in, qp, kp, w, o, st);
     if (e == cudaSuccess) e = launch_delta_back_local(d, in, qp, kp, w, o, st);
     return delta_status(e);
 }

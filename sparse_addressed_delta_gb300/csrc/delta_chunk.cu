@@ -22,12 +22,12 @@ namespace {
 
 constexpr int kLocalHeads = 4;          // value heads of one key head a block takes at most
 
-template <int KP, int DKP, int C, bool TC>
+template <int KP, int DKP, int C, int ZP>
 struct LocalSmem {
     static constexpr int KPITCH = delta_pitch(DKP * 2), TILE = C * KPITCH, NP = C + 4, XP = delta_pitch(C * 2);
-    // K and Q make room for the inverse (and two of its planes) once their products are taken
+    // K and Q make room for the inverse (and ZP of its planes) once their products are taken
     static constexpr int Q = KP * TILE, X = 0, XPL = C * NP * 4, FIRST = 2 * KP * TILE;
-    static constexpr int SECOND = XPL + (TC ? 2 * C * XP : 0);
+    static constexpr int SECOND = XPL + ZP * C * XP;
     static constexpr int N = FIRST > SECOND ? FIRST : SECOND, G = N + C * NP * 4;
     static constexpr int BYTES = G + kLocalHeads * 3 * C * 4;
 };
@@ -75,13 +75,14 @@ __device__ __forceinline__ void merge_columns(const float *N, float *X, int c0, 
 // stay in registers. For each head: the decays, then the inverse of I + N, N = A diag(beta) (BACK:
 // diag(beta) A): 16 x 16 diagonal blocks by substitution, a warp each, a lane a column, then merged
 // in pairs, -X_2 N X_1, with the columns spread over the warps.
-// TC: for the tcgen05 scan, Z = P X in the place of P (from two terms of each, as exact as the bfloat16
-// readings need).
+// TC: for the tcgen05 scans, Z = P X in the place of P (a forward's from two terms of each, as exact as
+// the bfloat16 readings need).
 // What bounds it: issue. At C = 64 the merges take about 40 % of its instructions, the planes 25 %.
 template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
-__global__ void __launch_bounds__(2 * C, C == 64 ? 4 : 1)
+__global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
     k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, int heads) {
-    using L = LocalSmem<KP, DKP, C, TC>;
+    constexpr int ZP = TC ? (BACK ? 3 : 2) : 0;                    // terms of P and X in Z = P X
+    using L = LocalSmem<KP, DKP, C, ZP>;
     constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = delta_pitch(C * 2), KPI = L::KPITCH;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(2 * C, C == 64 ? 4 : 1)
             for (int p = 0; p < 3; ++p) {
                 const uint4 y = make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
                 *reinterpret_cast<uint4 *>(ximg + p * PLANE + plane_at(r, c)) = y;
-                if (TC && p < 2) *reinterpret_cast<uint4 *>(smem + L::XPL + p * C * XP + delta_at<XP>(r, c)) = y;
+                if (p < ZP) *reinterpret_cast<uint4 *>(smem + L::XPL + p * C * XP + delta_at<XP>(r, c)) = y;
             }
         }
         if constexpr (TC) {
@@ -261,19 +262,20 @@ __global__ void __launch_bounds__(2 * C, C == 64 ? 4 : 1)
 #pragma unroll
             for (int ks = 0; ks < NB; ++ks) {                      // the accumulators of P are its A operand
                 if (ks > warp) break;
-                unsigned a[2][4];
-                split_frag<2>(pv, ks, a);
+                unsigned a[ZP][4];
+                split_frag<ZP>(pv, ks, a);
 #pragma unroll
                 for (int jj = 0; jj <= ks; ++jj) {
-                    unsigned bb[2][4];
+                    unsigned bb[ZP][4];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
+                    for (int p = 0; p < ZP; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        mma_bf16(z[2 * jj + e], a[1], bb[0][2 * e], bb[0][2 * e + 1]);
-                        mma_bf16(z[2 * jj + e], a[0], bb[1][2 * e], bb[1][2 * e + 1]);
-                        mma_bf16(z[2 * jj + e], a[0], bb[0][2 * e], bb[0][2 * e + 1]);
-                    }
+                    for (int x = ZP - 1; x >= 0; --x)
+#pragma unroll
+                        for (int y = ZP - 1; y >= 0; --y)
+                            if (plane_pair(x, y, ZP))
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) mma_bf16(z[2 * jj + e], a[x], bb[y][2 * e], bb[y][2 * e + 1]);
                 }
             }
 #pragma unroll
@@ -603,7 +605,7 @@ template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
 cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                       const DeltaLocal &w, cudaStream_t st) {
     auto kern = k_delta_local<KP, DKP, C, PP, TC, BACK>;
-    constexpr int bytes = LocalSmem<KP, DKP, C, TC>::BYTES;
+    constexpr int bytes = LocalSmem<KP, DKP, C, TC ? (BACK ? 3 : 2) : 0>::BYTES;
     set_kernel_smem(kern, bytes);
     // as many heads of a key head to a block as still leave four blocks for every SM
     const int group = d.H / d.Hk;
@@ -628,7 +630,9 @@ cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const Delt
         if (d.dtype == SDM_F32)
             return d.back ? go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, yes)
                           : go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, no);
-        if (d.back) return go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, no, yes);
+        if (d.back)
+            return d.tc ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, yes, yes)
+                        : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, no, yes);
         return d.tc ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, yes, no)
                     : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, no, no);
     };

@@ -42,7 +42,8 @@ struct DeltaPlanes {
 //   x   [3][C][C] bfloat16 planes of X
 //   p   [pp][C][C] planes of P diag(beta) (for the tcgen05 scan: of P diag(beta) X)
 //   aux [3][C] float: exp(L_t), exp(L_C - L_t) beta_t, beta_t
-// and for a backward: planes of (I + diag(beta) A)^-1 and of P, and exp(L_C - L_t) without beta.
+// and for a backward: planes of (I + diag(beta) A)^-1 =: X and of P (for tcgen05: of P X), and exp(L_C -
+// L_t) without beta.
 // The planes' rows have shared memory's layout (delta_pitch, or tcgen05's 128-byte rows with permuted
 // pieces, tc_at), so the scans copy them as they are. Blocks above the diagonal are never written and
 // never used. k_delta_local also clears the workspace's status block.
@@ -89,6 +90,8 @@ struct DeltaBack {
 cudaError_t launch_delta_back_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                                    const DeltaPlanes &k, const DeltaLocal &w, const DeltaBack &o,
                                    cudaStream_t st);
+cudaError_t launch_delta_back_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, const DeltaBack &o,
+                                      cudaStream_t st);
 cudaError_t launch_delta_back_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                                     const DeltaPlanes &k, const DeltaLocal &w, const DeltaBack &o,
                                     cudaStream_t st);

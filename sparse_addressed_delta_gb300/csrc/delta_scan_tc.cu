@@ -219,23 +219,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             auto tri = [&](uint32_t dst, uint32_t a, uint64_t tile, int ks) {
                 tc_mma_ts(one, tu + dst + 16 * ks, tu + a + 8 * ks, tile + (16 * ks * 128 + 32 * ks) / 16, tc_idesc<false>(C - 16 * ks), true);
             };
-            auto tri_v = [&](uint32_t dst, uint64_t tile, bool first) {
-#pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks)
-                    tc_mma_ss(one, tu + dst + 16 * ks, vm + 2048 * ks / 16, tile + (16 * ks * 128 + 32 * ks) / 16,
-                              tc_idesc<false, true>(C - 16 * ks), !first || ks > 0);
+            auto tri_v = [&](uint32_t dst, uint64_t tile, int ks, bool add) {
+                tc_mma_ss(one, tu + dst + 16 * ks, vm + 2048 * ks / 16, tile + (16 * ks * 128 + 32 * ks) / 16,
+                          tc_idesc<false, true>(C - 16 * ks), add);
             };
             // 16 tokens' or more rows of a [tokens][DKP] tile against the planes of S
             auto rows = [&](uint32_t dst, uint64_t tile, int t0, int tokens, int p, int ks, bool add) {
                 tc_mma_ts(one, tu + dst + t0, tu + L::SP + p * (DKP / 2) + 8 * ks, tile + (t0 * 128 + (ks >> 2) * L::TILE + 32 * (ks & 3)) / 16,
                           tc_idesc<false>(tokens), add);
             };
-            auto update = [&](int ks, int hd) {                    // half hd of Dk, or (Dk 64) all of it at once
-                constexpr int N = DKP == 128 ? 64 : DKP;
-#pragma unroll
-                for (int p = 2; p >= 0; --p)
-                    tc_mma_ts(one, tu + L::UP + 64 * hd, tu + (p < 2 ? L::U + 16 * ks + 8 * p : L::LO + 8 * ks),
-                              kn + (2048 * ks + hd * L::TILE) / 16, tc_idesc<true>(N), p < 2 || ks > 0);
+            auto update = [&](int ks, int hd, int p, bool add) {   // half hd of Dk, or (Dk 64) all of it at once
+                tc_mma_ts(one, tu + L::UP + 64 * hd, tu + (p < 2 ? L::U + 16 * ks + 8 * p : L::LO + 8 * ks),
+                          kn + (2048 * ks + hd * L::TILE) / 16, tc_idesc<true>(DKP == 128 ? 64 : DKP), add);
             };
             if (!tc_warp_wait(bar + B_FULL + par, (n >> 1) & 1, dead, d.spin)) break;
             if (n > 0 && !tc_warp_wait(bar + B_READ, par ^ 1, dead, d.spin)) break;
@@ -256,10 +251,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int ks = KS / 2; ks < KS; ++ks) rows(L::R, kd, 32 * hf, 32, p, ks, true);
                 tc_commit_to(one, bar + B_R + hf);
             }
+            // sums from their smallest terms up: the tensor core cuts an accumulator's low bits at every step
 #pragma unroll
-            for (int p = 2; p >= 0; --p) tri_v(L::U, xd + p * L::TILE / 16, p == 2);
+            for (int p = 2; p >= 1; --p)
 #pragma unroll
-            for (int p = 1; p >= 0; --p) tri_v(L::OA, zd + p * L::TILE / 16, p == 1);
+                for (int ks = 0; ks < C / 16; ++ks) tri_v(L::U, xd + p * L::TILE / 16, ks, p < 2 || ks > 0);
+#pragma unroll
+            for (int p = 1; p >= 0; --p)
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks) tri_v(L::OA, zd + p * L::TILE / 16, ks, p < 1 || ks > 0);
             bool ok = true;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -267,12 +267,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int a = 2; a >= 0; --a)
+                for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-                    for (int p = 2 - a; p >= 0; --p) {
-                        tri(L::U, L::UP + a * (C / 2), xd + p * L::TILE / 16, 2 * hf);
-                        tri(L::U, L::UP + a * (C / 2), xd + p * L::TILE / 16, 2 * hf + 1);
-                    }
+                    for (int a = sum; a >= 0; --a)
+#pragma unroll
+                        for (int ks = 2 * hf; ks < 2 * hf + 2; ++ks)
+                            tri(L::U, L::UP + a * (C / 2), xd + (sum - a) * L::TILE / 16, ks);
+#pragma unroll
+                for (int ks = 2 * hf; ks < 2 * hf + 2; ++ks) tri_v(L::U, xd, ks, true);
                 tc_commit_to(one, bar + B_UACC + hf);
             }
             if (!ok) break;
@@ -292,16 +294,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!tc_warp_wait(bar + B_U, par, dead, d.spin)) break;
             tc_fence_after();
 #pragma unroll
-            for (int hd = 0; hd < DKP / 64; ++hd) {
-                update(0, hd);
-                update(1, hd);
-            }
+            for (int p = 2; p >= 1; --p)
+#pragma unroll
+                for (int hd = 0; hd < DKP / 64; ++hd) {
+                    update(0, hd, p, p < 2);
+                    update(1, hd, p, true);
+                }
             if (!tc_warp_wait(bar + B_U + 1, par, dead, d.spin)) break;
             tc_fence_after();
 #pragma unroll
             for (int hd = 0; hd < DKP / 64; ++hd) {
-                update(2, hd);
-                update(3, hd);
+#pragma unroll
+                for (int p = 2; p >= 1; --p) {
+                    update(2, hd, p, true);
+                    update(3, hd, p, true);
+                }
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks) update(ks, hd, 0, true);
                 tc_commit_to(one, bar + B_UPD + hd);
             }
             if (DKP == 64) tc_commit_to(one, bar + B_UPD + 1);

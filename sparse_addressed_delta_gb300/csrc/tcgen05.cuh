@@ -91,6 +91,14 @@ __device__ __forceinline__ void tc_load_frag16(uint32_t a, uint32_t b, float (&v
         : "r"(a), "r"(b)
         : "memory");
 }
+__device__ __forceinline__ void tc_load_frag16(uint32_t a, float (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+        : "r"(a)
+        : "memory");
+}
 __device__ __forceinline__ void tc_store8(uint32_t addr, const unsigned (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
