@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     // 16 x 16 block (bi, bj) of the C x C products, on or below the diagonal
     const bool block = warp < BLOCKS;
     const int bi = warp < 1 ? 0 : warp < 3 ? 1 : warp < 6 ? 2 : 3, bj = warp - bi * (bi + 1) / 2;
-    float G1[MT][2][4] = {}, G2[MT][2][4] = {}, G3[MT][2][4] = {}, E[2][4] = {}, DP[2][4] = {};
+    // of the products that reach the gates, the lesser terms have sums of their own: the tensor core cuts
+    // an accumulator's low bits at every step
+    float G1[MT][2][4] = {}, L1[MT][2][4] = {}, G2[MT][2][4] = {}, G3[MT][2][4] = {}, E[2][4] = {}, DP[2][4] = {}, LP[2][4] = {};
     for (int c0 = 0; c0 < d.Dv; c0 += kBackCols) {
         __syncthreads();
         // dO, dw and r of this column tile as planes; <dw, v> and <dw, r>
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             if (s < PL && plane_pair(s, p, PL)) mma_bf16(E[e], aw[s < PL ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
-                            if (s < KP && plane_pair(s, p, 3)) mma_bf16(DP[e], ao[s < KP ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
+                            if (s < KP && plane_pair(s, p, 3)) mma_bf16(s + p ? LP[e] : DP[e], ao[s < KP ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
                         }
             }
         }
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                     for (int p = 2; p >= 0; --p)
                         if (plane_pair(s, p, 3))
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) mma_bf16(G1[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
+                            for (int e = 0; e < 2; ++e) mma_bf16(s + p ? L1[mt][e] : G1[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
 #pragma unroll
                 for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<VPI>(sw + p * L::VT, r0, 16 * ks, lane));
 #pragma unroll
@@ -544,8 +546,8 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
             for (int e = 0; e < 2; ++e) {
                 const int c = dk0 + 8 * e + 2 * i4;
                 float *a = &G1[mt][e][2 * half], *x = &G2[mt][e][2 * half], *y = &G3[mt][e][2 * half];
-                a[0] *= f1;
-                a[1] *= f1;
+                a[0] = (a[0] + L1[mt][e][2 * half]) * f1;
+                a[1] = (a[1] + L1[mt][e][2 * half + 1]) * f1;
 #pragma unroll
                 for (int p = KP - 1; p >= 0; --p) {
                     const unsigned qq = *reinterpret_cast<const unsigned *>(smem + L::Q + p * L::TILE + r * KPI + 2 * c);
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                 for (int m = 0; m < 2; ++m) {
                     const int s = 16 * bj + 8 * e + 2 * i4 + m, i = 2 * half + m;
                     const float f = s <= t ? expf((hi[t] - hi[s]) + (lo[t] - lo[s])) * be[s] : 0.f;
-                    pa[m] = s <= t ? d.scale * (DP[e][i] * f) : 0.f;
+                    pa[m] = s <= t ? d.scale * ((DP[e][i] + LP[e][i]) * f) : 0.f;
                     aa[m] = s < t ? -be[t] * (E[e][i] * f) : 0.f;
                     zr = s <= t ? fmaf(pa[m], qk[e][i], zr) : zr;
                 }

@@ -249,12 +249,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int ks = KS / 2; ks < KS; ++ks) rows(32 - 32 * hf, 32, p, ks, true);
                 tc_commit_to(one, bar + B_E + hf);
             }
+            // sums from their smallest terms up: the tensor core cuts an accumulator's low bits at every step
+            auto grads = [&](int p, int ks, bool add) {
+                tc_mma_ss(one, tu + L::W, gm + 2048 * ks / 16, zn + (p * L::TILE + 2048 * ks) / 16, tc_idesc<true, true>(16 * ks + 16), add);
+            };
 #pragma unroll
-            for (int p = 2; p >= 0; --p)
+            for (int p = 2; p >= 1; --p)
 #pragma unroll
-                for (int ks = C / 16 - 1; ks >= 0; --ks)
-                    tc_mma_ss(one, tu + L::W, gm + 2048 * ks / 16, zn + (p * L::TILE + 2048 * ks) / 16, tc_idesc<true, true>(16 * ks + 16),
-                              p < 2 || ks < C / 16 - 1);
+                for (int ks = C / 16 - 1; ks >= 0; --ks) grads(p, ks, p < 2 || ks < C / 16 - 1);
             bool ok = true;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -262,12 +264,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int a = 2; a >= 0; --a)
+                for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-                    for (int p = 2 - a; p >= 0; --p) {
-                        tri(L::UP + a * (C / 2), xn + p * L::TILE / 16, 3 - 2 * hf);
-                        tri(L::UP + a * (C / 2), xn + p * L::TILE / 16, 2 - 2 * hf);
-                    }
+                    for (int a = sum; a >= 0; --a)
+#pragma unroll
+                        for (int ks = 3 - 2 * hf; ks >= 2 - 2 * hf; --ks) tri(L::UP + a * (C / 2), xn + (sum - a) * L::TILE / 16, ks);
+#pragma unroll
+                for (int ks = 3 - 2 * hf; ks >= 2 - 2 * hf; --ks) grads(0, ks, true);
                 tc_commit_to(one, bar + B_WACC + hf);
             }
             if (!ok) break;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!tc_warp_wait(bar + B_WACC + 1, par, dead, d.spin)) break;   // the decayed E makes room for the update
             tc_fence_after();
 #pragma unroll
-            for (int p = 2; p >= 0; --p)
+            for (int p = 2; p >= 1; --p)
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks)
 #pragma unroll
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!tc_warp_wait(bar + B_W, par, dead, d.spin)) break;
             tc_fence_after();
 #pragma unroll
-            for (int p = 2; p >= 0; --p)
+            for (int p = 2; p >= 1; --p)
 #pragma unroll
                 for (int hd = 0; hd < DKP / 64; ++hd) {
                     update(3, hd, p, kn, L::W, L::LO, true);
@@ -294,9 +297,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int hd = 0; hd < DKP / 64; ++hd) {
 #pragma unroll
-                for (int p = 2; p >= 0; --p) {
+                for (int p = 2; p >= 1; --p) {
                     update(1, hd, p, kn, L::W, L::LO, true);
                     update(0, hd, p, kn, L::W, L::LO, true);
+                }
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks) {
+                    update(ks, hd, 0, kn, L::W, L::LO, true);
+                    update(ks, hd, 0, qn, L::E, L::GL, true);
                 }
                 tc_commit_to(one, bar + B_UPD + hd);
             }
