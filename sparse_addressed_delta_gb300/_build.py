@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libsdm.so")
 SOURCES = ["api.cu", "phase1.cu", "solve.cu", "phase2.cu", "dualmm_tc.cu", "phase2_fused.cu",
            "noalloc.cu", "backward.cu", "host_io.cu", "layer_io.cu", "product_key.cu",
            "norm.cu", "delta.cu", "delta_step.cu", "delta_chunk.cu",
-           "delta_back.cu", "delta_scan_tc.cu", "delta_back_tc.cu"]
+           "delta_back.cu", "delta_scan_tc.cu", "delta_back_tc.cu",
+           "delta_back_local_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         load_planes<PP, C, THREADS>(st + L::P, w.p + bhn * (PP * C * XP), tid);
         load_values<T, NW * 16, C, THREADS>(st + L::V, grad + t0 * d.os[1], d.os[1], nt, d.Dv - dv_blk, tid);
         for (int i = tid; i < 3 * C / 4; i += THREADS)
-            cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * 3 * C + 4 * i, true);
+            cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * kDeltaAux * C + 4 * i, true);
         cp_async_commit();
     };
     // element e of the state's fragment j: row 8 j + 2 i4 + (e & 1), column dv0 + g4 + 8 (e >> 1)
@@ -354,33 +354,13 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     load_tokens<KP, DKP, C, THREADS>(sk, k, b * k.s[0] + t0 * k.s[1] + hk * k.s[2], d.Dk, nt, tid);
     load_tokens<KP, DKP, C, THREADS>(sq, q, b * q.s[0] + t0 * q.s[1] + hk * q.s[2], d.Dk, nt, tid);
     cp_async_commit();
-    if (warp == 0) {
-        const float *aux = lw.aux + bhn * 3 * C;
-        double s = 0.0;
-        constexpr int TL = C / 32;
-        double run[TL];
-#pragma unroll
-        for (int i = 0; i < TL; ++i) {
-            const int r = lane * TL + i;
-            if (r < nt) s += (double)delta_decay(in.g[b * d.gs[0] + (long long)(t0 + r) * d.gs[1] + h * d.gs[2]]);
-            run[i] = s;
-            from[r] = aux[r];
-            to[r] = aux[C + r];
-            be[r] = aux[2 * C + r];
-        }
-        double before = s;
-#pragma unroll
-        for (int m = 1; m < 32; m *= 2) {
-            const double x = __shfl_up_sync(~0u, before, m);
-            if (lane >= m) before += x;
-        }
-        before -= s;
-#pragma unroll
-        for (int i = 0; i < TL; ++i) {
-            const double x = before + run[i];
-            hi[lane * TL + i] = (float)x;
-            lo[lane * TL + i] = (float)(x - (double)(float)x);
-        }
+    for (int i = tid; i < C; i += THREADS) {
+        const float *aux = lw.aux + bhn * kDeltaAux * C;
+        from[i] = aux[i];
+        to[i] = aux[C + i];
+        be[i] = aux[2 * C + i];
+        hi[i] = aux[3 * C + i];
+        lo[i] = aux[4 * C + i];
     }
     for (int i = tid; i < 2 * C; i += THREADS) dwv[i] = 0.f;      // and dwr behind it
 

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int c = 0; c < 2; ++c) tc_tensor_load(st + L::G + c * L::TILE, &mg, dv_blk + 64 * c, h, t0, b, full);
                 bulk_g2s(st + L::X, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
                 bulk_g2s(st + L::Z, w.p + bhn * (3 * L::TILE), 3 * L::TILE, full);
-                bulk_g2s(smem + L::AUX + L::AB * s, w.aux + bhn * 3 * C, L::AB, full);
+                bulk_g2s(smem + L::AUX + L::AB * s, w.aux + bhn * kDeltaAux * C, L::AB, full);
             }
             __syncwarp();
             if (!tc_warp_wait(full, (it >> 1) & 1, dead, d.spin)) {

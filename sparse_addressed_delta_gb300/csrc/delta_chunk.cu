@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
         }
         const double all = __shfl_sync(~0u, before, 31);
         before -= s;
-        float *aux = w.aux + (((long long)b * d.H + h) * d.Nt + n) * 3 * C;
+        float *aux = w.aux + (((long long)b * d.H + h) * d.Nt + n) * kDeltaAux * C;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
             const int r = lane * PL + i;
@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
             aux[r] = expf((float)x);
             aux[C + r] = expf((float)(all - x)) * (BACK ? 1.f : bt[i]);
             aux[2 * C + r] = bt[i];
+            aux[3 * C + r] = hi[r];
+            aux[4 * C + r] = lo[r];
         }
     }
     cp_async_wait<0>();
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         load_planes<PP, C, THREADS>(st + L::P, w.p + bhn * (PP * C * XP), tid);
         load_values<T, NW * 16, C, THREADS>(st + L::V, v + t0 * d.vs[1], d.vs[1], nt, d.Dv - dv_blk, tid);
         for (int i = tid; i < 3 * C / 4; i += THREADS)
-            cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * 3 * C + 4 * i, true);
+            cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * kDeltaAux * C + 4 * i, true);
         cp_async_commit();
     };
 

@@ -7,6 +7,7 @@
 namespace sdm {
 
 constexpr int kDeltaMaxDk = 128, kDeltaMaxDv = 512;
+constexpr int kDeltaAux = 5;
 constexpr int kDeltaStepTokens = 16;     // up to this many tokens take the token-by-token kernel
 // A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten
 // whole, and -inf (a hard reset) stays out of the running sums' differences.
@@ -41,7 +42,7 @@ struct DeltaPlanes {
 // Per chunk and head, written by the chunk-local kernel (k_delta_local) for the scans:
 //   x   [3][C][C] bfloat16 planes of X
 //   p   [pp][C][C] planes of P diag(beta) (for the tcgen05 scan: of P diag(beta) X)
-//   aux [3][C] float: exp(L_t), exp(L_C - L_t) beta_t, beta_t
+//   aux [kDeltaAux][C] float: exp(L_t), exp(L_C - L_t) beta_t, beta_t, L_t as the sum of two
 // and for a backward: planes of (I + diag(beta) A)^-1 =: X and of P (for tcgen05: of P X), and exp(L_C -
 // L_t) without beta.
 // The planes' rows have shared memory's layout (delta_pitch, or tcgen05's 128-byte rows with permuted
@@ -95,6 +96,8 @@ cudaError_t launch_delta_back_scan_tc(const DeltaDims &d, const DeltaIn &in, con
 cudaError_t launch_delta_back_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                                     const DeltaPlanes &k, const DeltaLocal &w, const DeltaBack &o,
                                     cudaStream_t st);
+cudaError_t launch_delta_back_local_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, const DeltaBack &o,
+                                       cudaStream_t st);
 
 // ---------------------------------------------------------------------------------------
 // device helpers

@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int c = 0; c < 2; ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, h, t0, b, full);
                 bulk_g2s(st + L::X, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
                 bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, full);
-                bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * 3 * C, 2 * C * 4, full);
+                bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * kDeltaAux * C, 2 * C * 4, full);
             }
             __syncwarp();
             if (!tc_warp_wait(full, (n >> 1) & 1, dead, d.spin)) {
@@ -409,22 +409,44 @@ cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, 
 
 }  // namespace
 
-cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *s, int B, int T, int heads, int D) {
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         cudaDriverEntryPointQueryResult found;
         void *fn = nullptr;
         const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
         return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn) : nullptr;
     }();
+    return encode;
+}
+
+cudaError_t encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *p, const cuuint64_t *dim,
+                       const cuuint64_t *strides, const cuuint32_t *box) {
+    const auto encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return encode(m, type, rank, const_cast<void *>(p), dim, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *s, int B, int T, int heads, int D) {
     const cuuint64_t dim[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
     // a dimension of one element is never stepped along: any stride will do
     auto bytes = [](long long stride, int n) { return (cuuint64_t)(n > 1 ? stride * 2 : 16); };
     const cuuint64_t str[3] = {bytes(s[2], heads), bytes(s[1], T), bytes(s[0], B)};
-    const cuuint32_t box[4] = {64, 1, 64, 1}, one[4] = {1, 1, 1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dim, str, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess : cudaErrorInvalidValue;
+    const cuuint32_t box[4] = {64, 1, 64, 1};
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dim, str, box);
+}
+
+cudaError_t tc_state_map(CUtensorMap *m, const void *p, long long slots, int Dk, int Dv) {
+    const cuuint64_t dim[3] = {(cuuint64_t)Dv, (cuuint64_t)Dk, (cuuint64_t)slots};
+    const cuuint64_t str[2] = {(cuuint64_t)Dv * 4, (cuuint64_t)Dk * Dv * 4};
+    const cuuint32_t box[3] = {32, 128, 1};
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dim, str, box);
 }
 
 cudaError_t launch_delta_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o,
