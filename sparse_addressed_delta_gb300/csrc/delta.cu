@@ -91,7 +91,7 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     if (backward) {
         l.ends = take(delta_chunks(d) * d.Dk * d.Dv * 4);
         l.w = take(delta_chunks(d) * d.C * d.Dv * 4);
-        const size_t part = d.H != d.Hk && !d.tc ? (size_t)d.B * d.T * d.H * d.Dk * 4 : 0;
+        const size_t part = d.H != d.Hk && !(d.tc && d.Dv <= 128) ? (size_t)d.B * d.T * d.H * d.Dk * 4 : 0;
         l.dq = take(part);
         l.dk = take(part);
     }
@@ -275,7 +275,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     o.dq = reinterpret_cast<float *>(ws + l.dq);
     o.dk = reinterpret_cast<float *>(ws + l.dk);
     if (e == cudaSuccess) e = d.tc ? launch_delta_back_scan_tc(d, in, w, o, st) : launch_delta_back_scan(d, in, qp, kp, w, o, st);
-    if (e == cudaSuccess) e = d.tc ? launch_delta_back_local_tc(d, in, w, o, st) : launch_delta_back_local(d, in, qp, kp, w, o, st);
+    if (e == cudaSuccess) e = d.tc && d.Dv <= 128 ? launch_delta_back_local_tc(d, in, w, o, st) : launch_delta_back_local(d, in, qp, kp, w, o, st);
     return delta_status(e);
 }
 

@@ -1,19 +1,19 @@
 // The chunk-local gradients of the gated delta rule (k_delta_back_local in delta_back.cu has the formulas)
-// on the 5th-generation tensor cores, for bfloat16 inputs. Transposed: 128 of Dk are the lanes of tensor
-// memory, the chunk's 64 tokens its columns.
-//   G1 = S0 dO^T (3 planes of S0);  G2 = S0 dw^T;  G3 = D1 r^T (two planes of each operand)
+// on the 5th-generation tensor cores, for bfloat16 inputs with up to 128 value columns. All sums lie in
+// tensor memory, with a product's M = 128 in its lanes:
+//   [dw; dO] r^T, q k^T  (rows: the tokens, 64 + 64)        three planes of r, two of dw
+//   G1 = S0 dO^T (3 planes of S0);  G2 = S0 dw^T;  G3 = D1 r^T  (rows: Dk; two planes of each operand)
 //   dq^T = scale G G1 + K^T p^T;    dk^T = -beta G G2 + e^{L_C - L} beta G3 + Q^T p + K^T (a + a^T)
-// S0 and D1 are A operands in tensor memory, as planes that their own lanes' threads store; dO, dw and r
-// are B operands in shared memory; K and Q are A operands there for the second line, whose B operands p
-// and a serve in both majors. The C x C products dw r^T, dO r^T and q k^T, ten 16 x 16 blocks on and below
-// the diagonal, are a warp's m16n8k16 products each, beside the others.
+// S0 and D1 are A operands in tensor memory, as planes that their own lanes' threads store; dO, dw, r, K
+// and Q are operands in shared memory, and so are the planes of p and a, which serve in both majors.
 //
 // A block stays on its SM and takes chunk after chunk, for all the value heads of one key head in turn:
 // dq and dk are summed over them in registers, in head order. Warps 0..15 compute, warp 16 issues the
 // products, warp 17 loads: K and Q of a chunk, dO of a head, the states in boxes of 32 columns (four
-// slots), always as far ahead as their places are free.
-// What bounds it: a head's chunk reads 225 KB and writes its gradients; the phases (planes, states,
-// products, results) follow one another with one block an SM.
+// slots: D1, the next chunk's start for <S1, D1>, S0), always as far ahead as their places are free, and
+// asks L2 for what the computing warps read themselves.
+// What bounds it: a head's chunk reads 240 KB and writes its gradients (10000 cycles at the card's copy
+// rate); its phases (planes, p and a, states, results) follow one another with one block an SM.
 //
 // Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block; the computing warps
 // then run through without waiting (they meet at barriers), the others stop and wait for what they have
@@ -27,32 +27,31 @@ constexpr int kC = 64, kWarps = 16, kThreads = 32 * (kWarps + 2);
 
 struct BackLocalTc {
     static constexpr int TILE = kC * 128, BOX = 128 * 128;         // 64 tokens; 32 float columns of a state
-    static constexpr int K = 0, Q = 2 * TILE, G = 4 * TILE;        // G: the readings' gradient
-    static constexpr int W = 6 * TILE, R = 10 * TILE;              // two planes of dw, three of r
-    static constexpr int P = W, A = W + 2 * TILE;                  // two planes each, once dw's are used
-    static constexpr int S = 16 * TILE;                            // four boxes
+    // K and Q, dw's first plane and dO: two tiles (columns) each, alternating, so that one operand of 128
+    // rows takes both
+    static constexpr int K = 0, Q = K + TILE, W = 4 * TILE, G = W + TILE, PAIR = 2 * TILE;
+    static constexpr int W1 = 8 * TILE, R = 10 * TILE;             // dw's second plane, r's three
+    static constexpr int P = R + 4 * TILE, A = 16 * TILE;          // two planes each; p's in the place of r's third
+    static constexpr int S = 18 * TILE;                            // four boxes
     static constexpr int F = S + 4 * BOX;
     // floats: from, to, beta, L (two) [5][C]; <dw, v>, <dw, r> [C]; row sums of p * qk [4][C]; row products
     // with q [4][C]; <S1, D1> [warps]
     static constexpr int FLOATS = 7 * kC + 4 * kC + 4 * kC + kWarps;
     static constexpr int BARS = F + FLOATS * 4, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024 && BARS % 8 == 0, "shared memory");
-    // tensor memory columns: planes of S0 (then dq's and dk's second terms), of D1, G1, G2, G3
-    static constexpr int SP = 0, DQ = 0, DK = 64, DP = 192, G1 = 320, G2 = 384, G3 = 448;
+    // tensor memory columns: [dw; dO] r^T, dw's second plane, [k; q] k^T, then in their place the planes of
+    // S0; planes of D1, then in their place dq's and dk's second terms; G1, G2, G3
+    static constexpr int E = 0, E2 = 64, QK = 128, SP = 0, DP = 192, DQ = 192, DK = 256, G1 = 320, G2 = 384, G3 = 448;
 };
 
 enum {
-    B_T = 0, B_TFREE, B_DO, B_DOFREE, B_BOX, B_BFREE = B_BOX + 4, B_PL = B_BFREE + 4, B_S0, B_D1, B_G, B_PA, B_DQ, B_DRAIN, B_COUNT
+    B_T = 0, B_TFREE, B_DO, B_DOFREE, B_BOX, B_BFREE = B_BOX + 4, B_PL = B_BFREE + 4, B_E, B_D1, B_G3, B_PA, B_DQ, B_S0, B_G, B_DRAIN, B_COUNT
 };
 
-// fragments of a [tokens][128] operand in two tiles as tc_at lays them out (frag_rc, frag_cr)
+// blocks (r, c), (r + 8, c), (r, c + 8), (r + 8, c + 8) of a [tokens][128] operand in two tiles, PAIR apart
 __device__ __forceinline__ unsigned at_rc(unsigned base, int r0, int c0, int lane) {
     const int r = r0 + (lane & 15), c = (c0 >> 3) + (lane >> 4);
-    return base + (c >> 3) * BackLocalTc::TILE + tc_at(r, c & 7);
-}
-__device__ __forceinline__ unsigned at_cr(unsigned base, int r0, int c0, int lane) {
-    const int r = r0 + (lane & 7) + ((lane >> 4) << 3), c = (c0 >> 3) + ((lane >> 3) & 1);
-    return base + (c >> 3) * BackLocalTc::TILE + tc_at(r, c & 7);
+    return base + (c >> 3) * BackLocalTc::PAIR + tc_at(r, c & 7);
 }
 
 __device__ __forceinline__ void state_load(void *dst, const CUtensorMap *m, int col, int slot, unsigned long long *bar) {
@@ -61,6 +60,10 @@ __device__ __forceinline__ void state_load(void *dst, const CUtensorMap *m, int 
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(m), "r"(col), "r"(0), "r"(slot), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p, size_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((unsigned)bytes) : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -77,13 +80,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *dead = reinterpret_cast<int *>(bar + B_COUNT);
     auto slot = reinterpret_cast<uint32_t *>(bar + B_COUNT + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
-    const int group = d.H / d.Hk, tiles = (d.Dv + 127) / 128;
-    const long long items = (long long)d.B * d.Hk * d.Nt;
+    const int group = d.H / d.Hk;
+    const unsigned items = (unsigned)((long long)d.B * d.Hk * d.Nt);    // below 2^31
 
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
-            const bool all = i == B_PL || i == B_S0 || i == B_D1;
-            mbar_init(bar + i, all ? kWarps : i == B_TFREE || i == B_DOFREE ? kWarps + 1 : i >= B_BFREE && i < B_PL ? 4 : i == B_PA ? 10 : 1);
+            const bool all = i == B_PL || i == B_D1 || i == B_PA || i == B_S0;
+            mbar_init(bar + i, all ? kWarps : i == B_TFREE ? kWarps + 1 : i >= B_BFREE && i < B_PL ? 4 : 1);
         }
         *dead = 0;
         fence_mbar_init();
@@ -99,12 +102,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     struct Item {
         int b, hk, n, nt;
     };
-    auto item = [&](long long i) {
+    auto item = [&](unsigned i) {
         Item x;
-        x.n = (int)(i % d.Nt);
-        const long long bh = i / d.Nt;
-        x.b = (int)(bh / d.Hk);
-        x.hk = (int)(bh % d.Hk);
+        x.n = (int)(i % (unsigned)d.Nt);
+        const unsigned bh = i / (unsigned)d.Nt;
+        x.b = (int)(bh / (unsigned)d.Hk);
+        x.hk = (int)(bh % (unsigned)d.Hk);
         const int nt = delta_valid(in.valid, x.b, d.T) - x.n * C;
         x.nt = nt < 0 ? 0 : nt < C ? nt : C;
         return x;
@@ -116,8 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned sb = smem_u32(smem);
         float *from = reinterpret_cast<float *>(smem + L::F), *to = from + C, *be = to + C, *hi = be + C, *lo = hi + C;
         float *dwv = lo + C, *dwr = dwv + C, *zrow = dwr + C, *dots = zrow + 4 * C, *ends = dots + 4 * C;
-        const bool block = warp < 10;
-        const int bi = warp < 1 ? 0 : warp < 3 ? 1 : warp < 6 ? 2 : 3, bj = warp - bi * (bi + 1) / 2;
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); };
         auto arrive = [&](int which) {
             __syncwarp();
@@ -127,11 +128,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto clear_rows = [&](unsigned char *tile, int nt) {
             for (int i = tid; i < (C - nt) * 16; i += 32 * kWarps) {
                 const int r = nt + (i >> 4), c = i & 15;
-                *reinterpret_cast<uint4 *>(tile + (c >> 3) * L::TILE + tc_at(r, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(tile + (c >> 3) * L::PAIR + tc_at(r, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
             }
         };
-        unsigned it = 0, unit = 0, step = 0;                       // items, heads and column tiles so far
-        for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+        unsigned it = 0, unit = 0;                                 // items and heads so far
+        for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
             const Item x = item(i);
             const int t0 = x.n * C, rows = d.T - t0 < C ? d.T - t0 : C;
             const long long tok = (long long)x.b * d.T + t0;
@@ -155,182 +156,152 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 meet();
             }
-            float qk[2][4] = {};
-            if (block) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    unsigned a[4], bb[4];
-                    ldsm4(a, at_rc(sb + L::Q, 16 * bi, 16 * ks, lane));
-                    ldsm4(bb, at_cr(sb + L::K, 16 * bj, 16 * ks, lane));
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) mma_bf16(qk[e], a, bb[2 * e], bb[2 * e + 1]);
-                }
-            }
             // this warp's 32 of Dk x 16 tokens of dq^T and dk^T, in fragments: [16 lanes][..]
             float dq[2][8] = {}, dk[2][8] = {};
             for (int hh = 0; hh < group; ++hh, ++unit) {
                 const int h = x.hk * group + hh;
-                const long long bh = (long long)x.b * d.H + h, bhn = bh * d.Nt + x.n, cells = (long long)d.Dk * d.Dv;
+                const long long bh = (long long)x.b * d.H + h, bhn = bh * d.Nt + x.n;
                 meet();                                            // the last head's floats are used
                 if (tid < 5 * C) from[tid] = lw.aux[bhn * kDeltaAux * C + tid];
-                else if (tid - 5 * C < 2 * C) dwv[tid - 5 * C] = 0.f;
                 const T *val = static_cast<const T *>(in.v) + x.b * d.vs[0] + t0 * d.vs[1] + h * d.vs[2];
                 const float *wp = o.w + bhn * C * (long long)d.Dv, *rp = o.r + bhn * C * (long long)d.Dv;
-                {
-                    const float4 *u = reinterpret_cast<const float4 *>(o.snap + (bh * (d.Nt + 1) + x.n + 1) * cells);
-                    const float4 *v = reinterpret_cast<const float4 *>(o.ends + bhn * cells);
-                    float s = 0.f;
-#pragma unroll 4
-                    for (int e = tid; e < (int)(cells / 4); e += 32 * kWarps) {
-                        const float4 a = __ldg(u + e), c = __ldg(v + e);
-                        s = fmaf(a.x, c.x, fmaf(a.y, c.y, fmaf(a.z, c.z, fmaf(a.w, c.w, s))));
+                meet();
+                const unsigned par = unit & 1;
+                // dw and r as planes; <dw, v> and <dw, r>
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int idx = tid + 32 * kWarps * e, r = idx >> 4, c = idx & 15, col = 8 * c;
+                    float y[8] = {}, u[8] = {}, v[8] = {};
+                    if (r < x.nt && col < d.Dv) {
+                        load_vec<float, 8, true>(wp + (long long)r * d.Dv + col, y);
+                        load_vec<float, 8, true>(rp + (long long)r * d.Dv + col, u);
+                        load_vec<T, 8, true>(val + r * d.vs[1] + col, v);
                     }
+                    float s = 0.f, z = 0.f;
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        s = fmaf(y[m], v[m], s);
+                        z = fmaf(y[m], u[m], z);
+                    }
+#pragma unroll
+                    for (int m = 1; m < 16; m *= 2) {
+                        s += __shfl_xor_sync(~0u, s, m);
+                        z += __shfl_xor_sync(~0u, z, m);
+                    }
+                    if (c == 0) {
+                        dwv[r] = s;
+                        dwr[r] = z;
+                    }
+                    const int off = tc_at(r, c & 7), hf = c >> 3;
+                    unsigned p2[4][2], p3[4][3];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        split_bf16<2>(y[2 * m], y[2 * m + 1], p2[m]);
+                        split_bf16<3>(u[2 * m], u[2 * m + 1], p3[m]);
+                    }
+                    *reinterpret_cast<uint4 *>(smem + L::W + hf * L::PAIR + off) = make_uint4(p2[0][0], p2[1][0], p2[2][0], p2[3][0]);
+                    *reinterpret_cast<uint4 *>(smem + L::W1 + hf * L::TILE + off) = make_uint4(p2[0][1], p2[1][1], p2[2][1], p2[3][1]);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        *reinterpret_cast<uint4 *>(smem + L::R + (2 * p + hf) * L::TILE + off) = make_uint4(p3[0][p], p3[1][p], p3[2][p], p3[3][p]);
+                }
+                tc_warp_wait(bar + B_DO, par, dead, d.spin);
+                if (x.nt < C) clear_rows(smem + L::G, x.nt);
+                fence_proxy_async_smem();
+                arrive(B_PL);
+                // this quarter's box of a state: 32 columns of the lane's row; phase 3 unit + j of its slot
+                const unsigned char *box = smem + L::S + part * L::BOX;
+                auto piece = [&](int c) { return *reinterpret_cast<const float4 *>(box + tc_at(lane0 + lane, c)); };
+                auto planes = [&](auto count, uint32_t dst, const float4 (&y)[8]) {
+                    constexpr int N = decltype(count)::value;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        unsigned p[N][8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            unsigned s0[N], s1[N];
+                            split_bf16<N>(y[4 * half + e].x, y[4 * half + e].y, s0);
+                            split_bf16<N>(y[4 * half + e].z, y[4 * half + e].w, s1);
+#pragma unroll
+                            for (int m = 0; m < N; ++m) {
+                                p[m][2 * e] = s0[m];
+                                p[m][2 * e + 1] = s1[m];
+                            }
+                        }
+#pragma unroll
+                        for (int m = 0; m < N; ++m) tc_store8(dst + 64 * m + 16 * part + 8 * half, p[m]);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                };
+                {
+                    float4 y[8];
+                    tc_warp_wait(bar + B_BOX + part, par, dead, d.spin);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) y[c] = piece(c);
+                    arrive(B_BFREE + part);
+                    planes(std::integral_constant<int, 2>{}, at + L::DP, y);
+                    arrive(B_D1);
+                    float s = 0.f;
+                    tc_warp_wait(bar + B_BOX + part, par ^ 1, dead, d.spin);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 z = piece(c);
+                        s = fmaf(y[c].x, z.x, fmaf(y[c].y, z.y, fmaf(y[c].z, z.z, fmaf(y[c].w, z.w, s))));
+                    }
+                    arrive(B_BFREE + part);
 #pragma unroll
                     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
                     if (lane == 0) ends[warp] = s;
                 }
-                meet();
-                // dP's lesser terms have a sum of their own: the tensor core cuts an accumulator's low bits
-                float E[2][4] = {}, DP[2][4] = {}, LP[2][4] = {};
-                for (int tl = 0; tl < tiles; ++tl, ++step) {
-                    const unsigned par = step & 1;
-                    const int c0 = 128 * tl;
-                    if (tl > 0) tc_warp_wait(bar + B_G, par ^ 1, dead, d.spin);   // the planes are used
-                    if (tl > 0) meet();
-                    // dw and r as planes; <dw, v> and <dw, r>
+                // a (lanes 0..63) and p with its row sums (lanes 64..127): a row t, 16 columns s
+                tc_warp_wait(bar + B_E, par, dead, d.spin);
+                tc_fence_after();
+                {
+                    const int t = (lane0 & 32) + lane;
+                    const bool is_p = lane0 >= 64;
+                    float y[16], z[16];
+                    tc_load16(at + L::E + 16 * part, y);
+                    tc_load16(at + (is_p ? L::QK : L::E2) + 16 * part, z);
+                    tc_fence_before();
+                    if (16 * part <= (lane0 & 32) + 31) {          // else above the diagonal: never used
+                        const float ht = hi[t], lt = lo[t], ft = is_p ? d.scale : -be[t];
+                        float zr = 0.f;
+                        unsigned pl[8][2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int idx = tid + 32 * kWarps * e, r = idx >> 4, c = idx & 15, col = c0 + 8 * c;
-                        float y[8] = {}, u[8] = {}, v[8] = {};
-                        if (r < x.nt && col < d.Dv) {
-                            load_vec<float, 8, true>(wp + (long long)r * d.Dv + col, y);
-                            load_vec<float, 8, true>(rp + (long long)r * d.Dv + col, u);
-                            load_vec<T, 8, true>(val + r * d.vs[1] + col, v);
-                        }
-                        float s = 0.f, z = 0.f;
-#pragma unroll
-                        for (int m = 0; m < 8; ++m) {
-                            s = fmaf(y[m], v[m], s);
-                            z = fmaf(y[m], u[m], z);
+                        for (int e = 0; e < 16; ++e) {
+                            const int s = 16 * part + e;
+                            const float f = s <= t ? expf((ht - hi[s]) + (lt - lo[s])) * be[s] : 0.f;
+                            const float w = ft * f * (is_p ? y[e] : y[e] + z[e]);
+                            y[e] = s < t || (is_p && s == t) ? w : 0.f;
+                            if (is_p) zr = s <= t ? fmaf(y[e], z[e], zr) : zr;
                         }
 #pragma unroll
-                        for (int m = 1; m < 16; m *= 2) {
-                            s += __shfl_xor_sync(~0u, s, m);
-                            z += __shfl_xor_sync(~0u, z, m);
-                        }
-                        if (c == 0) {
-                            dwv[r] += s;
-                            dwr[r] += z;
-                        }
-                        unsigned char *dst = smem + L::W + (c >> 3) * L::TILE + tc_at(r, c & 7);
-                        unsigned p2[4][2], p3[4][3];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            split_bf16<2>(y[2 * m], y[2 * m + 1], p2[m]);
-                            split_bf16<3>(u[2 * m], u[2 * m + 1], p3[m]);
-                        }
+                        for (int e = 0; e < 8; ++e) split_bf16<2>(y[2 * e], y[2 * e + 1], pl[e]);
+                        unsigned char *dst = smem + (is_p ? L::P : L::A);
 #pragma unroll
                         for (int p = 0; p < 2; ++p)
-                            *reinterpret_cast<uint4 *>(dst + 2 * p * L::TILE) = make_uint4(p2[0][p], p2[1][p], p2[2][p], p2[3][p]);
 #pragma unroll
-                        for (int p = 0; p < 3; ++p)
-                            *reinterpret_cast<uint4 *>(dst + (L::R - L::W) + 2 * p * L::TILE) = make_uint4(p3[0][p], p3[1][p], p3[2][p], p3[3][p]);
-                    }
-                    tc_warp_wait(bar + B_DO, par, dead, d.spin);
-                    if (x.nt < C) clear_rows(smem + L::G, x.nt);
-                    fence_proxy_async_smem();
-                    arrive(B_PL);
-                    // this quarter's box of a state, 32 columns of the lane's row, as N planes
-                    auto box = [&](auto planes, uint32_t dst, unsigned phase) {
-                        constexpr int N = decltype(planes)::value;
-                        tc_warp_wait(bar + B_BOX + part, phase, dead, d.spin);
-                        const unsigned char *src = smem + L::S + part * L::BOX;
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            unsigned p[N][8];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 y = *reinterpret_cast<const float4 *>(src + tc_at(lane0 + lane, 4 * half + e));
-                                unsigned s0[N], s1[N];
-                                split_bf16<N>(y.x, y.y, s0);
-                                split_bf16<N>(y.z, y.w, s1);
-#pragma unroll
-                                for (int m = 0; m < N; ++m) {
-                                    p[m][2 * e] = s0[m];
-                                    p[m][2 * e + 1] = s1[m];
-                                }
-                            }
-#pragma unroll
-                            for (int m = 0; m < N; ++m) tc_store8(at + dst + 64 * m + 16 * part + 8 * half, p[m]);
-                        }
-                        arrive(B_BFREE + part);
-                        tc_wait_st();
-                        tc_fence_before();
-                    };
-                    box(std::integral_constant<int, 3>{}, L::SP, 0);
-                    arrive(B_S0);
-                    box(std::integral_constant<int, 2>{}, L::DP, 1);
-                    arrive(B_D1);
-                    tc_warp_wait(bar + B_PL, par, dead, d.spin);
-                    if (block) {
-#pragma unroll 2
-                        for (int ks = 0; ks < 8; ++ks) {
-                            unsigned aw[2][4], ao[4], br[3][4];
-#pragma unroll
-                            for (int p = 0; p < 2; ++p) ldsm4(aw[p], at_rc(sb + L::W + 2 * p * L::TILE, 16 * bi, 16 * ks, lane));
-#pragma unroll
-                            for (int p = 0; p < 3; ++p) ldsm4(br[p], at_cr(sb + L::R + 2 * p * L::TILE, 16 * bj, 16 * ks, lane));
-                            ldsm4(ao, at_rc(sb + L::G, 16 * bi, 16 * ks, lane));
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                mma_bf16(LP[e], ao, br[2][2 * e], br[2][2 * e + 1]);
-                                mma_bf16(E[e], aw[1], br[0][2 * e], br[0][2 * e + 1]);
-                                mma_bf16(DP[e], ao, br[0][2 * e], br[0][2 * e + 1]);
-                                mma_bf16(E[e], aw[0], br[1][2 * e], br[1][2 * e + 1]);
-                                mma_bf16(LP[e], ao, br[1][2 * e], br[1][2 * e + 1]);
-                                mma_bf16(E[e], aw[0], br[0][2 * e], br[0][2 * e + 1]);
-                            }
-                        }
-                    }
-                    arrive(B_DOFREE);
-                }
-                tc_warp_wait(bar + B_G, (step - 1) & 1, dead, d.spin);
-                tc_fence_after();
-                meet();                                            // dw's planes are used by all
-                if (block) {                                       // p, a and the row sums of p * (q k^T)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int t = 16 * bi + g4 + 8 * half;
-                        const float ht = hi[t], lt = lo[t], bt = be[t];
-                        float zr = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float pa[2], aa[2];
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                const int s = 16 * bj + 8 * e + 2 * i4 + m, j = 2 * half + m;
-                                const float f = s <= t ? expf((ht - hi[s]) + (lt - lo[s])) * be[s] : 0.f;
-                                pa[m] = s <= t ? d.scale * ((DP[e][j] + LP[e][j]) * f) : 0.f;
-                                aa[m] = s < t ? -bt * (E[e][j] * f) : 0.f;
-                                zr = s <= t ? fmaf(pa[m], qk[e][j], zr) : zr;
-                            }
-                            const int off = tc_at(t, 2 * bj + e) + 4 * i4;
-                            unsigned pl[2];
-                            split_bf16<2>(pa[0], pa[1], pl);
-                            *reinterpret_cast<unsigned *>(smem + L::P + off) = pl[0];
-                            *reinterpret_cast<unsigned *>(smem + L::P + L::TILE + off) = pl[1];
-                            split_bf16<2>(aa[0], aa[1], pl);
-                            *reinterpret_cast<unsigned *>(smem + L::A + off) = pl[0];
-                            *reinterpret_cast<unsigned *>(smem + L::A + L::TILE + off) = pl[1];
-                        }
-                        zr += __shfl_xor_sync(~0u, zr, 1);
-                        zr += __shfl_xor_sync(~0u, zr, 2);
-                        if (i4 == 0) zrow[bj * C + t] = zr;
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<uint4 *>(dst + p * L::TILE + tc_at(t, 2 * part + e)) =
+                                    make_uint4(pl[4 * e][p], pl[4 * e + 1][p], pl[4 * e + 2][p], pl[4 * e + 3][p]);
+                        if (is_p) zrow[part * C + t] = zr;
                     }
                     fence_proxy_async_smem();
                     arrive(B_PA);
                 }
+                {
+                    float4 y[8];
+                    tc_warp_wait(bar + B_BOX + part, par, dead, d.spin);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) y[c] = piece(c);
+                    arrive(B_BFREE + part);
+                    planes(std::integral_constant<int, 3>{}, at + L::SP, y);
+                    arrive(B_S0);
+                }
                 // results: this warp's lanes (32 of Dk) and 16 tokens
+                tc_warp_wait(bar + B_G, par, dead, d.spin);
+                tc_fence_after();
                 float f1[4], f2[4], f3[4], s1[4] = {};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -368,8 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int m = 4; m < 32; m *= 2) s1[e] += __shfl_xor_sync(~0u, s1[e], m);
                     if (g4 == 0) dots[(warp & 3) * C + 16 * part + 8 * (e >> 1) + 2 * i4 + (e & 1)] = s1[e];
                 }
-                tc_warp_wait(bar + B_DQ, unit & 1, dead, d.spin);
-                tc_fence_after();
 #pragma unroll
                 for (int l = 0; l < 2; ++l) {
                     const uint32_t a = at + ((uint32_t)(16 * l) << 16);
@@ -416,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // dq and dk as rows in the places of dw's planes and r's first, stored as tensors
+            // dq and dk as rows in the places of dw's second plane and r's first, stored as tensors
             {
                 const int orow = 16 * part + 8 * (lane >> 4) + (lane & 7), ocol = (lane0 >> 3) + ((lane >> 3) & 1);
 #pragma unroll
@@ -427,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     auto live = [&](int m) { return 16 * part + 8 * (m >> 2) + 2 * i4 + (m & 1) < x.nt; };
 #pragma unroll
                     for (int e = 0; e < 4; ++e) r[e] = pack_bf16(live(2 * e) ? dq[l][2 * e] : 0.f, live(2 * e + 1) ? dq[l][2 * e + 1] : 0.f);
-                    stsm4t(dst + L::W, r);
+                    stsm4t(dst + L::W1, r);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) r[e] = pack_bf16(live(2 * e) ? dk[l][2 * e] : 0.f, live(2 * e + 1) ? dk[l][2 * e + 1] : 0.f);
                     stsm4t(dst + L::R, r);
@@ -438,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp == 0 && lane == 0) {
                     for (int c = 0; c < 2; ++c)
                         if (64 * c < d.Dk) {
-                            tc_tensor_store(&mdq, 64 * c, x.hk, t0, x.b, smem + L::W + c * L::TILE);
+                            tc_tensor_store(&mdq, 64 * c, x.hk, t0, x.b, smem + L::W1 + c * L::TILE);
                             tc_tensor_store(&mdk, 64 * c, x.hk, t0, x.b, smem + L::R + c * L::TILE);
                         }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -452,44 +421,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
-        const uint64_t gk = tc_k_major(base + L::G), wk = tc_k_major(base + L::W), rk = tc_k_major(base + L::R);
-        const uint64_t km = tc_n_major(base + L::K, L::TILE), qm = tc_n_major(base + L::Q, L::TILE);
+        // one tile's K steps of 16 columns, then the other's: `pair` bytes apart
+        auto at_ks = [](int ks, int pair) { return ((ks >> 2) * pair + 32 * (ks & 3)) / 16; };
+        const uint64_t kq = tc_k_major(base + L::K), wg = tc_k_major(base + L::W), w1 = tc_k_major(base + L::W1);
+        const uint64_t gk = tc_k_major(base + L::G), rk = tc_k_major(base + L::R);
+        const uint64_t km = tc_n_major(base + L::K, L::PAIR), qm = tc_n_major(base + L::Q, L::PAIR);
         const uint64_t pk = tc_k_major(base + L::P), pn = tc_n_major(base + L::P, L::TILE);
         const uint64_t ak = tc_k_major(base + L::A), an = tc_n_major(base + L::A, L::TILE);
-        unsigned unit = 0, step = 0;
+        unsigned it = 0, unit = 0;
         bool ok = true;
-        for (long long i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        for (unsigned i = blockIdx.x; i < items && ok; i += gridDim.x) {
             const Item x = item(i);
             if (x.nt == 0) continue;
             for (int hh = 0; hh < group && ok; ++hh, ++unit) {
-                for (int tl = 0; tl < tiles && ok; ++tl, ++step) {
-                    const unsigned par = step & 1;
-                    // 8 K steps of 16 columns; plane `a` of a state, plane tile of dO, dw or r
-                    auto states = [&](uint32_t dst, uint32_t a, uint64_t tile, bool first) {
+                const unsigned par = unit & 1;
+                auto states = [&](uint32_t dst, uint32_t a, uint64_t tile, int pair, bool first) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_ts(one, tu + dst, tu + a + 8 * ks, tile + ((ks >> 2) * L::TILE + 32 * (ks & 3)) / 16, tc_idesc<false>(C), !first || ks > 0 || tl > 0);
-                    };
-                    ok = tc_warp_wait(bar + B_PL, par, dead, d.spin) && tc_warp_wait(bar + B_S0, par, dead, d.spin);
-                    if (!ok) break;
-                    tc_fence_after();
-                    states(L::G1, L::SP + 128, gk, true);
-                    states(L::G1, L::SP + 64, gk, false);
-                    states(L::G1, L::SP, gk, false);
-                    states(L::G2, L::SP + 64, wk, true);
-                    states(L::G2, L::SP, wk + 2 * L::TILE / 16, false);
-                    states(L::G2, L::SP, wk, false);
-                    ok = tc_warp_wait(bar + B_D1, par, dead, d.spin);
-                    if (!ok) break;
-                    tc_fence_after();
-                    states(L::G3, L::DP + 64, rk, true);
-                    states(L::G3, L::DP, rk + 2 * L::TILE / 16, false);
-                    states(L::G3, L::DP, rk, false);
-                    tc_commit_to(one, bar + B_G);
-                    tc_commit_to(one, bar + B_DOFREE);
-                }
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_ts(one, tu + dst, tu + a + 8 * ks, tile + at_ks(ks, pair), tc_idesc<false>(C), !first || ks > 0);
+                };
+                auto rows = [&](uint32_t dst, uint64_t a, uint64_t tile, int apair, int pair, bool first) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_ss(one, tu + dst, a + at_ks(ks, apair), tile + at_ks(ks, pair), tc_idesc<false>(C), !first || ks > 0);
+                };
+                ok = tc_warp_wait(bar + B_PL, par, dead, d.spin);
                 if (!ok) break;
-                ok = tc_warp_wait(bar + B_PA, unit & 1, dead, d.spin) && tc_warp_wait(bar + B_G, (step - 1) & 1, dead, d.spin);
+                tc_fence_after();
+#pragma unroll
+                for (int p = 2; p >= 0; --p) rows(L::E, wg, rk + 2 * p * L::TILE / 16, L::PAIR, L::TILE, p == 2);
+                rows(L::E2, w1, rk, L::TILE, L::TILE, true);
+                rows(L::QK, kq, kq, L::PAIR, L::PAIR, true);
+                tc_commit_to(one, bar + B_E);
+                ok = tc_warp_wait(bar + B_D1, par, dead, d.spin);
+                if (!ok) break;
+                tc_fence_after();
+                states(L::G3, L::DP + 64, rk, L::TILE, true);
+                states(L::G3, L::DP, rk + 2 * L::TILE / 16, L::TILE, false);
+                states(L::G3, L::DP, rk, L::TILE, false);
+                tc_commit_to(one, bar + B_G3);
+                ok = tc_warp_wait(bar + B_PA, par, dead, d.spin) && tc_warp_wait(bar + B_G3, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
                 // B = lower triangular [t][s]: with t its N, K step s reaches the columns from 16 ks on; with
@@ -512,53 +483,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_mma_ss(one, tu + L::DK + 16 * ks, km + 2048 * ks / 16, ak + (p * L::TILE + 16 * ks * 128 + 32 * ks) / 16,
                                   tc_idesc<false, true>(C - 16 * ks), true);
                 }
-                tc_commit_to(one, bar + B_DQ);
+                ok = tc_warp_wait(bar + B_S0, par, dead, d.spin);
+                if (!ok) break;
+                tc_fence_after();
+                states(L::G1, L::SP + 128, gk, L::PAIR, true);
+                states(L::G1, L::SP + 64, gk, L::PAIR, false);
+                states(L::G1, L::SP, gk, L::PAIR, false);
+                states(L::G2, L::SP + 64, wg, L::PAIR, true);
+                states(L::G2, L::SP, w1, L::TILE, false);
+                states(L::G2, L::SP, wg, L::PAIR, false);
+                tc_commit_to(one, bar + B_G);
+                tc_commit_to(one, bar + B_DOFREE);
                 if (hh + 1 == group) tc_commit_to(one, bar + B_TFREE);
             }
+            ++it;
         }
         __syncwarp();
     } else {
         // ---- the loads
-        unsigned it = 0, step = 0;
-        unsigned boxes = 0, grads = 0;                             // started
+        unsigned it = 0, unit = 0, boxes = 0, grads = 0;           // the last two: started
         bool ok = true;
-        for (long long i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        for (unsigned i = blockIdx.x; i < items && ok; i += gridDim.x) {
             const Item x = item(i);
             if (x.nt == 0) continue;
             const int t0 = x.n * C;
-            if (it > 0) ok = tc_warp_wait(bar + B_TFREE, (it - 1) & 1, dead, d.spin);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar + B_T, 4 * L::TILE);
-                for (int c = 0; c < 2; ++c) {
-                    tc_tensor_load(smem + L::K + c * L::TILE, &mk, 64 * c, x.hk, t0, x.b, bar + B_T);
-                    tc_tensor_load(smem + L::Q + c * L::TILE, &mq, 64 * c, x.hk, t0, x.b, bar + B_T);
-                }
-            }
-            ++it;
-            for (int hh = 0; hh < group && ok; ++hh) {
+            for (int hh = 0; hh < group && ok; ++hh, ++unit) {
                 const int h = x.hk * group + hh;
-                const long long bh = (long long)x.b * d.H + h;
-                for (int tl = 0; tl < tiles && ok; ++tl, ++step) {
-                    if (step > 0) ok = tc_warp_wait(bar + B_DOFREE, (step - 1) & 1, dead, d.spin);
+                const long long bh = (long long)x.b * d.H + h, chunk = bh * d.Nt + x.n;
+                if (lane == 0) {
+                    const unsigned vals = (unsigned)(C * d.Dv * 4), cells = (unsigned)(d.Dk * d.Dv * 4);
+                    prefetch_l2(o.w + chunk * C * d.Dv, vals);
+                    prefetch_l2(o.r + chunk * C * d.Dv, vals);
+                    prefetch_l2(o.ends + chunk * d.Dk * d.Dv, cells);
+                    prefetch_l2(o.snap + (bh * (d.Nt + 1) + x.n) * d.Dk * d.Dv, cells);
+                }
+                __syncwarp();
+                // the slots free up in the middle of the head before: D1's boxes first
+                for (int e = 0; e < 12 && ok; ++e) {
+                    const int s = e & 3;
+                    if (unit > 0 || e >= 4) ok = tc_warp_wait(bar + B_BFREE + s, (3 * unit + e / 4 - 1) & 1, dead, d.spin);
                     if (!ok) break;
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(bar + B_DO, 2 * L::TILE);
-                        for (int c = 0; c < 2; ++c) tc_tensor_load(smem + L::G + c * L::TILE, &mg, 128 * tl + 64 * c, h, t0, x.b, bar + B_DO);
+                        mbar_arrive_expect_tx(bar + B_BOX + s, L::BOX);
+                        state_load(smem + L::S + s * L::BOX, e < 4 ? &md : &ms, 32 * s,
+                                   (int)(e < 4 ? chunk : bh * (d.Nt + 1) + x.n + (e < 8 ? 1 : 0)), bar + B_BOX + s);
                     }
                     __syncwarp();
-                    ++grads;
-                    for (int e = 0; e < 8 && ok; ++e) {            // S0's four boxes, then D1's
-                        const int s = e & 3;
-                        if (step > 0 || e >= 4) ok = tc_warp_wait(bar + B_BFREE + s, e >= 4 ? 0 : 1, dead, d.spin);
+                    ++boxes;
+                    if (e == 3) {
+                        if (unit > 0) ok = tc_warp_wait(bar + B_DOFREE, (unit - 1) & 1, dead, d.spin);
                         if (!ok) break;
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(bar + B_BOX + s, L::BOX);
-                            state_load(smem + L::S + s * L::BOX, e < 4 ? &ms : &md, 128 * tl + 32 * s,
-                                       (int)(e < 4 ? bh * (d.Nt + 1) + x.n : bh * d.Nt + x.n), bar + B_BOX + s);
+                            mbar_arrive_expect_tx(bar + B_DO, 2 * L::TILE);
+                            for (int c = 0; c < 2; ++c) tc_tensor_load(smem + L::G + c * L::PAIR, &mg, 64 * c, h, t0, x.b, bar + B_DO);
+                        }
+                        ++grads;
+                        if (hh == 0) {
+                            if (it > 0) ok = tc_warp_wait(bar + B_TFREE, (it - 1) & 1, dead, d.spin);
+                            if (!ok) break;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(bar + B_T, 4 * L::TILE);
+                                for (int c = 0; c < 2; ++c) {
+                                    tc_tensor_load(smem + L::K + c * L::PAIR, &mk, 64 * c, x.hk, t0, x.b, bar + B_T);
+                                    tc_tensor_load(smem + L::Q + c * L::PAIR, &mq, 64 * c, x.hk, t0, x.b, bar + B_T);
+                                }
+                            }
+                            ++it;
                         }
                         __syncwarp();
-                        ++boxes;
                     }
                 }
             }
