@@ -423,11 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
         // one tile's K steps of 16 columns, then the other's: `pair` bytes apart
         auto at_ks = [](int ks, int pair) { return ((ks >> 2) * pair + 32 * (ks & 3)) / 16; };
-        const uint64_t kq = tc_k_major(base + L::K), wg = tc_k_major(base + L::W), w1 = tc_k_major(base + L::W1);
-        const uint64_t gk = tc_k_major(base + L::G), rk = tc_k_major(base + L::R);
-        const uint64_t km = tc_n_major(base + L::K, L::PAIR), qm = tc_n_major(base + L::Q, L::PAIR);
-        const uint64_t pk = tc_k_major(base + L::P), pn = tc_n_major(base + L::P, L::TILE);
-        const uint64_t ak = tc_k_major(base + L::A), an = tc_n_major(base + L::A, L::TILE);
+        const uint32_t kq = tc_k_major(base + L::K), wg = tc_k_major(base + L::W), w1 = tc_k_major(base + L::W1);
+        const uint32_t gk = tc_k_major(base + L::G), rk = tc_k_major(base + L::R);
+        const uint32_t km = tc_n_major(base + L::K, L::PAIR), qm = tc_n_major(base + L::Q, L::PAIR);
+        const uint32_t pk = tc_k_major(base + L::P), pn = tc_n_major(base + L::P, L::TILE);
+        const uint32_t ak = tc_k_major(base + L::A), an = tc_n_major(base + L::A, L::TILE);
         unsigned it = 0, unit = 0;
         bool ok = true;
         for (unsigned i = blockIdx.x; i < items && ok; i += gridDim.x) {
@@ -435,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.nt == 0) continue;
             for (int hh = 0; hh < group && ok; ++hh, ++unit) {
                 const unsigned par = unit & 1;
-                auto states = [&](uint32_t dst, uint32_t a, uint64_t tile, int pair, bool first) {
+                auto states = [&](uint32_t dst, uint32_t a, uint32_t tile, int pair, bool first) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         tc_mma_ts(one, tu + dst, tu + a + 8 * ks, tile + at_ks(ks, pair), tc_idesc<false>(C), !first || ks > 0);
                 };
-                auto rows = [&](uint32_t dst, uint64_t a, uint64_t tile, int apair, int pair, bool first) {
+                auto rows = [&](uint32_t dst, uint32_t a, uint32_t tile, int apair, int pair, bool first) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         tc_mma_ss(one, tu + dst, a + at_ks(ks, apair), tile + at_ks(ks, pair), tc_idesc<false>(C), !first || ks > 0);

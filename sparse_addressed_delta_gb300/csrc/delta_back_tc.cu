@@ -216,19 +216,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const unsigned par = it & 1;
             const uint32_t st = base + par * L::STAGE;
             // a descriptor's address counts 16 bytes
-            const uint64_t kd = tc_k_major(st + L::K), xn = tc_n_major(st + L::X, L::TILE), zn = tc_n_major(st + L::Z, L::TILE);
-            const uint64_t kn = tc_n_major(st + L::K, L::TILE), qn = tc_n_major(st + L::Q, L::TILE), gm = tc_n_major(st + L::G, L::TILE);
+            const uint32_t kd = tc_k_major(st + L::K), xn = tc_n_major(st + L::X, L::TILE), zn = tc_n_major(st + L::Z, L::TILE);
+            const uint32_t kn = tc_n_major(st + L::K, L::TILE), qn = tc_n_major(st + L::Q, L::TILE), gm = tc_n_major(st + L::G, L::TILE);
             constexpr int KS = DKP / 16;
             auto rows = [&](int t0, int tokens, int p, int ks, bool add) {
                 tc_mma_ts(one, tu + L::E + t0, tu + L::SP + p * (DKP / 2) + 8 * ks, kd + (t0 * 128 + (ks >> 2) * L::TILE + 32 * (ks & 3)) / 16,
                           tc_idesc<false>(tokens), add);
             };
             // K step ks (tokens 16 ks ..) of a lower triangular B reaches the columns up to 16 ks + 15
-            auto tri = [&](uint32_t a, uint64_t tile, int ks) {
+            auto tri = [&](uint32_t a, uint32_t tile, int ks) {
                 tc_mma_ts(one, tu + L::W, tu + a + 8 * ks, tile + 2048 * ks / 16, tc_idesc<true>(16 * ks + 16), true);
             };
             constexpr int N = DKP == 128 ? 64 : DKP;
-            auto update = [&](int ks, int hd, int p, uint64_t tile, uint32_t two, uint32_t third, bool add) {
+            auto update = [&](int ks, int hd, int p, uint32_t tile, uint32_t two, uint32_t third, bool add) {
                 tc_mma_ts(one, tu + L::UP + 64 * hd, tu + (p < 2 ? two + 16 * ks + 8 * p : third + 8 * ks),
                           tile + (2048 * ks + hd * L::TILE) / 16, tc_idesc<true>(N), add);
             };

@@ -213,18 +213,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const unsigned par = n & 1;
             const uint32_t st = base + par * L::STAGE;
             // a descriptor's address counts 16 bytes
-            const uint64_t kd = tc_k_major(st + L::K), qd = tc_k_major(st + L::Q), xd = tc_k_major(st + L::X),
+            const uint32_t kd = tc_k_major(st + L::K), qd = tc_k_major(st + L::Q), xd = tc_k_major(st + L::X),
                            zd = tc_k_major(st + L::Z), kn = tc_n_major(st + L::K, L::TILE), vm = tc_n_major(st + L::V, L::TILE);
             // lower triangular B: K step ks reaches the columns from 16 ks on
-            auto tri = [&](uint32_t dst, uint32_t a, uint64_t tile, int ks) {
+            auto tri = [&](uint32_t dst, uint32_t a, uint32_t tile, int ks) {
                 tc_mma_ts(one, tu + dst + 16 * ks, tu + a + 8 * ks, tile + (16 * ks * 128 + 32 * ks) / 16, tc_idesc<false>(C - 16 * ks), true);
             };
-            auto tri_v = [&](uint32_t dst, uint64_t tile, int ks, bool add) {
+            auto tri_v = [&](uint32_t dst, uint32_t tile, int ks, bool add) {
                 tc_mma_ss(one, tu + dst + 16 * ks, vm + 2048 * ks / 16, tile + (16 * ks * 128 + 32 * ks) / 16,
                           tc_idesc<false, true>(C - 16 * ks), add);
             };
             // 16 tokens' or more rows of a [tokens][DKP] tile against the planes of S
-            auto rows = [&](uint32_t dst, uint64_t tile, int t0, int tokens, int p, int ks, bool add) {
+            auto rows = [&](uint32_t dst, uint32_t tile, int t0, int tokens, int p, int ks, bool add) {
                 tc_mma_ts(one, tu + dst + t0, tu + L::SP + p * (DKP / 2) + 8 * ks, tile + (t0 * 128 + (ks >> 2) * L::TILE + 32 * (ks & 3)) / 16,
                           tc_idesc<false>(tokens), add);
             };

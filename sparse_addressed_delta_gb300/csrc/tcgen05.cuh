@@ -11,17 +11,19 @@
 namespace sdm {
 
 // Operands in shared memory lie as tc_at puts them.
-// K-major operand (a row is one N index, its elements run along K): 8-row groups 1024 bytes apart;
-// a K step of 16 is 32 bytes along the row
-__device__ __forceinline__ uint64_t tc_k_major(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// An operand's descriptor: the lower word holds its address and the offset between tiles (both in units
+// of 16 bytes, so that steps are added to it), the upper one is the same for all: 8-row groups 1024 bytes
+// apart, 128-byte swizzle.
+__device__ __forceinline__ uint64_t tc_descriptor(uint32_t lower) {
+    return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lower;
 }
-// MN-major operand (a row is one K index, its elements run along N): 64 columns of N a tile, the next
-// tile `next` bytes on; 8 rows of K every 1024 bytes, so a K step of 16 is 2048 bytes
-__device__ __forceinline__ uint64_t tc_n_major(uint32_t addr, uint32_t next) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(next >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// K-major operand (a row is one M or N index, its elements run along K): a K step of 16 is 32 bytes along
+// the row
+__device__ __forceinline__ uint32_t tc_k_major(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
+// MN-major operand (a row is one K index, its elements run along M or N): 64 of them a tile, the next tile
+// `next` bytes on; a K step of 16 is 16 rows, 2048 bytes
+__device__ __forceinline__ uint32_t tc_n_major(uint32_t addr, uint32_t next) {
+    return ((addr >> 4) & 0x3FFFu) | ((next >> 4) << 16);
 }
 
 // instruction descriptor: bfloat16 x bfloat16 -> float32, M = 128, N columns
@@ -40,19 +42,19 @@ __device__ __forceinline__ uint32_t tc_elect() {
     return one;
 }
 // d [128 lanes x N] (+)= a [128 lanes x 16, two bfloat16 a column of tensor memory] b
-__device__ __forceinline__ void tc_mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
         "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
         " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(one)
+        "r"(a), "l"(tc_descriptor(b)), "r"(idesc), "r"((uint32_t)add), "r"(one)
         : "memory");
 }
 // the same with both operands in shared memory
-__device__ __forceinline__ void tc_mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
         "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
         " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(one)
+        "l"(tc_descriptor(a)), "l"(tc_descriptor(b)), "r"(idesc), "r"((uint32_t)add), "r"(one)
         : "memory");
 }
 
