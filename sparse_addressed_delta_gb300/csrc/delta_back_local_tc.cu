@@ -9,9 +9,9 @@
 //
 // A block stays on its SM and takes chunk after chunk, for all the value heads of one key head in turn:
 // dq and dk are summed over them in registers, in head order. Warps 0..15 compute, warp 16 issues the
-// products, warp 17 loads: K and Q of a chunk, dO of a head, the states in boxes of 32 columns (four
-// slots: D1, the next chunk's start for <S1, D1>, S0), always as far ahead as their places are free, and
-// asks L2 for what the computing warps read themselves.
+// products, warp 17 loads: K and Q of a chunk, dO of a head, and in boxes of 32 columns (four slots, in
+// turn) dw and r, D1, the next chunk's start for <S1, D1>, S0; always as far ahead as their places are
+// free.
 // What bounds it: a head's chunk reads 240 KB and writes its gradients (10000 cycles at the card's copy
 // rate); its phases (planes, p and a, states, results) follow one another with one block an SM.
 //
@@ -34,9 +34,9 @@ struct BackLocalTc {
     static constexpr int P = R + 4 * TILE, A = 16 * TILE;          // two planes each; p's in the place of r's third
     static constexpr int S = 18 * TILE;                            // four boxes
     static constexpr int F = S + 4 * BOX;
-    // floats: from, to, beta, L (two) [5][C]; <dw, v>, <dw, r> [C]; row sums of p * qk [4][C]; row products
-    // with q [4][C]; <S1, D1> [warps]
-    static constexpr int FLOATS = 7 * kC + 4 * kC + 4 * kC + kWarps;
+    // floats: from, to, beta, L (two) [5][C]; <dw, v>, <dw, r>, row sums of p * qk, row products with q
+    // [4 quarters][C] each; <S1, D1> [warps]
+    static constexpr int FLOATS = 5 * kC + 4 * 4 * kC + kWarps;
     static constexpr int BARS = F + FLOATS * 4, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024 && BARS % 8 == 0, "shared memory");
     // tensor memory columns: [dw; dO] r^T, dw's second plane, [k; q] k^T, then in their place the planes of
@@ -62,14 +62,11 @@ __device__ __forceinline__ void state_load(void *dst, const CUtensorMap *m, int 
         : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l2(const void *p, size_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((unsigned)bytes) : "memory");
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     k_delta_back_local_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                           const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap ms,
-                          const __grid_constant__ CUtensorMap md, const __grid_constant__ CUtensorMap mdq,
+                          const __grid_constant__ CUtensorMap md, const __grid_constant__ CUtensorMap mw,
+                          const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mdq,
                           const __grid_constant__ CUtensorMap mdk, DeltaDims d, DeltaIn in, DeltaLocal lw, DeltaBack o) {
     using L = BackLocalTc;
     using T = __nv_bfloat16;
@@ -118,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
         const unsigned sb = smem_u32(smem);
         float *from = reinterpret_cast<float *>(smem + L::F), *to = from + C, *be = to + C, *hi = be + C, *lo = hi + C;
-        float *dwv = lo + C, *dwr = dwv + C, *zrow = dwr + C, *dots = zrow + 4 * C, *ends = dots + 4 * C;
+        float *dwv = lo + C, *dwr = dwv + 4 * C, *zrow = dwr + 4 * C, *dots = zrow + 4 * C, *ends = dots + 4 * C;
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); };
         auto arrive = [&](int which) {
             __syncwarp();
@@ -164,53 +161,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 meet();                                            // the last head's floats are used
                 if (tid < 5 * C) from[tid] = lw.aux[bhn * kDeltaAux * C + tid];
                 const T *val = static_cast<const T *>(in.v) + x.b * d.vs[0] + t0 * d.vs[1] + h * d.vs[2];
-                const float *wp = o.w + bhn * C * (long long)d.Dv, *rp = o.r + bhn * C * (long long)d.Dv;
-                meet();
                 const unsigned par = unit & 1;
-                // dw and r as planes; <dw, v> and <dw, r>
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int idx = tid + 32 * kWarps * e, r = idx >> 4, c = idx & 15, col = 8 * c;
-                    float y[8] = {}, u[8] = {}, v[8] = {};
+                const unsigned char *box = smem + L::S + part * L::BOX;    // this quarter's slot
+                // dw and r as planes, <dw, v> and <dw, r>: a thread takes 16 of the quarter's columns of a row
+                {
+                    const int r = (tid & 127) >> 1, hc = tid & 1, col = 32 * part + 16 * hc;
+                    float v[16] = {};
                     if (r < x.nt && col < d.Dv) {
-                        load_vec<float, 8, true>(wp + (long long)r * d.Dv + col, y);
-                        load_vec<float, 8, true>(rp + (long long)r * d.Dv + col, u);
-                        load_vec<T, 8, true>(val + r * d.vs[1] + col, v);
+                        const T *vp = val + r * d.vs[1] + col;
+                        uint4 raw2[2] = {__ldg(reinterpret_cast<const uint4 *>(vp)), __ldg(reinterpret_cast<const uint4 *>(vp) + 1)};
+                        const T *e = reinterpret_cast<const T *>(raw2);
+#pragma unroll
+                        for (int m = 0; m < 16; ++m) v[m] = to_f32(e[m]);
                     }
+                    meet();                                        // the gates; the last head's floats and planes
+                    tc_warp_wait(bar + B_BOX + part, 0, dead, d.spin);
                     float s = 0.f, z = 0.f;
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        s = fmaf(y[m], v[m], s);
-                        z = fmaf(y[m], u[m], z);
-                    }
+                    for (int c = 0; c < 2; ++c) {                  // 8 columns: one piece of each plane
+                        float y[8], u[8];
 #pragma unroll
-                    for (int m = 1; m < 16; m *= 2) {
-                        s += __shfl_xor_sync(~0u, s, m);
-                        z += __shfl_xor_sync(~0u, z, m);
-                    }
-                    if (c == 0) {
-                        dwv[r] = s;
-                        dwr[r] = z;
-                    }
-                    const int off = tc_at(r, c & 7), hf = c >> 3;
-                    unsigned p2[4][2], p3[4][3];
+                        for (int e = 0; e < 2; ++e) {
+                            const int off = tc_at(r, 4 * hc + 2 * c + e);
+                            *reinterpret_cast<float4 *>(y + 4 * e) = *reinterpret_cast<const float4 *>(box + off);
+                            *reinterpret_cast<float4 *>(u + 4 * e) = *reinterpret_cast<const float4 *>(box + L::BOX / 2 + off);
+                        }
+                        unsigned p2[4][2], p3[4][3];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        split_bf16<2>(y[2 * m], y[2 * m + 1], p2[m]);
-                        split_bf16<3>(u[2 * m], u[2 * m + 1], p3[m]);
-                    }
-                    *reinterpret_cast<uint4 *>(smem + L::W + hf * L::PAIR + off) = make_uint4(p2[0][0], p2[1][0], p2[2][0], p2[3][0]);
-                    *reinterpret_cast<uint4 *>(smem + L::W1 + hf * L::TILE + off) = make_uint4(p2[0][1], p2[1][1], p2[2][1], p2[3][1]);
+                        for (int m = 0; m < 4; ++m) {
+                            split_bf16<2>(y[2 * m], y[2 * m + 1], p2[m]);
+                            split_bf16<3>(u[2 * m], u[2 * m + 1], p3[m]);
+                        }
 #pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                        *reinterpret_cast<uint4 *>(smem + L::R + (2 * p + hf) * L::TILE + off) = make_uint4(p3[0][p], p3[1][p], p3[2][p], p3[3][p]);
+                        for (int m = 0; m < 8; ++m) {
+                            s = fmaf(y[m], v[8 * c + m], s);
+                            z = fmaf(y[m], u[m], z);
+                        }
+                        const int pc = 4 * part + 2 * hc + c, off = tc_at(r, pc & 7), hf = pc >> 3;
+                        *reinterpret_cast<uint4 *>(smem + L::W + hf * L::PAIR + off) = make_uint4(p2[0][0], p2[1][0], p2[2][0], p2[3][0]);
+                        *reinterpret_cast<uint4 *>(smem + L::W1 + hf * L::TILE + off) = make_uint4(p2[0][1], p2[1][1], p2[2][1], p2[3][1]);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p)
+                            *reinterpret_cast<uint4 *>(smem + L::R + (2 * p + hf) * L::TILE + off) = make_uint4(p3[0][p], p3[1][p], p3[2][p], p3[3][p]);
+                    }
+                    arrive(B_BFREE + part);
+                    s += __shfl_xor_sync(~0u, s, 1);
+                    z += __shfl_xor_sync(~0u, z, 1);
+                    if (hc == 0) {
+                        dwv[part * C + r] = s;
+                        dwr[part * C + r] = z;
+                    }
                 }
                 tc_warp_wait(bar + B_DO, par, dead, d.spin);
                 if (x.nt < C) clear_rows(smem + L::G, x.nt);
                 fence_proxy_async_smem();
                 arrive(B_PL);
-                // this quarter's box of a state: 32 columns of the lane's row; phase 3 unit + j of its slot
-                const unsigned char *box = smem + L::S + part * L::BOX;
+                // boxes of the states: 32 columns of the lane's row
                 auto piece = [&](int c) { return *reinterpret_cast<const float4 *>(box + tc_at(lane0 + lane, c)); };
                 auto planes = [&](auto count, uint32_t dst, const float4 (&y)[8]) {
                     constexpr int N = decltype(count)::value;
@@ -236,14 +242,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 {
                     float4 y[8];
-                    tc_warp_wait(bar + B_BOX + part, par, dead, d.spin);
+                    tc_warp_wait(bar + B_BOX + part, 1, dead, d.spin);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) y[c] = piece(c);
                     arrive(B_BFREE + part);
                     planes(std::integral_constant<int, 2>{}, at + L::DP, y);
                     arrive(B_D1);
                     float s = 0.f;
-                    tc_warp_wait(bar + B_BOX + part, par ^ 1, dead, d.spin);
+                    tc_warp_wait(bar + B_BOX + part, 0, dead, d.spin);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const float4 z = piece(c);
@@ -269,12 +275,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float zr = 0.f;
                         unsigned pl[8][2];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int s = 16 * part + e;
-                            const float f = s <= t ? expf((ht - hi[s]) + (lt - lo[s])) * be[s] : 0.f;
-                            const float w = ft * f * (is_p ? y[e] : y[e] + z[e]);
-                            y[e] = s < t || (is_p && s == t) ? w : 0.f;
-                            if (is_p) zr = s <= t ? fmaf(y[e], z[e], zr) : zr;
+                        for (int e = 0; e < 16; e += 4) {
+                            float hs[4], ls[4], bs[4];
+                            *reinterpret_cast<float4 *>(hs) = *reinterpret_cast<const float4 *>(hi + 16 * part + e);
+                            *reinterpret_cast<float4 *>(ls) = *reinterpret_cast<const float4 *>(lo + 16 * part + e);
+                            *reinterpret_cast<float4 *>(bs) = *reinterpret_cast<const float4 *>(be + 16 * part + e);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const int s = 16 * part + e + m;
+                                const float f = s <= t ? expf((ht - hs[m]) + (lt - ls[m])) * bs[m] : 0.f;
+                                const float w = ft * f * (is_p ? y[e + m] : y[e + m] + z[e + m]);
+                                y[e + m] = s < t || (is_p && s == t) ? w : 0.f;
+                                zr = fmaf(y[e + m], z[e + m], zr);     // of p, with q k^T
+                            }
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) split_bf16<2>(y[2 * e], y[2 * e + 1], pl[e]);
@@ -292,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 {
                     float4 y[8];
-                    tc_warp_wait(bar + B_BOX + part, par, dead, d.spin);
+                    tc_warp_wait(bar + B_BOX + part, 1, dead, d.spin);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) y[c] = piece(c);
                     arrive(B_BFREE + part);
@@ -363,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (16 * p <= r) z += zrow[p * C + r];
                             z += dots[p * C + r];
                         }
-                        rev += (double)z - (double)be[r] * (double)dwv[r];
+                        rev += (double)z - (double)be[r] * (double)((dwv[r] + dwv[C + r]) + (dwv[2 * C + r] + dwv[3 * C + r]));
                         suf[e] = rev;
                     }
                     double after = rev;
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int r = 2 * lane + e;
                         if (r < rows) {
                             o.grad_decay[(tok + r) * d.H + h] = r < x.nt ? (float)(after + suf[e]) : 0.f;
-                            o.grad_beta[(tok + r) * d.H + h] = r < x.nt ? dwr[r] : 0.f;
+                            o.grad_beta[(tok + r) * d.H + h] = r < x.nt ? (dwr[r] + dwr[C + r]) + (dwr[2 * C + r] + dwr[3 * C + r]) : 0.f;
                         }
                     }
                 }
@@ -460,6 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 states(L::G3, L::DP, rk + 2 * L::TILE / 16, L::TILE, false);
                 states(L::G3, L::DP, rk, L::TILE, false);
                 tc_commit_to(one, bar + B_G3);
+                ok = tc_warp_wait(bar + B_S0, par, dead, d.spin);
+                if (!ok) break;
+                tc_fence_after();
+                states(L::G1, L::SP + 128, gk, L::PAIR, true);
+                states(L::G1, L::SP + 64, gk, L::PAIR, false);
+                states(L::G1, L::SP, gk, L::PAIR, false);
+                states(L::G2, L::SP + 64, wg, L::PAIR, true);
+                states(L::G2, L::SP, w1, L::TILE, false);
+                states(L::G2, L::SP, wg, L::PAIR, false);
                 ok = tc_warp_wait(bar + B_PA, par, dead, d.spin) && tc_warp_wait(bar + B_G3, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
@@ -483,15 +505,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_mma_ss(one, tu + L::DK + 16 * ks, km + 2048 * ks / 16, ak + (p * L::TILE + 16 * ks * 128 + 32 * ks) / 16,
                                   tc_idesc<false, true>(C - 16 * ks), true);
                 }
-                ok = tc_warp_wait(bar + B_S0, par, dead, d.spin);
-                if (!ok) break;
-                tc_fence_after();
-                states(L::G1, L::SP + 128, gk, L::PAIR, true);
-                states(L::G1, L::SP + 64, gk, L::PAIR, false);
-                states(L::G1, L::SP, gk, L::PAIR, false);
-                states(L::G2, L::SP + 64, wg, L::PAIR, true);
-                states(L::G2, L::SP, w1, L::TILE, false);
-                states(L::G2, L::SP, wg, L::PAIR, false);
                 tc_commit_to(one, bar + B_G);
                 tc_commit_to(one, bar + B_DOFREE);
                 if (hh + 1 == group) tc_commit_to(one, bar + B_TFREE);
@@ -510,23 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int hh = 0; hh < group && ok; ++hh, ++unit) {
                 const int h = x.hk * group + hh;
                 const long long bh = (long long)x.b * d.H + h, chunk = bh * d.Nt + x.n;
-                if (lane == 0) {
-                    const unsigned vals = (unsigned)(C * d.Dv * 4), cells = (unsigned)(d.Dk * d.Dv * 4);
-                    prefetch_l2(o.w + chunk * C * d.Dv, vals);
-                    prefetch_l2(o.r + chunk * C * d.Dv, vals);
-                    prefetch_l2(o.ends + chunk * d.Dk * d.Dv, cells);
-                    prefetch_l2(o.snap + (bh * (d.Nt + 1) + x.n) * d.Dk * d.Dv, cells);
-                }
-                __syncwarp();
-                // the slots free up in the middle of the head before: D1's boxes first
-                for (int e = 0; e < 12 && ok; ++e) {
-                    const int s = e & 3;
-                    if (unit > 0 || e >= 4) ok = tc_warp_wait(bar + B_BFREE + s, (3 * unit + e / 4 - 1) & 1, dead, d.spin);
+                // the slots free up in the middle of the head before: the next one's dw and r first
+                for (int e = 0; e < 16 && ok; ++e) {
+                    const int s = e & 3, j = e >> 2;
+                    if (unit > 0 || j > 0) ok = tc_warp_wait(bar + B_BFREE + s, (j + 1) & 1, dead, d.spin);
                     if (!ok) break;
                     if (lane == 0) {
+                        unsigned char *dst = smem + L::S + s * L::BOX;
                         mbar_arrive_expect_tx(bar + B_BOX + s, L::BOX);
-                        state_load(smem + L::S + s * L::BOX, e < 4 ? &md : &ms, 32 * s,
-                                   (int)(e < 4 ? chunk : bh * (d.Nt + 1) + x.n + (e < 8 ? 1 : 0)), bar + B_BOX + s);
+                        if (j == 0) {
+                            state_load(dst, &mw, 32 * s, (int)chunk, bar + B_BOX + s);
+                            state_load(dst + L::BOX / 2, &mr, 32 * s, (int)chunk, bar + B_BOX + s);
+                        } else {
+                            state_load(dst, j == 1 ? &md : &ms, 32 * s,
+                                       (int)(j == 1 ? chunk : bh * (d.Nt + 1) + x.n + (j == 2 ? 1 : 0)), bar + B_BOX + s);
+                        }
                     }
                     __syncwarp();
                     ++boxes;
@@ -581,19 +592,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 cudaError_t launch_delta_back_local_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, const DeltaBack &o,
                                        cudaStream_t st) {
     const long long ks[3] = {(long long)d.T * d.Hk * d.Dk, (long long)d.Hk * d.Dk, d.Dk};
-    CUtensorMap mq, mk, mg, ms, md, mdq, mdk;
+    CUtensorMap mq, mk, mg, ms, md, mw, mr, mdq, mdk;
     cudaError_t e = tc_tensor_map(&mq, in.q, d.qs, d.B, d.T, d.Hk, d.Dk);
     if (e == cudaSuccess) e = tc_tensor_map(&mk, in.k, d.ks, d.B, d.T, d.Hk, d.Dk);
     if (e == cudaSuccess) e = tc_tensor_map(&mg, o.grad, d.os, d.B, d.T, d.H, d.Dv);
     if (e == cudaSuccess) e = tc_tensor_map(&mdq, o.grad_q, ks, d.B, d.T, d.Hk, d.Dk);
     if (e == cudaSuccess) e = tc_tensor_map(&mdk, o.grad_k, ks, d.B, d.T, d.Hk, d.Dk);
-    if (e == cudaSuccess) e = tc_state_map(&ms, o.snap, (long long)d.B * d.H * (d.Nt + 1), d.Dk, d.Dv);
-    if (e == cudaSuccess) e = tc_state_map(&md, o.ends, (long long)d.B * d.H * d.Nt, d.Dk, d.Dv);
+    if (e == cudaSuccess) e = tc_state_map(&ms, o.snap, (long long)d.B * d.H * (d.Nt + 1), d.Dk, d.Dv, 128);
+    if (e == cudaSuccess) e = tc_state_map(&md, o.ends, (long long)d.B * d.H * d.Nt, d.Dk, d.Dv, 128);
+    if (e == cudaSuccess) e = tc_state_map(&mw, o.w, (long long)d.B * d.H * d.Nt, kC, d.Dv, kC);
+    if (e == cudaSuccess) e = tc_state_map(&mr, o.r, (long long)d.B * d.H * d.Nt, kC, d.Dv, kC);
     if (e != cudaSuccess) return e;
     set_kernel_smem(k_delta_back_local_tc, BackLocalTc::BYTES);
     const long long items = (long long)d.B * d.Hk * d.Nt;
     k_delta_back_local_tc<<<(unsigned)(items < kRefSms ? items : kRefSms), kThreads, BackLocalTc::BYTES, st>>>(
-        mq, mk, mg, ms, md, mdq, mdk, d, in, w, o);
+        mq, mk, mg, ms, md, mw, mr, mdq, mdk, d, in, w, o);
     return cudaGetLastError();
 }
 

@@ -442,10 +442,10 @@ cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *s, int
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dim, str, box);
 }
 
-cudaError_t tc_state_map(CUtensorMap *m, const void *p, long long slots, int Dk, int Dv) {
-    const cuuint64_t dim[3] = {(cuuint64_t)Dv, (cuuint64_t)Dk, (cuuint64_t)slots};
-    const cuuint64_t str[2] = {(cuuint64_t)Dv * 4, (cuuint64_t)Dk * Dv * 4};
-    const cuuint32_t box[3] = {32, 128, 1};
+cudaError_t tc_state_map(CUtensorMap *m, const void *p, long long slots, int rows, int columns, int box_rows) {
+    const cuuint64_t dim[3] = {(cuuint64_t)columns, (cuuint64_t)rows, (cuuint64_t)slots};
+    const cuuint64_t str[2] = {(cuuint64_t)columns * 4, (cuuint64_t)rows * columns * 4};
+    const cuuint32_t box[3] = {32, (cuuint32_t)box_rows, 1};
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dim, str, box);
 }
 

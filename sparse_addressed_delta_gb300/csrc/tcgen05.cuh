@@ -126,8 +126,8 @@ __device__ __forceinline__ void tc_store_planes(uint32_t hi, uint32_t mid, uint3
 // Tensor copies of 64 tokens x 64 columns of one head of a [B, T, heads, D] bfloat16 tensor, between
 // global memory and a tile as tc_at lays it out. Loads are 0, stores are left out, past T and D.
 cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *strides, int B, int T, int heads, int D);
-// boxes of 32 columns x 128 rows of float32 [slots, Dk, Dv] states (0 past Dk and Dv)
-cudaError_t tc_state_map(CUtensorMap *m, const void *p, long long slots, int Dk, int Dv);
+// boxes of 32 columns x `box` rows of float32 [slots, rows, columns] (0 past the rows and columns)
+cudaError_t tc_state_map(CUtensorMap *m, const void *p, long long slots, int rows, int columns, int box);
 // whether such a map can describe the tensor (a broadcast dimension has no stride to give)
 inline bool tc_tensor_fits(const long long *s, int B, int T, int heads) {
     const int n[3] = {B, T, heads};
