@@ -157,11 +157,23 @@ __device__ __forceinline__ void stsm4t(unsigned addr, const unsigned (&r)[4]) {
                  : "memory");
 }
 
+__device__ __forceinline__ bool mbar_test_wait(unsigned long long *bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits for a phase of `bar`, at most `limit` polls; gives up at once when another thread of the
 // block has. Returns whether the phase completed.
 __device__ __forceinline__ bool tc_wait(unsigned long long *bar, unsigned parity, volatile int *dead,
                                         long long limit) {
-    for (long long i = 0; i < limit; ++i) {
+    // one look first: a try_wait may wait by itself, and a limit of one poll is to give up at once
+    if (mbar_test_wait(bar, parity)) return true;
+    for (long long i = 1; i < limit; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*dead) return false;
     }
