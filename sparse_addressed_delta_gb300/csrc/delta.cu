@@ -1,10 +1,40 @@
 // C ABI of the gated delta rule (declared and documented in include/sdm.h): argument checks and the
 // launch sequence. Everything is queued on the caller's stream; nothing is allocated and nothing
 // synchronizes.
+#include <algorithm>
+
 #include "tcgen05.cuh"
 
 namespace sdm {
 namespace {
+
+// How many segments a sequence's scan takes (DeltaBlock in delta_internal.cuh): two launches and a join,
+// which pay when the heads alone leave SMs idle. By the times in microseconds measured for 128 x 128
+// states: a chunk alone and beside twice as many blocks, a chunk of the first launch, a block's start, the
+// join and each of its steps. Measured, whole call, in segments and not: 32 heads x 256 chunks 588 and 913 us,
+// 16 x 64 137 and 234, 4 x 64 111 and 213; 64 heads x 64 chunks 330 and 305, so not taken. A saving forward
+// takes the same segments, so that its results are the same.
+void delta_split(DeltaDims &d) {
+    constexpr double kAlone = 2.6, kBeside = 3.0, kCarry = 2.3, kStart = 8.0, kJoin = 8.0, kJoinStep = 4.0;
+    d.segs = d.first = 1;
+    if (!d.tc) return;
+    const long long heads = (long long)d.B * d.H, blocks = heads * delta_tiles(d);
+    const double startup = kStart / kBeside;                 // in chunks
+    double best = (kAlone * d.Nt + kStart) * ((blocks + kRefSms - 1) / kRefSms);
+    for (int s = 3; s <= d.Nt; ++s) {
+        const long long busy = std::max((s - 2) * (blocks + heads), (s - 1) * blocks);
+        if (busy >= kRefSms) break;                          // segment 0 needs SMs beside the others
+        // `rounds` blocks of segment 0 one after another take as long as one of the others
+        const double rounds = (double)((blocks + kRefSms - busy - 1) / (kRefSms - busy));
+        const double longer = std::min((d.Nt + startup * (1.0 - 1.0 / rounds)) / (s - 1 + 1.0 / rounds), d.Nt / (s - 1.0));
+        const double time = (kCarry + kBeside) * longer + 2 * kStart + kJoin + kJoinStep * (s - 2);
+        if (time < best) {
+            best = time;
+            d.segs = s;
+            d.first = (int)(256.0 * (d.Nt - (s - 1) * longer) / longer);
+        }
+    }
+}
 
 // Checks the shape; fills d. Returns SDM_OK or a refusal (message set).
 int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
@@ -30,6 +60,7 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.C = delta_chunk(s->dtype);
     d.pp = s->dtype == SDM_BF16 ? 2 : 3;
     d.back = 0;
+    d.segs = d.first = 1;
     d.spin = wait_limit();
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
@@ -70,6 +101,7 @@ bool by_token(const DeltaDims &d) { return d.T <= kDeltaStepTokens; }
 // Where the chunk form's buffers lie in a workspace; `bytes` is their end.
 struct DeltaLayout {
     size_t q, k, x, p, aux;              // q, k: the planes of float32 inputs
+    size_t starts, units;                // the segments'
     size_t ends, w, dq, dk;              // the backward's
     size_t bytes;
 };
@@ -88,6 +120,8 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     l.x = take(delta_chunks(d) * 3 * delta_plane_bytes(d));
     l.p = take(delta_chunks(d) * d.pp * delta_plane_bytes(d));
     l.aux = take(delta_chunks(d) * kDeltaAux * d.C * 4);
+    l.starts = take(d.segs > 1 ? d.segs * (size_t)delta_states(d) * 4 : 0);
+    l.units = take(d.segs > 1 ? (d.segs - 2) * (size_t)d.B * d.H * d.Dk * d.Dk * 4 : 0);
     if (backward) {
         l.ends = take(delta_chunks(d) * d.Dk * d.Dv * 4);
         l.w = take(delta_chunks(d) * d.C * d.Dv * 4);
@@ -128,7 +162,8 @@ cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaLayout
                         DeltaPlanes &q, DeltaPlanes &k, DeltaLocal &w, cudaStream_t st) {
     q = delta_planes(d, in.q, d.qs, ws + l.q);
     k = delta_planes(d, in.k, d.ks, ws + l.k);
-    w = DeltaLocal{ws + l.x, ws + l.p, reinterpret_cast<float *>(ws + l.aux), reinterpret_cast<DevStatus *>(ws)};
+    w = DeltaLocal{ws + l.x, ws + l.p, reinterpret_cast<float *>(ws + l.aux), reinterpret_cast<DevStatus *>(ws),
+                   reinterpret_cast<float *>(ws + l.starts), reinterpret_cast<float *>(ws + l.units)};
     if (d.dtype == SDM_F32) {
         cudaError_t e = launch_delta_split(d, in.q, d.qs, d.Hk, d.Dk, const_cast<__nv_bfloat16 *>(q.p), st);
         if (e == cudaSuccess)
@@ -169,6 +204,7 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
     if (!save && by_token(d)) return delta_status(launch_delta_step(d, in, state, readings, st));
+    delta_split(d);
     const DeltaLayout l = delta_layout(d, false);
     rc = delta_check_ws("workspace", workspace, workspace_bytes, l.bytes);
     if (rc == SDM_OK && save) rc = delta_check_ws("saved buffer", saved, saved_bytes, delta_saved(d));
@@ -191,6 +227,7 @@ extern "C" {
 size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
     if (delta_check(shape, d) != SDM_OK) return 0;
+    delta_split(d);
     return delta_layout(d, false).bytes + kAlign;
 }
 

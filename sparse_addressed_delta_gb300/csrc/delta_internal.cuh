@@ -20,6 +20,7 @@ struct DeltaDims {
     int back;                            // 1: the chunk-local work of a backward
     int dtype;
     int tc;                              // 1: the scans run on tcgen05 (planes of X and P in its layout)
+    int segs, first;                     // the sequence's segments, scanned at once (DeltaBlock)
     float scale;
     long long spin;                      // polls before a kernel's wait gives up (sdm_set_wait_limit)
     long long qs[3], ks[3], vs[3], gs[3], bs[3], os[3];   // element strides of (b, t, h)
@@ -52,9 +53,46 @@ struct DeltaLocal {
     unsigned char *x, *p;
     float *aux;
     DevStatus *status;
-};
+    float *starts, *units;               // with segments: their first states [segs][B, H, Dk, Dv], and
+};                                       // what the inner ones make of a unit matrix [segs - 2][B, H, Dk, Dk]
 
 __host__ __device__ constexpr int delta_chunk(int dtype) { return dtype == SDM_BF16 ? 64 : 32; }
+
+// A sequence in segments (d.segs > 1), for the tcgen05 scan. A segment's end state is linear in its first
+// state, M S + E. A first launch takes every segment but the last from a state of zeros (the first one
+// from the caller's, so it needs no M) to E, and the inner ones' M from a unit matrix with no values; a
+// join makes the first states from these; a second launch runs all segments at once. Segment 0's blocks
+// come last, several after one another where SMs are free; it is first / 256 as long as the others.
+__host__ __device__ inline long long delta_states(const DeltaDims &d) { return (long long)d.B * d.H * d.Dk * d.Dv; }
+__host__ __device__ inline int delta_tiles(const DeltaDims &d) { return (d.Dv + 127) / 128; }
+// first chunk of segment i of a sequence of `chunks`
+__host__ __device__ inline int delta_bound(const DeltaDims &d, int chunks, int i) {
+    return i == 0 ? 0 : (int)((long long)chunks * (d.first + (i - 1) * 256) / ((d.segs - 1) * 256 + d.first));
+}
+
+struct DeltaBlock {
+    int seg, tile;
+    bool unit;
+    long long bh;
+};
+template <bool SEG, bool CARRY>
+__device__ __forceinline__ DeltaBlock delta_block(const DeltaDims &d) {
+    DeltaBlock k;
+    const int tiles = delta_tiles(d), heads = d.B * d.H;
+    // the first launch: per inner segment and head, the state's tiles and a unit matrix
+    const int per = CARRY ? tiles + 1 : tiles, inner = !SEG ? 0 : CARRY ? d.segs - 2 : d.segs - 1;
+    unsigned i = blockIdx.x;
+    const bool first = !SEG || i >= (unsigned)(inner * heads * per);
+    if (first) i -= inner * heads * per;
+    const int of = first ? tiles : per;
+    k.tile = (int)(i % of);
+    i /= of;
+    k.bh = SEG ? i % heads : i;
+    k.seg = first ? 0 : 1 + (int)(i / heads);
+    k.unit = CARRY && !first && k.tile == tiles;
+    if (k.unit) k.tile = 0;
+    return k;
+}
 
 inline size_t delta_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 inline size_t delta_chunks(const DeltaDims &d) { return (size_t)d.B * d.H * d.Nt; }

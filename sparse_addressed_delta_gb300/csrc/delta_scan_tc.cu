@@ -51,23 +51,33 @@ enum {
     B_READ = 20, B_O1, B_O2, B_DRAIN, B_BULK, B_COUNT = B_BULK + 2
 };
 
-template <int DKP, bool SAVE>
+enum { SCAN_READ, SCAN_SAVE, SCAN_CARRY };
+
+// SCAN_SAVE: also what a backward needs. SCAN_CARRY: the segments' end states only (DeltaBlock). SEG: the
+// sequences are in segments; a form of its own, for its registers (one form for both spilled: a call with 8
+// sequences of up to 4096 tokens, 32 heads, took 600 us where it takes 575).
+template <int DKP, int MODE, bool SEG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_delta_scan_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, DeltaDims d,
                     DeltaIn in, DeltaLocal w, float *state, __nv_bfloat16 *o, float *snap, float *rsave) {
     using L = TcScan<DKP>;
     constexpr int C = kTcC, HD = DKP / 4;                          // columns of S a thread
+    constexpr bool SAVE = MODE == SCAN_SAVE, CARRY = MODE == SCAN_CARRY;
+    constexpr int UPD = CARRY ? (DKP == 128 ? L::R : L::OA) : L::UP, UPD1 = CARRY ? L::OA : L::UP + 64;   // the update's halves
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     auto bar = reinterpret_cast<unsigned long long *>(smem + L::BARS);
     volatile int *dead = reinterpret_cast<int *>(bar + B_COUNT);
     auto slot = reinterpret_cast<uint32_t *>(bar + B_COUNT + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tiles = (d.Dv + 127) / 128, dv_blk = (blockIdx.x % tiles) * 128;
-    const long long bh = blockIdx.x / tiles;
+    const DeltaBlock blk = delta_block<SEG, CARRY>(d);
+    const int dv_blk = blk.tile * 128, seg = blk.seg, width = CARRY && blk.unit ? d.Dk : d.Dv;
+    const long long bh = blk.bh;
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
-    const int ntok = delta_valid(in.valid, b, d.T), nch = (ntok + C - 1) / C;
+    const int ntok = delta_valid(in.valid, b, d.T), chunks = (ntok + C - 1) / C;
+    const int n0 = SEG ? delta_bound(d, chunks, seg) : 0, nch = SEG ? delta_bound(d, chunks, seg + 1) - n0 : chunks;
+    const bool last = !SEG || seg + 1 == d.segs;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -78,7 +88,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = B_S; i < B_R; ++i) mbar_init(bar + i, kTcWarps / 2);
         for (int i = B_R; i < B_COUNT; ++i) mbar_init(bar + i, i == B_READ ? kTcWarps : 1);
-        *dead = 0;
+        *dead = SEG && !CARRY && w.status->code != 0;              // an earlier kernel of this call gave up
         fence_mbar_init();
     }
     if (warp == kTcWarps) {
@@ -93,21 +103,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp < kTcWarps) {
         // ---- the lanes' threads
         const int part = warp >> 2, half = part >> 1, lane0 = 32 * (warp & 3), dv = dv_blk + lane0 + lane;
-        const bool mine = dv < d.Dv;
+        const bool mine = dv < width;
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
         const int dk0 = part * HD;
         float S[HD];
         {
-            const float *sp = state + (bh * d.Dk + dk0) * d.Dv + dv;
+            const bool real = !CARRY || seg == 0;
+            const float *sp = (SEG && !CARRY ? w.starts + seg * delta_states(d) : state) + (bh * d.Dk + dk0) * d.Dv + dv;
 #pragma unroll
-            for (int i = 0; i < HD; ++i) S[i] = mine && dk0 + i < d.Dk ? sp[(size_t)i * d.Dv] : 0.f;
+            for (int i = 0; i < HD; ++i) S[i] = real && mine && dk0 + i < d.Dk ? sp[(size_t)i * d.Dv] : blk.unit && dk0 + i == dv ? 1.f : 0.f;
         }
         // columns [i0, i1) of S as rows of a [Dk, Dv] state
         auto keep_state = [&](float *dst, int i0, int i1) {
-            dst += (size_t)dk0 * d.Dv + dv;
+            dst += (dk0 + i0) * width + dv;
 #pragma unroll
-            for (int i = 0; i < HD; ++i)
-                if (i >= i0 && i < i1 && mine && dk0 + i < d.Dk) dst[(size_t)i * d.Dv] = S[i];
+            for (int c = 0; c < HD; c += 16) {                     // Dk is a multiple of 16
+                if (c < i0 || c >= i1 || !mine || dk0 + c >= d.Dk) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tc_put(dst, S[c + i], width);
+            }
         };
         auto planes_of_s = [&] {
 #pragma unroll
@@ -132,10 +146,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the readings' 8 x 8 blocks in the row buffer: block b of a store is 8 columns of dv (b % 2) and
         // 8 tokens (b / 2), a lane's row one token
         const int orow = 16 * part + 8 * (lane >> 4) + (lane & 7), ocol = (lane0 >> 3) + ((lane >> 3) & 1);
-        for (int n = 0; n < nch; ++n) {
-            const unsigned par = n & 1;
+        for (int it = 0; it < nch; ++it) {
+            const unsigned par = it & 1;
+            const int n = n0 + it;
             float *keep = snap + ((bh * (d.Nt + 1) + n) * (long long)d.Dk) * d.Dv;
-            if (!tc_warp_wait(bar + B_FULL + par, (n >> 1) & 1, dead, d.spin)) break;
+            if (!tc_warp_wait(bar + B_FULL + par, (it >> 1) & 1, dead, d.spin)) break;
             const float *aux = reinterpret_cast<const float *>(smem + L::AUX + 512 * par);
             const float *from = aux + 16 * part, *to = aux + C + 16 * part;
             const float whole = aux[C - 1];
@@ -155,10 +170,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!tc_warp_wait(bar + B_UACC + half, par, dead, d.spin)) break;
             tc_fence_after();
             tc_load16(at + L::U + 16 * part, x);
-            float *rdst = rsave + ((bh * d.Nt + n) * (long long)C + 16 * part) * d.Dv + dv;
             if (SAVE && mine) {
+                float *dst = rsave + ((bh * d.Nt + n) * (long long)C + 16 * part) * d.Dv + dv;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) rdst[(size_t)i * d.Dv] = x[i];
+                for (int i = 0; i < 16; ++i) tc_put(dst, x[i], d.Dv);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] *= to[i];
@@ -170,47 +185,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             arrive(B_U + half);
             if (SAVE) keep_state(keep, HD / 2, HD);
             // the readings, in a buffer that warp 18 stores; 0 past the valid tokens
-            if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;
-            if (!tc_warp_wait(bar + B_O1, par, dead, d.spin)) break;
-            if (n >= 2 && !tc_warp_wait(bar + B_OFREE + par, ((n >> 1) - 1) & 1, dead, d.spin)) break;
-            tc_fence_after();
+            if constexpr (!CARRY) {
+                if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;
+                if (!tc_warp_wait(bar + B_O1, par, dead, d.spin)) break;
+                if (it >= 2 && !tc_warp_wait(bar + B_OFREE + par, ((it >> 1) - 1) & 1, dead, d.spin)) break;
+                tc_fence_after();
 #pragma unroll
-            for (int l = 0; l < 2; ++l) {                          // 16 lanes of dv
-                float y[8], z[8];
-                tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::R + 16 * part, at + ((uint32_t)(16 * l) << 16) + L::OA + 16 * part, y, z);
-                unsigned r[4];
+                for (int l = 0; l < 2; ++l) {                          // 16 lanes of dv
+                    float y[8], z[8];
+                    tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::R + 16 * part, at + ((uint32_t)(16 * l) << 16) + L::OA + 16 * part, y, z);
+                    unsigned r[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int t = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
-                    z[i] = n * C + 16 * part + t < ntok ? fmaf(d.scale * from[t], y[i], z[i]) : 0.f;
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                        z[i] = n * C + 16 * part + t < ntok ? fmaf(d.scale * from[t], y[i], z[i]) : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[2 * i], z[2 * i + 1]);
+                    const int c = ocol + 2 * l;
+                    stsm4t(smem_u32(smem) + L::O + (2 * par + (c >> 3)) * L::TILE + tc_at(orow, c & 7), r);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[2 * i], z[2 * i + 1]);
-                const int c = ocol + 2 * l;
-                stsm4t(smem_u32(smem) + L::O + (2 * par + (c >> 3)) * L::TILE + tc_at(orow, c & 7), r);
+                fence_proxy_async_smem();
+                arrive(B_READ);
+                if (lane == 0) mbar_arrive(bar + B_OUT + par);
             }
-            fence_proxy_async_smem();
-            arrive(B_READ);
-            if (lane == 0) mbar_arrive(bar + B_OUT + par);
             if (!tc_warp_wait(bar + B_UPD + half, par, dead, d.spin)) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
-                tc_load16(at + L::UP + dk0 + c, x);
+                tc_load16(at + (half == 0 || DKP == 64 ? UPD + dk0 : UPD1 + dk0 - 64) + c, x);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[c + i] = fmaf(whole, S[c + i], x[i]);
             }
-            if (n + 1 < nch) planes_of_s();
+            if (it + 1 < nch) planes_of_s();
             arrive(B_S + half);
             if (lane == 0) mbar_arrive(bar + B_EMPTY + par);
         }
-        if (nch > 0 && !*dead) keep_state(state + bh * d.Dk * (long long)d.Dv, 0, HD);
-        if (SAVE) keep_state(snap + ((bh * (d.Nt + 1) + nch) * (long long)d.Dk) * d.Dv, 0, HD);
+        if (CARRY)
+            keep_state(blk.unit ? w.units + ((seg - 1) * (long long)d.B * d.H + bh) * d.Dk * d.Dk
+                                : w.starts + (seg + 1) * delta_states(d) + bh * d.Dk * (long long)d.Dv, 0, HD);
+        else if (last && nch > 0 && !*dead)
+            keep_state(state + bh * d.Dk * (long long)d.Dv, 0, HD);
+        if (SAVE && last) keep_state(snap + ((bh * (d.Nt + 1) + chunks) * (long long)d.Dk) * d.Dv, 0, HD);
     } else if (warp == kTcWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
-        for (int n = 0; n < nch; ++n) {
-            const unsigned par = n & 1;
+        for (int it = 0; it < nch; ++it) {
+            const unsigned par = it & 1;
             const uint32_t st = base + par * L::STAGE;
             // a descriptor's address counts 16 bytes
             const uint32_t kd = tc_k_major(st + L::K), qd = tc_k_major(st + L::Q), xd = tc_k_major(st + L::X),
@@ -229,11 +250,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                           tc_idesc<false>(tokens), add);
             };
             auto update = [&](int ks, int hd, int p, bool add) {   // half hd of Dk, or (Dk 64) all of it at once
-                tc_mma_ts(one, tu + L::UP + 64 * hd, tu + (p < 2 ? L::U + 16 * ks + 8 * p : L::LO + 8 * ks),
+                tc_mma_ts(one, tu + (hd ? UPD1 : UPD), tu + (p < 2 ? L::U + 16 * ks + 8 * p : L::LO + 8 * ks),
                           kn + (2048 * ks + hd * L::TILE) / 16, tc_idesc<true>(DKP == 128 ? 64 : DKP), add);
             };
-            if (!tc_warp_wait(bar + B_FULL + par, (n >> 1) & 1, dead, d.spin)) break;
-            if (n > 0 && !tc_warp_wait(bar + B_READ, par ^ 1, dead, d.spin)) break;
+            if (!tc_warp_wait(bar + B_FULL + par, (it >> 1) & 1, dead, d.spin)) break;
+            if (!CARRY && it > 0 && !tc_warp_wait(bar + B_READ, par ^ 1, dead, d.spin)) break;
             if (!tc_warp_wait(bar + B_S, par, dead, d.spin)) break;
             tc_fence_after();
             constexpr int KS = DKP / 16;
@@ -256,10 +277,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int p = 2; p >= 1; --p)
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks) tri_v(L::U, xd + p * L::TILE / 16, ks, p < 2 || ks > 0);
+            if constexpr (!CARRY) {
 #pragma unroll
-            for (int p = 1; p >= 0; --p)
+                for (int p = 1; p >= 0; --p)
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks) tri_v(L::OA, zd + p * L::TILE / 16, ks, p < 1 || ks > 0);
+                    for (int ks = 0; ks < C / 16; ++ks) tri_v(L::OA, zd + p * L::TILE / 16, ks, p < 1 || ks > 0);
+            }
             bool ok = true;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -278,19 +301,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_commit_to(one, bar + B_UACC + hf);
             }
             if (!ok) break;
+            if constexpr (!CARRY) {
 #pragma unroll
-            for (int a = 1; a >= 0; --a)
+                for (int a = 1; a >= 0; --a)
 #pragma unroll
-                for (int p = 1 - a; p >= 0; --p)
+                    for (int p = 1 - a; p >= 0; --p)
 #pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks) tri(L::OA, L::UP + a * (C / 2), zd + p * L::TILE / 16, ks);
-            tc_commit_to(one, bar + B_O2);
+                        for (int ks = 0; ks < C / 16; ++ks) tri(L::OA, L::UP + a * (C / 2), zd + p * L::TILE / 16, ks);
+                tc_commit_to(one, bar + B_O2);
 #pragma unroll
-            for (int p = 1; p >= 0; --p)                           // R is used: S^T Q^T in its place
+                for (int p = 1; p >= 0; --p)                           // R is used: S^T Q^T in its place
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) rows(L::R, qd, 0, C, p, ks, p < 1 || ks > 0);
-            tc_commit_to(one, bar + B_O1);
-            if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;      // w's planes make room for the update
+                    for (int ks = 0; ks < KS; ++ks) rows(L::R, qd, 0, C, p, ks, p < 1 || ks > 0);
+                tc_commit_to(one, bar + B_O1);
+                if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;      // w's planes make room for the update
+            }
             if (!tc_warp_wait(bar + B_U, par, dead, d.spin)) break;
             tc_fence_after();
 #pragma unroll
@@ -319,26 +344,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else if (warp == kTcWarps + 1) {
         // ---- the chunks' inputs
-        for (int n = 0; n < nch; ++n) {
-            const int s = n & 1, t0 = n * C, nt = ntok - t0 < C ? ntok - t0 : C;
+        if (blk.unit) {                                            // no values
+            for (int i = lane; i < 2 * 2 * L::TILE / 16; i += 32)
+                *reinterpret_cast<uint4 *>(smem + (i / (2 * L::TILE / 16)) * L::STAGE + L::V + i % (2 * L::TILE / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+        }
+        const uint32_t bytes = 2 * C * 4 + (!CARRY ? L::STAGE : DKP / 64 * L::TILE + 3 * L::TILE + (blk.unit ? 0 : 2 * L::TILE));
+        for (int it = 0; it < nch; ++it) {
+            const int n = n0 + it, s = it & 1, t0 = n * C, nt = ntok - t0 < C ? ntok - t0 : C;
             unsigned char *st = smem + s * L::STAGE;
             const long long bhn = bh * d.Nt + n;
             unsigned long long *full = bar + B_BULK + s;
-            if (n >= 2 && !tc_warp_wait(bar + B_EMPTY + s, ((n >> 1) - 1) & 1, dead, d.spin)) break;
+            if (it >= 2 && !tc_warp_wait(bar + B_EMPTY + s, ((it >> 1) - 1) & 1, dead, d.spin)) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(full, L::STAGE + 2 * C * 4);
+                mbar_arrive_expect_tx(full, bytes);
                 for (int c = 0; c < DKP / 64; ++c) {
                     tc_tensor_load(st + L::K + c * L::TILE, &mk, 64 * c, hk, t0, b, full);
-                    tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, hk, t0, b, full);
+                    if (!CARRY) tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, hk, t0, b, full);
                 }
-                for (int c = 0; c < 2; ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, h, t0, b, full);
+                for (int c = 0; c < (blk.unit ? 0 : 2); ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, h, t0, b, full);
                 bulk_g2s(st + L::X, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
-                bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, full);
+                if (!CARRY) bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, full);
                 bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * kDeltaAux * C, 2 * C * 4, full);
             }
             __syncwarp();
-            if (!tc_warp_wait(full, (n >> 1) & 1, dead, d.spin)) {
-                mbar_wait_bounded(full, (n >> 1) & 1);             // nothing in flight behind a give-up
+            if (!tc_warp_wait(full, (it >> 1) & 1, dead, d.spin)) {
+                mbar_wait_bounded(full, (it >> 1) & 1);             // nothing in flight behind a give-up
                 break;
             }
             if (nt < C) {                                          // what lies past the valid tokens is not used
@@ -355,24 +386,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             mbar_arrive(bar + B_FULL + s);
         }
-    } else {
+    } else if (!CARRY) {
         // ---- the readings
-        for (int n = 0; n < nch; ++n) {
-            if (!tc_warp_wait(bar + B_OUT + (n & 1), (n >> 1) & 1, dead, d.spin)) break;
+        for (int it = 0; it < nch; ++it) {
+            if (!tc_warp_wait(bar + B_OUT + (it & 1), (it >> 1) & 1, dead, d.spin)) break;
             if (lane == 0) {
                 for (int c = 0; c < 2; ++c)
                     if (dv_blk + 64 * c < d.Dv)
-                        tc_tensor_store(&mo, dv_blk + 64 * c, h, n * C, b, smem + L::O + (2 * (n & 1) + c) * L::TILE);
+                        tc_tensor_store(&mo, dv_blk + 64 * c, h, (n0 + it) * C, b, smem + L::O + (2 * (it & 1) + c) * L::TILE);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                mbar_arrive(bar + B_OFREE + (n & 1));
+                mbar_arrive(bar + B_OFREE + (it & 1));
             }
             __syncwarp();
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         const int cols = d.Dv - dv_blk < 128 ? d.Dv - dv_blk : 128;
         __nv_bfloat16 *out = o + ((long long)b * d.T * d.H + h) * d.Dv + dv_blk;
-        for (long long t = (long long)nch * C + (lane >> 4); t < d.T; t += 2)
+        for (long long t = (long long)chunks * C + (lane >> 4); last && t < d.T; t += 2)
             if ((lane & 15) * 8 < cols) *reinterpret_cast<uint4 *>(out + t * d.H * d.Dv + (lane & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
@@ -390,7 +421,75 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == kTcWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
 }
 
-template <int DKP, bool SAVE>
+constexpr int kJoinPitch = kDeltaMaxDk + 4;                        // floats: eight rows in a row lie in different banks
+constexpr int kJoinUnit = kDeltaMaxDk * kJoinPitch, kJoinBytes = (kJoinUnit + kDeltaMaxDk * 16) * 4;
+
+// starts[i + 1] += units[i] starts[i], segment after segment (DeltaBlock): one block per head and 16 columns,
+// a thread 8 of them of a row; what the next step reads is in flight before this one's results are put down.
+// starts[0] is the caller's state. A tile of zeros is not multiplied, so a state of zeros stays one whatever
+// the unit's columns hold.
+__global__ void __launch_bounds__(2 * kDeltaMaxDk) k_delta_join(DeltaDims d, DeltaLocal w, const float *state) {
+    extern __shared__ __align__(16) float M[];
+    float *S = M + kJoinUnit;                                      // [rows][16]
+    const int tid = threadIdx.x, row = tid & (kDeltaMaxDk - 1), c0 = tid / kDeltaMaxDk * 8, slices = d.Dv / 16;
+    const long long bh = blockIdx.x / slices, base = (bh * d.Dk + row) * d.Dv + blockIdx.x % slices * 16 + c0;
+    const bool live = row < d.Dk;
+    auto fetch = [&](int s) {                                      // what leads from segment s - 1 to s
+        if (s >= 2 && s < d.segs) {
+            const float *m = w.units + ((s - 2) * (long long)d.B * d.H + bh) * d.Dk * d.Dk;
+            const int pieces = d.Dk / 4;
+            for (int i = tid; i < d.Dk * pieces; i += 2 * kDeltaMaxDk)
+                cp_async16_zfill(smem_u32(M) + (i / pieces * kJoinPitch + i % pieces * 4) * 4, m + 4 * i, true);
+        }
+        cp_async_commit();
+    };
+    __align__(16) float x[8] = {}, next[8] = {};
+    auto first = [&](int s) {
+        if (live && s < d.segs) {
+            const float *from = (s == 0 ? state : w.starts + s * delta_states(d)) + base;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(next + i) = *reinterpret_cast<const float4 *>(from + i);
+        }
+    };
+    fetch(2);
+    first(0);
+    for (int s = 0; s < d.segs; ++s) {
+        bool some = false;                                         // of the state before
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            some |= x[i] != 0.f;
+            x[i] = next[i];
+        }
+        first(s + 1);
+        cp_async_wait<0>();
+        if (__syncthreads_or(some) && s >= 2) {
+            const float *m = M + row * kJoinPitch;
+#pragma unroll 2
+            for (int k = 0; k < d.Dk; k += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(m + k);
+                const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    __align__(16) float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(y + i) = *reinterpret_cast<const float4 *>(S + (k + e) * 16 + c0 + i);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = fmaf(av[e], y[i], x[i]);
+                }
+            }
+        }
+        __syncthreads();                                           // M and S are used
+        if (s >= 2) fetch(s + 1);
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(x + i);
+            *reinterpret_cast<float4 *>(S + row * 16 + c0 + i) = y;
+            if (live && s != 1) *reinterpret_cast<float4 *>(w.starts + s * delta_states(d) + base + i) = y;
+        }
+    }
+}
+
+template <int DKP>
 cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o, float *snap,
                     float *r, cudaStream_t st) {
     const long long os[3] = {(long long)d.T * d.H * d.Dv, (long long)d.H * d.Dv, d.Dv};
@@ -400,11 +499,22 @@ cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, 
     if (e == cudaSuccess) e = tc_tensor_map(&mv, in.v, d.vs, d.B, d.T, d.H, d.Dv);
     if (e == cudaSuccess) e = tc_tensor_map(&mo, o, os, d.B, d.T, d.H, d.Dv);
     if (e != cudaSuccess) return e;
-    auto kern = k_delta_scan_tc<DKP, SAVE>;
-    set_kernel_smem(kern, TcScan<DKP>::BYTES);
-    kern<<<(unsigned)((long long)d.B * d.H * ((d.Dv + 127) / 128)), kTcThreads, TcScan<DKP>::BYTES, st>>>(
-        mq, mk, mv, mo, d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, r);
-    return cudaGetLastError();
+    const long long heads = (long long)d.B * d.H, blocks = heads * delta_tiles(d);
+    auto run = [&](auto kern, long long grid) {
+        set_kernel_smem(kern, TcScan<DKP>::BYTES);
+        kern<<<(unsigned)grid, kTcThreads, TcScan<DKP>::BYTES, st>>>(mq, mk, mv, mo, d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, r);
+        return cudaGetLastError();
+    };
+    if (d.segs > 1) {
+        e = run(k_delta_scan_tc<DKP, SCAN_CARRY, true>, (d.segs - 2) * (blocks + heads) + blocks);
+        if (e != cudaSuccess) return e;
+        set_kernel_smem(k_delta_join, kJoinBytes);
+        k_delta_join<<<(unsigned)(heads * (d.Dv / 16)), 2 * kDeltaMaxDk, kJoinBytes, st>>>(d, w, state);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        return snap ? run(k_delta_scan_tc<DKP, SCAN_SAVE, true>, d.segs * blocks) : run(k_delta_scan_tc<DKP, SCAN_READ, true>, d.segs * blocks);
+    }
+    return snap ? run(k_delta_scan_tc<DKP, SCAN_SAVE, false>, blocks) : run(k_delta_scan_tc<DKP, SCAN_READ, false>, blocks);
 }
 
 }  // namespace
@@ -451,11 +561,7 @@ cudaError_t tc_state_map(CUtensorMap *m, const void *p, long long slots, int row
 
 cudaError_t launch_delta_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o,
                                  float *snap, float *r, cudaStream_t st) {
-    if (d.Dk <= 64)
-        return snap ? scan_tc<64, true>(d, in, w, state, o, snap, r, st)
-                    : scan_tc<64, false>(d, in, w, state, o, snap, r, st);
-    return snap ? scan_tc<128, true>(d, in, w, state, o, snap, r, st)
-                : scan_tc<128, false>(d, in, w, state, o, snap, r, st);
+    return d.Dk <= 64 ? scan_tc<64>(d, in, w, state, o, snap, r, st) : scan_tc<128>(d, in, w, state, o, snap, r, st);
 }
 
 }  // namespace sdm

@@ -186,4 +186,11 @@ __device__ __forceinline__ bool tc_warp_wait(unsigned long long *bar, unsigned p
     return __all_sync(0xffffffffu, tc_wait(bar, parity, dead, limit));
 }
 
+// A value down a column of a matrix in global memory. In order, so that a column's addresses take one register
+// pair: computed at once they are spilled, and the reloads then stand behind the stores.
+__device__ __forceinline__ void tc_put(float *&at, float x, int row) {
+    asm volatile("st.global.f32 [%0], %1;" ::"l"(at), "f"(x) : "memory");
+    at += row;
+}
+
 }  // namespace sdm

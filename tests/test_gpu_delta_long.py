@@ -1,0 +1,77 @@
+"""The gated delta rule over long sequences of few heads, which are scanned in segments at once, against the
+float64 token loop and its reverse mode. The decays are weak, so that a first token's write is still in the
+last state. Tolerances are those of the short sequences: a segment's first state is one more float32 product."""
+
+import pytest
+import torch
+
+import sparse_addressed_delta_gb300 as sdm
+from test_gpu_delta import call, check, draw
+from test_gpu_delta_backward import check as check_train
+from test_gpu_delta_backward import grads
+
+pytestmark = pytest.mark.gpu
+
+# B, T, Hk, H, Dk, Dv
+SHAPES = [(1, 2048, 1, 2, 128, 128), (1, 1500, 1, 1, 64, 80), (2, 1281, 1, 2, 128, 320), (1, 2111, 6, 6, 80, 144), (1, 1800, 8, 32, 64, 128)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    sdm.library()
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(shape):
+    x = draw(*shape, "bf16", seed=sum(shape), decay=0.001)
+    first, again = check(x, "bf16"), call(x)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    # the state reaches the end: without it the readings are others
+    x["state"].zero_()
+    assert not torch.equal(call(x)[1], first[1])
+
+
+@pytest.mark.parametrize("shape", SHAPES[:4], ids=str)
+def test_backward(shape):
+    x = draw(*shape, "bf16", seed=sum(shape), decay=0.001)
+    check_train(x, *grads(shape, "bf16"), "bf16")
+
+
+def test_valid_tokens():
+    """Lengths from none to all of them: segments of a single chunk, and of none."""
+    shape = (6, 1900, 1, 2, 64, 128)
+    x = draw(*shape, "bf16", seed=5, decay=0.001)
+    valid = [1900, 0, 1, 65, 700, 1899]
+    o, state = check(x, "bf16", valid)
+    do, dS = grads(shape, "bf16")
+    trained = check_train(x, do, dS, "bf16", valid)
+    assert torch.equal(trained[0], o) and torch.equal(trained[1], state)
+    for name in ("q", "k", "v", "g", "beta"):
+        for b, n in enumerate(valid):
+            x[name][b, n:] = float("nan")
+    got = call(x, valid)
+    assert torch.equal(got[0], o) and torch.equal(got[1], state)
+    assert torch.equal(got[1][1], x["state"][1])
+
+
+def test_resets():
+    """A reset inside a segment and one at every token."""
+    x = draw(1, 1600, 1, 2, 128, 128, "bf16", seed=9, decay=0.001)
+    x["g"][0, 777, 0] = -torch.inf
+    x["g"][0, :, 1] = -torch.inf
+    check(x, "bf16")
+    check_train(x, *grads((1, 1600, 1, 2, 128, 128), "bf16"), "bf16")
+
+
+def test_nothing_written_stays_nothing():
+    """Keys that are too long would blow any state up (each token takes (1 - beta k k^T) = -1.3 of it along
+    them); a state of zeros stays one."""
+    x = draw(1, 64 * 40, 1, 1, 64, 128, "bf16", seed=4)
+    for name in ("state", "v", "g"):
+        x[name].zero_()
+    x["beta"].fill_(1.0)
+    x["k"].fill_((2.3 / 64) ** 0.5)
+    o, state = call(x)
+    assert not o.any() and not state.any()
