@@ -98,10 +98,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // columns [i0, i1) of D as rows of a [Dk, Dv] state
         auto keep_state = [&](float *dst, int i0, int i1) {
-            dst += (size_t)dk0 * d.Dv + dv;
+            dst += (dk0 + i0) * d.Dv + dv;
 #pragma unroll
-            for (int i = 0; i < HD; ++i)
-                if (i >= i0 && i < i1 && mine && dk0 + i < d.Dk) dst[(size_t)i * d.Dv] = S[i];
+            for (int c = 0; c < HD; c += 16) {                     // Dk is a multiple of 16
+                if (c < i0 || c >= i1 || !mine || dk0 + c >= d.Dk) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tc_put(dst, S[c + i], d.Dv);
+            }
         };
         auto planes_of_s = [&] {
 #pragma unroll
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (mine) {
                 float *dst = o.w + ((bh * d.Nt + n) * (long long)C + 16 * quarter) * d.Dv + dv;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) dst[(size_t)i * d.Dv] = x[i];
+                for (int i = 0; i < 16; ++i) tc_put(dst, x[i], d.Dv);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] *= -be[i] * from[i];
