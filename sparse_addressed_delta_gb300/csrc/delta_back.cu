@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
     const int slices = (d.Dv + NW * 16 - 1) / (NW * 16);
     const int dv_blk = (blockIdx.x % slices) * NW * 16;
-    const long long bh = blockIdx.x / slices;
+    const long long bh = delta_longest_first(d, in.valid, blockIdx.x / slices);
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
     const int dv0 = dv_blk + 16 * warp;
     const bool mine = dv0 < d.Dv;

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto slot = reinterpret_cast<uint32_t *>(bar + B_COUNT + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles = (d.Dv + 127) / 128, dv_blk = (blockIdx.x % tiles) * 128;
-    const long long bh = blockIdx.x / tiles;
+    const long long bh = delta_longest_first(d, in.valid, blockIdx.x / tiles);
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
     const int ntok = delta_valid(in.valid, b, d.T), nch = (ntok + C - 1) / C;
 

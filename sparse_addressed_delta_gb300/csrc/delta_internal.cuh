@@ -70,13 +70,33 @@ __host__ __device__ inline int delta_bound(const DeltaDims &d, int chunks, int i
     return i == 0 ? 0 : (int)((long long)chunks * (d.first + (i - 1) * 256) / ((d.segs - 1) * 256 + d.first));
 }
 
+__device__ __forceinline__ int delta_valid(const int32_t *valid, int b, int T) {
+    const int v = valid ? valid[b] : T;
+    return v < 0 ? 0 : (v > T ? T : v);
+}
+
 struct DeltaBlock {
     int seg, tile;
     bool unit;
     long long bh;
 };
+// The scans' blocks take the sequences from the longest down, so that the last ones to start are short
+// (8 sequences of up to 4096 tokens, 32 heads on 152 SMs: 326 -> 293 us). More than 32 sequences stay in their
+// order: their many blocks level out by themselves.
+__device__ __forceinline__ long long delta_longest_first(const DeltaDims &d, const int32_t *valid, long long bh) {
+    if (!valid || d.B > 32) return bh;
+    const int lane = threadIdx.x & 31, mine = lane < d.B ? delta_valid(valid, lane, d.T) : -1;
+    int rank = 0;
+    for (int i = 0; i < d.B; ++i) {
+        const int other = __shfl_sync(~0u, mine, i);
+        rank += other > mine || (other == mine && i < lane);
+    }
+    const int b = __ffs(__ballot_sync(~0u, rank == (int)(bh / d.H))) - 1;
+    return (long long)b * d.H + bh % d.H;
+}
+
 template <bool SEG, bool CARRY>
-__device__ __forceinline__ DeltaBlock delta_block(const DeltaDims &d) {
+__device__ __forceinline__ DeltaBlock delta_block(const DeltaDims &d, const int32_t *valid) {
     DeltaBlock k;
     const int tiles = delta_tiles(d), heads = d.B * d.H;
     // the first launch: per inner segment and head, the state's tiles and a unit matrix
@@ -87,7 +107,7 @@ __device__ __forceinline__ DeltaBlock delta_block(const DeltaDims &d) {
     const int of = first ? tiles : per;
     k.tile = (int)(i % of);
     i /= of;
-    k.bh = SEG ? i % heads : i;
+    k.bh = delta_longest_first(d, valid, SEG ? i % heads : i);
     k.seg = first ? 0 : 1 + (int)(i / heads);
     k.unit = CARRY && !first && k.tile == tiles;
     if (k.unit) k.tile = 0;
@@ -140,11 +160,6 @@ cudaError_t launch_delta_back_local_tc(const DeltaDims &d, const DeltaIn &in, co
 // ---------------------------------------------------------------------------------------
 // device helpers
 // ---------------------------------------------------------------------------------------
-
-__device__ __forceinline__ int delta_valid(const int32_t *valid, int b, int T) {
-    const int v = valid ? valid[b] : T;
-    return v < 0 ? 0 : (v > T ? T : v);
-}
 
 __device__ __forceinline__ float delta_decay(float g) { return g < kDeltaMinDecay ? kDeltaMinDecay : g; }
 

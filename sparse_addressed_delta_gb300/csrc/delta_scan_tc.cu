@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int *dead = reinterpret_cast<int *>(bar + B_COUNT);
     auto slot = reinterpret_cast<uint32_t *>(bar + B_COUNT + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const DeltaBlock blk = delta_block<SEG, CARRY>(d);
+    const DeltaBlock blk = delta_block<SEG, CARRY>(d, in.valid);
     const int dv_blk = blk.tile * 128, seg = blk.seg, width = CARRY && blk.unit ? d.Dk : d.Dv;
     const long long bh = blk.bh;
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
