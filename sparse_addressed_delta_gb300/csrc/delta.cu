@@ -8,26 +8,30 @@
 namespace sdm {
 namespace {
 
-// How many segments a sequence's scan takes (DeltaBlock in delta_internal.cuh): two launches and a join,
-// which pay when the heads alone leave SMs idle. By the times in microseconds measured for 128 x 128
-// states: a chunk alone and beside twice as many blocks, a chunk of the first launch, a block's start, the
-// join and each of its steps. Measured, whole call, in segments and not: 32 heads x 256 chunks 588 and 913 us,
-// 16 x 64 137 and 234, 4 x 64 111 and 213; 64 heads x 64 chunks 330 and 305, so not taken. A saving forward
-// takes the same segments, so that its results are the same.
-void delta_split(DeltaDims &d) {
-    constexpr double kAlone = 2.6, kBeside = 3.0, kCarry = 2.3, kStart = 8.0, kJoin = 8.0, kJoinStep = 4.0;
+// How many segments a sequence's scans take (DeltaBlock in delta_internal.cuh): two launches and a join,
+// which pay when the heads alone leave SMs idle. By the times in microseconds measured: a chunk alone and
+// beside twice as many blocks, a chunk of the first launch (the tensor-memory form at 128 x 128; the register
+// form by its products), a block's start, the join and each of its steps. Measured, whole call, in segments
+// and not, bfloat16 at 128 x 128: 32 heads x 256 chunks 580 and 913 us, 16 x 64 137 and 234, 4 x 64 111 and
+// 213 (backward 279 and 478, 160 and 371); 64 heads x 64 chunks 330 and 305, so not taken. float32 training, 8
+// heads of 64 x 64 x 32 chunks: 186 and 276. By shape and type alone: a saving forward's results are
+// the plain one's, and a backward's segments its forward's, whatever the strides.
+void delta_segments(DeltaDims &d) {
+    constexpr double kStart = 8.0, kJoin = 8.0, kJoinStep = 4.0;
+    const bool tensor = d.dtype == SDM_BF16 && d.Dv > 64;
+    const int of = tensor ? 128 : 64;
+    const double alone = tensor ? 2.6 : 0.5 * d.Dk / 16 + 1.0, beside = tensor ? 3.0 : alone, carry = tensor ? 2.3 : 0.36 * d.Dk / 16 + 0.6;
+    const long long heads = (long long)d.B * d.H, blocks = heads * delta_tiles(d.Dv, of), units = heads * delta_tiles(d.Dk, of);
+    const double startup = kStart / beside;                  // in chunks
+    double best = (alone * d.Nt + kStart) * ((blocks + kRefSms - 1) / kRefSms);
     d.segs = d.first = 1;
-    if (!d.tc) return;
-    const long long heads = (long long)d.B * d.H, blocks = heads * delta_tiles(d);
-    const double startup = kStart / kBeside;                 // in chunks
-    double best = (kAlone * d.Nt + kStart) * ((blocks + kRefSms - 1) / kRefSms);
     for (int s = 3; s <= d.Nt; ++s) {
-        const long long busy = std::max((s - 2) * (blocks + heads), (s - 1) * blocks);
+        const long long busy = std::max((s - 2) * (blocks + units), (s - 1) * blocks);
         if (busy >= kRefSms) break;                          // segment 0 needs SMs beside the others
         // `rounds` blocks of segment 0 one after another take as long as one of the others
         const double rounds = (double)((blocks + kRefSms - busy - 1) / (kRefSms - busy));
         const double longer = std::min((d.Nt + startup * (1.0 - 1.0 / rounds)) / (s - 1 + 1.0 / rounds), d.Nt / (s - 1.0));
-        const double time = (kCarry + kBeside) * longer + 2 * kStart + kJoin + kJoinStep * (s - 2);
+        const double time = (carry + beside) * longer + 2 * kStart + kJoin + kJoinStep * (s - 2);
         if (time < best) {
             best = time;
             d.segs = s;
@@ -60,7 +64,6 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.C = delta_chunk(s->dtype);
     d.pp = s->dtype == SDM_BF16 ? 2 : 3;
     d.back = 0;
-    d.segs = d.first = 1;
     d.spin = wait_limit();
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
@@ -78,6 +81,7 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     }
     d.tc = s->dtype == SDM_BF16 && s->Dv > 64 && tc_tensor_fits(d.qs, d.B, d.T, d.Hk) &&
            tc_tensor_fits(d.ks, d.B, d.T, d.Hk) && tc_tensor_fits(d.vs, d.B, d.T, d.H);
+    delta_segments(d);
     return SDM_OK;
 }
 
@@ -98,10 +102,12 @@ int delta_status(cudaError_t e) {
 
 bool by_token(const DeltaDims &d) { return d.T <= kDeltaStepTokens; }
 
+size_t delta_unit_bytes(const DeltaDims &d) { return d.segs > 1 ? (d.segs - 2) * (size_t)d.B * d.H * d.Dk * d.Dk * 4 : 0; }
+
 // Where the chunk form's buffers lie in a workspace; `bytes` is their end.
 struct DeltaLayout {
     size_t q, k, x, p, aux;              // q, k: the planes of float32 inputs
-    size_t starts, units;                // the segments'
+    size_t starts, units;                // the segments' (units: of a forward that saves nothing)
     size_t ends, w, dq, dk;              // the backward's
     size_t bytes;
 };
@@ -121,7 +127,7 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     l.p = take(delta_chunks(d) * d.pp * delta_plane_bytes(d));
     l.aux = take(delta_chunks(d) * kDeltaAux * d.C * 4);
     l.starts = take(d.segs > 1 ? d.segs * (size_t)delta_states(d) * 4 : 0);
-    l.units = take(d.segs > 1 ? (d.segs - 2) * (size_t)d.B * d.H * d.Dk * d.Dk * 4 : 0);
+    if (!backward) l.units = take(delta_unit_bytes(d));
     if (backward) {
         l.ends = take(delta_chunks(d) * d.Dk * d.Dv * 4);
         l.w = take(delta_chunks(d) * d.C * d.Dv * 4);
@@ -133,13 +139,12 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     return l;
 }
 
-// what the saving forward keeps: the state at every chunk's start and at the end, and r
+// what the saving forward keeps: the state at every chunk's start and at the end, r, and the segments' units
 size_t delta_saved_snap(const DeltaDims &d) {
     return delta_up((delta_chunks(d) + (size_t)d.B * d.H) * d.Dk * d.Dv * 4);
 }
-size_t delta_saved(const DeltaDims &d) {
-    return delta_saved_snap(d) + delta_up(delta_chunks(d) * d.C * d.Dv * 4);
-}
+size_t delta_saved_units(const DeltaDims &d) { return delta_saved_snap(d) + delta_up(delta_chunks(d) * d.C * d.Dv * 4); }
+size_t delta_saved(const DeltaDims &d) { return delta_saved_units(d) + delta_up(delta_unit_bytes(d)); }
 
 DeltaPlanes delta_planes(const DeltaDims &d, const void *x, const long long *s, unsigned char *split) {
     DeltaPlanes p;
@@ -204,7 +209,6 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
     if (!save && by_token(d)) return delta_status(launch_delta_step(d, in, state, readings, st));
-    delta_split(d);
     const DeltaLayout l = delta_layout(d, false);
     rc = delta_check_ws("workspace", workspace, workspace_bytes, l.bytes);
     if (rc == SDM_OK && save) rc = delta_check_ws("saved buffer", saved, saved_bytes, delta_saved(d));
@@ -212,6 +216,7 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
     DeltaPlanes qp, kp;
     DeltaLocal w;
     cudaError_t e = delta_local(d, in, l, static_cast<unsigned char *>(workspace), qp, kp, w, st);
+    if (save) w.units = reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_units(d));
     float *snap = save ? static_cast<float *>(saved) : nullptr;
     float *r = save ? reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_snap(d)) : nullptr;
     if (e == cudaSuccess)
@@ -227,7 +232,6 @@ extern "C" {
 size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
     if (delta_check(shape, d) != SDM_OK) return 0;
-    delta_split(d);
     return delta_layout(d, false).bytes + kAlign;
 }
 
@@ -296,6 +300,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     DeltaPlanes qp, kp;
     DeltaLocal w;
     cudaError_t e = delta_local(d, in, l, ws, qp, kp, w, st);
+    w.units = const_cast<float *>(reinterpret_cast<const float *>(static_cast<const unsigned char *>(saved) + delta_saved_units(d)));
     DeltaBack o;
     o.grad = grad_readings;
     o.state_in = grad_final_state;

@@ -37,20 +37,23 @@ struct BackSmem {
 // One block per head and NW * 16 of its columns, from the last chunk to the first.
 template <typename T, int DKP, int NW>
 __global__ void __launch_bounds__(NW * 32, 1)
-    k_delta_back_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, DeltaBack o) {
+    k_delta_back_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, DeltaBack o, int mode) {
     using L = BackSmem<T, DKP, NW>;
     constexpr bool BF = L::BF;
     constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, KPI = L::KPI, THREADS = NW * 32;
     constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
-    const int slices = (d.Dv + NW * 16 - 1) / (NW * 16);
-    const int dv_blk = (blockIdx.x % slices) * NW * 16;
-    const long long bh = delta_longest_first(d, in.valid, blockIdx.x / slices);
+    const bool carry = mode == DELTA_CARRY_BACK;
+    const DeltaBlock blk = delta_block(d, in.valid, d.segs > 1, mode, NW * 16);
+    const int dv_blk = blk.tile * NW * 16;
+    const long long bh = blk.bh;
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
     const int dv0 = dv_blk + 16 * warp;
     const bool mine = dv0 < d.Dv;
-    const int ntok = delta_valid(in.valid, b, d.T), nch = (ntok + C - 1) / C;
+    const int ntok = delta_valid(in.valid, b, d.T), chunks = (ntok + C - 1) / C;
+    const int n0 = delta_bound(d, chunks, blk.seg), n1 = delta_bound(d, chunks, blk.seg + 1), nch = n1 - n0;
+    const bool last = blk.seg + 1 == d.segs;
     const T *grad = static_cast<const T *>(o.grad) + b * d.os[0] + h * d.os[2] + dv_blk;
     const long long kbase = b * k.s[0] + hk * k.s[2], qbase = b * q.s[0] + hk * q.s[2];
     T *gv = static_cast<T *>(o.grad_v) + ((long long)b * d.T * d.H + h) * d.Dv;
@@ -72,13 +75,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
     };
     // element e of the state's fragment j: row 8 j + 2 i4 + (e & 1), column dv0 + g4 + 8 (e >> 1)
     float S[ND][4];
-    const float *sp = o.state_in + (bh * d.Dk) * d.Dv + dv0;
+    const float *from_end = d.segs > 1 && !carry ? w.starts + blk.seg * delta_states(d) : carry && !last ? nullptr : o.state_in;
+    const float *sp = from_end + (bh * d.Dk) * d.Dv + dv0;
 #pragma unroll
     for (int j = 0; j < ND; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int dk = 8 * j + 2 * i4 + (e & 1);
-            S[j][e] = mine && o.state_in && dk < d.Dk ? sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] : 0.f;
+            S[j][e] = mine && from_end && dk < d.Dk ? sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] : 0.f;
         }
     auto store_state = [&](float *dst) {
 #pragma unroll
@@ -89,11 +93,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 if (dk < d.Dk) dst[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
             }
     };
-    if (L::STAGES == 2 && nch > 0) load(nch - 1, 0);
+    if (L::STAGES == 2 && nch > 0) load(n1 - 1, 0);
     for (int it = 0; it < nch; ++it) {
-        const int n = nch - 1 - it;
+        const int n = n1 - 1 - it;
         if constexpr (L::STAGES == 2) {
-            if (n > 0) {
+            if (n > n0) {
                 load(n - 1, (it + 1) & 1);
                 cp_async_wait<1>();
             } else {
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         const float *from = reinterpret_cast<const float *>(smem + stage + L::AUX), *to = from + C, *be = to + C;
         const int nt = ntok - n * C < C ? ntok - n * C : C;
         if (mine) {
-            store_state(o.ends + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv + dv0);
+            if (!carry) store_state(o.ends + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv + dv0);
             // dO^T as an A operand, K step ks: KP planes of the stored values times `f` of the token
             auto grads = [&](int ks, float (&x)[4][2]) {
                 if constexpr (BF) {
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 8 * j + 2 * i4 + (e & 1), c = 16 * warp + g4 + 8 * (e >> 1);
-                    dst[(size_t)t * d.Dv + g4 + 8 * (e >> 1)] = W[j][e];
+                    if (!carry) dst[(size_t)t * d.Dv + g4 + 8 * (e >> 1)] = W[j][e];
                     const float x = be[t] * W[j][e];
                     *reinterpret_cast<T *>(smem + stage + L::V + delta_at<VP>(t, c / VE) + (c % VE) * sizeof(T)) = from_f32<T>(x);
                     W[j][e] = -from[t] * x;
@@ -268,15 +272,19 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 const long long t = (long long)n * C + r;
                 uint4 x = *reinterpret_cast<const uint4 *>(smem + stage + L::V + delta_at<VP>(r, 16 * warp / VE + c));
                 if (r >= nt) x = make_uint4(0u, 0u, 0u, 0u);
-                if (t < d.T) *reinterpret_cast<uint4 *>(gv + t * orow + dv0 + c * VE) = x;
+                if (t < d.T && !carry) *reinterpret_cast<uint4 *>(gv + t * orow + dv0 + c * VE) = x;
             }
         }
         __syncthreads();
     }
     if (!mine) return;
-    store_state(o.state_out + (bh * d.Dk) * d.Dv + dv0);
+    if (carry)
+        store_state(w.starts + (blk.seg - 1) * delta_states(d) + (bh * d.Dk) * d.Dv + dv0);
+    else if (blk.seg == 0)
+        store_state(o.state_out + (bh * d.Dk) * d.Dv + dv0);
+    if (carry || !last) return;
     constexpr int PR = 16 / VE;
-    for (long long t = (long long)nch * C + lane / PR; t < d.T; t += 32 / PR)
+    for (long long t = (long long)chunks * C + lane / PR; t < d.T; t += 32 / PR)
         *reinterpret_cast<uint4 *>(gv + t * orow + dv0 + (lane % PR) * VE) = make_uint4(0u, 0u, 0u, 0u);
 }
 
@@ -702,9 +710,16 @@ cudaError_t back_scan_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlan
     using L = BackSmem<T, DKP, NW>;
     auto kern = k_delta_back_scan<T, DKP, NW>;
     set_kernel_smem(kern, L::BYTES);
-    const long long slices = (d.Dv + NW * 16 - 1) / (NW * 16);
-    kern<<<(unsigned)((long long)d.B * d.H * slices), NW * 32, L::BYTES, st>>>(d, in, q, k, w, o);
-    return cudaGetLastError();
+    auto run = [&](int mode) {
+        kern<<<(unsigned)delta_blocks(d, mode, NW * 16), NW * 32, L::BYTES, st>>>(d, in, q, k, w, o, mode);
+        return cudaGetLastError();
+    };
+    if (d.segs > 1) {
+        cudaError_t e = run(DELTA_CARRY_BACK);
+        if (e == cudaSuccess) e = launch_delta_join(d, w, o.state_in, true, st);
+        if (e != cudaSuccess) return e;
+    }
+    return run(DELTA_RUN);
 }
 
 template <typename T, int DKP>

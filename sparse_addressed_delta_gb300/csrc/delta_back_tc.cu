@@ -44,7 +44,8 @@ enum {
     B_GRAD = 20, B_DRAIN, B_BULK, B_COUNT = B_BULK + 2
 };
 
-template <int DKP>
+// CARRY: the segments' first gradients only. SEG: the sequences are in segments (DeltaBlock).
+template <int DKP, bool SEG, bool CARRY>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_delta_back_scan_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mo, DeltaDims d,
@@ -57,10 +58,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int *dead = reinterpret_cast<int *>(bar + B_COUNT);
     auto slot = reinterpret_cast<uint32_t *>(bar + B_COUNT + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tiles = (d.Dv + 127) / 128, dv_blk = (blockIdx.x % tiles) * 128;
-    const long long bh = delta_longest_first(d, in.valid, blockIdx.x / tiles);
+    const DeltaBlock blk = delta_block(d, in.valid, SEG, CARRY ? DELTA_CARRY_BACK : DELTA_RUN, 128);
+    const int dv_blk = blk.tile * 128, seg = blk.seg;
+    const long long bh = blk.bh;
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
-    const int ntok = delta_valid(in.valid, b, d.T), nch = (ntok + C - 1) / C;
+    const int ntok = delta_valid(in.valid, b, d.T), chunks = (ntok + C - 1) / C;
+    const int n0 = SEG ? delta_bound(d, chunks, seg) : 0, n1 = SEG ? delta_bound(d, chunks, seg + 1) : chunks, nch = n1 - n0;
+    const bool last = !SEG || seg + 1 == d.segs;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -71,7 +75,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = B_S; i < B_E; ++i) mbar_init(bar + i, kTcWarps / 2);
         for (int i = B_E; i < B_COUNT; ++i) mbar_init(bar + i, i == B_GRAD ? kTcWarps : 1);
-        *dead = 0;
+        *dead = SEG && !CARRY && w.status->code != 0;              // an earlier kernel of this call gave up
         fence_mbar_init();
     }
     if (warp == kTcWarps) {
@@ -92,9 +96,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int dk0 = part * HD;
         float S[HD];
         {
-            const float *sp = o.state_in + (bh * d.Dk + dk0) * d.Dv + dv;
+            const float *end = SEG && !CARRY ? w.starts + seg * delta_states(d) : CARRY && !last ? nullptr : o.state_in;
+            const float *sp = end + (bh * d.Dk + dk0) * d.Dv + dv;
 #pragma unroll
-            for (int i = 0; i < HD; ++i) S[i] = o.state_in && mine && dk0 + i < d.Dk ? sp[(size_t)i * d.Dv] : 0.f;
+            for (int i = 0; i < HD; ++i) S[i] = end && mine && dk0 + i < d.Dk ? sp[(size_t)i * d.Dv] : 0.f;
         }
         // columns [i0, i1) of D as rows of a [Dk, Dv] state
         auto keep_state = [&](float *dst, int i0, int i1) {
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int orow = 16 * quarter + 8 * (lane >> 4) + (lane & 7), ocol = (lane0 >> 3) + ((lane >> 3) & 1);
         const int gcol = lane0 + lane;                             // this lane's column in dO's tiles
         for (int it = 0; it < nch; ++it) {
-            const int n = nch - 1 - it;
+            const int n = n1 - 1 - it;
             const unsigned par = it & 1;
             float *keep = o.ends + (bh * d.Nt + n) * (long long)d.Dk * d.Dv;
             if (!tc_warp_wait(bar + B_FULL + par, (it >> 1) & 1, dead, d.spin)) break;
@@ -162,13 +167,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_wait_st();
                 arrive(B_GRAD);
             }
-            keep_state(keep, 0, HD);
+            if (!CARRY) keep_state(keep, 0, HD);
             if (!tc_warp_wait(bar + B_WACC + half, par, dead, d.spin)) break;
-            if (it >= 2 && !tc_warp_wait(bar + B_OFREE + par, ((it >> 1) - 1) & 1, dead, d.spin)) break;
+            if (!CARRY && it >= 2 && !tc_warp_wait(bar + B_OFREE + par, ((it >> 1) - 1) & 1, dead, d.spin)) break;
             tc_fence_after();
             // the values' gradient, in a buffer that warp 18 stores; 0 past the valid tokens
 #pragma unroll
-            for (int l = 0; l < 2; ++l) {                          // 16 lanes of dv
+            for (int l = 0; l < (CARRY ? 0 : 2); ++l) {            // 16 lanes of dv
                 float y[8];
                 tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::W + 16 * quarter, y);
                 unsigned r[4];
@@ -182,11 +187,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int c = ocol + 2 * l;
                 stsm4t(smem_u32(smem) + L::O + (2 * par + (c >> 3)) * L::TILE + tc_at(orow, c & 7), r);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar + B_OUT + par);
+            if constexpr (!CARRY) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + B_OUT + par);
+            }
             tc_load16(at + L::W + 16 * quarter, x);
-            if (mine) {
+            if (!CARRY && mine) {
                 float *dst = o.w + ((bh * d.Nt + n) * (long long)C + 16 * quarter) * d.Dv + dv;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) tc_put(dst, x[i], d.Dv);
@@ -211,7 +218,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             arrive(B_S + half);
             if (lane == 0) mbar_arrive(bar + B_EMPTY + par);
         }
-        if (!*dead) keep_state(o.state_out + bh * d.Dk * (long long)d.Dv, 0, HD);
+        if (CARRY)
+            keep_state(w.starts + (seg - 1) * delta_states(d) + bh * d.Dk * (long long)d.Dv, 0, HD);
+        else if (seg == 0 && !*dead)
+            keep_state(o.state_out + bh * d.Dk * (long long)d.Dv, 0, HD);
     } else if (warp == kTcWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp == kTcWarps + 1) {
         // ---- the chunks' inputs
         for (int it = 0; it < nch; ++it) {
-            const int n = nch - 1 - it, s = it & 1, t0 = n * C, nt = ntok - t0 < C ? ntok - t0 : C;
+            const int n = n1 - 1 - it, s = it & 1, t0 = n * C, nt = ntok - t0 < C ? ntok - t0 : C;
             unsigned char *st = smem + s * L::STAGE;
             const long long bhn = bh * d.Nt + n;
             unsigned long long *full = bar + B_BULK + s;
@@ -353,14 +363,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             mbar_arrive(bar + B_FULL + s);
         }
-    } else {
+    } else if (!CARRY) {
         // ---- the values' gradient
         for (int it = 0; it < nch; ++it) {
             if (!tc_warp_wait(bar + B_OUT + (it & 1), (it >> 1) & 1, dead, d.spin)) break;
             if (lane == 0) {
                 for (int c = 0; c < 2; ++c)
                     if (dv_blk + 64 * c < d.Dv)
-                        tc_tensor_store(&mo, dv_blk + 64 * c, h, (nch - 1 - it) * C, b, smem + L::O + (2 * (it & 1) + c) * L::TILE);
+                        tc_tensor_store(&mo, dv_blk + 64 * c, h, (n1 - 1 - it) * C, b, smem + L::O + (2 * (it & 1) + c) * L::TILE);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 mbar_arrive(bar + B_OFREE + (it & 1));
@@ -370,7 +380,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         const int cols = d.Dv - dv_blk < 128 ? d.Dv - dv_blk : 128;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(o.grad_v) + ((long long)b * d.T * d.H + h) * d.Dv + dv_blk;
-        for (long long t = (long long)nch * C + (lane >> 4); t < d.T; t += 2)
+        for (long long t = (long long)chunks * C + (lane >> 4); last && t < d.T; t += 2)
             if ((lane & 15) * 8 < cols) *reinterpret_cast<uint4 *>(out + t * d.H * d.Dv + (lane & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
@@ -397,10 +407,15 @@ cudaError_t back_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal
     if (e == cudaSuccess) e = tc_tensor_map(&mg, o.grad, d.os, d.B, d.T, d.H, d.Dv);
     if (e == cudaSuccess) e = tc_tensor_map(&mo, o.grad_v, os, d.B, d.T, d.H, d.Dv);
     if (e != cudaSuccess) return e;
-    auto kern = k_delta_back_scan_tc<DKP>;
-    set_kernel_smem(kern, TcBack<DKP>::BYTES);
-    kern<<<(unsigned)((long long)d.B * d.H * ((d.Dv + 127) / 128)), kTcThreads, TcBack<DKP>::BYTES, st>>>(mq, mk, mg, mo, d, in, w, o);
-    return cudaGetLastError();
+    auto run = [&](auto kern, int mode) {
+        set_kernel_smem(kern, TcBack<DKP>::BYTES);
+        kern<<<(unsigned)delta_blocks(d, mode, 128), kTcThreads, TcBack<DKP>::BYTES, st>>>(mq, mk, mg, mo, d, in, w, o);
+        return cudaGetLastError();
+    };
+    if (d.segs == 1) return run(k_delta_back_scan_tc<DKP, false, false>, DELTA_RUN);
+    e = run(k_delta_back_scan_tc<DKP, true, true>, DELTA_CARRY_BACK);
+    if (e == cudaSuccess) e = launch_delta_join(d, w, o.state_in, true, st);
+    return e == cudaSuccess ? run(k_delta_back_scan_tc<DKP, true, false>, DELTA_RUN) : e;
 }
 
 }  // namespace

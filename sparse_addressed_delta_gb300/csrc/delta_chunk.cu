@@ -314,20 +314,23 @@ struct ScanSmem {
 template <typename T, int DKP, int NW, bool SAVE>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_delta_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, float *state,
-                 T *o, float *snap, float *rsave) {
+                 T *o, float *snap, float *rsave, int mode) {
     using L = ScanSmem<T, DKP, NW>;
     constexpr bool BF = L::BF;
     constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, KPI = L::KPI, THREADS = NW * 32;
     constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
-    const int slices = (d.Dv + NW * 16 - 1) / (NW * 16);
-    const int dv_blk = (blockIdx.x % slices) * NW * 16;
-    const long long bh = delta_longest_first(d, in.valid, blockIdx.x / slices);
+    const bool carry = !SAVE && mode == DELTA_CARRY;
+    const DeltaBlock blk = delta_block(d, in.valid, d.segs > 1, mode, NW * 16);
+    const int dv_blk = blk.tile * NW * 16, width = blk.unit ? d.Dk : d.Dv;
+    const long long bh = blk.bh;
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
     const int dv0 = dv_blk + 16 * warp;
-    const bool mine = dv0 < d.Dv;                            // else the warp only helps to load
-    const int ntok = delta_valid(in.valid, b, d.T), nch = (ntok + C - 1) / C;
+    const bool mine = dv0 < width;                           // else the warp only helps to load
+    const int ntok = delta_valid(in.valid, b, d.T), chunks = (ntok + C - 1) / C;
+    const int n0 = delta_bound(d, chunks, blk.seg), nch = delta_bound(d, chunks, blk.seg + 1);   // its chunks' ends
+    const bool last = blk.seg + 1 == d.segs;
     const T *v = static_cast<const T *>(in.v) + b * d.vs[0] + h * d.vs[2] + dv_blk;
     const long long kbase = b * k.s[0] + hk * k.s[2], qbase = b * q.s[0] + hk * q.s[2];
     T *out = o + ((long long)b * d.T * d.H + h) * d.Dv;
@@ -339,23 +342,27 @@ __global__ void __launch_bounds__(NW * 32, 1)
         const long long t0 = (long long)n * C, bhn = bh * d.Nt + n;
         const int nt = ntok - (int)t0 < C ? ntok - (int)t0 : C;
         load_tokens<KP, DKP, C, THREADS>(st, k, kbase + t0 * k.s[1], d.Dk, nt, tid);
-        load_tokens<KP, DKP, C, THREADS>(st + L::Q, q, qbase + t0 * q.s[1], d.Dk, nt, tid);
         load_planes<3, C, THREADS>(st + L::X, w.x + bhn * (3 * C * XP), tid);
-        load_planes<PP, C, THREADS>(st + L::P, w.p + bhn * (PP * C * XP), tid);
-        load_values<T, NW * 16, C, THREADS>(st + L::V, v + t0 * d.vs[1], d.vs[1], nt, d.Dv - dv_blk, tid);
+        if (!carry) {
+            load_tokens<KP, DKP, C, THREADS>(st + L::Q, q, qbase + t0 * q.s[1], d.Dk, nt, tid);
+            load_planes<PP, C, THREADS>(st + L::P, w.p + bhn * (PP * C * XP), tid);
+        }
+        load_values<T, NW * 16, C, THREADS>(st + L::V, v + t0 * d.vs[1], d.vs[1], nt, blk.unit ? 0 : d.Dv - dv_blk, tid);
         for (int i = tid; i < 3 * C / 4; i += THREADS)
             cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * kDeltaAux * C + 4 * i, true);
         cp_async_commit();
     };
 
     float S[ND][4];
-    float *sp = state + (bh * d.Dk) * d.Dv + dv0;
+    const bool real = !carry || blk.seg == 0;
+    const float *sp = (d.segs > 1 && !carry ? w.starts + blk.seg * delta_states(d) : state) + (bh * d.Dk) * d.Dv + dv0;
 #pragma unroll
     for (int j = 0; j < ND; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int dk = 8 * j + 2 * i4 + (e & 1);
-            S[j][e] = mine && dk < d.Dk ? sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] : 0.f;
+            const bool one = blk.unit && dk == dv0 + g4 + 8 * (e >> 1);
+            S[j][e] = real && mine && dk < d.Dk ? sp[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] : one ? 1.f : 0.f;
         }
     auto store_state = [&](float *dst) {
 #pragma unroll
@@ -363,19 +370,19 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int dk = 8 * j + 2 * i4 + (e & 1);
-                if (dk < d.Dk) dst[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
+                if (dk < d.Dk) dst[(size_t)dk * width + g4 + 8 * (e >> 1)] = S[j][e];
             }
     };
-    if (nch > 0) load(0, 0);
-    for (int n = 0; n < nch; ++n) {
+    if (n0 < nch) load(n0, 0);
+    for (int n = n0; n < nch; ++n) {
         if (n + 1 < nch) {
-            load(n + 1, (n + 1) & 1);
+            load(n + 1, (n + 1 - n0) & 1);
             cp_async_wait<1>();
         } else {
             cp_async_wait<0>();
         }
         __syncthreads();
-        const int stage = (n & 1) * L::STAGE;
+        const int stage = ((n - n0) & 1) * L::STAGE;
         const unsigned sk = s0 + stage, sq = sk + L::Q, sx = sk + L::X, spp = sk + L::P, sv = sk + L::V;
         const float *from = reinterpret_cast<const float *>(smem + stage + L::AUX), *to = from + C;
         const int nt = ntok - n * C < C ? ntok - n * C : C;
@@ -399,6 +406,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
                                 mma_bf16(R[j], a[x], bb[p][j >> 1][2 * (j & 1)], bb[p][j >> 1][2 * (j & 1) + 1]);
+                if (carry) continue;
 #pragma unroll
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
@@ -471,6 +479,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
 #pragma unroll
             for (int ks = 0; ks < C / 16; ++ks) {            // O += (P diag(beta) r)^T
+                if (carry) break;
                 unsigned a[PP][4];
                 split_frag<PP>(U, ks, a);
 #pragma unroll
@@ -489,17 +498,17 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 }
             }
             // the readings take the place of the warp's columns of the value tile, then leave as rows
-            __syncwarp();
+            if (!carry) {
+                __syncwarp();
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 8 * j + 2 * i4 + (e & 1), c = 16 * warp + g4 + 8 * (e >> 1);
-                    *reinterpret_cast<T *>(smem + stage + L::V + delta_at<VP>(t, c / VE) +
-                                           (c % VE) * sizeof(T)) = from_f32<T>(O[j][e]);
-                }
-            __syncwarp();
-            {
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 8 * j + 2 * i4 + (e & 1), c = 16 * warp + g4 + 8 * (e >> 1);
+                        *reinterpret_cast<T *>(smem + stage + L::V + delta_at<VP>(t, c / VE) +
+                                               (c % VE) * sizeof(T)) = from_f32<T>(O[j][e]);
+                    }
+                __syncwarp();
                 constexpr int PR = 16 / VE, RP = 32 / PR;    // pieces a row, rows at once
 #pragma unroll
                 for (int r0 = 0; r0 < C; r0 += RP) {
@@ -548,11 +557,92 @@ __global__ void __launch_bounds__(NW * 32, 1)
         __syncthreads();
     }
     if (!mine) return;
-    if (nch > 0) store_state(sp);
-    if (SAVE) store_state(snap + ((bh * (d.Nt + 1) + nch) * (long long)d.Dk) * d.Dv + dv0);
+    if (carry) {
+        store_state((blk.unit ? w.units + ((blk.seg - 1) * (long long)d.B * d.H + bh) * d.Dk * d.Dk
+                              : w.starts + (blk.seg + 1) * delta_states(d) + bh * d.Dk * (long long)d.Dv) + dv0);
+        return;
+    }
+    if (!last) return;
+    if (nch > 0) store_state(state + (bh * d.Dk) * d.Dv + dv0);
+    if (SAVE) store_state(snap + ((bh * (d.Nt + 1) + chunks) * (long long)d.Dk) * d.Dv + dv0);
     constexpr int PR = 16 / VE;
-    for (long long t = (long long)nch * C + lane / PR; t < d.T; t += 32 / PR)
+    for (long long t = (long long)chunks * C + lane / PR; t < d.T; t += 32 / PR)
         *reinterpret_cast<uint4 *>(out + t * orow + dv0 + (lane % PR) * VE) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+constexpr int kJoinPitch = kDeltaMaxDk + 4;                        // floats: eight rows in a row lie in different banks
+constexpr int kJoinUnit = kDeltaMaxDk * kJoinPitch, kJoinBytes = (kJoinUnit + kDeltaMaxDk * 16) * 4;
+
+// starts[i + 1] += units[i] starts[i], segment after segment (DeltaBlock): one block per head and 16 columns,
+// a thread 8 of them of a row; what the next step reads is in flight before this one's results are put down.
+// starts[0] is the caller's state. BACK: starts[i - 1] += units[i]^T starts[i], from the last down. A tile of
+// zeros is not multiplied, so a state of zeros stays one whatever the unit's columns hold.
+template <bool BACK>
+__global__ void __launch_bounds__(2 * kDeltaMaxDk) k_delta_join(DeltaDims d, DeltaLocal w, const float *state) {
+    extern __shared__ __align__(16) float M[];
+    float *S = M + kJoinUnit;                                      // [rows][16]
+    const int tid = threadIdx.x, row = tid & (kDeltaMaxDk - 1), c0 = tid / kDeltaMaxDk * 8, slices = d.Dv / 16;
+    const long long bh = blockIdx.x / slices, base = (bh * d.Dk + row) * d.Dv + blockIdx.x % slices * 16 + c0;
+    const bool live = row < d.Dk;
+    auto slot = [&](int s) { return BACK ? d.segs - 1 - s : s; };  // the s-th in the chain
+    auto fetch = [&](int s) {                                      // what leads to it from the one before
+        if (s >= 2 && s < d.segs) {
+            const float *m = w.units + ((BACK ? d.segs - 1 - s : s - 2) * (long long)d.B * d.H + bh) * d.Dk * d.Dk;
+            const int pieces = d.Dk / 4;
+            for (int i = tid; i < d.Dk * pieces; i += 2 * kDeltaMaxDk)
+                cp_async16_zfill(smem_u32(M) + (i / pieces * kJoinPitch + i % pieces * 4) * 4, m + 4 * i, true);
+        }
+        cp_async_commit();
+    };
+    __align__(16) float x[8] = {}, next[8] = {};
+    auto first = [&](int s) {
+        if (live && s < d.segs && (s > 0 || state)) {
+            const float *from = (s == 0 ? state : w.starts + slot(s) * delta_states(d)) + base;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(next + i) = *reinterpret_cast<const float4 *>(from + i);
+        }
+    };
+    fetch(2);
+    first(0);
+    for (int s = 0; s < d.segs; ++s) {
+        bool some = false;                                         // of the state before
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            some |= x[i] != 0.f;
+            x[i] = next[i];
+        }
+        first(s + 1);
+        cp_async_wait<0>();
+        if (__syncthreads_or(some) && s >= 2) {
+            const float *m = BACK ? M + row : M + row * kJoinPitch;
+#pragma unroll 2
+            for (int k = 0; k < d.Dk; k += 4) {
+                __align__(16) float av[4];
+                if constexpr (BACK) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) av[e] = m[(k + e) * kJoinPitch];
+                } else {
+                    *reinterpret_cast<float4 *>(av) = *reinterpret_cast<const float4 *>(m + k);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    __align__(16) float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(y + i) = *reinterpret_cast<const float4 *>(S + (k + e) * 16 + c0 + i);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = fmaf(av[e], y[i], x[i]);
+                }
+            }
+        }
+        __syncthreads();                                           // M and S are used
+        if (s >= 2) fetch(s + 1);
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(x + i);
+            *reinterpret_cast<float4 *>(S + row * 16 + c0 + i) = y;
+            if (live && s != 1) *reinterpret_cast<float4 *>(w.starts + slot(s) * delta_states(d) + base + i) = y;
+        }
+    }
 }
 
 // float32 rows [b, t, h] of D columns -> three contiguous bfloat16 planes [B, T, heads, D]
@@ -574,12 +664,11 @@ __global__ void __launch_bounds__(256) k_delta_split(DeltaDims d, const float *x
 
 template <typename T, int DKP, int NW, bool SAVE>
 cudaError_t scan_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
-                     const DeltaLocal &w, float *state, T *o, float *snap, float *r, cudaStream_t st) {
+                     const DeltaLocal &w, float *state, T *o, float *snap, float *r, int mode, cudaStream_t st) {
     using L = ScanSmem<T, DKP, NW>;
     auto kern = k_delta_scan<T, DKP, NW, SAVE>;
     set_kernel_smem(kern, L::BYTES);
-    const long long slices = (d.Dv + NW * 16 - 1) / (NW * 16);
-    kern<<<(unsigned)((long long)d.B * d.H * slices), NW * 32, L::BYTES, st>>>(d, in, q, k, w, state, o, snap, r);
+    kern<<<(unsigned)delta_blocks(d, mode, NW * 16), NW * 32, L::BYTES, st>>>(d, in, q, k, w, state, o, snap, r, mode);
     return cudaGetLastError();
 }
 
@@ -590,12 +679,17 @@ cudaError_t scan_any(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q
     // eight warps (two an SM sub-core) share a chunk's loads once there is a block for every SM;
     // with fewer heads four, so that every warp has a tensor core of its own
     const bool wide = d.Dv > 64 && (long long)d.B * d.H * ((d.Dv + 127) / 128) >= kRefSms;
-    auto go = [&](auto dkp, auto nw, auto save) {
+    auto go = [&](auto dkp, auto nw, auto save, int mode) {
         return scan_one<T, decltype(dkp)::value, decltype(nw)::value, decltype(save)::value>(
-            d, in, q, k, w, state, out, snap, r, st);
+            d, in, q, k, w, state, out, snap, r, mode, st);
     };
     auto pick = [&](auto dkp, auto nw) {
-        return snap ? go(dkp, nw, std::true_type{}) : go(dkp, nw, std::false_type{});
+        if (d.segs > 1) {
+            cudaError_t e = go(dkp, nw, std::false_type{}, DELTA_CARRY);
+            if (e == cudaSuccess) e = launch_delta_join(d, w, state, false, st);
+            if (e != cudaSuccess) return e;
+        }
+        return snap ? go(dkp, nw, std::true_type{}, DELTA_RUN) : go(dkp, nw, std::false_type{}, DELTA_RUN);
     };
     auto size = [&](auto dkp) {
         return wide ? pick(dkp, std::integral_constant<int, 8>{}) : pick(dkp, std::integral_constant<int, 4>{});
@@ -639,6 +733,13 @@ cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const Delt
                     : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, no, no);
     };
     return d.Dk <= 64 ? size(integral_constant<int, 64>{}) : size(integral_constant<int, 128>{});
+}
+
+cudaError_t launch_delta_join(const DeltaDims &d, const DeltaLocal &w, const float *state, bool back, cudaStream_t st) {
+    auto kern = back ? k_delta_join<true> : k_delta_join<false>;
+    set_kernel_smem(kern, kJoinBytes);
+    kern<<<(unsigned)((long long)d.B * d.H * (d.Dv / 16)), 2 * kDeltaMaxDk, kJoinBytes, st>>>(d, w, state);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,

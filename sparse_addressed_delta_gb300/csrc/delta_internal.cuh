@@ -53,18 +53,21 @@ struct DeltaLocal {
     unsigned char *x, *p;
     float *aux;
     DevStatus *status;
-    float *starts, *units;               // with segments: their first states [segs][B, H, Dk, Dv], and
-};                                       // what the inner ones make of a unit matrix [segs - 2][B, H, Dk, Dk]
+    // with segments: their first states (a backward: end states' gradients) [segs][B, H, Dk, Dv], and what
+    // the inner ones make of a unit matrix [segs - 2][B, H, Dk, Dk]
+    float *starts, *units;
+};
 
 __host__ __device__ constexpr int delta_chunk(int dtype) { return dtype == SDM_BF16 ? 64 : 32; }
 
-// A sequence in segments (d.segs > 1), for the tcgen05 scan. A segment's end state is linear in its first
-// state, M S + E. A first launch takes every segment but the last from a state of zeros (the first one
-// from the caller's, so it needs no M) to E, and the inner ones' M from a unit matrix with no values; a
-// join makes the first states from these; a second launch runs all segments at once. Segment 0's blocks
-// come last, several after one another where SMs are free; it is first / 256 as long as the others.
+// A sequence in segments (d.segs > 1), for the scans. A segment's end state is linear in its first state,
+// M S + E. A first launch takes every segment but the last from a state of zeros (the first one from the
+// caller's, so it needs no M) to E, and the inner ones' M from a unit matrix with no values; a join
+// (launch_delta_join) makes the first states from these; a second launch runs all segments at once. Segment
+// 0's blocks come last, several after one another where SMs are free; it is first / 256 as long as the others.
+// A backward goes the same way from the end (gradients of a segment's first state are M^T times those of its
+// end, and E), with the M that its forward saved.
 __host__ __device__ inline long long delta_states(const DeltaDims &d) { return (long long)d.B * d.H * d.Dk * d.Dv; }
-__host__ __device__ inline int delta_tiles(const DeltaDims &d) { return (d.Dv + 127) / 128; }
 // first chunk of segment i of a sequence of `chunks`
 __host__ __device__ inline int delta_bound(const DeltaDims &d, int chunks, int i) {
     return i == 0 ? 0 : (int)((long long)chunks * (d.first + (i - 1) * 256) / ((d.segs - 1) * 256 + d.first));
@@ -95,22 +98,29 @@ __device__ __forceinline__ long long delta_longest_first(const DeltaDims &d, con
     return (long long)b * d.H + bh % d.H;
 }
 
-template <bool SEG, bool CARRY>
-__device__ __forceinline__ DeltaBlock delta_block(const DeltaDims &d, const int32_t *valid) {
+enum { DELTA_RUN, DELTA_CARRY, DELTA_CARRY_BACK };                // the second launch, the first ones
+
+__host__ __device__ inline int delta_tiles(int columns, int of) { return (columns + of - 1) / of; }
+inline long long delta_blocks(const DeltaDims &d, int mode, int of) {
+    const long long heads = (long long)d.B * d.H, run = heads * delta_tiles(d.Dv, of);
+    return mode == DELTA_CARRY ? (d.segs - 2) * (run + heads * delta_tiles(d.Dk, of)) + run : mode == DELTA_RUN ? d.segs * run : (d.segs - 1) * run;
+}
+// this block's head, segment and tile of `of` columns, of the state or of a unit matrix
+__device__ __forceinline__ DeltaBlock delta_block(const DeltaDims &d, const int32_t *valid, bool segs, int mode, int of) {
     DeltaBlock k;
-    const int tiles = delta_tiles(d), heads = d.B * d.H;
-    // the first launch: per inner segment and head, the state's tiles and a unit matrix
-    const int per = CARRY ? tiles + 1 : tiles, inner = !SEG ? 0 : CARRY ? d.segs - 2 : d.segs - 1;
+    const int tiles = delta_tiles(d.Dv, of), heads = d.B * d.H;
+    const int per = mode == DELTA_CARRY ? tiles + delta_tiles(d.Dk, of) : tiles;
+    const int inner = !segs ? 0 : mode == DELTA_CARRY ? d.segs - 2 : d.segs - 1;
     unsigned i = blockIdx.x;
-    const bool first = !SEG || i >= (unsigned)(inner * heads * per);
+    const bool first = !segs || i >= (unsigned)(inner * heads * per);
     if (first) i -= inner * heads * per;
-    const int of = first ? tiles : per;
-    k.tile = (int)(i % of);
-    i /= of;
-    k.bh = delta_longest_first(d, valid, SEG ? i % heads : i);
+    const int each = first ? tiles : per;
+    k.tile = (int)(i % each);
+    i /= each;
+    k.bh = delta_longest_first(d, valid, segs ? i % heads : i);
     k.seg = first ? 0 : 1 + (int)(i / heads);
-    k.unit = CARRY && !first && k.tile == tiles;
-    if (k.unit) k.tile = 0;
+    k.unit = mode == DELTA_CARRY && k.tile >= tiles;
+    if (k.unit) k.tile -= tiles;
     return k;
 }
 
@@ -129,6 +139,10 @@ cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const Delt
 cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                               const DeltaPlanes &k, const DeltaLocal &w, float *state, void *o,
                               float *snap, float *r, cudaStream_t st);
+
+// the segments' first states (back: end states' gradients) into w.starts; state: the first (back: the last,
+// null: 0) of them
+cudaError_t launch_delta_join(const DeltaDims &d, const DeltaLocal &w, const float *state, bool back, cudaStream_t st);
 
 cudaError_t launch_delta_scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state,
                                  void *o, float *snap, float *r, cudaStream_t st);

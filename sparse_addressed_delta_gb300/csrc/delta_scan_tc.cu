@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int *dead = reinterpret_cast<int *>(bar + B_COUNT);
     auto slot = reinterpret_cast<uint32_t *>(bar + B_COUNT + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const DeltaBlock blk = delta_block<SEG, CARRY>(d, in.valid);
+    const DeltaBlock blk = delta_block(d, in.valid, SEG, CARRY ? DELTA_CARRY : DELTA_RUN, 128);
     const int dv_blk = blk.tile * 128, seg = blk.seg, width = CARRY && blk.unit ? d.Dk : d.Dv;
     const long long bh = blk.bh;
     const int b = (int)(bh / d.H), h = (int)(bh % d.H), hk = h / (d.H / d.Hk);
@@ -421,74 +421,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == kTcWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
 }
 
-constexpr int kJoinPitch = kDeltaMaxDk + 4;                        // floats: eight rows in a row lie in different banks
-constexpr int kJoinUnit = kDeltaMaxDk * kJoinPitch, kJoinBytes = (kJoinUnit + kDeltaMaxDk * 16) * 4;
-
-// starts[i + 1] += units[i] starts[i], segment after segment (DeltaBlock): one block per head and 16 columns,
-// a thread 8 of them of a row; what the next step reads is in flight before this one's results are put down.
-// starts[0] is the caller's state. A tile of zeros is not multiplied, so a state of zeros stays one whatever
-// the unit's columns hold.
-__global__ void __launch_bounds__(2 * kDeltaMaxDk) k_delta_join(DeltaDims d, DeltaLocal w, const float *state) {
-    extern __shared__ __align__(16) float M[];
-    float *S = M + kJoinUnit;                                      // [rows][16]
-    const int tid = threadIdx.x, row = tid & (kDeltaMaxDk - 1), c0 = tid / kDeltaMaxDk * 8, slices = d.Dv / 16;
-    const long long bh = blockIdx.x / slices, base = (bh * d.Dk + row) * d.Dv + blockIdx.x % slices * 16 + c0;
-    const bool live = row < d.Dk;
-    auto fetch = [&](int s) {                                      // what leads from segment s - 1 to s
-        if (s >= 2 && s < d.segs) {
-            const float *m = w.units + ((s - 2) * (long long)d.B * d.H + bh) * d.Dk * d.Dk;
-            const int pieces = d.Dk / 4;
-            for (int i = tid; i < d.Dk * pieces; i += 2 * kDeltaMaxDk)
-                cp_async16_zfill(smem_u32(M) + (i / pieces * kJoinPitch + i % pieces * 4) * 4, m + 4 * i, true);
-        }
-        cp_async_commit();
-    };
-    __align__(16) float x[8] = {}, next[8] = {};
-    auto first = [&](int s) {
-        if (live && s < d.segs) {
-            const float *from = (s == 0 ? state : w.starts + s * delta_states(d)) + base;
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(next + i) = *reinterpret_cast<const float4 *>(from + i);
-        }
-    };
-    fetch(2);
-    first(0);
-    for (int s = 0; s < d.segs; ++s) {
-        bool some = false;                                         // of the state before
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            some |= x[i] != 0.f;
-            x[i] = next[i];
-        }
-        first(s + 1);
-        cp_async_wait<0>();
-        if (__syncthreads_or(some) && s >= 2) {
-            const float *m = M + row * kJoinPitch;
-#pragma unroll 2
-            for (int k = 0; k < d.Dk; k += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(m + k);
-                const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    __align__(16) float y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(y + i) = *reinterpret_cast<const float4 *>(S + (k + e) * 16 + c0 + i);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = fmaf(av[e], y[i], x[i]);
-                }
-            }
-        }
-        __syncthreads();                                           // M and S are used
-        if (s >= 2) fetch(s + 1);
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(x + i);
-            *reinterpret_cast<float4 *>(S + row * 16 + c0 + i) = y;
-            if (live && s != 1) *reinterpret_cast<float4 *>(w.starts + s * delta_states(d) + base + i) = y;
-        }
-    }
-}
-
 template <int DKP>
 cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, float *state, void *o, float *snap,
                     float *r, cudaStream_t st) {
@@ -499,22 +431,18 @@ cudaError_t scan_tc(const DeltaDims &d, const DeltaIn &in, const DeltaLocal &w, 
     if (e == cudaSuccess) e = tc_tensor_map(&mv, in.v, d.vs, d.B, d.T, d.H, d.Dv);
     if (e == cudaSuccess) e = tc_tensor_map(&mo, o, os, d.B, d.T, d.H, d.Dv);
     if (e != cudaSuccess) return e;
-    const long long heads = (long long)d.B * d.H, blocks = heads * delta_tiles(d);
-    auto run = [&](auto kern, long long grid) {
+    auto run = [&](auto kern, int mode) {
         set_kernel_smem(kern, TcScan<DKP>::BYTES);
-        kern<<<(unsigned)grid, kTcThreads, TcScan<DKP>::BYTES, st>>>(mq, mk, mv, mo, d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, r);
+        kern<<<(unsigned)delta_blocks(d, mode, 128), kTcThreads, TcScan<DKP>::BYTES, st>>>(mq, mk, mv, mo, d, in, w, state, static_cast<__nv_bfloat16 *>(o), snap, r);
         return cudaGetLastError();
     };
     if (d.segs > 1) {
-        e = run(k_delta_scan_tc<DKP, SCAN_CARRY, true>, (d.segs - 2) * (blocks + heads) + blocks);
+        e = run(k_delta_scan_tc<DKP, SCAN_CARRY, true>, DELTA_CARRY);
+        if (e == cudaSuccess) e = launch_delta_join(d, w, state, false, st);
         if (e != cudaSuccess) return e;
-        set_kernel_smem(k_delta_join, kJoinBytes);
-        k_delta_join<<<(unsigned)(heads * (d.Dv / 16)), 2 * kDeltaMaxDk, kJoinBytes, st>>>(d, w, state);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        return snap ? run(k_delta_scan_tc<DKP, SCAN_SAVE, true>, d.segs * blocks) : run(k_delta_scan_tc<DKP, SCAN_READ, true>, d.segs * blocks);
+        return snap ? run(k_delta_scan_tc<DKP, SCAN_SAVE, true>, DELTA_RUN) : run(k_delta_scan_tc<DKP, SCAN_READ, true>, DELTA_RUN);
     }
-    return snap ? run(k_delta_scan_tc<DKP, SCAN_SAVE, false>, blocks) : run(k_delta_scan_tc<DKP, SCAN_READ, false>, blocks);
+    return snap ? run(k_delta_scan_tc<DKP, SCAN_SAVE, false>, DELTA_RUN) : run(k_delta_scan_tc<DKP, SCAN_READ, false>, DELTA_RUN);
 }
 
 }  // namespace

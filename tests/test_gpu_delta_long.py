@@ -6,14 +6,16 @@ import pytest
 import torch
 
 import sparse_addressed_delta_gb300 as sdm
-from test_gpu_delta import call, check, draw
+from oracle import delta as od
+from test_gpu_delta import call, check, draw, err, host
+from test_gpu_delta_backward import GATE, GRAD, GRAD_F32, grads, train
 from test_gpu_delta_backward import check as check_train
-from test_gpu_delta_backward import grads
 
 pytestmark = pytest.mark.gpu
 
 # B, T, Hk, H, Dk, Dv
-SHAPES = [(1, 2048, 1, 2, 128, 128), (1, 1500, 1, 1, 64, 80), (2, 1281, 1, 2, 128, 320), (1, 2111, 6, 6, 80, 144), (1, 1800, 8, 32, 64, 128)]
+SHAPES = [(1, 2048, 1, 2, 128, 128), (1, 1500, 1, 1, 64, 80), (2, 1281, 1, 2, 128, 320), (1, 2111, 6, 6, 80, 144),
+          (1, 1700, 1, 3, 48, 48), (1, 1800, 8, 32, 64, 128)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -23,30 +25,55 @@ def _cuda():
     sdm.library()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
-def test_forward(shape):
-    x = draw(*shape, "bf16", seed=sum(shape), decay=0.001)
-    first, again = check(x, "bf16"), call(x)
+def test_forward(dtype, shape):
+    x = draw(*shape, dtype, seed=sum(shape), decay=0.001)
+    first, again = check(x, dtype), call(x)
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
-    # the state reaches the end: without it the readings are others
+    # the state reaches the end: without it the last one is another
     x["state"].zero_()
     assert not torch.equal(call(x)[1], first[1])
 
 
-@pytest.mark.parametrize("shape", SHAPES[:4], ids=str)
-def test_backward(shape):
-    x = draw(*shape, "bf16", seed=sum(shape), decay=0.001)
-    check_train(x, *grads(shape, "bf16"), "bf16")
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES[:-1], ids=str)
+def test_backward(dtype, shape):
+    x = draw(*shape, dtype, seed=sum(shape), decay=0.001)
+    do, dS = grads(shape, dtype)
+    o, state, g = check_train(x, do, dS, dtype)
+    plain = call(x)
+    assert torch.equal(plain[0], o) and torch.equal(plain[1], state)
+    again = train(x, do, dS)[2]
+    assert all(torch.equal(again[n], g[n]) for n in g)
+    check_train(x, do, None, dtype)
 
 
-def test_valid_tokens():
+def test_backward_of_another_layout():
+    """What is saved depends on the shape alone: a forward of queries and keys whose strides no tensor copy takes
+    (a broadcast head), and a backward of their contiguous copies."""
+    shape = (1, 1500, 2, 2, 64, 128)
+    x = draw(*shape, "bf16", seed=3, decay=0.001)
+    do, dS = grads(shape, "bf16")
+    x["q"], x["k"] = x["q"][:, :, :1].contiguous().expand(-1, -1, 2, -1), x["k"][:, :, :1].contiguous().expand(-1, -1, 2, -1)
+    args = lambda y: (y["q"], y["k"], y["v"], y["g"], y["beta"], None)  # noqa: E731
+    y = dict(x, q=x["q"].contiguous(), k=x["k"].contiguous())
+    saved = sdm.gated_delta_save(x["state"].clone(), *args(x))[1]
+    got = sdm.gated_delta_backward(*args(y), saved, do, grad_state=dS)
+    want = od.gated_delta_backward(**{n: host(t) for n, t in x.items()}, do=host(do), dS=host(dS), valid=None, scale=64 ** -0.5)
+    for n, a in got.items():
+        assert err(a, want[n]) <= (GATE if n == "grad_log_decay" else GRAD["bf16"] if a.dtype == torch.bfloat16 else GRAD_F32), n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_valid_tokens(dtype):
     """Lengths from none to all of them: segments of a single chunk, and of none."""
     shape = (6, 1900, 1, 2, 64, 128)
-    x = draw(*shape, "bf16", seed=5, decay=0.001)
+    x = draw(*shape, dtype, seed=5, decay=0.001)
     valid = [1900, 0, 1, 65, 700, 1899]
-    o, state = check(x, "bf16", valid)
-    do, dS = grads(shape, "bf16")
-    trained = check_train(x, do, dS, "bf16", valid)
+    o, state = check(x, dtype, valid)
+    do, dS = grads(shape, dtype)
+    trained = check_train(x, do, dS, dtype, valid)
     assert torch.equal(trained[0], o) and torch.equal(trained[1], state)
     for name in ("q", "k", "v", "g", "beta"):
         for b, n in enumerate(valid):
@@ -56,13 +83,14 @@ def test_valid_tokens():
     assert torch.equal(got[1][1], x["state"][1])
 
 
-def test_resets():
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_resets(dtype):
     """A reset inside a segment and one at every token."""
-    x = draw(1, 1600, 1, 2, 128, 128, "bf16", seed=9, decay=0.001)
+    x = draw(1, 1600, 1, 2, 128, 128, dtype, seed=9, decay=0.001)
     x["g"][0, 777, 0] = -torch.inf
     x["g"][0, :, 1] = -torch.inf
-    check(x, "bf16")
-    check_train(x, *grads((1, 1600, 1, 2, 128, 128), "bf16"), "bf16")
+    check(x, dtype)
+    check_train(x, *grads((1, 1600, 1, 2, 128, 128), dtype), dtype)
 
 
 def test_nothing_written_stays_nothing():
