@@ -170,9 +170,7 @@ cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaLayout
     w = DeltaLocal{ws + l.x, ws + l.p, reinterpret_cast<float *>(ws + l.aux), reinterpret_cast<DevStatus *>(ws),
                    reinterpret_cast<float *>(ws + l.starts), reinterpret_cast<float *>(ws + l.units)};
     if (d.dtype == SDM_F32) {
-        cudaError_t e = launch_delta_split(d, in.q, d.qs, d.Hk, d.Dk, const_cast<__nv_bfloat16 *>(q.p), st);
-        if (e == cudaSuccess)
-            e = launch_delta_split(d, in.k, d.ks, d.Hk, d.Dk, const_cast<__nv_bfloat16 *>(k.p), st);
+        const cudaError_t e = launch_delta_split(d, in.q, in.k, const_cast<__nv_bfloat16 *>(q.p), const_cast<__nv_bfloat16 *>(k.p), st);
         if (e != cudaSuccess) return e;
     }
     return launch_delta_local(d, in, q, k, w, st);

@@ -688,9 +688,11 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
         }
 }
 
-// value heads that share a key head: their parts added in head order
+// value heads that share a key head: their parts of the gradients of q and k (blockIdx.y) added in head order
 template <typename T>
-__global__ void __launch_bounds__(256) k_delta_heads(const float *part, T *out, long long rows, int Hk, int group, int Dk) {
+__global__ void __launch_bounds__(256) k_delta_heads(DeltaBack o, long long rows, int Hk, int group, int Dk) {
+    const float *part = blockIdx.y ? o.dk : o.dq;
+    T *out = static_cast<T *>(blockIdx.y ? o.grad_k : o.grad_q);
     const long long all = rows * Hk * (Dk / 4);
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
         const int c = (int)(i % (Dk / 4)) * 4;
@@ -732,9 +734,8 @@ cudaError_t back_local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPla
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || d.H == d.Hk) return e;
     const long long rows = (long long)d.B * d.T, units = rows * d.Hk * (d.Dk / 4), blocks = (units + 255) / 256;
-    const unsigned grid = (unsigned)(blocks < 8 * kRefSms ? blocks : 8 * kRefSms);
-    k_delta_heads<T><<<grid, 256, 0, st>>>(o.dq, static_cast<T *>(o.grad_q), rows, d.Hk, d.H / d.Hk, d.Dk);
-    k_delta_heads<T><<<grid, 256, 0, st>>>(o.dk, static_cast<T *>(o.grad_k), rows, d.Hk, d.H / d.Hk, d.Dk);
+    const unsigned grid = (unsigned)(blocks < 4 * kRefSms ? blocks : 4 * kRefSms);
+    k_delta_heads<T><<<dim3(grid, 2), 256, 0, st>>>(o, rows, d.Hk, d.H / d.Hk, d.Dk);
     return cudaGetLastError();
 }
 

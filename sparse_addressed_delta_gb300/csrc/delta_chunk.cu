@@ -645,9 +645,14 @@ __global__ void __launch_bounds__(2 * kDeltaMaxDk) k_delta_join(DeltaDims d, Del
     }
 }
 
-// float32 rows [b, t, h] of D columns -> three contiguous bfloat16 planes [B, T, heads, D]
-__global__ void __launch_bounds__(256) k_delta_split(DeltaDims d, const float *x, long long sb, long long st,
-                                                     long long sh, int heads, int D, __nv_bfloat16 *planes) {
+// float32 queries and keys (blockIdx.y), rows [b, t, h] of Dk columns -> three contiguous bfloat16 planes [B, T,
+// Hk, Dk] each
+__global__ void __launch_bounds__(256) k_delta_split(DeltaDims d, const float *q, const float *k,
+                                                     __nv_bfloat16 *q_planes, __nv_bfloat16 *k_planes) {
+    const float *x = blockIdx.y ? k : q;
+    const long long sb = blockIdx.y ? d.ks[0] : d.qs[0], st = blockIdx.y ? d.ks[1] : d.qs[1], sh = blockIdx.y ? d.ks[2] : d.qs[2];
+    __nv_bfloat16 *planes = blockIdx.y ? k_planes : q_planes;
+    const int heads = d.Hk, D = d.Dk;
     const long long all = (long long)d.B * d.T * heads * (D / 4), plane = all * 4;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
         const long long row = i / (D / 4), h = row % heads, bt = row / heads, t = bt % d.T, b = bt / d.T;
@@ -748,11 +753,10 @@ cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const Delta
                                : scan_any<float>(d, in, q, k, w, state, o, snap, r, st);
 }
 
-cudaError_t launch_delta_split(const DeltaDims &d, const void *x, const long long *s, int heads, int D,
-                               __nv_bfloat16 *planes, cudaStream_t st) {
-    const long long units = (long long)d.B * d.T * heads * (D / 4), blocks = (units + 255) / 256;
-    k_delta_split<<<(unsigned)(blocks < 8 * kRefSms ? blocks : 8 * kRefSms), 256, 0, st>>>(
-        d, static_cast<const float *>(x), s[0], s[1], s[2], heads, D, planes);
+cudaError_t launch_delta_split(const DeltaDims &d, const void *q, const void *k, __nv_bfloat16 *q_planes, __nv_bfloat16 *k_planes, cudaStream_t st) {
+    const long long units = (long long)d.B * d.T * d.Hk * (d.Dk / 4), blocks = (units + 255) / 256;
+    k_delta_split<<<dim3((unsigned)(blocks < 4 * kRefSms ? blocks : 4 * kRefSms), 2), 256, 0, st>>>(
+        d, static_cast<const float *>(q), static_cast<const float *>(k), q_planes, k_planes);
     return cudaGetLastError();
 }
 

@@ -130,8 +130,8 @@ inline size_t delta_plane_bytes(const DeltaDims &d) { return (size_t)d.C * (d.C 
 
 cudaError_t launch_delta_step(const DeltaDims &d, const DeltaIn &in, float *state, void *o,
                               cudaStream_t st);
-cudaError_t launch_delta_split(const DeltaDims &d, const void *x, const long long *s, int heads,
-                               int D, __nv_bfloat16 *planes, cudaStream_t st);
+cudaError_t launch_delta_split(const DeltaDims &d, const void *q, const void *k, __nv_bfloat16 *q_planes,
+                               __nv_bfloat16 *k_planes, cudaStream_t st);
 cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                                const DeltaPlanes &k, const DeltaLocal &w, cudaStream_t st);
 // snap [B, H, Nt + 1, Dk, Dv] the state at each chunk's start and, behind the last chunk with tokens, the
