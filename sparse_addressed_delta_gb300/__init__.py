@@ -13,6 +13,7 @@ Main entry point: :func:`sdm_write_read` (sparse-delta-memory 2.0.0, memory_ops.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 import threading
@@ -66,11 +67,12 @@ class _DeviceStatus(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_fast = None
 
 
 def library() -> ctypes.CDLL:
     """The loaded libsdm.so (built in-tree by ``__graft_entry__.build()``)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -151,8 +153,22 @@ def library() -> ctypes.CDLL:
             lib.sdm_last_error.restype = ctypes.c_char_p
             lib.sdm_version.argtypes = []
             lib.sdm_version.restype = ctypes.c_char_p
+            _fast = _calls(lib)
             _lib = lib
     return _lib
+
+
+def _calls(lib: ctypes.CDLL):
+    """The module of the everyday calls (csrc/calls.cpp), built beside the library."""
+    spec = importlib.util.spec_from_file_location("_calls", os.path.join(_HERE, "_calls.so"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    at = lambda *names: tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names)  # noqa: E731
+    mod.setup((torch.Tensor, torch.nn.Parameter), (torch.float32, torch.bfloat16, torch.int32, torch.uint8),
+              (torch.empty, torch.empty_like, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream, _check),
+              DELTA_STEP_TOKENS, at("sdm_gated_delta", "sdm_gated_delta_workspace_bytes", "sdm_layer_norm",
+                                    "sdm_layer_norm_backward", "sdm_layer_norm_workspace_bytes"))
+    return mod
 
 
 def version() -> str:
@@ -692,8 +708,9 @@ def bank_sum(x: torch.Tensor, stream=None) -> torch.Tensor:
 # ------------------------------------------------------------------------------------------
 # the gated delta rule: the write/read's recurrence with dense keys
 # ------------------------------------------------------------------------------------------
-# A single token's kernel takes a few microseconds, so the checks below read each tensor property
-# once, and the shape goes to the library as packed bytes (include/sdm.h, sdm_delta_shape).
+# A single token's kernel takes a few microseconds, so calls whose arguments are all in order go through
+# csrc/calls.cpp; all others, and those with buffers of the caller's, through the checks below, which read each
+# tensor property once. The shape goes to the library as packed bytes (include/sdm.h, sdm_delta_shape).
 
 _DELTA_SHAPE = struct.Struct("=7if18q")
 
@@ -812,10 +829,14 @@ def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.
     if stream is not None:
         return _on(stream, gated_delta, state, q, k, v, log_decay, beta, valid_tokens, scale=scale,
                    readings=readings, workspace=workspace)
+    lib = library()
+    if workspace is None:
+        o = _fast.gated_delta(state, q, k, v, log_decay, beta, valid_tokens, scale, readings)
+        if o is not None:
+            return o
     shape, (B, T, H, Hk, Dk, Dv), dev, dt = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
     readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
-    lib = library()
     ws, n = (None, 0) if T <= DELTA_STEP_TOKENS else _scratch(workspace, lib.sdm_gated_delta_workspace_bytes, dev, shape)
     _call(lib.sdm_gated_delta, dev, shape, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_decay.data_ptr(), beta.data_ptr(), _at(valid_tokens), readings.data_ptr(), _at(ws), n)
@@ -938,6 +959,11 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     belongs to ``stream`` (None: the current one)."""
     if stream is not None:
         return _on(stream, layer_norm, x, weight, bias, eps=eps, out=out)
+    if out is None:
+        library()
+        y = _fast.layer_norm(x, weight, bias, eps, False)
+        if y is not None:
+            return y
     return _layer_norm(x, weight, bias, eps, out, None)
 
 
@@ -947,6 +973,11 @@ def layer_norm_save(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     """layer_norm that also returns what its backward needs: (y, stats [..., 2] float32)."""
     if stream is not None:
         return _on(stream, layer_norm_save, x, weight, bias, eps=eps, out=out)
+    if out is None:
+        library()
+        both = _fast.layer_norm(x, weight, bias, eps, True)
+        if both is not None:
+            return both
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")
     stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device)
@@ -960,6 +991,11 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: Optional[to
     them, grad_weight and (``bias``) grad_bias, float32 [n], summed over the rows in a fixed order."""
     if stream is not None:
         return _on(stream, layer_norm_backward, grad, x, weight, stats, bias=bias, workspace=workspace)
+    if workspace is None:
+        library()
+        out = _fast.layer_norm_backward(grad, x, weight, stats, bias)
+        if out is not None:
+            return out
     rows, n, step = _norm_rows(x, "x")
     gstep = _norm_rows(grad, "grad")[2]
     dt, dev = x.dtype, x.device

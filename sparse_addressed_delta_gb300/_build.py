@@ -1,4 +1,5 @@
-"""Builds libsdm.so (the sm_103a kernels and the C ABI) in-tree with nvcc.
+"""Builds libsdm.so (the sm_103a kernels and the C ABI) in-tree with nvcc, and _calls.so (the CPython module
+of the everyday calls, csrc/calls.cpp) with g++.
 
 One object per translation unit, compiled in parallel, linked into a shared library next to
 this file. Nothing is installed.
@@ -9,6 +10,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdm.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["api.cu", "phase1.cu", "solve.cu", "phase2.cu", "dualmm_tc.cu", "phase2_fused.cu",
            "noalloc.cu", "backward.cu", "host_io.cu", "layer_io.cu", "product_key.cu",
            "norm.cu", "delta.cu", "delta_step.cu", "delta_chunk.cu",
@@ -48,7 +51,7 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     deps = _deps()
-    if not force and not _stale(LIB, deps):
+    if not force and not _stale(LIB, deps) and not _stale(CALLS, deps):
         return LIB
     nvcc = _nvcc()
 
@@ -62,8 +65,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout, r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    def build_calls():
+        tmp = CALLS + f".tmp{os.getpid()}"
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+               "-I", INCLUDE, os.path.join(CSRC, "calls.cpp"), "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALLS)
+
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        calls = ex.submit(build_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
