@@ -45,20 +45,47 @@ __device__ __forceinline__ void unpack(const Vec<T, VEC> &r, float *o) {
 
 // A thread's own pieces of the rows ahead: `stage` holds NV vectors of each of ROWS tensors (and 8 bytes
 // of statistics) at [vector][thread].
-template <typename T, int VEC, int NV, int ROWS, bool STATS>
+// HULL: rows one behind the other whose length is no multiple of 16 bytes. A row is then copied from the 16-byte
+// boundary at or before its start (bytes of the row before; the first row starts on one), and its threads read
+// their elements from what they all copied, so they wait for one another. Forward and backward, us, by each
+// thread's own pieces and by hulls: 65536 x 1007 float32 121 + 193, 111 + 160; bfloat16 147 + 234, 114 + 142;
+// 16384 x 4099 bfloat16 220 + 433, 146 + 226. (Results put back and stored in whole pieces: no better, 121 + 136
+// and 142 + 218, and 126 + 153 for float32.)
+template <typename T, int VEC, int NV, int ROWS, bool STATS, bool HULL>
 struct RowRing {
     static constexpr int VB = VEC * (int)sizeof(T), ROW = NV * VB, THREAD = ROWS * ROW + (STATS ? 8 : 0);
+    static __host__ __device__ size_t hull(int n) { return ((size_t)n * sizeof(T) + 30) / 16 * 16; }
+    // bytes of the block: of rows (HULL), of the threads' pieces and statistics
+    static __host__ __device__ size_t stage_bytes(int n, int threads, int rows) {
+        return HULL ? (size_t)ROWS * rows * hull(n) + (STATS ? 8 : 0) * threads : (size_t)THREAD * threads;
+    }
     unsigned char *base;               // of the block
     int t, tpr, n;                     // thread of the row, threads of the row, columns
+    int sub, rpb;                      // row of the block, rows of a block
+
+    __device__ __forceinline__ unsigned char *row_at(int stage, int which) const {
+        return base + stage * stage_bytes(n, blockDim.x, rpb) + (which * rpb + sub) * hull(n);
+    }
 
     __device__ __forceinline__ unsigned char *at(int stage, int vector) const {
         return base + ((size_t)stage * THREAD) * blockDim.x + ((size_t)vector * blockDim.x + threadIdx.x) * VB;
     }
     __device__ __forceinline__ unsigned char *stats_at(int stage) const {
+        if (HULL) return base + stage * stage_bytes(n, blockDim.x, rpb) + ROWS * rpb * hull(n) + 8 * threadIdx.x;
         return base + ((size_t)stage * THREAD + ROWS * ROW) * blockDim.x + 8 * threadIdx.x;
     }
     // row `which` of `stage`; 0 past the row's end, or when the row is not live
     __device__ __forceinline__ void fetch(int stage, int which, const T *row, bool live) const {
+        if constexpr (HULL) {
+            const int shift = (int)((uintptr_t)row & 15), bytes = live ? shift + n * (int)sizeof(T) : (int)hull(n);
+            const unsigned char *src = reinterpret_cast<const unsigned char *>(row) - shift;
+            const unsigned dst = smem_u32(row_at(stage, which));
+            for (int at = 16 * t; at < bytes; at += 16 * tpr) {
+                const int take = !live ? 0 : bytes - at < 16 ? bytes - at : 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + at), "l"(src + at), "r"(take) : "memory");
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
@@ -76,7 +103,17 @@ struct RowRing {
     __device__ __forceinline__ void fetch_stats(int stage, const float2 *p, bool live) const {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(stats_at(stage))), "l"(p), "r"(live ? 8 : 0) : "memory");
     }
-    __device__ __forceinline__ void read(int stage, int which, float *o) const {
+    __device__ __forceinline__ void read(int stage, int which, const T *row, float *o) const {
+        if constexpr (HULL) {
+            const unsigned char *at = row_at(stage, which) + ((uintptr_t)row & 15);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * tpr + t) * VEC;
+                const Vec<T, VEC> r = c < n ? *reinterpret_cast<const Vec<T, VEC> *>(at + c * sizeof(T)) : Vec<T, VEC>{};
+                unpack<T, VEC>(r, o + i * VEC);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Vec<T, VEC> r = *reinterpret_cast<const Vec<T, VEC> *>(at(stage, which * NV + i));
@@ -155,7 +192,17 @@ __device__ __forceinline__ void row_sum(float (&v)[M], int tpr, float *red, int 
     }
 }
 
-template <typename T, int VEC, int NV, bool BLOCK>
+// the next row's pieces are there; with HULL, all its threads' (who are then also done with the row before)
+template <bool HULL, bool BLOCK, int PENDING>
+__device__ __forceinline__ void row_ready() {
+    cp_async_wait<PENDING>();
+    if constexpr (HULL) {
+        if constexpr (BLOCK) __syncthreads();
+        else __syncwarp();
+    }
+}
+
+template <typename T, int VEC, int NV, bool BLOCK, bool HULL>
 __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
     k_norm(const T *x, long long xs, long long rows, int n, int tpr, const void *w, const void *b,
            bool wf32, float eps, T *y, float2 *stats) {
@@ -181,7 +228,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
         if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = warp_cols;
         __syncthreads();
     }
-    const RowRing<T, VEC, NV, 1, false> ring{ring_smem, t, tpr, n};
+    const RowRing<T, VEC, NV, 1, false, HULL> ring{ring_smem, t, tpr, n, sub, rpb};
     long long base = (long long)blockIdx.x * rpb;
     auto fetch = [&](int stage, long long row) {
         ring.fetch(stage, 0, x + (row < rows ? row : 0) * xs, row < rows);
@@ -191,10 +238,11 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
     for (int i = 0; i < ST - 1; ++i) fetch(i, base + sub + i * step);
     for (int stage = 0; base < rows; base += step, stage = (stage + 1) % ST) {
         const long long row = base + sub;
+        if constexpr (HULL) row_ready<HULL, BLOCK, ST - 2>();
         fetch((stage + ST - 1) % ST, row + (ST - 1) * step);
-        cp_async_wait<ST - 1>();
+        if constexpr (!HULL) row_ready<HULL, BLOCK, ST - 1>();
         float v[E];
-        ring.read(stage, 0, v);
+        ring.read(stage, 0, x + row * xs, v);
         float s[1] = {0.f}, mean, m2;
 #pragma unroll
         for (int j = 0; j < E; ++j) s[0] += v[j];
@@ -248,13 +296,13 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
 }
 
 // part [blocks][2][n]: the block's column sums of dy xhat and of dy
-template <typename T, int VEC, int NV, bool BLOCK, bool WIDE>
+template <typename T, int VEC, int NV, bool BLOCK, bool WIDE, bool HULL>
 __global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
     k_norm_bwd(const T *dy, long long ds, const T *x, long long xs, long long rows, int n, int tpr,
                const void *w, bool wf32, const float2 *stats, T *dx, float *part) {
     constexpr int E = VEC * NV, ST = kNormStages<T>;
     extern __shared__ __align__(16) unsigned char ring_smem[];
-    using Ring = RowRing<T, VEC, NV, 2, true>;
+    using Ring = RowRing<T, VEC, NV, 2, true, HULL>;
     // WIDE: no ring, the column sums [2][n]; else they take the ring's place at the end
     float *cols = reinterpret_cast<float *>(ring_smem);
     __shared__ float red[2 * 2 * 32];
@@ -271,7 +319,7 @@ __global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
 #pragma unroll
         for (int j = 0; j < E; ++j) aw[j] = ab[j] = 0.f;
     }
-    const Ring ring{ring_smem, t, tpr, n};
+    const Ring ring{ring_smem, t, tpr, n, sub, rpb};
     long long base = (long long)blockIdx.x * rpb;
     auto fetch = [&](int stage, long long row) {
         const bool live = row < rows;
@@ -293,11 +341,12 @@ __global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
             load_row<T, VEC, NV>(x + row * xs, t, tpr, n, h);
             load_row<T, VEC, NV>(dy + row * ds, t, tpr, n, g);
         } else {
+            if constexpr (HULL) row_ready<HULL, BLOCK, ST - 2>();
             fetch((stage + ST - 1) % ST, row + (ST - 1) * step);
-            cp_async_wait<ST - 1>();
+            if constexpr (!HULL) row_ready<HULL, BLOCK, ST - 1>();
             ns = *reinterpret_cast<const float2 *>(ring.stats_at(stage));
-            ring.read(stage, 0, h);
-            ring.read(stage, 1, g);
+            ring.read(stage, 0, x + row * xs, h);
+            ring.read(stage, 1, dy + row * ds, g);
         }
         const float mean = ns.x, rstd = ns.y;
 #pragma unroll
@@ -395,6 +444,7 @@ __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
 
 struct NormGeom {
     int vec;        // elements per vector
+    bool hull;      // copied from 16-byte boundaries all the same (RowRing)
     int e;          // elements per thread
     int tpr;        // threads per row
     bool block;     // a row belongs to a whole block
@@ -406,6 +456,7 @@ struct NormGeom {
 NormGeom norm_geom(int n, int vec, bool backward) {
     NormGeom g;
     g.vec = vec;
+    g.hull = false;
     g.e = !backward && n > 16 * kNormBlock ? 32 : 16;
     const int need = (n + g.e - 1) / g.e;
     if (need <= 32) {
@@ -462,10 +513,15 @@ int norm_status(cudaError_t e) {
     return set_error(SDM_ERR_CUDA, "layer norm: %s", cudaGetErrorString(e));
 }
 
-template <typename T, int VEC, int E>
+// rows that no 16-byte vector divides, one behind the other from a 16-byte boundary
+bool norm_hull(int es, int vec, int n, long long stride, const void *p) {
+    return vec * es < 16 && stride == n && (uintptr_t)p % 16 == 0;
+}
+
+template <typename T, int VEC, int E, bool HULL>
 void norm_launch(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
                  const void *b, bool wf32, float eps, T *y, float2 *stats, cudaStream_t st) {
-    const size_t smem = (size_t)kNormStages<T> * E * sizeof(T) * g.threads;
+    const size_t smem = kNormStages<T> * RowRing<T, VEC, E / VEC, 1, false, HULL>::stage_bytes(n, g.threads, g.rpb);
     const long long need = (rows + g.rpb - 1) / g.rpb;
     auto go = [&](auto kern) {
         set_kernel_smem(kern, smem);
@@ -477,8 +533,8 @@ void norm_launch(const NormGeom &g, const T *x, long long xs, long long rows, in
         const unsigned grid = (unsigned)(need < most ? need : most);
         kern<<<grid, g.threads, smem, st>>>(x, xs, rows, n, g.tpr, w, b, wf32, eps, y, stats);
     };
-    if (g.block) go(k_norm<T, VEC, E / VEC, true>);
-    else go(k_norm<T, VEC, E / VEC, false>);
+    if (g.block) go(k_norm<T, VEC, E / VEC, true, HULL>);
+    else go(k_norm<T, VEC, E / VEC, false, HULL>);
 }
 
 template <typename T>
@@ -487,8 +543,15 @@ void norm_forward(const NormGeom &g, const T *x, long long xs, long long rows, i
     constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
     auto go = [&](auto vec) {
         constexpr int VEC = decltype(vec)::value;
-        if (g.e == 32) norm_launch<T, VEC, 32>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
-        else norm_launch<T, VEC, 16>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
+        auto with = [&](auto hull) {
+            constexpr bool HULL = decltype(hull)::value;
+            if (g.e == 32) norm_launch<T, VEC, 32, HULL>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
+            else norm_launch<T, VEC, 16, HULL>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
+        };
+        // wide rows of bfloat16 pairs fare better by their own pieces (8192 x 8190: 97 us, 117 by hulls)
+        if constexpr (VEC < V16)
+            if (g.hull && !(VEC == 2 && g.e == 32)) return with(std::true_type{});
+        with(std::false_type{});
     };
     if (g.vec == V16) return go(std::integral_constant<int, V16>{});
     if constexpr (V4 > 1)
@@ -501,15 +564,21 @@ void norm_bwd_launch(const NormGeom &g, int grid, const T *dy, long long ds, con
                      long long xs, long long rows, int n, const void *w, bool wf32,
                      const float2 *stats, T *dx, float *part, cudaStream_t st) {
     constexpr int NV = 16 / VEC;
-    const size_t ring = (size_t)kNormStages<T> * RowRing<T, VEC, NV, 2, true>::THREAD * g.threads;
     const size_t sums = (size_t)2 * (n > kNormRegCols ? n : kNormBlock * 16) * 4;
     auto go = [&](auto kern, size_t smem) {
         set_kernel_smem(kern, smem);
         kern<<<grid, g.threads, smem, st>>>(dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
     };
-    if (n > kNormRegCols) go(k_norm_bwd<T, VEC, NV, true, true>, sums);
-    else if (g.block) go(k_norm_bwd<T, VEC, NV, true, false>, ring);
-    else go(k_norm_bwd<T, VEC, NV, false, false>, ring > sums ? ring : sums);
+    if (n > kNormRegCols) return go(k_norm_bwd<T, VEC, NV, true, true, false>, sums);
+    auto with = [&](auto hull) {
+        constexpr bool HULL = decltype(hull)::value;
+        const size_t ring = kNormStages<T> * RowRing<T, VEC, NV, 2, true, HULL>::stage_bytes(n, g.threads, g.rpb);
+        if (g.block) go(k_norm_bwd<T, VEC, NV, true, false, HULL>, ring);
+        else go(k_norm_bwd<T, VEC, NV, false, false, HULL>, ring > sums ? ring : sums);
+    };
+    if constexpr (VEC * sizeof(T) < 16)
+        if (g.hull) return with(std::true_type{});
+    with(std::false_type{});
 }
 
 template <typename T>
@@ -540,7 +609,9 @@ int sdm_layer_norm(const void *x, long long rows, int n, long long x_stride, con
     if (!(eps >= 0.f)) return set_error(SDM_ERR_INVALID, "layer norm: eps must be >= 0");
     if (rows == 0) return SDM_OK;
     if (!y) return set_error(SDM_ERR_INVALID, "layer norm: NULL pointer");
-    const NormGeom g = norm_geom(n, norm_vec(dtype == SDM_BF16 ? 2 : 4, n, x_stride, x_stride, x, y, y), false);
+    const int es = dtype == SDM_BF16 ? 2 : 4;
+    NormGeom g = norm_geom(n, norm_vec(es, n, x_stride, x_stride, x, y, y), false);
+    g.hull = norm_hull(es, g.vec, n, x_stride, x);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto s2 = reinterpret_cast<float2 *>(stats);
     const bool wf32 = weight_dtype == SDM_F32;
@@ -581,8 +652,9 @@ int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void 
         return set_error(SDM_ERR_WORKSPACE, "layer norm backward: workspace NULL, too small or not "
                          "%zu-byte aligned", (size_t)kAlign);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const NormGeom g = norm_geom(
-        n, norm_vec(dtype == SDM_BF16 ? 2 : 4, n, x_stride, grad_stride, x, grad, grad_x), true);
+    const int es = dtype == SDM_BF16 ? 2 : 4;
+    NormGeom g = norm_geom(n, norm_vec(es, n, x_stride, grad_stride, x, grad, grad_x), true);
+    g.hull = norm_hull(es, g.vec, n, x_stride, x) && norm_hull(es, g.vec, n, grad_stride, grad);
     const int grid = rows ? norm_back_blocks(g, rows) : 0;
     float *part = sums ? static_cast<float *>(workspace) : nullptr;
     auto s2 = reinterpret_cast<const float2 *>(stats);

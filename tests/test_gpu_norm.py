@@ -72,6 +72,18 @@ def test_sizes(dtype, rows, n):
     check(x, dy, w, 0.1 * draw((n,), "f32", 3), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n", [(2, 9), (4001, 33), (2500, 66), (1300, 129), (1300, 1007), (700, 1006), (333, 4099), (170, 4098), (311, 8191)])
+def test_many_rows_no_vector_divides(dtype, rows, n):
+    """Rows one behind the other that start at any element of a 16-byte piece; more rows than blocks; an input that
+    is the result too."""
+    x, dy = draw((rows, n), dtype, rows + n), draw((rows, n), dtype, rows + n + 1, 0.0)
+    w, b = 1 + 0.2 * draw((n,), "f32", 2, 0.0), 0.1 * draw((n,), "f32", 3)
+    check(x, dy, w, b, dtype)
+    y = sdm.layer_norm(x, w, b)
+    assert torch.equal(sdm.layer_norm(x, w, b, out=x), y) and torch.equal(x, y)
+
+
 @pytest.mark.parametrize("n", [64, 250, 2048])
 @pytest.mark.parametrize("params", ["none", "weight", "bias", "bf16"])
 def test_parameters(params, n):
