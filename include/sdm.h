@@ -418,9 +418,13 @@ int sdm_product_key_topk_backward(const int64_t *lin, const void *grad_val, long
  *   valid_tokens [B] int32, or NULL: all T. Tokens past it change nothing and none of their inputs
  *                is used; their readings (and gradients) are 0. Clamped to [0, T].
  *   readings     [B, T, H, Dv] contiguous, written whole
- *   workspace    sdm_gated_delta_workspace_bytes(shape) bytes, 256-byte aligned
+ *   workspace    sdm_gated_delta_workspace_bytes(shape) bytes, 256-byte aligned; up to 16 tokens need
+ *                none (sdm_gated_delta only). It begins with a status block, cleared by each call and read
+ *                by sdm_get_device_status: SDM_ERR_TIMEOUT there means that a bounded wait of a kernel gave
+ *                up (sdm_set_wait_limit); the call's results are then undefined.
  * Deterministic. Products run on the tensor cores with the float32 operands (the state, the
- * corrections, the chunk's inverse) split into bfloat16 terms that keep float32's accuracy.
+ * corrections, the chunk's inverse) split into bfloat16 terms that keep float32's accuracy. Long sequences
+ * of few heads are scanned in segments at once; how many depends on the shape and type alone.
  * Each call returns SDM_OK once queued on stream, or a negative sdm_status (nothing queued).
  * --------------------------------------------------------------------------------------- */
 typedef struct {
@@ -439,8 +443,9 @@ int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, c
                     const int32_t *valid_tokens, void *readings, void *workspace,
                     size_t workspace_bytes, void *stream);
 
-/* The saving forward: sdm_gated_delta, and what the backward needs (the state at the start of every
- * chunk and the chunks' corrections, float32) in saved: sdm_gated_delta_saved_bytes(shape) bytes,
+/* The saving forward: sdm_gated_delta (its results are the same to the bit from 17 tokens on), and what the
+ * backward needs (the state at the start of every chunk, the chunks' corrections and the segments' transition
+ * matrices, float32) in saved: sdm_gated_delta_saved_bytes(shape) bytes,
  * 256-byte aligned. */
 size_t sdm_gated_delta_saved_bytes(const sdm_delta_shape *shape);
 int sdm_gated_delta_save(const sdm_delta_shape *shape, float *state, const void *q, const void *k,

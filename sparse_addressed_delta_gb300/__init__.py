@@ -849,7 +849,8 @@ def gated_delta_save(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
                      readings=None, saved=None, workspace=None, stream=None):
     """gated_delta that also keeps what its backward needs: (readings, saved), with ``state``
     advanced in place. ``saved`` (uint8) holds the state at the start of every chunk of 64 (float32
-    inputs: 32) tokens and the chunks' corrections."""
+    inputs: 32) tokens, the chunks' corrections and, for long sequences of few heads, the segments' transition
+    matrices."""
     if stream is not None:
         return _on(stream, gated_delta_save, state, q, k, v, log_decay, beta, valid_tokens, scale=scale,
                    readings=readings, saved=saved, workspace=workspace)

@@ -2,7 +2,8 @@
 // D1 the gradient of a chunk's end state, D0 of its start state):
 //   du = P^T dO + (e^{L_C - L} K) D1;   dw = X^T du;   dv = beta dw
 //   D0 = G_C D1 + (scale G Q)^T dO - K^T (beta G dw)
-// is a recurrence over the chunks from the last to the first (k_delta_back_scan), the forward scan's
+// is a recurrence over the chunks from the last to the first (k_delta_back_scan; 32 chunks of 8 float32 heads
+// of 64 x 64 in segments 42 us and the join 14, in one run 95), the forward scan's
 // mirror image: a warp owns 16 columns, and accumulators pass from product to product as A operands.
 // (X = (I + diag(beta) A)^-1 here.) Everything else needs only a chunk's own S0, r and end state S1 (saved
 // by the forward), D1 and dw (left by the scan), and runs for all chunks at once (k_delta_back_local):
@@ -136,29 +137,28 @@ __global__ void __launch_bounds__(NW * 32, 1)
             };
             float D[NT][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < DKP / 16; ++ks) {          // D = (K D1)^T
+            for (int pk = 2 * DKP / 16 - 1; pk >= 0; --pk) { // D = (K D1)^T
+                const int pass = pk / (DKP / 16), ks = pk % (DKP / 16);
                 unsigned a[3][4], bb[KP][C / 16][4];
                 split_frag<3>(S, ks, a);
 #pragma unroll
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
                     for (int jj = 0; jj < C / 16; ++jj)
-                        ldsm4(bb[p][jj], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+                        if (pass > 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int p = KP - 1; p >= 0; --p)
-                        if (plane_pair(x, p, 3))
+                        if (plane_pair(x, p, 3, pass))
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
                                 mma_bf16(D[j], a[x], bb[p][j >> 1][2 * (j & 1)], bb[p][j >> 1][2 * (j & 1) + 1]);
             }
+            float W[NT][4] = {};
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) D[j][e] *= to[8 * j + 2 * i4 + (e & 1)];
-#pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {            // D += (P^T dO)^T
+            for (int pk = 2 * C / 16 - 1; pk >= 0; --pk) {   // D += (P^T dO)^T
+                const int pass = pk / (C / 16), ks = pk % (C / 16);
                 float x[4][2];
                 unsigned a[KP][4];
                 grads(ks, x);
@@ -173,32 +173,41 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int jj = 0; jj <= ks; ++jj) {
                     unsigned bb[PP][4];
 #pragma unroll
-                    for (int p = 0; p < PP; ++p) ldsm4t(bb[p], frag_rc<XP>(spp + p * C * XP, 16 * ks, 16 * jj, lane));
+                    for (int p = 0; p < PP; ++p)
+                        if (pass > 0 || p == 0) ldsm4t(bb[p], frag_rc<XP>(spp + p * C * XP, 16 * ks, 16 * jj, lane));
 #pragma unroll
                     for (int y = KP - 1; y >= 0; --y)
 #pragma unroll
                         for (int p = PP - 1; p >= 0; --p)
-                            if (plane_pair(y, p, 3)) {
-                                mma_bf16(D[2 * jj], a[y], bb[p][0], bb[p][1]);
-                                mma_bf16(D[2 * jj + 1], a[y], bb[p][2], bb[p][3]);
+                            if (plane_pair(y, p, 3, pass)) {
+                                mma_bf16(W[2 * jj], a[y], bb[p][0], bb[p][1]);
+                                mma_bf16(W[2 * jj + 1], a[y], bb[p][2], bb[p][3]);
                             }
                 }
             }
-            float W[NT][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {            // W = (X^T du)^T
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    D[j][e] = fmaf(D[j][e], to[8 * j + 2 * i4 + (e & 1)], W[j][e]);
+                    W[j][e] = 0.f;
+                }
+#pragma unroll
+            for (int pk = 2 * C / 16 - 1; pk >= 0; --pk) {   // W = (X^T du)^T
+                const int pass = pk / (C / 16), ks = pk % (C / 16);
                 unsigned a[3][4];
                 split_frag<3>(D, ks, a);
 #pragma unroll
                 for (int jj = 0; jj <= ks; ++jj) {
                     unsigned bb[3][4];
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
+                    for (int p = 0; p < 3; ++p)
+                        if (pass > 0 || p == 0) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
 #pragma unroll
                     for (int x = 2; x >= 0; --x)
 #pragma unroll
                         for (int p = 2; p >= 0; --p)
-                            if (plane_pair(x, p, 3)) {
+                            if (plane_pair(x, p, 3, pass)) {
                                 mma_bf16(W[2 * jj], a[x], bb[p][0], bb[p][1]);
                                 mma_bf16(W[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
                             }
@@ -225,18 +234,19 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int nn = 0; nn < ND / 2; nn += 2) {
                     float acc[4][4] = {};
 #pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks) {
+                    for (int pk = 2 * C / 16 - 1; pk >= 0; --pk) {
+                        const int pass = pk / (C / 16), ks = pk % (C / 16);
                         unsigned bb[KP][2][4];
 #pragma unroll
                         for (int p = 0; p < KP; ++p)
 #pragma unroll
                             for (int m = 0; m < 2; ++m)
-                                ldsm4t(bb[p][m], frag_rc<KPI>(tile + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
+                                if (pass > 0 || p == 0) ldsm4t(bb[p][m], frag_rc<KPI>(tile + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
 #pragma unroll
                         for (int x = 2; x >= 0; --x)
 #pragma unroll
                             for (int p = KP - 1; p >= 0; --p)
-                                if (plane_pair(x, p, 3))
+                                if (plane_pair(x, p, 3, pass))
 #pragma unroll
                                     for (int m = 0; m < 4; ++m)
                                         mma_bf16(acc[m], ua[ks][x], bb[p][m >> 1][2 * (m & 1)], bb[p][m >> 1][2 * (m & 1) + 1]);
@@ -313,7 +323,7 @@ struct BackLocalSmem {
 // part of the tokens, and reads its rows of S0 and D1 straight into fragments, one step ahead; the C x C
 // products are split into 16 x 16 blocks, a warp each.
 // What bounds it: the m16n8k16 products, about 7600 a chunk and head at Dk = Dv = 128 (8 cycles each on
-// one of four tensor cores).
+// one of four tensor cores); 8 float32 heads of 64 x 64 x 32 chunks take 21 us.
 template <typename T, int DKP>
 __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     k_delta_back_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal lw, DeltaBack o) {
@@ -393,9 +403,13 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     // 16 x 16 block (bi, bj) of the C x C products, on or below the diagonal
     const bool block = warp < BLOCKS;
     const int bi = warp < 1 ? 0 : warp < 3 ? 1 : warp < 6 ? 2 : 3, bj = warp - bi * (bi + 1) / 2;
-    // of the products that reach the gates, the lesser terms have sums of their own: the tensor core cuts
-    // an accumulator's low bits at every step
+    // of the products that reach the gates or float32 gradients, the lesser terms have sums of their own: the
+    // tensor core cuts an accumulator's low bits at every step
     float G1[MT][2][4] = {}, L1[MT][2][4] = {}, G2[MT][2][4] = {}, G3[MT][2][4] = {}, E[2][4] = {}, DP[2][4] = {}, LP[2][4] = {};
+    float low2[BF ? 1 : MT][2][4] = {}, low3[BF ? 1 : MT][2][4] = {}, lowe[2][4] = {};
+    auto &L2 = *(BF ? (float (*)[MT][2][4])&G2 : (float (*)[MT][2][4])&low2);
+    auto &L3 = *(BF ? (float (*)[MT][2][4])&G3 : (float (*)[MT][2][4])&low3);
+    auto &LE = *(BF ? &E : &lowe);
     for (int c0 = 0; c0 < d.Dv; c0 += kBackCols) {
         __syncthreads();
         // dO, dw and r of this column tile as planes; <dw, v> and <dw, r>
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                     for (int p = 2; p >= 0; --p)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            if (s < PL && plane_pair(s, p, PL)) mma_bf16(E[e], aw[s < PL ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
+                            if (s < PL && plane_pair(s, p, PL)) mma_bf16(s + p ? LE[e] : E[e], aw[s < PL ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
                             if (s < KP && plane_pair(s, p, 3)) mma_bf16(s + p ? LP[e] : DP[e], ao[s < KP ? s : 0], br[p][2 * e], br[p][2 * e + 1]);
                         }
             }
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                     for (int p = PL - 1; p >= 0; --p)
                         if (plane_pair(s, p, PL))
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) mma_bf16(G2[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
+                            for (int e = 0; e < 2; ++e) mma_bf16(s + p ? L2[mt][e] : G2[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
 #pragma unroll
                 for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<VPI>(sr + p * L::VT, r0, 16 * ks, lane));
 #pragma unroll
@@ -518,7 +532,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                     for (int p = PL - 1; p >= 0; --p)
                         if (plane_pair(s, p, PL))
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) mma_bf16(G3[mt][e], a[s], bd[e][0][p], bd[e][1][p]);
+                            for (int e = 0; e < 2; ++e) mma_bf16(s + p ? L3[mt][e] : G3[mt][e], a[s], bd[e][0][p], bd[e][1][p]);
             }
         }
     }
@@ -541,6 +555,13 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                     const unsigned qq = *reinterpret_cast<const unsigned *>(smem + L::Q + p * L::TILE + r * KPI + 2 * c);
                     s1 = fmaf(lo_f32(qq), a[0], fmaf(hi_f32(qq), a[1], s1));
                 }
+                if constexpr (!BF) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        x[m] += L2[mt][e][2 * half + m];
+                        y[m] += L3[mt][e][2 * half + m];
+                    }
+                }
                 x[0] = fmaf(f2, x[0], f3 * y[0]);
                 x[1] = fmaf(f2, x[1], f3 * y[1]);
             }
@@ -550,7 +571,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
         }
     // the C x C blocks: q k^T again, then a, p and the row sums of p * (q k^T)
     if (block) {
-        float qk[2][4] = {};
+        float qk[2][4] = {}, lq[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < DKP / 16; ++ks) {
             unsigned aq[KP][4], bk[KP][4];
@@ -565,7 +586,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                 for (int p = KP - 1; p >= 0; --p)
                     if (plane_pair(s, p, KP))
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) mma_bf16(qk[e], aq[s], bk[p][2 * e], bk[p][2 * e + 1]);
+                        for (int e = 0; e < 2; ++e) mma_bf16(s + p ? lq[e] : qk[e], aq[s], bk[p][2 * e], bk[p][2 * e + 1]);
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -579,8 +600,8 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                     const int s = 16 * bj + 8 * e + 2 * i4 + m, i = 2 * half + m;
                     const float f = s <= t ? expf((hi[t] - hi[s]) + (lo[t] - lo[s])) * be[s] : 0.f;
                     pa[m] = s <= t ? d.scale * ((DP[e][i] + LP[e][i]) * f) : 0.f;
-                    aa[m] = s < t ? -be[t] * (E[e][i] * f) : 0.f;
-                    zr = s <= t ? fmaf(pa[m], qk[e][i], zr) : zr;
+                    aa[m] = s < t ? -be[t] * ((BF ? E[e][i] : E[e][i] + LE[e][i]) * f) : 0.f;
+                    zr = s <= t ? fmaf(pa[m], qk[e][i] + lq[e][i], zr) : zr;
                 }
                 unsigned pl[PL];
                 const int at = t * GPI + 2 * (16 * bj + 8 * e + 2 * i4);
@@ -630,7 +651,17 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
             }
         }
     }
-    // dq += p K;  dk += p^T Q + (a + a^T) K
+    // dq += p K;  dk += p^T Q + (a + a^T) K: float32 gradients in sums of their own, joined at the end
+    float H1[MT][2][4] = {};
+    if constexpr (!BF) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) G3[mt][e][i] = L1[mt][e][i] = L2[mt][e][i] = 0.f;
+    }
+    auto &Q1 = *(BF ? &G1 : &H1), &QL = *(BF ? &G1 : &L1), &K1 = *(BF ? &G2 : &G3), &KL = L2;
     const unsigned gp = sk + L::P, ga = sk + L::A;
 #pragma unroll
     for (int ks = 0; ks < NB; ++ks) {
@@ -643,31 +674,31 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int m = m0 + mt;
-            auto add = [&](float (&acc)[2][4], const unsigned (&a)[PL][4], const unsigned (&bb)[KP][4]) {
+            auto add = [&](float (&acc)[2][4], float (&low)[2][4], const unsigned (&a)[PL][4], const unsigned (&bb)[KP][4]) {
 #pragma unroll
                 for (int s = PL - 1; s >= 0; --s)
 #pragma unroll
                     for (int p = KP - 1; p >= 0; --p)
                         if (plane_pair(s, p, PL))
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) mma_bf16(acc[e], a[s], bb[p][2 * e], bb[p][2 * e + 1]);
+                            for (int e = 0; e < 2; ++e) mma_bf16(s + p ? low[e] : acc[e], a[s], bb[p][2 * e], bb[p][2 * e + 1]);
             };
             unsigned a[PL][4];
             if (ks <= m) {
 #pragma unroll
                 for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<GPI>(gp + p * L::GT, 16 * m, 16 * ks, lane));
-                add(G1[mt], a, bk);
+                add(Q1[mt], QL[mt], a, bk);
 #pragma unroll
                 for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<GPI>(ga + p * L::GT, 16 * m, 16 * ks, lane));
-                add(G2[mt], a, bk);
+                add(K1[mt], KL[mt], a, bk);
             }
             if (ks >= m) {
 #pragma unroll
                 for (int p = 0; p < PL; ++p) ldsm4t(a[p], frag_cr<GPI>(gp + p * L::GT, 16 * ks, 16 * m, lane));
-                add(G2[mt], a, bq);
+                add(K1[mt], KL[mt], a, bq);
 #pragma unroll
                 for (int p = 0; p < PL; ++p) ldsm4t(a[p], frag_cr<GPI>(ga + p * L::GT, 16 * ks, 16 * m, lane));
-                add(G2[mt], a, bk);
+                add(K1[mt], KL[mt], a, bk);
             }
         }
     }
@@ -682,6 +713,13 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                 const int c = dk0 + 8 * e + 2 * i4;
                 if (c >= d.Dk) continue;
                 const bool live = r < nt;
+                if constexpr (!BF) {
+#pragma unroll
+                    for (int j = 2 * half; j < 2 * half + 2; ++j) {
+                        G1[mt][e][j] += H1[mt][e][j] + L1[mt][e][j];
+                        G2[mt][e][j] += G3[mt][e][j] + L2[mt][e][j];
+                    }
+                }
                 store2(false, r, c, live ? G1[mt][e][2 * half] : 0.f, live ? G1[mt][e][2 * half + 1] : 0.f);
                 store2(true, r, c, live ? G2[mt][e][2 * half] : 0.f, live ? G2[mt][e][2 * half + 1] : 0.f);
             }

@@ -13,7 +13,8 @@
 // turn) dw and r, D1, the next chunk's start for <S1, D1>, S0; always as far ahead as their places are
 // free.
 // What bounds it: a head's chunk reads 240 KB and writes its gradients (10000 cycles at the card's copy
-// rate); its phases (planes, p and a, states, results) follow one another with one block an SM.
+// rate); its phases (planes, p and a, states, results) follow one another with one block an SM. Measured at
+// 128 x 128, 32 heads by twos x 2 x 64 chunks: 385 us (2.7 TB/s); by m16n8k16 products (delta_back.cu) 640.
 //
 // Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block; the computing warps
 // then run through without waiting (they meet at barriers), the others stop and wait for what they have

@@ -8,7 +8,8 @@
 // thread keeps its part of its lane of D in registers in float32 for the whole sequence.
 //
 // What bounds it: every chunk's chain E -> decayed E -> W -> its planes -> D, in two halves as in the
-// forward, here with the chunk's last 32 tokens ahead. The products with dO run in the gaps.
+// forward, here with the chunk's last 32 tokens ahead. The products with dO run in the gaps. Measured at 128
+// x 128: 64 heads x 64 chunks 267 us (4.2 a chunk); the register form (delta_back.cu) takes 543.
 //
 // Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of Dk and quarter 3 - warp / 4 of the
 // tokens), warp 16 issues the products, warp 17 loads, warp 18 stores the values' gradient. Two stages

@@ -6,7 +6,8 @@
 // X, P diag(beta) and the gates need no state: k_delta_local computes them for all chunks at once. k_delta_scan
 // then walks over each head's chunks.
 //
-// The scan keeps everything transposed, [Dv] x [tokens or Dk]: a warp owns 16 of the state's columns
+// The scan (32 chunks of 8 float32 heads of 64 x 64 in segments: 35 us and the join 14, in one run 92) keeps
+// everything transposed, [Dv] x [tokens or Dk]: a warp owns 16 of the state's columns
 // as the accumulators of m16n8k16 products, and the accumulators of one product are, in place, the A
 // operand of the next (S^T -> (K S)^T -> u^T -> S^T). Columns never mix, so warps share only the
 // loads of K, Q, X and P, and no value crosses a warp in the whole recurrence.
@@ -77,7 +78,11 @@ __device__ __forceinline__ void merge_columns(const float *N, float *X, int c0, 
 // in pairs, -X_2 N X_1, with the columns spread over the warps.
 // TC: for the tcgen05 scans, Z = P X in the place of P (a forward's from two terms of each, as exact as
 // the bfloat16 readings need).
-// What bounds it: issue. At C = 64 the merges take about 40 % of its instructions, the planes 25 %.
+// What bounds it: the latency of its steps, each behind a barrier, at 14 warps an SM (128 registers, 57 KB a
+// block): issue 45 %, shared memory 60 %. At C = 64 the merges are about 40 % of its instructions, the planes
+// 25 %. Measured at Dk = 128 with two value heads a key head: 12300 chunks of heads 242 us, 8192 168 us. (The
+// merges' operands fetched a step ahead: 252; decays as products of factors by blocks of 16 and running sums as
+// pairs of floats, for fewer exponentials and no doubles: 239, within what two runs differ.)
 template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
 __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
     k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, int heads) {
@@ -148,10 +153,12 @@ __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
 
     float kk[C / 8][4] = {}, qk[C / 8][4] = {};
 #pragma unroll
-    for (int ks = 0; ks < DKP / 16; ++ks) {
+    for (int pk = KP > 1 ? 2 * DKP / 16 - 1 : DKP / 16 - 1; pk >= 0; --pk) {   // passes of K steps
+        const int pass = pk / (DKP / 16), ks = pk % (DKP / 16);
         unsigned ak[KP][4], aq[KP][4];
 #pragma unroll
         for (int p = 0; p < KP; ++p) {
+            if (pass == 0 && p > 0) break;
             ldsm4(ak[p], frag_rc<KPI>(sk + p * L::TILE, 16 * warp, 16 * ks, lane));
             ldsm4(aq[p], frag_rc<KPI>(sq + p * L::TILE, 16 * warp, 16 * ks, lane));
         }
@@ -161,12 +168,12 @@ __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
             unsigned bk[KP][4];
 #pragma unroll
             for (int p = 0; p < KP; ++p)
-                ldsm4(bk[p], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+                if (pass > 0 || p == 0) ldsm4(bk[p], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
             for (int x = KP - 1; x >= 0; --x)
 #pragma unroll
                 for (int y = KP - 1; y >= 0; --y)
-                    if (plane_pair(x, y, KP))
+                    if (plane_pair(x, y, KP, pass))
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             mma_bf16(kk[2 * jj + e], ak[x], bk[y][2 * e], bk[y][2 * e + 1]);
@@ -319,6 +326,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
     constexpr bool BF = L::BF;
     constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, KPI = L::KPI, THREADS = NW * 32;
     constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / (int)sizeof(T);
+    // two passes over the terms for float32 inputs (with bfloat16's the registers of longer chunks would be
+    // spilled); X's diagonal blocks, its largest, and the latest tokens' updates come last in either
+    constexpr int PASSES = BF ? 1 : 2;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
     const bool carry = !SAVE && mode == DELTA_CARRY;
@@ -390,19 +400,20 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if constexpr (SAVE) store_state(snap + ((bh * (d.Nt + 1) + n) * (long long)d.Dk) * d.Dv + dv0);
             float R[NT][4] = {}, O[NT][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < DKP / 16; ++ks) {          // R = (K S)^T, O = (Q S)^T
+            for (int pk = 0; pk < PASSES * DKP / 16; ++pk) { // R = (K S)^T, O = (Q S)^T
+                const int pass = BF ? -1 : 1 - pk / (DKP / 16), ks = pk % (DKP / 16);
                 unsigned a[3][4], bb[KP][C / 16][4];
                 split_frag<3>(S, ks, a);
 #pragma unroll
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
                     for (int jj = 0; jj < C / 16; ++jj)
-                        ldsm4(bb[p][jj], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+                        if (pass != 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
                     for (int p = KP - 1; p >= 0; --p)
-                        if (plane_pair(x, p, 3))
+                        if (plane_pair(x, p, 3, pass))
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
                                 mma_bf16(R[j], a[x], bb[p][j >> 1][2 * (j & 1)], bb[p][j >> 1][2 * (j & 1) + 1]);
@@ -411,12 +422,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
                     for (int jj = 0; jj < C / 16; ++jj)
-                        ldsm4(bb[p][jj], frag_cr<KPI>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
+                        if (pass != 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = PP - 1; x >= 0; --x)            // bfloat16 readings: two terms (2^-17)
 #pragma unroll
                     for (int p = KP - 1; p >= 0; --p)
-                        if (plane_pair(x, p, PP))
+                        if (plane_pair(x, p, PP, pass))
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
                                 mma_bf16(O[j], a[x], bb[p][j >> 1][2 * (j & 1)], bb[p][j >> 1][2 * (j & 1) + 1]);
@@ -445,25 +456,29 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int e = 0; e < 8; ++e) {
                     const int j = 2 * jj + (e >> 2), t = 8 * j + 2 * i4 + (e & 1);
                     const float f = from[t];
-                    R[j][e & 3] = vv[e >> 2][e & 3] - f * R[j][e & 3];
-                    O[j][e & 3] *= d.scale * f;
+                    // spelled out: a contraction the compiler takes in one form and not in the other would give a
+                    // saving forward other bits
+                    R[j][e & 3] = fmaf(-f, R[j][e & 3], vv[e >> 2][e & 3]);
+                    O[j][e & 3] = __fmul_rn(O[j][e & 3], __fmul_rn(d.scale, f));
                 }
             }
             float U[NT][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {            // U = r^T = (X (v - G K S))^T
+            for (int pk = 0; pk < PASSES * C / 16; ++pk) {   // U = r^T = (X (v - G K S))^T
+                const int pass = BF ? -1 : 1 - pk / (C / 16), ks = pk % (C / 16);
                 unsigned a[3][4];
                 split_frag<3>(R, ks, a);
 #pragma unroll
                 for (int jj = ks; jj < C / 16; ++jj) {
                     unsigned bb[3][4];
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) ldsm4(bb[p], frag_cr<XP>(sx + p * C * XP, 16 * jj, 16 * ks, lane));
+                    for (int p = 0; p < 3; ++p)
+                        if (pass != 0 || p == 0) ldsm4(bb[p], frag_cr<XP>(sx + p * C * XP, 16 * jj, 16 * ks, lane));
 #pragma unroll
                     for (int x = 2; x >= 0; --x)
 #pragma unroll
                         for (int p = 2; p >= 0; --p)
-                            if (plane_pair(x, p, 3)) {
+                            if (plane_pair(x, p, 3, pass)) {
                                 mma_bf16(U[2 * jj], a[x], bb[p][0], bb[p][1]);
                                 mma_bf16(U[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
                             }
@@ -477,25 +492,41 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     for (int e = 0; e < 4; ++e)
                         dst[(size_t)(8 * j + 2 * i4 + (e & 1)) * d.Dv + g4 + 8 * (e >> 1)] = U[j][e];
             }
+            // O += (P diag(beta) r)^T, for float32 readings in sums of its own (R's place)
+            auto &add = *(BF ? &O : &R);
+            if constexpr (!BF) {
 #pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {            // O += (P diag(beta) r)^T
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) R[j][e] = 0.f;
+            }
+#pragma unroll
+            for (int pk = 0; pk < PASSES * C / 16; ++pk) {
                 if (carry) break;
+                const int pass = BF ? -1 : 1 - pk / (C / 16), ks = pk % (C / 16);
                 unsigned a[PP][4];
                 split_frag<PP>(U, ks, a);
 #pragma unroll
                 for (int jj = ks; jj < C / 16; ++jj) {
                     unsigned bb[PP][4];
 #pragma unroll
-                    for (int p = 0; p < PP; ++p) ldsm4(bb[p], frag_cr<XP>(spp + p * C * XP, 16 * jj, 16 * ks, lane));
+                    for (int p = 0; p < PP; ++p)
+                        if (pass != 0 || p == 0) ldsm4(bb[p], frag_cr<XP>(spp + p * C * XP, 16 * jj, 16 * ks, lane));
 #pragma unroll
                     for (int x = PP - 1; x >= 0; --x)
 #pragma unroll
                         for (int p = PP - 1; p >= 0; --p)
-                            if (plane_pair(x, p, PP)) {
-                                mma_bf16(O[2 * jj], a[x], bb[p][0], bb[p][1]);
-                                mma_bf16(O[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
+                            if (plane_pair(x, p, PP, pass)) {
+                                mma_bf16(add[2 * jj], a[x], bb[p][0], bb[p][1]);
+                                mma_bf16(add[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
                             }
                 }
+            }
+            if constexpr (!BF) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[j][e] += R[j][e];
             }
             // the readings take the place of the warp's columns of the value tile, then leave as rows
             if (!carry) {
@@ -532,18 +563,19 @@ __global__ void __launch_bounds__(NW * 32, 1)
             for (int nn = 0; nn < ND / 2; nn += 2) {
                 float acc[4][4] = {};
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks) {
+                for (int pk = 0; pk < PASSES * C / 16; ++pk) {
+                    const int pass = BF ? -1 : 1 - pk / (C / 16), ks = pk % (C / 16);
                     unsigned bb[KP][2][4];
 #pragma unroll
                     for (int p = 0; p < KP; ++p)
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
-                            ldsm4t(bb[p][m], frag_rc<KPI>(sk + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
+                            if (pass != 0 || p == 0) ldsm4t(bb[p][m], frag_rc<KPI>(sk + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
 #pragma unroll
                     for (int x = 2; x >= 0; --x)
 #pragma unroll
                         for (int p = KP - 1; p >= 0; --p)
-                            if (plane_pair(x, p, 3))
+                            if (plane_pair(x, p, 3, pass))
 #pragma unroll
                                 for (int m = 0; m < 4; ++m)
                                     mma_bf16(acc[m], ua[ks][x], bb[p][m >> 1][2 * (m & 1)], bb[p][m >> 1][2 * (m & 1) + 1]);
@@ -575,8 +607,10 @@ constexpr int kJoinUnit = kDeltaMaxDk * kJoinPitch, kJoinBytes = (kJoinUnit + kD
 
 // starts[i + 1] += units[i] starts[i], segment after segment (DeltaBlock): one block per head and 16 columns,
 // a thread 8 of them of a row; what the next step reads is in flight before this one's results are put down.
-// starts[0] is the caller's state. BACK: starts[i - 1] += units[i]^T starts[i], from the last down. A tile of
-// zeros is not multiplied, so a state of zeros stays one whatever the unit's columns hold.
+// Bound by the chain over the segments, about 3 us a step of 128 x 128 states (the unit's 64 KB from the level 2
+// cache, then its product). starts[0] is the caller's state. BACK: starts[i - 1] += units[i]^T starts[i], from
+// the last down. A tile of zeros is not multiplied, so a state of zeros stays one whatever the unit's columns
+// hold.
 template <bool BACK>
 __global__ void __launch_bounds__(2 * kDeltaMaxDk) k_delta_join(DeltaDims d, DeltaLocal w, const float *state) {
     extern __shared__ __align__(16) float M[];

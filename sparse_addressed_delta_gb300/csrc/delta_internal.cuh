@@ -268,6 +268,12 @@ __device__ __forceinline__ void split_frag(const float (&acc)[TILES][4], int ks,
 
 // whether the product of terms a and b (counted from the largest) is above 2^-8 `most` of the whole
 __device__ __forceinline__ constexpr bool plane_pair(int a, int b, int most) { return a + b < most; }
+// The same in two passes over a sum's steps, 1: the smaller terms' products, then 0: the largest terms'. The
+// tensor core cuts an accumulator's low bits at every step, so the sum is kept small for as long as it can be.
+// -1: all in one pass.
+__device__ __forceinline__ constexpr bool plane_pair(int a, int b, int most, int pass) {
+    return a + b < most && (pass < 0 || (a + b > 0) == (pass > 0));
+}
 
 // K or Q planes of a chunk's `nt` live tokens into tiles [KP][C] of DKP columns, zero elsewhere
 template <int KP, int DKP, int C, int THREADS>
