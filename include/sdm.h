@@ -418,7 +418,7 @@ int sdm_product_key_topk_backward(const int64_t *lin, const void *grad_val, long
  *   valid_tokens [B] int32, or NULL: all T. Tokens past it change nothing and none of their inputs
  *                is used; their readings (and gradients) are 0. Clamped to [0, T].
  *   readings     [B, T, H, Dv] contiguous, written whole
- *   workspace    sdm_gated_delta_workspace_bytes(shape) bytes, 256-byte aligned; up to 16 tokens need
+ *   workspace    sdm_gated_delta_workspace_bytes(shape) bytes, 256-byte aligned; up to 8 tokens need
  *                none (sdm_gated_delta only). It begins with a status block, cleared by each call and read
  *                by sdm_get_device_status: SDM_ERR_TIMEOUT there means that a bounded wait of a kernel gave
  *                up (sdm_set_wait_limit); the call's results are then undefined.
@@ -443,7 +443,7 @@ int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, c
                     const int32_t *valid_tokens, void *readings, void *workspace,
                     size_t workspace_bytes, void *stream);
 
-/* The saving forward: sdm_gated_delta (its results are the same to the bit from 17 tokens on), and what the
+/* The saving forward: sdm_gated_delta (its results are the same to the bit from 9 tokens on), and what the
  * backward needs (the state at the start of every chunk, the chunks' corrections and the segments' transition
  * matrices, float32) in saved: sdm_gated_delta_saved_bytes(shape) bytes,
  * 256-byte aligned. */

@@ -35,7 +35,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libsdm.so")
 
 SDM_F32, SDM_BF16 = 0, 1
-DELTA_STEP_TOKENS = 16            # gated_delta: up to this many tokens go one by one
+DELTA_STEP_TOKENS = 8             # gated_delta: up to this many tokens go one by one
 KERNEL_KINDS = ("phase1", "solve", "gather", "dualmm", "dw", "phase2")
 FLAG_PER_STEP_KERNELS = 1
 FLAG_SNAPSHOT_BF16 = 2
@@ -824,7 +824,7 @@ def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.
     q, k [B, T, Hk, Dk] and v [B, T, H, Dv], float32 or bfloat16, any strides that are multiples of
     16 bytes; H a multiple of Hk (value head h uses key head h // (H // Hk)); Dk (up to 128) and Dv
     (up to 512) multiples of 16. log_decay, beta [B, T, H] float32. valid_tokens [B] int32 (None:
-    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step; up to 16 tokens
+    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step; up to 8 tokens
     need no workspace. What is allocated here belongs to ``stream`` (None: the current one)."""
     if stream is not None:
         return _on(stream, gated_delta, state, q, k, v, log_decay, beta, valid_tokens, scale=scale,

@@ -18,7 +18,7 @@ namespace {
 // the plain one's, and a backward's segments its forward's, whatever the strides.
 void delta_segments(DeltaDims &d) {
     constexpr double kStart = 8.0, kJoin = 8.0, kJoinStep = 4.0;
-    const bool tensor = d.dtype == SDM_BF16 && d.Dv > 64;
+    const bool tensor = d.dtype == SDM_BF16;
     const int of = tensor ? 128 : 64;
     const double alone = tensor ? 2.6 : 0.5 * d.Dk / 16 + 1.0, beside = tensor ? 3.0 : alone, carry = tensor ? 2.3 : 0.36 * d.Dk / 16 + 0.6;
     const long long heads = (long long)d.B * d.H, blocks = heads * delta_tiles(d.Dv, of), units = heads * delta_tiles(d.Dk, of);
@@ -79,8 +79,12 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
         if (d.qs[i] < 0 || d.ks[i] < 0 || d.vs[i] < 0 || d.gs[i] < 0 || d.bs[i] < 0 || d.os[i] < 0)
             return set_error(SDM_ERR_INVALID, "gated delta: negative stride");
     }
-    d.tc = s->dtype == SDM_BF16 && s->Dv > 64 && tc_tensor_fits(d.qs, d.B, d.T, d.Hk) &&
-           tc_tensor_fits(d.ks, d.B, d.T, d.Hk) && tc_tensor_fits(d.vs, d.B, d.T, d.H);
+    // bfloat16 inputs run on tcgen05, with narrow states too: 4096 tokens, 32 heads of 128 x 64 or 128 x 16 take 189
+    // us, as three-plane products in registers they took 315 and 313
+    d.tc = s->dtype == SDM_BF16;
+    if (d.tc && !(tc_tensor_fits(d.qs, d.B, d.T, d.Hk) && tc_tensor_fits(d.ks, d.B, d.T, d.Hk) &&
+                  tc_tensor_fits(d.vs, d.B, d.T, d.H) && tc_tensor_fits(d.os, d.B, d.T, d.H)))
+        return set_error(SDM_ERR_UNSUPPORTED, "gated delta: bfloat16 strides must be below 2^39 elements");
     delta_segments(d);
     return SDM_OK;
 }
@@ -104,9 +108,15 @@ bool by_token(const DeltaDims &d) { return d.T <= kDeltaStepTokens; }
 
 size_t delta_unit_bytes(const DeltaDims &d) { return d.segs > 1 ? (d.segs - 2) * (size_t)d.B * d.H * d.Dk * d.Dk * 4 : 0; }
 
+// whether q, k, v or the gradient (i = 0 .. 3) is bfloat16 and broadcast along the tokens
+bool delta_flat(const DeltaDims &d, int i) {
+    return d.tc && d.T > 1 && (i == 0 ? d.qs : i == 1 ? d.ks : i == 2 ? d.vs : d.os)[1] == 0;
+}
+
 // Where the chunk form's buffers lie in a workspace; `bytes` is their end.
 struct DeltaLayout {
     size_t q, k, x, p, aux;              // q, k: the planes of float32 inputs
+    size_t flat[4];                      // bfloat16 q, k, v and gradient that are broadcast along the tokens
     size_t starts, units;                // the segments' (units: of a forward that saves nothing)
     size_t ends, w, dq, dk;              // the backward's
     size_t bytes;
@@ -135,8 +145,23 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
         l.dq = take(part);
         l.dk = take(part);
     }
+    for (int i = 0; i < 4; ++i) l.flat[i] = take(delta_flat(d, i) && (i < 3 || backward) ? (size_t)d.B * d.T * (i < 2 ? (size_t)d.Hk * d.Dk : (size_t)d.H * d.Dv) * 2 : 0);
     l.bytes = at;
     return l;
+}
+
+// Tensor copies step along the tokens: bfloat16 inputs that do not (one token's for all) are laid out in the
+// workspace first.
+cudaError_t delta_unroll(DeltaDims &d, const DeltaLayout &l, unsigned char *ws, int i, const void *&x, cudaStream_t st) {
+    if (!delta_flat(d, i)) return cudaSuccess;
+    long long *s = i == 0 ? d.qs : i == 1 ? d.ks : i == 2 ? d.vs : d.os;
+    const int heads = i < 2 ? d.Hk : d.H, width = i < 2 ? d.Dk : d.Dv;
+    const cudaError_t e = launch_delta_unroll(d, x, s, heads, width, ws + l.flat[i], st);
+    x = ws + l.flat[i];
+    s[0] = (long long)d.T * heads * width;
+    s[1] = (long long)heads * width;
+    s[2] = width;
+    return e;
 }
 
 // what the saving forward keeps: the state at every chunk's start and at the end, r, and the segments' units
@@ -205,15 +230,19 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
     if (off16(state) || off16(readings))
         return set_error(SDM_ERR_INVALID, "gated delta: the state and the readings must be 16-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
+    DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
     if (!save && by_token(d)) return delta_status(launch_delta_step(d, in, state, readings, st));
     const DeltaLayout l = delta_layout(d, false);
     rc = delta_check_ws("workspace", workspace, workspace_bytes, l.bytes);
     if (rc == SDM_OK && save) rc = delta_check_ws("saved buffer", saved, saved_bytes, delta_saved(d));
     if (rc != SDM_OK) return rc;
     DeltaPlanes qp, kp;
-    DeltaLocal w;
-    cudaError_t e = delta_local(d, in, l, static_cast<unsigned char *>(workspace), qp, kp, w, st);
+    DeltaLocal w{};
+    auto ws = static_cast<unsigned char *>(workspace);
+    cudaError_t e = delta_unroll(d, l, ws, 0, in.q, st);
+    if (e == cudaSuccess) e = delta_unroll(d, l, ws, 1, in.k, st);
+    if (e == cudaSuccess) e = delta_unroll(d, l, ws, 2, in.v, st);
+    if (e == cudaSuccess) e = delta_local(d, in, l, ws, qp, kp, w, st);
     if (save) w.units = reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_units(d));
     float *snap = save ? static_cast<float *>(saved) : nullptr;
     float *r = save ? reinterpret_cast<float *>(static_cast<unsigned char *>(saved) + delta_saved_snap(d)) : nullptr;
@@ -274,7 +303,6 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     if (rc != SDM_OK) return rc;
     d.pp = 3;                            // P reaches float32 gradients
     d.back = 1;
-    d.tc = d.tc && tc_tensor_fits(d.os, d.B, d.T, d.H);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d.B == 0) return SDM_OK;
     if (!grad_state) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
@@ -294,10 +322,14 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     if (rc == SDM_OK) rc = delta_check_ws("saved buffer", saved, saved_bytes, delta_saved(d));
     if (rc != SDM_OK) return rc;
     auto ws = static_cast<unsigned char *>(workspace);
-    const DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
+    DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
     DeltaPlanes qp, kp;
-    DeltaLocal w;
-    cudaError_t e = delta_local(d, in, l, ws, qp, kp, w, st);
+    DeltaLocal w{};
+    cudaError_t e = delta_unroll(d, l, ws, 0, in.q, st);
+    if (e == cudaSuccess) e = delta_unroll(d, l, ws, 1, in.k, st);
+    if (e == cudaSuccess) e = delta_unroll(d, l, ws, 2, in.v, st);
+    if (e == cudaSuccess) e = delta_unroll(d, l, ws, 3, grad_readings, st);
+    if (e == cudaSuccess) e = delta_local(d, in, l, ws, qp, kp, w, st);
     w.units = const_cast<float *>(reinterpret_cast<const float *>(static_cast<const unsigned char *>(saved) + delta_saved_units(d)));
     DeltaBack o;
     o.grad = grad_readings;

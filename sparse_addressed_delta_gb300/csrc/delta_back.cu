@@ -23,11 +23,10 @@
 namespace sdm {
 namespace {
 
-template <typename T, int DKP, int NW>
+template <int DKP, int NW>
 struct BackSmem {
-    static constexpr bool BF = sizeof(T) == 2;
-    static constexpr int C = BF ? 64 : 32, KP = BF ? 1 : 3, PP = 3;
-    static constexpr int XP = delta_pitch(C * 2), VP = delta_pitch(NW * 16 * (int)sizeof(T));
+    static constexpr int C = 32, KP = 3, PP = 3;
+    static constexpr int XP = delta_pitch(C * 2), VP = delta_pitch(NW * 16 * 4);
     static constexpr int KPI = delta_pitch(DKP * 2), TILE = C * KPI;
     static constexpr int Q = KP * TILE, X = 2 * KP * TILE, P = X + 3 * C * XP, V = P + PP * C * XP;
     static constexpr int AUX = V + C * VP, STAGE = AUX + 3 * C * 4;
@@ -36,13 +35,12 @@ struct BackSmem {
 };
 
 // One block per head and NW * 16 of its columns, from the last chunk to the first.
-template <typename T, int DKP, int NW>
+template <int DKP, int NW>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_delta_back_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, DeltaBack o, int mode) {
-    using L = BackSmem<T, DKP, NW>;
-    constexpr bool BF = L::BF;
+    using L = BackSmem<DKP, NW>;
     constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, KPI = L::KPI, THREADS = NW * 32;
-    constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / (int)sizeof(T);
+    constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / 4;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
     const bool carry = mode == DELTA_CARRY_BACK;
@@ -55,9 +53,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int ntok = delta_valid(in.valid, b, d.T), chunks = (ntok + C - 1) / C;
     const int n0 = delta_bound(d, chunks, blk.seg), n1 = delta_bound(d, chunks, blk.seg + 1), nch = n1 - n0;
     const bool last = blk.seg + 1 == d.segs;
-    const T *grad = static_cast<const T *>(o.grad) + b * d.os[0] + h * d.os[2] + dv_blk;
+    const float *grad = static_cast<const float *>(o.grad) + b * d.os[0] + h * d.os[2] + dv_blk;
     const long long kbase = b * k.s[0] + hk * k.s[2], qbase = b * q.s[0] + hk * q.s[2];
-    T *gv = static_cast<T *>(o.grad_v) + ((long long)b * d.T * d.H + h) * d.Dv;
+    float *gv = static_cast<float *>(o.grad_v) + ((long long)b * d.T * d.H + h) * d.Dv;
     const long long orow = (long long)d.H * d.Dv;
     const unsigned s0 = smem_u32(smem);
 
@@ -69,7 +67,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         load_tokens<KP, DKP, C, THREADS>(st + L::Q, q, qbase + t0 * q.s[1], d.Dk, nt, tid);
         load_planes<3, C, THREADS>(st + L::X, w.x + bhn * (3 * C * XP), tid);
         load_planes<PP, C, THREADS>(st + L::P, w.p + bhn * (PP * C * XP), tid);
-        load_values<T, NW * 16, C, THREADS>(st + L::V, grad + t0 * d.os[1], d.os[1], nt, d.Dv - dv_blk, tid);
+        load_values<float, NW * 16, C, THREADS>(st + L::V, grad + t0 * d.os[1], d.os[1], nt, d.Dv - dv_blk, tid);
         for (int i = tid; i < 3 * C / 4; i += THREADS)
             cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * kDeltaAux * C + 4 * i, true);
         cp_async_commit();
@@ -117,23 +115,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (!carry) store_state(o.ends + ((bh * d.Nt + n) * (long long)d.Dk) * d.Dv + dv0);
             // dO^T as an A operand, K step ks: KP planes of the stored values times `f` of the token
             auto grads = [&](int ks, float (&x)[4][2]) {
-                if constexpr (BF) {
-                    unsigned r[4];
-                    ldsm4t(r, frag_cr<VP>(sv, 16 * ks, 16 * warp, lane));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[i][0] = lo_f32(r[i]);
-                        x[i][1] = hi_f32(r[i]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = 16 * ks + 8 * (i >> 1) + 2 * i4 + e, c = 16 * warp + g4 + 8 * (i & 1);
+                        x[i][e] = *reinterpret_cast<const float *>(smem + stage + L::V + delta_at<VP>(t, c >> 2) + 4 * (c & 3));
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int t = 16 * ks + 8 * (i >> 1) + 2 * i4 + e, c = 16 * warp + g4 + 8 * (i & 1);
-                            x[i][e] = *reinterpret_cast<const float *>(smem + stage + L::V + delta_at<VP>(t, c >> 2) + 4 * (c & 3));
-                        }
-                }
             };
             float D[NT][4] = {};
 #pragma unroll
@@ -268,7 +256,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     const int t = 8 * j + 2 * i4 + (e & 1), c = 16 * warp + g4 + 8 * (e >> 1);
                     if (!carry) dst[(size_t)t * d.Dv + g4 + 8 * (e >> 1)] = W[j][e];
                     const float x = be[t] * W[j][e];
-                    *reinterpret_cast<T *>(smem + stage + L::V + delta_at<VP>(t, c / VE) + (c % VE) * sizeof(T)) = from_f32<T>(x);
+                    *reinterpret_cast<float *>(smem + stage + L::V + delta_at<VP>(t, c / VE) + (c % VE) * 4) = x;
                     W[j][e] = -from[t] * x;
                 }
 #pragma unroll
@@ -744,11 +732,11 @@ __global__ void __launch_bounds__(256) k_delta_heads(DeltaBack o, long long rows
     }
 }
 
-template <typename T, int DKP, int NW>
+template <int DKP, int NW>
 cudaError_t back_scan_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                           const DeltaLocal &w, const DeltaBack &o, cudaStream_t st) {
-    using L = BackSmem<T, DKP, NW>;
-    auto kern = k_delta_back_scan<T, DKP, NW>;
+    using L = BackSmem<DKP, NW>;
+    auto kern = k_delta_back_scan<DKP, NW>;
     set_kernel_smem(kern, L::BYTES);
     auto run = [&](int mode) {
         kern<<<(unsigned)delta_blocks(d, mode, NW * 16), NW * 32, L::BYTES, st>>>(d, in, q, k, w, o, mode);
@@ -783,15 +771,11 @@ cudaError_t launch_delta_back_scan(const DeltaDims &d, const DeltaIn &in, const 
                                    const DeltaLocal &w, const DeltaBack &o, cudaStream_t st) {
     // as the forward's scan
     const bool wide = d.Dv > 64 && (long long)d.B * d.H * ((d.Dv + 127) / 128) >= kRefSms;
-    auto go = [&](auto t, auto dkp) {
-        using T = decltype(t);
+    auto go = [&](auto dkp) {
         constexpr int DKP = decltype(dkp)::value;
-        return wide ? back_scan_one<T, DKP, 8>(d, in, q, k, w, o, st) : back_scan_one<T, DKP, 4>(d, in, q, k, w, o, st);
+        return wide ? back_scan_one<DKP, 8>(d, in, q, k, w, o, st) : back_scan_one<DKP, 4>(d, in, q, k, w, o, st);
     };
-    auto size = [&](auto t) {
-        return d.Dk <= 64 ? go(t, std::integral_constant<int, 64>{}) : go(t, std::integral_constant<int, 128>{});
-    };
-    return d.dtype == SDM_BF16 ? size(__nv_bfloat16{}) : size(float{});
+    return d.Dk <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }
 
 cudaError_t launch_delta_back_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,

@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(bar + B_DO, 2 * L::TILE);
-                            for (int c = 0; c < 2; ++c) tc_tensor_load(smem + L::G + c * L::PAIR, &mg, 64 * c, h, t0, x.b, bar + B_DO);
+                            for (int c = 0; c < 2; ++c) tc_tensor_load(smem + L::G + c * L::PAIR, &mg, 64 * c, tc_coord(d.os[2], h), t0, tc_coord(d.os[0], x.b), bar + B_DO);
                         }
                         ++grads;
                         if (hh == 0) {
@@ -556,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0) {
                                 mbar_arrive_expect_tx(bar + B_T, 4 * L::TILE);
                                 for (int c = 0; c < 2; ++c) {
-                                    tc_tensor_load(smem + L::K + c * L::PAIR, &mk, 64 * c, x.hk, t0, x.b, bar + B_T);
-                                    tc_tensor_load(smem + L::Q + c * L::PAIR, &mq, 64 * c, x.hk, t0, x.b, bar + B_T);
+                                    tc_tensor_load(smem + L::K + c * L::PAIR, &mk, 64 * c, tc_coord(d.ks[2], x.hk), t0, tc_coord(d.ks[0], x.b), bar + B_T);
+                                    tc_tensor_load(smem + L::Q + c * L::PAIR, &mq, 64 * c, tc_coord(d.qs[2], x.hk), t0, tc_coord(d.qs[0], x.b), bar + B_T);
                                 }
                             }
                             ++it;

@@ -9,7 +9,7 @@
 //
 // What bounds it: every chunk's chain E -> decayed E -> W -> its planes -> D, in two halves as in the
 // forward, here with the chunk's last 32 tokens ahead. The products with dO run in the gaps. Measured at 128
-// x 128: 64 heads x 64 chunks 267 us (4.2 a chunk); the register form (delta_back.cu) takes 543.
+// x 128: 64 heads x 64 chunks 267 us (4.2 a chunk); in registers (as delta_back.cu's for float32) 543.
 //
 // Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of Dk and quarter 3 - warp / 4 of the
 // tokens), warp 16 issues the products, warp 17 loads, warp 18 stores the values' gradient. Two stages
@@ -337,10 +337,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (lane == 0) {
                 mbar_arrive_expect_tx(full, L::STAGE + L::AB);
                 for (int c = 0; c < DKP / 64; ++c) {
-                    tc_tensor_load(st + L::K + c * L::TILE, &mk, 64 * c, hk, t0, b, full);
-                    tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, hk, t0, b, full);
+                    tc_tensor_load(st + L::K + c * L::TILE, &mk, 64 * c, tc_coord(d.ks[2], hk), t0, tc_coord(d.ks[0], b), full);
+                    tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, tc_coord(d.qs[2], hk), t0, tc_coord(d.qs[0], b), full);
                 }
-                for (int c = 0; c < 2; ++c) tc_tensor_load(st + L::G + c * L::TILE, &mg, dv_blk + 64 * c, h, t0, b, full);
+                for (int c = 0; c < 2; ++c) tc_tensor_load(st + L::G + c * L::TILE, &mg, dv_blk + 64 * c, tc_coord(d.os[2], h), t0, tc_coord(d.os[0], b), full);
                 bulk_g2s(st + L::X, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
                 bulk_g2s(st + L::Z, w.p + bhn * (3 * L::TILE), 3 * L::TILE, full);
                 bulk_g2s(smem + L::AUX + L::AB * s, w.aux + bhn * kDeltaAux * C, L::AB, full);

@@ -12,8 +12,8 @@
 // operand of the next (S^T -> (K S)^T -> u^T -> S^T). Columns never mix, so warps share only the
 // loads of K, Q, X and P, and no value crosses a warp in the whole recurrence.
 //
-// Accuracy: K and Q are bfloat16 (or three bfloat16 planes of a float32 input); S, the corrections w
-// and u, and X are float32 and enter products as three bfloat16 terms, the products of terms below
+// Accuracy: K and Q are bfloat16, for the scan here three bfloat16 planes of a float32 input (bfloat16 inputs
+// take the tcgen05 scan, delta_scan_tc.cu); S, the corrections w and u, and X are float32 and enter products as three bfloat16 terms, the products of terms below
 // 2^-24 of the result left out. The chunk's update of the state is summed by itself and added to the
 // decayed state in float32, outside the tensor cores' accumulation.
 #include "delta_internal.cuh"
@@ -304,12 +304,11 @@ __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
     }
 }
 
-template <typename T, int DKP, int NW>
+template <int DKP, int NW>
 struct ScanSmem {
-    static constexpr bool BF = sizeof(T) == 2;
-    static constexpr int C = BF ? 64 : 32, KP = BF ? 1 : 3, PP = BF ? 2 : 3;
+    static constexpr int C = 32, KP = 3, PP = 3;
     static constexpr int XP = delta_pitch(C * 2);            // row pitch of the X and P planes
-    static constexpr int VP = delta_pitch(NW * 16 * (int)sizeof(T));   // of the value tile
+    static constexpr int VP = delta_pitch(NW * 16 * 4);   // of the value tile
     static constexpr int KPI = delta_pitch(DKP * 2), TILE = C * KPI;
     static constexpr int Q = KP * TILE, X = 2 * KP * TILE, P = X + 3 * C * XP, V = P + PP * C * XP;
     static constexpr int AUX = V + C * VP, STAGE = AUX + 3 * C * 4;
@@ -318,17 +317,14 @@ struct ScanSmem {
 
 // One block per head and NW * 16 of its columns; two stages of chunk inputs, the next chunk's copies
 // in flight while this one is computed. SAVE: also stores S0 and u for the backward.
-template <typename T, int DKP, int NW, bool SAVE>
+template <int DKP, int NW, bool SAVE>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_delta_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, float *state,
-                 T *o, float *snap, float *rsave, int mode) {
-    using L = ScanSmem<T, DKP, NW>;
-    constexpr bool BF = L::BF;
+                 float *o, float *snap, float *rsave, int mode) {
+    using L = ScanSmem<DKP, NW>;
     constexpr int C = L::C, KP = L::KP, PP = L::PP, XP = L::XP, VP = L::VP, KPI = L::KPI, THREADS = NW * 32;
-    constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / (int)sizeof(T);
-    // two passes over the terms for float32 inputs (with bfloat16's the registers of longer chunks would be
-    // spilled); X's diagonal blocks, its largest, and the latest tokens' updates come last in either
-    constexpr int PASSES = BF ? 1 : 2;
+    constexpr int NT = C / 8, ND = DKP / 8, VE = 16 / 4;
+    // X's diagonal blocks, its largest, and the latest tokens' updates come last in either pass over the terms
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, i4 = lane & 3;
     const bool carry = !SAVE && mode == DELTA_CARRY;
@@ -341,9 +337,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int ntok = delta_valid(in.valid, b, d.T), chunks = (ntok + C - 1) / C;
     const int n0 = delta_bound(d, chunks, blk.seg), nch = delta_bound(d, chunks, blk.seg + 1);   // its chunks' ends
     const bool last = blk.seg + 1 == d.segs;
-    const T *v = static_cast<const T *>(in.v) + b * d.vs[0] + h * d.vs[2] + dv_blk;
+    const float *v = static_cast<const float *>(in.v) + b * d.vs[0] + h * d.vs[2] + dv_blk;
     const long long kbase = b * k.s[0] + hk * k.s[2], qbase = b * q.s[0] + hk * q.s[2];
-    T *out = o + ((long long)b * d.T * d.H + h) * d.Dv;
+    float *out = o + ((long long)b * d.T * d.H + h) * d.Dv;
     const long long orow = (long long)d.H * d.Dv;
     const unsigned s0 = smem_u32(smem);
 
@@ -357,7 +353,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             load_tokens<KP, DKP, C, THREADS>(st + L::Q, q, qbase + t0 * q.s[1], d.Dk, nt, tid);
             load_planes<PP, C, THREADS>(st + L::P, w.p + bhn * (PP * C * XP), tid);
         }
-        load_values<T, NW * 16, C, THREADS>(st + L::V, v + t0 * d.vs[1], d.vs[1], nt, blk.unit ? 0 : d.Dv - dv_blk, tid);
+        load_values<float, NW * 16, C, THREADS>(st + L::V, v + t0 * d.vs[1], d.vs[1], nt, blk.unit ? 0 : d.Dv - dv_blk, tid);
         for (int i = tid; i < 3 * C / 4; i += THREADS)
             cp_async16_zfill(st + L::AUX + 16 * i, w.aux + bhn * kDeltaAux * C + 4 * i, true);
         cp_async_commit();
@@ -400,15 +396,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if constexpr (SAVE) store_state(snap + ((bh * (d.Nt + 1) + n) * (long long)d.Dk) * d.Dv + dv0);
             float R[NT][4] = {}, O[NT][4] = {};
 #pragma unroll
-            for (int pk = 0; pk < PASSES * DKP / 16; ++pk) { // R = (K S)^T, O = (Q S)^T
-                const int pass = BF ? -1 : 1 - pk / (DKP / 16), ks = pk % (DKP / 16);
+            for (int pk = 0; pk < 2 * DKP / 16; ++pk) { // R = (K S)^T, O = (Q S)^T
+                const int pass = 1 - pk / (DKP / 16), ks = pk % (DKP / 16);
                 unsigned a[3][4], bb[KP][C / 16][4];
                 split_frag<3>(S, ks, a);
 #pragma unroll
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
                     for (int jj = 0; jj < C / 16; ++jj)
-                        if (pass != 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
+                        if (pass > 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sk + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -422,7 +418,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 for (int p = 0; p < KP; ++p)
 #pragma unroll
                     for (int jj = 0; jj < C / 16; ++jj)
-                        if (pass != 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
+                        if (pass > 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
                 for (int x = PP - 1; x >= 0; --x)            // bfloat16 readings: two terms (2^-17)
 #pragma unroll
@@ -436,21 +432,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
             for (int jj = 0; jj < C / 16; ++jj) {
                 float vv[2][4];
-                if constexpr (BF) {
-                    unsigned r[4];
-                    ldsm4t(r, frag_rc<VP>(sv, 16 * jj, 16 * warp, lane));
-                    vv[0][0] = lo_f32(r[0]); vv[0][1] = hi_f32(r[0]);
-                    vv[1][0] = lo_f32(r[1]); vv[1][1] = hi_f32(r[1]);
-                    vv[0][2] = lo_f32(r[2]); vv[0][3] = hi_f32(r[2]);
-                    vv[1][2] = lo_f32(r[3]); vv[1][3] = hi_f32(r[3]);
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int t = 16 * jj + 8 * (e >> 2) + 2 * i4 + (e & 1);
-                        const int c = 16 * warp + g4 + 8 * ((e >> 1) & 1);
-                        vv[e >> 2][e & 3] = *reinterpret_cast<const float *>(
-                            smem + stage + L::V + delta_at<VP>(t, c >> 2) + 4 * (c & 3));
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const int t = 16 * jj + 8 * (e >> 2) + 2 * i4 + (e & 1);
+                    const int c = 16 * warp + g4 + 8 * ((e >> 1) & 1);
+                    vv[e >> 2][e & 3] = *reinterpret_cast<const float *>(
+                        smem + stage + L::V + delta_at<VP>(t, c >> 2) + 4 * (c & 3));
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -464,8 +451,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
             float U[NT][4] = {};
 #pragma unroll
-            for (int pk = 0; pk < PASSES * C / 16; ++pk) {   // U = r^T = (X (v - G K S))^T
-                const int pass = BF ? -1 : 1 - pk / (C / 16), ks = pk % (C / 16);
+            for (int pk = 0; pk < 2 * C / 16; ++pk) {   // U = r^T = (X (v - G K S))^T
+                const int pass = 1 - pk / (C / 16), ks = pk % (C / 16);
                 unsigned a[3][4];
                 split_frag<3>(R, ks, a);
 #pragma unroll
@@ -473,7 +460,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     unsigned bb[3][4];
 #pragma unroll
                     for (int p = 0; p < 3; ++p)
-                        if (pass != 0 || p == 0) ldsm4(bb[p], frag_cr<XP>(sx + p * C * XP, 16 * jj, 16 * ks, lane));
+                        if (pass > 0 || p == 0) ldsm4(bb[p], frag_cr<XP>(sx + p * C * XP, 16 * jj, 16 * ks, lane));
 #pragma unroll
                     for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -492,18 +479,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     for (int e = 0; e < 4; ++e)
                         dst[(size_t)(8 * j + 2 * i4 + (e & 1)) * d.Dv + g4 + 8 * (e >> 1)] = U[j][e];
             }
-            // O += (P diag(beta) r)^T, for float32 readings in sums of its own (R's place)
-            auto &add = *(BF ? &O : &R);
-            if constexpr (!BF) {
+            // O += (P diag(beta) r)^T, in sums of its own (R's place)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) R[j][e] = 0.f;
-            }
+                for (int e = 0; e < 4; ++e) R[j][e] = 0.f;
 #pragma unroll
-            for (int pk = 0; pk < PASSES * C / 16; ++pk) {
+            for (int pk = 0; pk < 2 * C / 16; ++pk) {
                 if (carry) break;
-                const int pass = BF ? -1 : 1 - pk / (C / 16), ks = pk % (C / 16);
+                const int pass = 1 - pk / (C / 16), ks = pk % (C / 16);
                 unsigned a[PP][4];
                 split_frag<PP>(U, ks, a);
 #pragma unroll
@@ -511,23 +495,21 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     unsigned bb[PP][4];
 #pragma unroll
                     for (int p = 0; p < PP; ++p)
-                        if (pass != 0 || p == 0) ldsm4(bb[p], frag_cr<XP>(spp + p * C * XP, 16 * jj, 16 * ks, lane));
+                        if (pass > 0 || p == 0) ldsm4(bb[p], frag_cr<XP>(spp + p * C * XP, 16 * jj, 16 * ks, lane));
 #pragma unroll
                     for (int x = PP - 1; x >= 0; --x)
 #pragma unroll
                         for (int p = PP - 1; p >= 0; --p)
                             if (plane_pair(x, p, PP, pass)) {
-                                mma_bf16(add[2 * jj], a[x], bb[p][0], bb[p][1]);
-                                mma_bf16(add[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
+                                mma_bf16(R[2 * jj], a[x], bb[p][0], bb[p][1]);
+                                mma_bf16(R[2 * jj + 1], a[x], bb[p][2], bb[p][3]);
                             }
                 }
             }
-            if constexpr (!BF) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) O[j][e] += R[j][e];
-            }
+                for (int e = 0; e < 4; ++e) O[j][e] += R[j][e];
             // the readings take the place of the warp's columns of the value tile, then leave as rows
             if (!carry) {
                 __syncwarp();
@@ -536,8 +518,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int t = 8 * j + 2 * i4 + (e & 1), c = 16 * warp + g4 + 8 * (e >> 1);
-                        *reinterpret_cast<T *>(smem + stage + L::V + delta_at<VP>(t, c / VE) +
-                                               (c % VE) * sizeof(T)) = from_f32<T>(O[j][e]);
+                        *reinterpret_cast<float *>(smem + stage + L::V + delta_at<VP>(t, c / VE) +
+                                               (c % VE) * 4) = O[j][e];
                     }
                 __syncwarp();
                 constexpr int PR = 16 / VE, RP = 32 / PR;    // pieces a row, rows at once
@@ -563,14 +545,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
             for (int nn = 0; nn < ND / 2; nn += 2) {
                 float acc[4][4] = {};
 #pragma unroll
-                for (int pk = 0; pk < PASSES * C / 16; ++pk) {
-                    const int pass = BF ? -1 : 1 - pk / (C / 16), ks = pk % (C / 16);
+                for (int pk = 0; pk < 2 * C / 16; ++pk) {
+                    const int pass = 1 - pk / (C / 16), ks = pk % (C / 16);
                     unsigned bb[KP][2][4];
 #pragma unroll
                     for (int p = 0; p < KP; ++p)
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
-                            if (pass != 0 || p == 0) ldsm4t(bb[p][m], frag_rc<KPI>(sk + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
+                            if (pass > 0 || p == 0) ldsm4t(bb[p][m], frag_rc<KPI>(sk + p * L::TILE, 16 * ks, 16 * (nn + m), lane));
 #pragma unroll
                     for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -701,39 +683,23 @@ __global__ void __launch_bounds__(256) k_delta_split(DeltaDims d, const float *q
     }
 }
 
-template <typename T, int DKP, int NW, bool SAVE>
+__global__ void __launch_bounds__(256) k_delta_unroll(DeltaDims d, const __nv_bfloat16 *x, long long sb, long long st, long long sh, int heads,
+                                                      int width, __nv_bfloat16 *to) {
+    const long long all = (long long)d.B * d.T * heads * (width / 8);
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+        const long long row = i / (width / 8), h = row % heads, bt = row / heads, t = bt % d.T, b = bt / d.T;
+        reinterpret_cast<uint4 *>(to)[i] = *reinterpret_cast<const uint4 *>(x + b * sb + t * st + h * sh + i % (width / 8) * 8);
+    }
+}
+
+template <int DKP, int NW, bool SAVE>
 cudaError_t scan_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
-                     const DeltaLocal &w, float *state, T *o, float *snap, float *r, int mode, cudaStream_t st) {
-    using L = ScanSmem<T, DKP, NW>;
-    auto kern = k_delta_scan<T, DKP, NW, SAVE>;
+                     const DeltaLocal &w, float *state, float *o, float *snap, float *r, int mode, cudaStream_t st) {
+    using L = ScanSmem<DKP, NW>;
+    auto kern = k_delta_scan<DKP, NW, SAVE>;
     set_kernel_smem(kern, L::BYTES);
     kern<<<(unsigned)delta_blocks(d, mode, NW * 16), NW * 32, L::BYTES, st>>>(d, in, q, k, w, state, o, snap, r, mode);
     return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t scan_any(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
-                     const DeltaLocal &w, float *state, void *o, float *snap, float *r, cudaStream_t st) {
-    T *out = static_cast<T *>(o);
-    // eight warps (two an SM sub-core) share a chunk's loads once there is a block for every SM;
-    // with fewer heads four, so that every warp has a tensor core of its own
-    const bool wide = d.Dv > 64 && (long long)d.B * d.H * ((d.Dv + 127) / 128) >= kRefSms;
-    auto go = [&](auto dkp, auto nw, auto save, int mode) {
-        return scan_one<T, decltype(dkp)::value, decltype(nw)::value, decltype(save)::value>(
-            d, in, q, k, w, state, out, snap, r, mode, st);
-    };
-    auto pick = [&](auto dkp, auto nw) {
-        if (d.segs > 1) {
-            cudaError_t e = go(dkp, nw, std::false_type{}, DELTA_CARRY);
-            if (e == cudaSuccess) e = launch_delta_join(d, w, state, false, st);
-            if (e != cudaSuccess) return e;
-        }
-        return snap ? go(dkp, nw, std::true_type{}, DELTA_RUN) : go(dkp, nw, std::false_type{}, DELTA_RUN);
-    };
-    auto size = [&](auto dkp) {
-        return wide ? pick(dkp, std::integral_constant<int, 8>{}) : pick(dkp, std::integral_constant<int, 4>{});
-    };
-    return d.Dk <= 64 ? size(std::integral_constant<int, 64>{}) : size(std::integral_constant<int, 128>{});
 }
 
 template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
@@ -742,7 +708,8 @@ cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &
     auto kern = k_delta_local<KP, DKP, C, PP, TC, BACK>;
     constexpr int bytes = LocalSmem<KP, DKP, C, TC ? (BACK ? 3 : 2) : 0>::BYTES;
     set_kernel_smem(kern, bytes);
-    // as many heads of a key head to a block as still leave four blocks for every SM
+    // as many heads of a key head to a block as still leave four blocks for every SM (8 x 4096 tokens, 32 heads by
+    // fours: whole call 743 us with one head a block, 690 with two, 664 with four)
     const int group = d.H / d.Hk;
     int heads = kLocalHeads;
     while (heads > 1 && (group % heads || delta_chunks(d) / heads < 4 * kRefSms)) --heads;
@@ -765,11 +732,8 @@ cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const Delt
         if (d.dtype == SDM_F32)
             return d.back ? go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, yes)
                           : go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, no);
-        if (d.back)
-            return d.tc ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, yes, yes)
-                        : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, no, yes);
-        return d.tc ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, yes, no)
-                    : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, no, no);
+        return d.back ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, yes, yes)
+                      : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, yes, no);
     };
     return d.Dk <= 64 ? size(integral_constant<int, 64>{}) : size(integral_constant<int, 128>{});
 }
@@ -783,8 +747,34 @@ cudaError_t launch_delta_join(const DeltaDims &d, const DeltaLocal &w, const flo
 
 cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                               const DeltaLocal &w, float *state, void *o, float *snap, float *r, cudaStream_t st) {
-    return d.dtype == SDM_BF16 ? scan_any<__nv_bfloat16>(d, in, q, k, w, state, o, snap, r, st)
-                               : scan_any<float>(d, in, q, k, w, state, o, snap, r, st);
+    auto out = static_cast<float *>(o);
+    // eight warps (two an SM sub-core) share a chunk's loads once there is a block for every SM (float32, 8 x 1000
+    // tokens of 32 heads of 128 x 128: 696 us, 842 with four); with fewer heads four, so that every warp has a
+    // tensor core of its own
+    const bool wide = d.Dv > 64 && (long long)d.B * d.H * ((d.Dv + 127) / 128) >= kRefSms;
+    auto go = [&](auto dkp, auto nw, auto save, int mode) {
+        return scan_one<decltype(dkp)::value, decltype(nw)::value, decltype(save)::value>(
+            d, in, q, k, w, state, out, snap, r, mode, st);
+    };
+    auto pick = [&](auto dkp, auto nw) {
+        if (d.segs > 1) {
+            cudaError_t e = go(dkp, nw, std::false_type{}, DELTA_CARRY);
+            if (e == cudaSuccess) e = launch_delta_join(d, w, state, false, st);
+            if (e != cudaSuccess) return e;
+        }
+        return snap ? go(dkp, nw, std::true_type{}, DELTA_RUN) : go(dkp, nw, std::false_type{}, DELTA_RUN);
+    };
+    auto size = [&](auto dkp) {
+        return wide ? pick(dkp, std::integral_constant<int, 8>{}) : pick(dkp, std::integral_constant<int, 4>{});
+    };
+    return d.Dk <= 64 ? size(std::integral_constant<int, 64>{}) : size(std::integral_constant<int, 128>{});
+}
+
+cudaError_t launch_delta_unroll(const DeltaDims &d, const void *x, const long long *s, int heads, int width, void *to, cudaStream_t st) {
+    const long long units = (long long)d.B * d.T * heads * (width / 8), blocks = (units + 255) / 256;
+    k_delta_unroll<<<(unsigned)(blocks < 8 * kRefSms ? blocks : 8 * kRefSms), 256, 0, st>>>(
+        d, static_cast<const __nv_bfloat16 *>(x), s[0], s[1], s[2], heads, width, static_cast<__nv_bfloat16 *>(to));
+    return cudaGetLastError();
 }
 
 cudaError_t launch_delta_split(const DeltaDims &d, const void *q, const void *k, __nv_bfloat16 *q_planes, __nv_bfloat16 *k_planes, cudaStream_t st) {

@@ -8,7 +8,10 @@ namespace sdm {
 
 constexpr int kDeltaMaxDk = 128, kDeltaMaxDv = 512;
 constexpr int kDeltaAux = 5;
-constexpr int kDeltaStepTokens = 16;     // up to this many tokens take the token-by-token kernel
+// Up to this many tokens take the token-by-token kernel. Token by token and in a chunk, us: 16 heads x 8 tokens
+// 16 and 25, x 16 25 and 25; 64 sequences of 32 heads x 8 133 and 166, x 12 180 and 166, x 16 225 and 168 (bfloat16,
+// 128 x 128); float32, 8 of 6 heads of 64 x 96 x 8 16 and 23, x 16 27 and 23.
+constexpr int kDeltaStepTokens = 8;
 // A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten
 // whole, and -inf (a hard reset) stays out of the running sums' differences.
 constexpr float kDeltaMinDecay = -110.f;
@@ -132,6 +135,8 @@ cudaError_t launch_delta_step(const DeltaDims &d, const DeltaIn &in, float *stat
                               cudaStream_t st);
 cudaError_t launch_delta_split(const DeltaDims &d, const void *q, const void *k, __nv_bfloat16 *q_planes,
                                __nv_bfloat16 *k_planes, cudaStream_t st);
+// a bfloat16 [B, T, heads, width] of strides s, contiguous
+cudaError_t launch_delta_unroll(const DeltaDims &d, const void *x, const long long *s, int heads, int width, void *to, cudaStream_t st);
 cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q,
                                const DeltaPlanes &k, const DeltaLocal &w, cudaStream_t st);
 // snap [B, H, Nt + 1, Dk, Dv] the state at each chunk's start and, behind the last chunk with tokens, the
@@ -270,10 +275,7 @@ __device__ __forceinline__ void split_frag(const float (&acc)[TILES][4], int ks,
 __device__ __forceinline__ constexpr bool plane_pair(int a, int b, int most) { return a + b < most; }
 // The same in two passes over a sum's steps, 1: the smaller terms' products, then 0: the largest terms'. The
 // tensor core cuts an accumulator's low bits at every step, so the sum is kept small for as long as it can be.
-// -1: all in one pass.
-__device__ __forceinline__ constexpr bool plane_pair(int a, int b, int most, int pass) {
-    return a + b < most && (pass < 0 || (a + b > 0) == (pass > 0));
-}
+__device__ __forceinline__ constexpr bool plane_pair(int a, int b, int most, int pass) { return a + b < most && (a + b > 0) == (pass > 0); }
 
 // K or Q planes of a chunk's `nt` live tokens into tiles [KP][C] of DKP columns, zero elsewhere
 template <int KP, int DKP, int C, int THREADS>

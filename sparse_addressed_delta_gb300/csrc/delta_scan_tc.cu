@@ -16,8 +16,8 @@
 // U finish before the second tokens' w is there, the update's products start with the first tokens,
 // and the first half of the new S enters the next chunk's R while the second is being made. The values'
 // products and the readings run in the gaps. Measured at 128 x 128: 64 heads x 64 chunks, saving, 236 us (3.7 a
-// chunk; 2.6 to 3 without saving); 256 ragged heads x up to 64 chunks, 293 us. The register form (delta_chunk.cu)
-// takes 425 for the first: an m16n8k16 product is 8 cycles on one of four tensor cores.
+// chunk; 2.6 to 3 without saving); 256 ragged heads x up to 64 chunks, 293 us. In registers (as delta_chunk.cu's
+// for float32) the first took 425: an m16n8k16 product is 8 cycles on one of four tensor cores.
 //
 // Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the tokens and of Dk), warp 16 issues
 // the products, warp 17 loads, warp 18 stores the readings; K, Q, V and the readings move as tensor
@@ -361,10 +361,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (lane == 0) {
                 mbar_arrive_expect_tx(full, bytes);
                 for (int c = 0; c < DKP / 64; ++c) {
-                    tc_tensor_load(st + L::K + c * L::TILE, &mk, 64 * c, hk, t0, b, full);
-                    if (!CARRY) tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, hk, t0, b, full);
+                    tc_tensor_load(st + L::K + c * L::TILE, &mk, 64 * c, tc_coord(d.ks[2], hk), t0, tc_coord(d.ks[0], b), full);
+                    if (!CARRY) tc_tensor_load(st + L::Q + c * L::TILE, &mq, 64 * c, tc_coord(d.qs[2], hk), t0, tc_coord(d.qs[0], b), full);
                 }
-                for (int c = 0; c < (blk.unit ? 0 : 2); ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, h, t0, b, full);
+                for (int c = 0; c < (blk.unit ? 0 : 2); ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, tc_coord(d.vs[2], h), t0, tc_coord(d.vs[0], b), full);
                 bulk_g2s(st + L::X, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
                 if (!CARRY) bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, full);
                 bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * kDeltaAux * C, 2 * C * 4, full);
@@ -474,6 +474,8 @@ cudaError_t encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const
 }  // namespace
 
 cudaError_t tc_tensor_map(CUtensorMap *m, const void *p, const long long *s, int B, int T, int heads, int D) {
+    if (s[2] == 0) heads = 1;                                      // broadcast (tc_coord)
+    if (s[0] == 0) B = 1;
     const cuuint64_t dim[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
     // a dimension of one element is never stepped along: any stride will do
     auto bytes = [](long long stride, int n) { return (cuuint64_t)(n > 1 ? stride * 2 : 16); };

@@ -132,9 +132,11 @@ cudaError_t tc_state_map(CUtensorMap *m, const void *p, long long slots, int row
 inline bool tc_tensor_fits(const long long *s, int B, int T, int heads) {
     const int n[3] = {B, T, heads};
     for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && (s[i] == 0 || s[i] * 2 >= (1LL << 40))) return false;
+        if (n[i] > 1 && s[i] * 2 >= (1LL << 40)) return false;
     return true;
 }
+// coordinate of a sequence or head: an input broadcast along it has one of them in its map
+__device__ __forceinline__ int tc_coord(long long stride, int i) { return stride ? i : 0; }
 __device__ __forceinline__ void tc_tensor_load(void *dst, const CUtensorMap *m, int col, int head, int token, int seq,
                                                unsigned long long *bar) {
     asm volatile(

@@ -50,19 +50,21 @@ def test_backward(dtype, shape):
 
 
 def test_backward_of_another_layout():
-    """What is saved depends on the shape alone: a forward of queries and keys whose strides no tensor copy takes
-    (a broadcast head), and a backward of their contiguous copies."""
+    """What is saved depends on the shape alone: a forward of queries and keys of one broadcast head, and a backward
+    of their contiguous copies; the same with queries broadcast along the tokens, which are laid out first."""
     shape = (1, 1500, 2, 2, 64, 128)
     x = draw(*shape, "bf16", seed=3, decay=0.001)
     do, dS = grads(shape, "bf16")
     x["q"], x["k"] = x["q"][:, :, :1].contiguous().expand(-1, -1, 2, -1), x["k"][:, :, :1].contiguous().expand(-1, -1, 2, -1)
     args = lambda y: (y["q"], y["k"], y["v"], y["g"], y["beta"], None)  # noqa: E731
     y = dict(x, q=x["q"].contiguous(), k=x["k"].contiguous())
-    saved = sdm.gated_delta_save(x["state"].clone(), *args(x))[1]
-    got = sdm.gated_delta_backward(*args(y), saved, do, grad_state=dS)
-    want = od.gated_delta_backward(**{n: host(t) for n, t in x.items()}, do=host(do), dS=host(dS), valid=None, scale=64 ** -0.5)
-    for n, a in got.items():
-        assert err(a, want[n]) <= (GATE if n == "grad_log_decay" else GRAD["bf16"] if a.dtype == torch.bfloat16 else GRAD_F32), n
+    z = dict(x, q=x["q"][:, :1].expand(-1, 1500, -1, -1))
+    for one, other in ((x, y), (z, dict(z, q=z["q"].contiguous(), k=y["k"]))):
+        saved = sdm.gated_delta_save(one["state"].clone(), *args(one))[1]
+        got = sdm.gated_delta_backward(*args(other), saved, do, grad_state=dS)
+        want = od.gated_delta_backward(**{n: host(t) for n, t in one.items()}, do=host(do), dS=host(dS), valid=None, scale=64 ** -0.5)
+        for n, a in got.items():
+            assert err(a, want[n]) <= (GATE if n == "grad_log_decay" else GRAD["bf16"] if a.dtype == torch.bfloat16 else GRAD_F32), n
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
