@@ -9,7 +9,7 @@
 //
 // What bounds it: every chunk's chain E -> decayed E -> W -> its planes -> D, in two halves as in the
 // forward, here with the chunk's last 32 tokens ahead. The products with dO run in the gaps. Measured at 128
-// x 128: 64 heads x 64 chunks 267 us (4.2 a chunk); in registers (as delta_back.cu's for float32) 543.
+// x 128: 64 heads x 64 chunks 280 us (4.4 a chunk); in registers (as delta_back.cu's for float32) 543.
 //
 // Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of Dk and quarter 3 - warp / 4 of the
 // tokens), warp 16 issues the products, warp 17 loads, warp 18 stores the values' gradient. Two stages
@@ -249,8 +249,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!tc_warp_wait(bar + B_FULL + par, (it >> 1) & 1, dead, d.spin)) break;
             if (!tc_warp_wait(bar + B_S, par, dead, d.spin)) break;
             tc_fence_after();
+            // D1's largest terms wait for the second half of Dk: the lesser ones of both come first (268 us without,
+            // and the log-decays' gradients up to 1.1e-6 off instead of 7e-7)
 #pragma unroll
-            for (int p = 2; p >= 0; --p)
+            for (int p = 2; p >= 1; --p)
 #pragma unroll
                 for (int ks = 0; ks < KS / 2; ++ks) rows(0, C, p, ks, p < 2 || ks > 0);
             if (!tc_warp_wait(bar + B_S + 1, par, dead, d.spin)) break;
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int p = 2; p >= 0; --p)
 #pragma unroll
-                    for (int ks = KS / 2; ks < KS; ++ks) rows(32 - 32 * hf, 32, p, ks, true);
+                    for (int ks = p > 0 ? KS / 2 : 0; ks < KS; ++ks) rows(32 - 32 * hf, 32, p, ks, true);
                 tc_commit_to(one, bar + B_E + hf);
             }
             // sums from their smallest terms up: the tensor core cuts an accumulator's low bits at every step
