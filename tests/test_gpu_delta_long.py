@@ -105,3 +105,30 @@ def test_nothing_written_stays_nothing():
     x["k"].fill_((2.3 / 64) ** 0.5)
     o, state = call(x)
     assert not o.any() and not state.any()
+
+
+def test_gives_up_and_recovers():
+    """With a limit of one poll the first launch's waits give up; the second sees that in the status and leaves
+    too; the next call with the default limit is right."""
+    shape = (1, 2048, 1, 2, 128, 128)
+    x, (do, dS) = draw(*shape, "bf16", seed=6, decay=0.001), grads(shape, "bf16")
+    args = (x["q"], x["k"], x["v"], x["g"], x["beta"], None)
+    packed = sdm._delta_shape(*args, None, do)[0]
+    lib = sdm.library()
+    fws = torch.empty(lib.sdm_gated_delta_workspace_bytes(packed), dtype=torch.uint8, device="cuda")
+    bws = torch.empty(lib.sdm_gated_delta_backward_workspace_bytes(packed), dtype=torch.uint8, device="cuda")
+    want, saved = sdm.gated_delta_save(x["state"].clone(), *args, workspace=fws)
+    right = sdm.gated_delta_backward(*args, saved, do, grad_state=dS, workspace=bws)
+    assert sdm.device_status(fws)["code"] == 0 and sdm.device_status(bws)["code"] == 0
+    prev = sdm.set_wait_limit(1)
+    try:
+        sdm.gated_delta(x["state"].clone(), *args, workspace=fws)
+        assert sdm.device_status(fws)["code"] == -4                # SDM_ERR_TIMEOUT
+        sdm.gated_delta_backward(*args, saved, do, grad_state=dS, workspace=bws)
+        assert sdm.device_status(bws)["code"] == -4
+    finally:
+        assert sdm.set_wait_limit(prev) == 1
+    assert torch.equal(sdm.gated_delta(x["state"].clone(), *args, workspace=fws), want)
+    again = sdm.gated_delta_backward(*args, saved, do, grad_state=dS, workspace=bws)
+    assert sdm.device_status(fws)["code"] == 0 and sdm.device_status(bws)["code"] == 0
+    assert all(torch.equal(again[n], right[n]) for n in right)
