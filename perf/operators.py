@@ -22,11 +22,11 @@ DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 def listed():
     return [
         # one user's next token in a layer of 16 heads: latency only
-        dict(name="delta step 1", op="delta", B=1, T=1, Hk=16, H=16, Dk=128, Dv=128, dtype="bf16", ragged=False),
+        dict(name="delta step, 1 sequence", op="delta", B=1, T=1, Hk=16, H=16, Dk=128, Dv=128, dtype="bf16", ragged=False),
         # a serving batch's next token, two value heads for each key head: the states' bandwidth
-        dict(name="delta step 256", op="delta", B=256, T=1, Hk=16, H=32, Dk=128, Dv=128, dtype="bf16", ragged=False),
+        dict(name="delta step, 256 sequences", op="delta", B=256, T=1, Hk=16, H=32, Dk=128, Dv=128, dtype="bf16", ragged=False),
         # a few short, unequal prompts of a small float32 model
-        dict(name="delta short f32", op="delta", B=3, T=75, Hk=2, H=6, Dk=64, Dv=96, dtype="f32", ragged=True),
+        dict(name="delta short prompts, float32", op="delta", B=3, T=75, Hk=2, H=6, Dk=64, Dv=96, dtype="f32", ragged=True),
         # one long prompt: few heads, a long chain of chunks
         dict(name="delta long prompt", op="delta", B=1, T=16384, Hk=16, H=32, Dk=128, Dv=128, dtype="bf16", ragged=False),
         # a batch of unequal prompts: throughput
@@ -34,17 +34,17 @@ def listed():
         # a training step's forward and backward through the layer
         dict(name="delta train", op="delta_train", B=2, T=4096, Hk=16, H=32, Dk=128, Dv=128, dtype="bf16", ragged=False),
         # a small float32 model's training step on unequal sequences of odd length
-        dict(name="delta train f32", op="delta_train", B=2, T=1003, Hk=2, H=4, Dk=64, Dv=64, dtype="f32", ragged=True),
+        dict(name="delta train, float32", op="delta_train", B=2, T=1003, Hk=2, H=4, Dk=64, Dv=64, dtype="f32", ragged=True),
         # the layer's input norm for a decode batch: latency only
-        dict(name="norm 32 tokens", op="norm", rows=32, N=2048, dtype="bf16", bias=True),
+        dict(name="norm, 32 tokens", op="norm", rows=32, N=2048, dtype="bf16", bias=True),
         # the norm of every head's readings of a prompt batch: many short rows
-        dict(name="norm heads", op="norm", rows=1048576, N=128, dtype="bf16", bias=False),
+        dict(name="norm, heads", op="norm", rows=1048576, N=128, dtype="bf16", bias=False),
         # the input norm of a training step, forward and backward
-        dict(name="norm train wide", op="norm_train", rows=32768, N=4096, dtype="bf16", bias=True),
+        dict(name="norm train, wide", op="norm_train", rows=32768, N=4096, dtype="bf16", bias=True),
         # the readings' norm of a training step, forward and backward
-        dict(name="norm train heads", op="norm_train", rows=262144, N=128, dtype="bf16", bias=False),
+        dict(name="norm train, heads", op="norm_train", rows=262144, N=128, dtype="bf16", bias=False),
         # a width that no vector load divides
-        dict(name="norm train odd f32", op="norm_train", rows=5003, N=1007, dtype="f32", bias=True),
+        dict(name="norm train, odd, float32", op="norm_train", rows=5003, N=1007, dtype="f32", bias=True),
     ]
 
 
