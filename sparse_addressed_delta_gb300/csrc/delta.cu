@@ -62,7 +62,6 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.dtype = s->dtype;
     d.scale = s->scale;
     d.C = delta_chunk(s->dtype);
-    d.pp = s->dtype == SDM_BF16 ? 2 : 3;
     d.back = 0;
     d.spin = wait_limit();
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
@@ -134,7 +133,7 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     l.q = take(tok);
     l.k = take(tok);
     l.x = take(delta_chunks(d) * 3 * delta_plane_bytes(d));
-    l.p = take(delta_chunks(d) * d.pp * delta_plane_bytes(d));
+    l.p = take(delta_chunks(d) * 3 * delta_plane_bytes(d));
     l.aux = take(delta_chunks(d) * kDeltaAux * d.C * 4);
     l.starts = take(d.segs > 1 ? d.segs * (size_t)delta_states(d) * 4 : 0);
     if (!backward) l.units = take(delta_unit_bytes(d));
@@ -287,7 +286,6 @@ int sdm_gated_delta_save(const sdm_delta_shape *shape, float *state, const void 
 size_t sdm_gated_delta_backward_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
     if (delta_check(shape, d) != SDM_OK) return 0;
-    d.pp = 3;
     d.back = 1;
     return delta_layout(d, true).bytes + kAlign;
 }
@@ -301,7 +299,6 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     DeltaDims d;
     int rc = delta_check(shape, d);
     if (rc != SDM_OK) return rc;
-    d.pp = 3;                            // P reaches float32 gradients
     d.back = 1;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d.B == 0) return SDM_OK;

@@ -23,13 +23,13 @@ namespace {
 
 constexpr int kLocalHeads = 4;          // value heads of one key head a block takes at most
 
-template <int KP, int DKP, int C, int ZP>
+template <int KP, int DKP, int C, bool TC>
 struct LocalSmem {
     static constexpr int KPITCH = delta_pitch(DKP * 2), TILE = C * KPITCH, NP = C + 4, XP = delta_pitch(C * 2);
-    // K and Q make room for the inverse (and ZP of its planes) once their products are taken
-    static constexpr int Q = KP * TILE, X = 0, XPL = C * NP * 4, FIRST = 2 * KP * TILE;
-    static constexpr int SECOND = XPL + ZP * C * XP;
-    static constexpr int N = FIRST > SECOND ? FIRST : SECOND, G = N + C * NP * 4;
+    // K and Q make room for the inverse and for N, and N for the inverse's planes (TC), as each has been used
+    static constexpr int Q = KP * TILE, X = 0, N = C * NP * 4, XPL = N, FIRST = 2 * KP * TILE;
+    static constexpr int SECOND = N + (TC && 3 * XP > NP * 4 ? 3 * C * XP : C * NP * 4);
+    static constexpr int G = FIRST > SECOND ? FIRST : SECOND;
     static constexpr int BYTES = G + kLocalHeads * 3 * C * 4;
 };
 
@@ -76,19 +76,17 @@ __device__ __forceinline__ void merge_columns(const float *N, float *X, int c0, 
 // stay in registers. For each head: the decays, then the inverse of I + N, N = A diag(beta) (BACK:
 // diag(beta) A): 16 x 16 diagonal blocks by substitution, a warp each, a lane a column, then merged
 // in pairs, -X_2 N X_1, with the columns spread over the warps.
-// TC: for the tcgen05 scans, Z = P X in the place of P (a forward's from two terms of each, as exact as
-// the bfloat16 readings need).
+// TC: for the tcgen05 scans, Z = P X in the place of P.
 // What bounds it: the latency of its steps, each behind a barrier, at 14 warps an SM (128 registers, 57 KB a
 // block): issue 45 %, shared memory 60 %. At C = 64 the merges are about 40 % of its instructions, the planes
 // 25 %. Measured at Dk = 128 with two value heads a key head: 12300 chunks of heads 242 us, 8192 168 us. (The
 // merges' operands fetched a step ahead: 252; decays as products of factors by blocks of 16 and running sums as
 // pairs of floats, for fewer exponentials and no doubles: 239, within what two runs differ.)
-template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
-__global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
+template <int KP, int DKP, int C, bool TC, bool BACK>
+__global__ void __launch_bounds__(2 * C, C != 64 ? 1 : 4)
     k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, int heads) {
-    constexpr int ZP = TC ? (BACK ? 3 : 2) : 0;                    // terms of P and X in Z = P X
-    using L = LocalSmem<KP, DKP, C, ZP>;
-    constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = delta_pitch(C * 2), KPI = L::KPITCH;
+    using L = LocalSmem<KP, DKP, C, TC>;
+    constexpr int THREADS = 2 * C, NB = C / 16, NP = L::NP, XP = delta_pitch(C * 2), KPI = L::KPITCH, PP = 3;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (blockIdx.x == 0 && tid == 0) *w.status = DevStatus{};
@@ -261,7 +259,7 @@ __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
             for (int p = 0; p < 3; ++p) {
                 const uint4 y = make_uint4(pl[0][p], pl[1][p], pl[2][p], pl[3][p]);
                 *reinterpret_cast<uint4 *>(ximg + p * PLANE + plane_at(r, c)) = y;
-                if (p < ZP) *reinterpret_cast<uint4 *>(smem + L::XPL + p * C * XP + delta_at<XP>(r, c)) = y;
+                if constexpr (TC) *reinterpret_cast<uint4 *>(smem + L::XPL + p * C * XP + delta_at<XP>(r, c)) = y;
             }
         }
         if constexpr (TC) {
@@ -271,18 +269,18 @@ __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : TC && BACK ? 3 : 4)
 #pragma unroll
             for (int ks = 0; ks < NB; ++ks) {                      // the accumulators of P are its A operand
                 if (ks > warp) break;
-                unsigned a[ZP][4];
-                split_frag<ZP>(pv, ks, a);
+                unsigned a[PP][4];
+                split_frag<PP>(pv, ks, a);
 #pragma unroll
                 for (int jj = 0; jj <= ks; ++jj) {
-                    unsigned bb[ZP][4];
+                    unsigned bb[PP][4];
 #pragma unroll
-                    for (int p = 0; p < ZP; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
+                    for (int p = 0; p < PP; ++p) ldsm4t(bb[p], frag_rc<XP>(sx + p * C * XP, 16 * ks, 16 * jj, lane));
 #pragma unroll
-                    for (int x = ZP - 1; x >= 0; --x)
+                    for (int x = PP - 1; x >= 0; --x)
 #pragma unroll
-                        for (int y = ZP - 1; y >= 0; --y)
-                            if (plane_pair(x, y, ZP))
+                        for (int y = PP - 1; y >= 0; --y)
+                            if (plane_pair(x, y, PP))
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) mma_bf16(z[2 * jj + e], a[x], bb[y][2 * e], bb[y][2 * e + 1]);
                 }
@@ -420,7 +418,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     for (int jj = 0; jj < C / 16; ++jj)
                         if (pass > 0 || p == 0) ldsm4(bb[p][jj], frag_cr<KPI>(sq + p * L::TILE, 16 * jj, 16 * ks, lane));
 #pragma unroll
-                for (int x = PP - 1; x >= 0; --x)            // bfloat16 readings: two terms (2^-17)
+                for (int x = PP - 1; x >= 0; --x)
 #pragma unroll
                     for (int p = KP - 1; p >= 0; --p)
                         if (plane_pair(x, p, PP, pass))
@@ -702,11 +700,11 @@ cudaError_t scan_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q
     return cudaGetLastError();
 }
 
-template <int KP, int DKP, int C, int PP, bool TC, bool BACK>
+template <int KP, int DKP, int C, bool TC, bool BACK>
 cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                       const DeltaLocal &w, cudaStream_t st) {
-    auto kern = k_delta_local<KP, DKP, C, PP, TC, BACK>;
-    constexpr int bytes = LocalSmem<KP, DKP, C, TC ? (BACK ? 3 : 2) : 0>::BYTES;
+    auto kern = k_delta_local<KP, DKP, C, TC, BACK>;
+    constexpr int bytes = LocalSmem<KP, DKP, C, TC>::BYTES;
     set_kernel_smem(kern, bytes);
     // as many heads of a key head to a block as still leave four blocks for every SM (8 x 4096 tokens, 32 heads by
     // fours: whole call 743 us with one head a block, 690 with two, 664 with four)
@@ -721,19 +719,19 @@ cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &
 
 cudaError_t launch_delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &q, const DeltaPlanes &k,
                                const DeltaLocal &w, cudaStream_t st) {
-    auto go = [&](auto kp, auto dkp, auto c, auto pp, auto tc, auto back) {
-        return local_one<decltype(kp)::value, decltype(dkp)::value, decltype(c)::value, decltype(pp)::value,
-                         decltype(tc)::value, decltype(back)::value>(d, in, q, k, w, st);
+    auto go = [&](auto kp, auto dkp, auto c, auto tc, auto back) {
+        return local_one<decltype(kp)::value, decltype(dkp)::value, decltype(c)::value, decltype(tc)::value,
+                         decltype(back)::value>(d, in, q, k, w, st);
     };
     using std::integral_constant;
     auto size = [&](auto dkp) {
         const std::true_type yes;
         const std::false_type no;
         if (d.dtype == SDM_F32)
-            return d.back ? go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, yes)
-                          : go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, integral_constant<int, 3>{}, no, no);
-        return d.back ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 3>{}, yes, yes)
-                      : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, integral_constant<int, 2>{}, yes, no);
+            return d.back ? go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, no, yes)
+                          : go(integral_constant<int, 3>{}, dkp, integral_constant<int, 32>{}, no, no);
+        return d.back ? go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, yes, yes)
+                      : go(integral_constant<int, 1>{}, dkp, integral_constant<int, 64>{}, yes, no);
     };
     return d.Dk <= 64 ? size(integral_constant<int, 64>{}) : size(integral_constant<int, 128>{});
 }

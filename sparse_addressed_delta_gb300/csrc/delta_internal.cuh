@@ -19,7 +19,6 @@ constexpr float kDeltaMinDecay = -110.f;
 struct DeltaDims {
     int B, T, H, Hk, Dk, Dv;
     int C, Nt;                           // chunk length, chunks a sequence
-    int pp;                              // planes of P: 2 where it only reaches bfloat16 readings
     int back;                            // 1: the chunk-local work of a backward
     int dtype;
     int tc;                              // 1: the scans run on tcgen05 (planes of X and P in its layout)
@@ -45,7 +44,7 @@ struct DeltaPlanes {
 
 // Per chunk and head, written by the chunk-local kernel (k_delta_local) for the scans:
 //   x   [3][C][C] bfloat16 planes of X
-//   p   [pp][C][C] planes of P diag(beta) (for the tcgen05 scan: of P diag(beta) X)
+//   p   [3][C][C] planes of P diag(beta) (for the tcgen05 scan: of P diag(beta) X)
 //   aux [kDeltaAux][C] float: exp(L_t), exp(L_C - L_t) beta_t, beta_t, L_t as the sum of two
 // and for a backward: planes of (I + diag(beta) A)^-1 =: X and of P (for tcgen05: of P X), and exp(L_C -
 // L_t) without beta.

@@ -6,8 +6,8 @@
 //   o = scale G (S^T Q^T) + V^T Z^T + w Z^T      (all transposed; S before the chunk; U is r)
 // S, w and the decayed U are A operands in tensor memory, as bfloat16 planes that their own lanes'
 // threads store; V is an A operand in shared memory; K, Q, X and Z are B operands there, K in both its
-// majors (K S runs over Dk, the state's update over the tokens). Three planes (24 bits) go into R, U
-// and the update, two into the bfloat16 readings. A thread keeps its part of its lane of S in registers
+// majors (K S runs over Dk, the state's update over the tokens). Three planes (24 bits) go into every
+// product, so that readings differ from float32 arithmetic's only where that rounds the other way. A thread keeps its part of its lane of S in registers
 // in float32 for the whole sequence; the tensor core only ever sums one chunk's update.
 //
 // What bounds it: every chunk's chain R -> w -> U -> update -> S, products and the threads' work in
@@ -35,13 +35,13 @@ template <int DKP>
 struct TcScan {
     static constexpr int TILE = kTcC * 128;                        // 64 columns of a token tile
     static constexpr int K = 0, Q = K + DKP / 64 * TILE, X = Q + DKP / 64 * TILE, Z = X + 3 * TILE;
-    static constexpr int V = Z + 2 * TILE, STAGE = V + 2 * TILE;
+    static constexpr int V = Z + 3 * TILE, STAGE = V + 2 * TILE;
     static constexpr int O = 2 * STAGE, AUX = O + 2 * 2 * TILE,   // readings: two buffers like V's
                           BARS = AUX + 2 * 512, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    // Tensor memory columns: planes of S, planes of w (then the update), R (then S^T Q^T), U (then, in
-    // each quarter's own 16 columns, two planes of the decayed U), the readings' rest. The decayed U's
-    // third plane takes the second half of S's third, which only R reads.
+    // Tensor memory columns: planes of S, planes of w (then the update), R (then the readings' corrections), U
+    // (then, in each quarter's own 16 columns, two planes of the decayed U), S^T Q^T. The decayed U's third plane
+    // takes the second half of S's third, whose products with K and Q come before U's.
     static constexpr int SP = 0, UP = 3 * (DKP / 2), R = UP + 128, U = R + 64, OA = U + 64;
     static constexpr int LO = DKP == 128 ? SP + 160 : OA + 64;
     static_assert((DKP == 128 ? OA + 64 : LO + 32) <= 512, "tensor memory");
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int l = 0; l < 2; ++l) {                          // 16 lanes of dv
                     float y[8], z[8];
-                    tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::R + 16 * part, at + ((uint32_t)(16 * l) << 16) + L::OA + 16 * part, y, z);
+                    tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::OA + 16 * part, at + ((uint32_t)(16 * l) << 16) + L::R + 16 * part, y, z);
                     unsigned r[4];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -281,9 +281,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int ks = 0; ks < C / 16; ++ks) tri_v(L::U, xd + p * L::TILE / 16, ks, p < 2 || ks > 0);
             if constexpr (!CARRY) {
 #pragma unroll
-                for (int p = 1; p >= 0; --p)
-#pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks) tri_v(L::OA, zd + p * L::TILE / 16, ks, p < 1 || ks > 0);
+                for (int ks = 0; ks < KS; ++ks) rows(L::OA, qd, 0, C, 2, ks, ks > 0);
             }
             bool ok = true;
 #pragma unroll
@@ -305,16 +303,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             if constexpr (!CARRY) {
 #pragma unroll
-                for (int a = 1; a >= 0; --a)
+                for (int sum = 2; sum >= 0; --sum) {                   // R is used: V^T Z^T + w Z^T in its place
 #pragma unroll
-                    for (int p = 1 - a; p >= 0; --p)
+                    for (int ks = 0; ks < C / 16; ++ks)
+                        if (sum > 0) tri_v(L::R, zd + sum * L::TILE / 16, ks, sum < 2 || ks > 0);
 #pragma unroll
-                        for (int ks = 0; ks < C / 16; ++ks) tri(L::OA, L::UP + a * (C / 2), zd + p * L::TILE / 16, ks);
+                    for (int a = sum; a >= 0; --a)
+#pragma unroll
+                        for (int ks = 0; ks < C / 16; ++ks) tri(L::R, L::UP + a * (C / 2), zd + (sum - a) * L::TILE / 16, ks);
+                }
                 tc_commit_to(one, bar + B_O2);
 #pragma unroll
-                for (int p = 1; p >= 0; --p)                           // R is used: S^T Q^T in its place
+                for (int ks = 0; ks < C / 16; ++ks) tri_v(L::R, zd, ks, true);
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) rows(L::R, qd, 0, C, p, ks, p < 1 || ks > 0);
+                for (int p = 1; p >= 0; --p)
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) rows(L::OA, qd, 0, C, p, ks, true);
                 tc_commit_to(one, bar + B_O1);
                 if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;      // w's planes make room for the update
             }
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 for (int c = 0; c < (blk.unit ? 0 : 2); ++c) tc_tensor_load(st + L::V + c * L::TILE, &mv, dv_blk + 64 * c, tc_coord(d.vs[2], h), t0, tc_coord(d.vs[0], b), full);
                 bulk_g2s(st + L::X, w.x + bhn * (3 * L::TILE), 3 * L::TILE, full);
-                if (!CARRY) bulk_g2s(st + L::Z, w.p + bhn * (2 * L::TILE), 2 * L::TILE, full);
+                if (!CARRY) bulk_g2s(st + L::Z, w.p + bhn * (3 * L::TILE), 3 * L::TILE, full);
                 bulk_g2s(smem + L::AUX + 512 * s, w.aux + bhn * kDeltaAux * C, 2 * C * 4, full);
             }
             __syncwarp();
