@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int ks = 0; ks < C / 16; ++ks) tri_v(L::U, xd + p * L::TILE / 16, ks, p < 2 || ks > 0);
             if constexpr (!CARRY) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) rows(L::OA, qd, 0, C, 2, ks, ks > 0);
+                for (int p = 2; p >= 1; --p)
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) rows(L::OA, qd, 0, C, p, ks, p < 2 || ks > 0);
             }
             bool ok = true;
 #pragma unroll
@@ -316,9 +318,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks) tri_v(L::R, zd, ks, true);
 #pragma unroll
-                for (int p = 1; p >= 0; --p)
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) rows(L::OA, qd, 0, C, p, ks, true);
+                for (int ks = 0; ks < KS; ++ks) rows(L::OA, qd, 0, C, 0, ks, true);
                 tc_commit_to(one, bar + B_O1);
                 if (!tc_warp_wait(bar + B_O2, par, dead, d.spin)) break;      // w's planes make room for the update
             }
