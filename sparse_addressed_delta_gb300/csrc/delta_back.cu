@@ -16,8 +16,7 @@
 // undoes what is written, so dg_t = <S_{t-1}, dS_{t-1}> changes from token to token by
 //   dg_t = dg_{t+1} + <o_t, dO_t> - <v_t, dv_t>
 // and within a chunk it is <S1, D1> plus suffix sums; <o_t, dO_t> is the row sum of p * (q k^T) plus
-// <q_t, scale G dO_t S0^T>. Products that reach the gates' float32 gradients keep float32's accuracy; with
-// bfloat16 inputs the others take two terms of each operand (2^-17), as exact as their results need.
+// <q_t, scale G dO_t S0^T>. All products keep float32's accuracy.
 #include "delta_internal.cuh"
 
 namespace sdm {
@@ -293,7 +292,7 @@ struct BackLocalSmem {
     static constexpr bool BF = sizeof(T) == 2;
     static constexpr int C = BF ? 64 : 32, NB = C / 16;
     static constexpr int KP = BF ? 1 : 3;             // planes of q, k and dO
-    static constexpr int PL = BF ? 2 : 3;             // terms of products that reach only the inputs' type
+    static constexpr int PL = 3;                      // terms of float32 operands
     static constexpr int NWK = DKP / 16, WARPS = NWK * NB < 16 ? NWK * NB : 16;
     static constexpr int KPI = delta_pitch(DKP * 2), TILE = C * KPI;
     static constexpr int VPI = delta_pitch(kBackCols * 2), VT = C * VPI;   // planes of dO, dw and r

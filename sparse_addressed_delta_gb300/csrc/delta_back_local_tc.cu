@@ -1,11 +1,13 @@
 // The chunk-local gradients of the gated delta rule (k_delta_back_local in delta_back.cu has the formulas)
 // on the 5th-generation tensor cores, for bfloat16 inputs with up to 128 value columns. All sums lie in
 // tensor memory, with a product's M = 128 in its lanes:
-//   [dw; dO] r^T, q k^T  (rows: the tokens, 64 + 64)        three planes of r, two of dw
-//   G1 = S0 dO^T (3 planes of S0);  G2 = S0 dw^T;  G3 = D1 r^T  (rows: Dk; two planes of each operand)
+//   [dw; dO] r^T, q k^T  (rows: the tokens, 64 + 64)
+//   G1 = S0 dO^T;  G2 = S0 dw^T;  G3 = D1 r^T  (rows: Dk)
 //   dq^T = scale G G1 + K^T p^T;    dk^T = -beta G G2 + e^{L_C - L} beta G3 + Q^T p + K^T (a + a^T)
 // S0 and D1 are A operands in tensor memory, as planes that their own lanes' threads store; dO, dw, r, K
-// and Q are operands in shared memory, and so are the planes of p and a, which serve in both majors.
+// and Q are operands in shared memory, and so are the planes of p and a, which serve in both majors. Float32
+// operands are three planes (24 bits), so that dq and dk differ from float32 arithmetic's only where that rounds
+// the other way.
 //
 // A block stays on its SM and takes chunk after chunk, for all the value heads of one key head in turn:
 // dq and dk are summed over them in registers, in head order. Warps 0..15 compute, warp 16 issues the
@@ -31,8 +33,8 @@ struct BackLocalTc {
     // K and Q, dw's first plane and dO: two tiles (columns) each, alternating, so that one operand of 128
     // rows takes both
     static constexpr int K = 0, Q = K + TILE, W = 4 * TILE, G = W + TILE, PAIR = 2 * TILE;
-    static constexpr int W1 = 8 * TILE, R = 10 * TILE;             // dw's second plane, r's three
-    static constexpr int P = R + 4 * TILE, A = 16 * TILE;          // two planes each; p's in the place of r's third
+    static constexpr int W1 = 8 * TILE, W2 = 10 * TILE, R = 12 * TILE;   // dw's other planes, r's three
+    static constexpr int P = R, A = R + 3 * TILE;                  // three planes each, in the place of r's
     static constexpr int S = 18 * TILE;                            // four boxes
     static constexpr int F = S + 4 * BOX;
     // floats: from, to, beta, L (two) [5][C]; <dw, v>, <dw, r>, row sums of p * qk, row products with q
@@ -40,9 +42,9 @@ struct BackLocalTc {
     static constexpr int FLOATS = 5 * kC + 4 * 4 * kC + kWarps;
     static constexpr int BARS = F + FLOATS * 4, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024 && BARS % 8 == 0, "shared memory");
-    // tensor memory columns: [dw; dO] r^T, dw's second plane, [k; q] k^T, then in their place the planes of
-    // S0; planes of D1, then in their place dq's and dk's second terms; G1, G2, G3
-    static constexpr int E = 0, E2 = 64, QK = 128, SP = 0, DP = 192, DQ = 192, DK = 256, G1 = 320, G2 = 384, G3 = 448;
+    // tensor memory columns: [dw; dO] r^T, dw's other planes, [k; q] k^T, then in their place the planes of
+    // S0; planes of D1, then in their place G1, G2 and dq's second terms; G3; dk's second terms
+    static constexpr int E = 0, E2 = 64, QK = 128, SP = 0, DP = 192, G1 = 192, G2 = 256, DQ = 320, G3 = 384, DK = 448;
 };
 
 enum {
@@ -187,10 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4 *>(y + 4 * e) = *reinterpret_cast<const float4 *>(box + off);
                             *reinterpret_cast<float4 *>(u + 4 * e) = *reinterpret_cast<const float4 *>(box + L::BOX / 2 + off);
                         }
-                        unsigned p2[4][2], p3[4][3];
+                        unsigned p2[4][3], p3[4][3];
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
-                            split_bf16<2>(y[2 * m], y[2 * m + 1], p2[m]);
+                            split_bf16<3>(y[2 * m], y[2 * m + 1], p2[m]);
                             split_bf16<3>(u[2 * m], u[2 * m + 1], p3[m]);
                         }
 #pragma unroll
@@ -201,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int pc = 4 * part + 2 * hc + c, off = tc_at(r, pc & 7), hf = pc >> 3;
                         *reinterpret_cast<uint4 *>(smem + L::W + hf * L::PAIR + off) = make_uint4(p2[0][0], p2[1][0], p2[2][0], p2[3][0]);
                         *reinterpret_cast<uint4 *>(smem + L::W1 + hf * L::TILE + off) = make_uint4(p2[0][1], p2[1][1], p2[2][1], p2[3][1]);
+                        *reinterpret_cast<uint4 *>(smem + L::W2 + hf * L::TILE + off) = make_uint4(p2[0][2], p2[1][2], p2[2][2], p2[3][2]);
 #pragma unroll
                         for (int p = 0; p < 3; ++p)
                             *reinterpret_cast<uint4 *>(smem + L::R + (2 * p + hf) * L::TILE + off) = make_uint4(p3[0][p], p3[1][p], p3[2][p], p3[3][p]);
@@ -219,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 arrive(B_PL);
                 // boxes of the states: 32 columns of the lane's row
                 auto piece = [&](int c) { return *reinterpret_cast<const float4 *>(box + tc_at(lane0 + lane, c)); };
-                auto planes = [&](auto count, uint32_t dst, const float4 (&y)[8]) {
-                    constexpr int N = decltype(count)::value;
+                auto planes = [&](uint32_t dst, const float4 (&y)[8]) {
+                    constexpr int N = 3;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         unsigned p[N][8];
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 8; ++c) y[c] = piece(c);
                     arrive(B_BFREE + part);
-                    planes(std::integral_constant<int, 2>{}, at + L::DP, y);
+                    planes(at + L::DP, y);
                     arrive(B_D1);
                     float s = 0.f;
                     tc_warp_wait(bar + B_BOX + part, 0, dead, d.spin);
@@ -274,7 +277,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (16 * part <= (lane0 & 32) + 31) {          // else above the diagonal: never used
                         const float ht = hi[t], lt = lo[t], ft = is_p ? d.scale : -be[t];
                         float zr = 0.f;
-                        unsigned pl[8][2];
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             float hs[4], ls[4], bs[4];
@@ -290,15 +292,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 zr = fmaf(y[e + m], z[e + m], zr);     // of p, with q k^T
                             }
                         }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) split_bf16<2>(y[2 * e], y[2 * e + 1], pl[e]);
                         unsigned char *dst = smem + (is_p ? L::P : L::A);
+                        tc_warp_wait(bar + B_G3, par, dead, d.spin);   // r's planes are used
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)
+                        for (int p = 0; p < 3; ++p) {
+                            unsigned w[8];                         // a term of each, then what is left of it
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                w[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+                                y[2 * e] -= lo_f32(w[e]);
+                                y[2 * e + 1] -= hi_f32(w[e]);
+                            }
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
                                 *reinterpret_cast<uint4 *>(dst + p * L::TILE + tc_at(t, 2 * part + e)) =
-                                    make_uint4(pl[4 * e][p], pl[4 * e + 1][p], pl[4 * e + 2][p], pl[4 * e + 3][p]);
+                                    make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        }
                         if (is_p) zrow[part * C + t] = zr;
                     }
                     fence_proxy_async_smem();
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 8; ++c) y[c] = piece(c);
                     arrive(B_BFREE + part);
-                    planes(std::integral_constant<int, 3>{}, at + L::SP, y);
+                    planes(at + L::SP, y);
                     arrive(B_S0);
                 }
                 // results: this warp's lanes (32 of Dk) and 16 tokens
@@ -437,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
         // one tile's K steps of 16 columns, then the other's: `pair` bytes apart
         auto at_ks = [](int ks, int pair) { return ((ks >> 2) * pair + 32 * (ks & 3)) / 16; };
-        const uint32_t kq = tc_k_major(base + L::K), wg = tc_k_major(base + L::W), w1 = tc_k_major(base + L::W1);
+        const uint32_t kq = tc_k_major(base + L::K), wg = tc_k_major(base + L::W), w1 = tc_k_major(base + L::W1), w2 = tc_k_major(base + L::W2);
         const uint32_t gk = tc_k_major(base + L::G), rk = tc_k_major(base + L::R);
         const uint32_t km = tc_n_major(base + L::K, L::PAIR), qm = tc_n_major(base + L::Q, L::PAIR);
         const uint32_t pk = tc_k_major(base + L::P), pn = tc_n_major(base + L::P, L::TILE);
@@ -464,40 +473,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int p = 2; p >= 0; --p) rows(L::E, wg, rk + 2 * p * L::TILE / 16, L::PAIR, L::TILE, p == 2);
-                rows(L::E2, w1, rk, L::TILE, L::TILE, true);
+                rows(L::E2, w2, rk, L::TILE, L::TILE, true);
+                rows(L::E2, w1, rk + 2 * L::TILE / 16, L::TILE, L::TILE, false);
+                rows(L::E2, w1, rk, L::TILE, L::TILE, false);
                 rows(L::QK, kq, kq, L::PAIR, L::PAIR, true);
                 tc_commit_to(one, bar + B_E);
                 ok = tc_warp_wait(bar + B_D1, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
-                states(L::G3, L::DP + 64, rk, L::TILE, true);
-                states(L::G3, L::DP, rk + 2 * L::TILE / 16, L::TILE, false);
-                states(L::G3, L::DP, rk, L::TILE, false);
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)                 // pairs of terms from the smallest up
+#pragma unroll
+                    for (int a = sum; a >= 0; --a) states(L::G3, L::DP + 64 * a, rk + 2 * (sum - a) * L::TILE / 16, L::TILE, a == 2);
                 tc_commit_to(one, bar + B_G3);
-                ok = tc_warp_wait(bar + B_S0, par, dead, d.spin);
+                ok = tc_warp_wait(bar + B_S0, par, dead, d.spin) && tc_warp_wait(bar + B_G3, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
                 states(L::G1, L::SP + 128, gk, L::PAIR, true);
                 states(L::G1, L::SP + 64, gk, L::PAIR, false);
                 states(L::G1, L::SP, gk, L::PAIR, false);
-                states(L::G2, L::SP + 64, wg, L::PAIR, true);
+                states(L::G2, L::SP + 128, wg, L::PAIR, true);
+                states(L::G2, L::SP + 64, w1, L::TILE, false);
+                states(L::G2, L::SP, w2, L::TILE, false);
+                states(L::G2, L::SP + 64, wg, L::PAIR, false);
                 states(L::G2, L::SP, w1, L::TILE, false);
                 states(L::G2, L::SP, wg, L::PAIR, false);
-                ok = tc_warp_wait(bar + B_PA, par, dead, d.spin) && tc_warp_wait(bar + B_G3, par, dead, d.spin);
+                ok = tc_warp_wait(bar + B_PA, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
                 // B = lower triangular [t][s]: with t its N, K step s reaches the columns from 16 ks on; with
                 // s its N, K step t those up to 16 ks + 15
 #pragma unroll
-                for (int p = 1; p >= 0; --p) {
+                for (int p = 2; p >= 0; --p) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         tc_mma_ss(one, tu + L::DQ + 16 * ks, km + 2048 * ks / 16, pk + (p * L::TILE + 16 * ks * 128 + 32 * ks) / 16,
-                                  tc_idesc<false, true>(C - 16 * ks), p < 1 || ks > 0);
+                                  tc_idesc<false, true>(C - 16 * ks), p < 2 || ks > 0);
 #pragma unroll
                     for (int ks = 3; ks >= 0; --ks)
                         tc_mma_ss(one, tu + L::DK, qm + 2048 * ks / 16, pn + (p * L::TILE + 2048 * ks) / 16, tc_idesc<true, true>(16 * ks + 16),
-                                  p < 1 || ks < 3);
+                                  p < 2 || ks < 3);
 #pragma unroll
                     for (int ks = 3; ks >= 0; --ks)
                         tc_mma_ss(one, tu + L::DK, km + 2048 * ks / 16, an + (p * L::TILE + 2048 * ks) / 16, tc_idesc<true, true>(16 * ks + 16), true);

@@ -12,6 +12,7 @@ import torch
 import sparse_addressed_delta_gb300 as sdm
 from oracle import delta as od
 from test_gpu_delta import call, draw, host, ref
+from test_gpu_delta_backward import grads, train
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,23 @@ SHAPES = [(2, 300, 2, 4, 128, 128), (4, 64, 2, 4, 64, 128), (2, 257, 1, 2, 96, 2
 def test_readings(shape):
     x = draw(*shape, "bf16", seed=20)
     assert apart(call(x)[0], ref(x)[0]) <= ROUNDED
+
+
+# many values: a value that rounds the other way is rare
+GRADIENT_SHAPES = [(4, 150, 2, 4, 128, 128), (6, 100, 2, 4, 64, 128), (2, 150, 2, 2, 128, 192), (1, 1500, 2, 2, 64, 128)]
+
+
+@pytest.mark.parametrize("shape", GRADIENT_SHAPES, ids=str)
+def test_gradients(shape):
+    """The same by sums of |differences|, of which the expectation is sum |e_i| itself: few of a gradient's values are
+    large, and a sum of squares would hang on them alone. About n = 2^8 delta (sum |x|)^2 / sum x^2 equal steps make the
+    sum, so 3 / sqrt(n) of it is allowed to chance."""
+    x, (do, dS) = draw(*shape, "bf16", seed=21), grads(shape, "bf16")
+    got = train(x, do, dS)[2]
+    want = od.gated_delta_backward(**{n: host(t) for n, t in x.items()}, do=host(do), dS=host(dS), scale=shape[4] ** -0.5)
+    for name in ("grad_q", "grad_k", "grad_v"):
+        once = torch.from_numpy(want[name]).to(torch.bfloat16).double()
+        off, size = float((got[name].double().cpu() - once).abs().sum()), float(once.abs().sum())
+        delta = 4 * 2.0 ** -23
+        n = 2 ** 8 * delta * size ** 2 / float(once.square().sum())
+        assert off / size <= delta * (1 + 3 / n ** 0.5), name
