@@ -5,18 +5,18 @@
 // is a recurrence over the chunks from the last to the first (k_delta_back_scan; 32 chunks of 8 float32 heads
 // of 64 x 64 in segments 42 us and the join 14, in one run 95), the forward scan's
 // mirror image: a warp owns 16 columns, and accumulators pass from product to product as A operands.
-// (X = (I + diag(beta) A)^-1 here.) Everything else needs only a chunk's own S0, r and end state S1 (saved
-// by the forward), D1 and dw (left by the scan), and runs for all chunks at once (k_delta_back_local):
+// (X = (I + diag(beta) A)^-1 here.) Everything else needs only a chunk's own S0 and r (saved by the forward), D1 and dw (left by the scan), and runs for all chunks at once (k_delta_back_local):
 //   a[t,s] = -beta_t beta_s <dw_t, r_s> e^{L_t - L_s}  (s < t)
 //   p[t,s] = scale beta_s <dO_t, r_s> e^{L_t - L_s}    (s <= t)
 //   dq = p K + scale G (dO S0^T)
 //   dk = p^T Q + (a + a^T) K - beta G (dw S0^T) + e^{L_C - L} beta (r D1^T)
 //   dbeta_t = <dw_t, r_t>
-// The log-decays need no products of their own. Scaling the state before token t scales what is read and
-// undoes what is written, so dg_t = <S_{t-1}, dS_{t-1}> changes from token to token by
-//   dg_t = dg_{t+1} + <o_t, dO_t> - <v_t, dv_t>
-// and within a chunk it is <S1, D1> plus suffix sums; <o_t, dO_t> is the row sum of p * (q k^T) plus
-// <q_t, scale G dO_t S0^T>. All products keep float32's accuracy.
+// A log-decay's gradient is the sum of everything that crosses its token, all of it scaled by the decay itself:
+//   z[t,s] = p[t,s] (q_t . k_s) + a[t,s] (k_t . k_s)  (s < t);   x_t = <q_t, scale G dO_t S0^T> - <k_t, beta G dw_t S0^T>
+//   y_s = <k_s, e^{L_C - L} beta r_s D1^T>
+//   dg_t = sum_{t' >= t, s < t} z[t',s] + sum_{t' >= t} x_t' + sum_{s < t} y_s + G_C <S0, D1>
+// the first by suffix sums of row sums less column sums. (Sums without that scale, as of <o, dO> - <v, dv>, cancel
+// to it: at g = -10 they leave an error of 1 %.) Where e^g is 0 it is 0. All products keep float32's accuracy.
 #include "delta_internal.cuh"
 
 namespace sdm {
@@ -299,9 +299,9 @@ struct BackLocalSmem {
     static constexpr int GPI = delta_pitch(C * 2), GT = C * GPI;           // planes of p and a
     static constexpr int Q = KP * TILE, O = 2 * KP * TILE, W = O + KP * VT, R = W + PL * VT;
     static constexpr int P = R + 3 * VT, A = P + PL * GT, F = A + PL * GT;
-    // floats: hi, lo, from, to, beta, <dw, v>, <dw, r> [C]; row sums of p * qk [NB][C]; row products with
-    // q [NWK][C]; <S1, D1> [WARPS]
-    static constexpr int FLOATS = 7 * C + NB * C + NWK * C + WARPS;
+    // floats: hi, lo, from, to, beta, <dw, r> [C]; row and column sums of z [NB][C]; x and y [NWK][C]; <S0, D1>
+    // [WARPS]
+    static constexpr int FLOATS = 6 * C + 2 * NB * C + 2 * NWK * C + WARPS;
     static constexpr int BYTES = F + FLOATS * 4;
     static_assert(BYTES <= 227 * 1024, "shared memory");
 };
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     }
     const unsigned sk = smem_u32(smem), sq = sk + L::Q, so = sk + L::O, sw = sk + L::W, sr = sk + L::R;
     float *hi = reinterpret_cast<float *>(smem + L::F), *lo = hi + C, *from = lo + C, *to = from + C, *be = to + C;
-    float *dwv = be + C, *dwr = dwv + C, *zrow = dwr + C, *dots = zrow + NB * C, *ends = dots + NWK * C;
+    float *dwr = be + C, *zrow = dwr + C, *zcol = zrow + NB * C, *xs_t = zcol + NB * C, *ys_t = xs_t + NWK * C, *ends = ys_t + NWK * C;
 
     load_tokens<KP, DKP, C, THREADS>(sk, k, b * k.s[0] + t0 * k.s[1] + hk * k.s[2], d.Dk, nt, tid);
     load_tokens<KP, DKP, C, THREADS>(sq, q, b * q.s[0] + t0 * q.s[1] + hk * q.s[2], d.Dk, nt, tid);
@@ -367,16 +367,15 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
         hi[i] = aux[3 * C + i];
         lo[i] = aux[4 * C + i];
     }
-    for (int i = tid; i < 2 * C; i += THREADS) dwv[i] = 0.f;      // and dwr behind it
+    for (int i = tid; i < C; i += THREADS) dwr[i] = 0.f;
 
     const T *grad = static_cast<const T *>(o.grad) + b * d.os[0] + t0 * d.os[1] + h * d.os[2];
-    const T *val = static_cast<const T *>(in.v) + b * d.vs[0] + t0 * d.vs[1] + h * d.vs[2];
     const float *wp = o.w + bhn * C * (long long)d.Dv, *rp = o.r + bhn * C * (long long)d.Dv;
     const int dk0 = 16 * (warp % NWK), m0 = (warp / NWK) * MT;    // this warp's Dk columns and token tiles
     const long long cells = (long long)d.Dk * d.Dv;
     const float *s0p = o.snap + (bh * (d.Nt + 1) + n) * cells, *d1p = o.ends + bhn * cells;
     {
-        const float4 *x = reinterpret_cast<const float4 *>(s0p + cells), *y = reinterpret_cast<const float4 *>(d1p);
+        const float4 *x = reinterpret_cast<const float4 *>(s0p), *y = reinterpret_cast<const float4 *>(d1p);
         float s = 0.f;
 #pragma unroll 4
         for (int i = tid; i < (int)(cells / 4); i += THREADS) {
@@ -399,32 +398,22 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     auto &LE = *(BF ? &E : &lowe);
     for (int c0 = 0; c0 < d.Dv; c0 += kBackCols) {
         __syncthreads();
-        // dO, dw and r of this column tile as planes; <dw, v> and <dw, r>
+        // dO, dw and r of this column tile as planes; <dw, r>
         for (int i = tid; i < C * (kBackCols / 8); i += THREADS) {
             const int r = i / (kBackCols / 8), c = i % (kBackCols / 8), col = c0 + 8 * c;
             const bool live = r < nt && col < d.Dv;
-            float g[8] = {}, x[8] = {}, u[8] = {}, v[8] = {};
+            float g[8] = {}, x[8] = {}, u[8] = {};
             if (live) {
                 load_vec<T, 8, true>(grad + r * d.os[1] + col, g);
                 load_vec<float, 8, true>(wp + (long long)r * d.Dv + col, x);
                 load_vec<float, 8, true>(rp + (long long)r * d.Dv + col, u);
-                load_vec<T, 8, true>(val + r * d.vs[1] + col, v);
             }
-            float s = 0.f, z = 0.f;
+            float z = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s = fmaf(x[e], v[e], s);
-                z = fmaf(x[e], u[e], z);
-            }
+            for (int e = 0; e < 8; ++e) z = fmaf(x[e], u[e], z);
 #pragma unroll
-            for (int m = 1; m < kBackCols / 8; m *= 2) {
-                s += __shfl_xor_sync(~0u, s, m);
-                z += __shfl_xor_sync(~0u, z, m);
-            }
-            if (c == 0) {
-                dwv[r] += s;
-                dwr[r] += z;
-            }
+            for (int m = 1; m < kBackCols / 8; m *= 2) z += __shfl_xor_sync(~0u, z, m);
+            if (c == 0) dwr[r] += z;
             auto put = [&](unsigned char *dst, const float (&y)[8], auto planes) {
                 constexpr int N = decltype(planes)::value;
                 unsigned p[4][N];
@@ -523,13 +512,13 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
             }
         }
     }
-    // the terms of dq and dk in place, and the row products with q over this warp's columns
+    // the terms of dq and dk in place, and x and y over this warp's columns
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = 16 * (m0 + mt) + g4 + 8 * half;
-            float s1 = 0.f;
+            float s1 = 0.f, s2 = 0.f;
             const float f = from[r], f1 = f * d.scale, f2 = -be[r] * f, f3 = to[r] * be[r];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -537,11 +526,6 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                 float *a = &G1[mt][e][2 * half], *x = &G2[mt][e][2 * half], *y = &G3[mt][e][2 * half];
                 a[0] = (a[0] + L1[mt][e][2 * half]) * f1;
                 a[1] = (a[1] + L1[mt][e][2 * half + 1]) * f1;
-#pragma unroll
-                for (int p = KP - 1; p >= 0; --p) {
-                    const unsigned qq = *reinterpret_cast<const unsigned *>(smem + L::Q + p * L::TILE + r * KPI + 2 * c);
-                    s1 = fmaf(lo_f32(qq), a[0], fmaf(hi_f32(qq), a[1], s1));
-                }
                 if constexpr (!BF) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
@@ -549,22 +533,41 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                         y[m] += L3[mt][e][2 * half + m];
                     }
                 }
-                x[0] = fmaf(f2, x[0], f3 * y[0]);
-                x[1] = fmaf(f2, x[1], f3 * y[1]);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    x[m] *= f2;
+                    y[m] *= f3;
+                }
+#pragma unroll
+                for (int p = KP - 1; p >= 0; --p) {
+                    const int at = p * L::TILE + r * KPI + 2 * c;
+                    const unsigned qq = *reinterpret_cast<const unsigned *>(smem + L::Q + at), kk = *reinterpret_cast<const unsigned *>(smem + at);
+                    s1 = fmaf(lo_f32(qq), a[0], fmaf(hi_f32(qq), a[1], fmaf(lo_f32(kk), x[0], fmaf(hi_f32(kk), x[1], s1))));
+                    s2 = fmaf(lo_f32(kk), y[0], fmaf(hi_f32(kk), y[1], s2));
+                }
+                x[0] += y[0];
+                x[1] += y[1];
             }
-            s1 += __shfl_xor_sync(~0u, s1, 1);
-            s1 += __shfl_xor_sync(~0u, s1, 2);
-            if (i4 == 0) dots[(warp % NWK) * C + r] = s1;
+#pragma unroll
+            for (int m = 1; m < 4; m *= 2) {
+                s1 += __shfl_xor_sync(~0u, s1, m);
+                s2 += __shfl_xor_sync(~0u, s2, m);
+            }
+            if (i4 == 0) {
+                xs_t[(warp % NWK) * C + r] = s1;
+                ys_t[(warp % NWK) * C + r] = s2;
+            }
         }
-    // the C x C blocks: q k^T again, then a, p and the row sums of p * (q k^T)
+    // the C x C blocks: q k^T and k k^T again, then a, p and the row and column sums of z
     if (block) {
-        float qk[2][4] = {}, lq[2][4] = {};
+        float qk[2][4] = {}, lq[2][4] = {}, kk[2][4] = {}, lk[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < DKP / 16; ++ks) {
-            unsigned aq[KP][4], bk[KP][4];
+            unsigned aq[KP][4], ak[KP][4], bk[KP][4];
 #pragma unroll
             for (int p = 0; p < KP; ++p) {
                 ldsm4(aq[p], frag_rc<KPI>(sq + p * L::TILE, 16 * bi, 16 * ks, lane));
+                ldsm4(ak[p], frag_rc<KPI>(sk + p * L::TILE, 16 * bi, 16 * ks, lane));
                 ldsm4(bk[p], frag_cr<KPI>(sk + p * L::TILE, 16 * bj, 16 * ks, lane));
             }
 #pragma unroll
@@ -573,8 +576,12 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                 for (int p = KP - 1; p >= 0; --p)
                     if (plane_pair(s, p, KP))
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) mma_bf16(s + p ? lq[e] : qk[e], aq[s], bk[p][2 * e], bk[p][2 * e + 1]);
+                        for (int e = 0; e < 2; ++e) {
+                            mma_bf16(s + p ? lq[e] : qk[e], aq[s], bk[p][2 * e], bk[p][2 * e + 1]);
+                            mma_bf16(s + p ? lk[e] : kk[e], ak[s], bk[p][2 * e], bk[p][2 * e + 1]);
+                        }
         }
+        float zc[2][2] = {};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int t = 16 * bi + g4 + 8 * half;
@@ -588,7 +595,9 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                     const float f = s <= t ? expf((hi[t] - hi[s]) + (lo[t] - lo[s])) * be[s] : 0.f;
                     pa[m] = s <= t ? d.scale * ((DP[e][i] + LP[e][i]) * f) : 0.f;
                     aa[m] = s < t ? -be[t] * ((BF ? E[e][i] : E[e][i] + LE[e][i]) * f) : 0.f;
-                    zr = s <= t ? fmaf(pa[m], qk[e][i] + lq[e][i], zr) : zr;
+                    const float z = s < t ? fmaf(pa[m], qk[e][i] + lq[e][i], aa[m] * (kk[e][i] + lk[e][i])) : 0.f;
+                    zr += z;
+                    zc[e][m] += z;
                 }
                 unsigned pl[PL];
                 const int at = t * GPI + 2 * (16 * bj + 8 * e + 2 * i4);
@@ -603,37 +612,45 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
             zr += __shfl_xor_sync(~0u, zr, 2);
             if (i4 == 0) zrow[bj * C + t] = zr;
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                for (int w = 4; w < 32; w *= 2) zc[e][m] += __shfl_xor_sync(~0u, zc[e][m], w);
+                if (g4 == 0) zcol[bi * C + 16 * bj + 8 * e + 2 * i4 + m] = zc[e][m];
+            }
     }
     __syncthreads();
     if (warp == L::WARPS - 1) {
         constexpr int TL = C / 32;
-        double suf[TL], rev = 0.0;
+        float x[TL], y[TL];
+        double whole = 0.0;
 #pragma unroll
-        for (int i = TL - 1; i >= 0; --i) {
+        for (int i = 0; i < TL; ++i) {
             const int r = lane * TL + i;
-            float z = 0.f, x = 0.f;
+            x[i] = y[i] = 0.f;
 #pragma unroll
-            for (int p = 0; p < NB; ++p)
-                if (16 * p <= r) z += zrow[p * C + r];
+            for (int p = 0; p < NB; ++p) {
+                if (16 * p <= r) x[i] += zrow[p * C + r];
+                if (16 * p + 15 >= r) x[i] -= zcol[p * C + r];
+            }
 #pragma unroll
-            for (int p = 0; p < NWK; ++p) x += dots[p * C + r];
-            rev += (double)(z + x) - (double)be[r] * (double)dwv[r];
-            suf[i] = rev;
+            for (int p = 0; p < NWK; ++p) {
+                x[i] += xs_t[p * C + r];
+                y[i] += ys_t[p * C + r];
+            }
         }
-        double after = rev;
 #pragma unroll
-        for (int m = 1; m < 32; m *= 2) {
-            const double y = __shfl_down_sync(~0u, after, m);
-            if (lane + m < 32) after += y;
-        }
-        after -= rev;
-#pragma unroll
-        for (int p = 0; p < L::WARPS; ++p) after += (double)ends[p];
+        for (int p = 0; p < L::WARPS; ++p) whole += (double)ends[p];
+        double dg[TL];
+        delta_decay_sums(x, y, (double)from[C - 1] * whole, dg);
 #pragma unroll
         for (int i = 0; i < TL; ++i) {
             const int r = lane * TL + i;
             if (r < rows) {
-                gdec[(long long)r * d.H] = r < nt ? (float)(after + suf[i]) : 0.f;
+                const bool some = r < nt && expf(delta_decay(in.g[b * d.gs[0] + (t0 + r) * d.gs[1] + h * d.gs[2]])) != 0.f;
+                gdec[(long long)r * d.H] = some ? (float)dg[i] : 0.f;
                 gbeta[(long long)r * d.H] = r < nt ? dwr[r] : 0.f;
             }
         }

@@ -12,8 +12,8 @@
 // A block stays on its SM and takes chunk after chunk, for all the value heads of one key head in turn:
 // dq and dk are summed over them in registers, in head order. Warps 0..15 compute, warp 16 issues the
 // products, warp 17 loads: K and Q of a chunk, dO of a head, and in boxes of 32 columns (four slots, in
-// turn) dw and r, D1, the next chunk's start for <S1, D1>, S0; always as far ahead as their places are
-// free.
+// turn) dw and r, D1, S0 for <S0, D1>, and S0 again for its planes, whose place the first products have until
+// then; always as far ahead as their places are free.
 // What bounds it: a head's chunk reads 240 KB and writes its gradients (10000 cycles at the card's copy
 // rate); its phases (planes, p and a, states, results) follow one another with one block an SM. Measured at
 // 128 x 128, 32 heads by twos x 2 x 64 chunks: 385 us (2.7 TB/s); by m16n8k16 products (delta_back.cu) 640.
@@ -37,9 +37,9 @@ struct BackLocalTc {
     static constexpr int P = R, A = R + 3 * TILE;                  // three planes each, in the place of r's
     static constexpr int S = 18 * TILE;                            // four boxes
     static constexpr int F = S + 4 * BOX;
-    // floats: from, to, beta, L (two) [5][C]; <dw, v>, <dw, r>, row sums of p * qk, row products with q
-    // [4 quarters][C] each; <S1, D1> [warps]
-    static constexpr int FLOATS = 5 * kC + 4 * 4 * kC + kWarps;
+    // floats: from, to, beta, L (two) [5][C]; <dw, r>, row sums of a's part of z and of p's, column sums (of 32 rows
+    // of either), x, y [4][C] each; <S0, D1> [warps]
+    static constexpr int FLOATS = 5 * kC + 6 * 4 * kC + kWarps;
     static constexpr int BARS = F + FLOATS * 4, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024 && BARS % 8 == 0, "shared memory");
     // tensor memory columns: [dw; dO] r^T, dw's other planes, [k; q] k^T, then in their place the planes of
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
         const unsigned sb = smem_u32(smem);
         float *from = reinterpret_cast<float *>(smem + L::F), *to = from + C, *be = to + C, *hi = be + C, *lo = hi + C;
-        float *dwv = lo + C, *dwr = dwv + 4 * C, *zrow = dwr + 4 * C, *dots = zrow + 4 * C, *ends = dots + 4 * C;
+        float *dwr = lo + C, *zrow = dwr + 4 * C, *zcol = zrow + 8 * C, *xs_t = zcol + 4 * C, *ys_t = xs_t + 4 * C, *ends = ys_t + 4 * C;
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); };
         auto arrive = [&](int which) {
             __syncwarp();
@@ -163,23 +163,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const long long bh = (long long)x.b * d.H + h, bhn = bh * d.Nt + x.n;
                 meet();                                            // the last head's floats are used
                 if (tid < 5 * C) from[tid] = lw.aux[bhn * kDeltaAux * C + tid];
-                const T *val = static_cast<const T *>(in.v) + x.b * d.vs[0] + t0 * d.vs[1] + h * d.vs[2];
                 const unsigned par = unit & 1;
                 const unsigned char *box = smem + L::S + part * L::BOX;    // this quarter's slot
-                // dw and r as planes, <dw, v> and <dw, r>: a thread takes 16 of the quarter's columns of a row
+                // dw and r as planes, <dw, r>: a thread takes 16 of the quarter's columns of a row
                 {
-                    const int r = (tid & 127) >> 1, hc = tid & 1, col = 32 * part + 16 * hc;
-                    float v[16] = {};
-                    if (r < x.nt && col < d.Dv) {
-                        const T *vp = val + r * d.vs[1] + col;
-                        uint4 raw2[2] = {__ldg(reinterpret_cast<const uint4 *>(vp)), __ldg(reinterpret_cast<const uint4 *>(vp) + 1)};
-                        const T *e = reinterpret_cast<const T *>(raw2);
-#pragma unroll
-                        for (int m = 0; m < 16; ++m) v[m] = to_f32(e[m]);
-                    }
+                    const int r = (tid & 127) >> 1, hc = tid & 1;
                     meet();                                        // the gates; the last head's floats and planes
                     tc_warp_wait(bar + B_BOX + part, 0, dead, d.spin);
-                    float s = 0.f, z = 0.f;
+                    float z = 0.f;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {                  // 8 columns: one piece of each plane
                         float y[8], u[8];
@@ -196,10 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             split_bf16<3>(u[2 * m], u[2 * m + 1], p3[m]);
                         }
 #pragma unroll
-                        for (int m = 0; m < 8; ++m) {
-                            s = fmaf(y[m], v[8 * c + m], s);
-                            z = fmaf(y[m], u[m], z);
-                        }
+                        for (int m = 0; m < 8; ++m) z = fmaf(y[m], u[m], z);
                         const int pc = 4 * part + 2 * hc + c, off = tc_at(r, pc & 7), hf = pc >> 3;
                         *reinterpret_cast<uint4 *>(smem + L::W + hf * L::PAIR + off) = make_uint4(p2[0][0], p2[1][0], p2[2][0], p2[3][0]);
                         *reinterpret_cast<uint4 *>(smem + L::W1 + hf * L::TILE + off) = make_uint4(p2[0][1], p2[1][1], p2[2][1], p2[3][1]);
@@ -209,12 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4 *>(smem + L::R + (2 * p + hf) * L::TILE + off) = make_uint4(p3[0][p], p3[1][p], p3[2][p], p3[3][p]);
                     }
                     arrive(B_BFREE + part);
-                    s += __shfl_xor_sync(~0u, s, 1);
                     z += __shfl_xor_sync(~0u, z, 1);
-                    if (hc == 0) {
-                        dwv[part * C + r] = s;
-                        dwr[part * C + r] = z;
-                    }
+                    if (hc == 0) dwr[part * C + r] = z;
                 }
                 tc_warp_wait(bar + B_DO, par, dead, d.spin);
                 if (x.nt < C) clear_rows(smem + L::G, x.nt);
@@ -264,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
                     if (lane == 0) ends[warp] = s;
                 }
-                // a (lanes 0..63) and p with its row sums (lanes 64..127): a row t, 16 columns s
+                // a (lanes 0..63) and p (lanes 64..127) with the sums of their parts of z: a row t, 16 columns s
                 tc_warp_wait(bar + B_E, par, dead, d.spin);
                 tc_fence_after();
                 {
@@ -272,7 +256,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool is_p = lane0 >= 64;
                     float y[16], z[16];
                     tc_load16(at + L::E + 16 * part, y);
-                    tc_load16(at + (is_p ? L::QK : L::E2) + 16 * part, z);
+                    if (!is_p) {
+                        tc_load16(at + L::E2 + 16 * part, z);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] += z[e];
+                    }
+                    tc_load16(at + L::QK + 16 * part, z);
                     tc_fence_before();
                     if (16 * part <= (lane0 & 32) + 31) {          // else above the diagonal: never used
                         const float ht = hi[t], lt = lo[t], ft = is_p ? d.scale : -be[t];
@@ -287,11 +276,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int m = 0; m < 4; ++m) {
                                 const int s = 16 * part + e + m;
                                 const float f = s <= t ? expf((ht - hs[m]) + (lt - ls[m])) * bs[m] : 0.f;
-                                const float w = ft * f * (is_p ? y[e + m] : y[e + m] + z[e + m]);
+                                const float w = ft * f * y[e + m];
                                 y[e + m] = s < t || (is_p && s == t) ? w : 0.f;
-                                zr = fmaf(y[e + m], z[e + m], zr);     // of p, with q k^T
+                                z[e + m] = s < t ? w * z[e + m] : 0.f;
+                                zr += z[e + m];
                             }
                         }
+                        zrow[(is_p ? 4 : 0) * C + part * C + t] = zr;
+                        // columns over the warp's rows: at each step a lane keeps the half of its columns that its bit names
+#pragma unroll
+                        for (int n = 8; n > 0; n /= 2)
+#pragma unroll
+                            for (int e = 0; e < n; ++e) {
+                                const bool up = lane & (2 * n);
+                                const float give = up ? z[e] : z[e + n];
+                                z[e] = (up ? z[e + n] : z[e]) + __shfl_xor_sync(~0u, give, 2 * n);
+                            }
+                        z[0] += __shfl_xor_sync(~0u, z[0], 1);
+                        if (!(lane & 1)) zcol[(warp & 3) * C + 16 * part + (lane >> 1)] = z[0];
                         unsigned char *dst = smem + (is_p ? L::P : L::A);
                         tc_warp_wait(bar + B_G3, par, dead, d.spin);   // r's planes are used
 #pragma unroll
@@ -308,7 +310,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 *reinterpret_cast<uint4 *>(dst + p * L::TILE + tc_at(t, 2 * part + e)) =
                                     make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         }
-                        if (is_p) zrow[part * C + t] = zr;
                     }
                     fence_proxy_async_smem();
                     arrive(B_PA);
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // results: this warp's lanes (32 of Dk) and 16 tokens
                 tc_warp_wait(bar + B_G, par, dead, d.spin);
                 tc_fence_after();
-                float f1[4], f2[4], f3[4], s1[4] = {};
+                float f1[4], f2[4], f3[4], s1[4] = {}, s2[4] = {};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 16 * part + 8 * (e >> 1) + 2 * i4 + (e & 1);
@@ -350,17 +351,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dq[l][m] += y[m];
                     }
                     tc_load_frag16(a + L::G2 + 16 * part, a + L::G3 + 16 * part, y, z);
+                    ldsm4t(qf, at_rc(sb + L::K, 16 * part, lane0 + 16 * l, lane));
 #pragma unroll
                     for (int m = 0; m < 8; ++m) {
                         const int e = 2 * (m >> 2) + (m & 1);
-                        dk[l][m] += fmaf(f2[e], y[m], f3[e] * z[m]);
+                        const unsigned kk = qf[2 * ((m >> 1) & 1) + (m >> 2)];
+                        const float kv = m & 1 ? hi_f32(kk) : lo_f32(kk);
+                        y[m] *= f2[e];
+                        z[m] *= f3[e];
+                        s1[e] = fmaf(kv, y[m], s1[e]);
+                        s2[e] = fmaf(kv, z[m], s2[e]);
+                        dk[l][m] += y[m] + z[m];
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                    for (int m = 4; m < 32; m *= 2) s1[e] += __shfl_xor_sync(~0u, s1[e], m);
-                    if (g4 == 0) dots[(warp & 3) * C + 16 * part + 8 * (e >> 1) + 2 * i4 + (e & 1)] = s1[e];
+                    for (int m = 4; m < 32; m *= 2) {
+                        s1[e] += __shfl_xor_sync(~0u, s1[e], m);
+                        s2[e] += __shfl_xor_sync(~0u, s2[e], m);
+                    }
+                    if (g4 == 0) {
+                        const int r = (warp & 3) * C + 16 * part + 8 * (e >> 1) + 2 * i4 + (e & 1);
+                        xs_t[r] = s1[e];
+                        ys_t[r] = s2[e];
+                    }
                 }
 #pragma unroll
                 for (int l = 0; l < 2; ++l) {
@@ -376,33 +391,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 meet();
                 if (warp == kWarps - 1) {
-                    double suf[2], rev = 0.0;
+                    float xt[2], yt[2];
+                    double whole = 0.0, dg[2];
 #pragma unroll
-                    for (int e = 1; e >= 0; --e) {
+                    for (int e = 0; e < 2; ++e) {
                         const int r = 2 * lane + e;
-                        float z = 0.f;
+                        xt[e] = yt[e] = 0.f;
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
-                            if (16 * p <= r) z += zrow[p * C + r];
-                            z += dots[p * C + r];
+                            if (16 * p <= r) xt[e] += zrow[p * C + r] + zrow[(4 + p) * C + r];
+                            if ((p & 1) || r < 32) xt[e] -= zcol[p * C + r];   // rows 32 (p % 2)..
+                            xt[e] += xs_t[p * C + r];
+                            yt[e] += ys_t[p * C + r];
                         }
-                        rev += (double)z - (double)be[r] * (double)((dwv[r] + dwv[C + r]) + (dwv[2 * C + r] + dwv[3 * C + r]));
-                        suf[e] = rev;
                     }
-                    double after = rev;
 #pragma unroll
-                    for (int m = 1; m < 32; m *= 2) {
-                        const double y = __shfl_down_sync(~0u, after, m);
-                        if (lane + m < 32) after += y;
-                    }
-                    after -= rev;
-#pragma unroll
-                    for (int p = 0; p < kWarps; ++p) after += (double)ends[p];
+                    for (int p = 0; p < kWarps; ++p) whole += (double)ends[p];
+                    delta_decay_sums(xt, yt, (double)from[C - 1] * whole, dg);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = 2 * lane + e;
                         if (r < rows) {
-                            o.grad_decay[(tok + r) * d.H + h] = r < x.nt ? (float)(after + suf[e]) : 0.f;
+                            const bool some = r < x.nt && expf(delta_decay(in.g[x.b * d.gs[0] + (t0 + r) * d.gs[1] + h * d.gs[2]])) != 0.f;
+                            o.grad_decay[(tok + r) * d.H + h] = some ? (float)dg[e] : 0.f;
                             o.grad_beta[(tok + r) * d.H + h] = r < x.nt ? (dwr[r] + dwr[C + r]) + (dwr[2 * C + r] + dwr[3 * C + r]) : 0.f;
                         }
                     }
@@ -551,8 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             state_load(dst, &mw, 32 * s, (int)chunk, bar + B_BOX + s);
                             state_load(dst + L::BOX / 2, &mr, 32 * s, (int)chunk, bar + B_BOX + s);
                         } else {
-                            state_load(dst, j == 1 ? &md : &ms, 32 * s,
-                                       (int)(j == 1 ? chunk : bh * (d.Nt + 1) + x.n + (j == 2 ? 1 : 0)), bar + B_BOX + s);
+                            state_load(dst, j == 1 ? &md : &ms, 32 * s, (int)(j == 1 ? chunk : bh * (d.Nt + 1) + x.n), bar + B_BOX + s);
                         }
                     }
                     __syncwarp();

@@ -181,6 +181,38 @@ cudaError_t launch_delta_back_local_tc(const DeltaDims &d, const DeltaIn &in, co
 
 __device__ __forceinline__ float delta_decay(float g) { return g < kDeltaMinDecay ? kDeltaMinDecay : g; }
 
+// The log-decays' gradients of a chunk, TL tokens a lane: x summed from each token on, y up to the one before,
+// and what crosses the whole chunk
+template <int TL>
+__device__ __forceinline__ void delta_decay_sums(const float (&x)[TL], const float (&y)[TL], double whole, double (&dg)[TL]) {
+    const int lane = threadIdx.x & 31;
+    double xs = 0.0, ys = 0.0;
+#pragma unroll
+    for (int i = 0; i < TL; ++i) {
+        xs += (double)x[i];
+        ys += (double)y[i];
+    }
+    double from = xs, upto = ys;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+        const double a = __shfl_down_sync(~0u, from, m), b = __shfl_up_sync(~0u, upto, m);
+        if (lane + m < 32) from += a;
+        if (lane >= m) upto += b;
+    }
+    upto -= ys;
+    double rest = from - xs;                       // of the lanes behind
+#pragma unroll
+    for (int i = TL - 1; i >= 0; --i) {
+        rest += (double)x[i];
+        dg[i] = rest;
+    }
+#pragma unroll
+    for (int i = 0; i < TL; ++i) {
+        dg[i] += upto + whole;
+        upto += (double)y[i];
+    }
+}
+
 // Tiles in shared memory have rows of PITCH bytes, an odd multiple of 16: ldmatrix's eight rows at
 // one column then fall into different banks, and every fragment's address is the lane's own offset
 // plus a constant.
