@@ -207,23 +207,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // boxes of the states: 32 columns of the lane's row
                 auto piece = [&](int c) { return *reinterpret_cast<const float4 *>(box + tc_at(lane0 + lane, c)); };
                 auto planes = [&](uint32_t dst, const float4 (&y)[8]) {
-                    constexpr int N = 3;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        unsigned p[N][8];
+                        float x[16];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            unsigned s0[N], s1[N];
-                            split_bf16<N>(y[4 * half + e].x, y[4 * half + e].y, s0);
-                            split_bf16<N>(y[4 * half + e].z, y[4 * half + e].w, s1);
+                        for (int e = 0; e < 4; ++e) *reinterpret_cast<float4 *>(x + 4 * e) = y[4 * half + e];
 #pragma unroll
-                            for (int m = 0; m < N; ++m) {
-                                p[m][2 * e] = s0[m];
-                                p[m][2 * e + 1] = s1[m];
+                        for (int m = 0; m < 3; ++m) {              // a term of each, then what is left of it
+                            unsigned w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+                                x[2 * e] -= lo_f32(w[e]);
+                                x[2 * e + 1] -= hi_f32(w[e]);
                             }
+                            tc_store8(dst + 64 * m + 16 * part + 8 * half, w);
                         }
-#pragma unroll
-                        for (int m = 0; m < N; ++m) tc_store8(dst + 64 * m + 16 * part + 8 * half, p[m]);
                     }
                     tc_wait_st();
                     tc_fence_before();
@@ -454,14 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (warp == kWarps) {
         // ---- the products
-        const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
+        const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0);
         // one tile's K steps of 16 columns, then the other's: `pair` bytes apart
         auto at_ks = [](int ks, int pair) { return ((ks >> 2) * pair + 32 * (ks & 3)) / 16; };
-        const uint32_t kq = tc_k_major(base + L::K), wg = tc_k_major(base + L::W), w1 = tc_k_major(base + L::W1), w2 = tc_k_major(base + L::W2);
-        const uint32_t gk = tc_k_major(base + L::G), rk = tc_k_major(base + L::R);
-        const uint32_t km = tc_n_major(base + L::K, L::PAIR), qm = tc_n_major(base + L::Q, L::PAIR);
-        const uint32_t pk = tc_k_major(base + L::P), pn = tc_n_major(base + L::P, L::TILE);
-        const uint32_t ak = tc_k_major(base + L::A), an = tc_n_major(base + L::A, L::TILE);
         unsigned it = 0, unit = 0;
         bool ok = true;
         for (unsigned i = blockIdx.x; i < items && ok; i += gridDim.x) {
@@ -469,6 +463,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.nt == 0) continue;
             for (int hh = 0; hh < group && ok; ++hh, ++unit) {
                 const unsigned par = unit & 1;
+                // anew for every head: kept over the loop, the 230 descriptors are spilled
+                const uint32_t base = __shfl_sync(~0u, smem_u32(smem), 0);
+                const uint32_t kq = tc_k_major(base + L::K), wg = tc_k_major(base + L::W), w1 = tc_k_major(base + L::W1), w2 = tc_k_major(base + L::W2);
+                const uint32_t gk = tc_k_major(base + L::G), rk = tc_k_major(base + L::R);
+                const uint32_t km = tc_n_major(base + L::K, L::PAIR), qm = tc_n_major(base + L::Q, L::PAIR);
+                const uint32_t pk = tc_k_major(base + L::P), pn = tc_n_major(base + L::P, L::TILE);
+                const uint32_t ak = tc_k_major(base + L::A), an = tc_n_major(base + L::A, L::TILE);
                 auto states = [&](uint32_t dst, uint32_t a, uint32_t tile, int pair, bool first) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
