@@ -457,7 +457,7 @@ int sdm_gated_delta_save(const sdm_delta_shape *shape, float *state, const void 
  *   grad_readings     [B, T, H, Dv] dtype, strided
  *   grad_final_state  [B, H, Dk, Dv] float32, the gradient of the final state, or NULL (zeros)
  *   grad_state        [B, H, Dk, Dv] float32, the gradient of the initial state (may be
- *                     grad_final_state itself)
+ *                     grad_final_state itself); these two at any address
  *   grad_q, grad_k    [B, T, Hk, Dk] dtype, heads that share a key head added in float32 in head order
  *   grad_v            [B, T, H, Dv] dtype
  *   grad_log_decay, grad_beta  [B, T, H] float32

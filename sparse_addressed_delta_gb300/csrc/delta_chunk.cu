@@ -612,6 +612,11 @@ __global__ void __launch_bounds__(2 * kDeltaMaxDk) k_delta_join(DeltaDims d, Del
     auto first = [&](int s) {
         if (live && s < d.segs && (s > 0 || state)) {
             const float *from = (s == 0 ? state : w.starts + slot(s) * delta_states(d)) + base;
+            if (BACK && s == 0) {                                  // the caller's gradient: any alignment
+#pragma unroll
+                for (int i = 0; i < 8; ++i) next[i] = from[i];
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(next + i) = *reinterpret_cast<const float4 *>(from + i);
         }
