@@ -615,6 +615,7 @@ int sdm_layer_norm(const void *x, long long rows, int n, long long x_stride, con
     if (!(eps >= 0.f)) return set_error(SDM_ERR_INVALID, "layer norm: eps must be >= 0");
     if (rows == 0) return SDM_OK;
     if (!y) return set_error(SDM_ERR_INVALID, "layer norm: NULL pointer");
+    if ((uintptr_t)stats % 8) return set_error(SDM_ERR_INVALID, "layer norm: stats must be 8-byte aligned");
     const int es = dtype == SDM_BF16 ? 2 : 4;
     NormGeom g = norm_geom(n, norm_vec(es, n, x_stride, x_stride, x, y, y), false);
     g.hull = norm_hull(es, g.vec, n, x_stride, x);
@@ -652,6 +653,8 @@ int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void 
                          ">= 0, got %lld", grad_stride);
     if (rows > 0 && (!grad || !stats || !grad_x))
         return set_error(SDM_ERR_INVALID, "layer norm backward: NULL pointer");
+    if (rows > 0 && (uintptr_t)stats % 8)
+        return set_error(SDM_ERR_INVALID, "layer norm backward: stats must be 8-byte aligned");
     const bool sums = grad_weight || grad_bias;
     if (sums && (!workspace || workspace_bytes < sdm_layer_norm_workspace_bytes(rows, n) ||
                  (uintptr_t)workspace % kAlign))
