@@ -40,8 +40,8 @@ void delta_segments(DeltaDims &d) {
     }
 }
 
-// Checks the shape; fills d. Returns SDM_OK or a refusal (message set).
-int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
+// Checks the shape; fills d. Returns SDM_OK or a refusal (message set). A forward does not look at grad_stride.
+int delta_check(const sdm_delta_shape *s, DeltaDims &d, bool back) {
     if (!s) return set_error(SDM_ERR_INVALID, "gated delta: shape is NULL");
     if (s->B < 0 || s->T < 0)
         return set_error(SDM_ERR_INVALID, "gated delta: B and T must be >= 0, got %d, %d", s->B, s->T);
@@ -62,7 +62,7 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     d.dtype = s->dtype;
     d.scale = s->scale;
     d.C = delta_chunk(s->dtype);
-    d.back = 0;
+    d.back = back;
     d.spin = wait_limit();
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     // blocks of a launch: one per chunk and head, or per head and 16 columns of the state
@@ -71,7 +71,7 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d) {
     const int es = s->dtype == SDM_BF16 ? 2 : 4;
     for (int i = 0; i < 3; ++i) {
         d.qs[i] = s->q_stride[i]; d.ks[i] = s->k_stride[i]; d.vs[i] = s->v_stride[i];
-        d.gs[i] = s->decay_stride[i]; d.bs[i] = s->beta_stride[i]; d.os[i] = s->grad_stride[i];
+        d.gs[i] = s->decay_stride[i]; d.bs[i] = s->beta_stride[i]; d.os[i] = back ? s->grad_stride[i] : 0;
         if ((d.qs[i] * es) % 16 || (d.ks[i] * es) % 16 || (d.vs[i] * es) % 16 || (d.os[i] * es) % 16)
             return set_error(SDM_ERR_INVALID, "gated delta: the strides of q, k, v and the gradient "
                              "must be multiples of 16 bytes");
@@ -220,7 +220,7 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
                   bool save, void *saved, size_t saved_bytes, void *workspace, size_t workspace_bytes,
                   void *stream) {
     DeltaDims d;
-    int rc = delta_check(shape, d);
+    int rc = delta_check(shape, d, false);
     if (rc != SDM_OK) return rc;
     if (d.B == 0 || d.T == 0) return SDM_OK;
     rc = delta_check_inputs(q, k, v, log_decay, beta);
@@ -257,7 +257,7 @@ extern "C" {
 
 size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
-    if (delta_check(shape, d) != SDM_OK) return 0;
+    if (delta_check(shape, d, false) != SDM_OK) return 0;
     return delta_layout(d, false).bytes + kAlign;
 }
 
@@ -271,7 +271,7 @@ int sdm_gated_delta(const sdm_delta_shape *shape, float *state, const void *q, c
 
 size_t sdm_gated_delta_saved_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
-    if (delta_check(shape, d) != SDM_OK) return 0;
+    if (delta_check(shape, d, false) != SDM_OK) return 0;
     return delta_saved(d) + kAlign;
 }
 
@@ -285,8 +285,7 @@ int sdm_gated_delta_save(const sdm_delta_shape *shape, float *state, const void 
 
 size_t sdm_gated_delta_backward_workspace_bytes(const sdm_delta_shape *shape) {
     DeltaDims d;
-    if (delta_check(shape, d) != SDM_OK) return 0;
-    d.back = 1;
+    if (delta_check(shape, d, true) != SDM_OK) return 0;
     return delta_layout(d, true).bytes + kAlign;
 }
 
@@ -297,9 +296,8 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
                              void *grad_v, float *grad_log_decay, float *grad_beta, void *workspace,
                              size_t workspace_bytes, void *stream) {
     DeltaDims d;
-    int rc = delta_check(shape, d);
+    int rc = delta_check(shape, d, true);
     if (rc != SDM_OK) return rc;
-    d.back = 1;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d.B == 0) return SDM_OK;
     if (!grad_state) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
