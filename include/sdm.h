@@ -419,7 +419,8 @@ int sdm_product_key_topk_backward(const int64_t *lin, const void *grad_val, long
  *                is used; their readings (and gradients) are 0. Clamped to [0, T].
  *   readings     [B, T, H, Dv] contiguous, written whole
  *   workspace    sdm_gated_delta_workspace_bytes(shape) bytes, 256-byte aligned; up to 8 tokens need
- *                none (sdm_gated_delta only). It begins with a status block, cleared by each call and read
+ *                none (sdm_gated_delta only). It begins with a status block, cleared by each call (one that needs
+ *                no workspace clears it in a given one of 256 bytes or more) and read
  *                by sdm_get_device_status: SDM_ERR_TIMEOUT there means that a bounded wait of a kernel gave
  *                up (sdm_set_wait_limit); the call's results are then undefined.
  * Deterministic. Products run on the tensor cores with the float32 operands (the state, the

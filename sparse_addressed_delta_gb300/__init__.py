@@ -837,7 +837,8 @@ def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.
     shape, (B, T, H, Hk, Dk, Dv), dev, dt = _delta_shape(q, k, v, log_decay, beta, valid_tokens, scale)
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
     readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
-    ws, n = (None, 0) if T <= DELTA_STEP_TOKENS else _scratch(workspace, lib.sdm_gated_delta_workspace_bytes, dev, shape)
+    # short calls need no workspace; one that is given has its status block cleared
+    ws, n = (None, 0) if workspace is None and T <= DELTA_STEP_TOKENS else _scratch(workspace, lib.sdm_gated_delta_workspace_bytes, dev, shape)
     _call(lib.sdm_gated_delta, dev, shape, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_decay.data_ptr(), beta.data_ptr(), _at(valid_tokens), readings.data_ptr(), _at(ws), n)
     return readings

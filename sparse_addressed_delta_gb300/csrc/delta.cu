@@ -200,6 +200,12 @@ cudaError_t delta_local(const DeltaDims &d, const DeltaIn &in, const DeltaLayout
     return launch_delta_local(d, in, q, k, w, st);
 }
 
+// The status block of a workspace that no kernel of this call clears (one too small to hold it is no workspace:
+// such calls need none)
+cudaError_t delta_clear(void *ws, size_t have, cudaStream_t st) {
+    return ws && have >= kAlign ? cudaMemsetAsync(ws, 0, sizeof(DevStatus), st) : cudaSuccess;
+}
+
 int delta_check_ws(const char *what, const void *ws, size_t have, size_t need) {
     if (!ws || have < need || (uintptr_t)ws % kAlign)
         return set_error(SDM_ERR_WORKSPACE, "gated delta: %s NULL, too small (%zu of %zu bytes) "
@@ -222,15 +228,18 @@ int delta_forward(const sdm_delta_shape *shape, float *state, const void *q, con
     DeltaDims d;
     int rc = delta_check(shape, d, false);
     if (rc != SDM_OK) return rc;
-    if (d.B == 0 || d.T == 0) return SDM_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d.B == 0 || d.T == 0) return delta_status(delta_clear(workspace, workspace_bytes, st));
     rc = delta_check_inputs(q, k, v, log_decay, beta);
     if (rc != SDM_OK) return rc;
     if (!state || !readings) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
     if (off16(state) || off16(readings))
         return set_error(SDM_ERR_INVALID, "gated delta: the state and the readings must be 16-byte aligned");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     DeltaIn in{q, k, v, log_decay, beta, valid_tokens};
-    if (!save && by_token(d)) return delta_status(launch_delta_step(d, in, state, readings, st));
+    if (!save && by_token(d)) {
+        const cudaError_t e = delta_clear(workspace, workspace_bytes, st);
+        return delta_status(e == cudaSuccess ? launch_delta_step(d, in, state, readings, st) : e);
+    }
     const DeltaLayout l = delta_layout(d, false);
     rc = delta_check_ws("workspace", workspace, workspace_bytes, l.bytes);
     if (rc == SDM_OK && save) rc = delta_check_ws("saved buffer", saved, saved_bytes, delta_saved(d));
@@ -299,10 +308,12 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
     int rc = delta_check(shape, d, true);
     if (rc != SDM_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (d.B == 0) return SDM_OK;
+    if (d.B == 0) return delta_status(delta_clear(workspace, workspace_bytes, st));
     if (!grad_state) return set_error(SDM_ERR_INVALID, "gated delta: NULL pointer");
     if (d.T == 0) {                      // the final state is the initial one
         const size_t bytes = (size_t)d.B * d.H * d.Dk * d.Dv * 4;
+        const cudaError_t e = delta_clear(workspace, workspace_bytes, st);
+        if (e != cudaSuccess) return delta_status(e);
         return delta_status(grad_final_state ? cudaMemcpyAsync(grad_state, grad_final_state, bytes, cudaMemcpyDeviceToDevice, st)
                                              : cudaMemsetAsync(grad_state, 0, bytes, st));
     }
