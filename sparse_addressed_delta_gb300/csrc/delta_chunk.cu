@@ -310,11 +310,11 @@ struct ScanSmem {
     static constexpr int KPI = delta_pitch(DKP * 2), TILE = C * KPI;
     static constexpr int Q = KP * TILE, X = 2 * KP * TILE, P = X + 3 * C * XP, V = P + PP * C * XP;
     static constexpr int AUX = V + C * VP, STAGE = AUX + 3 * C * 4;
-    static constexpr int BYTES = 2 * STAGE;
+    static constexpr int BAD = 2 * STAGE, BYTES = BAD + NW * 16 * 4;   // per column: the first chunk delta_column takes
 };
 
 // One block per head and NW * 16 of its columns; two stages of chunk inputs, the next chunk's copies
-// in flight while this one is computed. SAVE: also stores S0 and u for the backward.
+// in flight while this one is computed. SAVE: also stores S0 and r for the backward.
 template <int DKP, int NW, bool SAVE>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_delta_scan(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, float *state,
@@ -340,6 +340,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
     float *out = o + ((long long)b * d.T * d.H + h) * d.Dv;
     const long long orow = (long long)d.H * d.Dv;
     const unsigned s0 = smem_u32(smem);
+    int *bad = reinterpret_cast<int *>(smem + L::BAD) + 16 * warp;
+    if (lane < 16) bad[lane] = -1;
+    __syncwarp();
 
     auto load = [&](int n, int stage) {
         const unsigned st = s0 + stage * L::STAGE;
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
 
     float S[ND][4];
     const bool real = !carry || blk.seg == 0;
-    const float *sp = (d.segs > 1 && !carry ? w.starts + blk.seg * delta_states(d) : state) + (bh * d.Dk) * d.Dv + dv0;
+    float *sp = (d.segs > 1 && !carry ? w.starts + blk.seg * delta_states(d) : state) + (bh * d.Dk) * d.Dv + dv0;
 #pragma unroll
     for (int j = 0; j < ND; ++j)
 #pragma unroll
@@ -560,6 +563,25 @@ __global__ void __launch_bounds__(NW * 32, 1)
                                 for (int m = 0; m < 4; ++m)
                                     mma_bf16(acc[m], ua[ks][x], bb[p][m >> 1][2 * (m & 1)], bb[p][m >> 1][2 * (m & 1) + 1]);
                 }
+                // a column's first update that is not finite (then no row of it is): its state before goes back to
+                // where it came from, for delta_column
+                if (nn == 0 && !carry) {
+                    const bool off[2] = {!delta_finite(acc[0][0]), !delta_finite(acc[0][2])};
+                    if (__any_sync(~0u, off[0] || off[1])) {
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const bool now = off[f] && bad[g4 + 8 * f] < 0;
+                            __syncwarp();
+                            if (now && i4 == 0) bad[g4 + 8 * f] = n;
+                            if (now)
+#pragma unroll
+                                for (int j = 0; j < ND; ++j)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (8 * j + 2 * i4 + e < d.Dk) sp[(size_t)(8 * j + 2 * i4 + e) * d.Dv + g4 + 8 * f] = S[j][2 * f + e];
+                        }
+                    }
+                }
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -569,6 +591,16 @@ __global__ void __launch_bounds__(NW * 32, 1)
         __syncthreads();
     }
     if (!mine) return;
+    if (!carry) {
+        __syncwarp();
+        for (int c = 0; c < 16; ++c) {
+            const int n = bad[c], t0 = n * C;
+            if (n < 0) continue;
+            delta_column<float>(d, in, b, h, dv0 + c, t0, ntok - t0 < C ? ntok - t0 : C, sp + c, out + t0 * orow + dv0 + c,
+                                SAVE ? rsave + (bh * d.Nt + n) * (long long)C * d.Dv + dv0 + c : nullptr);
+        }
+        __syncwarp();                                              // before the last state is stored over it
+    }
     if (carry) {
         store_state((blk.unit ? w.units + ((blk.seg - 1) * (long long)d.B * d.H + bh) * d.Dk * d.Dk
                               : w.starts + (blk.seg + 1) * delta_states(d) + bh * d.Dk * (long long)d.Dv) + dv0);

@@ -181,6 +181,52 @@ cudaError_t launch_delta_back_local_tc(const DeltaDims &d, const DeltaIn &in, co
 
 __device__ __forceinline__ float delta_decay(float g) { return g < kDeltaMinDecay ? kDeltaMinDecay : g; }
 
+__device__ __forceinline__ bool delta_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// One column of a chunk token by token, by one warp: S its state [Dk] at the chunk's start (Dv apart), o its readings
+// and r (may be null) what its values lack. For columns whose update in a chunk is not finite: in the chunk's products
+// a NaN or infinity of one token meets the zeros of the tokens before it (0 x inf is NaN), here it reaches the
+// later ones alone.
+template <typename T>
+__device__ __forceinline__ void delta_column(const DeltaDims &d, const DeltaIn &in, int b, int h, int dv, int t0, int nt, const float *S,
+                                             T *o, float *r) {
+    constexpr int NR = kDeltaMaxDk / 32;
+    const int lane = threadIdx.x & 31, hk = h / (d.H / d.Hk);
+    const T *q = static_cast<const T *>(in.q) + b * d.qs[0] + hk * d.qs[2] + t0 * d.qs[1];
+    const T *k = static_cast<const T *>(in.k) + b * d.ks[0] + hk * d.ks[2] + t0 * d.ks[1];
+    const T *v = static_cast<const T *>(in.v) + b * d.vs[0] + h * d.vs[2] + t0 * d.vs[1] + dv;
+    const float *g = in.g + b * d.gs[0] + h * d.gs[2] + t0 * d.gs[1], *be = in.beta + b * d.bs[0] + h * d.bs[2] + t0 * d.bs[1];
+    float s[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) s[i] = lane + 32 * i < d.Dk ? S[(size_t)(lane + 32 * i) * d.Dv] : 0.f;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+        const float fade = expf(delta_decay(g[t * d.gs[1]]));
+        float a = 0.f, c = 0.f;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (lane + 32 * i < d.Dk) {
+                s[i] *= fade;
+                a = fmaf(to_f32(k[t * d.ks[1] + lane + 32 * i]), s[i], a);
+            }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(~0u, a, m);
+        const float lack = to_f32(v[t * d.vs[1]]) - a, u = be[t * d.bs[1]] * lack;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (lane + 32 * i < d.Dk) {
+                s[i] = fmaf(to_f32(k[t * d.ks[1] + lane + 32 * i]), u, s[i]);
+                c = fmaf(to_f32(q[t * d.qs[1] + lane + 32 * i]), s[i], c);
+            }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) c += __shfl_xor_sync(~0u, c, m);
+        if (lane == 0) {
+            o[(long long)t * d.H * d.Dv] = from_f32<T>(d.scale * c);
+            if (r) r[(long long)t * d.Dv] = lack;
+        }
+    }
+}
+
 // The log-decays' gradients of a chunk, TL tokens a lane: x summed from each token on, y up to the one before,
 // and what crosses the whole chunk
 template <int TL>
