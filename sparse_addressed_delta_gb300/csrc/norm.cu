@@ -426,20 +426,39 @@ __global__ void __launch_bounds__(BLOCK ? (WIDE ? 1024 : 512) : kNormBlock)
     }
 }
 
-// column sums of the blocks' partials, in a fixed order: kNormColSlices runs of blocks, then them
+// s + x as the rounded sum and what the rounding lost, added to `low`
+__device__ __forceinline__ float add_exact(float s, float x, float &low) {
+    const float sum = s + x, of_x = sum - s;
+    low += (s - (sum - of_x)) + (x - of_x);
+    return sum;
+}
+
+// column sums of the blocks' partials, in a fixed order: kNormColSlices runs of blocks, then them in pairs, with what
+// the roundings lose kept beside (5003 x 1007 float32, in one float each: 1.7e-7 off float64 with the runs one after
+// the other, 1.4e-7 in pairs)
 __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
     k_norm_cols(const float *part, int parts, int n, float *dw, float *db) {
-    __shared__ float sh[kNormColSlices][kNormColThreads];
+    __shared__ float sh[kNormColSlices][kNormColThreads], lost[kNormColSlices][kNormColThreads];
     const int tx = threadIdx.x % kNormColThreads, ty = threadIdx.x / kNormColThreads;
     const int c = blockIdx.x * kNormColThreads + tx;     // over [2][n]
-    float s = 0.f;
+    float s = 0.f, low = 0.f;
     if (c < 2 * n)
 #pragma unroll 8
-        for (int p = ty; p < parts; p += kNormColSlices) s += __ldg(part + (size_t)p * 2 * n + c);
+        for (int p = ty; p < parts; p += kNormColSlices) s = add_exact(s, __ldg(part + (size_t)p * 2 * n + c), low);
     sh[ty][tx] = s;
-    __syncthreads();
+    lost[ty][tx] = low;
+#pragma unroll
+    for (int h = kNormColSlices / 2; h > 0; h /= 2) {
+        __syncthreads();
+        if (ty < h) {
+            low = lost[ty][tx] + lost[ty + h][tx];
+            sh[ty][tx] = add_exact(sh[ty][tx], sh[ty + h][tx], low);
+            lost[ty][tx] = low;
+        }
+    }
     if (ty == 0 && c < 2 * n) {
-        for (int k = 1; k < kNormColSlices; ++k) s += sh[k][tx];
+        s = sh[0][tx];
+        if (fabsf(s) <= 3.402823466e38f) s += lost[0][tx];   // an infinite sum is one; what it lost is a NaN
         if (c < n) {
             if (dw) dw[c] = s;
         } else if (db) {
