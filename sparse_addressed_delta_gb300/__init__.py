@@ -16,6 +16,7 @@ import ctypes
 import importlib.util
 import os
 import struct
+import sysconfig
 import threading
 from typing import Dict, Optional
 
@@ -33,6 +34,7 @@ __all__ = ["FLAG_SNAPSHOT_BF16", "FLAG_SNAPSHOT_FP8", "FLAG_TOKEN_GATE", "FLAG_S
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libsdm.so")
+_calls_path = os.path.join(_HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SDM_F32, SDM_BF16 = 0, 1
 DELTA_STEP_TOKENS = 8             # gated_delta: up to this many tokens go one by one
@@ -158,9 +160,16 @@ def library() -> ctypes.CDLL:
     return _lib
 
 
+class _NoCalls:
+    """In the place of a module of the everyday calls that is not there: it takes no call."""
+    gated_delta = layer_norm = layer_norm_backward = staticmethod(lambda *args: None)
+
+
 def _calls(lib: ctypes.CDLL):
-    """The module of the everyday calls (csrc/calls.cpp), built beside the library."""
-    spec = importlib.util.spec_from_file_location("_calls", os.path.join(_HERE, "_calls.so"))
+    """The module of the everyday calls (csrc/calls.cpp), where it was built for this interpreter."""
+    if not os.path.exists(_calls_path) or not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        return _NoCalls
+    spec = importlib.util.spec_from_file_location("_calls", _calls_path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     at = lambda *names: tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names)  # noqa: E731

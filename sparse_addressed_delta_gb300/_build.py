@@ -1,5 +1,6 @@
-"""Builds libsdm.so (the sm_103a kernels and the C ABI) in-tree with nvcc, and _calls.so (the CPython module
-of the everyday calls, csrc/calls.cpp) with g++.
+"""Builds libsdm.so (the sm_103a kernels and the C ABI) in-tree with nvcc, and _calls (the CPython module of the
+everyday calls, csrc/calls.cpp; named for this interpreter) with g++. The module saves host time alone: without
+Python's headers it is left out, and the binding makes those calls by itself.
 
 One object per translation unit, compiled in parallel, linked into a shared library next to
 this file. Nothing is installed.
@@ -19,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdm.so")
-CALLS = os.path.join(PKG, "_calls.so")
+CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cu", "phase1.cu", "solve.cu", "phase2.cu", "dualmm_tc.cu", "phase2_fused.cu",
            "noalloc.cu", "backward.cu", "host_io.cu", "layer_io.cu", "product_key.cu",
            "norm.cu", "delta.cu", "delta_step.cu", "delta_chunk.cu",
@@ -35,6 +36,12 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else (shutil.which("nvcc") or "nvcc")
 
 
+def _headers():
+    """Where Python.h is, or None."""
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) else None
+
+
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "sdm.h"))
@@ -48,10 +55,26 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(f) > t for f in deps)
 
 
+def build_calls() -> str | None:
+    """Builds the module of the everyday calls; None without Python's headers."""
+    include = _headers()
+    if include is None:
+        print("Python.h not found: built without the module of the everyday calls")
+        return None
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", include,
+           "-I", INCLUDE, os.path.join(CSRC, "calls.cpp"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     deps = _deps()
-    if not force and not _stale(LIB, deps) and not _stale(CALLS, deps):
+    if not force and not _stale(LIB, deps) and not (_headers() and _stale(CALLS, deps)):
         return LIB
     nvcc = _nvcc()
 
@@ -64,15 +87,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr)
         return obj
-
-    def build_calls():
-        tmp = CALLS + f".tmp{os.getpid()}"
-        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
-               "-I", INCLUDE, os.path.join(CSRC, "calls.cpp"), "-o", tmp]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, CALLS)
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         calls = ex.submit(build_calls)
