@@ -919,6 +919,8 @@ def _norm_rows(x: torch.Tensor, name: str):
     if not x.is_cuda or not shape or shape[-1] < 1:
         raise ValueError(f"{name} must be a CUDA tensor of rows, [..., n] with n >= 1")
     n = shape[-1]
+    if n > 0x7fffffff:                         # the C ABI's int would take what is left of it
+        raise SdmError(-2, f"layer norm: {name} has {n} columns")
     rows = x.numel() // n
     if x.is_contiguous():
         return rows, n, n

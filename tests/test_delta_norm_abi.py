@@ -1,6 +1,9 @@
 """Refusals of the layer norm's and the gated delta rule's C ABI that need no device: the addresses here are never
 read, every call returns before anything is queued."""
 
+import pytest
+import torch
+
 import sparse_addressed_delta_gb300 as sdm
 
 INVALID, WORKSPACE = -1, -5
@@ -37,3 +40,19 @@ def test_the_forward_ignores_the_gradients_strides():
         assert lib.sdm_gated_delta_save(s, *[AT] * 8, None, 0, None, 0, None) == WORKSPACE
         assert lib.sdm_gated_delta_backward_workspace_bytes(s) == 0
         assert lib.sdm_gated_delta_backward(s, *[AT] * 6, AT, 0, *[AT] * 8, None, 0, None) < 0
+
+
+class DeviceLike(torch.Tensor):
+    """A tensor without storage that says it is on a device."""
+    is_cuda = True
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 128])
+def test_more_columns_than_an_int(n):
+    """Refused as too many columns are, not taken as what an int keeps of them (128)."""
+    x = torch.empty((1, n), device="meta").as_subclass(DeviceLike)
+    for fn in (sdm.layer_norm, sdm.layer_norm_save):
+        with pytest.raises(sdm.SdmError, match="columns"):
+            fn(x)
+    with pytest.raises(sdm.SdmError, match="columns"):
+        sdm.layer_norm_backward(x, x, None, torch.empty((1, 2), device="meta"))
