@@ -29,8 +29,8 @@ struct BackSmem {
     static constexpr int KPI = delta_pitch(DKP * 2), TILE = C * KPI;
     static constexpr int Q = KP * TILE, X = 2 * KP * TILE, P = X + 3 * C * XP, V = P + PP * C * XP;
     static constexpr int AUX = V + C * VP, STAGE = AUX + 3 * C * 4;
-    static constexpr int STAGES = 2 * STAGE <= 227 * 1024 ? 2 : 1;
-    static constexpr int BYTES = STAGES * STAGE;
+    static constexpr int BYTES = 2 * STAGE;
+    static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 // One block per head and NW * 16 of its columns, from the last chunk to the first.
@@ -91,22 +91,17 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 if (dk < d.Dk) dst[(size_t)dk * d.Dv + g4 + 8 * (e >> 1)] = S[j][e];
             }
     };
-    if (L::STAGES == 2 && nch > 0) load(n1 - 1, 0);
+    if (nch > 0) load(n1 - 1, 0);
     for (int it = 0; it < nch; ++it) {
         const int n = n1 - 1 - it;
-        if constexpr (L::STAGES == 2) {
-            if (n > n0) {
-                load(n - 1, (it + 1) & 1);
-                cp_async_wait<1>();
-            } else {
-                cp_async_wait<0>();
-            }
+        if (n > n0) {
+            load(n - 1, (it + 1) & 1);
+            cp_async_wait<1>();
         } else {
-            load(n, 0);
             cp_async_wait<0>();
         }
         __syncthreads();
-        const int stage = L::STAGES == 2 ? (it & 1) * L::STAGE : 0;
+        const int stage = (it & 1) * L::STAGE;
         const unsigned sk = s0 + stage, sq = sk + L::Q, sx = sk + L::X, spp = sk + L::P, sv = sk + L::V;
         const float *from = reinterpret_cast<const float *>(smem + stage + L::AUX), *to = from + C, *be = to + C;
         const int nt = ntok - n * C < C ? ntok - n * C : C;
