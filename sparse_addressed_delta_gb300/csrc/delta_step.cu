@@ -16,7 +16,7 @@ namespace {
 constexpr int kStepThreads = 256, kStepWarps = kStepThreads / 32;
 
 // 128 columns: two blocks an SM, their loads and stores in turn (256 x 32 heads of 128 x 128: 182 us, 89 %
-// of the copy rate; 64 columns 181, 32 columns 244, 16 columns 339)
+// of the copy rate; 32 columns 246, 16 columns 342)
 template <typename T, int LPR>
 __global__ void __launch_bounds__(kStepThreads, LPR == 32 ? 2 : 4)
     k_delta_step(DeltaDims d, DeltaIn in, float *state, T *o) {
@@ -129,9 +129,11 @@ cudaError_t launch_step(const DeltaDims &d, const DeltaIn &in, float *state, voi
                         cudaStream_t st) {
     const long long heads = (long long)d.B * d.H;
     T *out = static_cast<T *>(o);
-    // whole rows of 128 columns when there are heads enough for every SM twice: fewer blocks read
-    // q and k; else narrow slices, which spread a head over more SMs
-    if (d.Dv % 128 == 0 && heads * (d.Dv / 128) >= 4 * kRefSms)
+    // whole rows of 128 columns once there is a block of them for every SM: fewer blocks read q and k. Fewer heads
+    // in narrow slices, which spread a head over more SMs. 128, 32 and 16 columns, us (heads of 128 x 128, bfloat16):
+    // 16 heads x 8 tokens 18.4, 16.4, 16.4; 96 x 1 10.2, 8.2, 12.3; 128 x 1 10.2, 10.2, 12.3; 256 x 1 12.3, 14.3, 18.4;
+    // 512 x 1 18.4, 22.5, 28.7; 512 x 8 41, 57, 104. 32 and 16, 16 heads of 64 x 64 6.2, 6.1; 512 12.3, 16.4.
+    if (d.Dv % 128 == 0 && heads * (d.Dv / 128) >= kRefSms)
         k_delta_step<T, 32><<<(unsigned)(heads * (d.Dv / 128)), kStepThreads, 0, st>>>(d, in, state, out);
     else if (d.Dv % 32 == 0 && heads * (d.Dv / 32) >= 2 * kRefSms)
         k_delta_step<T, 8><<<(unsigned)(heads * (d.Dv / 32)), kStepThreads, 0, st>>>(d, in, state, out);
