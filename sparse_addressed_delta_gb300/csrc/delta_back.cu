@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     {
         const float4 *x = reinterpret_cast<const float4 *>(s0p), *y = reinterpret_cast<const float4 *>(d1p);
         float s = 0.f;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = tid; i < (int)(cells / 4); i += THREADS) {
             const float4 u = __ldg(x + i), v = __ldg(y + i);
             s = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, s))));
@@ -425,24 +425,23 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
         const int rest = d.Dv - c0 < kBackCols ? d.Dv - c0 : kBackCols;
         // this lane's two rows of the states: columns 2 i4 and 8 + 2 i4 of each 16
         float2 xs[2][2], ys[2][2];
-        auto fetch = [&](int ks) {
+        auto fetch_into = [&](float2 (&x)[2][2], const float *from, int ks) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const int row = dk0 + 8 * e + g4;
-                    const long long at = (long long)row * d.Dv + c0 + 16 * ks + 8 * m + 2 * i4;
                     const bool live = row < d.Dk && 16 * ks < rest;
-                    xs[e][m] = live ? __ldg(reinterpret_cast<const float2 *>(s0p + at)) : make_float2(0.f, 0.f);
-                    ys[e][m] = live ? __ldg(reinterpret_cast<const float2 *>(d1p + at)) : make_float2(0.f, 0.f);
+                    x[e][m] = live ? __ldg(reinterpret_cast<const float2 *>(from + (long long)row * d.Dv + c0 + 16 * ks + 8 * m + 2 * i4)) : make_float2(0.f, 0.f);
                 }
         };
-        fetch(0);
+        fetch_into(xs, s0p, 0);
+        fetch_into(ys, d1p, 0);
         cp_async_wait<0>();
         __syncthreads();
         // E += dw r^T, dP += dO r^T
         if (block) {
-#pragma unroll 2
+#pragma unroll 1
             for (int ks = 0; ks < rest / 16; ++ks) {
                 unsigned aw[PL][4], ao[KP][4], br[3][4];
 #pragma unroll
@@ -464,15 +463,30 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
         }
         // products with the states over this column tile
         for (int ks = 0; ks < rest / 16; ++ks) {
-            unsigned bs[2][2][3], bd[2][2][PL];                   // [8-column tile][k half][plane]
+            unsigned bs[2][2][3];                                 // [8-column tile][k half][plane]
+            auto split = [&](const float2 (&x)[2][2]) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    split_bf16<3>(xs[e][m].x, xs[e][m].y, bs[e][m]);
-                    split_bf16<PL>(ys[e][m].x, ys[e][m].y, bd[e][m]);
-                }
-            fetch(ks + 1);
+                    for (int m = 0; m < 2; ++m) split_bf16<3>(x[e][m].x, x[e][m].y, bs[e][m]);
+            };
+            split(ys);
+            fetch_into(ys, d1p, ks + 1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                unsigned a[PL][4];
+#pragma unroll
+                for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<VPI>(sr + p * L::VT, 16 * (m0 + mt), 16 * ks, lane));
+#pragma unroll
+                for (int s = PL - 1; s >= 0; --s)
+#pragma unroll
+                    for (int p = PL - 1; p >= 0; --p)
+                        if (plane_pair(s, p, PL))
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) mma_bf16(s + p ? L3[mt][e] : G3[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
+            }
+            split(xs);
+            fetch_into(xs, s0p, ks + 1);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 unsigned a[3][4];
@@ -495,15 +509,6 @@ __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
                         if (plane_pair(s, p, PL))
 #pragma unroll
                             for (int e = 0; e < 2; ++e) mma_bf16(s + p ? L2[mt][e] : G2[mt][e], a[s], bs[e][0][p], bs[e][1][p]);
-#pragma unroll
-                for (int p = 0; p < PL; ++p) ldsm4(a[p], frag_rc<VPI>(sr + p * L::VT, r0, 16 * ks, lane));
-#pragma unroll
-                for (int s = PL - 1; s >= 0; --s)
-#pragma unroll
-                    for (int p = PL - 1; p >= 0; --p)
-                        if (plane_pair(s, p, PL))
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) mma_bf16(s + p ? L3[mt][e] : G3[mt][e], a[s], bd[e][0][p], bd[e][1][p]);
             }
         }
     }
