@@ -438,7 +438,8 @@ __device__ __forceinline__ float add_exact(float s, float x, float &low) {
 // the other, 1.4e-7 in pairs)
 __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
     k_norm_cols(const float *part, int parts, int n, float *dw, float *db) {
-    __shared__ float sh[kNormColSlices][kNormColThreads], lost[kNormColSlices][kNormColThreads];
+    static_assert(kNormColSlices == 64 && kNormColThreads <= 32, "a warp a column, two runs a lane");
+    __shared__ float sh[kNormColSlices][kNormColThreads + 1], lost[kNormColSlices][kNormColThreads + 1];
     const int tx = threadIdx.x % kNormColThreads, ty = threadIdx.x / kNormColThreads;
     const int c = blockIdx.x * kNormColThreads + tx;     // over [2][n]
     float s = 0.f, low = 0.f;
@@ -447,22 +448,23 @@ __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
         for (int p = ty; p < parts; p += kNormColSlices) s = add_exact(s, __ldg(part + (size_t)p * 2 * n + c), low);
     sh[ty][tx] = s;
     lost[ty][tx] = low;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * kNormColThreads + warp;
+    if (warp >= kNormColThreads) return;
+    low = lost[lane][warp] + lost[lane + 32][warp];
+    s = add_exact(sh[lane][warp], sh[lane + 32][warp], low);
 #pragma unroll
-    for (int h = kNormColSlices / 2; h > 0; h /= 2) {
-        __syncthreads();
-        if (ty < h) {
-            low = lost[ty][tx] + lost[ty + h][tx];
-            sh[ty][tx] = add_exact(sh[ty][tx], sh[ty + h][tx], low);
-            lost[ty][tx] = low;
-        }
+    for (int m = 16; m > 0; m >>= 1) {
+        const float x = __shfl_down_sync(~0u, s, m);
+        low += __shfl_down_sync(~0u, low, m);
+        s = add_exact(s, x, low);
     }
-    if (ty == 0 && c < 2 * n) {
-        s = sh[0][tx];
-        if (fabsf(s) <= 3.402823466e38f) s += lost[0][tx];   // an infinite sum is one; what it lost is a NaN
-        if (c < n) {
-            if (dw) dw[c] = s;
+    if (lane == 0 && col < 2 * n) {
+        if (fabsf(s) <= 3.402823466e38f) s += low;           // an infinite sum is one; what it lost is a NaN
+        if (col < n) {
+            if (dw) dw[col] = s;
         } else if (db) {
-            db[c - n] = s;
+            db[col - n] = s;
         }
     }
 }
