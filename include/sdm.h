@@ -423,9 +423,12 @@ int sdm_product_key_topk_backward(const int64_t *lin, const void *grad_val, long
  *                no workspace clears it in a given one of 256 bytes or more) and read
  *                by sdm_get_device_status: SDM_ERR_TIMEOUT there means that a bounded wait of a kernel gave
  *                up (sdm_set_wait_limit); the call's results are then undefined.
- * Deterministic. Products run on the tensor cores with the float32 operands (the state, the
- * corrections, the chunk's inverse) split into bfloat16 terms that keep float32's accuracy. Long sequences
- * of few heads are scanned in segments at once; how many depends on the shape and type alone.
+ * Deterministic. Products run on the tensor cores with every float32 operand (the state, the corrections,
+ * the chunk's inverse) split into three bfloat16 terms that keep float32's accuracy; bfloat16 readings and
+ * gradients are such results, rounded once. Long sequences of few heads are scanned in segments at once; how
+ * many depends on the shape and type alone.
+ * A NaN or infinity of an input reaches the readings and states that the recurrence carries it to, and no others.
+ * The gradients of a sequence and key head that has one are undefined.
  * Each call returns SDM_OK once queued on stream, or a negative sdm_status (nothing queued).
  * --------------------------------------------------------------------------------------- */
 typedef struct {

@@ -834,7 +834,11 @@ def gated_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.
     16 bytes; H a multiple of Hk (value head h uses key head h // (H // Hk)); Dk (up to 128) and Dv
     (up to 512) multiples of 16. log_decay, beta [B, T, H] float32. valid_tokens [B] int32 (None:
     all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step; up to 8 tokens
-    need no workspace. What is allocated here belongs to ``stream`` (None: the current one)."""
+    need no workspace. What is allocated here belongs to ``stream`` (None: the current one).
+
+    The tensor-core kernels' waits are bounded; one that gives up (a fault elsewhere, or a limit that
+    set_wait_limit lowered) says so in the workspace alone. A caller who wants to know gives a
+    ``workspace`` and asks device_status(workspace) after the call; without one the report is lost."""
     if stream is not None:
         return _on(stream, gated_delta, state, q, k, v, log_decay, beta, valid_tokens, scale=scale,
                    readings=readings, workspace=workspace)
@@ -860,7 +864,7 @@ def gated_delta_save(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     """gated_delta that also keeps what its backward needs: (readings, saved), with ``state``
     advanced in place. ``saved`` (uint8) holds the state at the start of every chunk of 64 (float32
     inputs: 32) tokens, the chunks' corrections and, for long sequences of few heads, the segments' transition
-    matrices."""
+    matrices. A wait that gives up is reported as gated_delta's: in a ``workspace`` of the caller's."""
     if stream is not None:
         return _on(stream, gated_delta_save, state, q, k, v, log_decay, beta, valid_tokens, scale=scale,
                    readings=readings, saved=saved, workspace=workspace)
@@ -883,7 +887,8 @@ def gated_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     """The backward after gated_delta_save (same inputs and scale): a dict of grad_q, grad_k, grad_v
     (the inputs' dtype; heads that share a key head are summed), grad_log_decay, grad_beta and
     grad_state (float32; of the initial state). ``grad_state`` [B, H, Dk, Dv] float32: the gradient
-    of the final state (None: zero); it is not changed."""
+    of the final state (None: zero); it is not changed. A wait that gives up is reported as
+    gated_delta's: in a ``workspace`` of the caller's."""
     if stream is not None:
         return _on(stream, gated_delta_backward, q, k, v, log_decay, beta, valid_tokens, saved, grad_readings,
                    grad_state=grad_state, scale=scale, workspace=workspace)

@@ -12,10 +12,11 @@ namespace {
 // which pay when the heads alone leave SMs idle. By the times in microseconds measured: a chunk alone and
 // beside twice as many blocks, a chunk of the first launch (the tensor-memory form at 128 x 128; the register
 // form by its products), a block's start, the join and each of its steps. Measured, whole call, in segments
-// and not, bfloat16 at 128 x 128: 32 heads x 256 chunks 580 and 913 us, 16 x 64 137 and 234, 4 x 64 111 and
-// 213 (backward 279 and 478, 160 and 371); 64 heads x 64 chunks 330 and 305, so not taken. float32 training, 8
-// heads of 64 x 64 x 32 chunks: 186 and 276. By shape and type alone: a saving forward's results are
-// the plain one's, and a backward's segments its forward's, whatever the strides.
+// and not, bfloat16 at 128 x 128: 32 heads x 256 chunks 637 and 1006 us, 16 x 64 139 and 250, 4 x 64 109 and
+// 229 (backward 294 and 451, 169 and 336). Narrower heads are taken to cost the same: at 64 x 64, 16 heads x 64
+// chunks 111 and 205, 4 x 64 84 and 184 (backward 242 and 359, 136 and 257); at 64 x 128, 32 x 64 170 and 225.
+// float32 training, 8 heads of 64 x 64 x 32 chunks: 191 and 332. By shape and type alone: a saving forward's results
+// are the plain one's, and a backward's segments its forward's, whatever the strides.
 void delta_segments(DeltaDims &d) {
     constexpr double kStart = 8.0, kJoin = 8.0, kJoinStep = 4.0;
     const bool tensor = d.dtype == SDM_BF16;
@@ -78,7 +79,7 @@ int delta_check(const sdm_delta_shape *s, DeltaDims &d, bool back) {
         if (d.qs[i] < 0 || d.ks[i] < 0 || d.vs[i] < 0 || d.gs[i] < 0 || d.bs[i] < 0 || d.os[i] < 0)
             return set_error(SDM_ERR_INVALID, "gated delta: negative stride");
     }
-    // bfloat16 inputs run on tcgen05, with narrow states too: 4096 tokens, 32 heads of 128 x 64 or 128 x 16 take 189
+    // bfloat16 inputs run on tcgen05, with narrow states too: 4096 tokens, 32 heads of 128 x 64 or 128 x 16 take 206
     // us, as three-plane products in registers they took 315 and 313
     d.tc = s->dtype == SDM_BF16;
     if (d.tc && !(tc_tensor_fits(d.qs, d.B, d.T, d.Hk) && tc_tensor_fits(d.ks, d.B, d.T, d.Hk) &&

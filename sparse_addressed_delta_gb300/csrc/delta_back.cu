@@ -3,7 +3,7 @@
 //   du = P^T dO + (e^{L_C - L} K) D1;   dw = X^T du;   dv = beta dw
 //   D0 = G_C D1 + (scale G Q)^T dO - K^T (beta G dw)
 // is a recurrence over the chunks from the last to the first (k_delta_back_scan; 32 chunks of 8 float32 heads
-// of 64 x 64 in segments 42 us and the join 14, in one run 95), the forward scan's
+// of 64 x 64 in segments 44 us and the join 16, in one run 95), the forward scan's
 // mirror image: a warp owns 16 columns, and accumulators pass from product to product as A operands.
 // (X = (I + diag(beta) A)^-1 here.) Everything else needs only a chunk's own S0 and r (saved by the forward), D1 and dw (left by the scan), and runs for all chunks at once (k_delta_back_local):
 //   a[t,s] = -beta_t beta_s <dw_t, r_s> e^{L_t - L_s}  (s < t)
@@ -304,8 +304,9 @@ struct BackLocalSmem {
 // One block per chunk and head. For the products with the states a warp owns 16 of the Dk columns and a
 // part of the tokens, and reads its rows of S0 and D1 straight into fragments, one step ahead; the C x C
 // products are split into 16 x 16 blocks, a warp each.
-// What bounds it: the m16n8k16 products, about 7600 a chunk and head at Dk = Dv = 128 (8 cycles each on
-// one of four tensor cores); 8 float32 heads of 64 x 64 x 32 chunks take 21 us.
+// What bounds it: the m16n8k16 products, about 11400 a chunk of 64 and head at Dk = Dv = 128 (8 cycles each on
+// one of four tensor cores), and its phases in turn with one block an SM (tensor pipe 30 %); 8 float32 heads of 64 x
+// 64 x 32 chunks take 25 us, 64 bfloat16 heads of 128 x 192 x 64 chunks 1340.
 template <typename T, int DKP>
 __global__ void __launch_bounds__(BackLocalSmem<T, DKP>::WARPS * 32, 1)
     k_delta_back_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal lw, DeltaBack o) {

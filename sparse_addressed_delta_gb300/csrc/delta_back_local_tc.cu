@@ -14,9 +14,10 @@
 // products, warp 17 loads: K and Q of a chunk, dO of a head, and in boxes of 32 columns (four slots, in
 // turn) dw and r, D1, S0 for <S0, D1>, and S0 again for its planes, whose place the first products have until
 // then; always as far ahead as their places are free.
-// What bounds it: a head's chunk reads 240 KB and writes its gradients (10000 cycles at the card's copy
+// What bounds it: a head's chunk reads 230 KB and writes its gradients (10000 cycles at the card's copy
 // rate); its phases (planes, p and a, states, results) follow one another with one block an SM. Measured at
-// 128 x 128, 32 heads by twos x 2 x 64 chunks: 385 us (2.7 TB/s); by m16n8k16 products (delta_back.cu) 640.
+// 128 x 128, 32 heads by twos x 2 x 64 chunks: 460 us (2.2 TB/s), the whole backward 855; by m16n8k16 products
+// (delta_back.cu) 1408. At 64 x 128 763 and 941.
 //
 // Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block; the computing warps
 // then run through without waiting (they meet at barriers), the others stop and wait for what they have

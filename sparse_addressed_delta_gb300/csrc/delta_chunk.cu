@@ -6,15 +6,15 @@
 // X, P diag(beta) and the gates need no state: k_delta_local computes them for all chunks at once. k_delta_scan
 // then walks over each head's chunks.
 //
-// The scan (32 chunks of 8 float32 heads of 64 x 64 in segments: 35 us and the join 14, in one run 92) keeps
+// The scan (32 chunks of 8 float32 heads of 64 x 64 in segments: 40 us and the join 16, in one run 92) keeps
 // everything transposed, [Dv] x [tokens or Dk]: a warp owns 16 of the state's columns
 // as the accumulators of m16n8k16 products, and the accumulators of one product are, in place, the A
 // operand of the next (S^T -> (K S)^T -> u^T -> S^T). Columns never mix, so warps share only the
 // loads of K, Q, X and P, and no value crosses a warp in the whole recurrence.
 //
 // Accuracy: K and Q are bfloat16, for the scan here three bfloat16 planes of a float32 input (bfloat16 inputs
-// take the tcgen05 scan, delta_scan_tc.cu); S, the corrections w and u, and X are float32 and enter products as three bfloat16 terms, the products of terms below
-// 2^-24 of the result left out. The chunk's update of the state is summed by itself and added to the
+// take the tcgen05 scan, delta_scan_tc.cu); S, the corrections w and u, X and P are float32 and enter products as
+// three bfloat16 terms, the products of terms below 2^-24 of the result left out. The chunk's update of the state is summed by itself and added to the
 // decayed state in float32, outside the tensor cores' accumulation.
 #include "delta_internal.cuh"
 
@@ -77,11 +77,12 @@ __device__ __forceinline__ void merge_columns(const float *N, float *X, int c0, 
 // diag(beta) A): 16 x 16 diagonal blocks by substitution, a warp each, a lane a column, then merged
 // in pairs, -X_2 N X_1, with the columns spread over the warps.
 // TC: for the tcgen05 scans, Z = P X in the place of P.
-// What bounds it: the latency of its steps, each behind a barrier, at 14 warps an SM (128 registers, 57 KB a
-// block): issue 45 %, shared memory 60 %. At C = 64 the merges are about 40 % of its instructions, the planes
-// 25 %. Measured at Dk = 128 with two value heads a key head: 12300 chunks of heads 242 us, 8192 168 us. (The
-// merges' operands fetched a step ahead: 252; decays as products of factors by blocks of 16 and running sums as
-// pairs of floats, for fewer exponentials and no doubles: 239, within what two runs differ.)
+// What bounds it: the latency of its steps, each behind a barrier, at 15 warps an SM (128 registers, 48 KB a
+// block): issue 47 %. At C = 64 the merges are about 40 % of its instructions, the planes a quarter. Measured at Dk =
+// 128 with two value heads a key head: 12300 chunks of heads 268 us, 8192 187 us. (Three blocks an SM, without the 64
+// bytes spilled: 16384 tokens 643 us a call, 632 with four. With Z from two terms, 242 us then: the merges' operands
+// fetched a step ahead 252; decays as products of factors by blocks of 16 and running sums as pairs of floats, for
+// fewer exponentials and no doubles, 239, within what two runs differ.)
 template <int KP, int DKP, int C, bool TC, bool BACK>
 __global__ void __launch_bounds__(2 * C, C != 64 ? 1 : 4)
     k_delta_local(DeltaDims d, DeltaIn in, DeltaPlanes q, DeltaPlanes k, DeltaLocal w, int heads) {
@@ -744,7 +745,7 @@ cudaError_t local_one(const DeltaDims &d, const DeltaIn &in, const DeltaPlanes &
     constexpr int bytes = LocalSmem<KP, DKP, C, TC>::BYTES;
     set_kernel_smem(kern, bytes);
     // as many heads of a key head to a block as still leave four blocks for every SM (8 x 4096 tokens, 32 heads by
-    // fours: whole call 743 us with one head a block, 690 with two, 664 with four)
+    // fours: whole call 639 us with one head a block, 594 with two, 571 with four)
     const int group = d.H / d.Hk;
     int heads = kLocalHeads;
     while (heads > 1 && (group % heads || delta_chunks(d) / heads < 4 * kRefSms)) --heads;
@@ -784,7 +785,8 @@ cudaError_t launch_delta_scan(const DeltaDims &d, const DeltaIn &in, const Delta
                               const DeltaLocal &w, float *state, void *o, float *snap, float *r, cudaStream_t st) {
     auto out = static_cast<float *>(o);
     // eight warps (two an SM sub-core) share a chunk's loads once there is a block for every SM (float32, 8 x 1000
-    // tokens of 32 heads of 128 x 128: 696 us, 842 with four); with fewer heads four, so that every warp has a
+    // tokens of 32 heads of 128 x 128: 688 us, 832 with four; of 128 x 256 1219 and 1358; 4 x 1000 of 64 heads of 64 x
+    // 128 422 and 449); with fewer heads four, so that every warp has a
     // tensor core of its own
     const bool wide = d.Dv > 64 && (long long)d.B * d.H * ((d.Dv + 127) / 128) >= kRefSms;
     auto go = [&](auto dkp, auto nw, auto save, int mode) {

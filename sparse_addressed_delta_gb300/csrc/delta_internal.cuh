@@ -9,8 +9,9 @@ namespace sdm {
 constexpr int kDeltaMaxDk = 128, kDeltaMaxDv = 512;
 constexpr int kDeltaAux = 5;
 // Up to this many tokens take the token-by-token kernel. Token by token and in a chunk, us: 16 heads x 8 tokens
-// 16 and 25, x 16 25 and 25; 64 sequences of 32 heads x 8 133 and 166, x 12 180 and 166, x 16 225 and 168 (bfloat16,
-// 128 x 128); float32, 8 of 6 heads of 64 x 96 x 8 16 and 23, x 16 27 and 23.
+// 16 and 27, x 12 21 and 27, x 16 25 and 27; 64 sequences of 32 heads x 8 125 and 182, x 12 168 and 182, x 16 211 and
+// 184 (bfloat16, 128 x 128); 16 heads of 64 x 64 x 8 55 and 80, x 12 78 and 80; float32, 8 of 6 heads of 64 x 96 x 8
+// 16 and 25, x 16 27 and 25. The two cross between 12 and 14 tokens; callers without a workspace have the promise of 8.
 constexpr int kDeltaStepTokens = 8;
 // A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten
 // whole, and -inf (a hard reset) stays out of the running sums' differences.
@@ -86,7 +87,8 @@ struct DeltaBlock {
     long long bh;
 };
 // The scans' blocks take the sequences from the longest down, so that the last ones to start are short
-// (8 sequences of up to 4096 tokens, 32 heads on 152 SMs: 326 -> 293 us). More than 32 sequences stay in their
+// (8 sequences of 2048 to 4096 tokens, 32 heads, whole call by five draws of lengths: 600 to 660 us, in their order
+// 623 to 682). More than 32 sequences stay in their
 // order: their many blocks level out by themselves.
 __device__ __forceinline__ long long delta_longest_first(const DeltaDims &d, const int32_t *valid, long long bh) {
     if (!valid || d.B > 32) return bh;

@@ -15,8 +15,8 @@
 // tokens and the first half of Dk, the others the rest. The triangular products let the first tokens'
 // U finish before the second tokens' w is there, the update's products start with the first tokens,
 // and the first half of the new S enters the next chunk's R while the second is being made. The values'
-// products and the readings run in the gaps. Measured at 128 x 128: 64 heads x 64 chunks, saving, 236 us (3.7 a
-// chunk; 2.6 to 3 without saving); 256 ragged heads x up to 64 chunks, 293 us. In registers (as delta_chunk.cu's
+// products and the readings run in the gaps. Measured at 128 x 128: 64 heads x 64 chunks, saving, 253 us (4.0 a
+// chunk; 3 to 3.4 without saving); 256 ragged heads x up to 64 chunks, 335 us. In registers (as delta_chunk.cu's
 // for float32) the first took 425: an m16n8k16 product is 8 cycles on one of four tensor cores.
 //
 // Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the tokens and of Dk), warp 16 issues
@@ -58,7 +58,7 @@ enum { SCAN_READ, SCAN_SAVE, SCAN_CARRY };
 
 // SCAN_SAVE: also what a backward needs. SCAN_CARRY: the segments' end states only (DeltaBlock). SEG: the
 // sequences are in segments; a form of its own, for its registers (one form for both spilled: a call with 8
-// sequences of up to 4096 tokens, 32 heads, took 600 us where it takes 575).
+// sequences of up to 4096 tokens, 32 heads, took 4 % longer).
 template <int DKP, int MODE, bool SEG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_delta_scan_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,

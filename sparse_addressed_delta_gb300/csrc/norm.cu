@@ -7,7 +7,7 @@
 // the mean, from the row kept in registers: no cancellation, and x is read once.
 //
 // Bound by memory: a row is read once, held in registers and written once (bfloat16, 1048576 x 128: 92 us,
-// 87 % of the copy rate; 32768 x 4096 105 us and its backward 141 us; 262144 x 128 forward and backward 71 us,
+// 87 % of the copy rate; 32768 x 4096 107 us and its backward 144 us; 262144 x 128 forward and backward 70 us,
 // the second behind the first's warm cache). A row belongs to TPR
 // threads (a part of a warp up to 32, else the whole block), each with E elements as whole vectors
 // (16 bytes when the row length, its stride and the pointers allow it, else 4 or one element).
@@ -25,13 +25,15 @@ namespace {
 constexpr int kNormBlock = 128;        // threads of a block whose rows belong to parts of warps
 constexpr int kNormMaxCols = 16384;
 constexpr int kNormRegCols = 8192;     // backward: column sums in registers up to this width
-// columns and runs of partials of a block that adds them (262144 x 128, whole training call: 69.5 us, 71.4 with
-// 32 x 32)
+// columns and runs of partials of a block that adds them, 32 lanes of which take two runs each. Whole training call,
+// us, with 16 x 64 and (runs in shared memory throughout) 32 x 32: 5003 x 1007 float32 41, 42; 20000 x 1007 94, 96;
+// 262144 x 128 bfloat16 68, 68; 2000 x 4096 49, 46; 32768 x 4096 259, 257
 constexpr int kNormColThreads = 16, kNormColSlices = 64;
 template <typename T>
 constexpr int kNormStages = sizeof(T) == 2 ? 4 : 3;   // rows in the ring, the one in use among them
-// backward: at least this many rows a block, for fewer partials (5003 x 1007 float32, whole training call: 39.0 us;
-// 42.9 with 8, 46.2 with 12, 38.9 with 4)
+// backward: at least this many rows a block, for fewer partials. Whole training call, us, with 4, 6, 8 and 12: 5003 x
+// 1007 float32 39, 41, 45, 49; 2000 x 4096 bfloat16 49, 49, 48, 54; the same with each: 500 x 2048, 32768 x 4096,
+// 262144 x 128, 20000 x 1007 and 3000 x 8192 (a block has more rows, or there are too few for it)
 constexpr int kNormRowsBlock = 6;
 
 template <int BYTES> struct VecOf;
