@@ -117,7 +117,7 @@ bool delta_flat(const DeltaDims &d, int i) {
 struct DeltaLayout {
     size_t q, k, x, p, aux;              // q, k: the planes of float32 inputs
     size_t flat[4];                      // bfloat16 q, k, v and gradient that are broadcast along the tokens
-    size_t starts, units;                // the segments' (units: of a forward that saves nothing)
+    size_t starts, units;                // the segments' (units: of a forward that saves nothing); a forward's own
     size_t ends, w, dq, dk;              // the backward's
     size_t bytes;
 };
@@ -136,7 +136,8 @@ DeltaLayout delta_layout(const DeltaDims &d, bool backward) {
     l.x = take(delta_chunks(d) * 3 * delta_plane_bytes(d));
     l.p = take(delta_chunks(d) * 3 * delta_plane_bytes(d));
     l.aux = take(delta_chunks(d) * kDeltaAux * d.C * 4);
-    l.starts = take(d.segs > 1 ? d.segs * (size_t)delta_states(d) * 4 : 0);
+    // (a forward of one segment: where a column's state goes that delta_column takes again)
+    l.starts = take(d.segs > 1 || !backward ? d.segs * (size_t)delta_states(d) * 4 : 0);
     if (!backward) l.units = take(delta_unit_bytes(d));
     if (backward) {
         l.ends = take(delta_chunks(d) * d.Dk * d.Dv * 4);

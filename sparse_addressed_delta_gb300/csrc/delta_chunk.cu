@@ -564,14 +564,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
                                 for (int m = 0; m < 4; ++m)
                                     mma_bf16(acc[m], ua[ks][x], bb[p][m >> 1][2 * (m & 1)], bb[p][m >> 1][2 * (m & 1) + 1]);
                 }
-                // a column's first update that is not finite (then no row of it is): its state before goes back to
-                // where it came from, for delta_column
+                // a column's first update that is finite in no row (as a NaN or infinity of a token leaves it): its
+                // state before goes back to where it came from, for delta_column
                 if (nn == 0 && !carry) {
-                    const bool off[2] = {!delta_finite(acc[0][0]), !delta_finite(acc[0][2])};
-                    if (__any_sync(~0u, off[0] || off[1])) {
+                    const unsigned off[2] = {__ballot_sync(~0u, !delta_finite(acc[0][0])), __ballot_sync(~0u, !delta_finite(acc[0][2]))};
+                    if (off[0] | off[1]) {
 #pragma unroll
                         for (int f = 0; f < 2; ++f) {
-                            const bool now = off[f] && bad[g4 + 8 * f] < 0;
+                            const bool now = (off[f] >> (4 * g4) & 15) == 15 && bad[g4 + 8 * f] < 0;
                             __syncwarp();
                             if (now && i4 == 0) bad[g4 + 8 * f] = n;
                             if (now)

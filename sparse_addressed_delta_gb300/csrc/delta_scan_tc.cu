@@ -218,10 +218,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
                 tc_load16(at + (half == 0 || DKP == 64 ? UPD + dk0 : UPD1 + dk0 - 64) + c, x);
-                // no row of such an update is finite; the column's state before goes back to where it came from
+                // a NaN or infinity of a token leaves no row of the update finite; the column's state before is kept
                 if (!CARRY && c == 0 && mine && !delta_finite(x[0]) && first < 0) {
                     first = n;
-                    keep_state((SEG ? w.starts + seg * delta_states(d) : state) + bh * d.Dk * (long long)d.Dv, 0, HD);
+                    keep_state(w.starts + seg * delta_states(d) + bh * d.Dk * (long long)d.Dv, 0, HD);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[c + i] = fmaf(whole, S[c + i], x[i]);
@@ -233,10 +233,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (CARRY)
             keep_state(blk.unit ? w.units + ((seg - 1) * (long long)d.B * d.H + bh) * d.Dk * d.Dk
                                 : w.starts + (seg + 1) * delta_states(d) + bh * d.Dk * (long long)d.Dv, 0, HD);
-        else if (last && nch > 0 && !*dead && (SEG || first < 0))
+        else if (last && nch > 0 && !*dead)
             keep_state(state + bh * d.Dk * (long long)d.Dv, 0, HD);
         if (SAVE && last) keep_state(snap + ((bh * (d.Nt + 1) + chunks) * (long long)d.Dk) * d.Dv, 0, HD);
-        if (part == 0) reinterpret_cast<int *>(smem + L::BAD)[lane0 + lane] = first;
+        if (part == 0) reinterpret_cast<int *>(smem + L::BAD)[lane0 + lane] = first;   // if the other parts agree
     } else if (warp == kTcWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
@@ -434,15 +434,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const bool bad = __syncthreads_or(first >= 0);
     if (warp == kTcWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
     if (CARRY || !bad || *dead) return;
+    if (warp >= 4 && warp < kTcWarps) {
+        int *own = reinterpret_cast<int *>(smem + L::BAD) + 32 * (warp & 3) + lane;
+        if (first != *own) *own = -1;
+    }
+    __syncthreads();
     for (int c = warp; c < 128; c += kTcThreads / 32) {
         const int n = reinterpret_cast<int *>(smem + L::BAD)[c], t0 = n * C, dv = dv_blk + c;
         if (n < 0) continue;
-        float *S = (SEG ? w.starts + seg * delta_states(d) : state) + bh * d.Dk * (long long)d.Dv + dv;
-        delta_column(d, in, b, h, dv, t0, ntok - t0 < C ? ntok - t0 : C, S, o + (((long long)b * d.T + t0) * d.H + h) * d.Dv + dv,
+        delta_column(d, in, b, h, dv, t0, ntok - t0 < C ? ntok - t0 : C, w.starts + seg * delta_states(d) + bh * d.Dk * (long long)d.Dv + dv, o + (((long long)b * d.T + t0) * d.H + h) * d.Dv + dv,
                      SAVE ? rsave + (bh * d.Nt + n) * (long long)C * d.Dv + dv : nullptr);
-        __syncwarp();
-        if (!SEG)                                                  // the last state is no more finite than this chunk's
-            for (int i = lane; i < d.Dk; i += 32) S[(size_t)i * d.Dv] = __int_as_float(0x7fc00000);
     }
 }
 

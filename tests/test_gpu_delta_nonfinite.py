@@ -97,3 +97,16 @@ def test_a_decay_too_large_for_float32(dtype):
     assert np.abs(host(o)[0, :, 0] - ro[0, :, 0]).max() <= TOL[dtype] * np.abs(ro[0, :, 0]).max()
     assert np.abs(host(o)[0, :41] - ro[0, :41]).max() <= TOL[dtype] * np.abs(ro[0, :41]).max()
     assert not torch.isfinite(o[0, 41:, 1]).any() and not torch.isfinite(state[0, 1]).any() and torch.isfinite(state[0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [20, 99])
+def test_large_values_are_finite(dtype, t):
+    """Near the largest float, and no infinity: every column as the definition has it."""
+    x = draw(1, 100, 1, 2, 48, 64, dtype, seed=64)
+    x["v"][0, t, 0, 3] = 2e38
+    o, state = call(x)
+    ro, rs = ref(x)
+    for a, want, tol in ((host(o), ro, TOL[dtype]), (host(state), rs, F32_TOL), (host(o)[:, :t], ro[:, :t], TOL[dtype])):
+        for part in (np.s_[..., 3], np.s_[..., 4:]):
+            assert np.abs(a[part] - want[part]).max() <= tol * np.abs(want[part]).max()
