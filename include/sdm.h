@@ -477,6 +477,71 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
                              size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the recurrence without the delta. A head's Dk x Dv state
+ * decays by the head's own factor at every token, the key writes its value, the query reads:
+ *     S = exp(g) S + k v^T;  o = scale S^T q
+ *   B  sequences, T  tokens (both may be 0), H  value heads, Hk  key heads (H a multiple of Hk: value head h
+ *   reads key head h / (H / Hk)), B H at most 65535; Dk, Dv  head widths, multiples of 16, Dk up to 128 and Dv
+ *   up to 512; dtype SDM_F32 or SDM_BF16 of q, k, v, the readings and their gradients; the state and the decays
+ *   are float32. Strides are in elements, for (sequence, token, head); the last dimension is contiguous.
+ *   Strides must be multiples of 16 bytes, addresses 16-byte aligned; a stride of 0 (a broadcast input) is fine.
+ *
+ *   state        [B, H, Dk, Dv] float32, advanced in place
+ *   q, k         [B, T, Hk, Dk]
+ *   v            [B, T, H, Dv]
+ *   log_decay    [H] float32, 0 or below; below -110 (and -inf) the state is forgotten whole at every token
+ *   valid_tokens [B] int32, or NULL: all T. Tokens past it change nothing and none of their inputs
+ *                is used; their readings (and gradients) are 0. Clamped to [0, T].
+ *   readings     [B, T, H, Dv] contiguous, written whole
+ *   workspace    sdm_linear_attention_workspace_bytes(shape) bytes, 256-byte aligned; it begins with a status
+ *                block, as the gated delta rule's does
+ * Deterministic. bfloat16 readings and gradients are float32 results, rounded once.
+ * A NaN or infinity of an input reaches the readings and states that the recurrence carries it to, and no others.
+ * The gradients of a sequence and key head that has one are undefined.
+ * Each call returns SDM_OK once queued on stream, or a negative sdm_status (nothing queued).
+ * --------------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t B, T, H, Hk, Dk, Dv;
+    int32_t dtype;
+    float scale;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    int64_t grad_stride[3];   /* of grad_readings; the forward ignores it */
+} sdm_linear_shape;
+
+/* Workspace of sdm_linear_attention and sdm_linear_attention_save; 0 for a refused shape. */
+size_t sdm_linear_attention_workspace_bytes(const sdm_linear_shape *shape);
+
+int sdm_linear_attention(const sdm_linear_shape *shape, float *state, const void *q, const void *k,
+                         const void *v, const float *log_decay, const int32_t *valid_tokens,
+                         void *readings, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The saving forward: sdm_linear_attention, and what the backward needs in saved:
+ * sdm_linear_attention_saved_bytes(shape) bytes, 256-byte aligned. */
+size_t sdm_linear_attention_saved_bytes(const sdm_linear_shape *shape);
+int sdm_linear_attention_save(const sdm_linear_shape *shape, float *state, const void *q, const void *k,
+                              const void *v, const float *log_decay, const int32_t *valid_tokens,
+                              void *readings, void *saved, size_t saved_bytes, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* The backward after sdm_linear_attention_save with the same shape and inputs (grad_stride now given).
+ *   grad_readings     [B, T, H, Dv] dtype, strided
+ *   grad_final_state  [B, H, Dk, Dv] float32, the gradient of the final state, or NULL (zeros)
+ *   grad_state        [B, H, Dk, Dv] float32, the gradient of the initial state (may be
+ *                     grad_final_state itself)
+ *   grad_q, grad_k    [B, T, Hk, Dk] dtype, heads that share a key head added in float32 in head order
+ *   grad_v            [B, T, H, Dv] dtype
+ *   grad_log_decay    [H] float32, summed over the sequences in order; NULL where the decays are fixed
+ * all contiguous and written whole. workspace: sdm_linear_attention_backward_workspace_bytes(shape) bytes,
+ * 256-byte aligned. */
+size_t sdm_linear_attention_backward_workspace_bytes(const sdm_linear_shape *shape);
+int sdm_linear_attention_backward(const sdm_linear_shape *shape, const void *q, const void *k, const void *v,
+                                  const float *log_decay, const int32_t *valid_tokens, const void *saved,
+                                  size_t saved_bytes, const void *grad_readings,
+                                  const float *grad_final_state, float *grad_state, void *grad_q,
+                                  void *grad_k, void *grad_v, float *grad_log_decay, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------
  * Layer norm over rows of n columns (1..16384), float32 arithmetic, y rounded once:
  *     y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
  *   x       device rows of n contiguous elements, x_stride >= 0 elements apart; dtype SDM_F32 or

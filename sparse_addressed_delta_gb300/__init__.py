@@ -28,7 +28,8 @@ __all__ = ["FLAG_SNAPSHOT_BF16", "FLAG_SNAPSHOT_FP8", "FLAG_TOKEN_GATE", "FLAG_S
            "backward_workspace_bytes", "launch_count",
            "phase1_debug", "KERNEL_KINDS", "set_wait_limit", "product_key_topk",
            "product_key_topk_backward", "gated_delta", "gated_delta_save",
-           "gated_delta_backward", "layer_norm", "layer_norm_save",
+           "gated_delta_backward", "linear_attention", "linear_attention_save",
+           "linear_attention_backward", "layer_norm", "layer_norm_save",
            "layer_norm_backward",
            "device_status", "SdmError", "Shape", "library", "library_path", "version"]
 
@@ -149,6 +150,14 @@ def library() -> ctypes.CDLL:
             lib.sdm_layer_norm_backward.argtypes = [vp, ll, vp, ll, ll, i32, vp, i32, vp, i32, vp,
                                                     vp, vp, vp, sz, vp]
             lib.sdm_layer_norm_backward.restype = i32
+            lib.sdm_linear_attention.argtypes = [vp] + [vp] * 7 + [vp, sz, vp]
+            lib.sdm_linear_attention_save.argtypes = [vp] + [vp] * 7 + [vp, sz, vp, sz, vp]
+            lib.sdm_linear_attention_backward.argtypes = [vp] + [vp] * 5 + [vp, sz] + [vp] * 7 + [vp, sz, vp]
+            for name in ("sdm_linear_attention", "sdm_linear_attention_save", "sdm_linear_attention_backward"):
+                getattr(lib, name).restype = i32
+            for name in ("workspace", "saved", "backward_workspace"):
+                getattr(lib, f"sdm_linear_attention_{name}_bytes").argtypes = [vp]
+                getattr(lib, f"sdm_linear_attention_{name}_bytes").restype = sz
             lib.sdm_set_wait_limit.argtypes = [ctypes.c_longlong]
             lib.sdm_set_wait_limit.restype = ctypes.c_longlong
             lib.sdm_last_error.argtypes = []
@@ -909,6 +918,121 @@ def gated_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
           _at(valid_tokens), _at(saved), m, _at(grad_readings), _at(grad_state), _at(out["grad_state"]),
           _at(out["grad_q"]), _at(out["grad_k"]), _at(out["grad_v"]), _at(out["grad_log_decay"]),
           _at(out["grad_beta"]), _at(ws), n)
+    return out
+
+
+# ------------------------------------------------------------------------------------------
+# linear attention with a decay for each head: the recurrence without the delta
+# ------------------------------------------------------------------------------------------
+
+_LINEAR_SHAPE = struct.Struct("=7if12q")
+
+
+def _linear_shape(q, k, v, log_decay, valid_tokens, scale, grad=None):
+    """Checks the inputs against each other; (packed shape, (B, T, H, Hk, Dk, Dv), device, dtype)."""
+    for t, name in ((q, "q"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [B, T, heads, width]")
+    dev, dt = v.device, v.dtype
+    if dev.type != "cuda":
+        raise ValueError("q, k and v must be CUDA tensors")
+    code = _dtype_code(dt)
+    es = 2 if code == SDM_BF16 else 4
+    kshape, vshape = q.shape, v.shape
+    B, T, Hk, Dk = kshape
+    H, Dv = vshape[2], vshape[3]
+    if vshape[0] != B or vshape[1] != T:
+        raise ValueError(f"v must be [{B}, {T}, heads, width], got {tuple(vshape)}")
+    strides = (_rows(q, "q", kshape, dt, dev, es) + _rows(k, "k", kshape, dt, dev, es) + _rows(v, "v", vshape, dt, dev, es)
+               + ((0, 0, 0) if grad is None else _rows(grad, "grad_readings", vshape, dt, dev, es)))
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    if valid_tokens is not None:
+        _need(valid_tokens, "valid_tokens", (B,), torch.int32, dev)
+    if scale is None:
+        scale = Dk ** -0.5 if Dk else 1.0
+    return (_LINEAR_SHAPE.pack(B, T, H, Hk, Dk, Dv, code, scale, *strides), (B, T, H, Hk, Dk, Dv), dev, dt)
+
+
+def linear_attention(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: torch.Tensor, valid_tokens: Optional[torch.Tensor] = None, *,
+                     scale: Optional[float] = None, readings: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Linear attention with a decay for each head over B sequences; returns readings [B, T, H, Dv] and
+    advances ``state`` ([B, H, Dk, Dv] float32, contiguous) in place. Per token and head:
+    S = exp(g) S + k v^T; o = scale S^T q.
+
+    q, k [B, T, Hk, Dk] and v [B, T, H, Dv], float32 or bfloat16, any strides that are multiples of
+    16 bytes; H a multiple of Hk (value head h uses key head h // (H // Hk)); Dk (up to 128) and Dv
+    (up to 512) multiples of 16. log_decay [H] float32, 0 or below. valid_tokens [B] int32 (None:
+    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step. What is allocated
+    here belongs to ``stream`` (None: the current one). A wait that gives up is reported as
+    gated_delta's: in a ``workspace`` of the caller's."""
+    if stream is not None:
+        return _on(stream, linear_attention, state, q, k, v, log_decay, valid_tokens, scale=scale,
+                   readings=readings, workspace=workspace)
+    lib = library()
+    shape, (B, T, H, Hk, Dk, Dv), dev, dt = _linear_shape(q, k, v, log_decay, valid_tokens, scale)
+    _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
+    readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
+    ws, n = _scratch(workspace, lib.sdm_linear_attention_workspace_bytes, dev, shape)
+    _call(lib.sdm_linear_attention, dev, shape, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), _at(valid_tokens), readings.data_ptr(), _at(ws), n)
+    return readings
+
+
+def linear_attention_save(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                          log_decay: torch.Tensor, valid_tokens: Optional[torch.Tensor] = None, *,
+                          scale: Optional[float] = None, readings=None, saved=None, workspace=None,
+                          stream=None):
+    """linear_attention that also keeps what its backward needs: (readings, saved), with ``state``
+    advanced in place. ``saved`` (uint8) holds the initial state and, for long sequences of few heads,
+    the states their segments begin with."""
+    if stream is not None:
+        return _on(stream, linear_attention_save, state, q, k, v, log_decay, valid_tokens, scale=scale,
+                   readings=readings, saved=saved, workspace=workspace)
+    shape, (B, T, H, Hk, Dk, Dv), dev, dt = _linear_shape(q, k, v, log_decay, valid_tokens, scale)
+    _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
+    readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
+    lib = library()
+    ws, n = _scratch(workspace, lib.sdm_linear_attention_workspace_bytes, dev, shape)
+    saved, m = _scratch(saved, lib.sdm_linear_attention_saved_bytes, dev, shape)
+    _call(lib.sdm_linear_attention_save, dev, shape, _at(state), _at(q), _at(k), _at(v), _at(log_decay),
+          _at(valid_tokens), _at(readings), _at(saved), m, _at(ws), n)
+    return readings, saved
+
+
+def linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                              valid_tokens: Optional[torch.Tensor], saved: torch.Tensor,
+                              grad_readings: torch.Tensor, *, grad_state: Optional[torch.Tensor] = None,
+                              scale: Optional[float] = None, decay: bool = True, workspace=None,
+                              stream=None) -> Dict[str, torch.Tensor]:
+    """The backward after linear_attention_save (same inputs and scale): a dict of grad_q, grad_k, grad_v
+    (the inputs' dtype; heads that share a key head are summed), grad_state (float32; of the initial
+    state) and, unless ``decay`` is false (fixed decays), grad_log_decay ([H] float32, summed over the
+    sequences). ``grad_state`` [B, H, Dk, Dv] float32: the gradient of the final state (None: zero); it
+    is not changed."""
+    if stream is not None:
+        return _on(stream, linear_attention_backward, q, k, v, log_decay, valid_tokens, saved, grad_readings,
+                   grad_state=grad_state, scale=scale, decay=decay, workspace=workspace)
+    shape, (B, T, H, Hk, Dk, Dv), dev, dt = _linear_shape(q, k, v, log_decay, valid_tokens, scale, grad_readings)
+    if grad_state is not None:
+        _need(grad_state, "grad_state", (B, H, Dk, Dv), torch.float32, dev)
+    if saved is None:
+        raise TypeError("saved must be a tensor")
+    saved, m = _scratch(saved, None, dev)
+    lib = library()
+    ws, n = _scratch(workspace, lib.sdm_linear_attention_backward_workspace_bytes, dev, shape)
+    out = {"grad_q": torch.empty((B, T, Hk, Dk), dtype=dt, device=dev),
+           "grad_k": torch.empty((B, T, Hk, Dk), dtype=dt, device=dev),
+           "grad_v": torch.empty((B, T, H, Dv), dtype=dt, device=dev),
+           "grad_state": torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)}
+    if decay:
+        out["grad_log_decay"] = torch.empty(H, dtype=torch.float32, device=dev)
+    _call(lib.sdm_linear_attention_backward, dev, shape, _at(q), _at(k), _at(v), _at(log_decay), _at(valid_tokens),
+          _at(saved), m, _at(grad_readings), _at(grad_state), _at(out["grad_state"]), _at(out["grad_q"]),
+          _at(out["grad_k"]), _at(out["grad_v"]), _at(out.get("grad_log_decay")), _at(ws), n)
     return out
 
 

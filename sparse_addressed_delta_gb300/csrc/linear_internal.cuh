@@ -1,0 +1,72 @@
+// Shared by the linear attention's kernels (linear*.cu). A head's state decays by the head's own factor at
+// every token, is written and read:
+//   S = e^g S + k v^T;   o = scale S^T q
+// The backward's parts have the same form. With R the gradient of the state, run from the last token back,
+//   dq = scale S do                   is the forward's with (do, v, k) for (q, k, v) and S transposed,
+//   dk = R v,  dv = R^T k,  R += scale q do^T;  dk, dv are read, then R = e^g R
+// are its mirror image with (v, do, q) and (k, q, do), so one kernel makes them all: a pass.
+#pragma once
+
+#include "sdm_internal.cuh"
+
+namespace sdm {
+
+constexpr int kLinearMaxDk = 128, kLinearMaxDv = 512;
+// A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten whole, and
+// -inf (a hard reset at every token) has no 0 x inf among its powers.
+constexpr double kLinearMinDecay = -110.0;
+
+struct LinearDims {
+    int B, T, H, Hk, Dk, Dv, dtype;
+    int C, Nt;                           // chunk length, chunks a sequence
+    int segs;                            // segments a sequence is cut into, run at once
+    float scale;
+    long long spin;                      // polls before a kernel's wait gives up (sdm_set_wait_limit)
+    long long qs[3], ks[3], vs[3], os[3];   // element strides of (b, t, h); os: of the readings' gradient
+};
+
+// a tensor [B, T, heads, width] whose head h / share belongs to head h of a pass
+struct LinearOperand {
+    const void *p;
+    long long s[3];
+    int share;
+};
+
+struct LinearPass {
+    LinearOperand q, k, v;
+    int K, V;                            // widths of q and k, and of v and the result
+    int blocks;                          // of K: each 128 columns, a result of its own
+    bool reverse;
+    float pair, from, to;                // scales: of q k, of what is read, of what is written
+    const float *first;                  // state to begin with, null: 0
+    float *last;                         // state to end with, or null
+    long long sk, sv;                    // strides of a head's [Dk, Dv] state along K and V
+    void *out;                           // [blocks][B, T, H, V] contiguous
+    bool out_f32;                        // else of the inputs' type
+};
+
+struct LinearIn {
+    const float *g;                      // [H]
+    const int32_t *valid;                // may be null
+};
+
+__device__ __forceinline__ int linear_valid(const int32_t *valid, int b, int T) {
+    const int v = valid ? valid[b] : T;
+    return v < 0 ? 0 : (v > T ? T : v);
+}
+// e^(g n) for whole n >= 0, from 64 bits: the exponent's own rounding would grow with n
+__device__ __forceinline__ double linear_power(double g, double n) { return n == 0.0 ? 1.0 : exp((g < kLinearMinDecay ? kLinearMinDecay : g) * n); }
+
+inline int linear_tiles(int columns) { return (columns + 127) / 128; }
+inline long long linear_states(const LinearDims &d) { return (long long)d.B * d.H * d.Dk * d.Dv; }
+
+cudaError_t launch_linear_tokens(const LinearDims &d, const LinearPass &p, const LinearIn &in, cudaStream_t st);
+// out [B, T, Hk, width] = the sum over a key head's heads, and over `blocks` parts, of part [blocks][B, T, H, width]
+cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, cudaStream_t st);
+// grad_decay [H] from q, k, v, the readings' gradient, the first state and the final state's gradient (may be
+// null); part: B H tiles(Dv) doubles
+cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearOperand &q, const LinearOperand &k, const LinearOperand &v,
+                                const LinearOperand &grad, const float *first, const float *final_grad, double *part, float *grad_decay,
+                                cudaStream_t st);
+
+}  // namespace sdm
