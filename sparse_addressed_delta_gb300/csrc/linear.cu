@@ -2,12 +2,23 @@
 // checks and the launch sequence. Everything is queued on the caller's stream; nothing is allocated and
 // nothing synchronizes.
 #include "linear_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace sdm {
 namespace {
 
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
+
+// How many segments a sequence is run in (launch_linear_scan): they pay where the heads alone leave SMs idle.
+void linear_segments(LinearDims &d) {
+    const long long blocks = (long long)d.B * d.H * linear_tiles(d.Dv);
+    d.segs = 1;
+    if (blocks * 2 <= kRefSms && d.Nt >= 8) {
+        const int most = (int)(kRefSms / (blocks ? blocks : 1)), by = d.Nt / 4;
+        d.segs = most < by ? most : by;
+    }
+}
 
 // Checks the shape; fills d. Returns SDM_OK or a refusal (message set). A forward does not look at grad_stride.
 int linear_check(const sdm_linear_shape *s, LinearDims &d, bool back) {
@@ -29,10 +40,10 @@ int linear_check(const sdm_linear_shape *s, LinearDims &d, bool back) {
     d.scale = s->scale;
     d.C = 64;
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
-    d.segs = 1;
     d.spin = wait_limit();
     if ((long long)s->B * s->H > 65535)
         return set_error(SDM_ERR_UNSUPPORTED, "linear attention: B H must be at most 65535");
+    linear_segments(d);
     const int es = s->dtype == SDM_BF16 ? 2 : 4;
     for (int i = 0; i < 3; ++i) {
         d.qs[i] = s->q_stride[i]; d.ks[i] = s->k_stride[i]; d.vs[i] = s->v_stride[i]; d.os[i] = back ? s->grad_stride[i] : 0;
@@ -42,6 +53,9 @@ int linear_check(const sdm_linear_shape *s, LinearDims &d, bool back) {
         if (d.qs[i] < 0 || d.ks[i] < 0 || d.vs[i] < 0 || d.os[i] < 0)
             return set_error(SDM_ERR_INVALID, "linear attention: negative stride");
     }
+    if (d.dtype == SDM_BF16 && !(tc_tensor_fits(d.qs, d.B, d.T, d.Hk) && tc_tensor_fits(d.ks, d.B, d.T, d.Hk) &&
+                                 tc_tensor_fits(d.vs, d.B, d.T, d.H) && tc_tensor_fits(d.os, d.B, d.T, d.H)))
+        return set_error(SDM_ERR_UNSUPPORTED, "linear attention: bfloat16 strides must be below 2^39 elements");
     return SDM_OK;
 }
 
@@ -72,8 +86,16 @@ cudaError_t linear_clear(void *ws, size_t have, cudaStream_t st) {
 // dq and dk are parts for each head and each 128 columns of Dv where there is more than one of them
 bool linear_parts(const LinearDims &d) { return d.H != d.Hk || d.Dv > 128; }
 
+// whether q, k, v or the gradient (i = 0 .. 3) has to be laid out for the tensor copies: float32, or bfloat16 and
+// broadcast along the tokens (they step along them)
+bool linear_lays(const LinearDims &d, int i) {
+    return d.dtype == SDM_F32 || (d.T > 1 && (i == 0 ? d.qs : i == 1 ? d.ks : i == 2 ? d.vs : d.os)[1] == 0);
+}
+
 // Where a call's buffers lie in its workspace; `bytes` is their end.
 struct LinearLayout {
+    size_t laid[4];                      // q, k, v and the gradient where linear_lays
+    size_t starts;                       // the segments' first states (a saving forward's are saved; a backward: of the gradient)
     size_t dq, dk, decay, bytes;
 };
 
@@ -85,6 +107,9 @@ LinearLayout linear_layout(const LinearDims &d, bool back) {
         at += up(bytes);
         return here;
     };
+    for (int i = 0; i < (back ? 4 : 3); ++i)
+        l.laid[i] = take(linear_lays(d, i) ? (size_t)d.B * d.T * (i < 2 ? (size_t)d.Hk * d.Dk : (size_t)d.H * d.Dv) * (d.dtype == SDM_F32 ? 6 : 2) : 0);
+    l.starts = take(d.segs > 1 ? d.segs * (size_t)linear_states(d) * 4 : 0);
     if (back) {
         const size_t part = linear_parts(d) ? (size_t)linear_tiles(d.Dv) * d.B * d.T * d.H * d.Dk * 4 : 0;
         l.dq = take(part);
@@ -95,7 +120,35 @@ LinearLayout linear_layout(const LinearDims &d, bool back) {
     return l;
 }
 
-size_t linear_saved(const LinearDims &d) { return up((size_t)linear_states(d) * 4); }
+// what the saving forward keeps: the states its segments begin with, the initial one first
+size_t linear_saved(const LinearDims &d) { return up(d.segs * (size_t)linear_states(d) * 4); }
+
+// q, k, v (and with grad the readings' gradient) as the tensor copies take them
+cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char *ws, const void *const (&src)[4], LinearLaid (&laid)[4],
+                       cudaStream_t st) {
+    LinearLay lay[4];
+    int n = 0;
+    for (int i = 0; i < 4 && src[i]; ++i) {
+        const long long *s = i == 0 ? d.qs : i == 1 ? d.ks : i == 2 ? d.vs : d.os;
+        const int heads = i < 2 ? d.Hk : d.H, width = i < 2 ? d.Dk : d.Dv;
+        laid[i] = LinearLaid{src[i], {s[0], s[1], s[2]}, heads, width};
+        if (!linear_lays(d, i)) continue;
+        lay[n++] = LinearLay{src[i], {s[0], s[1], s[2]}, heads, width, ws + l.laid[i]};
+        laid[i] = LinearLaid{ws + l.laid[i], {(long long)d.T * heads * width, (long long)heads * width, width}, heads, width};
+    }
+    return launch_linear_lay(d, lay, n, st);
+}
+
+// a pass's launches; starts: where its segments' first states are or, with `carry`, go
+cudaError_t linear_pass(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], float *starts, bool carry,
+                        void *status, cudaStream_t st) {
+    if (d.segs > 1 && carry) {
+        cudaError_t e = launch_linear_scan(d, p, in, laid, starts, true, status, st);
+        if (e == cudaSuccess) e = launch_linear_join(d, in, p.first, p.reverse, starts, st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_linear_scan(d, p, in, laid, starts, false, status, st);
+}
 
 LinearOperand operand(const void *p, const long long *s, int share) { return LinearOperand{p, {s[0], s[1], s[2]}, share}; }
 
@@ -113,17 +166,27 @@ int linear_forward(const sdm_linear_shape *shape, float *state, const void *q, c
     if (!state || !readings) return set_error(SDM_ERR_INVALID, "linear attention: NULL pointer");
     if (off16(state) || off16(readings))
         return set_error(SDM_ERR_INVALID, "linear attention: the state and the readings must be 16-byte aligned");
-    rc = linear_check_ws("workspace", workspace, workspace_bytes, linear_layout(d, false).bytes);
-    if (rc == SDM_OK && save) rc = linear_check_ws("saved buffer", saved, saved_bytes, linear_saved(d));
-    if (rc != SDM_OK) return rc;
-    cudaError_t e = linear_clear(workspace, workspace_bytes, st);
-    if (e == cudaSuccess && save) e = cudaMemcpyAsync(saved, state, (size_t)linear_states(d) * 4, cudaMemcpyDeviceToDevice, st);
-    if (e != cudaSuccess) return linear_status(e);
     const LinearIn in{log_decay, valid_tokens};
     const int group = d.H / d.Hk;
     const LinearPass p{operand(q, d.qs, group), operand(k, d.ks, group), operand(v, d.vs, 1), d.Dk, d.Dv, 1, false, d.scale, d.scale, 1.f,
                        state, state, d.Dv, 1, readings, false};
-    return linear_status(launch_linear_tokens(d, p, in, st));
+    if (!save && d.T <= kLinearStepTokens) {
+        const cudaError_t e = linear_clear(workspace, workspace_bytes, st);
+        return linear_status(e == cudaSuccess ? launch_linear_tokens(d, p, in, st) : e);
+    }
+    const LinearLayout l = linear_layout(d, false);
+    rc = linear_check_ws("workspace", workspace, workspace_bytes, l.bytes);
+    if (rc == SDM_OK && save) rc = linear_check_ws("saved buffer", saved, saved_bytes, linear_saved(d));
+    if (rc != SDM_OK) return rc;
+    auto ws = static_cast<unsigned char *>(workspace);
+    LinearLaid laid[4];
+    cudaError_t e = linear_clear(workspace, workspace_bytes, st);
+    if (e == cudaSuccess && save && d.segs == 1)
+        e = cudaMemcpyAsync(saved, state, (size_t)linear_states(d) * 4, cudaMemcpyDeviceToDevice, st);
+    if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, nullptr}, laid, st);
+    float *starts = save ? static_cast<float *>(saved) : reinterpret_cast<float *>(ws + l.starts);
+    if (e == cudaSuccess) e = linear_pass(d, p, in, {laid[0], laid[1], laid[2]}, starts, true, ws, st);
+    return linear_status(e);
 }
 
 }  // namespace
@@ -202,15 +265,18 @@ int sdm_linear_attention_backward(const sdm_linear_shape *shape, const void *q, 
     const LinearPass pq{og, ov, ok, d.Dv, d.Dk, tiles, false, d.scale, d.scale, 1.f, first, nullptr, 1, d.Dv, dq, parts};
     const LinearPass pk{ov, og, oq, d.Dv, d.Dk, tiles, true, d.scale, 1.f, d.scale, grad_final_state, nullptr, 1, d.Dv, dk, parts};
     const LinearPass pv{ok, oq, og, d.Dk, d.Dv, 1, true, d.scale, 1.f, d.scale, grad_final_state, grad_state, d.Dv, 1, grad_v, false};
+    LinearLaid laid[4];
     cudaError_t e = linear_clear(workspace, workspace_bytes, st);
+    if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, st);
+    float *ends = reinterpret_cast<float *>(ws + l.starts);
     // the final state's gradient may be grad_state itself, which the last pass writes
     if (e == cudaSuccess && grad_log_decay)
         e = launch_linear_decay(d, in, oq, ok, ov, og, first, grad_final_state, reinterpret_cast<double *>(ws + l.decay), grad_log_decay, st);
-    if (e == cudaSuccess) e = launch_linear_tokens(d, pq, in, st);
-    if (e == cudaSuccess) e = launch_linear_tokens(d, pk, in, st);
+    if (e == cudaSuccess) e = linear_pass(d, pq, in, {laid[3], laid[2], laid[1]}, const_cast<float *>(first), false, ws, st);
+    if (e == cudaSuccess) e = linear_pass(d, pk, in, {laid[2], laid[3], laid[0]}, ends, true, ws, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dq), tiles, d.Dk, grad_q, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dk), tiles, d.Dk, grad_k, st);
-    if (e == cudaSuccess) e = launch_linear_tokens(d, pv, in, st);
+    if (e == cudaSuccess) e = linear_pass(d, pv, in, {laid[1], laid[0], laid[3]}, ends, false, ws, st);
     return linear_status(e);
 }
 

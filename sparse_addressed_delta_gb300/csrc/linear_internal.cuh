@@ -12,6 +12,7 @@
 namespace sdm {
 
 constexpr int kLinearMaxDk = 128, kLinearMaxDv = 512;
+constexpr int kLinearStepTokens = 8;     // up to this many tokens go one by one
 // A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten whole, and
 // -inf (a hard reset at every token) has no 0 x inf among its powers.
 constexpr double kLinearMinDecay = -110.0;
@@ -59,6 +60,27 @@ __device__ __forceinline__ double linear_power(double g, double n) { return n ==
 
 inline int linear_tiles(int columns) { return (columns + 127) / 128; }
 inline long long linear_states(const LinearDims &d) { return (long long)d.B * d.H * d.Dk * d.Dv; }
+
+// an operand as the tensor copies take it: bfloat16 [B, T, heads, width], float32 ones as three planes whose sum
+// they are, [3 B, T, heads, width]
+struct LinearLaid {
+    const void *p;
+    long long s[3];
+    int heads, width;
+};
+// one to be laid out so: contiguous in dst
+struct LinearLay {
+    const void *src;
+    long long s[3];
+    int heads, width;
+    void *dst;
+};
+cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, cudaStream_t st);
+// A sequence in segments (d.segs > 1): a first launch (carry) takes every segment but the pass's last from a state
+// of zeros to what it adds, a join makes the states they begin with of that, and a second launch runs all at once.
+cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], float *starts, bool carry,
+                               void *status, cudaStream_t st);
+cudaError_t launch_linear_join(const LinearDims &d, const LinearIn &in, const float *first, bool reverse, float *starts, cudaStream_t st);
 
 cudaError_t launch_linear_tokens(const LinearDims &d, const LinearPass &p, const LinearIn &in, cudaStream_t st);
 // out [B, T, Hk, width] = the sum over a key head's heads, and over `blocks` parts, of part [blocks][B, T, H, width]

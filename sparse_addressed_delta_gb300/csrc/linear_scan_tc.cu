@@ -1,0 +1,602 @@
+// Linear attention's pass (linear_internal.cuh) over a head's chunks of 64 tokens on the 5th-generation tensor
+// cores. Everything is transposed: 128 of the result's columns are the 128 lanes of tensor memory. With L the
+// head's log-decay, i and j tokens of a chunk that begins with state S (a mirrored pass has i and j exchanged):
+//   Z = (Q K^T) e^{L (i - j)} for j <= i, else 0          P, then planes in shared memory
+//   o = e^{L (i + 1)} (S^T Q^T) + V^T Z^T                 OA and OB
+//   S = e^{L n} S + V^T (e^{L (n - 1 - j)} K)              U
+// A float operand (S, Z, the decayed keys) goes in as three bfloat16 planes (24 bits), so results keep float32's
+// accuracy and bfloat16 ones differ from float32 arithmetic's only where that rounds the other way. float32 inputs
+// come as three planes too (NP = 3), with six of their products. The state stays in registers in float32; the
+// tensor core only ever sums one chunk, from the smallest terms up (it cuts an accumulator's low bits at every
+// step).
+//
+// S^T's planes are an A operand in tensor memory, V one in shared memory; Q, Z and the decayed keys are B operands
+// there. Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the tokens and of K), warp 16 issues the
+// products, warp 17 loads by tensor copies. While the threads make Z and the decayed keys of the next chunk the
+// tensor core reads the state; while they store the results and split the new state it makes the next chunk's U,
+// OB and P. Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block, and the block
+// leaves after its copies and products in flight.
+#include <type_traits>
+
+#include "linear_internal.cuh"
+#include "tcgen05.cuh"
+
+namespace sdm {
+namespace {
+
+constexpr int kLinC = 64, kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 2);
+
+template <int KP, int NP>
+struct LinScan {
+    static constexpr int TILE = kLinC * 128, KT = KP / 64;         // 64 columns of 64 tokens; such tiles of Q or K
+    static constexpr int Q = 0, K = Q + NP * KT * TILE, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
+    static constexpr int STAGES = NP == 1 ? 3 : 1;
+    static constexpr int KX = STAGES * STAGE, Z = KX + 3 * KT * TILE, AUX = Z + 3 * TILE;   // decayed keys, Z: planes
+    static constexpr int POW = AUX, PAIR = POW + 4 * 80, BAD = PAIR + 4 * 128, BARS = BAD + 4 * 512, BYTES = BARS + 256 + 1024;
+    static_assert(BYTES <= 227 * 1024, "shared memory");
+    static constexpr int SP = 0, OA = 3 * (KP / 2), OB = OA + kLinC, U = OB + kLinC, P = U + KP;
+    static_assert(P + kLinC <= 512, "tensor memory");
+};
+
+enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_P = 9, B_ZK, B_U, B_UF, B_O, B_OF, B_S, B_DRAIN, B_COUNT };
+
+enum { LIN_RUN, LIN_CARRY };
+
+struct LinArgs {
+    LinearPass p;
+    const float *g;
+    const int32_t *valid;
+    float *starts;                       // [segs][B, H, Dk, Dv] states the segments begin with, in the pass's order
+    DevStatus *status;
+    long long heads[3];                  // head strides of the laid operands, 0: broadcast
+    long long seqs[3];
+    bool column;                         // columns with NaN or infinity are taken again (linear_column)
+};
+
+// One column of a segment by one warp, token by token from the state it begins with; the readings of tokens from
+// t1 on are stored. For columns whose update in a chunk is not finite: in the chunk's products a NaN or infinity of
+// one token meets the zeros that stand for the tokens before it (0 x inf is NaN), here it reaches the later ones alone.
+template <typename T>
+__device__ __noinline__ void linear_column(const LinearDims &d, const LinearPass &p, float fade, int b, int h, int col, int t0, int t1, int t2,
+                                           const float *S) {
+    constexpr int NR = kLinearMaxDk / 32;
+    const int lane = threadIdx.x & 31;
+    const T *q = static_cast<const T *>(p.q.p) + b * p.q.s[0] + h / p.q.share * p.q.s[2];
+    const T *k = static_cast<const T *>(p.k.p) + b * p.k.s[0] + h / p.k.share * p.k.s[2];
+    const T *v = static_cast<const T *>(p.v.p) + b * p.v.s[0] + h / p.v.share * p.v.s[2] + col;
+    T *o = static_cast<T *>(p.out) + ((long long)b * d.T * d.H + h) * p.V + col;
+    float s[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) s[i] = S && lane + 32 * i < p.K ? S[(lane + 32 * i) * p.sk] : 0.f;
+#pragma unroll 1
+    for (int t = t0; t < t2; ++t) {
+        const float x = to_f32(v[t * p.v.s[1]]);
+        float c = 0.f;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (lane + 32 * i < p.K) {
+                s[i] = fmaf(to_f32(k[t * p.k.s[1] + lane + 32 * i]), x, s[i] * fade);
+                c = fmaf(to_f32(q[t * p.q.s[1] + lane + 32 * i]), s[i], c);
+            }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) c += __shfl_xor_sync(~0u, c, m);
+        if (lane == 0 && t >= t1) o[(long long)t * d.H * p.V] = from_f32<T>(p.from * c);
+    }
+}
+
+// the sequences from the longest down, so that the last blocks to start are short
+__device__ __forceinline__ int linear_longest_first(const LinearDims &d, const int32_t *valid, int b) {
+    if (!valid || d.B > 32) return b;
+    const int lane = threadIdx.x & 31, mine = lane < d.B ? linear_valid(valid, lane, d.T) : -1;
+    int rank = 0;
+    for (int i = 0; i < d.B; ++i) {
+        const int other = __shfl_sync(~0u, mine, i);
+        rank += other > mine || (other == mine && i < lane);
+    }
+    return __ffs(__ballot_sync(~0u, rank == b)) - 1;
+}
+
+template <int KP, int NP, int MODE, bool REV, typename OT>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    k_linear_scan(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ LinearDims d, const __grid_constant__ LinArgs a) {
+    using L = LinScan<KP, NP>;
+    constexpr int C = kLinC, HD = KP / 4, ST = L::STAGES, KT = L::KT, TILE = L::TILE;
+    constexpr bool CARRY = MODE == LIN_CARRY;
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    auto bar = reinterpret_cast<unsigned long long *>(smem + L::BARS);
+    volatile int *dead = reinterpret_cast<int *>(bar + B_COUNT);
+    auto slot = reinterpret_cast<uint32_t *>(bar + B_COUNT + 1);
+    float *pw = reinterpret_cast<float *>(smem + L::POW), *pair = reinterpret_cast<float *>(smem + L::PAIR);
+    const LinearPass &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // this block's columns, part of K, head and segment
+    unsigned at_block = blockIdx.x;
+    const int tiles = (p.V + 127) / 128;
+    const int tile = (int)(at_block % tiles);
+    at_block /= tiles;
+    const int kb = (int)(at_block % p.blocks);
+    at_block /= p.blocks;
+    const int h = (int)(at_block % d.H);
+    at_block /= d.H;
+    const int b = linear_longest_first(d, a.valid, (int)(at_block % d.B)), seg = (int)(at_block / d.B);   // seg: in the pass's order
+    const long long bh = (long long)b * d.H + h;
+    const int v0 = tile * 128, k0 = kb * 128, K = p.K - k0 < 128 ? p.K - k0 : 128;
+    const int ntok = linear_valid(a.valid, b, d.T), chunks = (ntok + C - 1) / C;
+    const int place = REV ? d.segs - 1 - seg : seg;
+    const int n0 = (int)((long long)chunks * place / d.segs), nch = (int)((long long)chunks * (place + 1) / d.segs) - n0;
+    const long long states = (long long)d.B * d.H * d.Dk * d.Dv, own = bh * d.Dk * d.Dv + k0 * p.sk;
+
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(bar + B_FULL + i, 32);
+            mbar_init(bar + B_BULK + i, 1);
+            mbar_init(bar + B_EMPTY + i, 1);
+        }
+        for (int i = B_P; i < B_COUNT; ++i) mbar_init(bar + i, i == B_ZK || i == B_UF || i == B_OF || i == B_S ? kLinWarps : 1);
+        *dead = a.status->code != 0;                               // an earlier kernel of this call gave up
+        fence_mbar_init();
+    }
+    if (warp == kLinWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid < 128) {
+        const double g = a.g[h];
+        const float x = tid <= C ? (float)linear_power(g, tid) : 0.f;
+        if (tid <= C) pw[tid] = x;
+        // e^{L n} of n tokens apart, 0 before
+        pair[tid] = tid < C ? 0.f : p.pair * (float)linear_power(g, tid - C);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *slot;
+    auto chunk_at = [&](int it) { return REV ? n0 + nch - 1 - it : n0 + it; };
+    int first = -1;                                                // iteration of the column's first update that is not finite
+    float S[HD];
+
+    if (warp < kLinWarps) {
+        const int part = warp >> 2, lane0 = 32 * (warp & 3), col = v0 + lane0 + lane, kk = part * HD;
+        const bool mine = col < p.V;
+        const uint32_t at = tm + ((uint32_t)lane0 << 16);
+        const float *begin = CARRY ? nullptr : d.segs > 1 ? a.starts + seg * states : p.first;
+#pragma unroll
+        for (int i = 0; i < HD; ++i) S[i] = begin && mine && kk + i < K ? begin[own + (kk + i) * p.sk + col * p.sv] : 0.f;
+        auto planes_of_s = [&] {
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = S[c + i];
+                const uint32_t dst = at + L::SP + (kk + c) / 2;
+                tc_store_planes(dst, dst + KP / 2, dst + KP, x);
+            }
+            tc_wait_st();
+        };
+        auto arrive = [&](int which) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + which);
+        };
+        // Z (lanes 0..63: a token's row each) and the decayed keys (the other lanes) of chunk `it`
+        auto local = [&](int it) {
+            const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
+            if (!CARRY && !tc_warp_wait(bar + B_P, it & 1, dead, d.spin)) return false;   // (and the products that read them last)
+            if (CARRY || (warp & 3) >= 2) {
+                constexpr int THREADS = CARRY ? 512 : 256;
+                const int id = CARRY ? tid : part * 64 + ((warp & 3) - 2) * 32 + lane;
+                if (!tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin)) return false;
+                const unsigned char *src = smem + it % ST * L::STAGE + L::K;
+#pragma unroll
+                for (int i = id; i < C * KP / 8; i += THREADS) {
+                    const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
+                    const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
+                    float x[8];
+#pragma unroll
+                    for (int m = NP - 1; m >= 0; --m) {
+                        const uint4 r = *reinterpret_cast<const uint4 *>(src + m * KT * TILE + off);
+                        const unsigned u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[2 * e] = m == NP - 1 ? lo_f32(u[e]) : x[2 * e] + lo_f32(u[e]);
+                            x[2 * e + 1] = m == NP - 1 ? hi_f32(u[e]) : x[2 * e + 1] + hi_f32(u[e]);
+                        }
+                    }
+                    unsigned pl[3][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        unsigned s[3];
+                        split_bf16<3>(x[2 * e] * w, x[2 * e + 1] * w, s);
+                        pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
+                    }
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        *reinterpret_cast<uint4 *>(smem + L::KX + m * KT * TILE + off) = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
+                }
+            } else {
+                const int row = lane0 + lane;
+                tc_fence_after();
+                float x[16];
+                tc_load16(at + L::P + 16 * part, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int apart = REV ? 16 * part + i - row : row - 16 * part - i;
+                    x[i] = apart >= 0 ? x[i] * pair[C + apart] : 0.f;
+                }
+                unsigned pl[3][8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    unsigned s[3];
+                    split_bf16<3>(x[2 * e], x[2 * e + 1], s);
+                    pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
+                }
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<uint4 *>(smem + L::Z + m * TILE + tc_at(row, 2 * part + c)) =
+                            make_uint4(pl[m][4 * c], pl[m][4 * c + 1], pl[m][4 * c + 2], pl[m][4 * c + 3]);
+            }
+            fence_proxy_async_smem();
+            arrive(B_ZK);
+            return true;
+        };
+        if (!CARRY && nch > 0) {
+            planes_of_s();
+            arrive(B_S);
+        }
+        bool ok = nch > 0 && local(0);
+        for (int it = 0; ok && it < nch; ++it) {
+            const unsigned par = it & 1;
+            const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
+            float x[16];
+            ok = tc_warp_wait(bar + B_U, par, dead, d.spin);
+            if (!ok) break;
+            tc_fence_after();
+            const float whole = pw[nt];
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+                tc_load16(at + L::U + kk + c, x);
+                if (!CARRY && c == 0 && first < 0 && !(fabsf(x[0]) <= 3.402823466e38f)) first = it;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[c + i] = fmaf(whole, S[c + i], x[i]);
+            }
+            arrive(B_UF);
+            if (it + 1 < nch) {
+                ok = local(it + 1);
+                if (!ok) break;
+            }
+            if constexpr (!CARRY) {
+                ok = tc_warp_wait(bar + B_O, par, dead, d.spin);
+                if (!ok) break;
+                tc_fence_after();
+                float y[16];
+                tc_load16(at + L::OA + 16 * part, y);
+                tc_load16(at + L::OB + 16 * part, x);
+                arrive(B_OF);
+                OT *out = static_cast<OT *>(p.out) + ((((long long)kb * d.B + b) * d.T + n * C + 16 * part) * d.H + h) * p.V + col;
+                const int left = d.T - n * C - 16 * part;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int t = 16 * part + i;
+                    const float r = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[i], x[i]) : 0.f;
+                    if (mine && i < left) *out = from_f32<OT>(r);
+                    out += (long long)d.H * p.V;
+                }
+                if (it + 1 < nch) {
+                    planes_of_s();
+                    arrive(B_S);
+                }
+            }
+        }
+        reinterpret_cast<int *>(smem + L::BAD)[part * 128 + lane0 + lane] = first;
+    } else if (warp == kLinWarps) {
+        // ---- the products
+        const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
+        constexpr int KS = KP / 16;
+        const uint32_t zd = tc_k_major(base + L::Z), kx = tc_n_major(base + L::KX, TILE);
+        auto scores = [&](int it) {                                // lanes 64.. hold whatever follows Q
+            const uint32_t st = base + it % ST * L::STAGE, qd = tc_k_major(st + L::Q), kd = tc_k_major(st + L::K);
+            bool add = false;
+#pragma unroll
+            for (int sum = NP - 1; sum >= 0; --sum)
+#pragma unroll
+                for (int m = sum; m >= 0; --m)
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const int off = ((ks >> 2) * TILE + 32 * (ks & 3)) / 16;
+                        tc_mma_ss(one, tu + L::P, qd + m * KT * TILE / 16 + off, kd + (sum - m) * KT * TILE / 16 + off, tc_idesc<false>(C), add);
+                        add = true;
+                    }
+            tc_commit_to(one, bar + B_P);
+        };
+        bool ok = nch > 0;
+        if (!CARRY && ok) {
+            ok = tc_warp_wait(bar + B_FULL, 0, dead, d.spin);
+            tc_fence_after();
+            if (ok) scores(0);
+        }
+        for (int it = 0; ok && it < nch; ++it) {
+            const uint32_t st = base + it % ST * L::STAGE, qd = tc_k_major(st + L::Q), vm = tc_n_major(st + L::V, TILE);
+            const unsigned par = it & 1;
+            ok = tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin) && tc_warp_wait(bar + B_ZK, par, dead, d.spin) &&
+                 (it == 0 || tc_warp_wait(bar + B_UF, par ^ 1, dead, d.spin));
+            if (!ok) break;
+            tc_fence_after();
+            bool add = false;
+#pragma unroll
+            for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks) {
+                        tc_mma_ss(one, tu + L::U, vm + (m * 2 * TILE + 2048 * ks) / 16, kx + ((sum - m) * KT * TILE + 2048 * ks) / 16,
+                                  tc_idesc<true, true>(KP), add);
+                        add = true;
+                    }
+            tc_commit_to(one, bar + B_U);
+            if constexpr (!CARRY) {
+                if (it > 0) {
+                    ok = tc_warp_wait(bar + B_OF, par ^ 1, dead, d.spin);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                // Z is triangular: the 16 tokens of step ks reach those from 16 ks on (mirrored: up to 16 ks + 15)
+                add = false;
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
+#pragma unroll
+                        for (int i = 0; i < C / 16; ++i) {
+                            const int ks = REV ? C / 16 - 1 - i : i, row = REV ? 0 : 16 * ks;
+                            tc_mma_ss(one, tu + L::OB + row, vm + (m * 2 * TILE + 2048 * ks) / 16,
+                                      zd + ((sum - m) * TILE + row * 128 + 32 * ks) / 16, tc_idesc<false, true>(REV ? 16 * ks + 16 : C - row), add);
+                            add = true;
+                        }
+                if (ST > 1 && it + 1 < nch) {
+                    ok = tc_warp_wait(bar + B_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(it + 1);
+                }
+                ok = tc_warp_wait(bar + B_S, par, dead, d.spin);
+                if (!ok) break;
+                tc_fence_after();
+                add = false;
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            tc_mma_ts(one, tu + L::OA, tu + L::SP + (sum - m) * (KP / 2) + 8 * ks,
+                                      qd + (m * KT * TILE + (ks >> 2) * TILE + 32 * (ks & 3)) / 16, tc_idesc<false>(C), add);
+                            add = true;
+                        }
+                tc_commit_to(one, bar + B_O);
+            }
+            tc_commit_to(one, bar + B_EMPTY + it % ST);
+            if (!CARRY && ST == 1 && it + 1 < nch) {
+                ok = tc_warp_wait(bar + B_FULL, (it + 1) & 1, dead, d.spin);
+                if (!ok) break;
+                tc_fence_after();
+                scores(it + 1);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- the chunks' inputs
+        constexpr uint32_t bytes = CARRY ? NP * (KT + 2) * TILE : L::STAGE;
+        for (int it = 0; it < nch; ++it) {
+            const int s = it % ST, t0 = chunk_at(it) * C, nt = ntok - t0 < C ? ntok - t0 : C;
+            unsigned char *st = smem + s * L::STAGE;
+            unsigned long long *full = bar + B_BULK + s;
+            if (it >= ST && !tc_warp_wait(bar + B_EMPTY + s, (it / ST - 1) & 1, dead, d.spin)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+                for (int m = 0; m < NP; ++m) {
+#pragma unroll
+                    for (int c = 0; c < KT; ++c) {
+                        if (!CARRY)
+                            tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], h / p.q.share), t0,
+                                           tc_coord(a.seqs[0], b) + m * d.B, full);
+                        tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], h / p.k.share), t0,
+                                       tc_coord(a.seqs[1], b) + m * d.B, full);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[2], h / p.v.share), t0,
+                                       tc_coord(a.seqs[2], b) + m * d.B, full);
+                }
+            }
+            __syncwarp();
+            if (!tc_warp_wait(full, it / ST & 1, dead, d.spin)) {
+                mbar_wait_bounded(full, it / ST & 1);              // nothing in flight behind a give-up
+                break;
+            }
+            if (nt < C) {                                          // what lies past the valid tokens is not used
+                for (int i = lane; i < (C - nt) * 8; i += 32) {
+                    const int off = tc_at(nt + (i >> 3), i & 7);
+                    for (int c = 0; c < L::STAGE / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(bar + B_FULL + s);
+        }
+    }
+    __syncthreads();
+    if (*dead) {
+        // the products issued so far are waited for (the copies were, by their own warp)
+        if (tid == 32 * kLinWarps) {
+            tc_commit_to(1, bar + B_DRAIN);
+            mbar_wait_bounded(bar + B_DRAIN, 0);
+            atomicCAS(&a.status->code, 0, (int)SDM_ERR_TIMEOUT);
+        }
+        __syncthreads();
+    }
+    tc_fence_before();
+    const bool bad = __syncthreads_or(first >= 0);
+    if (warp == kLinWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
+    if (*dead) return;
+    if constexpr (!CARRY) {
+        if (bad && a.column) {
+            const int *at = reinterpret_cast<int *>(smem + L::BAD);
+            const float *begin = d.segs > 1 ? a.starts + seg * states : p.first;
+            for (int c = warp; c < 128; c += kLinThreads / 32) {
+                const int n = at[c], col = v0 + c;
+                // a value's NaN leaves no row of the update finite
+                if (n < 0 || col >= p.V || at[128 + c] != n || at[256 + c] != n || at[384 + c] != n) continue;
+                const int t1 = (n0 + n) * C, t2 = t1 + C < ntok ? t1 + C : ntok;
+                using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
+                linear_column<IT>(d, p, (float)linear_power(a.g[h], 1.0), b, h, col, n0 * C, t1, t2, begin ? begin + own + col * p.sv : nullptr);
+            }
+            __syncthreads();
+        }
+        if (seg + 1 == d.segs) {
+            const int cols = p.V - v0 < 128 ? p.V - v0 : 128;
+            OT *out = static_cast<OT *>(p.out) + (((long long)kb * d.B + b) * d.T * d.H + h) * p.V + v0;
+            for (long long t = (long long)chunks * C + (tid >> 7); t < d.T; t += kLinThreads >> 7)
+                if ((tid & 127) < cols && tid < (kLinThreads >> 7 << 7)) out[t * d.H * p.V + (tid & 127)] = from_f32<OT>(0.f);
+        }
+    }
+    // where the state goes: a carried segment's is the next one's share
+    float *end = CARRY ? a.starts + (seg + 1) * states : seg + 1 == d.segs ? p.last : nullptr;
+    if (warp < kLinWarps && end) {
+        const int kk = (warp >> 2) * HD, col = v0 + 32 * (warp & 3) + lane;
+        if (col < p.V)
+#pragma unroll
+            for (int i = 0; i < HD; ++i)
+                if (kk + i < K) end[own + (kk + i) * p.sk + col * p.sv] = S[i];
+    }
+}
+
+// starts [segs]: the state itself, then each segment's first state from the one before and what the carry left
+__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ LinearDims d, const float *g, const int32_t *valid, const float *first,
+                                                     bool reverse, float *starts) {
+    const long long cells = (long long)d.Dk * d.Dv, states = cells * d.B * d.H;
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= states) return;
+    const long long bh = i / cells;
+    const int b = (int)(bh / d.H), h = (int)(bh % d.H);
+    const int ntok = linear_valid(valid, b, d.T), chunks = (ntok + d.C - 1) / d.C;
+    auto bound = [&](int n) {
+        const int t = (int)((long long)chunks * n / d.segs) * d.C;
+        return t < ntok ? t : ntok;
+    };
+    float4 s = first ? make_float4(first[i], first[i + 1], first[i + 2], first[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4 *>(starts + i) = s;
+    for (int m = 1; m < d.segs; ++m) {
+        const int place = reverse ? d.segs - m : m - 1;            // of the segment before
+        const float w = (float)linear_power(g[h], bound(place + 1) - bound(place));
+        float4 *at = reinterpret_cast<float4 *>(starts + m * states + i);
+        const float4 e = *at;
+        s = make_float4(fmaf(w, s.x, e.x), fmaf(w, s.y, e.y), fmaf(w, s.z, e.z), fmaf(w, s.w, e.w));
+        *at = s;
+    }
+}
+
+template <int KP, int NP, int MODE, bool REV, typename OT>
+cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+    auto kern = k_linear_scan<KP, NP, MODE, REV, OT>;
+    using L = LinScan<KP, NP>;
+    set_kernel_smem(kern, L::BYTES);
+    const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * (MODE == LIN_CARRY ? d.segs - 1 : d.segs);
+    kern<<<(unsigned)blocks, kLinThreads, L::BYTES, st>>>(mq, mk, mv, d, a);
+    return cudaGetLastError();
+}
+
+template <int KP, int NP>
+cudaError_t scan_of(const LinearDims &d, const LinArgs &a, bool carry, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                    cudaStream_t st) {
+    using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
+    if (carry)
+        return a.p.reverse ? scan<KP, NP, LIN_CARRY, true, IT>(d, a, mq, mk, mv, st) : scan<KP, NP, LIN_CARRY, false, IT>(d, a, mq, mk, mv, st);
+    if constexpr (NP == 1)
+        if (a.p.out_f32)
+            return a.p.reverse ? scan<KP, NP, LIN_RUN, true, float>(d, a, mq, mk, mv, st) : scan<KP, NP, LIN_RUN, false, float>(d, a, mq, mk, mv, st);
+    return a.p.reverse ? scan<KP, NP, LIN_RUN, true, IT>(d, a, mq, mk, mv, st) : scan<KP, NP, LIN_RUN, false, IT>(d, a, mq, mk, mv, st);
+}
+
+// the operands as the tensor copies take them: float32 ones as three bfloat16 planes, the others contiguous
+struct LayTable {
+    const void *src[4];
+    __nv_bfloat16 *dst[4];
+    long long s[4][3];
+    int heads[4], width[4];
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_linear_lay(const __grid_constant__ LayTable t, int B, int T_) {
+    const int w = blockIdx.y, heads = t.heads[w], width = t.width[w];
+    const T *x = static_cast<const T *>(t.src[w]);
+    const long long all = (long long)B * T_ * heads * (width / 8);
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+        const long long row = i / (width / 8), h = row % heads, bt = row / heads, at = bt % T_, b = bt / T_;
+        const T *src = x + b * t.s[w][0] + at * t.s[w][1] + h * t.s[w][2] + i % (width / 8) * 8;
+        if constexpr (sizeof(T) == 2) {
+            reinterpret_cast<uint4 *>(t.dst[w])[i] = *reinterpret_cast<const uint4 *>(src);
+        } else {
+            float f[8];
+            load_vec<float, 8, true>(src, f);
+            unsigned pl[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                unsigned s[3];
+                split_bf16<3>(f[2 * e], f[2 * e + 1], s);
+                pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
+            }
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+                reinterpret_cast<uint4 *>(t.dst[w])[m * all + i] = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], float *starts, bool carry,
+                               void *status, cudaStream_t st) {
+    const int np = d.dtype == SDM_F32 ? 3 : 1;
+    LinArgs a{p, in.g, in.valid, starts, static_cast<DevStatus *>(status), {}, {}, p.last != nullptr && !p.reverse};
+    CUtensorMap m[3];
+    for (int i = 0; i < 3; ++i) {
+        const cudaError_t e = tc_tensor_map(m + i, laid[i].p, laid[i].s, np * d.B, d.T, laid[i].heads, laid[i].width);
+        if (e != cudaSuccess) return e;
+        a.seqs[i] = laid[i].s[0];
+        a.heads[i] = laid[i].s[2];
+    }
+    const bool wide = p.K > 64;
+    if (np == 1) return wide ? scan_of<128, 1>(d, a, carry, m[0], m[1], m[2], st) : scan_of<64, 1>(d, a, carry, m[0], m[1], m[2], st);
+    return wide ? scan_of<128, 3>(d, a, carry, m[0], m[1], m[2], st) : scan_of<64, 3>(d, a, carry, m[0], m[1], m[2], st);
+}
+
+cudaError_t launch_linear_join(const LinearDims &d, const LinearIn &in, const float *first, bool reverse, float *starts, cudaStream_t st) {
+    const long long blocks = (linear_states(d) / 4 + 255) / 256;
+    k_linear_join<<<(unsigned)blocks, 256, 0, st>>>(d, in.g, in.valid, first, reverse, starts);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, cudaStream_t st) {
+    if (n == 0) return cudaSuccess;
+    LayTable t{};
+    long long most = 0;
+    for (int i = 0; i < n; ++i) {
+        t.src[i] = lay[i].src;
+        t.dst[i] = static_cast<__nv_bfloat16 *>(lay[i].dst);
+        for (int j = 0; j < 3; ++j) t.s[i][j] = lay[i].s[j];
+        t.heads[i] = lay[i].heads;
+        t.width[i] = lay[i].width;
+        const long long units = (long long)d.B * d.T * lay[i].heads * (lay[i].width / 8);
+        most = units > most ? units : most;
+    }
+    const long long want = (most + 255) / 256;
+    const dim3 grid((unsigned)(want < 8 * kRefSms ? want : 8 * kRefSms), n);
+    if (d.dtype == SDM_F32) k_linear_lay<float><<<grid, 256, 0, st>>>(t, d.B, d.T);
+    else k_linear_lay<__nv_bfloat16><<<grid, 256, 0, st>>>(t, d.B, d.T);
+    return cudaGetLastError();
+}
+
+}  // namespace sdm
