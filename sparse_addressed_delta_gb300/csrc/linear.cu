@@ -114,7 +114,7 @@ LinearLayout linear_layout(const LinearDims &d, bool back) {
         const size_t part = linear_parts(d) ? (size_t)linear_tiles(d.Dv) * d.B * d.T * d.H * d.Dk * 4 : 0;
         l.dq = take(part);
         l.dk = take(part);
-        l.decay = take((size_t)d.B * d.H * linear_tiles(d.Dv) * 8);
+        l.decay = take((size_t)linear_decay_parts(d) * 8);
     }
     l.bytes = at;
     return l;
@@ -269,13 +269,14 @@ int sdm_linear_attention_backward(const sdm_linear_shape *shape, const void *q, 
     cudaError_t e = linear_clear(workspace, workspace_bytes, st);
     if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, st);
     float *ends = reinterpret_cast<float *>(ws + l.starts);
-    // the final state's gradient may be grad_state itself, which the last pass writes
-    if (e == cudaSuccess && grad_log_decay)
-        e = launch_linear_decay(d, in, oq, ok, ov, og, first, grad_final_state, reinterpret_cast<double *>(ws + l.decay), grad_log_decay, st);
     if (e == cudaSuccess) e = linear_pass(d, pq, in, {laid[3], laid[2], laid[1]}, const_cast<float *>(first), false, ws, st);
     if (e == cudaSuccess) e = linear_pass(d, pk, in, {laid[2], laid[3], laid[0]}, ends, true, ws, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dq), tiles, d.Dk, grad_q, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dk), tiles, d.Dk, grad_k, st);
+    if (e == cudaSuccess && grad_log_decay)
+        e = launch_linear_decay(d, in, laid, first, d.segs > 1 ? ends : grad_final_state, reinterpret_cast<double *>(ws + l.decay), grad_log_decay,
+                                ws, st);
+    // last: the final state's gradient may be grad_state itself
     if (e == cudaSuccess) e = linear_pass(d, pv, in, {laid[1], laid[0], laid[3]}, ends, false, ws, st);
     return linear_status(e);
 }

@@ -1,0 +1,395 @@
+// The gradient of linear attention's decays. With G = dS / dL carried along beside a head's state S (L its
+// log-decay), a chunk of n tokens that begins with (S, G) adds, with i, j its tokens,
+//   sum_{j < i} (i - j) e^{L (i - j)} (q_i . k_j) (do_i . v_j) + <S, A'> + <G, A>
+//   A  = sum_i e^{L (i + 1)} q_i do_i^T,   A' = sum_i (i + 1) e^{L (i + 1)} q_i do_i^T
+// (times scale) and goes on with
+//   G = e^{L n} (G + n S) + W',  W' = sum_j (n - 1 - j) e^{L (n - 1 - j)} k_j v_j^T
+//   S = e^{L n} S + W,           W  = sum_j e^{L (n - 1 - j)} k_j v_j^T
+// Every term carries its own decay, so none is a difference of larger ones. A segment begins with the state that
+// the forward kept and G = 0, and ends with <G, R>, R the gradient of the state there.
+//
+// S and G stay in registers in float32, transposed: 128 of Dv's columns are the lanes of tensor memory (a quarter
+// of KP a thread). The four products are V^T or dO^T (A operands in shared memory) with decayed queries and keys,
+// three bfloat16 planes each, through two buffers in turn: while one is multiplied the threads fill the other and
+// take what the product before it made. All is bilinear in (Dk, Dv), so blocks take KP columns of Dk and 128 of Dv
+// for themselves, the pairs' sums too. Warps as in linear_scan_tc.cu.
+#include <type_traits>
+
+#include "linear_internal.cuh"
+#include "tcgen05.cuh"
+
+namespace sdm {
+namespace {
+
+constexpr int kDecC = 64, kDecWarps = 16, kDecThreads = 32 * (kDecWarps + 2);
+
+template <int KP, int NP>
+struct LinDecay {
+    static constexpr int TILE = kDecC * 128, KT = KP / 64;
+    // (a product's A operand of 128 rows reads on past the 64 of Q and dO: into what follows them)
+    static constexpr int Q = 0, G = Q + NP * KT * TILE, K = G + NP * 2 * TILE, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
+    static constexpr int STAGES = NP == 1 ? 2 : 1;
+    static constexpr int BUF = STAGES * STAGE, BUFFER = 3 * KT * TILE, AUX = BUF + 2 * BUFFER;
+    static constexpr int POW = AUX, SUMS = POW + 4 * 80, BARS = SUMS + 8 * kDecWarps, BYTES = BARS + 256 + 1024;
+    static_assert(BYTES <= 227 * 1024, "shared memory");
+    static constexpr int A = 0, A1 = KP, W = 2 * KP, W1 = 3 * KP;  // (the pairs' products in A1's place, 2 x 64 columns)
+    static_assert(KP >= 64 && 4 * KP <= 512, "tensor memory");
+    static constexpr int PQ = KP == 128 ? A1 : 4 * KP, PG = PQ + 64;
+};
+
+enum { D_FULL = 0, D_BULK = 2, D_EMPTY = 4, D_MUL = 6, D_CONV = 10, D_PAIR = 14, D_PREAD, D_A1READ, D_DRAIN, D_COUNT };
+
+struct DecayArgs {
+    const float *g;
+    const int32_t *valid;
+    const float *starts, *ends;          // [segs] states, in order; gradients of the ends, from the last (segs == 1: null: 0)
+    double *part;
+    DevStatus *status;
+    long long heads[4], seqs[4];         // q, k, v, grad: strides of the laid operands, 0: broadcast
+    int share, kblocks;
+};
+
+template <int KP, int NP>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    k_linear_decay(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                   const __grid_constant__ CUtensorMap mg, const __grid_constant__ LinearDims d, const __grid_constant__ DecayArgs a) {
+    using L = LinDecay<KP, NP>;
+    constexpr int C = kDecC, HD = KP / 4, ST = L::STAGES, KT = L::KT, TILE = L::TILE;
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    auto bar = reinterpret_cast<unsigned long long *>(smem + L::BARS);
+    volatile int *dead = reinterpret_cast<int *>(bar + D_COUNT);
+    auto slot = reinterpret_cast<uint32_t *>(bar + D_COUNT + 1);
+    float *pw = reinterpret_cast<float *>(smem + L::POW);
+    double *sums = reinterpret_cast<double *>(smem + L::SUMS);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    unsigned at_block = blockIdx.x;
+    const int tiles = (d.Dv + 127) / 128;
+    const int tile = (int)(at_block % tiles);
+    at_block /= tiles;
+    const int kb = (int)(at_block % a.kblocks);
+    at_block /= a.kblocks;
+    const int seg = (int)(at_block % d.segs);
+    const long long bh = at_block / d.segs;
+    const int b = (int)(bh / d.H), h = (int)(bh % d.H);
+    const int v0 = tile * 128, k0 = kb * KP;
+    const int ntok = linear_valid(a.valid, b, d.T), chunks = (ntok + C - 1) / C;
+    const int n0 = (int)((long long)chunks * seg / d.segs), nch = (int)((long long)chunks * (seg + 1) / d.segs) - n0;
+    const long long states = (long long)d.B * d.H * d.Dk * d.Dv;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar + D_FULL + i, 32);
+            mbar_init(bar + D_BULK + i, 1);
+            mbar_init(bar + D_EMPTY + i, 1);
+        }
+        for (int i = D_MUL; i < D_COUNT; ++i)
+            mbar_init(bar + i, (i >= D_CONV && i < D_PAIR) || i == D_PREAD || i == D_A1READ ? kDecWarps : 1);
+        *dead = a.status->code != 0;
+        fence_mbar_init();
+    }
+    if (warp == kDecWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid <= C) pw[tid] = (float)linear_power(a.g[h], tid);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *slot;
+
+    if (warp < kDecWarps) {
+        const int part = warp >> 2, lane0 = 32 * (warp & 3), col = v0 + lane0 + lane, kk = part * HD;
+        const bool mine = col < d.Dv;
+        const uint32_t at = tm + ((uint32_t)lane0 << 16);
+        const long long own = bh * d.Dk * d.Dv + (long long)(k0 + kk) * d.Dv + col;
+        float S[HD], G[HD];
+        double acc = 0.0;
+        const float *begin = a.starts + seg * states + own;
+#pragma unroll
+        for (int i = 0; i < HD; ++i) {
+            S[i] = mine && k0 + kk + i < d.Dk && nch > 0 ? begin[(long long)i * d.Dv] : 0.f;
+            G[i] = 0.f;
+        }
+        auto arrive = [&](int which) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + which);
+        };
+        auto wait = [&](int which, int it) {
+            const bool there = tc_warp_wait(bar + which, it & 1, dead, d.spin);
+            tc_fence_after();
+            return there;
+        };
+        // rows of Q or K times their weights, as planes in a buffer
+        auto convert = [&](const unsigned char *src, unsigned char *dst, auto weight) {
+#pragma unroll
+            for (int i = tid; i < C * KP / 8; i += 32 * kDecWarps) {
+                const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
+                const float w = weight(row);
+                float x[8];
+#pragma unroll
+                for (int m = NP - 1; m >= 0; --m) {
+                    const uint4 r = *reinterpret_cast<const uint4 *>(src + m * KT * TILE + off);
+                    const unsigned u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] = m == NP - 1 ? lo_f32(u[e]) : x[2 * e] + lo_f32(u[e]);
+                        x[2 * e + 1] = m == NP - 1 ? hi_f32(u[e]) : x[2 * e + 1] + hi_f32(u[e]);
+                    }
+                }
+                unsigned pl[3][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    unsigned s[3];
+                    split_bf16<3>(x[2 * e] * w, x[2 * e + 1] * w, s);
+                    pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
+                }
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    *reinterpret_cast<uint4 *>(dst + m * KT * TILE + off) = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
+            }
+            fence_proxy_async_smem();
+        };
+        // <this thread's part of the state, a product>
+        auto dot = [&](int where, const float (&s)[HD]) {
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+                float x[16];
+                tc_load16(at + where + kk + c, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum = fmaf(s[c + i], x[i], sum);
+            }
+            if (mine) acc += (double)sum;
+        };
+        // s = w s + a product
+        auto advance = [&](int where, float w, float (&s)[HD]) {
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+                float x[16];
+                tc_load16(at + where + kk + c, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[c + i] = fmaf(w, s[c + i], x[i]);
+            }
+        };
+        unsigned char *buf0 = smem + L::BUF, *buf1 = buf0 + L::BUFFER;
+        float whole = 1.f;
+        bool ok = true;
+        for (int it = 0; it < nch; ++it) {
+            const int nt = ntok - (n0 + it) * C < C ? ntok - (n0 + it) * C : C;
+            const unsigned char *st = smem + it % ST * L::STAGE;
+            ok = tc_warp_wait(bar + D_FULL + it % ST, it / ST & 1, dead, d.spin) && (it == 0 || wait(D_MUL + 2, it - 1));
+            if (!ok) break;
+            convert(st + L::Q, buf0, [&](int t) { return t < nt ? d.scale * pw[t + 1] : 0.f; });
+            arrive(D_CONV);
+            if (it > 0) advance(L::W, whole, S);
+            // the pairs: a token's row each of lanes 0..63
+            if (!(ok = wait(D_PAIR, it))) break;
+            if ((warp & 3) < 2) {
+                const int row = lane0 + lane;
+                float x[16], y[16], sum = 0.f;
+                tc_load16(at + L::PQ + 16 * part, x);
+                tc_load16(at + L::PG + 16 * part, y);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int apart = row - 16 * part - i;
+                    if (apart > 0) sum = fmaf(apart * pw[apart] * x[i], y[i], sum);
+                }
+                acc += (double)(d.scale * sum);
+            }
+            arrive(D_PREAD);
+            if (it > 0 && !(ok = wait(D_MUL + 3, it - 1))) break;
+            convert(st + L::Q, buf1, [&](int t) { return t < nt ? (t + 1) * (d.scale * pw[t + 1]) : 0.f; });
+            arrive(D_CONV + 1);
+            if (it > 0) advance(L::W1, 1.f, G);
+            if (!(ok = wait(D_MUL, it))) break;
+            convert(st + L::K, buf0, [&](int t) { return t < nt ? pw[nt - 1 - t] : 0.f; });
+            arrive(D_CONV + 2);
+            dot(L::A, G);
+            if (!(ok = wait(D_MUL + 1, it))) break;
+            convert(st + L::K, buf1, [&](int t) { return t < nt ? (nt - 1 - t) * pw[nt - 1 - t] : 0.f; });
+            arrive(D_CONV + 3);
+            dot(L::A1, S);
+            arrive(D_A1READ);
+            whole = pw[nt];
+#pragma unroll
+            for (int i = 0; i < HD; ++i) G[i] = whole * fmaf((float)nt, S[i], G[i]);
+        }
+        if (ok && nch > 0 && wait(D_MUL + 3, nch - 1)) {
+            advance(L::W1, 1.f, G);
+            if (a.ends && mine) {
+                const float *end = a.ends + (d.segs - 1 - seg) * states + own;
+                double sum = 0.0;
+#pragma unroll
+                for (int i = 0; i < HD; ++i)
+                    if (k0 + kk + i < d.Dk) sum += (double)G[i] * end[(long long)i * d.Dv];
+                acc += sum;
+            }
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) acc += __shfl_xor_sync(~0u, acc, m);
+        if (lane == 0) sums[warp] = acc;
+    } else if (warp == kDecWarps) {
+        // ---- the products
+        const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
+        // [64 tokens] x [64 tokens] over `steps` of the width, NP planes each
+        auto scores = [&](uint32_t dst, uint32_t x, uint32_t y, auto tiles_of) {
+            constexpr int TL = decltype(tiles_of)::value;
+            bool add = false;
+#pragma unroll
+            for (int sum = NP - 1; sum >= 0; --sum)
+#pragma unroll
+                for (int m = sum; m >= 0; --m)
+#pragma unroll
+                    for (int ks = 0; ks < 4 * TL; ++ks) {
+                        const int off = ((ks >> 2) * TILE + 32 * (ks & 3)) / 16;
+                        tc_mma_ss(one, dst, x + m * TL * TILE / 16 + off, y + (sum - m) * TL * TILE / 16 + off, tc_idesc<false>(C), add);
+                        add = true;
+                    }
+        };
+        auto pairs = [&](int it) {
+            const uint32_t st = base + it % ST * L::STAGE;
+            scores(tu + L::PQ, tc_k_major(st + L::Q), tc_k_major(st + L::K), std::integral_constant<int, KT>{});
+            scores(tu + L::PG, tc_k_major(st + L::G), tc_k_major(st + L::V), std::integral_constant<int, 2>{});
+            tc_commit_to(one, bar + D_PAIR);
+        };
+        auto product = [&](uint32_t dst, uint32_t vm, uint32_t kn) {
+            bool add = false;
+#pragma unroll
+            for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks) {
+                        tc_mma_ss(one, dst, vm + (m * 2 * TILE + 2048 * ks) / 16, kn + ((sum - m) * KT * TILE + 2048 * ks) / 16,
+                                  tc_idesc<true, true>(KP), add);
+                        add = true;
+                    }
+        };
+        bool ok = nch > 0 && tc_warp_wait(bar + D_FULL, 0, dead, d.spin);
+        tc_fence_after();
+        if (ok) pairs(0);
+        for (int it = 0; ok && it < nch; ++it) {
+            const uint32_t st = base + it % ST * L::STAGE, gm = tc_n_major(st + L::G, TILE), vm = tc_n_major(st + L::V, TILE);
+            const uint32_t b0 = tc_n_major(base + L::BUF, TILE), b1 = tc_n_major(base + L::BUF + L::BUFFER, TILE);
+            const unsigned par = it & 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ok = ok && tc_warp_wait(bar + D_CONV + i, par, dead, d.spin) && (i != 1 || tc_warp_wait(bar + D_PREAD, par, dead, d.spin));
+                if (!ok) break;
+                tc_fence_after();
+                product(tu + (i == 0 ? L::A : i == 1 ? L::A1 : i == 2 ? L::W : L::W1), i < 2 ? gm : vm, i & 1 ? b1 : b0);
+                tc_commit_to(one, bar + D_MUL + i);
+            }
+            if (!ok) break;
+            tc_commit_to(one, bar + D_EMPTY + it % ST);
+            if (it + 1 < nch) {
+                ok = tc_warp_wait(bar + D_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin) &&
+                     tc_warp_wait(bar + D_A1READ, par, dead, d.spin);
+                if (!ok) break;
+                tc_fence_after();
+                pairs(it + 1);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- the chunks' inputs
+        for (int it = 0; it < nch; ++it) {
+            const int s = it % ST, t0 = (n0 + it) * C, nt = ntok - t0 < C ? ntok - t0 : C;
+            unsigned char *st = smem + s * L::STAGE;
+            unsigned long long *full = bar + D_BULK + s;
+            if (it >= ST && !tc_warp_wait(bar + D_EMPTY + s, (it / ST - 1) & 1, dead, d.spin)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full, L::STAGE);
+                const int hk = h / a.share;
+#pragma unroll
+                for (int m = 0; m < NP; ++m) {
+#pragma unroll
+                    for (int c = 0; c < KT; ++c) {
+                        tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], hk), t0, tc_coord(a.seqs[0], b) + m * d.B, full);
+                        tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], hk), t0, tc_coord(a.seqs[1], b) + m * d.B, full);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tc_tensor_load(st + L::G + (m * 2 + c) * TILE, &mg, v0 + 64 * c, tc_coord(a.heads[3], h), t0, tc_coord(a.seqs[3], b) + m * d.B, full);
+                        tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[2], h), t0, tc_coord(a.seqs[2], b) + m * d.B, full);
+                    }
+                }
+            }
+            __syncwarp();
+            if (!tc_warp_wait(full, it / ST & 1, dead, d.spin)) {
+                mbar_wait_bounded(full, it / ST & 1);              // nothing in flight behind a give-up
+                break;
+            }
+            if (nt < C) {                                          // what lies past the valid tokens is not used
+                for (int i = lane; i < (C - nt) * 8; i += 32) {
+                    const int off = tc_at(nt + (i >> 3), i & 7);
+                    for (int c = 0; c < L::STAGE / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(bar + D_FULL + s);
+        }
+    }
+    __syncthreads();
+    if (*dead) {
+        // the products issued so far are waited for (the copies were, by their own warp)
+        if (tid == 32 * kDecWarps) {
+            tc_commit_to(1, bar + D_DRAIN);
+            mbar_wait_bounded(bar + D_DRAIN, 0);
+            atomicCAS(&a.status->code, 0, (int)SDM_ERR_TIMEOUT);
+        }
+        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kDecWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
+    if (tid == 0) {
+        double s = 0.0;
+        for (int i = 0; i < kDecWarps; ++i) s += sums[i];
+        a.part[blockIdx.x] = s;
+    }
+}
+
+// a head's parts of all sequences, in order
+__global__ void __launch_bounds__(128) k_linear_decay_sum(const double *part, int B, int H, int each, float *out) {
+    __shared__ double sums[128];
+    const int h = blockIdx.x;
+    double s = 0.0;
+    for (long long i = threadIdx.x; i < (long long)B * each; i += 128) s += part[(i / each * H + h) * each + i % each];
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int i = 1; i < 128; ++i) s += sums[i];
+    out[h] = (float)s;
+}
+
+template <int KP, int NP>
+cudaError_t decay(const LinearDims &d, const DecayArgs &a, const CUtensorMap *m, cudaStream_t st) {
+    using L = LinDecay<KP, NP>;
+    set_kernel_smem(k_linear_decay<KP, NP>, L::BYTES);
+    k_linear_decay<KP, NP><<<(unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearLaid (&laid)[4], const float *starts, const float *ends,
+                                double *part, float *grad_decay, void *status, cudaStream_t st) {
+    const int np = d.dtype == SDM_F32 ? 3 : 1;
+    DecayArgs a{in.g, in.valid, starts, ends, part, static_cast<DevStatus *>(status), {}, {}, d.H / d.Hk, linear_decay_blocks(d)};
+    CUtensorMap m[4];
+    for (int i = 0; i < 4; ++i) {
+        const cudaError_t e = tc_tensor_map(m + i, laid[i].p, laid[i].s, np * d.B, d.T, laid[i].heads, laid[i].width);
+        if (e != cudaSuccess) return e;
+        a.seqs[i] = laid[i].s[0];
+        a.heads[i] = laid[i].s[2];
+    }
+    const cudaError_t e = np == 3 ? decay<64, 3>(d, a, m, st) : d.Dk > 64 ? decay<128, 1>(d, a, m, st) : decay<64, 1>(d, a, m, st);
+    if (e != cudaSuccess) return e;
+    k_linear_decay_sum<<<d.H, 128, 0, st>>>(part, d.B, d.H, a.kblocks * linear_tiles(d.Dv) * d.segs, grad_decay);
+    return cudaGetLastError();
+}
+
+}  // namespace sdm

@@ -85,10 +85,11 @@ cudaError_t launch_linear_join(const LinearDims &d, const LinearIn &in, const fl
 cudaError_t launch_linear_tokens(const LinearDims &d, const LinearPass &p, const LinearIn &in, cudaStream_t st);
 // out [B, T, Hk, width] = the sum over a key head's heads, and over `blocks` parts, of part [blocks][B, T, H, width]
 cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, cudaStream_t st);
-// grad_decay [H] from q, k, v, the readings' gradient, the first state and the final state's gradient (may be
-// null); part: B H tiles(Dv) doubles
-cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearOperand &q, const LinearOperand &k, const LinearOperand &v,
-                                const LinearOperand &grad, const float *first, const float *final_grad, double *part, float *grad_decay,
-                                cudaStream_t st);
+// grad_decay [H] from the laid q, k, v and readings' gradient, the segments' first states and the gradients of the
+// states they end with (from the last one; one segment: may be null)
+inline int linear_decay_blocks(const LinearDims &d) { return d.dtype == SDM_F32 ? (d.Dk + 63) / 64 : 1; }   // of Dk
+inline long long linear_decay_parts(const LinearDims &d) { return (long long)d.B * d.H * d.segs * linear_decay_blocks(d) * linear_tiles(d.Dv); }
+cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearLaid (&laid)[4], const float *starts, const float *ends,
+                                double *part, float *grad_decay, void *status, cudaStream_t st);
 
 }  // namespace sdm

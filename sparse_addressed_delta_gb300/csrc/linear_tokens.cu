@@ -48,65 +48,6 @@ __global__ void __launch_bounds__(kTokThreads) k_linear_tokens(LinearDims d, Lin
             if (i < K) p.last[state + i * p.sk] = S[i];
 }
 
-// The decay's gradient by carrying G = dS / dg along: G = e^g (G + S_before), and <do, scale G^T q> at every token
-template <typename T>
-__global__ void __launch_bounds__(kTokThreads) k_linear_decay(LinearDims d, LinearIn in, LinearOperand oq, LinearOperand ok, LinearOperand ov,
-                                                              LinearOperand og, const float *first, const float *final_grad, double *part) {
-    extern __shared__ float G[];                                   // [Dk][threads]
-    __shared__ float sq[kLinearMaxDk], sk[kLinearMaxDk];
-    __shared__ double sum[kTokThreads];
-    const int tid = threadIdx.x, col = blockIdx.x * kTokThreads + tid, h = (int)(blockIdx.y % d.H), b = (int)(blockIdx.y / d.H);
-    const bool mine = col < d.Dv;
-    const T *q = static_cast<const T *>(oq.p) + b * oq.s[0] + h / oq.share * oq.s[2];
-    const T *k = static_cast<const T *>(ok.p) + b * ok.s[0] + h / ok.share * ok.s[2];
-    const T *v = static_cast<const T *>(ov.p) + b * ov.s[0] + h / ov.share * ov.s[2] + col;
-    const T *g = static_cast<const T *>(og.p) + b * og.s[0] + h / og.share * og.s[2] + col;
-    const long long state = ((long long)b * d.H + h) * d.Dk * d.Dv + col;
-    const int n = linear_valid(in.valid, b, d.T);
-    const float fade = (float)linear_power(in.g[h], 1.0);
-    float S[kLinearMaxDk];
-#pragma unroll
-    for (int i = 0; i < kLinearMaxDk; ++i) {
-        S[i] = mine && i < d.Dk ? first[state + (long long)i * d.Dv] : 0.f;
-        if (i < d.Dk) G[i * kTokThreads + tid] = 0.f;
-    }
-    double acc = 0.0;
-    for (int t = 0; t < n; ++t) {
-        __syncthreads();
-        sq[tid] = tid < d.Dk ? to_f32(q[t * oq.s[1] + tid]) : 0.f;
-        sk[tid] = tid < d.Dk ? to_f32(k[t * ok.s[1] + tid]) : 0.f;
-        __syncthreads();
-        const float x = mine ? to_f32(v[t * ov.s[1]]) : 0.f, got = mine ? to_f32(g[t * og.s[1]]) : 0.f;
-        float s = 0.f;
-#pragma unroll
-        for (int r = 0; r < kLinearMaxDk; ++r)
-            if (r < d.Dk) {
-                const float a = fade * (G[r * kTokThreads + tid] + S[r]);
-                G[r * kTokThreads + tid] = a;
-                S[r] = fmaf(sk[r], x, fade * S[r]);
-                s = fmaf(sq[r], a, s);
-            }
-        acc += (double)(d.scale * s) * got;
-    }
-    if (final_grad && mine)
-        for (int r = 0; r < d.Dk; ++r) acc += (double)G[r * kTokThreads + tid] * final_grad[state + (long long)r * d.Dv];
-    sum[tid] = acc;
-    __syncthreads();
-    if (tid == 0) {
-        for (int i = 1; i < kTokThreads; ++i) acc += sum[i];
-        part[(long long)blockIdx.y * gridDim.x + blockIdx.x] = acc;
-    }
-}
-
-__global__ void k_linear_decay_sum(const double *part, int B, int H, int tiles, float *out) {
-    const int h = blockIdx.x * blockDim.x + threadIdx.x;
-    if (h >= H) return;
-    double s = 0.0;
-    for (int b = 0; b < B; ++b)
-        for (int i = 0; i < tiles; ++i) s += part[((long long)b * H + h) * tiles + i];
-    out[h] = (float)s;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_sum(const float *part, long long rows, int H, int group, int blocks, int width, T *out) {
     const int heads = H / group, pieces = width / 4;
@@ -139,22 +80,6 @@ cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks
     const unsigned grid = (unsigned)(want < 8 * kRefSms ? want : 8 * kRefSms);
     if (d.dtype == SDM_BF16) k_linear_sum<<<grid, 256, 0, st>>>(part, rows, d.H, d.H / d.Hk, blocks, width, static_cast<__nv_bfloat16 *>(out));
     else k_linear_sum<<<grid, 256, 0, st>>>(part, rows, d.H, d.H / d.Hk, blocks, width, static_cast<float *>(out));
-    return cudaGetLastError();
-}
-
-cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearOperand &q, const LinearOperand &k, const LinearOperand &v,
-                                const LinearOperand &grad, const float *first, const float *final_grad, double *part, float *grad_decay,
-                                cudaStream_t st) {
-    const int tiles = linear_tiles(d.Dv);
-    const size_t smem = (size_t)d.Dk * kTokThreads * 4;
-    auto go = [&](auto kern) {
-        set_kernel_smem(kern, smem);
-        kern<<<dim3(tiles, d.B * d.H), kTokThreads, smem, st>>>(d, in, q, k, v, grad, first, final_grad, part);
-        return cudaGetLastError();
-    };
-    const cudaError_t e = d.dtype == SDM_BF16 ? go(k_linear_decay<__nv_bfloat16>) : go(k_linear_decay<float>);
-    if (e != cudaSuccess) return e;
-    k_linear_decay_sum<<<(d.H + 63) / 64, 64, 0, st>>>(part, d.B, d.H, tiles, grad_decay);
     return cudaGetLastError();
 }
 
