@@ -481,8 +481,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
  * decays by the head's own factor at every token, the key writes its value, the query reads:
  *     S = exp(g) S + k v^T;  o = scale S^T q
  *   B  sequences, T  tokens (both may be 0), H  value heads, Hk  key heads (H a multiple of Hk: value head h
- *   reads key head h / (H / Hk)), B H at most 65535; Dk, Dv  head widths, multiples of 16, Dk up to 128 and Dv
- *   up to 512; dtype SDM_F32 or SDM_BF16 of q, k, v, the readings and their gradients; the state and the decays
+ *   reads key head h / (H / Hk)); Dk, Dv  head widths, multiples of 16, Dk up to 128 and Dv up to 512; dtype SDM_F32 or SDM_BF16 of q, k, v, the readings and their gradients; the state and the decays
  *   are float32. Strides are in elements, for (sequence, token, head); the last dimension is contiguous.
  *   Strides must be multiples of 16 bytes, addresses 16-byte aligned; a stride of 0 (a broadcast input) is fine.
  *
@@ -493,8 +492,8 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
  *   valid_tokens [B] int32, or NULL: all T. Tokens past it change nothing and none of their inputs
  *                is used; their readings (and gradients) are 0. Clamped to [0, T].
  *   readings     [B, T, H, Dv] contiguous, written whole
- *   workspace    sdm_linear_attention_workspace_bytes(shape) bytes, 256-byte aligned; it begins with a status
- *                block, as the gated delta rule's does
+ *   workspace    sdm_linear_attention_workspace_bytes(shape) bytes, 256-byte aligned; up to 8 tokens need none
+ *                (sdm_linear_attention only). It begins with a status block, as the gated delta rule's does
  * Deterministic. bfloat16 readings and gradients are float32 results, rounded once.
  * A NaN or infinity of an input reaches the readings and states that the recurrence carries it to, and no others.
  * The gradients of a sequence and key head that has one are undefined.
@@ -564,6 +563,38 @@ int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void 
                             int weight_dtype, const float *stats, int dtype, void *grad_x,
                             float *grad_weight, float *grad_bias, void *workspace,
                             size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Group norm with an activation over [N, L, C], channels last: a sample's group is its L positions and C / G
+ * neighbouring channels. float32 arithmetic, y rounded once:
+ *     z = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps);  y = z, or z / (1 + exp(-z))
+ *   x       N L positions of C contiguous elements (C up to 16384, a multiple of G), x_stride >= 0 elements apart, a
+ *           sample's one behind the other; dtype SDM_F32 or SDM_BF16; any alignment (groups that 16-byte pieces
+ *           divide are the fast ones). A token's heads are the groups of a sample of one position (L = 1).
+ *   weight, bias  [C] of weight_dtype (SDM_F32, or dtype), each may be NULL (1 and 0)
+ *   activation  SDM_ACT_NONE or SDM_ACT_SILU
+ *   y       [N, L, C] contiguous, dtype; may be x itself when x_stride is C
+ *   stats   [N, G, 2] float32 (mean, rstd) for the backward, or NULL; 8-byte aligned
+ *   workspace  sdm_group_norm_workspace_bytes(N, L, C, G) bytes, 256-byte aligned; may be NULL for L = 1 and groups of
+ *           up to 8192 channels
+ * N and L may be 0. Deterministic. */
+enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1 };
+size_t sdm_group_norm_workspace_bytes(long long N, long long L, int C, int G);
+int sdm_group_norm(const void *x, long long x_stride, long long N, long long L, int C, int G,
+                   const void *weight, const void *bias, int weight_dtype, float eps, int activation,
+                   int dtype, void *y, float *stats, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/* Its backward. grad: positions of C elements of dtype, grad_stride apart; weight, bias and activation as the
+ * forward's; stats as it stored them; grad_x [N, L, C] contiguous, dtype (may be grad itself when grad_stride is
+ * C); grad_weight and grad_bias [C] float32, summed over samples and positions in a fixed order, each may be NULL.
+ * workspace: sdm_group_norm_backward_workspace_bytes(N, L, C, G) bytes, 256-byte aligned. */
+size_t sdm_group_norm_backward_workspace_bytes(long long N, long long L, int C, int G);
+int sdm_group_norm_backward(const void *grad, long long grad_stride, const void *x, long long x_stride,
+                            long long N, long long L, int C, int G, const void *weight, const void *bias,
+                            int weight_dtype, int activation, const float *stats, int dtype, void *grad_x,
+                            float *grad_weight, float *grad_bias, void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /* Testing aid: the number of polls after which a kernel's bounded wait for its own bulk copies
  * gives up (default 2^22, seconds at most), for calls queued after this one, process-wide;

@@ -30,7 +30,7 @@ __all__ = ["FLAG_SNAPSHOT_BF16", "FLAG_SNAPSHOT_FP8", "FLAG_TOKEN_GATE", "FLAG_S
            "product_key_topk_backward", "gated_delta", "gated_delta_save",
            "gated_delta_backward", "linear_attention", "linear_attention_save",
            "linear_attention_backward", "layer_norm", "layer_norm_save",
-           "layer_norm_backward",
+           "layer_norm_backward", "group_norm", "group_norm_save", "group_norm_backward",
            "device_status", "SdmError", "Shape", "library", "library_path", "version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +39,7 @@ _calls_path = os.path.join(_HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFI
 
 SDM_F32, SDM_BF16 = 0, 1
 DELTA_STEP_TOKENS = 8             # gated_delta: up to this many tokens go one by one
+LINEAR_STEP_TOKENS = 8            # linear_attention: the same
 KERNEL_KINDS = ("phase1", "solve", "gather", "dualmm", "dw", "phase2")
 FLAG_PER_STEP_KERNELS = 1
 FLAG_SNAPSHOT_BF16 = 2
@@ -158,6 +159,12 @@ def library() -> ctypes.CDLL:
             for name in ("workspace", "saved", "backward_workspace"):
                 getattr(lib, f"sdm_linear_attention_{name}_bytes").argtypes = [vp]
                 getattr(lib, f"sdm_linear_attention_{name}_bytes").restype = sz
+            lib.sdm_group_norm.argtypes = [vp, ll, ll, ll, i32, i32, vp, vp, i32, ctypes.c_float, i32, i32, vp, vp, vp, sz, vp]
+            lib.sdm_group_norm_backward.argtypes = [vp, ll, vp, ll, ll, ll, i32, i32, vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]
+            for name in ("sdm_group_norm", "sdm_group_norm_backward"):
+                getattr(lib, name).restype = i32
+                getattr(lib, name + "_workspace_bytes").argtypes = [ll, ll, i32, i32]
+                getattr(lib, name + "_workspace_bytes").restype = sz
             lib.sdm_set_wait_limit.argtypes = [ctypes.c_longlong]
             lib.sdm_set_wait_limit.restype = ctypes.c_longlong
             lib.sdm_last_error.argtypes = []
@@ -966,8 +973,8 @@ def linear_attention(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     q, k [B, T, Hk, Dk] and v [B, T, H, Dv], float32 or bfloat16, any strides that are multiples of
     16 bytes; H a multiple of Hk (value head h uses key head h // (H // Hk)); Dk (up to 128) and Dv
     (up to 512) multiples of 16. log_decay [H] float32, 0 or below. valid_tokens [B] int32 (None:
-    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step. What is allocated
-    here belongs to ``stream`` (None: the current one). A wait that gives up is reported as
+    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step; up to 8 tokens need
+    no workspace. What is allocated here belongs to ``stream`` (None: the current one). A wait that gives up is reported as
     gated_delta's: in a ``workspace`` of the caller's."""
     if stream is not None:
         return _on(stream, linear_attention, state, q, k, v, log_decay, valid_tokens, scale=scale,
@@ -976,7 +983,8 @@ def linear_attention(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     shape, (B, T, H, Hk, Dk, Dv), dev, dt = _linear_shape(q, k, v, log_decay, valid_tokens, scale)
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
     readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
-    ws, n = _scratch(workspace, lib.sdm_linear_attention_workspace_bytes, dev, shape)
+    # short calls need no workspace; one that is given has its status block cleared
+    ws, n = (None, 0) if workspace is None and T <= LINEAR_STEP_TOKENS else _scratch(workspace, lib.sdm_linear_attention_workspace_bytes, dev, shape)
     _call(lib.sdm_linear_attention, dev, shape, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_decay.data_ptr(), _at(valid_tokens), readings.data_ptr(), _at(ws), n)
     return readings
@@ -1156,4 +1164,93 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: Optional[to
     _call(lib.sdm_layer_norm_backward, dev, grad.data_ptr(), gstep, x.data_ptr(), step, rows, n,
           _at(weight), wdt, stats.data_ptr(), code, out["grad_x"].data_ptr(), _at(out.get("grad_weight")),
           _at(out.get("grad_bias")), ws.data_ptr(), nbytes)
+    return out
+
+
+# ------------------------------------------------------------------------------------------
+# group norm with an activation, channels last
+# ------------------------------------------------------------------------------------------
+
+ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def _group_shape(x, groups, activation):
+    """(samples, positions, channels, stride between positions, activation's code) of x [N, ..., C]."""
+    rows, n, step = _norm_rows(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must be [N, ..., C]")
+    if not isinstance(groups, int) or groups < 1 or n % groups:
+        raise ValueError(f"groups must divide the {n} channels, got {groups}")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    N = x.shape[0]
+    return N, rows // N if N else 0, n, step, ACTIVATIONS[activation]
+
+
+def _group_norm(x, groups, weight, bias, activation, eps, out, stats, workspace):
+    N, L, C, step, act = _group_shape(x, groups, activation)
+    dt, dev = x.dtype, x.device
+    code = _dtype_code(dt)
+    wdt = _norm_params(x, C, weight, bias)
+    out = torch.empty(x.shape, dtype=dt, device=dev) if out is None else _result(out, "out", x.shape, dt, dev)
+    lib = library()
+    ws, n = (None, 0) if workspace is None and L == 1 and C // groups <= 8192 else _scratch(
+        workspace, lib.sdm_group_norm_workspace_bytes, dev, N, L, C, groups)
+    _call(lib.sdm_group_norm, dev, x.data_ptr(), step, N, L, C, groups, _at(weight), _at(bias), wdt, eps, act, code, out.data_ptr(),
+          _at(stats), _at(ws), n)
+    return out
+
+
+def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, *, activation: Optional[str] = None, eps: float = 1e-5,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Group norm of x [N, ..., C], channels last (up to 16384 of them): z = (x - mean) rstd weight + bias, the
+    statistics of a sample's group over all its positions and C / groups neighbouring channels; then y = z, or with
+    ``activation`` "silu" z / (1 + exp(-z)); in float32, rounded once to x's dtype (float32 or bfloat16). weight and
+    bias [C], float32 or x's dtype, each optional. The first dimension is the samples': a norm of every token's heads
+    takes [tokens, C] with the heads as groups. Positions may be strided; the result is contiguous. What is allocated
+    here belongs to ``stream`` (None: the current one)."""
+    if stream is not None:
+        return _on(stream, group_norm, x, groups, weight, bias, activation=activation, eps=eps, out=out, workspace=workspace)
+    return _group_norm(x, groups, weight, bias, activation, eps, out, None, workspace)
+
+
+def group_norm_save(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+                    bias: Optional[torch.Tensor] = None, *, activation: Optional[str] = None, eps: float = 1e-5,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """group_norm that also returns what its backward needs: (y, stats [N, groups, 2] float32)."""
+    if stream is not None:
+        return _on(stream, group_norm_save, x, groups, weight, bias, activation=activation, eps=eps, out=out, workspace=workspace)
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    if not isinstance(groups, int) or groups < 1:
+        raise ValueError(f"groups must divide the channels, got {groups}")
+    stats = torch.empty(x.shape[:1] + (groups, 2), dtype=torch.float32, device=x.device)
+    return _group_norm(x, groups, weight, bias, activation, eps, out, stats, workspace), stats
+
+
+def group_norm_backward(grad: torch.Tensor, x: torch.Tensor, groups: int, weight: Optional[torch.Tensor],
+                        bias: Optional[torch.Tensor], stats: torch.Tensor, *, activation: Optional[str] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """The backward after group_norm_save (same weight, bias and activation): a dict of grad_x (x's dtype) and, where
+    the forward had them, grad_weight and grad_bias, float32 [C], summed over samples and positions in a fixed order."""
+    if stream is not None:
+        return _on(stream, group_norm_backward, grad, x, groups, weight, bias, stats, activation=activation, workspace=workspace)
+    N, L, C, step, act = _group_shape(x, groups, activation)
+    gstep = _norm_rows(grad, "grad")[2]
+    dt, dev = x.dtype, x.device
+    if grad.shape != x.shape or grad.dtype is not dt or grad.device != dev:
+        raise ValueError("grad must have x's shape, dtype and device")
+    code = _dtype_code(dt)
+    wdt = _norm_params(x, C, weight, bias)
+    _need(stats, "stats", (N, groups, 2), torch.float32, dev)
+    out = {"grad_x": torch.empty(x.shape, dtype=dt, device=dev)}
+    if weight is not None:
+        out["grad_weight"] = torch.empty(C, dtype=torch.float32, device=dev)
+    if bias is not None:
+        out["grad_bias"] = torch.empty(C, dtype=torch.float32, device=dev)
+    lib = library()
+    ws, nbytes = _scratch(workspace, lib.sdm_group_norm_backward_workspace_bytes, dev, N, L, C, groups)
+    _call(lib.sdm_group_norm_backward, dev, grad.data_ptr(), gstep, x.data_ptr(), step, N, L, C, groups, _at(weight), _at(bias), wdt, act,
+          stats.data_ptr(), code, out["grad_x"].data_ptr(), _at(out.get("grad_weight")), _at(out.get("grad_bias")), ws.data_ptr(), nbytes)
     return out

@@ -1,0 +1,762 @@
+// Group norm with an activation over [N, L, C], channels last: the statistics of a sample's group are over its L
+// positions and C / G channels.
+//   mean, rstd of the group;  xhat = (x - mean) rstd;  z = xhat w + b;  y = z, or z / (1 + e^-z)
+//   dz = dy act'(z);  dx = rstd (w dz - mean(w dz) - xhat mean(w dz xhat));  dw = sum dz xhat;  db = sum dz
+// All arithmetic is float32; y and dx are rounded once.
+//
+// Two forms. One position a sample (a token's heads): a group is a row of C / G elements, kept in registers, read
+// once (k_group_row*): a row belongs to a part of a warp or to a block, blocks walk over the samples with a stride
+// that keeps every thread at its group, so weights and column sums stay in registers. More positions, or rows past
+// the registers: a sample's positions are split over blocks, each thread at its channels; a first launch makes every
+// split's statistics (or column sums), the second joins them and reads the rows again, from L2 where they fit.
+#include <type_traits>
+
+#include "norm_rows.cuh"
+
+namespace sdm {
+namespace {
+
+constexpr int kGroupThreads = 256, kGroupBatch = 8, kGroupMaxCols = 16384, kGroupRowCols = 8192;
+
+// The sigmoid. bfloat16: by the approximate exponential and reciprocal instructions, within 2^-20 of it where it is not
+// negligible, far inside the results' rounding of 2^-9; the exact ones would bound the kernel (25 instructions an
+// element). An infinite e^-z makes 0 of both.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (sizeof(T) == 2) {
+        float e, p;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504089f * z));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
+        return p;
+    } else {
+        return 1.f / (1.f + expf(-z));
+    }
+}
+template <typename T, bool ACT>
+__device__ __forceinline__ float activate(float z) {
+    return ACT ? z * sigmoid<T>(z) : z;
+}
+// dy times the activation's slope at z
+template <typename T, bool ACT>
+__device__ __forceinline__ float back(float dy, float z) {
+    if constexpr (!ACT) return dy;
+    const float p = sigmoid<T>(z);
+    return dy * (p * fmaf(z, 1.f - p, 1.f));
+}
+
+// mean and sum of squares around it of nb values joined to those of n
+struct Moments {
+    float n, mean, m2;
+    __device__ __forceinline__ void join(float nb, float mb, float qb) {
+        const float all = n + nb;
+        if (nb == 0.f) return;
+        if (n == 0.f) {                                  // (0 times a difference's square, which may be infinite)
+            *this = Moments{nb, mb, qb};
+            return;
+        }
+        const float d = mb - mean, f = nb / all;
+        mean = fmaf(d, f, mean);
+        m2 += fmaf(d * d, n * f, qb);
+        n = all;
+    }
+    template <int LANES>
+    __device__ __forceinline__ void join_lanes() {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            const float nb = __shfl_xor_sync(~0u, n, o), mb = __shfl_xor_sync(~0u, mean, o), qb = __shfl_xor_sync(~0u, m2, o);
+            // both halves of a pair join in the same order, so that all lanes agree
+            Moments a = threadIdx.x & o ? Moments{nb, mb, qb} : *this;
+            const Moments c = threadIdx.x & o ? *this : Moments{nb, mb, qb};
+            a.join(c.n, c.mean, c.m2);
+            *this = a;
+        }
+    }
+};
+
+struct GroupShape {
+    long long N, L, xs, gs;              // samples, positions, elements between positions of x and of the gradient
+    int C, G, splits;
+    bool wf32;
+    float eps;
+    const void *w, *b;
+};
+
+// ---- one position a sample ----------------------------------------------------------------------
+
+template <typename T, int VEC, int NV, bool BLOCK, bool ACT>
+__global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
+    k_group_row(const __grid_constant__ GroupShape s, const T *x, int tpr, T *y, float2 *stats) {
+    constexpr int E = VEC * NV, ST = kNormStages<T>;
+    extern __shared__ __align__(16) unsigned char ring_smem[];
+    __shared__ float red[2 * 2 * 32];
+    int turn = 0;
+    const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr, rpb = BLOCK ? 1 : kNormBlock / tpr;
+    const int c = s.C / s.G;
+    const long long row0 = (long long)blockIdx.x * rpb + sub, step = (long long)gridDim.x * rpb / s.G;   // (a multiple of G)
+    const int g = (int)(row0 % s.G);
+    long long n = row0 / s.G;
+    float wv[E], bv[E];
+    const size_t at = (size_t)g * c, ws = s.wf32 ? 4 : sizeof(T);
+    load_cols<T, VEC, NV>(s.w ? static_cast<const char *>(s.w) + at * ws : nullptr, s.wf32, 1.f, t, tpr, c, wv);
+    load_cols<T, VEC, NV>(s.b ? static_cast<const char *>(s.b) + at * ws : nullptr, s.wf32, 0.f, t, tpr, c, bv);
+    const RowRing<T, VEC, NV, 1, false, false> ring{ring_smem, t, tpr, c, sub, rpb};
+    auto fetch = [&](int stage, long long i) {
+        ring.fetch(stage, 0, x + (i < s.N ? i : 0) * s.xs + at, i < s.N);
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(i, n + i * step);
+    // all threads of a block make as many turns: its first sample is in the first row's
+    for (long long first = (long long)blockIdx.x * rpb / s.G, stage = 0; first < s.N; first += step, n += step, stage = (stage + 1) % ST) {
+        fetch((int)(stage + ST - 1) % ST, n + (ST - 1) * step);
+        cp_async_wait<ST - 1>();
+        float v[E], sum[1] = {0.f};
+        ring.read((int)stage, 0, nullptr, v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) sum[0] += v[j];
+        row_sum<BLOCK, 1>(sum, tpr, red, turn);
+        const float mean = sum[0] / (float)c;
+        float q[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                v[i * VEC + j] -= mean;
+                if ((i * tpr + t) * VEC < c) q[0] = fmaf(v[i * VEC + j], v[i * VEC + j], q[0]);
+            }
+        row_sum<BLOCK, 1>(q, tpr, red, turn);
+        const float rstd = 1.f / sqrtf(q[0] / (float)c + s.eps);
+        if (n < s.N) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = activate<T, ACT>(fmaf(v[j] * rstd, wv[j], bv[j]));
+            store_row<T, VEC, NV>(y + n * s.C + at, t, tpr, c, v);
+            if (stats && t == 0) stats[n * s.G + g] = make_float2(mean, rstd);
+        }
+    }
+}
+
+// part [..][2][C]: column sums of dz xhat and of dz, of a block (same) or of each of its rows
+template <typename T, int VEC, int NV, bool BLOCK, bool ACT>
+__global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
+    k_group_row_bwd(const __grid_constant__ GroupShape s, const T *dy, const T *x, int tpr, bool same, const float2 *stats, T *dx, float *part) {
+    constexpr int E = VEC * NV, ST = kNormStages<T>;
+    extern __shared__ __align__(16) unsigned char ring_smem[];
+    __shared__ float red[2 * 2 * 32];
+    int turn = 0;
+    const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr, rpb = BLOCK ? 1 : kNormBlock / tpr;
+    const int c = s.C / s.G;
+    // a block's rows are one group's of several samples, so that it adds their column sums itself; fewer samples than
+    // that: as in the forward
+    const long long row0 = (long long)blockIdx.x * rpb + sub, step = (long long)gridDim.x * rpb / s.G;
+    const long long first0 = same ? (long long)(blockIdx.x / s.G) * rpb : (long long)blockIdx.x * rpb / s.G;
+    const int g = (int)(same ? blockIdx.x % s.G : row0 % s.G);
+    long long n = same ? first0 + sub : row0 / s.G;
+    float wv[E], bv[ACT ? E : 1], aw[E], ab[E];
+    const size_t at = (size_t)g * c, ws = s.wf32 ? 4 : sizeof(T);
+    load_cols<T, VEC, NV>(s.w ? static_cast<const char *>(s.w) + at * ws : nullptr, s.wf32, 1.f, t, tpr, c, wv);
+    if constexpr (ACT) load_cols<T, VEC, NV>(s.b ? static_cast<const char *>(s.b) + at * ws : nullptr, s.wf32, 0.f, t, tpr, c, bv);
+#pragma unroll
+    for (int j = 0; j < E; ++j) aw[j] = ab[j] = 0.f;
+    const RowRing<T, VEC, NV, 2, true, false> ring{ring_smem, t, tpr, c, sub, rpb};
+    auto fetch = [&](int stage, long long i) {
+        const bool live = i < s.N;
+        const long long m = live ? i : 0;
+        ring.fetch(stage, 0, x + m * s.xs + at, live);
+        ring.fetch(stage, 1, dy + m * s.gs + at, live);
+        ring.fetch_stats(stage, stats + m * s.G + g, live);
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(i, n + i * step);
+    for (long long first = first0, stage = 0; first < s.N; first += step, n += step, stage = (stage + 1) % ST) {
+        fetch((int)(stage + ST - 1) % ST, n + (ST - 1) * step);
+        cp_async_wait<ST - 1>();
+        const float2 ns = *reinterpret_cast<const float2 *>(ring.stats_at((int)stage));
+        float h[E], d[E], sum[2] = {0.f, 0.f};
+        ring.read((int)stage, 0, nullptr, h);
+        ring.read((int)stage, 1, nullptr, d);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            // past the row's end x and dy are 0, and dy = 0 keeps the sums clean
+            h[j] = (h[j] - ns.x) * ns.y;
+            if constexpr (ACT) d[j] = back<T, ACT>(d[j], fmaf(h[j], wv[j], bv[j]));
+            aw[j] = fmaf(d[j], h[j], aw[j]);
+            ab[j] += d[j];
+            d[j] *= wv[j];
+            sum[0] += d[j];
+            sum[1] = fmaf(d[j], h[j], sum[1]);
+        }
+        row_sum<BLOCK, 2>(sum, tpr, red, turn);
+        const float c1 = sum[0] / (float)c, c2 = sum[1] / (float)c;
+        if (n < s.N) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) d[j] = ns.y * (d[j] - c1 - h[j] * c2);
+            store_row<T, VEC, NV>(dx + n * s.C + at, t, tpr, c, d);
+        }
+    }
+    if (!part) return;
+    cp_async_wait<0>();
+    if (!BLOCK && same) {
+        // the block's rows, added in their order: cols [2][rows][tpr E]
+        __syncthreads();
+        float *cols = reinterpret_cast<float *>(ring_smem);
+        const int wide = tpr * E;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int col = (i * tpr + t) * VEC + j;
+                cols[sub * wide + col] = aw[i * VEC + j];
+                cols[(rpb + sub) * wide + col] = ab[i * VEC + j];
+            }
+        __syncthreads();
+        float *out = part + (size_t)(blockIdx.x / s.G) * 2 * s.C + at;
+        for (int col = threadIdx.x; col < c; col += kNormBlock) {
+            float a = 0.f, b = 0.f;
+            for (int r = 0; r < rpb; ++r) {
+                a += cols[r * wide + col];
+                b += cols[(rpb + r) * wide + col];
+            }
+            out[col] = a;
+            out[s.C + col] = b;
+        }
+        return;
+    }
+    float *out = part + (size_t)(row0 / s.G) * 2 * s.C + at;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const int col = (i * tpr + t) * VEC + j;
+            if (col < c) {
+                out[col] = aw[i * VEC + j];
+                out[s.C + col] = ab[i * VEC + j];
+            }
+        }
+}
+
+// ---- positions split over blocks ----------------------------------------------------------------
+
+// A block's threads over a [positions][C] tile: CV = C / VEC vectors a position; up to kGroupThreads of them are taken
+// side by side, with several positions (slots) where there are fewer.
+struct Spread {
+    int cv, slots;
+    __device__ Spread(int C, int vec) : cv(C / vec), slots(cv < kGroupThreads ? kGroupThreads / cv : 1) {}
+};
+// this block's sample and positions
+struct Piece {
+    long long n, from, to;
+    int split;
+    __device__ explicit Piece(const GroupShape &s) {
+        split = (int)(blockIdx.x % s.splits);
+        n = blockIdx.x / s.splits;
+        from = s.L * split / s.splits;
+        to = s.L * (split + 1) / s.splits;
+    }
+};
+
+// part [N][splits][G]: mean and sum of squares around it
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kGroupThreads) k_group_stats(const __grid_constant__ GroupShape s, const T *x, float2 *part) {
+    extern __shared__ float2 acc[];                      // [slots][cv]
+    const Piece p(s);
+    const Spread sp(s.C, VEC);
+    const int slot = threadIdx.x / sp.cv < sp.slots ? threadIdx.x / sp.cv : -1;
+    const T *base = x + p.n * s.L * s.xs;
+    for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += kGroupThreads) {
+        Moments m{0.f, 0.f, 0.f};
+        if (slot >= 0 || sp.slots == 1) {
+            const T *col = base + cv * VEC;
+            for (long long r = p.from + (sp.slots > 1 ? slot : 0); r < p.to; r += (long long)sp.slots * kGroupBatch) {
+                float v[kGroupBatch][VEC], sum = 0.f, q = 0.f, count = 0.f;
+#pragma unroll
+                for (int i = 0; i < kGroupBatch; ++i) {
+                    const long long at = r + (long long)i * sp.slots;
+                    Vec<T, VEC> raw{};
+                    if (at < p.to) {
+                        raw = __ldg(reinterpret_cast<const Vec<T, VEC> *>(col + at * s.xs));
+                        count += VEC;
+                    }
+                    unpack<T, VEC>(raw, v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kGroupBatch; ++i)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) sum += v[i][j];
+                const float mean = sum / count;
+#pragma unroll
+                for (int i = 0; i < kGroupBatch; ++i)
+                    if (r + (long long)i * sp.slots < p.to)
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) {
+                            const float d = v[i][j] - mean;
+                            q = fmaf(d, d, q);
+                        }
+                m.join(count, mean, q);
+            }
+        }
+        if (slot >= 0 || sp.slots == 1) acc[(sp.slots > 1 ? slot : 0) * sp.cv + cv] = make_float2(m.mean, m.m2);
+        if (sp.slots > 1) break;
+    }
+    __syncthreads();
+    const int each = sp.cv / s.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int g = warp; g < s.G; g += kGroupThreads / 32) {
+        Moments m{0.f, 0.f, 0.f};
+        for (int i = lane; i < each * sp.slots; i += 32) {
+            const int sl = i / each;
+            const float2 a = acc[sl * sp.cv + g * each + i % each];
+            const long long rows = p.to - p.from - sl;
+            m.join((float)((rows > 0 ? (rows + sp.slots - 1) / sp.slots : 0) * VEC), a.x, a.y);
+        }
+        m.join_lanes<32>();
+        if (lane == 0) part[((size_t)p.n * s.splits + p.split) * s.G + g] = make_float2(m.mean, m.m2);
+    }
+}
+
+// the group's statistics from its splits', by 8 lanes
+__device__ __forceinline__ float2 group_join(const GroupShape &s, const float2 *part, long long n, int g) {
+    const float c = (float)(s.C / s.G);
+    Moments m{0.f, 0.f, 0.f};
+    if (g < s.G)
+        for (int i = threadIdx.x & 7; i < s.splits; i += 8) {
+            const float2 a = __ldg(part + ((size_t)n * s.splits + i) * s.G + g);
+            m.join((float)(s.L * (i + 1) / s.splits - s.L * i / s.splits) * c, a.x, a.y);
+        }
+    m.join_lanes<8>();
+    return make_float2(m.mean, 1.f / sqrtf(m.m2 / ((float)s.L * c) + s.eps));
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_params(const void *p, bool f32, float fill, int c0, float (&o)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+        o[j] = !p ? fill : f32 ? static_cast<const float *>(p)[c0 + j] : to_f32(static_cast<const T *>(p)[c0 + j]);
+}
+
+template <typename T, int VEC, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads)
+    k_group_apply(const __grid_constant__ GroupShape s, const T *x, const float2 *part, T *y, float2 *stats) {
+    extern __shared__ float2 norm[];                     // [G] mean, rstd
+    const Piece p(s);
+    const Spread sp(s.C, VEC);
+    const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
+    const T *base = x + p.n * s.L * s.xs;
+    T *out = y + p.n * s.L * s.C;
+    const int cv0 = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x, wide = sp.slots > 1 ? sp.cv : kGroupThreads;
+    const bool here = slot < sp.slots && cv0 < sp.cv;
+    Vec<T, VEC> raw[kGroupBatch];
+    auto fetch = [&](long long r, int c0) {
+#pragma unroll
+        for (int i = 0; i < kGroupBatch; ++i) {
+            const long long at = r + (long long)i * sp.slots;
+            if (at < p.to) raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0));
+        }
+    };
+    if (here) fetch(p.from + slot, cv0 * VEC);           // in the statistics' time
+    for (int g0 = 0; g0 < s.G; g0 += kGroupThreads / 8) {
+        const int g = g0 + (threadIdx.x >> 3);
+        const float2 a = group_join(s, part, p.n, g);
+        if ((threadIdx.x & 7) == 0 && g < s.G) {
+            norm[g] = a;
+            if (stats && p.split == 0) stats[p.n * s.G + g] = a;
+        }
+    }
+    __syncthreads();
+    if (!here) return;
+    for (int cv = cv0; cv < sp.cv; cv += wide) {
+        const int c0 = cv * VEC;
+        const float2 a = norm[c0 / each];
+        float w[VEC], b[VEC];
+        load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
+        load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
+        if (cv != cv0) fetch(p.from + slot, c0);
+        for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * kGroupBatch) {
+#pragma unroll
+            for (int i = 0; i < kGroupBatch; ++i) {
+                const long long at = r + (long long)i * sp.slots;
+                if (at >= p.to) continue;
+                float v[VEC];
+                unpack<T, VEC>(raw[i], v);
+                const long long next = at + (long long)sp.slots * kGroupBatch;
+                if (next < p.to) raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + next * s.xs + c0));
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[j] = activate<T, ACT>(fmaf((v[j] - a.x) * a.y, w[j], b[j]));
+                store_vec<T, VEC>(out + at * s.C + c0, v);
+            }
+        }
+    }
+}
+
+// part [N][splits][2][C]: column sums of dz xhat and of dz
+template <typename T, int VEC, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads)
+    k_group_sums(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, float *part) {
+    extern __shared__ float sums[];                      // [slots][2][C] where there are several
+    const Piece p(s);
+    const Spread sp(s.C, VEC);
+    const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
+    const T *base = x + p.n * s.L * s.xs, *gbase = dy + p.n * s.L * s.gs;
+    float *out = part + ((size_t)p.n * s.splits + p.split) * 2 * s.C;
+    if (slot < sp.slots)
+        for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += sp.slots > 1 ? sp.cv : kGroupThreads) {
+            const int c0 = cv * VEC;
+            const float2 a = stats[p.n * s.G + c0 / each];
+            float w[VEC], b[VEC], sw[VEC], sb[VEC];
+            load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
+            load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sw[j] = sb[j] = 0.f;
+            constexpr int BATCH = kGroupBatch / 2;
+            for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * BATCH) {
+                Vec<T, VEC> rx[BATCH], rg[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const long long at = r + (long long)i * sp.slots;
+                    rx[i] = rg[i] = Vec<T, VEC>{};
+                    if (at < p.to) {
+                        rx[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0));
+                        rg[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(gbase + at * s.gs + c0));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    float h[VEC], d[VEC];
+                    unpack<T, VEC>(rx[i], h);
+                    unpack<T, VEC>(rg[i], d);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {      // where no position is, dy is 0
+                        h[j] = (h[j] - a.x) * a.y;
+                        d[j] = back<T, ACT>(d[j], fmaf(h[j], w[j], b[j]));
+                        sw[j] = fmaf(d[j], h[j], sw[j]);
+                        sb[j] += d[j];
+                    }
+                }
+            }
+            float *to = sp.slots > 1 ? sums + (size_t)slot * 2 * s.C : out;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                to[c0 + j] = sw[j];
+                to[s.C + c0 + j] = sb[j];
+            }
+        }
+    if (sp.slots == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * s.C; c += kGroupThreads) {
+        float t = 0.f;
+        for (int i = 0; i < sp.slots; ++i) t += sums[(size_t)i * 2 * s.C + c];
+        out[c] = t;
+    }
+}
+
+// terms [N][G]: means over the group of w dz and of w dz xhat; a warp a group
+template <typename T>
+__global__ void __launch_bounds__(kGroupThreads) k_group_terms(const __grid_constant__ GroupShape s, const float *part, float2 *terms) {
+    const long long i = (long long)blockIdx.x * (kGroupThreads / 32) + (threadIdx.x >> 5);
+    if (i >= s.N * s.G) return;
+    const int lane = threadIdx.x & 31, g = (int)(i % s.G), each = s.C / s.G;
+    const long long n = i / s.G;
+    double a = 0.0, b = 0.0;
+#pragma unroll 4
+    for (int e = lane; e < s.splits * each; e += 32) {
+        const int c = g * each + e % each;
+        float w[1];
+        load_params<T, 1>(s.w, s.wf32, 1.f, c, w);
+        const float *at = part + ((size_t)n * s.splits + e / each) * 2 * s.C + c;
+        a += (double)at[s.C] * w[0];
+        b += (double)at[0] * w[0];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(~0u, a, o);
+        b += __shfl_xor_sync(~0u, b, o);
+    }
+    const double count = (double)s.L * each;
+    if (lane == 0) terms[i] = make_float2((float)(a / count), (float)(b / count));
+}
+
+template <typename T, int VEC, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads)
+    k_group_apply_bwd(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, const float2 *terms, T *dx) {
+    const Piece p(s);
+    const Spread sp(s.C, VEC);
+    const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
+    if (slot >= sp.slots) return;
+    const T *base = x + p.n * s.L * s.xs, *gbase = dy + p.n * s.L * s.gs;
+    T *out = dx + p.n * s.L * s.C;
+    for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += sp.slots > 1 ? sp.cv : kGroupThreads) {
+        const int c0 = cv * VEC;
+        const float2 a = stats[p.n * s.G + c0 / each], m = terms[p.n * s.G + c0 / each];
+        float w[VEC], b[VEC];
+        load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
+        load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
+        constexpr int BATCH = kGroupBatch / 2;
+        for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * BATCH) {
+            Vec<T, VEC> rx[BATCH], rg[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const long long at = r + (long long)i * sp.slots;
+                if (at < p.to) {
+                    rx[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0));
+                    rg[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(gbase + at * s.gs + c0));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const long long at = r + (long long)i * sp.slots;
+                if (at >= p.to) continue;
+                float h[VEC], d[VEC];
+                unpack<T, VEC>(rx[i], h);
+                unpack<T, VEC>(rg[i], d);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    h[j] = (h[j] - a.x) * a.y;
+                    d[j] = back<T, ACT>(d[j], fmaf(h[j], w[j], b[j])) * w[j];
+                    d[j] = a.y * (d[j] - m.x - h[j] * m.y);
+                }
+                store_vec<T, VEC>(out + at * s.C + c0, d);
+            }
+        }
+    }
+}
+
+// ---- which form, and its launches ---------------------------------------------------------------
+
+// blocks of a sample: enough of them for the card, 16 positions at least each
+int group_splits(long long N, long long L) {
+    const long long want = 4LL * kRefSms / (N ? N : 1), most = L / 16;
+    const long long s = want < most ? want : most;
+    return s < 1 ? 1 : s > 256 ? 256 : (int)s;
+}
+
+// The rows' blocks: a multiple of as many as make their rows at once a multiple of G, at most `most` where that allows it
+long long group_grid(long long rows, int rpb, int G, long long most) {
+    int a = rpb, b = G;
+    while (b) {
+        const int r = a % b;
+        a = b;
+        b = r;
+    }
+    const long long unit = G / a, need = ((rows + rpb - 1) / rpb + unit - 1) / unit, fit = most / unit;
+    return unit * (need < fit ? need : fit > 1 ? fit : 1);
+}
+
+bool group_rows(long long L, int each) { return L == 1 && each <= kGroupRowCols; }
+
+// the backward's blocks over rows, and how many partials of the column sums they leave
+struct GroupBack {
+    bool same;
+    long long blocks, parts;
+};
+GroupBack group_back(const NormGeom &g, long long N, int G) {
+    const int per_sm = g.threads >= 512 ? 1 : 512 / g.threads;
+    const long long few = N * G / g.rpb / kNormRowsBlock;
+    const long long fill = (long long)kRefSms * per_sm, most = few > kRefSms ? few : kRefSms, cap = fill < most ? fill : most;
+    if (N < g.rpb) {
+        const long long blocks = group_grid(N * G, g.rpb, G, cap);
+        return {false, blocks, blocks * g.rpb / G};
+    }
+    const long long need = (N + g.rpb - 1) / g.rpb, fit = cap / G, parts = need < fit ? need : fit > 1 ? fit : 1;
+    return {true, parts * G, parts};
+}
+
+template <typename T, typename F>
+void group_by_vec(int vec, F f) {
+    constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
+    if (vec == V16) return f(std::integral_constant<int, V16>{});
+    if constexpr (V4 > 1)
+        if (vec == V4) return f(std::integral_constant<int, V4>{});
+    f(std::integral_constant<int, 1>{});
+}
+
+template <typename T, bool ACT>
+void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, int vec, cudaStream_t st) {
+    const int each = s.C / s.G;
+    group_by_vec<T>(vec, [&](auto v) {
+        constexpr int VEC = decltype(v)::value;
+        if (group_rows(s.L, each)) {
+            const NormGeom g = norm_geom(each, VEC, true);
+            constexpr int NV = 16 / VEC;
+            const size_t smem = kNormStages<T> * RowRing<T, VEC, NV, 1, false, false>::stage_bytes(each, g.threads, g.rpb);
+            auto go = [&](auto kern) {
+                set_kernel_smem(kern, smem);
+                int per_sm = 1;
+                if (s.N * s.G > (long long)kRefSms * g.rpb) cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, g.threads, smem);
+                const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (per_sm > 1 ? per_sm : 1));
+                kern<<<(unsigned)grid, g.threads, smem, st>>>(s, x, g.tpr, y, stats);
+            };
+            if (g.block) go(k_group_row<T, VEC, NV, true, ACT>);
+            else go(k_group_row<T, VEC, NV, false, ACT>);
+            return;
+        }
+        const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+        const unsigned grid = (unsigned)(s.N * s.splits);
+        const size_t smem = (size_t)slots * cv * 8;
+        set_kernel_smem(k_group_stats<T, VEC>, smem);
+        k_group_stats<T, VEC><<<grid, kGroupThreads, smem, st>>>(s, x, part);
+        set_kernel_smem(k_group_apply<T, VEC, ACT>, s.G * 8);
+        k_group_apply<T, VEC, ACT><<<grid, kGroupThreads, s.G * 8, st>>>(s, x, part, y, stats);
+    });
+}
+
+// returns the partials of the column sums
+template <typename T, bool ACT>
+long long group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, bool sums, float *part, float2 *terms, int vec,
+                         cudaStream_t st) {
+    const int each = s.C / s.G;
+    long long parts = 0;
+    group_by_vec<T>(vec, [&](auto v) {
+        constexpr int VEC = decltype(v)::value;
+        if (group_rows(s.L, each)) {
+            const NormGeom g = norm_geom(each, VEC, true);
+            constexpr int NV = 16 / VEC;
+            const size_t smem = kNormStages<T> * RowRing<T, VEC, NV, 2, true, false>::stage_bytes(each, g.threads, g.rpb);
+            const GroupBack to = group_back(g, s.N, s.G);
+            const size_t cols = g.block ? 0 : (size_t)2 * kNormBlock * 16 * 4;
+            auto go = [&](auto kern) {
+                const size_t bytes = smem > cols ? smem : cols;
+                set_kernel_smem(kern, bytes);
+                kern<<<(unsigned)to.blocks, g.threads, bytes, st>>>(s, dy, x, g.tpr, to.same, stats, dx, sums ? part : nullptr);
+            };
+            if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>);
+            else go(k_group_row_bwd<T, VEC, NV, false, ACT>);
+            parts = to.parts;
+            return;
+        }
+        const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+        const unsigned grid = (unsigned)(s.N * s.splits);
+        const size_t smem = slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0;
+        set_kernel_smem(k_group_sums<T, VEC, ACT>, smem);
+        k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, part);
+        const long long warps = s.N * s.G;
+        k_group_terms<T><<<(unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st>>>(s, part, terms);
+        k_group_apply_bwd<T, VEC, ACT><<<grid, kGroupThreads, 0, st>>>(s, dy, x, stats, terms, dx);
+        parts = s.N * s.splits;
+    });
+    return parts;
+}
+
+int group_check(const char *what, long long N, long long L, int C, int G, long long xs, int wdtype, int act, int dtype) {
+    if (dtype != SDM_F32 && dtype != SDM_BF16) return set_error(SDM_ERR_INVALID, "%s: dtype must be SDM_F32 or SDM_BF16", what);
+    if (wdtype != SDM_F32 && wdtype != dtype)
+        return set_error(SDM_ERR_INVALID, "%s: the weight's dtype must be SDM_F32 or the channels'", what);
+    if (act != SDM_ACT_NONE && act != SDM_ACT_SILU) return set_error(SDM_ERR_INVALID, "%s: unknown activation %d", what, act);
+    if (N < 0 || L < 0 || C < 1 || G < 1 || C % G || xs < 0)
+        return set_error(SDM_ERR_INVALID, "%s: N and L must be >= 0, C a multiple of G >= 1 and the stride >= 0, got %lld, %lld, %d, %d, %lld",
+                         what, N, L, C, G, xs);
+    if (C > kGroupMaxCols) return set_error(SDM_ERR_UNSUPPORTED, "%s: at most %d channels, got %d", what, kGroupMaxCols, C);
+    if (N > (1LL << 31) / 256 || L >= (1LL << 31) || N * G >= (1LL << 31))
+        return set_error(SDM_ERR_UNSUPPORTED, "%s: N must be at most 2^23, N G and L below 2^31", what);
+    return SDM_OK;
+}
+
+// the parts of a workspace: partials, then (a backward of split positions) the groups' terms
+size_t group_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+size_t group_part_bytes(long long N, long long L, int C, int G, bool back) {
+    if (group_rows(L, C / G)) {
+        if (!back) return 0;
+        // every vector width has the same blocks
+        const NormGeom g = norm_geom(C / G, 1, true);
+        return group_up((size_t)group_back(g, N, G).parts * 2 * C * 4);
+    }
+    const size_t pieces = (size_t)N * group_splits(N, L);
+    return group_up(pieces * (back ? (size_t)2 * C * 4 : (size_t)G * 8));
+}
+size_t group_bytes(long long N, long long L, int C, int G, bool back) {
+    return group_part_bytes(N, L, C, G, back) + (back && !group_rows(L, C / G) ? group_up((size_t)N * G * 8) : 0) + kAlign;
+}
+
+int group_check_ws(const char *what, const void *ws, size_t have, size_t need) {
+    if (!ws || have < need || (uintptr_t)ws % kAlign)
+        return set_error(SDM_ERR_WORKSPACE, "%s: workspace NULL, too small (%zu of %zu bytes) or not %zu-byte aligned", what, have, need, (size_t)kAlign);
+    return SDM_OK;
+}
+
+int group_status(const char *what, cudaError_t e) {
+    return e == cudaSuccess ? SDM_OK : set_error(SDM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" {
+
+size_t sdm_group_norm_workspace_bytes(long long N, long long L, int C, int G) {
+    if (group_check("group norm", N, L, C, G, 0, SDM_F32, SDM_ACT_NONE, SDM_F32) != SDM_OK) return 0;
+    return group_bytes(N, L, C, G, false);
+}
+
+int sdm_group_norm(const void *x, long long x_stride, long long N, long long L, int C, int G, const void *weight, const void *bias,
+                   int weight_dtype, float eps, int activation, int dtype, void *y, float *stats, void *workspace, size_t workspace_bytes,
+                   void *stream) {
+    const char *what = "group norm";
+    int rc = group_check(what, N, L, C, G, x_stride, weight_dtype, activation, dtype);
+    if (rc != SDM_OK) return rc;
+    if (!(eps >= 0.f)) return set_error(SDM_ERR_INVALID, "group norm: eps must be >= 0");
+    if (N == 0 || L == 0) return SDM_OK;
+    if (!x || !y) return set_error(SDM_ERR_INVALID, "group norm: NULL pointer");
+    if ((uintptr_t)stats % 8) return set_error(SDM_ERR_INVALID, "group norm: stats must be 8-byte aligned");
+    if (!group_rows(L, C / G)) {
+        rc = group_check_ws(what, workspace, workspace_bytes, group_bytes(N, L, C, G, false) - kAlign);
+        if (rc != SDM_OK) return rc;
+    }
+    const GroupShape s{N, L, x_stride, 0, C, G, group_splits(N, L), weight_dtype == SDM_F32, eps, weight, bias};
+    const int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, C, x, y, y);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto type, auto act) {
+        using T = decltype(type);
+        group_forward<T, decltype(act)::value>(s, static_cast<const T *>(x), static_cast<T *>(y), reinterpret_cast<float2 *>(stats),
+                                               static_cast<float2 *>(workspace), vec, st);
+    };
+    const bool silu = activation == SDM_ACT_SILU;
+    if (dtype == SDM_BF16) silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});
+    else silu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
+    return group_status(what, cudaGetLastError());
+}
+
+size_t sdm_group_norm_backward_workspace_bytes(long long N, long long L, int C, int G) {
+    if (group_check("group norm backward", N, L, C, G, 0, SDM_F32, SDM_ACT_NONE, SDM_F32) != SDM_OK) return 0;
+    return group_bytes(N, L, C, G, true);
+}
+
+int sdm_group_norm_backward(const void *grad, long long grad_stride, const void *x, long long x_stride, long long N, long long L, int C, int G,
+                            const void *weight, const void *bias, int weight_dtype, int activation, const float *stats, int dtype, void *grad_x,
+                            float *grad_weight, float *grad_bias, void *workspace, size_t workspace_bytes, void *stream) {
+    const char *what = "group norm backward";
+    int rc = group_check(what, N, L, C, G, x_stride, weight_dtype, activation, dtype);
+    if (rc != SDM_OK) return rc;
+    if (grad_stride < 0) return set_error(SDM_ERR_INVALID, "group norm backward: the gradient's stride must be >= 0, got %lld", grad_stride);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool sums = grad_weight || grad_bias, rows = group_rows(L, C / G);
+    if (N == 0 || L == 0) {
+        cudaError_t e = cudaSuccess;
+        if (grad_weight) e = cudaMemsetAsync(grad_weight, 0, (size_t)C * 4, st);
+        if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, (size_t)C * 4, st);
+        return group_status(what, e);
+    }
+    if (!grad || !x || !stats || !grad_x) return set_error(SDM_ERR_INVALID, "group norm backward: NULL pointer");
+    if ((uintptr_t)stats % 8) return set_error(SDM_ERR_INVALID, "group norm backward: stats must be 8-byte aligned");
+    if (sums || !rows) {
+        rc = group_check_ws(what, workspace, workspace_bytes, group_bytes(N, L, C, G, true) - kAlign);
+        if (rc != SDM_OK) return rc;
+    }
+    const GroupShape s{N, L, x_stride, grad_stride, C, G, group_splits(N, L), weight_dtype == SDM_F32, 0.f, weight, bias};
+    int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, grad_stride, x, grad, grad_x);
+    auto part = static_cast<float *>(workspace);
+    auto terms = rows ? nullptr : reinterpret_cast<float2 *>(static_cast<unsigned char *>(workspace) + group_part_bytes(N, L, C, G, true));
+    long long parts = 0;
+    auto go = [&](auto type, auto act) {
+        using T = decltype(type);
+        parts = group_backward<T, decltype(act)::value>(s, static_cast<const T *>(grad), static_cast<const T *>(x),
+                                                        reinterpret_cast<const float2 *>(stats), static_cast<T *>(grad_x), sums, part, terms, vec, st);
+    };
+    const bool silu = activation == SDM_ACT_SILU;
+    if (dtype == SDM_BF16) silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});
+    else silu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
+    if (sums)
+        k_norm_cols<<<(2 * C + kNormColThreads - 1) / kNormColThreads, kNormColThreads * kNormColSlices, 0, st>>>(part, (int)parts, C, grad_weight, grad_bias);
+    return group_status(what, cudaGetLastError());
+}
+
+}  // extern "C"

@@ -41,8 +41,9 @@ int linear_check(const sdm_linear_shape *s, LinearDims &d, bool back) {
     d.C = 64;
     d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
     d.spin = wait_limit();
-    if ((long long)s->B * s->H > 65535)
-        return set_error(SDM_ERR_UNSUPPORTED, "linear attention: B H must be at most 65535");
+    // blocks of a launch: one per head and 16 columns of the state
+    if ((long long)s->B * s->H * (s->Dv / 16) >= (1LL << 31))
+        return set_error(SDM_ERR_INVALID, "linear attention: B H Dv / 16 must be below 2^31");
     linear_segments(d);
     const int es = s->dtype == SDM_BF16 ? 2 : 4;
     for (int i = 0; i < 3; ++i) {
@@ -172,7 +173,7 @@ int linear_forward(const sdm_linear_shape *shape, float *state, const void *q, c
                        state, state, d.Dv, 1, readings, false};
     if (!save && d.T <= kLinearStepTokens) {
         const cudaError_t e = linear_clear(workspace, workspace_bytes, st);
-        return linear_status(e == cudaSuccess ? launch_linear_tokens(d, p, in, st) : e);
+        return linear_status(e == cudaSuccess ? launch_linear_step(d, in, q, k, v, state, readings, st) : e);
     }
     const LinearLayout l = linear_layout(d, false);
     rc = linear_check_ws("workspace", workspace, workspace_bytes, l.bytes);

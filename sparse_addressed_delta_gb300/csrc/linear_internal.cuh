@@ -82,7 +82,9 @@ cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const L
                                void *status, cudaStream_t st);
 cudaError_t launch_linear_join(const LinearDims &d, const LinearIn &in, const float *first, bool reverse, float *starts, cudaStream_t st);
 
-cudaError_t launch_linear_tokens(const LinearDims &d, const LinearPass &p, const LinearIn &in, cudaStream_t st);
+// up to kLinearStepTokens tokens (any number, but slowly)
+cudaError_t launch_linear_step(const LinearDims &d, const LinearIn &in, const void *q, const void *k, const void *v, float *state, void *o,
+                               cudaStream_t st);
 // out [B, T, Hk, width] = the sum over a key head's heads, and over `blocks` parts, of part [blocks][B, T, H, width]
 cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, cudaStream_t st);
 // grad_decay [H] from the laid q, k, v and readings' gradient, the segments' first states and the gradients of the
