@@ -179,6 +179,7 @@ def library() -> ctypes.CDLL:
 class _NoCalls:
     """In the place of a module of the everyday calls that is not there: it takes no call."""
     gated_delta = layer_norm = layer_norm_backward = staticmethod(lambda *args: None)
+    linear_attention = linear_attention_backward = group_norm = group_norm_backward = gated_delta
 
 
 def _calls(lib: ctypes.CDLL):
@@ -191,8 +192,10 @@ def _calls(lib: ctypes.CDLL):
     at = lambda *names: tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names)  # noqa: E731
     mod.setup((torch.Tensor, torch.nn.Parameter), (torch.float32, torch.bfloat16, torch.int32, torch.uint8),
               (torch.empty, torch.empty_like, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream, _check),
-              DELTA_STEP_TOKENS, at("sdm_gated_delta", "sdm_gated_delta_workspace_bytes", "sdm_layer_norm",
-                                    "sdm_layer_norm_backward", "sdm_layer_norm_workspace_bytes"))
+              DELTA_STEP_TOKENS, LINEAR_STEP_TOKENS, at("sdm_gated_delta", "sdm_gated_delta_workspace_bytes", "sdm_layer_norm",
+                                    "sdm_layer_norm_backward", "sdm_layer_norm_workspace_bytes"),
+              at(*(f"sdm_linear_attention{n}" for n in ("", "_workspace_bytes", "_save", "_saved_bytes", "_backward", "_backward_workspace_bytes"))),
+              at(*(f"sdm_group_norm{n}" for n in ("", "_workspace_bytes", "_backward", "_backward_workspace_bytes"))))
     return mod
 
 
@@ -980,6 +983,10 @@ def linear_attention(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
         return _on(stream, linear_attention, state, q, k, v, log_decay, valid_tokens, scale=scale,
                    readings=readings, workspace=workspace)
     lib = library()
+    if workspace is None:
+        o = _fast.linear_attention(state, q, k, v, log_decay, valid_tokens, scale, readings, False)
+        if o is not None:
+            return o
     shape, (B, T, H, Hk, Dk, Dv), dev, dt = _linear_shape(q, k, v, log_decay, valid_tokens, scale)
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
     readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
@@ -1000,6 +1007,11 @@ def linear_attention_save(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     if stream is not None:
         return _on(stream, linear_attention_save, state, q, k, v, log_decay, valid_tokens, scale=scale,
                    readings=readings, saved=saved, workspace=workspace)
+    if saved is None and workspace is None:
+        library()
+        both = _fast.linear_attention(state, q, k, v, log_decay, valid_tokens, scale, readings, True)
+        if both is not None:
+            return both
     shape, (B, T, H, Hk, Dk, Dv), dev, dt = _linear_shape(q, k, v, log_decay, valid_tokens, scale)
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
     readings = _result(readings, "readings", (B, T, H, Dv), dt, dev)
@@ -1024,6 +1036,11 @@ def linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if stream is not None:
         return _on(stream, linear_attention_backward, q, k, v, log_decay, valid_tokens, saved, grad_readings,
                    grad_state=grad_state, scale=scale, decay=decay, workspace=workspace)
+    if workspace is None:
+        library()
+        out = _fast.linear_attention_backward(q, k, v, log_decay, valid_tokens, saved, grad_readings, grad_state, scale, decay)
+        if out is not None:
+            return out
     shape, (B, T, H, Hk, Dk, Dv), dev, dt = _linear_shape(q, k, v, log_decay, valid_tokens, scale, grad_readings)
     if grad_state is not None:
         _need(grad_state, "grad_state", (B, H, Dk, Dv), torch.float32, dev)
@@ -1212,6 +1229,11 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     here belongs to ``stream`` (None: the current one)."""
     if stream is not None:
         return _on(stream, group_norm, x, groups, weight, bias, activation=activation, eps=eps, out=out, workspace=workspace)
+    if out is None and workspace is None:
+        library()
+        y = _fast.group_norm(x, groups, weight, bias, activation, eps, False)
+        if y is not None:
+            return y
     return _group_norm(x, groups, weight, bias, activation, eps, out, None, workspace)
 
 
@@ -1221,6 +1243,11 @@ def group_norm_save(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor]
     """group_norm that also returns what its backward needs: (y, stats [N, groups, 2] float32)."""
     if stream is not None:
         return _on(stream, group_norm_save, x, groups, weight, bias, activation=activation, eps=eps, out=out, workspace=workspace)
+    if out is None and workspace is None:
+        library()
+        both = _fast.group_norm(x, groups, weight, bias, activation, eps, True)
+        if both is not None:
+            return both
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")
     if not isinstance(groups, int) or groups < 1:
@@ -1236,6 +1263,11 @@ def group_norm_backward(grad: torch.Tensor, x: torch.Tensor, groups: int, weight
     the forward had them, grad_weight and grad_bias, float32 [C], summed over samples and positions in a fixed order."""
     if stream is not None:
         return _on(stream, group_norm_backward, grad, x, groups, weight, bias, stats, activation=activation, workspace=workspace)
+    if workspace is None:
+        library()
+        out = _fast.group_norm_backward(grad, x, groups, weight, bias, stats, activation)
+        if out is not None:
+            return out
     N, L, C, step, act = _group_shape(x, groups, activation)
     gstep = _norm_rows(grad, "grad")[2]
     dt, dev = x.dtype, x.device

@@ -17,6 +17,7 @@ namespace sdm {
 namespace {
 
 constexpr int kGroupThreads = 256, kGroupBatch = 8, kGroupMaxCols = 16384, kGroupRowCols = 8192;
+constexpr int kGroupRowThreads = 512;                   // an SM, of the forward over rows (128 registers each)
 
 // The sigmoid. bfloat16: by the approximate exponential and reciprocal instructions, within 2^-20 of it where it is not
 // negligible, far inside the results' rounding of 2^-9; the exact ones would bound the kernel (25 instructions an
@@ -84,7 +85,7 @@ struct GroupShape {
 // ---- one position a sample ----------------------------------------------------------------------
 
 template <typename T, int VEC, int NV, bool BLOCK, bool ACT>
-__global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
+__global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock, kGroupRowThreads / (BLOCK ? 512 : kNormBlock))
     k_group_row(const __grid_constant__ GroupShape s, const T *x, int tpr, T *y, float2 *stats) {
     constexpr int E = VEC * NV, ST = kNormStages<T>;
     extern __shared__ __align__(16) unsigned char ring_smem[];
@@ -579,9 +580,7 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
             const size_t smem = kNormStages<T> * RowRing<T, VEC, NV, 1, false, false>::stage_bytes(each, g.threads, g.rpb);
             auto go = [&](auto kern) {
                 set_kernel_smem(kern, smem);
-                int per_sm = 1;
-                if (s.N * s.G > (long long)kRefSms * g.rpb) cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, g.threads, smem);
-                const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (per_sm > 1 ? per_sm : 1));
+                const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (kGroupRowThreads / g.threads));
                 kern<<<(unsigned)grid, g.threads, smem, st>>>(s, x, g.tpr, y, stats);
             };
             if (g.block) go(k_group_row<T, VEC, NV, true, ACT>);

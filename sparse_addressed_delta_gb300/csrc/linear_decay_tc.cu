@@ -15,8 +15,7 @@
 // for themselves, the pairs' sums too. Warps as in linear_scan_tc.cu.
 #include <type_traits>
 
-#include "linear_internal.cuh"
-#include "tcgen05.cuh"
+#include "linear_tc.cuh"
 
 namespace sdm {
 namespace {
@@ -126,28 +125,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
             for (int i = tid; i < C * KP / 8; i += 32 * kDecWarps) {
                 const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
-                const float w = weight(row);
-                float x[8];
-#pragma unroll
-                for (int m = NP - 1; m >= 0; --m) {
-                    const uint4 r = *reinterpret_cast<const uint4 *>(src + m * KT * TILE + off);
-                    const unsigned u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[2 * e] = m == NP - 1 ? lo_f32(u[e]) : x[2 * e] + lo_f32(u[e]);
-                        x[2 * e + 1] = m == NP - 1 ? hi_f32(u[e]) : x[2 * e + 1] + hi_f32(u[e]);
-                    }
-                }
-                unsigned pl[3][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    unsigned s[3];
-                    split_bf16<3>(x[2 * e] * w, x[2 * e + 1] * w, s);
-                    pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
-                }
-#pragma unroll
-                for (int m = 0; m < 3; ++m)
-                    *reinterpret_cast<uint4 *>(dst + m * KT * TILE + off) = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
+                scale_piece<NP, KT * TILE>(src, dst, off, weight(row));
             }
             fence_proxy_async_smem();
         };

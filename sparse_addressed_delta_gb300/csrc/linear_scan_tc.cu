@@ -12,19 +12,18 @@
 //
 // S^T's planes are an A operand in tensor memory, V one in shared memory; Q, Z and the decayed keys are B operands
 // there. Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the tokens and of K), warp 16 issues the
-// products, warp 17 loads by tensor copies. While the threads make Z and the decayed keys of the next chunk the
+// products, warp 17 loads and warp 18 stores bfloat16 results, both by tensor copies. While the threads make Z and the decayed keys of the next chunk the
 // tensor core reads the state; while they store the results and split the new state it makes the next chunk's U,
 // OB and P. Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block, and the block
 // leaves after its copies and products in flight.
 #include <type_traits>
 
-#include "linear_internal.cuh"
-#include "tcgen05.cuh"
+#include "linear_tc.cuh"
 
 namespace sdm {
 namespace {
 
-constexpr int kLinC = 64, kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 2);
+constexpr int kLinC = 64, kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 3);
 
 template <int KP, int NP>
 struct LinScan {
@@ -38,7 +37,7 @@ struct LinScan {
     static_assert(P + kLinC <= 512, "tensor memory");
 };
 
-enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_P = 9, B_ZK, B_U, B_UF, B_O, B_OF, B_S, B_DRAIN, B_COUNT };
+enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_P = 9, B_ZK, B_U, B_UF, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
 
 enum { LIN_RUN, LIN_CARRY };
 
@@ -99,7 +98,8 @@ __device__ __forceinline__ int linear_longest_first(const LinearDims &d, const i
 template <int KP, int NP, int MODE, bool REV, typename OT>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear_scan(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ LinearDims d, const __grid_constant__ LinArgs a) {
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const __grid_constant__ LinearDims d,
+                  const __grid_constant__ LinArgs a) {
     using L = LinScan<KP, NP>;
     constexpr int C = kLinC, HD = KP / 4, ST = L::STAGES, KT = L::KT, TILE = L::TILE;
     constexpr bool CARRY = MODE == LIN_CARRY;
@@ -132,9 +132,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int i = 0; i < ST; ++i) {
             mbar_init(bar + B_FULL + i, 32);
             mbar_init(bar + B_BULK + i, 1);
-            mbar_init(bar + B_EMPTY + i, 1);
+            mbar_init(bar + B_EMPTY + i, !CARRY && sizeof(OT) == 2 ? 2 : 1);
         }
-        for (int i = B_P; i < B_COUNT; ++i) mbar_init(bar + i, i == B_ZK || i == B_UF || i == B_OF || i == B_S ? kLinWarps : 1);
+        for (int i = B_P; i < B_COUNT; ++i) mbar_init(bar + i, i == B_ZK || i == B_UF || i == B_OF || i == B_S || i == B_OUT ? kLinWarps : 1);
         *dead = a.status->code != 0;                               // an earlier kernel of this call gave up
         fence_mbar_init();
     }
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t tm = *slot;
     auto chunk_at = [&](int it) { return REV ? n0 + nch - 1 - it : n0 + it; };
     int first = -1;                                                // iteration of the column's first update that is not finite
-    float S[HD];
+    float2 S[HD / 2];
 
     if (warp < kLinWarps) {
         const int part = warp >> 2, lane0 = 32 * (warp & 3), col = v0 + lane0 + lane, kk = part * HD;
@@ -163,15 +163,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
         const float *begin = CARRY ? nullptr : d.segs > 1 ? a.starts + seg * states : p.first;
 #pragma unroll
-        for (int i = 0; i < HD; ++i) S[i] = begin && mine && kk + i < K ? begin[own + (kk + i) * p.sk + col * p.sv] : 0.f;
+        for (int i = 0; i < HD; ++i) reinterpret_cast<float *>(S)[i] = begin && mine && kk + i < K ? begin[own + (kk + i) * p.sk + col * p.sv] : 0.f;
         auto planes_of_s = [&] {
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
-                float x[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = S[c + i];
                 const uint32_t dst = at + L::SP + (kk + c) / 2;
-                tc_store_planes(dst, dst + KP / 2, dst + KP, x);
+                store_planes3(dst, dst + KP / 2, dst + KP, S + c / 2);
             }
             tc_wait_st();
         };
@@ -193,56 +190,57 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 for (int i = id; i < C * KP / 8; i += THREADS) {
                     const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
                     const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
-                    float x[8];
+                    scale_piece<NP, KT * TILE>(src, smem + L::KX, off, w);
+                }
+            } else {
+                // blocks that lie past the diagonal whole are not read
+                const int row = lane0 + lane, ahead = REV ? 16 * part - lane0 - 31 : lane0 - 16 * part - 15;   // least tokens apart
+                if (ahead >= -46) {
+                    tc_fence_after();
+                    float2 x[8];
+                    tc_load16(at + L::P + 16 * part, reinterpret_cast<float(&)[16]>(x));
+                    if (ahead >= 0) {                              // e^{L apart} = e^{L least} e^{L rest}, all of it before the diagonal
+                        const float w = pair[C + (REV ? 16 * part - row : row - 16 * part - 15)];
 #pragma unroll
-                    for (int m = NP - 1; m >= 0; --m) {
-                        const uint4 r = *reinterpret_cast<const uint4 *>(src + m * KT * TILE + off);
-                        const unsigned u[4] = {r.x, r.y, r.z, r.w};
+                        for (int i = 0; i < 8; ++i)
+                            x[i] = mul2(mul2(x[i], make_float2(w, w)), REV ? make_float2(pw[2 * i], pw[2 * i + 1]) : make_float2(pw[15 - 2 * i], pw[14 - 2 * i]));
+                    } else {
+                        const int apart = REV ? 16 * part - row : row - 16 * part;   // of column 0; the others' step by step
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[2 * e] = m == NP - 1 ? lo_f32(u[e]) : x[2 * e] + lo_f32(u[e]);
-                            x[2 * e + 1] = m == NP - 1 ? hi_f32(u[e]) : x[2 * e + 1] + hi_f32(u[e]);
+                        for (int i = 0; i < 8; ++i) {
+                            const int a0 = REV ? apart + 2 * i : apart - 2 * i, a1 = REV ? a0 + 1 : a0 - 1;
+                            x[i].x = a0 >= 0 ? x[i].x * pair[C + a0] : 0.f;
+                            x[i].y = a1 >= 0 ? x[i].y * pair[C + a1] : 0.f;
                         }
                     }
-                    unsigned pl[3][4];
+                    unsigned pl[3][8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         unsigned s[3];
-                        split_bf16<3>(x[2 * e] * w, x[2 * e + 1] * w, s);
+                        split3(x[e].x, x[e].y, s);
                         pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
                     }
 #pragma unroll
                     for (int m = 0; m < 3; ++m)
-                        *reinterpret_cast<uint4 *>(smem + L::KX + m * KT * TILE + off) = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            *reinterpret_cast<uint4 *>(smem + L::Z + m * TILE + tc_at(row, 2 * part + c)) =
+                                make_uint4(pl[m][4 * c], pl[m][4 * c + 1], pl[m][4 * c + 2], pl[m][4 * c + 3]);
                 }
-            } else {
-                const int row = lane0 + lane;
-                tc_fence_after();
-                float x[16];
-                tc_load16(at + L::P + 16 * part, x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int apart = REV ? 16 * part + i - row : row - 16 * part - i;
-                    x[i] = apart >= 0 ? x[i] * pair[C + apart] : 0.f;
-                }
-                unsigned pl[3][8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    unsigned s[3];
-                    split_bf16<3>(x[2 * e], x[2 * e + 1], s);
-                    pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
-                }
-#pragma unroll
-                for (int m = 0; m < 3; ++m)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<uint4 *>(smem + L::Z + m * TILE + tc_at(row, 2 * part + c)) =
-                            make_uint4(pl[m][4 * c], pl[m][4 * c + 1], pl[m][4 * c + 2], pl[m][4 * c + 3]);
             }
             fence_proxy_async_smem();
             arrive(B_ZK);
             return true;
         };
+        // bfloat16 results, 8 x 8 blocks stored transposed: block i of a store is 8 columns (i % 2) and 8 tokens (i / 2), a
+        // lane's row one token; and what the state's readings are times, of a whole chunk
+        const int orow = 16 * part + 8 * (lane >> 4) + (lane & 7), ocol = (lane0 >> 3) + ((lane >> 3) & 1);
+        float reads[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 16 * part + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+            reads[i] = p.from * pw[REV ? C - 1 - t : t + 1];
+        }
         if (!CARRY && nch > 0) {
             planes_of_s();
             arrive(B_S);
@@ -251,17 +249,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int it = 0; ok && it < nch; ++it) {
             const unsigned par = it & 1;
             const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
-            float x[16];
             ok = tc_warp_wait(bar + B_U, par, dead, d.spin);
             if (!ok) break;
             tc_fence_after();
             const float whole = pw[nt];
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
-                tc_load16(at + L::U + kk + c, x);
-                if (!CARRY && c == 0 && first < 0 && !(fabsf(x[0]) <= 3.402823466e38f)) first = it;
+                float2 x[8];
+                tc_load16(at + L::U + kk + c, reinterpret_cast<float(&)[16]>(x));
+                if (!CARRY && c == 0 && first < 0 && !(fabsf(x[0].x) <= 3.402823466e38f)) first = it;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[c + i] = fmaf(whole, S[c + i], x[i]);
+                for (int i = 0; i < 8; ++i) S[c / 2 + i] = fma2(make_float2(whole, whole), S[c / 2 + i], x[i]);
             }
             arrive(B_UF);
             if (it + 1 < nch) {
@@ -272,18 +270,47 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 ok = tc_warp_wait(bar + B_O, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
-                float y[16];
-                tc_load16(at + L::OA + 16 * part, y);
-                tc_load16(at + L::OB + 16 * part, x);
-                arrive(B_OF);
-                OT *out = static_cast<OT *>(p.out) + ((((long long)kb * d.B + b) * d.T + n * C + 16 * part) * d.H + h) * p.V + col;
-                const int left = d.T - n * C - 16 * part;
+                if constexpr (sizeof(OT) == 2) {
+                    // in the place of the chunk's V, which warp 18 stores
+                    unsigned char *to = smem + it % ST * L::STAGE + L::V;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = 16 * part + i;
-                    const float r = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[i], x[i]) : 0.f;
-                    if (mine && i < left) *out = from_f32<OT>(r);
-                    out += (long long)d.H * p.V;
+                    for (int l = 0; l < 2; ++l) {                  // 16 lanes of columns
+                        float y[8], z[8];
+                        tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::OA + 16 * part, at + ((uint32_t)(16 * l) << 16) + L::OB + 16 * part, y, z);
+                        if (l == 1) arrive(B_OF);
+                        if (nt == C) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) z[i] = fmaf(reads[(i >> 2) * 2 + (i & 1)], y[i], z[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int t = 16 * part + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                                z[i] = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[i], z[i]) : 0.f;
+                            }
+                        }
+                        unsigned r[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[2 * i], z[2 * i + 1]);
+                        const int c = ocol + 2 * l;
+                        stsm4t(smem_u32(to) + (c >> 3) * TILE + tc_at(orow, c & 7), r);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar + B_OUT);
+                } else {
+                    float x[16], y[16];
+                    tc_load16(at + L::OA + 16 * part, y);
+                    tc_load16(at + L::OB + 16 * part, x);
+                    arrive(B_OF);
+                    float *out = static_cast<float *>(p.out) + ((((long long)kb * d.B + b) * d.T + n * C + 16 * part) * d.H + h) * p.V + col;
+                    const int left = d.T - n * C - 16 * part;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int t = 16 * part + i;
+                        const float r = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[i], x[i]) : 0.f;
+                        if (mine && i < left) *out = r;
+                        out += (long long)d.H * p.V;
+                    }
                 }
                 if (it + 1 < nch) {
                     planes_of_s();
@@ -387,7 +414,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp == kLinWarps + 1) {
         // ---- the chunks' inputs
         constexpr uint32_t bytes = CARRY ? NP * (KT + 2) * TILE : L::STAGE;
         for (int it = 0; it < nch; ++it) {
@@ -427,6 +454,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             mbar_arrive(bar + B_FULL + s);
         }
+    } else if (!CARRY && sizeof(OT) == 2) {
+        // ---- the bfloat16 results
+        for (int it = 0; it < nch; ++it) {
+            if (!tc_warp_wait(bar + B_OUT, it & 1, dead, d.spin)) break;
+            if (lane == 0) {
+                for (int c = 0; c < 2; ++c)
+                    if (v0 + 64 * c < p.V)
+                        tc_tensor_store(&mo, v0 + 64 * c, h, chunk_at(it) * C, b, smem + it % ST * L::STAGE + L::V + c * TILE);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                mbar_arrive(bar + B_EMPTY + it % ST);
+            }
+            __syncwarp();
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncthreads();
     if (*dead) {
@@ -459,8 +501,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (seg + 1 == d.segs) {
             const int cols = p.V - v0 < 128 ? p.V - v0 : 128;
             OT *out = static_cast<OT *>(p.out) + (((long long)kb * d.B + b) * d.T * d.H + h) * p.V + v0;
-            for (long long t = (long long)chunks * C + (tid >> 7); t < d.T; t += kLinThreads >> 7)
-                if ((tid & 127) < cols && tid < (kLinThreads >> 7 << 7)) out[t * d.H * p.V + (tid & 127)] = from_f32<OT>(0.f);
+            for (long long t = (long long)chunks * C + (tid >> 7); t < d.T && tid < 512; t += 4)
+                if ((tid & 127) < cols) out[t * d.H * p.V + (tid & 127)] = from_f32<OT>(0.f);
         }
     }
     // where the state goes: a carried segment's is the next one's share
@@ -470,7 +512,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (col < p.V)
 #pragma unroll
             for (int i = 0; i < HD; ++i)
-                if (kk + i < K) end[own + (kk + i) * p.sk + col * p.sv] = S[i];
+                if (kk + i < K) end[own + (kk + i) * p.sk + col * p.sv] = reinterpret_cast<float *>(S)[i];
     }
 }
 
@@ -500,25 +542,24 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
 }
 
 template <int KP, int NP, int MODE, bool REV, typename OT>
-cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, cudaStream_t st) {
     auto kern = k_linear_scan<KP, NP, MODE, REV, OT>;
     using L = LinScan<KP, NP>;
     set_kernel_smem(kern, L::BYTES);
     const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * (MODE == LIN_CARRY ? d.segs - 1 : d.segs);
-    kern<<<(unsigned)blocks, kLinThreads, L::BYTES, st>>>(mq, mk, mv, d, a);
+    kern<<<(unsigned)blocks, kLinThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
     return cudaGetLastError();
 }
 
 template <int KP, int NP>
-cudaError_t scan_of(const LinearDims &d, const LinArgs &a, bool carry, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                    cudaStream_t st) {
+cudaError_t scan_of(const LinearDims &d, const LinArgs &a, bool carry, const CUtensorMap *m, cudaStream_t st) {
     using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
     if (carry)
-        return a.p.reverse ? scan<KP, NP, LIN_CARRY, true, IT>(d, a, mq, mk, mv, st) : scan<KP, NP, LIN_CARRY, false, IT>(d, a, mq, mk, mv, st);
+        return a.p.reverse ? scan<KP, NP, LIN_CARRY, true, IT>(d, a, m, st) : scan<KP, NP, LIN_CARRY, false, IT>(d, a, m, st);
     if constexpr (NP == 1)
         if (a.p.out_f32)
-            return a.p.reverse ? scan<KP, NP, LIN_RUN, true, float>(d, a, mq, mk, mv, st) : scan<KP, NP, LIN_RUN, false, float>(d, a, mq, mk, mv, st);
-    return a.p.reverse ? scan<KP, NP, LIN_RUN, true, IT>(d, a, mq, mk, mv, st) : scan<KP, NP, LIN_RUN, false, IT>(d, a, mq, mk, mv, st);
+            return a.p.reverse ? scan<KP, NP, LIN_RUN, true, float>(d, a, m, st) : scan<KP, NP, LIN_RUN, false, float>(d, a, m, st);
+    return a.p.reverse ? scan<KP, NP, LIN_RUN, true, IT>(d, a, m, st) : scan<KP, NP, LIN_RUN, false, IT>(d, a, m, st);
 }
 
 // the operands as the tensor copies take them: float32 ones as three bfloat16 planes, the others contiguous
@@ -561,16 +602,22 @@ cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const L
                                void *status, cudaStream_t st) {
     const int np = d.dtype == SDM_F32 ? 3 : 1;
     LinArgs a{p, in.g, in.valid, starts, static_cast<DevStatus *>(status), {}, {}, p.last != nullptr && !p.reverse};
-    CUtensorMap m[3];
+    CUtensorMap m[4];
     for (int i = 0; i < 3; ++i) {
         const cudaError_t e = tc_tensor_map(m + i, laid[i].p, laid[i].s, np * d.B, d.T, laid[i].heads, laid[i].width);
         if (e != cudaSuccess) return e;
         a.seqs[i] = laid[i].s[0];
         a.heads[i] = laid[i].s[2];
     }
+    m[3] = m[2];                                                    // (of bfloat16 results alone)
+    if (!carry && np == 1 && !p.out_f32) {
+        const long long os[3] = {(long long)d.T * d.H * p.V, (long long)d.H * p.V, p.V};
+        const cudaError_t e = tc_tensor_map(m + 3, p.out, os, d.B, d.T, d.H, p.V);
+        if (e != cudaSuccess) return e;
+    }
     const bool wide = p.K > 64;
-    if (np == 1) return wide ? scan_of<128, 1>(d, a, carry, m[0], m[1], m[2], st) : scan_of<64, 1>(d, a, carry, m[0], m[1], m[2], st);
-    return wide ? scan_of<128, 3>(d, a, carry, m[0], m[1], m[2], st) : scan_of<64, 3>(d, a, carry, m[0], m[1], m[2], st);
+    if (np == 1) return wide ? scan_of<128, 1>(d, a, carry, m, st) : scan_of<64, 1>(d, a, carry, m, st);
+    return wide ? scan_of<128, 3>(d, a, carry, m, st) : scan_of<64, 3>(d, a, carry, m, st);
 }
 
 cudaError_t launch_linear_join(const LinearDims &d, const LinearIn &in, const float *first, bool reverse, float *starts, cudaStream_t st) {

@@ -1,0 +1,91 @@
+// Arithmetic of the linear attention's tensor-core kernels: floats split into bfloat16 planes and pairs of floats in
+// packed operations. The scans issue instructions at 85 % of what an SM can, so these count: a pair's three planes take
+// seven (three conversions, four mixed-precision subtractions), where widening the planes to floats takes eleven.
+#pragma once
+
+#include "linear_internal.cuh"
+#include "tcgen05.cuh"
+
+namespace sdm {
+
+// x minus the lower or upper bfloat16 of a pair, exact where that is x rounded
+__device__ __forceinline__ float minus_lo(float x, unsigned p) {
+    float r;
+    asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %1;\n mov.b16 m, 0xBF80;\n fma.rn.f32.bf16 %0, l, m, %2;\n}" : "=f"(r) : "r"(p), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float minus_hi(float x, unsigned p) {
+    float r;
+    asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %1;\n mov.b16 m, 0xBF80;\n fma.rn.f32.bf16 %0, h, m, %2;\n}" : "=f"(r) : "r"(p), "f"(x));
+    return r;
+}
+
+// x0, x1 as sums of three bfloat16 terms each
+__device__ __forceinline__ void split3(float x0, float x1, unsigned (&p)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = pack_bf16(x0, x1);
+        if (i < 2) {
+            x0 = minus_lo(x0, p[i]);
+            x1 = minus_hi(x1, p[i]);
+        }
+    }
+}
+
+// two floats at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)), "l"(reinterpret_cast<unsigned long long &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return d;
+}
+
+// 16 floats as three planes of 8 packed columns of tensor memory
+__device__ __forceinline__ void store_planes3(uint32_t hi, uint32_t mid, uint32_t lo, const float2 *x) {
+    unsigned p[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        unsigned s[3];
+        split3(x[i].x, x[i].y, s);
+        p[0][i] = s[0]; p[1][i] = s[1]; p[2][i] = s[2];
+    }
+    tc_store8(hi, p[0]);
+    tc_store8(mid, p[1]);
+    tc_store8(lo, p[2]);
+}
+
+// 8 columns of a row of a [64 tokens] tile of NP planes (PLANE bytes apart), times w, as three planes
+template <int NP, int PLANE>
+__device__ __forceinline__ void scale_piece(const unsigned char *src, unsigned char *dst, int off, float w) {
+    float2 x[4];
+#pragma unroll
+    for (int m = NP - 1; m >= 0; --m) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(src + m * PLANE + off);
+        const unsigned u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 y = make_float2(lo_f32(u[e]), hi_f32(u[e]));
+            x[e] = m == NP - 1 ? y : make_float2(x[e].x + y.x, x[e].y + y.y);
+        }
+    }
+    unsigned pl[3][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        unsigned s[3];
+        x[e] = mul2(x[e], make_float2(w, w));
+        split3(x[e].x, x[e].y, s);
+        pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
+    }
+#pragma unroll
+    for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4 *>(dst + m * PLANE + off) = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
+}
+
+}  // namespace sdm
