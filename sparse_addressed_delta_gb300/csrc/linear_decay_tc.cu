@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (tid <= C) pw[tid] = (float)linear_power(a.g[h], tid);
+    if (tid <= C) pw[tid] = linear_power(a.g[h], tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -103,7 +103,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
         const long long own = bh * d.Dk * d.Dv + (long long)(k0 + kk) * d.Dv + col;
         float S[HD], G[HD];
-        double acc = 0.0;
+        // the sum so far and what its roundings lost: a double addition takes a warp 16 cycles of the SM
+        float acc = 0.f, lost = 0.f;
+        auto add = [&](float x) {
+            const float sum = acc + x, of_x = sum - acc;
+            lost += (acc - (sum - of_x)) + (x - of_x);
+            acc = sum;
+        };
         const float *begin = a.starts + seg * states + own;
 #pragma unroll
         for (int i = 0; i < HD; ++i) {
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sum = fmaf(s[c + i], x[i], sum);
             }
-            if (mine) acc += (double)sum;
+            if (mine) add(sum);
         };
         // s = w s + a product
         auto advance = [&](int where, float w, float (&s)[HD]) {
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     const int apart = row - 16 * part - i;
                     if (apart > 0) sum = fmaf(apart * pw[apart] * x[i], y[i], sum);
                 }
-                acc += (double)(d.scale * sum);
+                add(d.scale * sum);
             }
             arrive(D_PREAD);
             if (it > 0 && !(ok = wait(D_MUL + 3, it - 1))) break;
@@ -198,16 +204,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             advance(L::W1, 1.f, G);
             if (a.ends && mine) {
                 const float *end = a.ends + (d.segs - 1 - seg) * states + own;
-                double sum = 0.0;
+                float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < HD; ++i)
-                    if (k0 + kk + i < d.Dk) sum += (double)G[i] * end[(long long)i * d.Dv];
-                acc += sum;
+                    if (k0 + kk + i < d.Dk) sum = fmaf(G[i], end[(long long)i * d.Dv], sum);
+                add(sum);
             }
         }
+        double all = (double)acc + (double)lost;
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) acc += __shfl_xor_sync(~0u, acc, m);
-        if (lane == 0) sums[warp] = acc;
+        for (int m = 16; m > 0; m >>= 1) all += __shfl_xor_sync(~0u, all, m);
+        if (lane == 0) sums[warp] = all;
     } else if (warp == kDecWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
@@ -330,17 +337,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
 }
 
-// a head's parts of all sequences, in order
-__global__ void __launch_bounds__(128) k_linear_decay_sum(const double *part, int B, int H, int each, float *out) {
-    __shared__ double sums[128];
+// a head's parts of all sequences, in a fixed order; a warp a head
+__global__ void __launch_bounds__(32) k_linear_decay_sum(const double *part, int B, int H, int each, float *out) {
     const int h = blockIdx.x;
     double s = 0.0;
-    for (long long i = threadIdx.x; i < (long long)B * each; i += 128) s += part[(i / each * H + h) * each + i % each];
-    sums[threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.x) return;
-    for (int i = 1; i < 128; ++i) s += sums[i];
-    out[h] = (float)s;
+    for (long long i = threadIdx.x; i < (long long)B * each; i += 32) s += part[(i / each * H + h) * each + i % each];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
+    if (threadIdx.x == 0) out[h] = (float)s;
 }
 
 template <int KP, int NP>
@@ -366,7 +370,7 @@ cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const L
     }
     const cudaError_t e = np == 3 ? decay<64, 3>(d, a, m, st) : d.Dk > 64 ? decay<128, 1>(d, a, m, st) : decay<64, 1>(d, a, m, st);
     if (e != cudaSuccess) return e;
-    k_linear_decay_sum<<<d.H, 128, 0, st>>>(part, d.B, d.H, a.kblocks * linear_tiles(d.Dv) * d.segs, grad_decay);
+    k_linear_decay_sum<<<d.H, 32, 0, st>>>(part, d.B, d.H, a.kblocks * linear_tiles(d.Dv) * d.segs, grad_decay);
     return cudaGetLastError();
 }
 

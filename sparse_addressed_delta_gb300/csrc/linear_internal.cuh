@@ -15,7 +15,7 @@ constexpr int kLinearMaxDk = 128, kLinearMaxDv = 512;
 constexpr int kLinearStepTokens = 8;     // up to this many tokens go one by one
 // A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten whole, and
 // -inf (a hard reset at every token) has no 0 x inf among its powers.
-constexpr double kLinearMinDecay = -110.0;
+constexpr float kLinearMinDecay = -110.f;
 
 struct LinearDims {
     int B, T, H, Hk, Dk, Dv, dtype;
@@ -55,8 +55,28 @@ __device__ __forceinline__ int linear_valid(const int32_t *valid, int b, int T) 
     const int v = valid ? valid[b] : T;
     return v < 0 ? 0 : (v > T ? T : v);
 }
-// e^(g n) for whole n >= 0, from 64 bits: the exponent's own rounding would grow with n
-__device__ __forceinline__ double linear_power(double g, double n) { return n == 0.0 ? 1.0 : exp((g < kLinearMinDecay ? kLinearMinDecay : g) * n); }
+// e^(g n) for whole n >= 0, within one unit in the last place. The powers multiply up along a sequence, and the
+// rounding of g n itself would grow with n, so its low part is kept; the exponential is the argument reduction of Cody
+// and Waite (n ln 2 in two parts, the first of few bits) and the Taylor series of the remainder. In 32 bits: a double
+// exponential costs a block 2 us (the card has 2 lanes of doubles an SM).
+__device__ __forceinline__ float linear_power(float g, int n) {
+    if (g < kLinearMinDecay) g = kLinearMinDecay;
+    const float m = (float)n, x = g * m, low = fmaf(g, m, -x);
+    if (n == 0) return 1.f;
+    if (!(x >= -110.f)) return x == x ? 0.f : x;
+    if (x > 89.f) return __int_as_float(0x7f800000);
+    const float k = rintf(x * 1.4426950408889634f);
+    constexpr double kLn2 = 0.69314718055994530942;
+    constexpr float kHigh = 0.693359375f, kLow = (float)(kLn2 - 0.693359375);   // 355 / 512: k times it is exact
+    const float r = fmaf(k, -kHigh, x), r1 = r + fmaf(k, -kLow, low);
+    float p = 1.f / 5040.f;
+    p = fmaf(p, r1, 1.f / 720.f);
+    p = fmaf(p, r1, 1.f / 120.f);
+    p = fmaf(p, r1, 1.f / 24.f);
+    p = fmaf(p, r1, 1.f / 6.f);
+    p = fmaf(p, r1, 0.5f);
+    return ldexpf(1.f + fmaf(p * r1, r1, r1), (int)k);
+}
 
 inline int linear_tiles(int columns) { return (columns + 127) / 128; }
 inline long long linear_states(const LinearDims &d) { return (long long)d.B * d.H * d.Dk * d.Dv; }

@@ -143,11 +143,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid < 128) {
-        const double g = a.g[h];
-        const float x = tid <= C ? (float)linear_power(g, tid) : 0.f;
-        if (tid <= C) pw[tid] = x;
-        // e^{L n} of n tokens apart, 0 before
-        pair[tid] = tid < C ? 0.f : p.pair * (float)linear_power(g, tid - C);
+        // e^{L n} of n tokens; with the scale, of tokens n apart (0 before)
+        const int n = tid < C ? C - tid : tid - C;
+        const float x = linear_power(a.g[h], n);
+        if (tid <= C) pw[n] = x;
+        if (tid == C) pw[0] = 1.f;
+        pair[tid] = tid < C ? 0.f : p.pair * x;
     }
     tc_fence_before();
     __syncthreads();
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 if (n < 0 || col >= p.V || at[128 + c] != n || at[256 + c] != n || at[384 + c] != n) continue;
                 const int t1 = (n0 + n) * C, t2 = t1 + C < ntok ? t1 + C : ntok;
                 using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
-                linear_column<IT>(d, p, (float)linear_power(a.g[h], 1.0), b, h, col, n0 * C, t1, t2, begin ? begin + own + col * p.sv : nullptr);
+                linear_column<IT>(d, p, linear_power(a.g[h], 1), b, h, col, n0 * C, t1, t2, begin ? begin + own + col * p.sv : nullptr);
             }
             __syncthreads();
         }
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
     *reinterpret_cast<float4 *>(starts + i) = s;
     for (int m = 1; m < d.segs; ++m) {
         const int place = reverse ? d.segs - m : m - 1;            // of the segment before
-        const float w = (float)linear_power(g[h], bound(place + 1) - bound(place));
+        const float w = linear_power(g[h], bound(place + 1) - bound(place));
         float4 *at = reinterpret_cast<float4 *>(starts + m * states + i);
         const float4 e = *at;
         s = make_float4(fmaf(w, s.x, e.x), fmaf(w, s.y, e.y), fmaf(w, s.z, e.z), fmaf(w, s.w, e.w));
