@@ -9,10 +9,13 @@
 // the forward kept and G = 0, and ends with <G, R>, R the gradient of the state there.
 //
 // S and G stay in registers in float32, transposed: 128 of Dv's columns are the lanes of tensor memory (a quarter
-// of KP a thread). The four products are V^T or dO^T (A operands in shared memory) with decayed queries and keys,
-// three bfloat16 planes each, through two buffers in turn: while one is multiplied the threads fill the other and
-// take what the product before it made. All is bilinear in (Dk, Dv), so blocks take KP columns of Dk and 128 of Dv
-// for themselves, the pairs' sums too. Warps as in linear_scan_tc.cu.
+// of KP a thread). dO^T and V^T are A operands in shared memory, the queries and keys with both their weights, three
+// bfloat16 planes each, one B operand of 2 KP columns: A and A' come from one product, W and W' from the next, in the
+// same buffer. With four products of KP columns, two buffers in turn, it took 188 us where it takes @@ (64 heads of
+// 128 x 128 x 64 chunks): shared memory bounds it (a product of 128 x 128 x 16 reads its operands at all of its rate,
+// and the threads that fill the other buffer wait for it), and the wider product reads its A operand half as often.
+// All is bilinear in (Dk, Dv), so blocks take KP columns of Dk and 128 of Dv for themselves, the pairs' sums too.
+// Warps as in linear_scan_tc.cu.
 #include <type_traits>
 
 #include "linear_tc.cuh"
@@ -28,15 +31,15 @@ struct LinDecay {
     // (a product's A operand of 128 rows reads on past the 64 of Q and dO: into what follows them)
     static constexpr int Q = 0, G = Q + NP * KT * TILE, K = G + NP * 2 * TILE, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
     static constexpr int STAGES = NP == 1 ? 2 : 1;
-    static constexpr int BUF = STAGES * STAGE, BUFFER = 3 * KT * TILE, AUX = BUF + 2 * BUFFER;
-    static constexpr int POW = AUX, SUMS = POW + 4 * 80, BARS = SUMS + 8 * kDecWarps, BYTES = BARS + 256 + 1024;
+    static constexpr int BUF = STAGES * STAGE, PLANE = 2 * KT * TILE, AUX = BUF + 3 * PLANE;   // [plane][weight][KT tiles]
+    static constexpr int POW = AUX, PAIR = POW + 4 * 80, SUMS = PAIR + 4 * 128, BARS = SUMS + 8 * kDecWarps, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    static constexpr int A = 0, A1 = KP, W = 2 * KP, W1 = 3 * KP;  // (the pairs' products in A1's place, 2 x 64 columns)
+    static constexpr int A = 0, A1 = KP, W = 2 * KP, W1 = 3 * KP;  // A', W' behind A and W (the pairs' products in A1's place, 2 x 64 columns)
     static_assert(KP >= 64 && 4 * KP <= 512, "tensor memory");
     static constexpr int PQ = KP == 128 ? A1 : 4 * KP, PG = PQ + 64;
 };
 
-enum { D_FULL = 0, D_BULK = 2, D_EMPTY = 4, D_MUL = 6, D_CONV = 10, D_PAIR = 14, D_PREAD, D_A1READ, D_DRAIN, D_COUNT };
+enum { D_FULL = 0, D_BULK = 2, D_EMPTY = 4, D_MUL = 6, D_CONV = 8, D_PAIR = 10, D_READ, D_DRAIN, D_COUNT };
 
 struct DecayArgs {
     const float *g;
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             mbar_init(bar + D_EMPTY + i, 1);
         }
         for (int i = D_MUL; i < D_COUNT; ++i)
-            mbar_init(bar + i, (i >= D_CONV && i < D_PAIR) || i == D_PREAD || i == D_A1READ ? kDecWarps : 1);
+            mbar_init(bar + i, (i >= D_CONV && i < D_PAIR) || i == D_READ ? kDecWarps : 1);
         *dead = a.status->code != 0;
         fence_mbar_init();
     }
@@ -91,7 +94,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (tid <= C) pw[tid] = linear_power(a.g[h], tid);
+    float *pair = reinterpret_cast<float *>(smem + L::PAIR);
+    if (tid < 128) {
+        // e^{L n}, and n e^{L n} of tokens n apart (0 before)
+        const int n = tid < C ? C - tid : tid - C;
+        const float x = linear_power(a.g[h], n);
+        pw[n] = x;
+        if (tid == C) pw[0] = 1.f;
+        pair[tid] = tid < C ? 0.f : (float)n * x;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -126,12 +137,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             tc_fence_after();
             return there;
         };
-        // rows of Q or K times their weights, as planes in a buffer
-        auto convert = [&](const unsigned char *src, unsigned char *dst, auto weight) {
+        // rows of Q or K times their two weights, as planes
+        auto convert = [&](const unsigned char *src, auto weights) {
 #pragma unroll
             for (int i = tid; i < C * KP / 8; i += 32 * kDecWarps) {
                 const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
-                scale_piece<NP, KT * TILE>(src, dst, off, weight(row));
+                const float2 w = weights(row);
+                float2 x[4];
+                load_piece<NP, KT * TILE>(src + off, x);
+                scale_piece(x, w.x, smem + L::BUF + off, L::PLANE);
+                scale_piece(x, w.y, smem + L::BUF + KT * TILE + off, L::PLANE);
             }
             fence_proxy_async_smem();
         };
@@ -157,50 +172,47 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int i = 0; i < 16; ++i) s[c + i] = fmaf(w, s[c + i], x[i]);
             }
         };
-        unsigned char *buf0 = smem + L::BUF, *buf1 = buf0 + L::BUFFER;
         float whole = 1.f;
         bool ok = true;
         for (int it = 0; it < nch; ++it) {
             const int nt = ntok - (n0 + it) * C < C ? ntok - (n0 + it) * C : C;
             const unsigned char *st = smem + it % ST * L::STAGE;
-            ok = tc_warp_wait(bar + D_FULL + it % ST, it / ST & 1, dead, d.spin) && (it == 0 || wait(D_MUL + 2, it - 1));
-            if (!ok) break;
-            convert(st + L::Q, buf0, [&](int t) { return t < nt ? d.scale * pw[t + 1] : 0.f; });
-            arrive(D_CONV);
-            if (it > 0) advance(L::W, whole, S);
             // the pairs: a token's row each of lanes 0..63
             if (!(ok = wait(D_PAIR, it))) break;
             if ((warp & 3) < 2) {
-                const int row = lane0 + lane;
+                const float *apart = pair + C + lane0 + lane - 16 * part;
                 float x[16], y[16], sum = 0.f;
                 tc_load16(at + L::PQ + 16 * part, x);
                 tc_load16(at + L::PG + 16 * part, y);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int apart = row - 16 * part - i;
-                    if (apart > 0) sum = fmaf(apart * pw[apart] * x[i], y[i], sum);
-                }
+                for (int i = 0; i < 16; ++i) sum = fmaf(apart[-i] * x[i], y[i], sum);
                 add(d.scale * sum);
             }
-            arrive(D_PREAD);
-            if (it > 0 && !(ok = wait(D_MUL + 3, it - 1))) break;
-            convert(st + L::Q, buf1, [&](int t) { return t < nt ? (t + 1) * (d.scale * pw[t + 1]) : 0.f; });
-            arrive(D_CONV + 1);
-            if (it > 0) advance(L::W1, 1.f, G);
+            ok = tc_warp_wait(bar + D_FULL + it % ST, it / ST & 1, dead, d.spin) && (it == 0 || wait(D_MUL + 1, it - 1));
+            if (!ok) break;
+            convert(st + L::Q, [&](int t) {
+                const float w = t < nt ? d.scale * pw[t + 1] : 0.f;
+                return make_float2(w, (float)(t + 1) * w);
+            });
+            arrive(D_CONV);
+            if (it > 0) {
+                advance(L::W, whole, S);
+                advance(L::W1, 1.f, G);
+            }
             if (!(ok = wait(D_MUL, it))) break;
-            convert(st + L::K, buf0, [&](int t) { return t < nt ? pw[nt - 1 - t] : 0.f; });
-            arrive(D_CONV + 2);
+            convert(st + L::K, [&](int t) {
+                const float w = t < nt ? pw[nt - 1 - t] : 0.f;
+                return make_float2(w, (float)(nt - 1 - t) * w);
+            });
+            arrive(D_CONV + 1);
             dot(L::A, G);
-            if (!(ok = wait(D_MUL + 1, it))) break;
-            convert(st + L::K, buf1, [&](int t) { return t < nt ? (nt - 1 - t) * pw[nt - 1 - t] : 0.f; });
-            arrive(D_CONV + 3);
             dot(L::A1, S);
-            arrive(D_A1READ);
+            arrive(D_READ);
             whole = pw[nt];
 #pragma unroll
             for (int i = 0; i < HD; ++i) G[i] = whole * fmaf((float)nt, S[i], G[i]);
         }
-        if (ok && nch > 0 && wait(D_MUL + 3, nch - 1)) {
+        if (ok && nch > 0 && wait(D_MUL + 1, nch - 1)) {
             advance(L::W1, 1.f, G);
             if (a.ends && mine) {
                 const float *end = a.ends + (d.segs - 1 - seg) * states + own;
@@ -239,7 +251,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             scores(tu + L::PG, tc_k_major(st + L::G), tc_k_major(st + L::V), std::integral_constant<int, 2>{});
             tc_commit_to(one, bar + D_PAIR);
         };
-        auto product = [&](uint32_t dst, uint32_t vm, uint32_t kn) {
+        const uint32_t kn = tc_n_major(base + L::BUF, TILE);
+        auto product = [&](uint32_t dst, uint32_t vm) {
             bool add = false;
 #pragma unroll
             for (int sum = 2; sum >= 0; --sum)
@@ -247,8 +260,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks) {
-                        tc_mma_ss(one, dst, vm + (m * 2 * TILE + 2048 * ks) / 16, kn + ((sum - m) * KT * TILE + 2048 * ks) / 16,
-                                  tc_idesc<true, true>(KP), add);
+                        tc_mma_ss(one, dst, vm + (m * 2 * TILE + 2048 * ks) / 16, kn + ((sum - m) * L::PLANE + 2048 * ks) / 16,
+                                  tc_idesc<true, true>(2 * KP), add);
                         add = true;
                     }
         };
@@ -256,22 +269,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         tc_fence_after();
         if (ok) pairs(0);
         for (int it = 0; ok && it < nch; ++it) {
-            const uint32_t st = base + it % ST * L::STAGE, gm = tc_n_major(st + L::G, TILE), vm = tc_n_major(st + L::V, TILE);
-            const uint32_t b0 = tc_n_major(base + L::BUF, TILE), b1 = tc_n_major(base + L::BUF + L::BUFFER, TILE);
+            const uint32_t st = base + it % ST * L::STAGE;
             const unsigned par = it & 1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ok = ok && tc_warp_wait(bar + D_CONV + i, par, dead, d.spin) && (i != 1 || tc_warp_wait(bar + D_PREAD, par, dead, d.spin));
+            for (int i = 0; i < 2; ++i) {
+                ok = ok && tc_warp_wait(bar + D_CONV + i, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
-                product(tu + (i == 0 ? L::A : i == 1 ? L::A1 : i == 2 ? L::W : L::W1), i < 2 ? gm : vm, i & 1 ? b1 : b0);
+                product(tu + (i == 0 ? L::A : L::W), tc_n_major(st + (i == 0 ? L::G : L::V), TILE));
                 tc_commit_to(one, bar + D_MUL + i);
             }
             if (!ok) break;
             tc_commit_to(one, bar + D_EMPTY + it % ST);
             if (it + 1 < nch) {
-                ok = tc_warp_wait(bar + D_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin) &&
-                     tc_warp_wait(bar + D_A1READ, par, dead, d.spin);
+                ok = tc_warp_wait(bar + D_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin) && tc_warp_wait(bar + D_READ, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
                 pairs(it + 1);

@@ -191,7 +191,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 for (int i = id; i < C * KP / 8; i += THREADS) {
                     const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
                     const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
-                    scale_piece<NP, KT * TILE>(src, smem + L::KX, off, w);
+                    float2 x[4];
+                    load_piece<NP, KT * TILE>(src + off, x);
+                    scale_piece(x, w, smem + L::KX + off, KT * TILE);
                 }
             } else {
                 // blocks that lie past the diagonal whole are not read

@@ -62,13 +62,12 @@ __device__ __forceinline__ void store_planes3(uint32_t hi, uint32_t mid, uint32_
     tc_store8(lo, p[2]);
 }
 
-// 8 columns of a row of a [64 tokens] tile of NP planes (PLANE bytes apart), times w, as three planes
-template <int NP, int PLANE>
-__device__ __forceinline__ void scale_piece(const unsigned char *src, unsigned char *dst, int off, float w) {
-    float2 x[4];
+// 8 columns of a row of a [64 tokens] tile whose NP planes lie SRC bytes apart
+template <int NP, int SRC>
+__device__ __forceinline__ void load_piece(const unsigned char *src, float2 (&x)[4]) {
 #pragma unroll
     for (int m = NP - 1; m >= 0; --m) {
-        const uint4 r = *reinterpret_cast<const uint4 *>(src + m * PLANE + off);
+        const uint4 r = *reinterpret_cast<const uint4 *>(src + m * SRC);
         const unsigned u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -76,16 +75,19 @@ __device__ __forceinline__ void scale_piece(const unsigned char *src, unsigned c
             x[e] = m == NP - 1 ? y : make_float2(x[e].x + y.x, x[e].y + y.y);
         }
     }
+}
+// such a piece times w, as three planes `plane` bytes apart
+__device__ __forceinline__ void scale_piece(const float2 (&x)[4], float w, unsigned char *dst, int plane) {
     unsigned pl[3][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         unsigned s[3];
-        x[e] = mul2(x[e], make_float2(w, w));
-        split3(x[e].x, x[e].y, s);
+        const float2 y = mul2(x[e], make_float2(w, w));
+        split3(y.x, y.y, s);
         pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
     }
 #pragma unroll
-    for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4 *>(dst + m * PLANE + off) = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
+    for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4 *>(dst + m * plane) = make_uint4(pl[m][0], pl[m][1], pl[m][2], pl[m][3]);
 }
 
 }  // namespace sdm
