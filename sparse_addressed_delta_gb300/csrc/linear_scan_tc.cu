@@ -1,9 +1,9 @@
 // Linear attention's pass (linear_internal.cuh) over a head's chunks of 64 tokens on the 5th-generation tensor
 // cores. Everything is transposed: 128 of the result's columns are the 128 lanes of tensor memory. With L the
 // head's log-decay, i and j tokens of a chunk that begins with state S (a mirrored pass has i and j exchanged):
-//   Z = (Q K^T) e^{L (i - j)} for j <= i, else 0          P, then planes in shared memory
+//   Z = (Q K^T) e^{L (i - j)} for j <= i, else 0          P (transposed), then planes in shared memory
 //   o = e^{L (i + 1)} (S^T Q^T) + V^T Z^T                 OA and OB
-//   S = e^{L n} S + V^T (e^{L (n - 1 - j)} K)              U
+//   S = e^{L n} S + V^T (e^{L (n - 1 - j)} K)              U, in one product with OB
 // A float operand (S, Z, the decayed keys) goes in as three bfloat16 planes (24 bits), so results keep float32's
 // accuracy and bfloat16 ones differ from float32 arithmetic's only where that rounds the other way. float32 inputs
 // come as three planes too (NP = 3), with six of their products. The state stays in registers in float32; the
@@ -30,14 +30,17 @@ struct LinScan {
     static constexpr int TILE = kLinC * 128, KT = KP / 64;         // 64 columns of 64 tokens; such tiles of Q or K
     static constexpr int Q = 0, K = Q + NP * KT * TILE, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
     static constexpr int STAGES = NP == 1 ? 3 : 1;
-    static constexpr int KX = STAGES * STAGE, Z = KX + 3 * KT * TILE, AUX = Z + 3 * TILE;   // decayed keys, Z: planes
+    // planes of the decayed keys and, in the same rows behind them, of Z^T
+    static constexpr int PLANE = (KT + 1) * TILE, KX = STAGES * STAGE, Z = KX + KT * TILE, AUX = KX + 3 * PLANE;
+    // a carry has no queries: a second buffer of decayed keys in their place
+    static constexpr int KX2 = Q, PLANE2 = NP == 1 ? STAGE : KT * TILE;
     static constexpr int POW = AUX, PAIR = POW + 4 * 80, BAD = PAIR + 4 * 128, BARS = BAD + 4 * 512, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    static constexpr int SP = 0, OA = 3 * (KP / 2), OB = OA + kLinC, U = OB + kLinC, P = U + KP;
+    static constexpr int SP = 0, OA = 3 * (KP / 2), U = OA + kLinC, OB = U + KP, P = OB + kLinC;
     static_assert(P + kLinC <= 512, "tensor memory");
 };
 
-enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_P = 9, B_ZK, B_U, B_UF, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
+enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_ZK = 9, B_U = 11, B_UF = 13, B_P = 15, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
 
 enum { LIN_RUN, LIN_CARRY };
 
@@ -134,7 +137,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             mbar_init(bar + B_BULK + i, 1);
             mbar_init(bar + B_EMPTY + i, !CARRY && sizeof(OT) == 2 ? 2 : 1);
         }
-        for (int i = B_P; i < B_COUNT; ++i) mbar_init(bar + i, i == B_ZK || i == B_UF || i == B_OF || i == B_S || i == B_OUT ? kLinWarps : 1);
+        for (int i = B_ZK; i < B_COUNT; ++i)
+            mbar_init(bar + i, i < B_U || i == B_UF || i == B_UF + 1 || i == B_OF || i == B_S || i == B_OUT ? kLinWarps : 1);
         *dead = a.status->code != 0;                               // an earlier kernel of this call gave up
         fence_mbar_init();
     }
@@ -150,10 +154,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (tid == C) pw[0] = 1.f;
         pair[tid] = tid < C ? 0.f : p.pair * x;
     }
+    if (!CARRY)                                                    // blocks of Z^T that hold no pairs are never written again
+        for (int i = tid; i < 3 * TILE / 16; i += kLinThreads)
+            *reinterpret_cast<uint4 *>(smem + L::Z + i / (TILE / 16) * L::PLANE + i % (TILE / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *slot;
+    // a carry's chunks go through two buffers of decayed keys and two of U in turn
+    auto turn = [](int it) { return CARRY ? it & 1 : 0; };
+    auto phase = [](int it) { return (unsigned)(CARRY ? it >> 1 : it) & 1; };
     auto chunk_at = [&](int it) { return REV ? n0 + nch - 1 - it : n0 + it; };
     int first = -1;                                                // iteration of the column's first update that is not finite
     float2 S[HD / 2];
@@ -163,8 +174,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const bool mine = col < p.V;
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
         const float *begin = CARRY ? nullptr : d.segs > 1 ? a.starts + seg * states : p.first;
+        if (begin) begin += own + kk * p.sk + col * p.sv;
+        if (p.sk == 1 && ((uintptr_t)begin & 15) == 0) {           // transposed: K runs along the row
 #pragma unroll
-        for (int i = 0; i < HD; ++i) reinterpret_cast<float *>(S)[i] = begin && mine && kk + i < K ? begin[own + (kk + i) * p.sk + col * p.sv] : 0.f;
+            for (int i = 0; i < HD / 4; ++i) {
+                const float4 x = begin && mine && kk + 4 * i < K ? *reinterpret_cast<const float4 *>(begin + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                S[2 * i] = make_float2(x.x, x.y);
+                S[2 * i + 1] = make_float2(x.z, x.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < HD; ++i) reinterpret_cast<float *>(S)[i] = begin && mine && kk + i < K ? begin[i * p.sk] : 0.f;
+        }
         auto planes_of_s = [&] {
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
@@ -178,7 +199,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + which);
         };
-        // Z (lanes 0..63: a token's row each) and the decayed keys (the other lanes) of chunk `it`
+        // Z^T (lanes 0..63: a key's row each) and the decayed keys (the other lanes) of chunk `it`
         auto local = [&](int it) {
             const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
             if (!CARRY && !tc_warp_wait(bar + B_P, it & 1, dead, d.spin)) return false;   // (and the products that read them last)
@@ -193,25 +214,24 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
                     float2 x[4];
                     load_piece<NP, KT * TILE>(src + off, x);
-                    scale_piece(x, w, smem + L::KX + off, KT * TILE);
+                    scale_piece(x, w, smem + (turn(it) ? L::KX2 : L::KX) + off, turn(it) ? L::PLANE2 : L::PLANE);
                 }
             } else {
-                // blocks that lie past the diagonal whole are not read
-                const int row = lane0 + lane, ahead = REV ? 16 * part - lane0 - 31 : lane0 - 16 * part - 15;   // least tokens apart
+                const int row = lane0 + lane, ahead = REV ? lane0 - 16 * part - 15 : 16 * part - lane0 - 31;   // least tokens apart
                 if (ahead >= -46) {
                     tc_fence_after();
                     float2 x[8];
                     tc_load16(at + L::P + 16 * part, reinterpret_cast<float(&)[16]>(x));
                     if (ahead >= 0) {                              // e^{L apart} = e^{L least} e^{L rest}, all of it before the diagonal
-                        const float w = pair[C + (REV ? 16 * part - row : row - 16 * part - 15)];
+                        const float w = pair[C + (REV ? row - 16 * part - 15 : 16 * part - row)];
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            x[i] = mul2(mul2(x[i], make_float2(w, w)), REV ? make_float2(pw[2 * i], pw[2 * i + 1]) : make_float2(pw[15 - 2 * i], pw[14 - 2 * i]));
+                            x[i] = mul2(mul2(x[i], make_float2(w, w)), REV ? make_float2(pw[15 - 2 * i], pw[14 - 2 * i]) : make_float2(pw[2 * i], pw[2 * i + 1]));
                     } else {
-                        const int apart = REV ? 16 * part - row : row - 16 * part;   // of column 0; the others' step by step
+                        const int apart = REV ? row - 16 * part : 16 * part - row;   // of column 0; the others' step by step
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const int a0 = REV ? apart + 2 * i : apart - 2 * i, a1 = REV ? a0 + 1 : a0 - 1;
+                            const int a0 = REV ? apart - 2 * i : apart + 2 * i, a1 = REV ? a0 - 1 : a0 + 1;
                             x[i].x = a0 >= 0 ? x[i].x * pair[C + a0] : 0.f;
                             x[i].y = a1 >= 0 ? x[i].y * pair[C + a1] : 0.f;
                         }
@@ -227,12 +247,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     for (int m = 0; m < 3; ++m)
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-                            *reinterpret_cast<uint4 *>(smem + L::Z + m * TILE + tc_at(row, 2 * part + c)) =
+                            *reinterpret_cast<uint4 *>(smem + L::Z + m * L::PLANE + tc_at(row, 2 * part + c)) =
                                 make_uint4(pl[m][4 * c], pl[m][4 * c + 1], pl[m][4 * c + 2], pl[m][4 * c + 3]);
                 }
             }
             fence_proxy_async_smem();
-            arrive(B_ZK);
+            arrive(B_ZK + turn(it));
             return true;
         };
         // bfloat16 results, 8 x 8 blocks stored transposed: block i of a store is 8 columns (i % 2) and 8 tokens (i / 2), a
@@ -252,23 +272,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int it = 0; ok && it < nch; ++it) {
             const unsigned par = it & 1;
             const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
-            ok = tc_warp_wait(bar + B_U, par, dead, d.spin);
+            if (CARRY && it + 1 < nch && !(ok = local(it + 1))) break;
+            ok = tc_warp_wait(bar + B_U + turn(it), phase(it), dead, d.spin);
             if (!ok) break;
             tc_fence_after();
             const float whole = pw[nt];
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
                 float2 x[8];
-                tc_load16(at + L::U + kk + c, reinterpret_cast<float(&)[16]>(x));
+                tc_load16(at + (turn(it) ? L::SP : L::U) + kk + c, reinterpret_cast<float(&)[16]>(x));
                 if (!CARRY && c == 0 && first < 0 && !(fabsf(x[0].x) <= 3.402823466e38f)) first = it;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) S[c / 2 + i] = fma2(make_float2(whole, whole), S[c / 2 + i], x[i]);
             }
-            arrive(B_UF);
-            if (it + 1 < nch) {
-                ok = local(it + 1);
-                if (!ok) break;
-            }
+            arrive(B_UF + turn(it));
+            if (!CARRY && it + 1 < nch && !(ok = local(it + 1))) break;
             if constexpr (!CARRY) {
                 ok = tc_warp_wait(bar + B_O, par, dead, d.spin);
                 if (!ok) break;
@@ -326,8 +344,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
         constexpr int KS = KP / 16;
-        const uint32_t zd = tc_k_major(base + L::Z), kx = tc_n_major(base + L::KX, TILE);
-        auto scores = [&](int it) {                                // lanes 64.. hold whatever follows Q
+        auto scores = [&](int it) {                                // K Q^T; lanes 64.. hold whatever follows K
             const uint32_t st = base + it % ST * L::STAGE, qd = tc_k_major(st + L::Q), kd = tc_k_major(st + L::K);
             bool add = false;
 #pragma unroll
@@ -337,7 +354,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         const int off = ((ks >> 2) * TILE + 32 * (ks & 3)) / 16;
-                        tc_mma_ss(one, tu + L::P, qd + m * KT * TILE / 16 + off, kd + (sum - m) * KT * TILE / 16 + off, tc_idesc<false>(C), add);
+                        tc_mma_ss(one, tu + L::P, kd + m * KT * TILE / 16 + off, qd + (sum - m) * KT * TILE / 16 + off, tc_idesc<false>(C), add);
                         add = true;
                     }
             tc_commit_to(one, bar + B_P);
@@ -350,11 +367,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         for (int it = 0; ok && it < nch; ++it) {
             const uint32_t st = base + it % ST * L::STAGE, qd = tc_k_major(st + L::Q), vm = tc_n_major(st + L::V, TILE);
+            const uint32_t kx = tc_n_major(base + (turn(it) ? L::KX2 : L::KX), TILE), plane = (turn(it) ? L::PLANE2 : L::PLANE) / 16;
             const unsigned par = it & 1;
-            ok = tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin) && tc_warp_wait(bar + B_ZK, par, dead, d.spin) &&
-                 (it == 0 || tc_warp_wait(bar + B_UF, par ^ 1, dead, d.spin));
+            ok = tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin) && tc_warp_wait(bar + B_ZK + turn(it), phase(it), dead, d.spin);
+            if (CARRY) ok = ok && (it < 2 || tc_warp_wait(bar + B_UF + turn(it), phase(it) ^ 1, dead, d.spin));
+            else ok = ok && (it == 0 || (tc_warp_wait(bar + B_UF, par ^ 1, dead, d.spin) && tc_warp_wait(bar + B_OF, par ^ 1, dead, d.spin)));
             if (!ok) break;
             tc_fence_after();
+            // U and, in the columns behind it, OB: V^T is read once for both
             bool add = false;
 #pragma unroll
             for (int sum = 2; sum >= 0; --sum)
@@ -362,30 +382,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks) {
-                        tc_mma_ss(one, tu + L::U, vm + (m * 2 * TILE + 2048 * ks) / 16, kx + ((sum - m) * KT * TILE + 2048 * ks) / 16,
-                                  tc_idesc<true, true>(KP), add);
+                        tc_mma_ss(one, tu + (turn(it) ? L::SP : L::U), vm + (m * 2 * TILE + 2048 * ks) / 16, kx + (sum - m) * plane + 2048 * ks / 16,
+                                  tc_idesc<true, true>(CARRY ? KP : KP + C), add);
                         add = true;
                     }
-            tc_commit_to(one, bar + B_U);
+            tc_commit_to(one, bar + B_U + turn(it));
             if constexpr (!CARRY) {
-                if (it > 0) {
-                    ok = tc_warp_wait(bar + B_OF, par ^ 1, dead, d.spin);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                // Z is triangular: the 16 tokens of step ks reach those from 16 ks on (mirrored: up to 16 ks + 15)
-                add = false;
-#pragma unroll
-                for (int sum = 2; sum >= 0; --sum)
-#pragma unroll
-                    for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
-#pragma unroll
-                        for (int i = 0; i < C / 16; ++i) {
-                            const int ks = REV ? C / 16 - 1 - i : i, row = REV ? 0 : 16 * ks;
-                            tc_mma_ss(one, tu + L::OB + row, vm + (m * 2 * TILE + 2048 * ks) / 16,
-                                      zd + ((sum - m) * TILE + row * 128 + 32 * ks) / 16, tc_idesc<false, true>(REV ? 16 * ks + 16 : C - row), add);
-                            add = true;
-                        }
                 if (ST > 1 && it + 1 < nch) {
                     ok = tc_warp_wait(bar + B_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin);
                     if (!ok) break;
@@ -451,7 +453,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (nt < C) {                                          // what lies past the valid tokens is not used
                 for (int i = lane; i < (C - nt) * 8; i += 32) {
                     const int off = tc_at(nt + (i >> 3), i & 7);
-                    for (int c = 0; c < L::STAGE / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int c = CARRY ? NP * KT : 0; c < L::STAGE / TILE; ++c)   // (a carry has a buffer where Q is)
+                        *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
