@@ -25,22 +25,22 @@ namespace {
 
 constexpr int kLinC = 64, kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 3);
 
-template <int KP, int NP>
+// CARRY: no queries, no Z; more stages of less, and two buffers of decayed keys
+template <int KP, int NP, bool CARRY>
 struct LinScan {
     static constexpr int TILE = kLinC * 128, KT = KP / 64;         // 64 columns of 64 tokens; such tiles of Q or K
-    static constexpr int Q = 0, K = Q + NP * KT * TILE, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
-    static constexpr int STAGES = NP == 1 ? 3 : 1;
+    static constexpr int Q = 0, K = Q + (CARRY ? 0 : NP * KT * TILE), V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
+    static constexpr int STAGES = NP == 3 ? 1 : CARRY ? 4 : 3;
     // planes of the decayed keys and, in the same rows behind them, of Z^T
-    static constexpr int PLANE = (KT + 1) * TILE, KX = STAGES * STAGE, Z = KX + KT * TILE, AUX = KX + 3 * PLANE;
-    // a carry has no queries: a second buffer of decayed keys in their place
-    static constexpr int KX2 = Q, PLANE2 = NP == 1 ? STAGE : KT * TILE;
-    static constexpr int POW = AUX, PAIR = POW + 4 * 80, BAD = PAIR + 4 * 128, BARS = BAD + 4 * 512, BYTES = BARS + 256 + 1024;
+    static constexpr int PLANE = (CARRY ? KT : KT + 1) * TILE, KX = STAGES * STAGE, KX2 = KX + 3 * PLANE, Z = KX + KT * TILE;
+    static constexpr int AUX = CARRY ? KX2 + 3 * PLANE : KX2;
+    static constexpr int POW = AUX, PAIR = POW + 4 * 80, BARS = PAIR + 4 * 128, BAD = BARS + 256, BYTES = BAD + (CARRY ? 0 : 4 * 512) + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
     static constexpr int SP = 0, OA = 3 * (KP / 2), U = OA + kLinC, OB = U + KP, P = OB + kLinC;
     static_assert(P + kLinC <= 512, "tensor memory");
 };
 
-enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_ZK = 9, B_U = 11, B_UF = 13, B_P = 15, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
+enum { B_FULL = 0, B_BULK = 4, B_EMPTY = 8, B_ZK = 12, B_U = 14, B_UF = 16, B_P = 18, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
 
 enum { LIN_RUN, LIN_CARRY };
 
@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear_scan(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const __grid_constant__ LinearDims d,
                   const __grid_constant__ LinArgs a) {
-    using L = LinScan<KP, NP>;
-    constexpr int C = kLinC, HD = KP / 4, ST = L::STAGES, KT = L::KT, TILE = L::TILE;
     constexpr bool CARRY = MODE == LIN_CARRY;
+    using L = LinScan<KP, NP, CARRY>;
+    constexpr int C = kLinC, HD = KP / 4, ST = L::STAGES, KT = L::KT, TILE = L::TILE;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     auto bar = reinterpret_cast<unsigned long long *>(smem + L::BARS);
@@ -199,27 +199,46 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + which);
         };
-        // Z^T (lanes 0..63: a key's row each) and the decayed keys (the other lanes) of chunk `it`
+        // The decayed keys, in units of 8 columns of 32 tokens, and Z^T (by lanes 0..63 of tensor memory, a key's row each)
+        // of chunk `it`. A scheduler has every fourth warp, so those of the other lanes, and those whose block of Z^T holds
+        // no pairs, take more of the units: 3, 3, 3 and, with a block off the diagonal, 1 of each 4 x 4 (a narrow state: half
+        // of them each). Measured, 32 heads x 256 chunks: all units by the other lanes' warps 145 us, so @@.
+        const int ahead = REV ? lane0 - 16 * part - 15 : 16 * part - lane0 - 31;   // least tokens apart
+        int unit0, unit1;
+        {
+            constexpr int UNITS = 2 * KP / 8;                      // 32 or 16
+            if (CARRY) {
+                unit0 = warp * (UNITS / 16);
+                unit1 = unit0 + UNITS / 16;
+            } else {
+                // warps of lanes 64..: 3 of each 4; without pairs: 3; off the diagonal: 1; on it: none
+                const bool other = (warp & 3) >= 2;
+                const int none = REV ? (warp & 3) == 0 && part >= 2 : (warp & 3) == 1 && part < 2;
+                const int off = REV ? (warp & 3) == 1 && part < 2 : (warp & 3) == 0 && part >= 2;
+                const int at_other = part * 2 + (warp & 1), at_rest = part & 1;
+                const int from = other ? 3 * at_other : none ? 24 + 3 * at_rest : off ? 30 + at_rest : 32, many = other || none ? 3 : off ? 1 : 0;
+                unit0 = from * UNITS / 32;
+                unit1 = (from + many) * UNITS / 32;
+            }
+        }
         auto local = [&](int it) {
             const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
-            if (!CARRY && !tc_warp_wait(bar + B_P, it & 1, dead, d.spin)) return false;   // (and the products that read them last)
-            if (CARRY || (warp & 3) >= 2) {
-                constexpr int THREADS = CARRY ? 512 : 256;
-                const int id = CARRY ? tid : part * 64 + ((warp & 3) - 2) * 32 + lane;
-                if (!tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin)) return false;
+            if (!tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin)) return false;
+            {
                 const unsigned char *src = smem + it % ST * L::STAGE + L::K;
-#pragma unroll
-                for (int i = id; i < C * KP / 8; i += THREADS) {
-                    const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
+                for (int i = unit0; i < unit1; ++i) {
+                    const int row = 32 * (i & 1) + lane, piece = i >> 1, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
                     const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
                     float2 x[4];
                     load_piece<NP, KT * TILE>(src + off, x);
-                    scale_piece(x, w, smem + (turn(it) ? L::KX2 : L::KX) + off, turn(it) ? L::PLANE2 : L::PLANE);
+                    scale_piece(x, w, smem + (turn(it) ? L::KX2 : L::KX) + off, L::PLANE);
                 }
-            } else {
-                const int row = lane0 + lane, ahead = REV ? lane0 - 16 * part - 15 : 16 * part - lane0 - 31;   // least tokens apart
-                if (ahead >= -46) {
-                    tc_fence_after();
+            }
+            if (!CARRY && (warp & 3) < 2 && ahead >= -46) {
+                if (!tc_warp_wait(bar + B_P, it & 1, dead, d.spin)) return false;
+                tc_fence_after();
+                {
+                    const int row = lane0 + lane;
                     float2 x[8];
                     tc_load16(at + L::P + 16 * part, reinterpret_cast<float(&)[16]>(x));
                     if (ahead >= 0) {                              // e^{L apart} = e^{L least} e^{L rest}, all of it before the diagonal
@@ -232,8 +251,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int a0 = REV ? apart - 2 * i : apart + 2 * i, a1 = REV ? a0 - 1 : a0 + 1;
-                            x[i].x = a0 >= 0 ? x[i].x * pair[C + a0] : 0.f;
-                            x[i].y = a1 >= 0 ? x[i].y * pair[C + a1] : 0.f;
+                            const float2 y = mul2(x[i], make_float2(pair[C + a0], pair[C + a1]));
+                            x[i] = make_float2(a0 >= 0 ? y.x : 0.f, a1 >= 0 ? y.y : 0.f);   // (a NaN past the diagonal stays out)
                         }
                     }
                     unsigned pl[3][8];
@@ -339,7 +358,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             }
         }
-        reinterpret_cast<int *>(smem + L::BAD)[part * 128 + lane0 + lane] = first;
+        if (!CARRY) reinterpret_cast<int *>(smem + L::BAD)[part * 128 + lane0 + lane] = first;   // (a carry has no room for it)
     } else if (warp == kLinWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
@@ -367,7 +386,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         for (int it = 0; ok && it < nch; ++it) {
             const uint32_t st = base + it % ST * L::STAGE, qd = tc_k_major(st + L::Q), vm = tc_n_major(st + L::V, TILE);
-            const uint32_t kx = tc_n_major(base + (turn(it) ? L::KX2 : L::KX), TILE), plane = (turn(it) ? L::PLANE2 : L::PLANE) / 16;
+            const uint32_t kx = tc_n_major(base + (turn(it) ? L::KX2 : L::KX), TILE), plane = L::PLANE / 16;
             const unsigned par = it & 1;
             ok = tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin) && tc_warp_wait(bar + B_ZK + turn(it), phase(it), dead, d.spin);
             if (CARRY) ok = ok && (it < 2 || tc_warp_wait(bar + B_UF + turn(it), phase(it) ^ 1, dead, d.spin));
@@ -453,8 +472,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (nt < C) {                                          // what lies past the valid tokens is not used
                 for (int i = lane; i < (C - nt) * 8; i += 32) {
                     const int off = tc_at(nt + (i >> 3), i & 7);
-                    for (int c = CARRY ? NP * KT : 0; c < L::STAGE / TILE; ++c)   // (a carry has a buffer where Q is)
-                        *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int c = 0; c < L::STAGE / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
@@ -550,7 +568,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
 template <int KP, int NP, int MODE, bool REV, typename OT>
 cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, cudaStream_t st) {
     auto kern = k_linear_scan<KP, NP, MODE, REV, OT>;
-    using L = LinScan<KP, NP>;
+    using L = LinScan<KP, NP, MODE == LIN_CARRY>;
     set_kernel_smem(kern, L::BYTES);
     const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * (MODE == LIN_CARRY ? d.segs - 1 : d.segs);
     kern<<<(unsigned)blocks, kLinThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
