@@ -26,7 +26,8 @@ SOURCES = ["api.cu", "phase1.cu", "solve.cu", "phase2.cu", "dualmm_tc.cu", "phas
            "norm.cu", "delta.cu", "delta_step.cu", "delta_chunk.cu",
            "delta_back.cu", "delta_scan_tc.cu", "delta_back_tc.cu",
            "delta_back_local_tc.cu", "linear.cu", "linear_step.cu",
-           "linear_scan_tc.cu", "linear_decay_tc.cu", "group_norm.cu"]
+           "linear_scan_tc.cu", "linear_carry_tc.cu",
+           "linear_decay_tc.cu", "group_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -140,14 +140,6 @@ cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char
     return launch_linear_lay(d, lay, n, st);
 }
 
-// the states that a pass's segments begin with, into starts
-cudaError_t linear_carry(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], float *starts, void *status,
-                         cudaStream_t st) {
-    if (d.segs == 1) return cudaSuccess;
-    const cudaError_t e = launch_linear_scan(d, p, in, laid, starts, true, status, st);
-    return e == cudaSuccess ? launch_linear_join(d, in, p.first, p.reverse, starts, st) : e;
-}
-
 LinearOperand operand(const void *p, const long long *s, int share) { return LinearOperand{p, {s[0], s[1], s[2]}, share}; }
 
 // sdm_linear_attention and, with `save`, sdm_linear_attention_save
@@ -183,8 +175,8 @@ int linear_forward(const sdm_linear_shape *shape, float *state, const void *q, c
         e = cudaMemcpyAsync(saved, state, (size_t)linear_states(d) * 4, cudaMemcpyDeviceToDevice, st);
     if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, nullptr}, laid, st);
     float *starts = save ? static_cast<float *>(saved) : reinterpret_cast<float *>(ws + l.starts);
-    if (e == cudaSuccess) e = linear_carry(d, p, in, {laid[0], laid[1], laid[2]}, starts, ws, st);
-    if (e == cudaSuccess) e = launch_linear_scan(d, p, in, {laid[0], laid[1], laid[2]}, starts, false, ws, st);
+    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, p, in, laid[1], laid[2], starts, ws, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, p, in, {laid[0], laid[1], laid[2]}, starts, ws, st);
     return linear_status(e);
 }
 
@@ -268,16 +260,16 @@ int sdm_linear_attention_backward(const sdm_linear_shape *shape, const void *q, 
     cudaError_t e = linear_clear(workspace, workspace_bytes, st);
     if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, st);
     float *ends = reinterpret_cast<float *>(ws + l.starts);
-    if (e == cudaSuccess) e = launch_linear_scan(d, pq, in, {laid[3], laid[2], laid[1]}, const_cast<float *>(first), false, ws, st);
-    if (e == cudaSuccess) e = linear_carry(d, pv, in, {laid[1], laid[0], laid[3]}, ends, ws, st);
-    if (e == cudaSuccess) e = launch_linear_scan(d, pk, in, {laid[2], laid[3], laid[0]}, ends, false, ws, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, pq, in, {laid[3], laid[2], laid[1]}, first, ws, st);
+    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, pv, in, laid[0], laid[3], ends, ws, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, pk, in, {laid[2], laid[3], laid[0]}, ends, ws, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dq), tiles, d.Dk, grad_q, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dk), tiles, d.Dk, grad_k, st);
     if (e == cudaSuccess && grad_log_decay)
         e = launch_linear_decay(d, in, laid, first, d.segs > 1 ? ends : grad_final_state, reinterpret_cast<double *>(ws + l.decay), grad_log_decay,
                                 ws, st);
     // last: the final state's gradient may be grad_state itself
-    if (e == cudaSuccess) e = launch_linear_scan(d, pv, in, {laid[1], laid[0], laid[3]}, ends, false, ws, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, pv, in, {laid[1], laid[0], laid[3]}, ends, ws, st);
     return linear_status(e);
 }
 

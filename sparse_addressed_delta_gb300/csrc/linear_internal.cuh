@@ -96,11 +96,13 @@ struct LinearLay {
     void *dst;
 };
 cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, cudaStream_t st);
-// A sequence in segments (d.segs > 1): a first launch (carry) takes every segment but the pass's last from a state
-// of zeros to what it adds, a join makes the states they begin with of that, and a second launch runs all at once.
-cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], float *starts, bool carry,
+cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts,
                                void *status, cudaStream_t st);
-cudaError_t launch_linear_join(const LinearDims &d, const LinearIn &in, const float *first, bool reverse, float *starts, cudaStream_t st);
+// A sequence in segments (d.segs > 1): a first launch takes every segment but the pass's last from a state of zeros to
+// what it adds, a join makes the states they begin with of that, and the scan runs all at once. k, v: the laid operands
+// of a pass along the state's rows (sv = 1).
+cudaError_t launch_linear_carry(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid &k, const LinearLaid &v, float *starts,
+                                void *status, cudaStream_t st);
 
 // up to kLinearStepTokens tokens (any number, but slowly)
 cudaError_t launch_linear_step(const LinearDims &d, const LinearIn &in, const void *q, const void *k, const void *v, float *state, void *o,

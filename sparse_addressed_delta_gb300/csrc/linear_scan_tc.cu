@@ -25,30 +25,26 @@ namespace {
 
 constexpr int kLinC = 64, kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 3);
 
-// CARRY: no queries, no Z; more stages of less, and two buffers of decayed keys
-template <int KP, int NP, bool CARRY>
+template <int KP, int NP>
 struct LinScan {
     static constexpr int TILE = kLinC * 128, KT = KP / 64;         // 64 columns of 64 tokens; such tiles of Q or K
-    static constexpr int Q = 0, K = Q + (CARRY ? 0 : NP * KT * TILE), V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
-    static constexpr int STAGES = NP == 3 ? 1 : CARRY ? 4 : 3;
+    static constexpr int Q = 0, K = Q + NP * KT * TILE, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
+    static constexpr int STAGES = NP == 3 ? 1 : 3;
     // planes of the decayed keys and, in the same rows behind them, of Z^T
-    static constexpr int PLANE = (CARRY ? KT : KT + 1) * TILE, KX = STAGES * STAGE, KX2 = KX + 3 * PLANE, Z = KX + KT * TILE;
-    static constexpr int AUX = CARRY ? KX2 + 3 * PLANE : KX2;
-    static constexpr int POW = AUX, PAIR = POW + 4 * 80, BARS = PAIR + 4 * 128, BAD = BARS + 256, BYTES = BAD + (CARRY ? 0 : 4 * 512) + 1024;
+    static constexpr int PLANE = (KT + 1) * TILE, KX = STAGES * STAGE, Z = KX + KT * TILE, AUX = KX + 3 * PLANE;
+    static constexpr int POW = AUX, PAIR = POW + 4 * 80, BARS = PAIR + 4 * 128, BAD = BARS + 256, BYTES = BAD + 4 * 512 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
     static constexpr int SP = 0, OA = 3 * (KP / 2), U = OA + kLinC, OB = U + KP, P = OB + kLinC;
     static_assert(P + kLinC <= 512, "tensor memory");
 };
 
-enum { B_FULL = 0, B_BULK = 4, B_EMPTY = 8, B_ZK = 12, B_U = 14, B_UF = 16, B_P = 18, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
-
-enum { LIN_RUN, LIN_CARRY };
+enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_ZK = 9, B_U, B_UF, B_P, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
 
 struct LinArgs {
     LinearPass p;
     const float *g;
     const int32_t *valid;
-    float *starts;                       // [segs][B, H, Dk, Dv] states the segments begin with, in the pass's order
+    const float *starts;                 // [segs][B, H, Dk, Dv] states the segments begin with, in the pass's order
     DevStatus *status;
     long long heads[3];                  // head strides of the laid operands, 0: broadcast
     long long seqs[3];
@@ -86,25 +82,12 @@ __device__ __noinline__ void linear_column(const LinearDims &d, const LinearPass
     }
 }
 
-// the sequences from the longest down, so that the last blocks to start are short
-__device__ __forceinline__ int linear_longest_first(const LinearDims &d, const int32_t *valid, int b) {
-    if (!valid || d.B > 32) return b;
-    const int lane = threadIdx.x & 31, mine = lane < d.B ? linear_valid(valid, lane, d.T) : -1;
-    int rank = 0;
-    for (int i = 0; i < d.B; ++i) {
-        const int other = __shfl_sync(~0u, mine, i);
-        rank += other > mine || (other == mine && i < lane);
-    }
-    return __ffs(__ballot_sync(~0u, rank == b)) - 1;
-}
-
-template <int KP, int NP, int MODE, bool REV, typename OT>
+template <int KP, int NP, bool REV, typename OT>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear_scan(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const __grid_constant__ LinearDims d,
                   const __grid_constant__ LinArgs a) {
-    constexpr bool CARRY = MODE == LIN_CARRY;
-    using L = LinScan<KP, NP, CARRY>;
+    using L = LinScan<KP, NP>;
     constexpr int C = kLinC, HD = KP / 4, ST = L::STAGES, KT = L::KT, TILE = L::TILE;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -135,10 +118,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int i = 0; i < ST; ++i) {
             mbar_init(bar + B_FULL + i, 32);
             mbar_init(bar + B_BULK + i, 1);
-            mbar_init(bar + B_EMPTY + i, !CARRY && sizeof(OT) == 2 ? 2 : 1);
+            mbar_init(bar + B_EMPTY + i, sizeof(OT) == 2 ? 2 : 1);
         }
         for (int i = B_ZK; i < B_COUNT; ++i)
-            mbar_init(bar + i, i < B_U || i == B_UF || i == B_UF + 1 || i == B_OF || i == B_S || i == B_OUT ? kLinWarps : 1);
+            mbar_init(bar + i, i == B_ZK || i == B_UF || i == B_OF || i == B_S || i == B_OUT ? kLinWarps : 1);
         *dead = a.status->code != 0;                               // an earlier kernel of this call gave up
         fence_mbar_init();
     }
@@ -154,17 +137,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (tid == C) pw[0] = 1.f;
         pair[tid] = tid < C ? 0.f : p.pair * x;
     }
-    if (!CARRY)                                                    // blocks of Z^T that hold no pairs are never written again
-        for (int i = tid; i < 3 * TILE / 16; i += kLinThreads)
-            *reinterpret_cast<uint4 *>(smem + L::Z + i / (TILE / 16) * L::PLANE + i % (TILE / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    // blocks of Z^T that hold no pairs are never written again
+    for (int i = tid; i < 3 * TILE / 16; i += kLinThreads)
+        *reinterpret_cast<uint4 *>(smem + L::Z + i / (TILE / 16) * L::PLANE + i % (TILE / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *slot;
-    // a carry's chunks go through two buffers of decayed keys and two of U in turn
-    auto turn = [](int it) { return CARRY ? it & 1 : 0; };
-    auto phase = [](int it) { return (unsigned)(CARRY ? it >> 1 : it) & 1; };
     auto chunk_at = [&](int it) { return REV ? n0 + nch - 1 - it : n0 + it; };
     int first = -1;                                                // iteration of the column's first update that is not finite
     float2 S[HD / 2];
@@ -173,7 +153,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const int part = warp >> 2, lane0 = 32 * (warp & 3), col = v0 + lane0 + lane, kk = part * HD;
         const bool mine = col < p.V;
         const uint32_t at = tm + ((uint32_t)lane0 << 16);
-        const float *begin = CARRY ? nullptr : d.segs > 1 ? a.starts + seg * states : p.first;
+        const float *begin = d.segs > 1 ? a.starts + seg * states : p.first;
         if (begin) begin += own + kk * p.sk + col * p.sv;
         if (p.sk == 1 && ((uintptr_t)begin & 15) == 0) {           // transposed: K runs along the row
 #pragma unroll
@@ -207,10 +187,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         int unit0, unit1;
         {
             constexpr int UNITS = 2 * KP / 8;                      // 32 or 16
-            if (CARRY) {
-                unit0 = warp * (UNITS / 16);
-                unit1 = unit0 + UNITS / 16;
-            } else {
+            {
                 // warps of lanes 64..: 3 of each 4; without pairs: 3; off the diagonal: 1; on it: none
                 const bool other = (warp & 3) >= 2;
                 const int none = REV ? (warp & 3) == 0 && part >= 2 : (warp & 3) == 1 && part < 2;
@@ -231,10 +208,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
                     float2 x[4];
                     load_piece<NP, KT * TILE>(src + off, x);
-                    scale_piece(x, w, smem + (turn(it) ? L::KX2 : L::KX) + off, L::PLANE);
+                    scale_piece(x, w, smem + L::KX + off, L::PLANE);
                 }
             }
-            if (!CARRY && (warp & 3) < 2 && ahead >= -46) {
+            if ((warp & 3) < 2 && ahead >= -46) {
                 if (!tc_warp_wait(bar + B_P, it & 1, dead, d.spin)) return false;
                 tc_fence_after();
                 {
@@ -271,7 +248,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             }
             fence_proxy_async_smem();
-            arrive(B_ZK + turn(it));
+            arrive(B_ZK);
             return true;
         };
         // bfloat16 results, 8 x 8 blocks stored transposed: block i of a store is 8 columns (i % 2) and 8 tokens (i / 2), a
@@ -283,7 +260,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const int t = 16 * part + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
             reads[i] = p.from * pw[REV ? C - 1 - t : t + 1];
         }
-        if (!CARRY && nch > 0) {
+        if (nch > 0) {
             planes_of_s();
             arrive(B_S);
         }
@@ -291,46 +268,46 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int it = 0; ok && it < nch; ++it) {
             const unsigned par = it & 1;
             const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
-            if (CARRY && it + 1 < nch && !(ok = local(it + 1))) break;
-            ok = tc_warp_wait(bar + B_U + turn(it), phase(it), dead, d.spin);
+            ok = tc_warp_wait(bar + B_U, par, dead, d.spin);
             if (!ok) break;
             tc_fence_after();
             const float whole = pw[nt];
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
                 float2 x[8];
-                tc_load16(at + (turn(it) ? L::SP : L::U) + kk + c, reinterpret_cast<float(&)[16]>(x));
-                if (!CARRY && c == 0 && first < 0 && !(fabsf(x[0].x) <= 3.402823466e38f)) first = it;
+                tc_load16(at + L::U + kk + c, reinterpret_cast<float(&)[16]>(x));
+                if (c == 0 && first < 0 && !(fabsf(x[0].x) <= 3.402823466e38f)) first = it;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) S[c / 2 + i] = fma2(make_float2(whole, whole), S[c / 2 + i], x[i]);
             }
-            arrive(B_UF + turn(it));
-            if (!CARRY && it + 1 < nch && !(ok = local(it + 1))) break;
-            if constexpr (!CARRY) {
+            arrive(B_UF);
+            if (it + 1 < nch && !(ok = local(it + 1))) break;
+            {
                 ok = tc_warp_wait(bar + B_O, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (sizeof(OT) == 2) {
                     // in the place of the chunk's V, which warp 18 stores
                     unsigned char *to = smem + it % ST * L::STAGE + L::V;
+                    float y[2][8], z[2][8];                        // 16 lanes of columns each
+                    tc_load_frag16(at + L::OA + 16 * part, at + L::OB + 16 * part, y[0], z[0]);
+                    tc_load_frag16(at + (16u << 16) + L::OA + 16 * part, at + (16u << 16) + L::OB + 16 * part, y[1], z[1]);
+                    arrive(B_OF);
 #pragma unroll
-                    for (int l = 0; l < 2; ++l) {                  // 16 lanes of columns
-                        float y[8], z[8];
-                        tc_load_frag16(at + ((uint32_t)(16 * l) << 16) + L::OA + 16 * part, at + ((uint32_t)(16 * l) << 16) + L::OB + 16 * part, y, z);
-                        if (l == 1) arrive(B_OF);
+                    for (int l = 0; l < 2; ++l) {
                         if (nt == C) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) z[i] = fmaf(reads[(i >> 2) * 2 + (i & 1)], y[i], z[i]);
+                            for (int i = 0; i < 8; ++i) z[l][i] = fmaf(reads[(i >> 2) * 2 + (i & 1)], y[l][i], z[l][i]);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int t = 16 * part + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
-                                z[i] = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[i], z[i]) : 0.f;
+                                z[l][i] = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[l][i], z[l][i]) : 0.f;
                             }
                         }
                         unsigned r[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[2 * i], z[2 * i + 1]);
+                        for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[l][2 * i], z[l][2 * i + 1]);
                         const int c = ocol + 2 * l;
                         stsm4t(smem_u32(to) + (c >> 3) * TILE + tc_at(orow, c & 7), r);
                     }
@@ -358,7 +335,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             }
         }
-        if (!CARRY) reinterpret_cast<int *>(smem + L::BAD)[part * 128 + lane0 + lane] = first;   // (a carry has no room for it)
+        reinterpret_cast<int *>(smem + L::BAD)[part * 128 + lane0 + lane] = first;
     } else if (warp == kLinWarps) {
         // ---- the products
         const uint32_t one = tc_elect(), tu = __shfl_sync(~0u, tm, 0), base = __shfl_sync(~0u, smem_u32(smem), 0);
@@ -379,18 +356,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             tc_commit_to(one, bar + B_P);
         };
         bool ok = nch > 0;
-        if (!CARRY && ok) {
+        if (ok) {
             ok = tc_warp_wait(bar + B_FULL, 0, dead, d.spin);
             tc_fence_after();
             if (ok) scores(0);
         }
         for (int it = 0; ok && it < nch; ++it) {
             const uint32_t st = base + it % ST * L::STAGE, qd = tc_k_major(st + L::Q), vm = tc_n_major(st + L::V, TILE);
-            const uint32_t kx = tc_n_major(base + (turn(it) ? L::KX2 : L::KX), TILE), plane = L::PLANE / 16;
+            const uint32_t kx = tc_n_major(base + L::KX, TILE);
             const unsigned par = it & 1;
-            ok = tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin) && tc_warp_wait(bar + B_ZK + turn(it), phase(it), dead, d.spin);
-            if (CARRY) ok = ok && (it < 2 || tc_warp_wait(bar + B_UF + turn(it), phase(it) ^ 1, dead, d.spin));
-            else ok = ok && (it == 0 || (tc_warp_wait(bar + B_UF, par ^ 1, dead, d.spin) && tc_warp_wait(bar + B_OF, par ^ 1, dead, d.spin)));
+            ok = tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin) && tc_warp_wait(bar + B_ZK, par, dead, d.spin);
+            ok = ok && (it == 0 || (tc_warp_wait(bar + B_UF, par ^ 1, dead, d.spin) && tc_warp_wait(bar + B_OF, par ^ 1, dead, d.spin)));
             if (!ok) break;
             tc_fence_after();
             // U and, in the columns behind it, OB: V^T is read once for both
@@ -401,12 +377,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks) {
-                        tc_mma_ss(one, tu + (turn(it) ? L::SP : L::U), vm + (m * 2 * TILE + 2048 * ks) / 16, kx + (sum - m) * plane + 2048 * ks / 16,
-                                  tc_idesc<true, true>(CARRY ? KP : KP + C), add);
+                        tc_mma_ss(one, tu + L::U, vm + (m * 2 * TILE + 2048 * ks) / 16, kx + ((sum - m) * L::PLANE + 2048 * ks) / 16,
+                                  tc_idesc<true, true>(KP + C), add);
                         add = true;
                     }
-            tc_commit_to(one, bar + B_U + turn(it));
-            if constexpr (!CARRY) {
+            tc_commit_to(one, bar + B_U);
+            {
                 if (ST > 1 && it + 1 < nch) {
                     ok = tc_warp_wait(bar + B_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin);
                     if (!ok) break;
@@ -430,7 +406,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 tc_commit_to(one, bar + B_O);
             }
             tc_commit_to(one, bar + B_EMPTY + it % ST);
-            if (!CARRY && ST == 1 && it + 1 < nch) {
+            if (ST == 1 && it + 1 < nch) {
                 ok = tc_warp_wait(bar + B_FULL, (it + 1) & 1, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
@@ -440,21 +416,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         __syncwarp();
     } else if (warp == kLinWarps + 1) {
         // ---- the chunks' inputs
-        constexpr uint32_t bytes = CARRY ? NP * (KT + 2) * TILE : L::STAGE;
         for (int it = 0; it < nch; ++it) {
             const int s = it % ST, t0 = chunk_at(it) * C, nt = ntok - t0 < C ? ntok - t0 : C;
             unsigned char *st = smem + s * L::STAGE;
             unsigned long long *full = bar + B_BULK + s;
             if (it >= ST && !tc_warp_wait(bar + B_EMPTY + s, (it / ST - 1) & 1, dead, d.spin)) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(full, bytes);
+                mbar_arrive_expect_tx(full, L::STAGE);
 #pragma unroll
                 for (int m = 0; m < NP; ++m) {
 #pragma unroll
                     for (int c = 0; c < KT; ++c) {
-                        if (!CARRY)
-                            tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], h / p.q.share), t0,
-                                           tc_coord(a.seqs[0], b) + m * d.B, full);
+                        tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], h / p.q.share), t0,
+                                       tc_coord(a.seqs[0], b) + m * d.B, full);
                         tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], h / p.k.share), t0,
                                        tc_coord(a.seqs[1], b) + m * d.B, full);
                     }
@@ -478,7 +452,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             mbar_arrive(bar + B_FULL + s);
         }
-    } else if (!CARRY && sizeof(OT) == 2) {
+    } else if (sizeof(OT) == 2) {
         // ---- the bfloat16 results
         for (int it = 0; it < nch; ++it) {
             if (!tc_warp_wait(bar + B_OUT, it & 1, dead, d.spin)) break;
@@ -508,7 +482,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const bool bad = __syncthreads_or(first >= 0);
     if (warp == kLinWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
     if (*dead) return;
-    if constexpr (!CARRY) {
+    {
         if (bad && a.column) {
             const int *at = reinterpret_cast<int *>(smem + L::BAD);
             const float *begin = d.segs > 1 ? a.starts + seg * states : p.first;
@@ -529,8 +503,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 if ((tid & 127) < cols) out[t * d.H * p.V + (tid & 127)] = from_f32<OT>(0.f);
         }
     }
-    // where the state goes: a carried segment's is the next one's share
-    float *end = CARRY ? a.starts + (seg + 1) * states : seg + 1 == d.segs ? p.last : nullptr;
+    float *end = seg + 1 == d.segs ? p.last : nullptr;
     if (warp < kLinWarps && end) {
         const int kk = (warp >> 2) * HD, col = v0 + 32 * (warp & 3) + lane;
         if (col < p.V)
@@ -540,50 +513,22 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
 }
 
-// starts [segs]: the state itself, then each segment's first state from the one before and what the carry left
-__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ LinearDims d, const float *g, const int32_t *valid, const float *first,
-                                                     bool reverse, float *starts) {
-    const long long cells = (long long)d.Dk * d.Dv, states = cells * d.B * d.H;
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= states) return;
-    const long long bh = i / cells;
-    const int b = (int)(bh / d.H), h = (int)(bh % d.H);
-    const int ntok = linear_valid(valid, b, d.T), chunks = (ntok + d.C - 1) / d.C;
-    auto bound = [&](int n) {
-        const int t = (int)((long long)chunks * n / d.segs) * d.C;
-        return t < ntok ? t : ntok;
-    };
-    float4 s = first ? make_float4(first[i], first[i + 1], first[i + 2], first[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4 *>(starts + i) = s;
-    for (int m = 1; m < d.segs; ++m) {
-        const int place = reverse ? d.segs - m : m - 1;            // of the segment before
-        const float w = linear_power(g[h], bound(place + 1) - bound(place));
-        float4 *at = reinterpret_cast<float4 *>(starts + m * states + i);
-        const float4 e = *at;
-        s = make_float4(fmaf(w, s.x, e.x), fmaf(w, s.y, e.y), fmaf(w, s.z, e.z), fmaf(w, s.w, e.w));
-        *at = s;
-    }
-}
-
-template <int KP, int NP, int MODE, bool REV, typename OT>
+template <int KP, int NP, bool REV, typename OT>
 cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, cudaStream_t st) {
-    auto kern = k_linear_scan<KP, NP, MODE, REV, OT>;
-    using L = LinScan<KP, NP, MODE == LIN_CARRY>;
+    auto kern = k_linear_scan<KP, NP, REV, OT>;
+    using L = LinScan<KP, NP>;
     set_kernel_smem(kern, L::BYTES);
-    const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * (MODE == LIN_CARRY ? d.segs - 1 : d.segs);
+    const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * d.segs;
     kern<<<(unsigned)blocks, kLinThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
     return cudaGetLastError();
 }
 
 template <int KP, int NP>
-cudaError_t scan_of(const LinearDims &d, const LinArgs &a, bool carry, const CUtensorMap *m, cudaStream_t st) {
+cudaError_t scan_of(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, cudaStream_t st) {
     using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
-    if (carry)
-        return a.p.reverse ? scan<KP, NP, LIN_CARRY, true, IT>(d, a, m, st) : scan<KP, NP, LIN_CARRY, false, IT>(d, a, m, st);
     if constexpr (NP == 1)
-        if (a.p.out_f32)
-            return a.p.reverse ? scan<KP, NP, LIN_RUN, true, float>(d, a, m, st) : scan<KP, NP, LIN_RUN, false, float>(d, a, m, st);
-    return a.p.reverse ? scan<KP, NP, LIN_RUN, true, IT>(d, a, m, st) : scan<KP, NP, LIN_RUN, false, IT>(d, a, m, st);
+        if (a.p.out_f32) return a.p.reverse ? scan<KP, NP, true, float>(d, a, m, st) : scan<KP, NP, false, float>(d, a, m, st);
+    return a.p.reverse ? scan<KP, NP, true, IT>(d, a, m, st) : scan<KP, NP, false, IT>(d, a, m, st);
 }
 
 // the operands as the tensor copies take them: float32 ones as three bfloat16 planes, the others contiguous
@@ -622,8 +567,8 @@ __global__ void __launch_bounds__(256) k_linear_lay(const __grid_constant__ LayT
 
 }  // namespace
 
-cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], float *starts, bool carry,
-                               void *status, cudaStream_t st) {
+cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts, void *status,
+                               cudaStream_t st) {
     const int np = d.dtype == SDM_F32 ? 3 : 1;
     LinArgs a{p, in.g, in.valid, starts, static_cast<DevStatus *>(status), {}, {}, p.last != nullptr && !p.reverse};
     CUtensorMap m[4];
@@ -634,20 +579,14 @@ cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const L
         a.heads[i] = laid[i].s[2];
     }
     m[3] = m[2];                                                    // (of bfloat16 results alone)
-    if (!carry && np == 1 && !p.out_f32) {
+    if (np == 1 && !p.out_f32) {
         const long long os[3] = {(long long)d.T * d.H * p.V, (long long)d.H * p.V, p.V};
         const cudaError_t e = tc_tensor_map(m + 3, p.out, os, d.B, d.T, d.H, p.V);
         if (e != cudaSuccess) return e;
     }
     const bool wide = p.K > 64;
-    if (np == 1) return wide ? scan_of<128, 1>(d, a, carry, m, st) : scan_of<64, 1>(d, a, carry, m, st);
-    return wide ? scan_of<128, 3>(d, a, carry, m, st) : scan_of<64, 3>(d, a, carry, m, st);
-}
-
-cudaError_t launch_linear_join(const LinearDims &d, const LinearIn &in, const float *first, bool reverse, float *starts, cudaStream_t st) {
-    const long long blocks = (linear_states(d) / 4 + 255) / 256;
-    k_linear_join<<<(unsigned)blocks, 256, 0, st>>>(d, in.g, in.valid, first, reverse, starts);
-    return cudaGetLastError();
+    if (np == 1) return wide ? scan_of<128, 1>(d, a, m, st) : scan_of<64, 1>(d, a, m, st);
+    return wide ? scan_of<128, 3>(d, a, m, st) : scan_of<64, 3>(d, a, m, st);
 }
 
 cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, cudaStream_t st) {

@@ -8,6 +8,18 @@
 
 namespace sdm {
 
+// the sequences from the longest down, so that the last blocks to start are short
+__device__ __forceinline__ int linear_longest_first(const LinearDims &d, const int32_t *valid, int b) {
+    if (!valid || d.B > 32) return b;
+    const int lane = threadIdx.x & 31, mine = lane < d.B ? linear_valid(valid, lane, d.T) : -1;
+    int rank = 0;
+    for (int i = 0; i < d.B; ++i) {
+        const int other = __shfl_sync(~0u, mine, i);
+        rank += other > mine || (other == mine && i < lane);
+    }
+    return __ffs(__ballot_sync(~0u, rank == b)) - 1;
+}
+
 // x minus the lower or upper bfloat16 of a pair, exact where that is x rounded
 __device__ __forceinline__ float minus_lo(float x, unsigned p) {
     float r;
