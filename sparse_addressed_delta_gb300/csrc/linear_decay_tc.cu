@@ -39,7 +39,7 @@ struct LinDecay {
     static constexpr int PQ = KP == 128 ? A1 : 4 * KP, PG = PQ + 64;
 };
 
-enum { D_FULL = 0, D_BULK = 2, D_EMPTY = 4, D_MUL = 6, D_CONV = 8, D_PAIR = 10, D_READ, D_DRAIN, D_COUNT };
+enum { D_FULL = 0, D_EMPTY = 2, D_MUL = 4, D_CONV = 6, D_PAIR = 8, D_READ, D_PART, D_DRAIN, D_COUNT };
 
 struct DecayArgs {
     const float *g;
@@ -81,8 +81,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar + D_FULL + i, 32);
-            mbar_init(bar + D_BULK + i, 1);
+            mbar_init(bar + D_FULL + i, 1);
             mbar_init(bar + D_EMPTY + i, 1);
         }
         for (int i = D_MUL; i < D_COUNT; ++i)
@@ -291,42 +290,23 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         __syncwarp();
     } else {
         // ---- the chunks' inputs
-        for (int it = 0; it < nch; ++it) {
-            const int s = it % ST, t0 = (n0 + it) * C, nt = ntok - t0 < C ? ntok - t0 : C;
-            unsigned char *st = smem + s * L::STAGE;
-            unsigned long long *full = bar + D_BULK + s;
-            if (it >= ST && !tc_warp_wait(bar + D_EMPTY + s, (it / ST - 1) & 1, dead, d.spin)) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(full, L::STAGE);
-                const int hk = h / a.share;
+        const int hk = h / a.share;
+        linear_loads<ST>(smem, L::STAGE, bar + D_FULL, bar + D_EMPTY, bar + D_PART, nch, ntok, [&](int it) { return n0 + it; },
+                         [&](unsigned char *st, int t0, unsigned long long *full) {
 #pragma unroll
-                for (int m = 0; m < NP; ++m) {
+            for (int m = 0; m < NP; ++m) {
 #pragma unroll
-                    for (int c = 0; c < KT; ++c) {
-                        tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], hk), t0, tc_coord(a.seqs[0], b) + m * d.B, full);
-                        tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], hk), t0, tc_coord(a.seqs[1], b) + m * d.B, full);
-                    }
+                for (int c = 0; c < KT; ++c) {
+                    tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], hk), t0, tc_coord(a.seqs[0], b) + m * d.B, full);
+                    tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], hk), t0, tc_coord(a.seqs[1], b) + m * d.B, full);
+                }
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tc_tensor_load(st + L::G + (m * 2 + c) * TILE, &mg, v0 + 64 * c, tc_coord(a.heads[3], h), t0, tc_coord(a.seqs[3], b) + m * d.B, full);
-                        tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[2], h), t0, tc_coord(a.seqs[2], b) + m * d.B, full);
-                    }
+                for (int c = 0; c < 2; ++c) {
+                    tc_tensor_load(st + L::G + (m * 2 + c) * TILE, &mg, v0 + 64 * c, tc_coord(a.heads[3], h), t0, tc_coord(a.seqs[3], b) + m * d.B, full);
+                    tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[2], h), t0, tc_coord(a.seqs[2], b) + m * d.B, full);
                 }
             }
-            __syncwarp();
-            if (!tc_warp_wait(full, it / ST & 1, dead, d.spin)) {
-                mbar_wait_bounded(full, it / ST & 1);              // nothing in flight behind a give-up
-                break;
-            }
-            if (nt < C) {                                          // what lies past the valid tokens is not used
-                for (int i = lane; i < (C - nt) * 8; i += 32) {
-                    const int off = tc_at(nt + (i >> 3), i & 7);
-                    for (int c = 0; c < L::STAGE / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-            }
-            mbar_arrive(bar + D_FULL + s);
-        }
+        }, dead, d.spin);
     }
     __syncthreads();
     if (*dead) {

@@ -38,7 +38,7 @@ struct LinScan {
     static_assert(P + kLinC <= 512, "tensor memory");
 };
 
-enum { B_FULL = 0, B_BULK = 3, B_EMPTY = 6, B_ZK = 9, B_U, B_UF, B_P, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
+enum { B_FULL = 0, B_EMPTY = 3, B_PART = 6, B_ZK, B_U, B_UF, B_P, B_O, B_OF, B_S, B_OUT, B_DRAIN, B_COUNT };
 
 struct LinArgs {
     LinearPass p;
@@ -116,11 +116,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(bar + B_FULL + i, 32);
-            mbar_init(bar + B_BULK + i, 1);
+            mbar_init(bar + B_FULL + i, 1);
             mbar_init(bar + B_EMPTY + i, sizeof(OT) == 2 ? 2 : 1);
         }
-        for (int i = B_ZK; i < B_COUNT; ++i)
+        for (int i = B_PART; i < B_COUNT; ++i)
             mbar_init(bar + i, i == B_ZK || i == B_UF || i == B_OF || i == B_S || i == B_OUT ? kLinWarps : 1);
         *dead = a.status->code != 0;                               // an earlier kernel of this call gave up
         fence_mbar_init();
@@ -416,42 +415,22 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         __syncwarp();
     } else if (warp == kLinWarps + 1) {
         // ---- the chunks' inputs
-        for (int it = 0; it < nch; ++it) {
-            const int s = it % ST, t0 = chunk_at(it) * C, nt = ntok - t0 < C ? ntok - t0 : C;
-            unsigned char *st = smem + s * L::STAGE;
-            unsigned long long *full = bar + B_BULK + s;
-            if (it >= ST && !tc_warp_wait(bar + B_EMPTY + s, (it / ST - 1) & 1, dead, d.spin)) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(full, L::STAGE);
+        linear_loads<ST>(smem, L::STAGE, bar + B_FULL, bar + B_EMPTY, bar + B_PART, nch, ntok, chunk_at, [&](unsigned char *st, int t0, unsigned long long *full) {
 #pragma unroll
-                for (int m = 0; m < NP; ++m) {
+            for (int m = 0; m < NP; ++m) {
 #pragma unroll
-                    for (int c = 0; c < KT; ++c) {
-                        tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], h / p.q.share), t0,
-                                       tc_coord(a.seqs[0], b) + m * d.B, full);
-                        tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], h / p.k.share), t0,
-                                       tc_coord(a.seqs[1], b) + m * d.B, full);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[2], h / p.v.share), t0,
-                                       tc_coord(a.seqs[2], b) + m * d.B, full);
+                for (int c = 0; c < KT; ++c) {
+                    tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], h / p.q.share), t0,
+                                   tc_coord(a.seqs[0], b) + m * d.B, full);
+                    tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], h / p.k.share), t0,
+                                   tc_coord(a.seqs[1], b) + m * d.B, full);
                 }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[2], h / p.v.share), t0,
+                                   tc_coord(a.seqs[2], b) + m * d.B, full);
             }
-            __syncwarp();
-            if (!tc_warp_wait(full, it / ST & 1, dead, d.spin)) {
-                mbar_wait_bounded(full, it / ST & 1);              // nothing in flight behind a give-up
-                break;
-            }
-            if (nt < C) {                                          // what lies past the valid tokens is not used
-                for (int i = lane; i < (C - nt) * 8; i += 32) {
-                    const int off = tc_at(nt + (i >> 3), i & 7);
-                    for (int c = 0; c < L::STAGE / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-            }
-            mbar_arrive(bar + B_FULL + s);
-        }
+        }, dead, d.spin);
     } else if (sizeof(OT) == 2) {
         // ---- the bfloat16 results
         for (int it = 0; it < nch; ++it) {

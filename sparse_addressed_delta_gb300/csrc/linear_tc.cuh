@@ -20,6 +20,47 @@ __device__ __forceinline__ int linear_longest_first(const LinearDims &d, const i
     return __ffs(__ballot_sync(~0u, rank == b)) - 1;
 }
 
+// The loading warp: chunk after chunk of `nch` into ST stages of shared memory as they are emptied, by tensor copies that
+// complete full[stage] (of one arrival); issue(stage, first token, barrier) starts a stage's, `bytes` of them in tiles of
+// 64 rows. Copies of all stages are in flight at once (with each awaited before the next, a carry's chunk took 1.2 us).
+// A chunk of fewer than 64 tokens, of which a sequence has one at most, goes by a barrier of its own: what lies past the
+// tokens is not used, so its rows are cleared before the stage counts as full.
+template <int ST, typename At, typename Issue>
+__device__ __forceinline__ void linear_loads(unsigned char *smem, int bytes, unsigned long long *full, unsigned long long *empty,
+                                             unsigned long long *partial, int nch, int ntok, At chunk_at, Issue issue, volatile int *dead, long long spin) {
+    constexpr int C = 64, TILE = C * 128;
+    const int lane = threadIdx.x & 31;
+    int it = 0;
+    for (; it < nch; ++it) {
+        const int s = it % ST, t0 = chunk_at(it) * C, nt = ntok - t0 < C ? ntok - t0 : C;
+        unsigned char *st = smem + s * bytes;
+        if (it >= ST && !tc_warp_wait(empty + s, (it / ST - 1) & 1, dead, spin)) break;
+        unsigned long long *to = nt < C ? partial : full + s;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(to, bytes);
+            issue(st, t0, to);
+        }
+        __syncwarp();
+        if (nt == C) continue;
+        if (!tc_warp_wait(to, 0, dead, spin)) {
+            mbar_wait_bounded(to, 0);                              // nothing in flight behind a give-up
+            break;
+        }
+        for (int i = lane; i < (C - nt) * 8; i += 32) {
+            const int off = tc_at(nt + (i >> 3), i & 7);
+            for (int c = 0; c < bytes / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + s);
+    }
+    if (!*dead) return;
+    for (int i = it > ST ? it - ST : 0; i < it; ++i) {
+        const int t0 = chunk_at(i) * C;
+        if (ntok - t0 >= C) mbar_wait_bounded(full + i % ST, i / ST & 1);
+    }
+}
+
 // x minus the lower or upper bfloat16 of a pair, exact where that is x rounded
 __device__ __forceinline__ float minus_lo(float x, unsigned p) {
     float r;
