@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "norm_rows.cuh"
+#include "pairs.cuh"
 
 namespace sdm {
 namespace {
@@ -23,26 +24,29 @@ constexpr int kGroupRowThreads = 512;                   // an SM, of the forward
 // negligible, far inside the results' rounding of 2^-9; the exact ones would bound the kernel (25 instructions an
 // element). An infinite e^-z makes 0 of both.
 template <typename T>
-__device__ __forceinline__ float sigmoid(float z) {
+__device__ __forceinline__ float2 sigmoid(float2 z) {
     if constexpr (sizeof(T) == 2) {
-        float e, p;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504089f * z));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
+        float2 e = mul2(z, both(-1.44269504089f)), p;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+        e = add2(e, both(1.f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(e.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(e.y));
         return p;
     } else {
-        return 1.f / (1.f + expf(-z));
+        return make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
     }
 }
 template <typename T, bool ACT>
-__device__ __forceinline__ float activate(float z) {
-    return ACT ? z * sigmoid<T>(z) : z;
+__device__ __forceinline__ float2 activate(float2 z) {
+    return ACT ? mul2(z, sigmoid<T>(z)) : z;
 }
 // dy times the activation's slope at z
 template <typename T, bool ACT>
-__device__ __forceinline__ float back(float dy, float z) {
+__device__ __forceinline__ float2 back(float2 dy, float2 z) {
     if constexpr (!ACT) return dy;
-    const float p = sigmoid<T>(z);
-    return dy * (p * fmaf(z, 1.f - p, 1.f));
+    const float2 p = sigmoid<T>(z);
+    return mul2(dy, mul2(p, fma2(z, fma2(p, both(-1.f), both(1.f)), both(1.f))));
 }
 
 // mean and sum of squares around it of nb values joined to those of n
@@ -84,6 +88,94 @@ struct GroupShape {
 
 // ---- one position a sample ----------------------------------------------------------------------
 
+// What bounds these is the issue of instructions (the first form, one float at a time, took 25 an element, 125 us for
+// 32768 x 4096 bfloat16 with the activation, where memory takes 80), so the arithmetic is in pairs and the addresses
+// step along.
+
+// The threads' own pieces of the rows ahead, as in the layer norm (RowRing): a thread copies NV vectors of each of ROWS
+// tensors (and 8 bytes of statistics) into shared memory and reads them back itself.
+template <typename T, int VEC, int NV, int ROWS, bool STATS>
+struct GroupRing {
+    static constexpr int ST = kNormStages<T>, VB = VEC * (int)sizeof(T), THREAD = ROWS * NV * VB + (STATS ? 8 : 0);
+    static __host__ __device__ size_t bytes(int threads) { return (size_t)ST * THREAD * threads; }
+    unsigned at, stage_bytes, read_at, write_at, end;
+    int c, tpr, t;
+    __device__ GroupRing(unsigned char *smem, int t_, int tpr_, int c_) : c(c_), tpr(tpr_), t(t_) {
+        at = smem_u32(smem) + threadIdx.x * VB;
+        stage_bytes = THREAD * blockDim.x;
+        read_at = write_at = 0;
+        end = ST * stage_bytes;
+        // vectors past the row's end are never fetched
+        for (int s = 0; s < ST; ++s)
+            for (int i = 0; i < ROWS * NV; ++i)
+                if ((i % NV * tpr + t) * VEC >= c)
+                    *reinterpret_cast<Vec<T, VEC> *>(smem + threadIdx.x * VB + s * stage_bytes + i * VB * blockDim.x) = Vec<T, VEC>{};
+    }
+    // row `which` into the stage that is written next
+    __device__ __forceinline__ void fetch(int which, const T *row) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * tpr + t) * VEC < c) {
+                const unsigned to = at + write_at + (which * NV + i) * VB * blockDim.x;
+                const T *src = row + (i * tpr + t) * VEC;
+                if constexpr (VB == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+                else if constexpr (VB == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
+                else asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const unsigned short *>(src)) : "memory");
+            }
+    }
+    __device__ __forceinline__ unsigned stats_at(unsigned stage) const { return at - threadIdx.x * VB + stage + (THREAD - 8) * blockDim.x + 8 * threadIdx.x; }
+    __device__ __forceinline__ void fetch_stats(const float2 *p) const {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(stats_at(write_at)), "l"(p) : "memory");
+    }
+    __device__ __forceinline__ void fetched() {
+        cp_async_commit();
+        write_at = write_at + stage_bytes == end ? 0 : write_at + stage_bytes;
+    }
+    __device__ __forceinline__ void next() { read_at = read_at + stage_bytes == end ? 0 : read_at + stage_bytes; }
+    __device__ __forceinline__ void read(int which, float2 (&o)[VEC * NV / 2]) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const unsigned from = at + read_at + (which * NV + i) * VB * blockDim.x;
+            Vec<T, VEC> r;
+            if constexpr (VB == 16) asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(from) : "memory");
+            else if constexpr (VB == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(from) : "memory");
+            else asm volatile("ld.shared.b16 %0, [%1];" : "=h"(r) : "r"(from) : "memory");
+            unpack<T, VEC>(r, reinterpret_cast<float *>(o) + i * VEC);
+        }
+    }
+    __device__ __forceinline__ float2 read_stats() const {
+        float2 r;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(stats_at(read_at)) : "memory");
+        return r;
+    }
+};
+
+// sums over a row's threads, a part of a warp or the block
+template <bool BLOCK, int M>
+__device__ __forceinline__ void group_sum(float (&v)[M], int tpr, float *red, int &turn) {
+    if constexpr (BLOCK) {
+        row_sum<true, M>(v, tpr, red, turn);
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < tpr)
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(~0u, v[m], o);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float reciprocal_root(float x) {
+    if constexpr (sizeof(T) == 2) return rsqrtf(x);                // (2 units in the last place of float32)
+    return 1.f / sqrtf(x);
+}
+
+// NV vectors of a row at `row`
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_pairs(T *row, int t, int tpr, int c, const float2 (&v)[VEC * NV / 2]) {
+    store_row<T, VEC, NV>(row, t, tpr, c, reinterpret_cast<const float *>(v));
+}
+
 template <typename T, int VEC, int NV, bool BLOCK, bool ACT>
 __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock, kGroupRowThreads / (BLOCK ? 512 : kNormBlock))
     k_group_row(const __grid_constant__ GroupShape s, const T *x, int tpr, T *y, float2 *stats) {
@@ -93,45 +185,59 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock, kGroupRowThreads / (
     int turn = 0;
     const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr, rpb = BLOCK ? 1 : kNormBlock / tpr;
     const int c = s.C / s.G;
-    const long long row0 = (long long)blockIdx.x * rpb + sub, step = (long long)gridDim.x * rpb / s.G;   // (a multiple of G)
-    const int g = (int)(row0 % s.G);
-    long long n = row0 / s.G;
-    float wv[E], bv[E];
+    // (the rows at once are a multiple of G)
+    const long long row0 = (long long)blockIdx.x * rpb + sub;
+    const int step = (int)((long long)gridDim.x * rpb / s.G), g = (int)(row0 % s.G);
+    int n = (int)(row0 / s.G), turns = (int)s.N - (int)((long long)blockIdx.x * rpb / s.G);   // (of the block: its first row's)
+    float2 wv[E / 2], bv[E / 2];
     const size_t at = (size_t)g * c, ws = s.wf32 ? 4 : sizeof(T);
-    load_cols<T, VEC, NV>(s.w ? static_cast<const char *>(s.w) + at * ws : nullptr, s.wf32, 1.f, t, tpr, c, wv);
-    load_cols<T, VEC, NV>(s.b ? static_cast<const char *>(s.b) + at * ws : nullptr, s.wf32, 0.f, t, tpr, c, bv);
-    const RowRing<T, VEC, NV, 1, false, false> ring{ring_smem, t, tpr, c, sub, rpb};
-    auto fetch = [&](int stage, long long i) {
-        ring.fetch(stage, 0, x + (i < s.N ? i : 0) * s.xs + at, i < s.N);
-        cp_async_commit();
+    load_cols<T, VEC, NV>(s.w ? static_cast<const char *>(s.w) + at * ws : nullptr, s.wf32, 1.f, t, tpr, c, reinterpret_cast<float *>(wv));
+    load_cols<T, VEC, NV>(s.b ? static_cast<const char *>(s.b) + at * ws : nullptr, s.wf32, 0.f, t, tpr, c, reinterpret_cast<float *>(bv));
+    GroupRing<T, VEC, NV, 1, false> ring(ring_smem, t, tpr, c);
+    const T *src = x + n * s.xs + at;
+    T *dst = y + (long long)n * s.C + at;
+    const long long src_step = step * s.xs, dst_step = (long long)step * s.C;
+    const int N = (int)s.N;
+    int ahead = n;
+    auto fetch = [&] {
+        if (ahead < N) ring.fetch(0, src);
+        ring.fetched();
+        ahead += step;
+        src += src_step;
     };
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) fetch(i, n + i * step);
-    // all threads of a block make as many turns: its first sample is in the first row's
-    for (long long first = (long long)blockIdx.x * rpb / s.G, stage = 0; first < s.N; first += step, n += step, stage = (stage + 1) % ST) {
-        fetch((int)(stage + ST - 1) % ST, n + (ST - 1) * step);
+    for (int i = 0; i < ST - 1; ++i) fetch();
+    const float inv = 1.f / (float)c;
+    for (; turns > 0; turns -= step, n += step, dst += dst_step) {
+        fetch();
         cp_async_wait<ST - 1>();
-        float v[E], sum[1] = {0.f};
-        ring.read((int)stage, 0, nullptr, v);
+        float2 v[E / 2], two = both(0.f);
+        ring.read(0, v);
+        ring.next();
 #pragma unroll
-        for (int j = 0; j < E; ++j) sum[0] += v[j];
-        row_sum<BLOCK, 1>(sum, tpr, red, turn);
-        const float mean = sum[0] / (float)c;
-        float q[1] = {0.f};
+        for (int j = 0; j < E / 2; ++j) two = add2(two, v[j]);
+        float sum[1] = {two.x + two.y};
+        group_sum<BLOCK, 1>(sum, tpr, red, turn);
+        const float mean = sum[0] * inv;
+        two = both(0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                v[i * VEC + j] -= mean;
-                if ((i * tpr + t) * VEC < c) q[0] = fmaf(v[i * VEC + j], v[i * VEC + j], q[0]);
+        for (int j = 0; j < E / 2; ++j) {
+            v[j] = add2(v[j], both(-mean));
+            if constexpr (VEC > 1) {
+                if ((j * 2 / VEC * tpr + t) * VEC < c) two = fma2(v[j], v[j], two);
+            } else {
+                if (2 * j * tpr + t < c) two.x = fmaf(v[j].x, v[j].x, two.x);
+                if ((2 * j + 1) * tpr + t < c) two.y = fmaf(v[j].y, v[j].y, two.y);
             }
-        row_sum<BLOCK, 1>(q, tpr, red, turn);
-        const float rstd = 1.f / sqrtf(q[0] / (float)c + s.eps);
-        if (n < s.N) {
+        }
+        sum[0] = two.x + two.y;
+        group_sum<BLOCK, 1>(sum, tpr, red, turn);
+        const float rstd = reciprocal_root<T>(fmaf(sum[0], inv, s.eps));
+        if (n < N) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = activate<T, ACT>(fmaf(v[j] * rstd, wv[j], bv[j]));
-            store_row<T, VEC, NV>(y + n * s.C + at, t, tpr, c, v);
-            if (stats && t == 0) stats[n * s.G + g] = make_float2(mean, rstd);
+            for (int j = 0; j < E / 2; ++j) v[j] = activate<T, ACT>(fma2(mul2(v[j], both(rstd)), wv[j], bv[j]));
+            store_pairs<T, VEC, NV>(dst, t, tpr, c, v);
+            if (stats && t == 0) stats[(long long)n * s.G + g] = make_float2(mean, rstd);
         }
     }
 }
@@ -148,55 +254,72 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
     const int c = s.C / s.G;
     // a block's rows are one group's of several samples, so that it adds their column sums itself; fewer samples than
     // that: as in the forward
-    const long long row0 = (long long)blockIdx.x * rpb + sub, step = (long long)gridDim.x * rpb / s.G;
-    const long long first0 = same ? (long long)(blockIdx.x / s.G) * rpb : (long long)blockIdx.x * rpb / s.G;
+    const long long row0 = (long long)blockIdx.x * rpb + sub;
+    const int step = (int)((long long)gridDim.x * rpb / s.G), N = (int)s.N;
+    const int first0 = (int)(same ? (long long)(blockIdx.x / s.G) * rpb : (long long)blockIdx.x * rpb / s.G);
     const int g = (int)(same ? blockIdx.x % s.G : row0 % s.G);
-    long long n = same ? first0 + sub : row0 / s.G;
-    float wv[E], bv[ACT ? E : 1], aw[E], ab[E];
+    int n = same ? first0 + sub : (int)(row0 / s.G);
+    float2 wv[E / 2], bv[ACT ? E / 2 : 1], aw[E / 2], ab[E / 2];
     const size_t at = (size_t)g * c, ws = s.wf32 ? 4 : sizeof(T);
-    load_cols<T, VEC, NV>(s.w ? static_cast<const char *>(s.w) + at * ws : nullptr, s.wf32, 1.f, t, tpr, c, wv);
-    if constexpr (ACT) load_cols<T, VEC, NV>(s.b ? static_cast<const char *>(s.b) + at * ws : nullptr, s.wf32, 0.f, t, tpr, c, bv);
+    load_cols<T, VEC, NV>(s.w ? static_cast<const char *>(s.w) + at * ws : nullptr, s.wf32, 1.f, t, tpr, c, reinterpret_cast<float *>(wv));
+    if constexpr (ACT)
+        load_cols<T, VEC, NV>(s.b ? static_cast<const char *>(s.b) + at * ws : nullptr, s.wf32, 0.f, t, tpr, c, reinterpret_cast<float *>(bv));
 #pragma unroll
-    for (int j = 0; j < E; ++j) aw[j] = ab[j] = 0.f;
-    const RowRing<T, VEC, NV, 2, true, false> ring{ring_smem, t, tpr, c, sub, rpb};
-    auto fetch = [&](int stage, long long i) {
-        const bool live = i < s.N;
-        const long long m = live ? i : 0;
-        ring.fetch(stage, 0, x + m * s.xs + at, live);
-        ring.fetch(stage, 1, dy + m * s.gs + at, live);
-        ring.fetch_stats(stage, stats + m * s.G + g, live);
-        cp_async_commit();
+    for (int j = 0; j < E / 2; ++j) aw[j] = ab[j] = both(0.f);
+    GroupRing<T, VEC, NV, 2, true> ring(ring_smem, t, tpr, c);
+    const T *xp = x + n * s.xs + at, *gp = dy + n * s.gs + at;
+    const float2 *sp = stats + (long long)n * s.G + g;
+    T *dst = dx + (long long)n * s.C + at;
+    const long long x_step = step * s.xs, g_step = step * s.gs, s_step = (long long)step * s.G, d_step = (long long)step * s.C;
+    int ahead = n;
+    auto fetch = [&] {
+        if (ahead < N) {
+            ring.fetch(0, xp);
+            ring.fetch(1, gp);
+            ring.fetch_stats(sp);
+        }
+        ring.fetched();
+        ahead += step;
+        xp += x_step;
+        gp += g_step;
+        sp += s_step;
     };
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) fetch(i, n + i * step);
-    for (long long first = first0, stage = 0; first < s.N; first += step, n += step, stage = (stage + 1) % ST) {
-        fetch((int)(stage + ST - 1) % ST, n + (ST - 1) * step);
+    for (int i = 0; i < ST - 1; ++i) fetch();
+    const float inv = 1.f / (float)c;
+    for (int turns = N - first0; turns > 0; turns -= step, n += step, dst += d_step) {
+        fetch();
         cp_async_wait<ST - 1>();
-        const float2 ns = *reinterpret_cast<const float2 *>(ring.stats_at((int)stage));
-        float h[E], d[E], sum[2] = {0.f, 0.f};
-        ring.read((int)stage, 0, nullptr, h);
-        ring.read((int)stage, 1, nullptr, d);
+        const float2 ns = ring.read_stats();
+        float2 h[E / 2], d[E / 2], s0 = both(0.f), s1 = both(0.f);
+        ring.read(0, h);
+        ring.read(1, d);
+        ring.next();
+        if (n < N) {                                               // (what a stage without a row holds is an earlier one)
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            // past the row's end x and dy are 0, and dy = 0 keeps the sums clean
-            h[j] = (h[j] - ns.x) * ns.y;
-            if constexpr (ACT) d[j] = back<T, ACT>(d[j], fmaf(h[j], wv[j], bv[j]));
-            aw[j] = fmaf(d[j], h[j], aw[j]);
-            ab[j] += d[j];
-            d[j] *= wv[j];
-            sum[0] += d[j];
-            sum[1] = fmaf(d[j], h[j], sum[1]);
+            for (int j = 0; j < E / 2; ++j) {
+                // past the row's end x and dy are 0, and dy = 0 keeps the sums clean
+                h[j] = mul2(add2(h[j], both(-ns.x)), both(ns.y));
+                if constexpr (ACT) d[j] = back<T, ACT>(d[j], fma2(h[j], wv[j], bv[j]));
+                aw[j] = fma2(d[j], h[j], aw[j]);
+                ab[j] = add2(ab[j], d[j]);
+                d[j] = mul2(d[j], wv[j]);
+                s0 = add2(s0, d[j]);
+                s1 = fma2(d[j], h[j], s1);
+            }
         }
-        row_sum<BLOCK, 2>(sum, tpr, red, turn);
-        const float c1 = sum[0] / (float)c, c2 = sum[1] / (float)c;
-        if (n < s.N) {
+        float sum[2] = {s0.x + s0.y, s1.x + s1.y};
+        group_sum<BLOCK, 2>(sum, tpr, red, turn);
+        const float2 c1 = both(-sum[0] * inv), c2 = both(-sum[1] * inv);
+        if (n < N) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) d[j] = ns.y * (d[j] - c1 - h[j] * c2);
-            store_row<T, VEC, NV>(dx + n * s.C + at, t, tpr, c, d);
+            for (int j = 0; j < E / 2; ++j) d[j] = mul2(both(ns.y), fma2(h[j], c2, add2(d[j], c1)));
+            store_pairs<T, VEC, NV>(dst, t, tpr, c, d);
         }
     }
     if (!part) return;
     cp_async_wait<0>();
+    const float *sw = reinterpret_cast<const float *>(aw), *sb = reinterpret_cast<const float *>(ab);
     if (!BLOCK && same) {
         // the block's rows, added in their order: cols [2][rows][tpr E]
         __syncthreads();
@@ -207,8 +330,8 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const int col = (i * tpr + t) * VEC + j;
-                cols[sub * wide + col] = aw[i * VEC + j];
-                cols[(rpb + sub) * wide + col] = ab[i * VEC + j];
+                cols[sub * wide + col] = sw[i * VEC + j];
+                cols[(rpb + sub) * wide + col] = sb[i * VEC + j];
             }
         __syncthreads();
         float *out = part + (size_t)(blockIdx.x / s.G) * 2 * s.C + at;
@@ -223,15 +346,15 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
         }
         return;
     }
-    float *out = part + (size_t)(row0 / s.G) * 2 * s.C + at;
+    float *out = part + (size_t)(same ? blockIdx.x / s.G : row0 / s.G) * 2 * s.C + at;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             const int col = (i * tpr + t) * VEC + j;
             if (col < c) {
-                out[col] = aw[i * VEC + j];
-                out[s.C + col] = ab[i * VEC + j];
+                out[col] = sw[i * VEC + j];
+                out[s.C + col] = sb[i * VEC + j];
             }
         }
 }
@@ -314,17 +437,27 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_stats(const __grid_cons
     }
 }
 
-// the group's statistics from its splits', by 8 lanes
+// the group's statistics from its splits', by 8 lanes: the mean, then the squares around it (the partials are in L1 by then)
 __device__ __forceinline__ float2 group_join(const GroupShape &s, const float2 *part, long long n, int g) {
-    const float c = (float)(s.C / s.G);
-    Moments m{0.f, 0.f, 0.f};
-    if (g < s.G)
-        for (int i = threadIdx.x & 7; i < s.splits; i += 8) {
-            const float2 a = __ldg(part + ((size_t)n * s.splits + i) * s.G + g);
-            m.join((float)(s.L * (i + 1) / s.splits - s.L * i / s.splits) * c, a.x, a.y);
-        }
-    m.join_lanes<8>();
-    return make_float2(m.mean, 1.f / sqrtf(m.m2 / ((float)s.L * c) + s.eps));
+    const float c = (float)(s.C / s.G), all = (float)s.L * c;
+    const float2 *at = part + (size_t)n * s.splits * s.G + g;
+    const int lane = threadIdx.x & 7, many = g < s.G ? s.splits : 0;
+    auto count = [&](int i) { return (float)(s.L * (i + 1) / s.splits - s.L * i / s.splits) * c; };
+    float sum = 0.f, q = 0.f;
+#pragma unroll 4
+    for (int i = lane; i < many; i += 8) sum = fmaf(count(i), __ldg(&at[(size_t)i * s.G].x), sum);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    const float mean = sum / all;
+#pragma unroll 4
+    for (int i = lane; i < many; i += 8) {
+        const float2 a = __ldg(at + (size_t)i * s.G);
+        const float d = a.x - mean;
+        q += fmaf(count(i) * d, d, a.y);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
+    return make_float2(mean, 1.f / sqrtf(q / all + s.eps));
 }
 
 template <typename T, int VEC>
@@ -381,7 +514,13 @@ __global__ void __launch_bounds__(kGroupThreads)
                 const long long next = at + (long long)sp.slots * kGroupBatch;
                 if (next < p.to) raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + next * s.xs + c0));
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) v[j] = activate<T, ACT>(fmaf((v[j] - a.x) * a.y, w[j], b[j]));
+                for (int j = 0; j < VEC; j += 2) {
+                    float2 z = make_float2(v[j], j + 1 < VEC ? v[j + 1] : 0.f);
+                    z = mul2(add2(z, both(-a.x)), both(a.y));
+                    z = activate<T, ACT>(fma2(z, make_float2(w[j], j + 1 < VEC ? w[j + 1] : 0.f), make_float2(b[j], j + 1 < VEC ? b[j + 1] : 0.f)));
+                    v[j] = z.x;
+                    if (j + 1 < VEC) v[j + 1] = z.y;
+                }
                 store_vec<T, VEC>(out + at * s.C + c0, v);
             }
         }
@@ -425,11 +564,17 @@ __global__ void __launch_bounds__(kGroupThreads)
                     unpack<T, VEC>(rx[i], h);
                     unpack<T, VEC>(rg[i], d);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {      // where no position is, dy is 0
-                        h[j] = (h[j] - a.x) * a.y;
-                        d[j] = back<T, ACT>(d[j], fmaf(h[j], w[j], b[j]));
-                        sw[j] = fmaf(d[j], h[j], sw[j]);
-                        sb[j] += d[j];
+                    for (int j = 0; j < VEC; j += 2) {   // where no position is, dy is 0
+                        constexpr bool TWO = VEC > 1;
+                        float2 z = mul2(add2(make_float2(h[j], TWO ? h[j + 1] : 0.f), both(-a.x)), both(a.y));
+                        const float2 t = back<T, ACT>(make_float2(d[j], TWO ? d[j + 1] : 0.f),
+                                                      fma2(z, make_float2(w[j], TWO ? w[j + 1] : 0.f), make_float2(b[j], TWO ? b[j + 1] : 0.f)));
+                        sw[j] = fmaf(t.x, z.x, sw[j]);
+                        sb[j] += t.x;
+                        if constexpr (TWO) {
+                            sw[j + 1] = fmaf(t.y, z.y, sw[j + 1]);
+                            sb[j + 1] += t.y;
+                        }
                     }
                 }
             }
@@ -509,10 +654,14 @@ __global__ void __launch_bounds__(kGroupThreads)
                 unpack<T, VEC>(rx[i], h);
                 unpack<T, VEC>(rg[i], d);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    h[j] = (h[j] - a.x) * a.y;
-                    d[j] = back<T, ACT>(d[j], fmaf(h[j], w[j], b[j])) * w[j];
-                    d[j] = a.y * (d[j] - m.x - h[j] * m.y);
+                for (int j = 0; j < VEC; j += 2) {
+                    constexpr bool TWO = VEC > 1;
+                    const float2 wj = make_float2(w[j], TWO ? w[j + 1] : 0.f);
+                    const float2 z = mul2(add2(make_float2(h[j], TWO ? h[j + 1] : 0.f), both(-a.x)), both(a.y));
+                    float2 t = mul2(back<T, ACT>(make_float2(d[j], TWO ? d[j + 1] : 0.f), fma2(z, wj, make_float2(b[j], TWO ? b[j + 1] : 0.f))), wj);
+                    t = mul2(both(a.y), fma2(z, both(-m.y), add2(t, both(-m.x))));
+                    d[j] = t.x;
+                    if constexpr (TWO) d[j + 1] = t.y;
                 }
                 store_vec<T, VEC>(out + at * s.C + c0, d);
             }
@@ -577,7 +726,7 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
         if (group_rows(s.L, each)) {
             const NormGeom g = norm_geom(each, VEC, true);
             constexpr int NV = 16 / VEC;
-            const size_t smem = kNormStages<T> * RowRing<T, VEC, NV, 1, false, false>::stage_bytes(each, g.threads, g.rpb);
+            const size_t smem = GroupRing<T, VEC, NV, 1, false>::bytes(g.threads);
             auto go = [&](auto kern) {
                 set_kernel_smem(kern, smem);
                 const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (kGroupRowThreads / g.threads));
@@ -608,7 +757,7 @@ long long group_backward(const GroupShape &s, const T *dy, const T *x, const flo
         if (group_rows(s.L, each)) {
             const NormGeom g = norm_geom(each, VEC, true);
             constexpr int NV = 16 / VEC;
-            const size_t smem = kNormStages<T> * RowRing<T, VEC, NV, 2, true, false>::stage_bytes(each, g.threads, g.rpb);
+            const size_t smem = GroupRing<T, VEC, NV, 2, true>::bytes(g.threads);
             const GroupBack to = group_back(g, s.N, s.G);
             const size_t cols = g.block ? 0 : (size_t)2 * kNormBlock * 16 * 4;
             auto go = [&](auto kern) {

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "linear_internal.cuh"
+#include "pairs.cuh"
 #include "tcgen05.cuh"
 
 namespace sdm {
@@ -83,22 +84,6 @@ __device__ __forceinline__ void split3(float x0, float x1, unsigned (&p)[3]) {
             x1 = minus_hi(x1, p[i]);
         }
     }
-}
-
-// two floats at once
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<unsigned long long &>(d))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)), "l"(reinterpret_cast<unsigned long long &>(c)));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<unsigned long long &>(d))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return d;
 }
 
 // 16 floats as three planes of 8 packed columns of tensor memory
