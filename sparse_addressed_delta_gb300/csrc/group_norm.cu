@@ -49,34 +49,45 @@ __device__ __forceinline__ float2 back(float2 dy, float2 z) {
     return mul2(dy, mul2(p, fma2(z, fma2(p, both(-1.f), both(1.f)), both(1.f))));
 }
 
-// mean and sum of squares around it of nb values joined to those of n
+// a running count, mean and sum of squares around it
 struct Moments {
     float n, mean, m2;
+    // those of nb values joined
     __device__ __forceinline__ void join(float nb, float mb, float qb) {
-        const float all = n + nb;
-        if (nb == 0.f) return;
         if (n == 0.f) {                                  // (0 times a difference's square, which may be infinite)
             *this = Moments{nb, mb, qb};
             return;
         }
-        const float d = mb - mean, f = nb / all;
+        const float d = mb - mean, f = __fdividef(nb, n + nb);   // (a weight's error moves the mean by 2^-22 of the difference)
         mean = fmaf(d, f, mean);
         m2 += fmaf(d * d, n * f, qb);
-        n = all;
-    }
-    template <int LANES>
-    __device__ __forceinline__ void join_lanes() {
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) {
-            const float nb = __shfl_xor_sync(~0u, n, o), mb = __shfl_xor_sync(~0u, mean, o), qb = __shfl_xor_sync(~0u, m2, o);
-            // both halves of a pair join in the same order, so that all lanes agree
-            Moments a = threadIdx.x & o ? Moments{nb, mb, qb} : *this;
-            const Moments c = threadIdx.x & o ? *this : Moments{nb, mb, qb};
-            a.join(c.n, c.mean, c.m2);
-            *this = a;
-        }
+        n += nb;
     }
 };
+// The mean and the squares around it of `many` parts by LANES lanes: entry(i) is a part's count, mean and squares. In two
+// passes, sums alone: joined one by one, each with a division, the parts of 76 blocks took 20 us.
+template <int LANES, typename F>
+__device__ __forceinline__ float2 join_parts(int many, float all, F entry) {
+    const int lane = threadIdx.x % LANES;
+    float sum = 0.f, q = 0.f;
+#pragma unroll 4
+    for (int i = lane; i < many; i += LANES) {
+        const Moments p = entry(i);
+        sum = fmaf(p.n, p.mean, sum);
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    const float mean = sum / all;
+#pragma unroll 4
+    for (int i = lane; i < many; i += LANES) {
+        const Moments p = entry(i);
+        const float d = p.mean - mean;
+        q += p.n > 0.f ? fmaf(p.n * d, d, p.m2) : 0.f;
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
+    return make_float2(mean, q);
+}
 
 struct GroupShape {
     long long N, L, xs, gs;              // samples, positions, elements between positions of x and of the gradient
@@ -423,41 +434,31 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_stats(const __grid_cons
         if (sp.slots > 1) break;
     }
     __syncthreads();
-    const int each = sp.cv / s.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int g = warp; g < s.G; g += kGroupThreads / 32) {
-        Moments m{0.f, 0.f, 0.f};
-        for (int i = lane; i < each * sp.slots; i += 32) {
+    const int each = sp.cv / s.G;
+    const long long rows = p.to - p.from;
+    const float all = (float)rows * (float)(s.C / s.G);
+    for (int g0 = 0; g0 < s.G; g0 += kGroupThreads / 8) {
+        const int g = g0 + (threadIdx.x >> 3);
+        const float2 a = join_parts<8>(g < s.G ? each * sp.slots : 0, all, [&](int i) {
             const int sl = i / each;
-            const float2 a = acc[sl * sp.cv + g * each + i % each];
-            const long long rows = p.to - p.from - sl;
-            m.join((float)((rows > 0 ? (rows + sp.slots - 1) / sp.slots : 0) * VEC), a.x, a.y);
-        }
-        m.join_lanes<32>();
-        if (lane == 0) part[((size_t)p.n * s.splits + p.split) * s.G + g] = make_float2(m.mean, m.m2);
+            const float2 e = acc[sl * sp.cv + g * each + i % each];
+            return Moments{(float)((rows > sl ? (rows - sl + sp.slots - 1) / sp.slots : 0) * VEC), e.x, e.y};
+        });
+        if (g < s.G && (threadIdx.x & 7) == 0) part[((size_t)p.n * s.splits + p.split) * s.G + g] = a;
     }
 }
 
-// the group's statistics from its splits', by 8 lanes: the mean, then the squares around it (the partials are in L1 by then)
-__device__ __forceinline__ float2 group_join(const GroupShape &s, const float2 *part, long long n, int g) {
+// joined [N][G] mean and rstd from the splits', a warp a group
+__global__ void __launch_bounds__(kGroupThreads) k_group_join(const __grid_constant__ GroupShape s, const float2 *part, float2 *joined) {
+    const long long i = (long long)blockIdx.x * (kGroupThreads / 32) + (threadIdx.x >> 5);
+    if (i >= s.N * s.G) return;
     const float c = (float)(s.C / s.G), all = (float)s.L * c;
-    const float2 *at = part + (size_t)n * s.splits * s.G + g;
-    const int lane = threadIdx.x & 7, many = g < s.G ? s.splits : 0;
-    auto count = [&](int i) { return (float)(s.L * (i + 1) / s.splits - s.L * i / s.splits) * c; };
-    float sum = 0.f, q = 0.f;
-#pragma unroll 4
-    for (int i = lane; i < many; i += 8) sum = fmaf(count(i), __ldg(&at[(size_t)i * s.G].x), sum);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    const float mean = sum / all;
-#pragma unroll 4
-    for (int i = lane; i < many; i += 8) {
-        const float2 a = __ldg(at + (size_t)i * s.G);
-        const float d = a.x - mean;
-        q += fmaf(count(i) * d, d, a.y);
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
-    return make_float2(mean, 1.f / sqrtf(q / all + s.eps));
+    const float2 *at = part + i / s.G * s.splits * s.G + i % s.G;
+    const float2 a = join_parts<32>(s.splits, all, [&](int k) {
+        const float2 e = __ldg(at + (size_t)k * s.G);
+        return Moments{(float)(s.L * (k + 1) / s.splits - s.L * k / s.splits) * c, e.x, e.y};
+    });
+    if ((threadIdx.x & 31) == 0) joined[i] = make_float2(a.x, 1.f / sqrtf(a.y / all + s.eps));
 }
 
 template <typename T, int VEC>
@@ -468,16 +469,14 @@ __device__ __forceinline__ void load_params(const void *p, bool f32, float fill,
 }
 
 template <typename T, int VEC, bool ACT>
-__global__ void __launch_bounds__(kGroupThreads)
-    k_group_apply(const __grid_constant__ GroupShape s, const T *x, const float2 *part, T *y, float2 *stats) {
-    extern __shared__ float2 norm[];                     // [G] mean, rstd
+__global__ void __launch_bounds__(kGroupThreads) k_group_apply(const __grid_constant__ GroupShape s, const T *x, const float2 *stats, T *y) {
     const Piece p(s);
     const Spread sp(s.C, VEC);
     const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
+    const int cv0 = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x, wide = sp.slots > 1 ? sp.cv : kGroupThreads;
+    if (slot >= sp.slots) return;
     const T *base = x + p.n * s.L * s.xs;
     T *out = y + p.n * s.L * s.C;
-    const int cv0 = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x, wide = sp.slots > 1 ? sp.cv : kGroupThreads;
-    const bool here = slot < sp.slots && cv0 < sp.cv;
     Vec<T, VEC> raw[kGroupBatch];
     auto fetch = [&](long long r, int c0) {
 #pragma unroll
@@ -486,24 +485,13 @@ __global__ void __launch_bounds__(kGroupThreads)
             if (at < p.to) raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0));
         }
     };
-    if (here) fetch(p.from + slot, cv0 * VEC);           // in the statistics' time
-    for (int g0 = 0; g0 < s.G; g0 += kGroupThreads / 8) {
-        const int g = g0 + (threadIdx.x >> 3);
-        const float2 a = group_join(s, part, p.n, g);
-        if ((threadIdx.x & 7) == 0 && g < s.G) {
-            norm[g] = a;
-            if (stats && p.split == 0) stats[p.n * s.G + g] = a;
-        }
-    }
-    __syncthreads();
-    if (!here) return;
     for (int cv = cv0; cv < sp.cv; cv += wide) {
         const int c0 = cv * VEC;
-        const float2 a = norm[c0 / each];
+        fetch(p.from + slot, c0);
+        const float2 a = stats[p.n * s.G + c0 / each];
         float w[VEC], b[VEC];
         load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
         load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
-        if (cv != cv0) fetch(p.from + slot, c0);
         for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * kGroupBatch) {
 #pragma unroll
             for (int i = 0; i < kGroupBatch; ++i) {
@@ -594,30 +582,40 @@ __global__ void __launch_bounds__(kGroupThreads)
     }
 }
 
-// terms [N][G]: means over the group of w dz and of w dz xhat; a warp a group
+// terms [N][G]: means over the group of w dz and of w dz xhat, from the partials' columns; by `lanes` (32 or all of the
+// block's) threads a group
 template <typename T>
-__global__ void __launch_bounds__(kGroupThreads) k_group_terms(const __grid_constant__ GroupShape s, const float *part, float2 *terms) {
-    const long long i = (long long)blockIdx.x * (kGroupThreads / 32) + (threadIdx.x >> 5);
-    if (i >= s.N * s.G) return;
-    const int lane = threadIdx.x & 31, g = (int)(i % s.G), each = s.C / s.G;
-    const long long n = i / s.G;
-    double a = 0.0, b = 0.0;
+__global__ void __launch_bounds__(kGroupThreads) k_group_terms(const __grid_constant__ GroupShape s, const float *part, int lanes, float2 *terms) {
+    __shared__ float2 sums[kGroupThreads / 32];
+    const long long i = (long long)blockIdx.x * (kGroupThreads / lanes) + threadIdx.x / lanes;
+    const int g = (int)(i % s.G), each = s.C / s.G, many = i < s.N * s.G ? s.splits * each : 0;
+    const float *at = part + (size_t)(i / s.G) * s.splits * 2 * s.C + g * each;
+    float a = 0.f, b = 0.f;
 #pragma unroll 4
-    for (int e = lane; e < s.splits * each; e += 32) {
-        const int c = g * each + e % each;
+    for (int e = threadIdx.x % lanes; e < many; e += lanes) {
+        const int c = e % each;
+        const float *p = at + (size_t)(e / each) * 2 * s.C + c;
         float w[1];
-        load_params<T, 1>(s.w, s.wf32, 1.f, c, w);
-        const float *at = part + ((size_t)n * s.splits + e / each) * 2 * s.C + c;
-        a += (double)at[s.C] * w[0];
-        b += (double)at[0] * w[0];
+        load_params<T, 1>(s.w, s.wf32, 1.f, g * each + c, w);
+        a = fmaf(p[s.C], w[0], a);
+        b = fmaf(p[0], w[0], b);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a += __shfl_xor_sync(~0u, a, o);
         b += __shfl_xor_sync(~0u, b, o);
     }
-    const double count = (double)s.L * each;
-    if (lane == 0) terms[i] = make_float2((float)(a / count), (float)(b / count));
+    if (lanes > 32) {
+        if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+        for (int w = 0; w < kGroupThreads / 32; ++w) {
+            a += sums[w].x;
+            b += sums[w].y;
+        }
+    }
+    const float count = (float)s.L * (float)each;
+    if (threadIdx.x % lanes == 0 && i < s.N * s.G) terms[i] = make_float2(a / count, b / count);
 }
 
 template <typename T, int VEC, bool ACT>
@@ -741,8 +739,10 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
         const size_t smem = (size_t)slots * cv * 8;
         set_kernel_smem(k_group_stats<T, VEC>, smem);
         k_group_stats<T, VEC><<<grid, kGroupThreads, smem, st>>>(s, x, part);
-        set_kernel_smem(k_group_apply<T, VEC, ACT>, s.G * 8);
-        k_group_apply<T, VEC, ACT><<<grid, kGroupThreads, s.G * 8, st>>>(s, x, part, y, stats);
+        float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
+        const long long warps = s.N * s.G;
+        k_group_join<<<(unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st>>>(s, part, joined);
+        k_group_apply<T, VEC, ACT><<<grid, kGroupThreads, 0, st>>>(s, x, joined, y);
     });
 }
 
@@ -775,8 +775,9 @@ long long group_backward(const GroupShape &s, const T *dy, const T *x, const flo
         const size_t smem = slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0;
         set_kernel_smem(k_group_sums<T, VEC, ACT>, smem);
         k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, part);
-        const long long warps = s.N * s.G;
-        k_group_terms<T><<<(unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st>>>(s, part, terms);
+        const int lanes = (long long)s.splits * each > 8 * 32 ? kGroupThreads : 32;
+        const long long groups = s.N * s.G, per = kGroupThreads / lanes;
+        k_group_terms<T><<<(unsigned)((groups + per - 1) / per), kGroupThreads, 0, st>>>(s, part, lanes, terms);
         k_group_apply_bwd<T, VEC, ACT><<<grid, kGroupThreads, 0, st>>>(s, dy, x, stats, terms, dx);
         parts = s.N * s.splits;
     });
@@ -807,7 +808,8 @@ size_t group_part_bytes(long long N, long long L, int C, int G, bool back) {
         return group_up((size_t)group_back(g, N, G).parts * 2 * C * 4);
     }
     const size_t pieces = (size_t)N * group_splits(N, L);
-    return group_up(pieces * (back ? (size_t)2 * C * 4 : (size_t)G * 8));
+    // (a forward that keeps no statistics: those of the whole samples behind the splits')
+    return group_up(pieces * (back ? (size_t)2 * C * 4 : (size_t)G * 8) + (back ? 0 : (size_t)N * G * 8));
 }
 size_t group_bytes(long long N, long long L, int C, int G, bool back) {
     return group_part_bytes(N, L, C, G, back) + (back && !group_rows(L, C / G) ? group_up((size_t)N * G * 8) : 0) + kAlign;
