@@ -202,12 +202,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (!tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin)) return false;
             {
                 const unsigned char *src = smem + it % ST * L::STAGE + L::K;
-                for (int i = unit0; i < unit1; ++i) {
+                auto one = [&](int i) {
                     const int row = 32 * (i & 1) + lane, piece = i >> 1, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
                     const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
                     float2 x[4];
                     load_piece<NP, KT * TILE>(src + off, x);
                     scale_piece(x, w, smem + L::KX + off, L::PLANE);
+                };
+                if (unit1 - unit0 == 3) {                          // side by side: one takes 500 cycles by itself
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) one(unit0 + i);
+                } else {
+                    for (int i = unit0; i < unit1; ++i) one(i);
                 }
             }
             if ((warp & 3) < 2 && ahead >= -46) {
