@@ -8,13 +8,12 @@
 // Every term carries its own decay, so none is a difference of larger ones. A segment begins with the state that
 // the forward kept and G = 0, and ends with <G, R>, R the gradient of the state there.
 //
-// S and G stay in registers in float32, transposed: 128 of Dv's columns are the lanes of tensor memory (a quarter
-// of KP a thread). dO^T and V^T are A operands in shared memory, the queries and keys with both their weights, three
-// bfloat16 planes each, one B operand of 2 KP columns: A and A' come from one product, W and W' from the next, in the
-// same buffer. With four products of KP columns, two buffers in turn, it took 188 us where it takes @@ (64 heads of
-// 128 x 128 x 64 chunks): shared memory bounds it (a product of 128 x 128 x 16 reads its operands at all of its rate,
-// and the threads that fill the other buffer wait for it), and the wider product reads its A operand half as often.
-// All is bilinear in (Dk, Dv), so blocks take KP columns of Dk and 128 of Dv for themselves, the pairs' sums too.
+// S and G stay in registers in float32, transposed: 128 of Dv's columns are the lanes of tensor memory. dO^T and V^T are
+// A operands in shared memory, the queries and keys with both their weights, three bfloat16 planes each, one B operand:
+// A and A' come from one product, W and W' from the next. All is bilinear in (Dk, Dv), so a block takes 64 columns of Dk
+// and 128 of Dv for itself, the pairs' sums too: it has room for a buffer of queries and one of keys, so that the threads
+// fill one (what they and the products take is shared memory's rate) while the other is multiplied. 64 heads of 128 x 128
+// x 64 chunks: @@ us; 128 columns of Dk a block, with one buffer, 157; four products instead of two 188.
 // Warps as in linear_scan_tc.cu.
 #include <type_traits>
 
@@ -25,18 +24,16 @@ namespace {
 
 constexpr int kDecC = 64, kDecWarps = 16, kDecThreads = 32 * (kDecWarps + 2);
 
-template <int KP, int NP>
+template <int NP>
 struct LinDecay {
-    static constexpr int TILE = kDecC * 128, KT = KP / 64;
+    static constexpr int KP = 64, TILE = kDecC * 128;
     // (a product's A operand of 128 rows reads on past the 64 of Q and dO: into what follows them)
-    static constexpr int Q = 0, G = Q + NP * KT * TILE, K = G + NP * 2 * TILE, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE;
-    static constexpr int STAGES = NP == 1 ? 2 : 1;
-    static constexpr int BUF = STAGES * STAGE, PLANE = 2 * KT * TILE, AUX = BUF + 3 * PLANE;   // [plane][weight][KT tiles]
+    static constexpr int Q = 0, G = Q + NP * TILE, K = G + NP * 2 * TILE, V = K + NP * TILE, STAGE = V + NP * 2 * TILE;
+    static constexpr int STAGES = NP == 1 ? 2 : 1, BUFS = NP == 1 ? 2 : 1;
+    static constexpr int BUF = STAGES * STAGE, PLANE = 2 * TILE, BUFFER = 3 * PLANE, AUX = BUF + BUFS * BUFFER;   // [plane][weight]
     static constexpr int POW = AUX, PAIR = POW + 4 * 80, SUMS = PAIR + 4 * 128, BARS = SUMS + 8 * kDecWarps, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    static constexpr int A = 0, A1 = KP, W = 2 * KP, W1 = 3 * KP;  // A', W' behind A and W (the pairs' products in A1's place, 2 x 64 columns)
-    static_assert(KP >= 64 && 4 * KP <= 512, "tensor memory");
-    static constexpr int PQ = KP == 128 ? A1 : 4 * KP, PG = PQ + 64;
+    static constexpr int A = 0, A1 = KP, W = 2 * KP, W1 = 3 * KP, PQ = 4 * KP, PG = PQ + 64;   // A', W' behind A and W; the pairs' products
 };
 
 enum { D_FULL = 0, D_EMPTY = 2, D_MUL = 4, D_CONV = 6, D_PAIR = 8, D_READ, D_PART, D_DRAIN, D_COUNT };
@@ -51,12 +48,13 @@ struct DecayArgs {
     int share, kblocks;
 };
 
-template <int KP, int NP>
+template <int NP>
 __global__ void __launch_bounds__(kDecThreads, 1)
     k_linear_decay(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                    const __grid_constant__ CUtensorMap mg, const __grid_constant__ LinearDims d, const __grid_constant__ DecayArgs a) {
-    using L = LinDecay<KP, NP>;
-    constexpr int C = kDecC, HD = KP / 4, ST = L::STAGES, KT = L::KT, TILE = L::TILE;
+    using L = LinDecay<NP>;
+    constexpr int C = kDecC, KP = L::KP, HD = KP / 4, ST = L::STAGES, TILE = L::TILE;
+    constexpr bool TWO = L::BUFS == 2;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     auto bar = reinterpret_cast<unsigned long long *>(smem + L::BARS);
@@ -136,17 +134,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             tc_fence_after();
             return there;
         };
-        // rows of Q or K times their two weights, as planes
-        auto convert = [&](const unsigned char *src, auto weights) {
-#pragma unroll
-            for (int i = tid; i < C * KP / 8; i += 32 * kDecWarps) {
-                const int row = i % C, piece = i / C, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
-                const float2 w = weights(row);
-                float2 x[4];
-                load_piece<NP, KT * TILE>(src + off, x);
-                scale_piece(x, w.x, smem + L::BUF + off, L::PLANE);
-                scale_piece(x, w.y, smem + L::BUF + KT * TILE + off, L::PLANE);
-            }
+        // rows of Q or K times their two weights, as planes: a piece of 8 columns a thread
+        static_assert(C * KP / 8 == 32 * kDecWarps, "one piece a thread");
+        auto convert = [&](const unsigned char *src, unsigned char *dst, auto weights) {
+            const int row = tid % C, off = tc_at(row, tid / C);
+            const float2 w = weights(row);
+            float2 x[4];
+            load_piece<NP, TILE>(src + off, x);
+            scale_piece(x, w.x, dst + off, L::PLANE);
+            scale_piece(x, w.y, dst + TILE + off, L::PLANE);
             fence_proxy_async_smem();
         };
         // <this thread's part of the state, a product>
@@ -173,9 +169,28 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         };
         float whole = 1.f;
         bool ok = true;
+        unsigned char *buf = smem + L::BUF, *keys = buf + (TWO ? L::BUFFER : 0);
         for (int it = 0; it < nch; ++it) {
             const int nt = ntok - (n0 + it) * C < C ? ntok - (n0 + it) * C : C;
             const unsigned char *st = smem + it % ST * L::STAGE;
+            ok = tc_warp_wait(bar + D_FULL + it % ST, it / ST & 1, dead, d.spin) && (TWO || it == 0 || wait(D_MUL + 1, it - 1));
+            if (!ok) break;
+            convert(st + L::Q, buf, [&](int t) {                   // (the product before from this buffer was waited for)
+                const float w = t < nt ? d.scale * pw[t + 1] : 0.f;
+                return make_float2(w, (float)(t + 1) * w);
+            });
+            arrive(D_CONV);
+            if (it > 0) {
+                if (TWO && !(ok = wait(D_MUL + 1, it - 1))) break;
+                advance(L::W, whole, S);
+                advance(L::W1, 1.f, G);
+            }
+            if (!TWO && !(ok = wait(D_MUL, it))) break;
+            convert(st + L::K, keys, [&](int t) {
+                const float w = t < nt ? pw[nt - 1 - t] : 0.f;
+                return make_float2(w, (float)(nt - 1 - t) * w);
+            });
+            arrive(D_CONV + 1);
             // the pairs: a token's row each of lanes 0..63
             if (!(ok = wait(D_PAIR, it))) break;
             if ((warp & 3) < 2) {
@@ -187,26 +202,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int i = 0; i < 16; ++i) sum = fmaf(apart[-i] * x[i], y[i], sum);
                 add(d.scale * sum);
             }
-            ok = tc_warp_wait(bar + D_FULL + it % ST, it / ST & 1, dead, d.spin) && (it == 0 || wait(D_MUL + 1, it - 1));
-            if (!ok) break;
-            convert(st + L::Q, [&](int t) {
-                const float w = t < nt ? d.scale * pw[t + 1] : 0.f;
-                return make_float2(w, (float)(t + 1) * w);
-            });
-            arrive(D_CONV);
-            if (it > 0) {
-                advance(L::W, whole, S);
-                advance(L::W1, 1.f, G);
-            }
-            if (!(ok = wait(D_MUL, it))) break;
-            convert(st + L::K, [&](int t) {
-                const float w = t < nt ? pw[nt - 1 - t] : 0.f;
-                return make_float2(w, (float)(nt - 1 - t) * w);
-            });
-            arrive(D_CONV + 1);
+            arrive(D_READ);
+            if (TWO && !(ok = wait(D_MUL, it))) break;
             dot(L::A, G);
             dot(L::A1, S);
-            arrive(D_READ);
             whole = pw[nt];
 #pragma unroll
             for (int i = 0; i < HD; ++i) G[i] = whole * fmaf((float)nt, S[i], G[i]);
@@ -246,12 +245,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         };
         auto pairs = [&](int it) {
             const uint32_t st = base + it % ST * L::STAGE;
-            scores(tu + L::PQ, tc_k_major(st + L::Q), tc_k_major(st + L::K), std::integral_constant<int, KT>{});
+            scores(tu + L::PQ, tc_k_major(st + L::Q), tc_k_major(st + L::K), std::integral_constant<int, 1>{});
             scores(tu + L::PG, tc_k_major(st + L::G), tc_k_major(st + L::V), std::integral_constant<int, 2>{});
             tc_commit_to(one, bar + D_PAIR);
         };
-        const uint32_t kn = tc_n_major(base + L::BUF, TILE);
-        auto product = [&](uint32_t dst, uint32_t vm) {
+        auto product = [&](uint32_t dst, uint32_t vm, uint32_t kn) {
             bool add = false;
 #pragma unroll
             for (int sum = 2; sum >= 0; --sum)
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 ok = ok && tc_warp_wait(bar + D_CONV + i, par, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
-                product(tu + (i == 0 ? L::A : L::W), tc_n_major(st + (i == 0 ? L::G : L::V), TILE));
+                product(tu + (i == 0 ? L::A : L::W), tc_n_major(st + (i == 0 ? L::G : L::V), TILE), tc_n_major(base + L::BUF + (TWO ? i : 0) * L::BUFFER, TILE));
                 tc_commit_to(one, bar + D_MUL + i);
             }
             if (!ok) break;
@@ -295,11 +293,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                          [&](unsigned char *st, int t0, unsigned long long *full) {
 #pragma unroll
             for (int m = 0; m < NP; ++m) {
-#pragma unroll
-                for (int c = 0; c < KT; ++c) {
-                    tc_tensor_load(st + L::Q + (m * KT + c) * TILE, &mq, k0 + 64 * c, tc_coord(a.heads[0], hk), t0, tc_coord(a.seqs[0], b) + m * d.B, full);
-                    tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, k0 + 64 * c, tc_coord(a.heads[1], hk), t0, tc_coord(a.seqs[1], b) + m * d.B, full);
-                }
+                tc_tensor_load(st + L::Q + m * TILE, &mq, k0, tc_coord(a.heads[0], hk), t0, tc_coord(a.seqs[0], b) + m * d.B, full);
+                tc_tensor_load(st + L::K + m * TILE, &mk, k0, tc_coord(a.heads[1], hk), t0, tc_coord(a.seqs[1], b) + m * d.B, full);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     tc_tensor_load(st + L::G + (m * 2 + c) * TILE, &mg, v0 + 64 * c, tc_coord(a.heads[3], h), t0, tc_coord(a.seqs[3], b) + m * d.B, full);
@@ -338,11 +333,11 @@ __global__ void __launch_bounds__(32) k_linear_decay_sum(const double *part, int
     if (threadIdx.x == 0) out[h] = (float)s;
 }
 
-template <int KP, int NP>
+template <int NP>
 cudaError_t decay(const LinearDims &d, const DecayArgs &a, const CUtensorMap *m, cudaStream_t st) {
-    using L = LinDecay<KP, NP>;
-    set_kernel_smem(k_linear_decay<KP, NP>, L::BYTES);
-    k_linear_decay<KP, NP><<<(unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
+    using L = LinDecay<NP>;
+    set_kernel_smem(k_linear_decay<NP>, L::BYTES);
+    k_linear_decay<NP><<<(unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
     return cudaGetLastError();
 }
 
@@ -359,7 +354,7 @@ cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const L
         a.seqs[i] = laid[i].s[0];
         a.heads[i] = laid[i].s[2];
     }
-    const cudaError_t e = np == 3 ? decay<64, 3>(d, a, m, st) : d.Dk > 64 ? decay<128, 1>(d, a, m, st) : decay<64, 1>(d, a, m, st);
+    const cudaError_t e = np == 3 ? decay<3>(d, a, m, st) : decay<1>(d, a, m, st);
     if (e != cudaSuccess) return e;
     k_linear_decay_sum<<<d.H, 32, 0, st>>>(part, d.B, d.H, a.kblocks * linear_tiles(d.Dv) * d.segs, grad_decay);
     return cudaGetLastError();

@@ -111,7 +111,7 @@ cudaError_t launch_linear_step(const LinearDims &d, const LinearIn &in, const vo
 cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, cudaStream_t st);
 // grad_decay [H] from the laid q, k, v and readings' gradient, the segments' first states and the gradients of the
 // states they end with (from the last one; one segment: may be null)
-inline int linear_decay_blocks(const LinearDims &d) { return d.dtype == SDM_F32 ? (d.Dk + 63) / 64 : 1; }   // of Dk
+inline int linear_decay_blocks(const LinearDims &d) { return (d.Dk + 63) / 64; }   // of Dk
 inline long long linear_decay_parts(const LinearDims &d) { return (long long)d.B * d.H * d.segs * linear_decay_blocks(d) * linear_tiles(d.Dv); }
 cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearLaid (&laid)[4], const float *starts, const float *ends,
                                 double *part, float *grad_decay, void *status, cudaStream_t st);
