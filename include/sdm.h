@@ -492,7 +492,7 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
  *   valid_tokens [B] int32, or NULL: all T. Tokens past it change nothing and none of their inputs
  *                is used; their readings (and gradients) are 0. Clamped to [0, T].
  *   readings     [B, T, H, Dv] contiguous, written whole
- *   workspace    sdm_linear_attention_workspace_bytes(shape) bytes, 256-byte aligned; up to 8 tokens need none
+ *   workspace    sdm_linear_attention_workspace_bytes(shape) bytes, 256-byte aligned; up to 12 tokens need none
  *                (sdm_linear_attention only). It begins with a status block, as the gated delta rule's does
  * Deterministic. bfloat16 readings and gradients are float32 results, rounded once.
  * A NaN or infinity of an input reaches the readings and states that the recurrence carries it to, and no others.

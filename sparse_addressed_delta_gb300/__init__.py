@@ -39,7 +39,7 @@ _calls_path = os.path.join(_HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFI
 
 SDM_F32, SDM_BF16 = 0, 1
 DELTA_STEP_TOKENS = 8             # gated_delta: up to this many tokens go one by one
-LINEAR_STEP_TOKENS = 8            # linear_attention: the same
+LINEAR_STEP_TOKENS = 12           # linear_attention: the same
 KERNEL_KINDS = ("phase1", "solve", "gather", "dualmm", "dw", "phase2")
 FLAG_PER_STEP_KERNELS = 1
 FLAG_SNAPSHOT_BF16 = 2
@@ -976,9 +976,9 @@ def linear_attention(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     q, k [B, T, Hk, Dk] and v [B, T, H, Dv], float32 or bfloat16, any strides that are multiples of
     16 bytes; H a multiple of Hk (value head h uses key head h // (H // Hk)); Dk (up to 128) and Dv
     (up to 512) multiples of 16. log_decay [H] float32, 0 or below. valid_tokens [B] int32 (None:
-    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step; up to 8 tokens need
-    no workspace. What is allocated here belongs to ``stream`` (None: the current one). A wait that gives up is reported as
-    gated_delta's: in a ``workspace`` of the caller's."""
+    all T). scale: Dk ** -0.5 unless given. One token (T = 1) is the serving step; up to 12
+    tokens need no workspace. What is allocated here belongs to ``stream`` (None: the current one). A
+    wait that gives up is reported as gated_delta's: in a ``workspace`` of the caller's."""
     if stream is not None:
         return _on(stream, linear_attention, state, q, k, v, log_decay, valid_tokens, scale=scale,
                    readings=readings, workspace=workspace)

@@ -10,13 +10,23 @@ namespace {
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 
-// How many segments a sequence is run in (launch_linear_scan): they pay where the heads alone leave SMs idle.
+// How many segments a sequence is run in (launch_linear_carry): they pay where the heads alone leave SMs idle, one block
+// an SM. By the times in microseconds measured: a chunk of the scan and of the carry, a block's start, the join and each
+// of its steps. By shape and type alone: a saving forward's results are the plain one's, and a backward's segments its
+// forward's, whatever the strides. Measured, forward: @@SEGMENTS@@
 void linear_segments(LinearDims &d) {
+    const bool tensor = d.dtype == SDM_BF16;
+    const double scan = tensor ? 2.1 : 4.5, carry = tensor ? 1.0 : 2.0, start = tensor ? 4.0 : 5.0, join = 5.0, step = 0.2;
     const long long blocks = (long long)d.B * d.H * linear_tiles(d.Dv);
+    double best = start + scan * d.Nt;
     d.segs = 1;
-    if (blocks * 2 <= kRefSms && d.Nt >= 8) {
-        const int most = (int)(kRefSms / (blocks ? blocks : 1)), by = d.Nt / 4;
-        d.segs = most < by ? most : by;
+    for (int s = 2; s <= d.Nt && blocks * s <= kRefSms; ++s) {
+        const int chunks = (d.Nt + s - 1) / s;
+        const double time = 2 * start + (scan + carry) * chunks + join + step * s;
+        if (time < best) {
+            best = time;
+            d.segs = s;
+        }
     }
 }
 

@@ -26,7 +26,7 @@ struct LinCarry {
     static constexpr int U = 0, KX = 256;                          // columns: two products of 128, two buffers of 3 x 32
 };
 
-enum { C_FULL = 0, C_BULK = 4, C_EMPTY = 8, C_KX = 12, C_U = 14, C_UF = 16, C_DRAIN = 18, C_COUNT };
+enum { C_FULL = 0, C_EMPTY = 4, C_KX = 8, C_U = 10, C_UF = 12, C_PART = 14, C_DRAIN, C_COUNT };
 
 struct CarryArgs {
     const float *g;
@@ -65,8 +65,7 @@ __global__ void __launch_bounds__(kCarThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(bar + C_FULL + i, 32);
-            mbar_init(bar + C_BULK + i, 1);
+            mbar_init(bar + C_FULL + i, 1);
             mbar_init(bar + C_EMPTY + i, 1);
         }
         for (int i = C_KX; i < C_COUNT; ++i) mbar_init(bar + i, i < C_U || i == C_UF || i == C_UF + 1 ? kCarWarps : 1);
@@ -175,39 +174,19 @@ __global__ void __launch_bounds__(kCarThreads, 1)
         __syncwarp();
     } else {
         // ---- the chunks' inputs
-        for (int it = 0; it < nch; ++it) {
-            const int s = it % ST, t0 = chunk_at(it) * C, nt = ntok - t0 < C ? ntok - t0 : C;
-            unsigned char *st = smem + s * L::STAGE;
-            unsigned long long *full = bar + C_BULK + s;
-            if (it >= ST && !tc_warp_wait(bar + C_EMPTY + s, (it / ST - 1) & 1, dead, d.spin)) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(full, L::STAGE);
+        linear_loads<ST>(smem, L::STAGE, bar + C_FULL, bar + C_EMPTY, bar + C_PART, nch, ntok, chunk_at, [&](unsigned char *st, int t0, unsigned long long *full) {
 #pragma unroll
-                for (int m = 0; m < NP; ++m) {
+            for (int m = 0; m < NP; ++m) {
 #pragma unroll
-                    for (int c = 0; c < KT; ++c)
-                        tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, 64 * c, tc_coord(a.heads[0], h / a.kshare), t0,
-                                       tc_coord(a.seqs[0], b) + m * d.B, full);
+                for (int c = 0; c < KT; ++c)
+                    tc_tensor_load(st + L::K + (m * KT + c) * TILE, &mk, 64 * c, tc_coord(a.heads[0], h / a.kshare), t0,
+                                   tc_coord(a.seqs[0], b) + m * d.B, full);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[1], h / a.vshare), t0,
-                                       tc_coord(a.seqs[1], b) + m * d.B, full);
-                }
+                for (int c = 0; c < 2; ++c)
+                    tc_tensor_load(st + L::V + (m * 2 + c) * TILE, &mv, v0 + 64 * c, tc_coord(a.heads[1], h / a.vshare), t0,
+                                   tc_coord(a.seqs[1], b) + m * d.B, full);
             }
-            __syncwarp();
-            if (!tc_warp_wait(full, it / ST & 1, dead, d.spin)) {
-                mbar_wait_bounded(full, it / ST & 1);              // nothing in flight behind a give-up
-                break;
-            }
-            if (nt < C) {                                          // what lies past the valid tokens is not used
-                for (int i = lane; i < (C - nt) * 8; i += 32) {
-                    const int off = tc_at(nt + (i >> 3), i & 7);
-                    for (int c = 0; c < L::STAGE / TILE; ++c) *reinterpret_cast<uint4 *>(st + c * TILE + off) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-            }
-            mbar_arrive(bar + C_FULL + s);
-        }
+        }, dead, d.spin);
     }
     __syncthreads();
     if (*dead) {
@@ -239,13 +218,21 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
     };
     float4 s = first ? make_float4(first[i], first[i + 1], first[i + 2], first[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<float4 *>(starts + i) = s;
-    for (int m = 1; m < d.segs; ++m) {
-        const int place = reverse ? d.segs - m : m - 1;            // of the segment before
-        const float w = linear_power(g[h], bound(place + 1) - bound(place));
-        float4 *at = reinterpret_cast<float4 *>(starts + m * states + i);
-        const float4 e = *at;
-        s = make_float4(fmaf(w, s.x, e.x), fmaf(w, s.y, e.y), fmaf(w, s.z, e.z), fmaf(w, s.w, e.w));
-        *at = s;
+    // what the segments add is fetched eight at a time: one by one each waits for memory (16 segments 10 us)
+    for (int m0 = 1; m0 < d.segs; m0 += 8) {
+        float4 e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (m0 + j < d.segs) e[j] = *reinterpret_cast<const float4 *>(starts + (m0 + j) * states + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int m = m0 + j;
+            if (m >= d.segs) break;
+            const int place = reverse ? d.segs - m : m - 1;        // of the segment before
+            const float w = linear_power(g[h], bound(place + 1) - bound(place));
+            s = make_float4(fmaf(w, s.x, e[j].x), fmaf(w, s.y, e[j].y), fmaf(w, s.z, e[j].z), fmaf(w, s.w, e[j].w));
+            *reinterpret_cast<float4 *>(starts + m * states + i) = s;
+        }
     }
 }
 

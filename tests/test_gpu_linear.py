@@ -69,7 +69,7 @@ def check(x, dtype, valid=None, scale=None):
 
 SHAPES = [  # B, T, Hk, H, Dk, Dv
     (2, 1, 2, 4, 128, 128), (1, 1, 1, 1, 16, 16), (3, 2, 1, 3, 48, 80), (40, 1, 2, 16, 128, 128), (5, 1, 4, 8, 96, 192),
-    (1, 5, 2, 2, 64, 512), (2, 8, 1, 2, 32, 64), (2, 9, 1, 2, 128, 64), (2, 17, 1, 2, 128, 64), (1, 31, 2, 2, 64, 64),
+    (1, 5, 2, 2, 64, 512), (2, 12, 1, 2, 32, 64), (2, 13, 1, 2, 128, 64), (2, 17, 1, 2, 128, 64), (1, 31, 2, 2, 64, 64),
     (1, 33, 1, 2, 112, 16), (2, 63, 1, 1, 128, 128), (2, 64, 1, 1, 128, 128), (1, 65, 2, 4, 128, 128),
     (1, 128, 1, 1, 80, 96), (2, 200, 1, 3, 64, 144), (1, 333, 2, 2, 128, 256), (3, 129, 2, 2, 16, 32), (1, 70, 20, 20, 64, 64),
     (1, 70, 1, 160, 64, 32), (1, 1500, 1, 2, 64, 64), (1, 900, 2, 2, 48, 272),

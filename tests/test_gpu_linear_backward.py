@@ -49,7 +49,7 @@ def check(x, dtype, seed=0, valid=None, scale=None, with_state=True):
     kept = None if dS is None else dS.clone()
     o, state, got = train(x, do, dS, valid, scale)
     plain = call(x, valid, **({} if scale is None else {"scale": scale}))
-    if x["v"].shape[1] > 8:
+    if x["v"].shape[1] > sdm.LINEAR_STEP_TOKENS:
         assert torch.equal(o, plain[0]) and torch.equal(state, plain[1])
     assert dS is None or torch.equal(dS, kept)
     scale = x["q"].shape[-1] ** -0.5 if scale is None else scale

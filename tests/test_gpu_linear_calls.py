@@ -40,7 +40,7 @@ def both(monkeypatch, call):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("T", [1, 8, 9, 90])
+@pytest.mark.parametrize("T", [1, 12, 13, 90])
 @pytest.mark.parametrize("options", [{}, dict(scale=0.3)], ids=str)
 def test_linear_attention(monkeypatch, dtype, T, options):
     x = draw(3, T, 2, 4, 64, 96, dtype, seed=T)
