@@ -13,7 +13,9 @@ bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 // How many segments a sequence is run in (launch_linear_carry): they pay where the heads alone leave SMs idle, one block
 // an SM. By the times in microseconds measured: a chunk of the scan and of the carry, a block's start, the join and each
 // of its steps. By shape and type alone: a saving forward's results are the plain one's, and a backward's segments its
-// forward's, whatever the strides. Measured, forward: @@SEGMENTS@@
+// forward's, whatever the strides. Measured, forward,
+// in segments and not: 16 heads of 128 x 128 x 128 chunks 70 and 259 us, x 16 29 and 42; 32 x 64 72 and 136; 64 x 64 117
+// and 136; float32, 8 heads of 64 x 64 x 16 30 and 72, x 128 74 and 525.
 void linear_segments(LinearDims &d) {
     const bool tensor = d.dtype == SDM_BF16;
     const double scan = tensor ? 2.1 : 4.5, carry = tensor ? 1.0 : 2.0, start = tensor ? 4.0 : 5.0, join = 5.0, step = 0.2;
@@ -49,7 +51,8 @@ int linear_check(const sdm_linear_shape *s, LinearDims &d, bool back) {
     d.dtype = s->dtype;
     d.scale = s->scale;
     d.C = 64;
-    d.Nt = (int)(((long long)s->T + d.C - 1) / d.C);
+    if (s->T > INT32_MAX - d.C) return set_error(SDM_ERR_UNSUPPORTED, "linear attention: T must be at most 2^31 - 65, got %d", s->T);
+    d.Nt = (s->T + d.C - 1) / d.C;
     d.spin = wait_limit();
     // blocks of a launch: one per head and 16 columns of the state
     if ((long long)s->B * s->H * (s->Dv / 16) >= (1LL << 31))

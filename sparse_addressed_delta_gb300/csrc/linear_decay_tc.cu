@@ -13,7 +13,8 @@
 // A and A' come from one product, W and W' from the next. All is bilinear in (Dk, Dv), so a block takes 64 columns of Dk
 // and 128 of Dv for itself, the pairs' sums too: it has room for a buffer of queries and one of keys, so that the threads
 // fill one (what they and the products take is shared memory's rate) while the other is multiplied. 64 heads of 128 x 128
-// x 64 chunks: @@ us; 128 columns of Dk a block, with one buffer, 157; four products instead of two 188.
+// x 64 chunks: 139 us; 128 columns of Dk a block, with one buffer, 157; four products instead of two 188. A chunk takes
+// 3450 cycles, of which shared memory is busy 3390 (operands of the products 2110, their buffers 900, copies 380).
 // Warps as in linear_scan_tc.cu.
 #include <type_traits>
 

@@ -10,12 +10,20 @@
 // tensor core only ever sums one chunk, from the smallest terms up (it cuts an accumulator's low bits at every
 // step).
 //
-// S^T's planes are an A operand in tensor memory, V one in shared memory; Q, Z and the decayed keys are B operands
-// there. Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the tokens and of K), warp 16 issues the
-// products, warp 17 loads and warp 18 stores bfloat16 results, both by tensor copies. While the threads make Z and the decayed keys of the next chunk the
-// tensor core reads the state; while they store the results and split the new state it makes the next chunk's U,
-// OB and P. Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block, and the block
-// leaves after its copies and products in flight.
+// S^T's planes are an A operand in tensor memory, V^T one in shared memory; Q, Z^T and the decayed keys are B operands
+// there, the last two side by side: one product makes U and OB, and reads V^T once for both. Warps 0..15 compute (lanes
+// 32 (warp % 4).., quarter warp / 4 of the tokens and of K), warp 16 issues the products, warp 17 loads and warp 18
+// stores bfloat16 results, both by tensor copies. While the threads make the next chunk's decayed keys and Z the tensor
+// core reads the state (OA) and makes P; while they store the results and split the new state it makes U and OB.
+//
+// What bounds it: shared memory. A 128 x 128 chunk moves 390 KB through it (copies in and out 80, the decayed keys 64,
+// Z 24, operands of P 48, of U and OB 120, of OA 48), 3070 cycles of the 4000 that a chunk takes (2.0 us); the rest is
+// the hand-over of U, keys and readings from one to the next. Measured: 128 blocks of 64 chunks 134 us, of 32 saving
+// nothing 71, mirrored 72; float32 parts for shared heads 84 and 80 (64 bytes a lane's store). U before OB, in products of
+// their own, so that the keys could start earlier: 135, the operands read twice eat what it gains.
+//
+// Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block, and the block leaves after its
+// copies and products in flight.
 #include <type_traits>
 
 #include "linear_tc.cuh"
@@ -180,8 +188,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         };
         // The decayed keys, in units of 8 columns of 32 tokens, and Z^T (by lanes 0..63 of tensor memory, a key's row each)
         // of chunk `it`. A scheduler has every fourth warp, so those of the other lanes, and those whose block of Z^T holds
-        // no pairs, take more of the units: 3, 3, 3 and, with a block off the diagonal, 1 of each 4 x 4 (a narrow state: half
-        // of them each). Measured, 32 heads x 256 chunks: all units by the other lanes' warps 145 us, so @@.
+        // no pairs, take three of the units each, and those with a block off the diagonal one (a narrow state: half of that).
+        // 32 heads x 256 chunks in four segments: all units by the other lanes' warps 145 us, so 137, three at once 134.
         const int ahead = REV ? lane0 - 16 * part - 15 : 16 * part - lane0 - 31;   // least tokens apart
         int unit0, unit1;
         {

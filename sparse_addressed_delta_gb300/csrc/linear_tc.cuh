@@ -55,7 +55,7 @@ __device__ __forceinline__ void linear_loads(unsigned char *smem, int bytes, uns
         __syncwarp();
         if (lane == 0) mbar_arrive(full + s);
     }
-    if (!*dead) return;
+    // nothing is in flight when the block ends, also where its other warps gave up
     for (int i = it > ST ? it - ST : 0; i < it; ++i) {
         const int t0 = chunk_at(i) * C;
         if (ntok - t0 >= C) mbar_wait_bounded(full + i % ST, i / ST & 1);
