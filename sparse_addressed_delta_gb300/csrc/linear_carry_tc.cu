@@ -20,7 +20,7 @@ template <int KP, int NP>
 struct LinCarry {
     static constexpr int TILE = kCarC * 128, KT = KP / 64;
     static constexpr int K = 0, V = K + NP * KT * TILE, STAGE = V + NP * 2 * TILE, STAGES = NP == 1 ? 4 : 2;
-    static constexpr int POW = STAGES * STAGE, BARS = POW + 4 * 80, BYTES = BARS + 256 + 1024;
+    static constexpr int POW = STAGES * STAGE, WEIGHT = POW + 4 * 80, BARS = WEIGHT + 4 * 64, BYTES = BARS + 256 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory");
     static constexpr int U = 0, KX = 256;                          // columns: two products of 128, two buffers of 3 x 32
 };
@@ -75,7 +75,12 @@ __global__ void __launch_bounds__(kCarThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (tid <= C) pw[tid] = linear_power(a.g[h], tid);
+    float *weight = reinterpret_cast<float *>(smem + L::WEIGHT);   // of a whole chunk's tokens
+    if (tid <= C) {
+        const float x = linear_power(a.g[h], tid);
+        pw[tid] = x;
+        if (REV ? tid > 0 : tid < C) weight[REV ? tid - 1 : C - 1 - tid] = a.to * x;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -99,7 +104,7 @@ __global__ void __launch_bounds__(kCarThreads, 1)
             if (!tc_warp_wait(bar + C_FULL + it % ST, it / ST & 1, dead, d.spin)) return false;
             if (lane0 < KP) {
                 // column `row` of the tile: 2 bytes of each token's 128, pieces of 8 exchanged by token (tc_at)
-                const unsigned char *src = smem + it % ST * L::STAGE + L::K + (row >> 6) * TILE + 2 * (row & 7);
+                const unsigned char *src = smem + it % ST * L::STAGE + L::K + (row >> 6) * TILE + 2 * (row & 7) + 16 * part * 128;
                 const int piece = (row & 63) >> 3;
                 float2 x[8];
 #pragma unroll
@@ -107,14 +112,27 @@ __global__ void __launch_bounds__(kCarThreads, 1)
                     float y[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int t = 16 * part + 2 * i + e;
                         y[e] = 0.f;
 #pragma unroll
-                        for (int m = NP - 1; m >= 0; --m)
-                            y[e] += __uint_as_float((unsigned)*reinterpret_cast<const unsigned short *>(src + m * KT * TILE + tc_at(t, piece)) << 16);
-                        y[e] *= t < nt ? a.to * pw[REV ? t + 1 : nt - 1 - t] : 0.f;
+                        for (int m = NP - 1; m >= 0; --m) {
+                            const float k = __uint_as_float((unsigned)*reinterpret_cast<const unsigned short *>(
+                                                                src + m * KT * TILE + (2 * i + e) * 128 + ((piece ^ ((2 * i + e) & 7)) << 4)) << 16);
+                            y[e] = m == NP - 1 ? k : y[e] + k;
+                        }
                     }
                     x[i] = make_float2(y[0], y[1]);
+                }
+                if (nt == C) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 w = *reinterpret_cast<const float4 *>(weight + 16 * part + 4 * i);
+                        x[2 * i] = mul2(x[2 * i], make_float2(w.x, w.y));
+                        x[2 * i + 1] = mul2(x[2 * i + 1], make_float2(w.z, w.w));
+                    }
+                } else {
+                    auto of = [&](int t) { return t < nt ? a.to * pw[REV ? t + 1 : nt - 1 - t] : 0.f; };
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], make_float2(of(16 * part + 2 * i), of(16 * part + 2 * i + 1)));
                 }
                 const uint32_t dst = at + L::KX + 96 * (it & 1) + 8 * part;
                 store_planes3(dst, dst + 32, dst + 64, x);
