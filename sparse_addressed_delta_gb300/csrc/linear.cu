@@ -18,7 +18,7 @@ bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 // and 136; float32, 8 heads of 64 x 64 x 16 30 and 72, x 128 74 and 525.
 void linear_segments(LinearDims &d) {
     const bool tensor = d.dtype == SDM_BF16;
-    const double scan = tensor ? 2.1 : 4.5, carry = tensor ? 1.0 : 2.0, start = tensor ? 4.0 : 5.0, join = 5.0, step = 0.2;
+    const double scan = tensor ? 2.0 : 4.5, carry = tensor ? 0.86 : 2.0, start = tensor ? 4.0 : 5.0, join = 5.0, step = 0.2;
     const long long blocks = (long long)d.B * d.H * linear_tiles(d.Dv);
     double best = start + scan * d.Nt;
     d.segs = 1;
