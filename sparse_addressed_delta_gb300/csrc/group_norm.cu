@@ -17,8 +17,9 @@
 namespace sdm {
 namespace {
 
-constexpr int kGroupThreads = 256, kGroupBatch = 8, kGroupMaxCols = 16384, kGroupRowCols = 8192;
-constexpr int kGroupRowThreads = 512;                   // an SM, of the forward over rows (128 registers each)
+constexpr int kGroupThreads = 256, kGroupSm = 3, kGroupBatch = 8, kGroupMaxCols = 16384, kGroupRowCols = 8192;
+// an SM's threads of the forward over rows, 128 registers each (1024 of 64: 145 us for 32768 x 4096 bfloat16 where this took 123)
+constexpr int kGroupRowThreads = 512;
 
 // The sigmoid. bfloat16: by the approximate exponential and reciprocal instructions, within 2^-20 of it where it is not
 // negligible, far inside the results' rounding of 2^-9; the exact ones would bound the kernel (25 instructions an
@@ -91,10 +92,18 @@ __device__ __forceinline__ float2 join_parts(int many, float all, F entry) {
 
 struct GroupShape {
     long long N, L, xs, gs;              // samples, positions, elements between positions of x and of the gradient
-    int C, G, splits;
+    int C, G;
     bool wf32;
     float eps;
     const void *w, *b;
+    int splits, more;                    // blocks of a sample: `per` positions each, the first `more` of them one more
+    long long per;
+    // into how many, and how
+    void split(int n) {
+        splits = n;
+        per = L / n;
+        more = (int)(L % n);
+    }
 };
 
 // ---- one position a sample ----------------------------------------------------------------------
@@ -385,49 +394,54 @@ struct Piece {
     __device__ explicit Piece(const GroupShape &s) {
         split = (int)(blockIdx.x % s.splits);
         n = blockIdx.x / s.splits;
-        from = s.L * split / s.splits;
-        to = s.L * (split + 1) / s.splits;
+        from = split * s.per + (split < s.more ? split : s.more);
+        to = from + s.per + (split < s.more);
     }
 };
 
 // part [N][splits][G]: mean and sum of squares around it
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kGroupThreads) k_group_stats(const __grid_constant__ GroupShape s, const T *x, float2 *part) {
+__global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const __grid_constant__ GroupShape s, const T *x, float2 *part) {
     extern __shared__ float2 acc[];                      // [slots][cv]
     const Piece p(s);
     const Spread sp(s.C, VEC);
-    const int slot = threadIdx.x / sp.cv < sp.slots ? threadIdx.x / sp.cv : -1;
+    const int at_slot = (int)threadIdx.x / sp.cv, slot = at_slot < sp.slots ? at_slot : -1;
     const T *base = x + p.n * s.L * s.xs;
     for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += kGroupThreads) {
         Moments m{0.f, 0.f, 0.f};
         if (slot >= 0 || sp.slots == 1) {
             const T *col = base + cv * VEC;
             for (long long r = p.from + (sp.slots > 1 ? slot : 0); r < p.to; r += (long long)sp.slots * kGroupBatch) {
-                float v[kGroupBatch][VEC], sum = 0.f, q = 0.f, count = 0.f;
+                // (kept as they came: widened they would take the registers of another block)
+                Vec<T, VEC> raw[kGroupBatch];
+                float2 sum = both(0.f), q = both(0.f);
+                float count = 0.f;
 #pragma unroll
                 for (int i = 0; i < kGroupBatch; ++i) {
                     const long long at = r + (long long)i * sp.slots;
-                    Vec<T, VEC> raw{};
+                    raw[i] = Vec<T, VEC>{};
                     if (at < p.to) {
-                        raw = __ldg(reinterpret_cast<const Vec<T, VEC> *>(col + at * s.xs));
+                        raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(col + at * s.xs));
                         count += VEC;
                     }
-                    unpack<T, VEC>(raw, v[i]);
                 }
+                auto each_pair = [&](auto f) {
 #pragma unroll
-                for (int i = 0; i < kGroupBatch; ++i)
+                    for (int i = 0; i < kGroupBatch; ++i) {
+                        float v[VEC];
+                        unpack<T, VEC>(raw[i], v);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) sum += v[i][j];
-                const float mean = sum / count;
-#pragma unroll
-                for (int i = 0; i < kGroupBatch; ++i)
-                    if (r + (long long)i * sp.slots < p.to)
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) {
-                            const float d = v[i][j] - mean;
-                            q = fmaf(d, d, q);
-                        }
-                m.join(count, mean, q);
+                        for (int j = 0; j < VEC; j += 2) f(r + (long long)i * sp.slots < p.to, make_float2(v[j], VEC > 1 ? v[VEC > 1 ? j + 1 : 0] : 0.f));
+                    }
+                };
+                each_pair([&](bool, float2 v) { sum = add2(sum, v); });
+                const float mean = (sum.x + sum.y) / count;
+                each_pair([&](bool live, float2 v) {
+                    const float2 d = add2(v, both(-mean));
+                    if (live) q = fma2(d, d, q);
+                });
+                if (VEC == 1) q.y = 0.f;                           // (no second one of the pair)
+                m.join(count, mean, q.x + q.y);
             }
         }
         if (slot >= 0 || sp.slots == 1) acc[(sp.slots > 1 ? slot : 0) * sp.cv + cv] = make_float2(m.mean, m.m2);
@@ -456,7 +470,7 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_join(const __grid_const
     const float2 *at = part + i / s.G * s.splits * s.G + i % s.G;
     const float2 a = join_parts<32>(s.splits, all, [&](int k) {
         const float2 e = __ldg(at + (size_t)k * s.G);
-        return Moments{(float)(s.L * (k + 1) / s.splits - s.L * k / s.splits) * c, e.x, e.y};
+        return Moments{(float)(s.per + (k < s.more)) * c, e.x, e.y};
     });
     if ((threadIdx.x & 31) == 0) joined[i] = make_float2(a.x, 1.f / sqrtf(a.y / all + s.eps));
 }
@@ -469,7 +483,7 @@ __device__ __forceinline__ void load_params(const void *p, bool f32, float fill,
 }
 
 template <typename T, int VEC, bool ACT>
-__global__ void __launch_bounds__(kGroupThreads) k_group_apply(const __grid_constant__ GroupShape s, const T *x, const float2 *stats, T *y) {
+__global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_apply(const __grid_constant__ GroupShape s, const T *x, const float2 *stats, T *y) {
     const Piece p(s);
     const Spread sp(s.C, VEC);
     const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
@@ -515,16 +529,18 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_apply(const __grid_cons
     }
 }
 
-// part [N][splits][2][C]: column sums of dz xhat and of dz
+// part [N][splits][2][C], where it is wanted: column sums of dz xhat and of dz; terms [N][splits][G]: sums over a group of
+// w dz and of w dz xhat
 template <typename T, int VEC, bool ACT>
-__global__ void __launch_bounds__(kGroupThreads)
-    k_group_sums(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, float *part) {
-    extern __shared__ float sums[];                      // [slots][2][C] where there are several
+__global__ void __launch_bounds__(kGroupThreads, kGroupSm)
+    k_group_sums(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, float *part, float2 *terms) {
+    extern __shared__ __align__(16) float sums[];        // [slots][2][C] where there are several slots; then [slots][cv] a thread's terms
     const Piece p(s);
     const Spread sp(s.C, VEC);
     const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
     const T *base = x + p.n * s.L * s.xs, *gbase = dy + p.n * s.L * s.gs;
-    float *out = part + ((size_t)p.n * s.splits + p.split) * 2 * s.C;
+    float2 *pairs = reinterpret_cast<float2 *>(sums + (sp.slots > 1 ? sp.slots * 2 * s.C : 0));
+    float *out = part ? part + ((size_t)p.n * s.splits + p.split) * 2 * s.C : nullptr;
     if (slot < sp.slots)
         for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += sp.slots > 1 ? sp.cv : kGroupThreads) {
             const int c0 = cv * VEC;
@@ -534,7 +550,7 @@ __global__ void __launch_bounds__(kGroupThreads)
             load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) sw[j] = sb[j] = 0.f;
-            constexpr int BATCH = kGroupBatch / 2;
+            constexpr int BATCH = VEC == 8 && ACT ? 2 : 4;   // (8 x 4096 x 512 bfloat16: 25 us, with 4, which spill, 33; without silu 23, 20)
             for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * BATCH) {
                 Vec<T, VEC> rx[BATCH], rg[BATCH];
 #pragma unroll
@@ -566,15 +582,28 @@ __global__ void __launch_bounds__(kGroupThreads)
                     }
                 }
             }
-            float *to = sp.slots > 1 ? sums + (size_t)slot * 2 * s.C : out;
+            float2 mine = both(0.f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                to[c0 + j] = sw[j];
-                to[s.C + c0 + j] = sb[j];
+            for (int j = 0; j < VEC; ++j) mine = fma2(make_float2(sb[j], sw[j]), both(w[j]), mine);
+            if (out) {
+                float *to = (sp.slots > 1 ? sums + (size_t)slot * 2 * s.C : out) + c0;
+                store_vec<float, VEC>(to, sw);
+                store_vec<float, VEC>(to + s.C, sb);
             }
+            pairs[slot * sp.cv + cv] = mine;
         }
-    if (sp.slots == 1) return;
     __syncthreads();
+    const int wide = sp.cv / s.G;
+    for (int g0 = 0; g0 < s.G; g0 += kGroupThreads / 8) {
+        const int g = g0 + (threadIdx.x >> 3);
+        float2 a = both(0.f);
+        if (g < s.G)
+            for (int i = threadIdx.x & 7; i < wide * sp.slots; i += 8) a = add2(a, pairs[i / wide * sp.cv + g * wide + i % wide]);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) a = add2(a, make_float2(__shfl_xor_sync(~0u, a.x, o), __shfl_xor_sync(~0u, a.y, o)));
+        if (g < s.G && (threadIdx.x & 7) == 0) terms[((size_t)p.n * s.splits + p.split) * s.G + g] = a;
+    }
+    if (sp.slots == 1 || !out) return;
     for (int c = threadIdx.x; c < 2 * s.C; c += kGroupThreads) {
         float t = 0.f;
         for (int i = 0; i < sp.slots; ++i) t += sums[(size_t)i * 2 * s.C + c];
@@ -582,44 +611,22 @@ __global__ void __launch_bounds__(kGroupThreads)
     }
 }
 
-// terms [N][G]: means over the group of w dz and of w dz xhat, from the partials' columns; by `lanes` (32 or all of the
-// block's) threads a group
-template <typename T>
-__global__ void __launch_bounds__(kGroupThreads) k_group_terms(const __grid_constant__ GroupShape s, const float *part, int lanes, float2 *terms) {
-    __shared__ float2 sums[kGroupThreads / 32];
-    const long long i = (long long)blockIdx.x * (kGroupThreads / lanes) + threadIdx.x / lanes;
-    const int g = (int)(i % s.G), each = s.C / s.G, many = i < s.N * s.G ? s.splits * each : 0;
-    const float *at = part + (size_t)(i / s.G) * s.splits * 2 * s.C + g * each;
-    float a = 0.f, b = 0.f;
+// terms [N][G]: means over the group from the splits' sums, a warp a group
+__global__ void __launch_bounds__(kGroupThreads) k_group_terms(const __grid_constant__ GroupShape s, const float2 *part, float2 *terms) {
+    const long long i = (long long)blockIdx.x * (kGroupThreads / 32) + (threadIdx.x >> 5);
+    if (i >= s.N * s.G) return;
+    const float2 *at = part + i / s.G * s.splits * s.G + i % s.G;
+    float2 a = both(0.f);
 #pragma unroll 4
-    for (int e = threadIdx.x % lanes; e < many; e += lanes) {
-        const int c = e % each;
-        const float *p = at + (size_t)(e / each) * 2 * s.C + c;
-        float w[1];
-        load_params<T, 1>(s.w, s.wf32, 1.f, g * each + c, w);
-        a = fmaf(p[s.C], w[0], a);
-        b = fmaf(p[0], w[0], b);
-    }
+    for (int k = threadIdx.x & 31; k < s.splits; k += 32) a = add2(a, __ldg(at + (size_t)k * s.G));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(~0u, a, o);
-        b += __shfl_xor_sync(~0u, b, o);
-    }
-    if (lanes > 32) {
-        if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        a = b = 0.f;
-        for (int w = 0; w < kGroupThreads / 32; ++w) {
-            a += sums[w].x;
-            b += sums[w].y;
-        }
-    }
-    const float count = (float)s.L * (float)each;
-    if (threadIdx.x % lanes == 0 && i < s.N * s.G) terms[i] = make_float2(a / count, b / count);
+    for (int o = 16; o > 0; o >>= 1) a = add2(a, make_float2(__shfl_xor_sync(~0u, a.x, o), __shfl_xor_sync(~0u, a.y, o)));
+    const float count = (float)s.L * (float)(s.C / s.G);
+    if ((threadIdx.x & 31) == 0) terms[i] = make_float2(a.x / count, a.y / count);
 }
 
 template <typename T, int VEC, bool ACT>
-__global__ void __launch_bounds__(kGroupThreads)
+__global__ void __launch_bounds__(kGroupThreads, kGroupSm)
     k_group_apply_bwd(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, const float2 *terms, T *dx) {
     const Piece p(s);
     const Spread sp(s.C, VEC);
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(kGroupThreads)
         float w[VEC], b[VEC];
         load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
         load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
-        constexpr int BATCH = kGroupBatch / 2;
+        constexpr int BATCH = 4;
         for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * BATCH) {
             Vec<T, VEC> rx[BATCH], rg[BATCH];
 #pragma unroll
@@ -669,11 +676,13 @@ __global__ void __launch_bounds__(kGroupThreads)
 
 // ---- which form, and its launches ---------------------------------------------------------------
 
-// blocks of a sample: enough of them for the card, 16 positions at least each
+// Blocks of a sample: kGroupSm an SM in all, 8 positions at least each. kGroupSm 3, of 80 registers: 8 x 4096 x 512 bfloat16
+// with silu 26 us and backward 51; 4, with spills, 29; 2, of 128 registers, 28 and 72. At least 8 / 16 / 32 positions, forward
+// and backward: 2 x 64 x 1280 10.2, 15.5 / 12.8, 21.0 / 18.0, 31.8 us; 8 x 256 x 512 11.1, 14.2 / 10.3, 13.6 / 11.0, 16.1.
 int group_splits(long long N, long long L) {
-    const long long want = 4LL * kRefSms / (N ? N : 1), most = L / 16;
+    const long long want = (long long)kGroupSm * kRefSms / (N ? N : 1), most = L / 8;
     const long long s = want < most ? want : most;
-    return s < 1 ? 1 : s > 256 ? 256 : (int)s;
+    return s < 1 ? 1 : (int)s;
 }
 
 // The rows' blocks: a multiple of as many as make their rows at once a multiple of G, at most `most` where that allows it
@@ -688,9 +697,14 @@ long long group_grid(long long rows, int rpb, int G, long long most) {
     return unit * (need < fit ? need : fit > 1 ? fit : 1);
 }
 
+// Rows in registers wherever they fit: 32768 x 4096 bfloat16 of 32 groups with silu 89 us forward and 75 backward (the split
+// form, one position a block: 1056 and 1130), 1024 x 8192 of 8 10 and 33 (64 and 82). The registers end at 8192 columns
+// (512 threads of 16 elements).
 bool group_rows(long long L, int each) { return L == 1 && each <= kGroupRowCols; }
 
-// the backward's blocks over rows, and how many partials of the column sums they leave
+// The backward's blocks over rows, and how many partials of the column sums they leave. `same`: all rows of a block are
+// of one group and joined before they leave, as soon as there are samples enough for a block (32768 x 256 of 16 groups 29 us,
+// by rows side by side, each with its own partial, 37; 200000 x 64 of one group 23 and 57; 1024 x 4096 of 32 13.6 and 19.7).
 struct GroupBack {
     bool same;
     long long blocks, parts;
@@ -772,12 +786,12 @@ long long group_backward(const GroupShape &s, const T *dy, const T *x, const flo
         }
         const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
         const unsigned grid = (unsigned)(s.N * s.splits);
-        const size_t smem = slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0;
+        const size_t smem = (size_t)slots * cv * 8 + (slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0);
         set_kernel_smem(k_group_sums<T, VEC, ACT>, smem);
-        k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, part);
-        const int lanes = (long long)s.splits * each > 8 * 32 ? kGroupThreads : 32;
-        const long long groups = s.N * s.G, per = kGroupThreads / lanes;
-        k_group_terms<T><<<(unsigned)((groups + per - 1) / per), kGroupThreads, 0, st>>>(s, part, lanes, terms);
+        float2 *split_terms = terms + s.N * s.G;
+        k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
+        const long long groups = s.N * s.G, per = kGroupThreads / 32;
+        k_group_terms<<<(unsigned)((groups + per - 1) / per), kGroupThreads, 0, st>>>(s, split_terms, terms);
         k_group_apply_bwd<T, VEC, ACT><<<grid, kGroupThreads, 0, st>>>(s, dy, x, stats, terms, dx);
         parts = s.N * s.splits;
     });
@@ -798,7 +812,7 @@ int group_check(const char *what, long long N, long long L, int C, int G, long l
     return SDM_OK;
 }
 
-// the parts of a workspace: partials, then (a backward of split positions) the groups' terms
+// the parts of a workspace: partials, then (a backward of split positions) the groups' terms and those of the splits
 size_t group_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 size_t group_part_bytes(long long N, long long L, int C, int G, bool back) {
     if (group_rows(L, C / G)) {
@@ -812,7 +826,8 @@ size_t group_part_bytes(long long N, long long L, int C, int G, bool back) {
     return group_up(pieces * (back ? (size_t)2 * C * 4 : (size_t)G * 8) + (back ? 0 : (size_t)N * G * 8));
 }
 size_t group_bytes(long long N, long long L, int C, int G, bool back) {
-    return group_part_bytes(N, L, C, G, back) + (back && !group_rows(L, C / G) ? group_up((size_t)N * G * 8) : 0) + kAlign;
+    const bool terms = back && !group_rows(L, C / G);
+    return group_part_bytes(N, L, C, G, back) + (terms ? group_up((size_t)N * (1 + group_splits(N, L)) * G * 8) : 0) + kAlign;
 }
 
 int group_check_ws(const char *what, const void *ws, size_t have, size_t need) {
@@ -851,7 +866,8 @@ int sdm_group_norm(const void *x, long long x_stride, long long N, long long L, 
         rc = group_check_ws(what, workspace, workspace_bytes, group_bytes(N, L, C, G, false) - kAlign);
         if (rc != SDM_OK) return rc;
     }
-    const GroupShape s{N, L, x_stride, 0, C, G, group_splits(N, L), weight_dtype == SDM_F32, eps, weight, bias};
+    GroupShape s{N, L, x_stride, 0, C, G, weight_dtype == SDM_F32, eps, weight, bias};
+    s.split(group_splits(N, L));
     const int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, C, x, y, y);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto type, auto act) {
@@ -891,7 +907,8 @@ int sdm_group_norm_backward(const void *grad, long long grad_stride, const void 
         rc = group_check_ws(what, workspace, workspace_bytes, group_bytes(N, L, C, G, true) - kAlign);
         if (rc != SDM_OK) return rc;
     }
-    const GroupShape s{N, L, x_stride, grad_stride, C, G, group_splits(N, L), weight_dtype == SDM_F32, 0.f, weight, bias};
+    GroupShape s{N, L, x_stride, grad_stride, C, G, weight_dtype == SDM_F32, 0.f, weight, bias};
+    s.split(group_splits(N, L));
     int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, grad_stride, x, grad, grad_x);
     auto part = static_cast<float *>(workspace);
     auto terms = rows ? nullptr : reinterpret_cast<float2 *>(static_cast<unsigned char *>(workspace) + group_part_bytes(N, L, C, G, true));

@@ -3,10 +3,14 @@
 //   S = e^{L n} S + (e^{L (n - 1 - j)} K)^T V         (mirrored, for the gradient of the state: e^{L (j + 1)})
 // on the 5th-generation tensor cores. The rows of the state are the lanes of tensor memory: the decayed keys, three
 // bfloat16 planes, are an A operand there, which the threads of their lanes store; V is the B operand in shared memory.
-// S stays in registers in float32. Two buffers of decayed keys and of products, four stages of inputs. Bound by the
-// inputs: 16384 tokens, 32 heads of 128 x 128, three of four segments take 63 us on 96 SMs, where the copies alone, as
-// deep, take 42 (4.7 TB/s). float32 inputs come as three planes with six of their products (NP = 3). Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the tokens and of
-// the columns), warp 16 issues the products, warp 17 loads.
+// S stays in registers in float32. Two buffers of decayed keys and of products, four stages of inputs, float32 inputs as
+// three planes with six of their products (NP = 3). Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the
+// tokens and of the columns), warp 16 issues the products, warp 17 loads.
+//
+// Bound by the issue of instructions (72 % of its cycles): splitting the decayed keys in three planes and adding a product to
+// the state, 0.86 us a chunk, near the copies' own time. 16384 tokens, 32 heads of 128 x 128, three of four segments:
+// 55 us on 96 SMs, where the copies alone, as deep, take 42 (4.7 TB/s). Warps that take even and odd chunks instead of
+// quarters of each 65.6 (63 then), the copies awaited one after the other 80.
 #include <type_traits>
 
 #include "linear_tc.cuh"

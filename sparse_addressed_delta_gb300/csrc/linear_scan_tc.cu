@@ -19,8 +19,9 @@
 // What bounds it: shared memory. A 128 x 128 chunk moves 390 KB through it (copies in and out 80, the decayed keys 64,
 // Z 24, operands of P 48, of U and OB 120, of OA 48), 3070 cycles of the 4000 that a chunk takes (2.0 us); the rest is
 // the hand-over of U, keys and readings from one to the next. Measured: 128 blocks of 64 chunks 134 us, of 32 saving
-// nothing 71, mirrored 72; float32 parts for shared heads 84 and 80 (64 bytes a lane's store). U before OB, in products of
-// their own, so that the keys could start earlier: 135, the operands read twice eat what it gains.
+// nothing 71, mirrored 72; float32 parts for shared heads 84 and 80 (64 bytes a lane's store; through shared memory 88 and
+// 85). bfloat16 results stored by the threads themselves 151. U before OB, in products of their own, so that the keys could
+// start earlier: 135, the operands read twice eat what it gains.
 //
 // Every wait is bounded: one that gives up sets SDM_ERR_TIMEOUT in the status block, and the block leaves after its
 // copies and products in flight.
