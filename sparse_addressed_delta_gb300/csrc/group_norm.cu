@@ -22,7 +22,7 @@ constexpr int kGroupThreads = 256, kGroupSm = 3, kGroupBatch = 8, kGroupMaxCols 
 constexpr int kGroupRowThreads = 512;
 
 // The sigmoid. bfloat16: by the approximate exponential and reciprocal instructions, within 2^-20 of it where it is not
-// negligible, far inside the results' rounding of 2^-9; the exact ones would bound the kernel (25 instructions an
+// negligible, far inside the results' rounding of 2^-8; the exact ones would bound the kernel (25 instructions an
 // element). An infinite e^-z makes 0 of both.
 template <typename T>
 __device__ __forceinline__ float2 sigmoid(float2 z) {
@@ -611,10 +611,15 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
     }
 }
 
-// terms [N][G]: means over the group from the splits' sums, a warp a group
-__global__ void __launch_bounds__(kGroupThreads) k_group_terms(const __grid_constant__ GroupShape s, const float2 *part, float2 *terms) {
-    const long long i = (long long)blockIdx.x * (kGroupThreads / 32) + (threadIdx.x >> 5);
-    if (i >= s.N * s.G) return;
+// terms [N][G]: means over the group from the splits' sums, a warp a group; and in blocks behind those the column sums of
+// all samples' splits (norm_cols), where they are wanted: a launch of their own was 5 us of the backward of 8 x 4096 x 512.
+// (8 groups a block: as many as it has warps, 32, make one block of 32 groups of 456 splits, 9.4 us.)
+constexpr int kGroupTermThreads = kNormColThreads * kNormColSlices, kGroupTermWarps = 8;
+__global__ void __launch_bounds__(kGroupTermThreads) k_group_terms(const __grid_constant__ GroupShape s, const float2 *part, float2 *terms, int blocks,
+                                                                   const float *cols, float *dw, float *db) {
+    if ((int)blockIdx.x >= blocks) return norm_cols(blockIdx.x - blocks, cols, (int)(s.N * s.splits), s.C, dw, db);
+    const long long i = (long long)blockIdx.x * kGroupTermWarps + (threadIdx.x >> 5);
+    if (threadIdx.x >= 32 * kGroupTermWarps || i >= s.N * s.G) return;
     const float2 *at = part + i / s.G * s.splits * s.G + i % s.G;
     float2 a = both(0.f);
 #pragma unroll 4
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
 // ---- which form, and its launches ---------------------------------------------------------------
 
 // Blocks of a sample: kGroupSm an SM in all, 8 positions at least each. kGroupSm 3, of 80 registers: 8 x 4096 x 512 bfloat16
-// with silu 26 us and backward 51; 4, with spills, 29; 2, of 128 registers, 28 and 72. At least 8 / 16 / 32 positions, forward
+// with silu 25 us and backward 47; 4, with spills, 29; 2, of 128 registers, 28 and 72. At least 8 / 16 / 32 positions, forward
 // and backward: 2 x 64 x 1280 10.2, 15.5 / 12.8, 21.0 / 18.0, 31.8 us; 8 x 256 x 512 11.1, 14.2 / 10.3, 13.6 / 11.0, 16.1.
 int group_splits(long long N, long long L) {
     const long long want = (long long)kGroupSm * kRefSms / (N ? N : 1), most = L / 8;
@@ -721,6 +726,12 @@ GroupBack group_back(const NormGeom &g, long long N, int G) {
     return {true, parts * G, parts};
 }
 
+// (what any kernel may take, 48 KB with its own arrays, needs no call)
+template <typename K>
+void group_smem(K kern, size_t bytes) {
+    if (bytes > 40 * 1024) set_kernel_smem(kern, bytes);
+}
+
 template <typename T, typename F>
 void group_by_vec(int vec, F f) {
     constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
@@ -740,7 +751,7 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
             constexpr int NV = 16 / VEC;
             const size_t smem = GroupRing<T, VEC, NV, 1, false>::bytes(g.threads);
             auto go = [&](auto kern) {
-                set_kernel_smem(kern, smem);
+                group_smem(kern, smem);
                 const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (kGroupRowThreads / g.threads));
                 kern<<<(unsigned)grid, g.threads, smem, st>>>(s, x, g.tpr, y, stats);
             };
@@ -751,7 +762,7 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
         const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
         const unsigned grid = (unsigned)(s.N * s.splits);
         const size_t smem = (size_t)slots * cv * 8;
-        set_kernel_smem(k_group_stats<T, VEC>, smem);
+        group_smem(k_group_stats<T, VEC>, smem);
         k_group_stats<T, VEC><<<grid, kGroupThreads, smem, st>>>(s, x, part);
         float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
         const long long warps = s.N * s.G;
@@ -760,12 +771,11 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
     });
 }
 
-// returns the partials of the column sums
 template <typename T, bool ACT>
-long long group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, bool sums, float *part, float2 *terms, int vec,
-                         cudaStream_t st) {
+void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, float *dw, float *db, float *part, float2 *terms, int vec,
+                    cudaStream_t st) {
     const int each = s.C / s.G;
-    long long parts = 0;
+    const bool sums = dw || db;
     group_by_vec<T>(vec, [&](auto v) {
         constexpr int VEC = decltype(v)::value;
         if (group_rows(s.L, each)) {
@@ -776,26 +786,24 @@ long long group_backward(const GroupShape &s, const T *dy, const T *x, const flo
             const size_t cols = g.block ? 0 : (size_t)2 * kNormBlock * 16 * 4;
             auto go = [&](auto kern) {
                 const size_t bytes = smem > cols ? smem : cols;
-                set_kernel_smem(kern, bytes);
+                group_smem(kern, bytes);
                 kern<<<(unsigned)to.blocks, g.threads, bytes, st>>>(s, dy, x, g.tpr, to.same, stats, dx, sums ? part : nullptr);
             };
             if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>);
             else go(k_group_row_bwd<T, VEC, NV, false, ACT>);
-            parts = to.parts;
+            if (sums) k_norm_cols<<<norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st>>>(part, (int)to.parts, s.C, dw, db);
             return;
         }
         const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
         const unsigned grid = (unsigned)(s.N * s.splits);
         const size_t smem = (size_t)slots * cv * 8 + (slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0);
-        set_kernel_smem(k_group_sums<T, VEC, ACT>, smem);
+        group_smem(k_group_sums<T, VEC, ACT>, smem);
         float2 *split_terms = terms + s.N * s.G;
         k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
-        const long long groups = s.N * s.G, per = kGroupThreads / 32;
-        k_group_terms<<<(unsigned)((groups + per - 1) / per), kGroupThreads, 0, st>>>(s, split_terms, terms);
+        const int blocks = (int)((s.N * s.G + kGroupTermWarps - 1) / kGroupTermWarps);
+        k_group_terms<<<blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st>>>(s, split_terms, terms, blocks, part, dw, db);
         k_group_apply_bwd<T, VEC, ACT><<<grid, kGroupThreads, 0, st>>>(s, dy, x, stats, terms, dx);
-        parts = s.N * s.splits;
     });
-    return parts;
 }
 
 int group_check(const char *what, long long N, long long L, int C, int G, long long xs, int wdtype, int act, int dtype) {
@@ -912,17 +920,14 @@ int sdm_group_norm_backward(const void *grad, long long grad_stride, const void 
     int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, grad_stride, x, grad, grad_x);
     auto part = static_cast<float *>(workspace);
     auto terms = rows ? nullptr : reinterpret_cast<float2 *>(static_cast<unsigned char *>(workspace) + group_part_bytes(N, L, C, G, true));
-    long long parts = 0;
     auto go = [&](auto type, auto act) {
         using T = decltype(type);
-        parts = group_backward<T, decltype(act)::value>(s, static_cast<const T *>(grad), static_cast<const T *>(x),
-                                                        reinterpret_cast<const float2 *>(stats), static_cast<T *>(grad_x), sums, part, terms, vec, st);
+        group_backward<T, decltype(act)::value>(s, static_cast<const T *>(grad), static_cast<const T *>(x), reinterpret_cast<const float2 *>(stats),
+                                                static_cast<T *>(grad_x), grad_weight, grad_bias, part, terms, vec, st);
     };
     const bool silu = activation == SDM_ACT_SILU;
     if (dtype == SDM_BF16) silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});
     else silu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
-    if (sums)
-        k_norm_cols<<<(2 * C + kNormColThreads - 1) / kNormColThreads, kNormColThreads * kNormColSlices, 0, st>>>(part, (int)parts, C, grad_weight, grad_bias);
     return group_status(what, cudaGetLastError());
 }
 

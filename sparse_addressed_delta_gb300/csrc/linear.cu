@@ -137,7 +137,7 @@ LinearLayout linear_layout(const LinearDims &d, bool back) {
 // what the saving forward keeps: the states its segments begin with, the initial one first
 size_t linear_saved(const LinearDims &d) { return up(d.segs * (size_t)linear_states(d) * 4); }
 
-// q, k, v (and with grad the readings' gradient) as the tensor copies take them
+// q, k, v (and with grad the readings' gradient) as the tensor copies take them; clears the status block
 cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char *ws, const void *const (&src)[4], LinearLaid (&laid)[4],
                        cudaStream_t st) {
     LinearLay lay[4];
@@ -150,7 +150,7 @@ cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char
         lay[n++] = LinearLay{src[i], {s[0], s[1], s[2]}, heads, width, ws + l.laid[i]};
         laid[i] = LinearLaid{ws + l.laid[i], {(long long)d.T * heads * width, (long long)heads * width, width}, heads, width};
     }
-    return launch_linear_lay(d, lay, n, st);
+    return n ? launch_linear_lay(d, lay, n, reinterpret_cast<DevStatus *>(ws), st) : linear_clear(ws, kAlign, st);
 }
 
 LinearOperand operand(const void *p, const long long *s, int share) { return LinearOperand{p, {s[0], s[1], s[2]}, share}; }
@@ -183,8 +183,8 @@ int linear_forward(const sdm_linear_shape *shape, float *state, const void *q, c
     if (rc != SDM_OK) return rc;
     auto ws = static_cast<unsigned char *>(workspace);
     LinearLaid laid[4];
-    cudaError_t e = linear_clear(workspace, workspace_bytes, st);
-    if (e == cudaSuccess && save && d.segs == 1)
+    cudaError_t e = cudaSuccess;
+    if (save && d.segs == 1)
         e = cudaMemcpyAsync(saved, state, (size_t)linear_states(d) * 4, cudaMemcpyDeviceToDevice, st);
     if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, nullptr}, laid, st);
     float *starts = save ? static_cast<float *>(saved) : reinterpret_cast<float *>(ws + l.starts);
@@ -270,8 +270,7 @@ int sdm_linear_attention_backward(const sdm_linear_shape *shape, const void *q, 
     const LinearPass pk{ov, og, oq, d.Dv, d.Dk, tiles, true, d.scale, 1.f, d.scale, grad_final_state, nullptr, 1, d.Dv, dk, parts};
     const LinearPass pv{ok, oq, og, d.Dk, d.Dv, 1, true, d.scale, 1.f, d.scale, grad_final_state, grad_state, d.Dv, 1, grad_v, false};
     LinearLaid laid[4];
-    cudaError_t e = linear_clear(workspace, workspace_bytes, st);
-    if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, st);
+    cudaError_t e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, st);
     float *ends = reinterpret_cast<float *>(ws + l.starts);
     if (e == cudaSuccess) e = launch_linear_scan(d, pq, in, {laid[3], laid[2], laid[1]}, first, ws, st);
     if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, pv, in, laid[0], laid[3], ends, ws, st);

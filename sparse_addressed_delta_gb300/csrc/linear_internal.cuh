@@ -97,7 +97,8 @@ struct LinearLay {
     int heads, width;
     void *dst;
 };
-cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, cudaStream_t st);
+// n > 0 of them; clears the status block too
+cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, DevStatus *status, cudaStream_t st);
 cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts,
                                void *status, cudaStream_t st);
 // A sequence in segments (d.segs > 1): a first launch takes every segment but the pass's last from a state of zeros to

@@ -533,7 +533,8 @@ struct LayTable {
     int heads[4], width[4];
 };
 template <typename T>
-__global__ void __launch_bounds__(256) k_linear_lay(const __grid_constant__ LayTable t, int B, int T_) {
+__global__ void __launch_bounds__(256) k_linear_lay(const __grid_constant__ LayTable t, int B, int T_, DevStatus *status) {
+    if (blockIdx.x + blockIdx.y + threadIdx.x == 0) *status = DevStatus{};
     const int w = blockIdx.y, heads = t.heads[w], width = t.width[w];
     const T *x = static_cast<const T *>(t.src[w]);
     const long long all = (long long)B * T_ * heads * (width / 8);
@@ -583,8 +584,7 @@ cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const L
     return wide ? scan_of<128, 3>(d, a, m, st) : scan_of<64, 3>(d, a, m, st);
 }
 
-cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, cudaStream_t st) {
-    if (n == 0) return cudaSuccess;
+cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, DevStatus *status, cudaStream_t st) {
     LayTable t{};
     long long most = 0;
     for (int i = 0; i < n; ++i) {
@@ -598,8 +598,8 @@ cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, 
     }
     const long long want = (most + 255) / 256;
     const dim3 grid((unsigned)(want < 8 * kRefSms ? want : 8 * kRefSms), n);
-    if (d.dtype == SDM_F32) k_linear_lay<float><<<grid, 256, 0, st>>>(t, d.B, d.T);
-    else k_linear_lay<__nv_bfloat16><<<grid, 256, 0, st>>>(t, d.B, d.T);
+    if (d.dtype == SDM_F32) k_linear_lay<float><<<grid, 256, 0, st>>>(t, d.B, d.T, status);
+    else k_linear_lay<__nv_bfloat16><<<grid, 256, 0, st>>>(t, d.B, d.T, status);
     return cudaGetLastError();
 }
 

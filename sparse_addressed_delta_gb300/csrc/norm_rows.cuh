@@ -205,12 +205,11 @@ __device__ __forceinline__ float add_exact(float s, float x, float &low) {
 // column sums of the blocks' partials, in a fixed order: kNormColSlices runs of blocks, then them in pairs, with what
 // the roundings lose kept beside (5003 x 1007 float32, in one float each: 1.7e-7 off float64 with the runs one after
 // the other, 1.4e-7 in pairs)
-__global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
-    k_norm_cols(const float *part, int parts, int n, float *dw, float *db) {
+__device__ __forceinline__ void norm_cols(int block, const float *part, int parts, int n, float *dw, float *db) {
     static_assert(kNormColSlices == 64 && kNormColThreads <= 32, "a warp a column, two runs a lane");
     __shared__ float sh[kNormColSlices][kNormColThreads + 1], lost[kNormColSlices][kNormColThreads + 1];
     const int tx = threadIdx.x % kNormColThreads, ty = threadIdx.x / kNormColThreads;
-    const int c = blockIdx.x * kNormColThreads + tx;     // over [2][n]
+    const int c = block * kNormColThreads + tx;          // over [2][n]
     float s = 0.f, low = 0.f;
     if (c < 2 * n)
 #pragma unroll 8
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
     sh[ty][tx] = s;
     lost[ty][tx] = low;
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * kNormColThreads + warp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = block * kNormColThreads + warp;
     if (warp >= kNormColThreads) return;
     low = lost[lane][warp] + lost[lane + 32][warp];
     s = add_exact(sh[lane][warp], sh[lane + 32][warp], low);
@@ -237,6 +236,11 @@ __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
         }
     }
 }
+__global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
+    k_norm_cols(const float *part, int parts, int n, float *dw, float *db) {
+    norm_cols(blockIdx.x, part, parts, n, dw, db);
+}
+inline unsigned norm_col_blocks(int n) { return (2 * n + kNormColThreads - 1) / kNormColThreads; }
 
 struct NormGeom {
     int vec;        // elements per vector
