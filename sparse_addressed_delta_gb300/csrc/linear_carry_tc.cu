@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kCarThreads, 1)
     const int v0 = tile * 128;
     const int ntok = linear_valid(a.valid, b, d.T), chunks = (ntok + C - 1) / C;
     const int place = REV ? d.segs - 1 - seg : seg;
-    const int n0 = (int)((long long)chunks * place / d.segs), nch = (int)((long long)chunks * (place + 1) / d.segs) - n0;
+    const int n0 = linear_cut(chunks, place, d.segs), nch = linear_cut(chunks, place + 1, d.segs) - n0;
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -234,9 +234,10 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
     const int b = (int)(bh / d.H), h = (int)(bh % d.H);
     const int ntok = linear_valid(valid, b, d.T), chunks = (ntok + d.C - 1) / d.C;
     auto bound = [&](int n) {
-        const int t = (int)((long long)chunks * n / d.segs) * d.C;
+        const int t = linear_cut(chunks, n, d.segs) * d.C;
         return t < ntok ? t : ntok;
     };
+    const float decay = g[h];
     float4 s = first ? make_float4(first[i], first[i + 1], first[i + 2], first[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<float4 *>(starts + i) = s;
     // what the segments add is fetched eight at a time: one by one each waits for memory (16 segments 10 us)
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
             const int m = m0 + j;
             if (m >= d.segs) break;
             const int place = reverse ? d.segs - m : m - 1;        // of the segment before
-            const float w = linear_power(g[h], bound(place + 1) - bound(place));
+            const float w = linear_power(decay, bound(place + 1) - bound(place));
             s = make_float4(fmaf(w, s.x, e[j].x), fmaf(w, s.y, e[j].y), fmaf(w, s.z, e[j].z), fmaf(w, s.w, e[j].w));
             *reinterpret_cast<float4 *>(starts + m * states + i) = s;
         }

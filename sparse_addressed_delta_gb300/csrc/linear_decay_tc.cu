@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int b = (int)(bh / d.H), h = (int)(bh % d.H);
     const int v0 = tile * 128, k0 = kb * KP;
     const int ntok = linear_valid(a.valid, b, d.T), chunks = (ntok + C - 1) / C;
-    const int n0 = (int)((long long)chunks * seg / d.segs), nch = (int)((long long)chunks * (seg + 1) / d.segs) - n0;
+    const int n0 = linear_cut(chunks, seg, d.segs), nch = linear_cut(chunks, seg + 1, d.segs) - n0;
     const long long states = (long long)d.B * d.H * d.Dk * d.Dv;
 
     if (tid == 0) {

@@ -57,6 +57,11 @@ __device__ __forceinline__ int linear_valid(const int32_t *valid, int b, int T) 
     const int v = valid ? valid[b] : T;
     return v < 0 ? 0 : (v > T ? T : v);
 }
+// floor(chunks n / segs), the chunk that segment n begins with, in 32 bits (segs is at most the SMs)
+__device__ __forceinline__ int linear_cut(int chunks, int n, int segs) {
+    const unsigned whole = (unsigned)chunks / (unsigned)segs, rest = (unsigned)chunks % (unsigned)segs;
+    return (int)(whole * n + rest * n / segs);
+}
 // e^(g n) for whole n >= 0, within one unit in the last place. The powers multiply up along a sequence, and the
 // rounding of g n itself would grow with n, so its low part is kept; the exponential is the argument reduction of Cody
 // and Waite (n ln 2 in two parts, the first of few bits) and the Taylor series of the remainder. In 32 bits: a double

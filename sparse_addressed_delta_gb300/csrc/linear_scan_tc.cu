@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int v0 = tile * 128, k0 = kb * 128, K = p.K - k0 < 128 ? p.K - k0 : 128;
     const int ntok = linear_valid(a.valid, b, d.T), chunks = (ntok + C - 1) / C;
     const int place = REV ? d.segs - 1 - seg : seg;
-    const int n0 = (int)((long long)chunks * place / d.segs), nch = (int)((long long)chunks * (place + 1) / d.segs) - n0;
+    const int n0 = linear_cut(chunks, place, d.segs), nch = linear_cut(chunks, place + 1, d.segs) - n0;
     const long long states = (long long)d.B * d.H * d.Dk * d.Dv, own = bh * d.Dk * d.Dv + k0 * p.sk;
 
     if (tid == 0) {
@@ -490,12 +490,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             __syncthreads();
         }
-        if (seg + 1 == d.segs) {
-            const int cols = p.V - v0 < 128 ? p.V - v0 : 128;
-            OT *out = static_cast<OT *>(p.out) + (((long long)kb * d.B + b) * d.T * d.H + h) * p.V + v0;
-            for (long long t = (long long)chunks * C + (tid >> 7); t < d.T && tid < 512; t += 4)
-                if ((tid & 127) < cols) out[t * d.H * p.V + (tid & 127)] = from_f32<OT>(0.f);
-        }
+        // Results behind the last chunk are 0: 16 bytes a thread, by all the sequence's segments in turn (one value a
+        // thread by its last one: 4 of the 14 us of two sequences of up to 1003 tokens).
+        constexpr int PIECE = 16 / (int)sizeof(OT);
+        const int pieces = (p.V - v0 < 128 ? p.V - v0 : 128) / PIECE, rows = kLinThreads / pieces, row = tid / pieces;
+        const long long step = (long long)d.H * p.V;
+        OT *out = static_cast<OT *>(p.out) + (((long long)kb * d.B + b) * d.T * d.H + h) * p.V + v0 + tid % pieces * PIECE;
+        if (row < rows)
+            for (long long t = (long long)chunks * C + (long long)seg * rows + row; t < d.T; t += (long long)rows * d.segs)
+                *reinterpret_cast<uint4 *>(out + t * step) = make_uint4(0, 0, 0, 0);
     }
     float *end = seg + 1 == d.segs ? p.last : nullptr;
     if (warp < kLinWarps && end) {
