@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock)
     constexpr int E = VEC * NV, ST = kNormStages<T>;
     extern __shared__ __align__(16) unsigned char ring_smem[];
     __shared__ float red[2 * 2 * 32];
+    chain_next();
     int turn = 0;
     const int sub = BLOCK ? 0 : threadIdx.x / tpr, t = BLOCK ? threadIdx.x : threadIdx.x % tpr, rpb = BLOCK ? 1 : kNormBlock / tpr;
     const int c = s.C / s.G;
@@ -403,6 +404,7 @@ struct Piece {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const __grid_constant__ GroupShape s, const T *x, float2 *part) {
     extern __shared__ float2 acc[];                      // [slots][cv]
+    chain_next();
     const Piece p(s);
     const Spread sp(s.C, VEC);
     const int at_slot = (int)threadIdx.x / sp.cv, slot = at_slot < sp.slots ? at_slot : -1;
@@ -465,6 +467,8 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const _
 // joined [N][G] mean and rstd from the splits', a warp a group
 __global__ void __launch_bounds__(kGroupThreads) k_group_join(const __grid_constant__ GroupShape s, const float2 *part, float2 *joined) {
     const long long i = (long long)blockIdx.x * (kGroupThreads / 32) + (threadIdx.x >> 5);
+    chain_wait();
+    chain_next();
     if (i >= s.N * s.G) return;
     const float c = (float)(s.C / s.G), all = (float)s.L * c;
     const float2 *at = part + i / s.G * s.splits * s.G + i % s.G;
@@ -502,10 +506,11 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_apply(const _
     for (int cv = cv0; cv < sp.cv; cv += wide) {
         const int c0 = cv * VEC;
         fetch(p.from + slot, c0);
-        const float2 a = stats[p.n * s.G + c0 / each];
         float w[VEC], b[VEC];
         load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
         load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
+        chain_wait();
+        const float2 a = stats[p.n * s.G + c0 / each];
         for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * kGroupBatch) {
 #pragma unroll
             for (int i = 0; i < kGroupBatch; ++i) {
@@ -535,6 +540,7 @@ template <typename T, int VEC, bool ACT>
 __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
     k_group_sums(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, float *part, float2 *terms) {
     extern __shared__ __align__(16) float sums[];        // [slots][2][C] where there are several slots; then [slots][cv] a thread's terms
+    chain_next();
     const Piece p(s);
     const Spread sp(s.C, VEC);
     const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
@@ -617,6 +623,8 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
 constexpr int kGroupTermThreads = kNormColThreads * kNormColSlices, kGroupTermWarps = 8;
 __global__ void __launch_bounds__(kGroupTermThreads) k_group_terms(const __grid_constant__ GroupShape s, const float2 *part, float2 *terms, int blocks,
                                                                    const float *cols, float *dw, float *db) {
+    chain_wait();
+    chain_next();
     if ((int)blockIdx.x >= blocks) return norm_cols(blockIdx.x - blocks, cols, (int)(s.N * s.splits), s.C, dw, db);
     const long long i = (long long)blockIdx.x * kGroupTermWarps + (threadIdx.x >> 5);
     if (threadIdx.x >= 32 * kGroupTermWarps || i >= s.N * s.G) return;
@@ -641,10 +649,11 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
     T *out = dx + p.n * s.L * s.C;
     for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += sp.slots > 1 ? sp.cv : kGroupThreads) {
         const int c0 = cv * VEC;
-        const float2 a = stats[p.n * s.G + c0 / each], m = terms[p.n * s.G + c0 / each];
         float w[VEC], b[VEC];
         load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
         load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
+        chain_wait();
+        const float2 a = stats[p.n * s.G + c0 / each], m = terms[p.n * s.G + c0 / each];
         constexpr int BATCH = 4;
         for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * BATCH) {
             Vec<T, VEC> rx[BATCH], rg[BATCH];
@@ -766,8 +775,8 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
         k_group_stats<T, VEC><<<grid, kGroupThreads, smem, st>>>(s, x, part);
         float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
         const long long warps = s.N * s.G;
-        k_group_join<<<(unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st>>>(s, part, joined);
-        k_group_apply<T, VEC, ACT><<<grid, kGroupThreads, 0, st>>>(s, x, joined, y);
+        chain_launch(true, k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
+        chain_launch(true, k_group_apply<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
     });
 }
 
@@ -791,7 +800,7 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
             };
             if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>);
             else go(k_group_row_bwd<T, VEC, NV, false, ACT>);
-            if (sums) k_norm_cols<<<norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st>>>(part, (int)to.parts, s.C, dw, db);
+            if (sums) chain_launch(true, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
             return;
         }
         const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
@@ -801,8 +810,8 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
         float2 *split_terms = terms + s.N * s.G;
         k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
         const int blocks = (int)((s.N * s.G + kGroupTermWarps - 1) / kGroupTermWarps);
-        k_group_terms<<<blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st>>>(s, split_terms, terms, blocks, part, dw, db);
-        k_group_apply_bwd<T, VEC, ACT><<<grid, kGroupThreads, 0, st>>>(s, dy, x, stats, terms, dx);
+        chain_launch(true, k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
+        chain_launch(true, k_group_apply_bwd<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
     });
 }
 

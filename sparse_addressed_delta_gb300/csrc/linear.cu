@@ -139,7 +139,7 @@ size_t linear_saved(const LinearDims &d) { return up(d.segs * (size_t)linear_sta
 
 // q, k, v (and with grad the readings' gradient) as the tensor copies take them; clears the status block
 cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char *ws, const void *const (&src)[4], LinearLaid (&laid)[4],
-                       cudaStream_t st) {
+                       bool &chained, cudaStream_t st) {
     LinearLay lay[4];
     int n = 0;
     for (int i = 0; i < 4 && src[i]; ++i) {
@@ -150,6 +150,7 @@ cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char
         lay[n++] = LinearLay{src[i], {s[0], s[1], s[2]}, heads, width, ws + l.laid[i]};
         laid[i] = LinearLaid{ws + l.laid[i], {(long long)d.T * heads * width, (long long)heads * width, width}, heads, width};
     }
+    chained = n > 0;
     return n ? launch_linear_lay(d, lay, n, reinterpret_cast<DevStatus *>(ws), st) : linear_clear(ws, kAlign, st);
 }
 
@@ -183,13 +184,14 @@ int linear_forward(const sdm_linear_shape *shape, float *state, const void *q, c
     if (rc != SDM_OK) return rc;
     auto ws = static_cast<unsigned char *>(workspace);
     LinearLaid laid[4];
+    bool chained = false;
     cudaError_t e = cudaSuccess;
     if (save && d.segs == 1)
         e = cudaMemcpyAsync(saved, state, (size_t)linear_states(d) * 4, cudaMemcpyDeviceToDevice, st);
-    if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, nullptr}, laid, st);
+    if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, nullptr}, laid, chained, st);
     float *starts = save ? static_cast<float *>(saved) : reinterpret_cast<float *>(ws + l.starts);
-    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, p, in, laid[1], laid[2], starts, ws, st);
-    if (e == cudaSuccess) e = launch_linear_scan(d, p, in, {laid[0], laid[1], laid[2]}, starts, ws, st);
+    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, p, in, laid[1], laid[2], starts, ws, chained, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, p, in, {laid[0], laid[1], laid[2]}, starts, ws, chained || d.segs > 1, st);
     return linear_status(e);
 }
 
@@ -270,18 +272,19 @@ int sdm_linear_attention_backward(const sdm_linear_shape *shape, const void *q, 
     const LinearPass pk{ov, og, oq, d.Dv, d.Dk, tiles, true, d.scale, 1.f, d.scale, grad_final_state, nullptr, 1, d.Dv, dk, parts};
     const LinearPass pv{ok, oq, og, d.Dk, d.Dv, 1, true, d.scale, 1.f, d.scale, grad_final_state, grad_state, d.Dv, 1, grad_v, false};
     LinearLaid laid[4];
-    cudaError_t e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, st);
+    bool chained = false;
+    cudaError_t e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, chained, st);
     float *ends = reinterpret_cast<float *>(ws + l.starts);
-    if (e == cudaSuccess) e = launch_linear_scan(d, pq, in, {laid[3], laid[2], laid[1]}, first, ws, st);
-    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, pv, in, laid[0], laid[3], ends, ws, st);
-    if (e == cudaSuccess) e = launch_linear_scan(d, pk, in, {laid[2], laid[3], laid[0]}, ends, ws, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, pq, in, {laid[3], laid[2], laid[1]}, first, ws, chained, st);
+    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, pv, in, laid[0], laid[3], ends, ws, true, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, pk, in, {laid[2], laid[3], laid[0]}, ends, ws, true, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dq), tiles, d.Dk, grad_q, st);
     if (e == cudaSuccess && parts) e = launch_linear_sum(d, static_cast<const float *>(dk), tiles, d.Dk, grad_k, st);
     if (e == cudaSuccess && grad_log_decay)
         e = launch_linear_decay(d, in, laid, first, d.segs > 1 ? ends : grad_final_state, reinterpret_cast<double *>(ws + l.decay), grad_log_decay,
                                 ws, st);
     // last: the final state's gradient may be grad_state itself
-    if (e == cudaSuccess) e = launch_linear_scan(d, pv, in, {laid[1], laid[0], laid[3]}, ends, ws, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, pv, in, {laid[1], laid[0], laid[3]}, ends, ws, true, st);
     return linear_status(e);
 }
 

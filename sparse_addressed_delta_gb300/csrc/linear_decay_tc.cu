@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         for (int i = D_MUL; i < D_COUNT; ++i)
             mbar_init(bar + i, (i >= D_CONV && i < D_PAIR) || i == D_READ ? kDecWarps : 1);
-        *dead = a.status->code != 0;
         fence_mbar_init();
     }
     if (warp == kDecWarps) {
@@ -101,6 +100,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (tid == C) pw[0] = 1.f;
         pair[tid] = tid < C ? 0.f : (float)n * x;
     }
+    chain_wait();
+    if (tid == 0) *dead = a.status->code != 0;                     // an earlier kernel of this call gave up
+    chain_next();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -326,6 +328,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
 // a head's parts of all sequences, in a fixed order; a warp a head
 __global__ void __launch_bounds__(32) k_linear_decay_sum(const double *part, int B, int H, int each, float *out) {
+    chain_wait();
+    chain_next();
     const int h = blockIdx.x;
     double s = 0.0;
     for (long long i = threadIdx.x; i < (long long)B * each; i += 32) s += part[(i / each * H + h) * each + i % each];
@@ -338,8 +342,7 @@ template <int NP>
 cudaError_t decay(const LinearDims &d, const DecayArgs &a, const CUtensorMap *m, cudaStream_t st) {
     using L = LinDecay<NP>;
     set_kernel_smem(k_linear_decay<NP>, L::BYTES);
-    k_linear_decay<NP><<<(unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
-    return cudaGetLastError();
+    return chain_launch(true, k_linear_decay<NP>, (unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
 }
 
 }  // namespace
@@ -357,8 +360,7 @@ cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const L
     }
     const cudaError_t e = np == 3 ? decay<3>(d, a, m, st) : decay<1>(d, a, m, st);
     if (e != cudaSuccess) return e;
-    k_linear_decay_sum<<<d.H, 32, 0, st>>>(part, d.B, d.H, a.kblocks * linear_tiles(d.Dv) * d.segs, grad_decay);
-    return cudaGetLastError();
+    return chain_launch(true, k_linear_decay_sum, d.H, 32, 0, st, part, d.B, d.H, a.kblocks * linear_tiles(d.Dv) * d.segs, grad_decay);
 }
 
 }  // namespace sdm

@@ -7,6 +7,7 @@
 // are its mirror image with (v, do, q) and (k, q, do), so one kernel makes them all: a pass.
 #pragma once
 
+#include "chain.cuh"
 #include "sdm_internal.cuh"
 
 namespace sdm {
@@ -104,13 +105,14 @@ struct LinearLay {
 };
 // n > 0 of them; clears the status block too
 cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, DevStatus *status, cudaStream_t st);
+// (chained: behind another kernel of the call)
 cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts,
-                               void *status, cudaStream_t st);
+                               void *status, bool chained, cudaStream_t st);
 // A sequence in segments (d.segs > 1): a first launch takes every segment but the pass's last from a state of zeros to
 // what it adds, a join makes the states they begin with of that, and the scan runs all at once. k, v: the laid operands
 // of a pass along the state's rows (sv = 1).
 cudaError_t launch_linear_carry(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid &k, const LinearLaid &v, float *starts,
-                                void *status, cudaStream_t st);
+                                void *status, bool chained, cudaStream_t st);
 
 // up to kLinearStepTokens tokens (any number, but slowly)
 cudaError_t launch_linear_step(const LinearDims &d, const LinearIn &in, const void *q, const void *k, const void *v, float *state, void *o,

@@ -130,7 +130,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         for (int i = B_PART; i < B_COUNT; ++i)
             mbar_init(bar + i, i == B_ZK || i == B_UF || i == B_OF || i == B_S || i == B_OUT ? kLinWarps : 1);
-        *dead = a.status->code != 0;                               // an earlier kernel of this call gave up
         fence_mbar_init();
     }
     if (warp == kLinWarps) {
@@ -149,6 +148,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     for (int i = tid; i < 3 * TILE / 16; i += kLinThreads)
         *reinterpret_cast<uint4 *>(smem + L::Z + i / (TILE / 16) * L::PLANE + i % (TILE / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
+    chain_wait();
+    if (tid == 0) *dead = a.status->code != 0;                     // an earlier kernel of this call gave up
+    chain_next();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -511,21 +513,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 }
 
 template <int KP, int NP, bool REV, typename OT>
-cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, cudaStream_t st) {
+cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, bool chained, cudaStream_t st) {
     auto kern = k_linear_scan<KP, NP, REV, OT>;
     using L = LinScan<KP, NP>;
     set_kernel_smem(kern, L::BYTES);
     const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * d.segs;
-    kern<<<(unsigned)blocks, kLinThreads, L::BYTES, st>>>(m[0], m[1], m[2], m[3], d, a);
-    return cudaGetLastError();
+    return chain_launch(chained, kern, (unsigned)blocks, kLinThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
 }
 
 template <int KP, int NP>
-cudaError_t scan_of(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, cudaStream_t st) {
+cudaError_t scan_of(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, bool chained, cudaStream_t st) {
     using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
     if constexpr (NP == 1)
-        if (a.p.out_f32) return a.p.reverse ? scan<KP, NP, true, float>(d, a, m, st) : scan<KP, NP, false, float>(d, a, m, st);
-    return a.p.reverse ? scan<KP, NP, true, IT>(d, a, m, st) : scan<KP, NP, false, IT>(d, a, m, st);
+        if (a.p.out_f32) return a.p.reverse ? scan<KP, NP, true, float>(d, a, m, chained, st) : scan<KP, NP, false, float>(d, a, m, chained, st);
+    return a.p.reverse ? scan<KP, NP, true, IT>(d, a, m, chained, st) : scan<KP, NP, false, IT>(d, a, m, chained, st);
 }
 
 // the operands as the tensor copies take them: float32 ones as three bfloat16 planes, the others contiguous
@@ -537,6 +538,7 @@ struct LayTable {
 };
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_lay(const __grid_constant__ LayTable t, int B, int T_, DevStatus *status) {
+    chain_next();
     if (blockIdx.x + blockIdx.y + threadIdx.x == 0) *status = DevStatus{};
     const int w = blockIdx.y, heads = t.heads[w], width = t.width[w];
     const T *x = static_cast<const T *>(t.src[w]);
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(256) k_linear_lay(const __grid_constant__ LayT
 }  // namespace
 
 cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts, void *status,
-                               cudaStream_t st) {
+                               bool chained, cudaStream_t st) {
     const int np = d.dtype == SDM_F32 ? 3 : 1;
     LinArgs a{p, in.g, in.valid, starts, static_cast<DevStatus *>(status), {}, {}, p.last != nullptr && !p.reverse};
     CUtensorMap m[4];
@@ -583,8 +585,8 @@ cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const L
         if (e != cudaSuccess) return e;
     }
     const bool wide = p.K > 64;
-    if (np == 1) return wide ? scan_of<128, 1>(d, a, m, st) : scan_of<64, 1>(d, a, m, st);
-    return wide ? scan_of<128, 3>(d, a, m, st) : scan_of<64, 3>(d, a, m, st);
+    if (np == 1) return wide ? scan_of<128, 1>(d, a, m, chained, st) : scan_of<64, 1>(d, a, m, chained, st);
+    return wide ? scan_of<128, 3>(d, a, m, chained, st) : scan_of<64, 3>(d, a, m, chained, st);
 }
 
 cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, DevStatus *status, cudaStream_t st) {

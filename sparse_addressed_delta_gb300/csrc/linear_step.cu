@@ -123,6 +123,8 @@ cudaError_t launch_step(const LinearDims &d, const LinearIn &in, const void *q, 
 constexpr int kSumRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_sum(const float *part, long long rows, int group, int blocks, int width, T *out) {
+    chain_wait();
+    chain_next();
     const int pieces = width / 4, rpb = 256 / pieces, sub = threadIdx.x / pieces, c = threadIdx.x % pieces * 4;
     if (sub >= rpb) return;
     const long long row = (long long)blockIdx.x * rpb * kSumRows + sub, plane = rows * group * width;
@@ -157,9 +159,9 @@ cudaError_t launch_linear_step(const LinearDims &d, const LinearIn &in, const vo
 cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, cudaStream_t st) {
     const long long rows = (long long)d.B * d.T * d.Hk, each = 256 / (width / 4) * kSumRows, grid = (rows + each - 1) / each;
     const int group = d.H / d.Hk;
-    if (d.dtype == SDM_BF16) k_linear_sum<<<(unsigned)grid, 256, 0, st>>>(part, rows, group, blocks, width, static_cast<__nv_bfloat16 *>(out));
-    else k_linear_sum<<<(unsigned)grid, 256, 0, st>>>(part, rows, group, blocks, width, static_cast<float *>(out));
-    return cudaGetLastError();
+    if (d.dtype == SDM_BF16)
+        return chain_launch(true, k_linear_sum<__nv_bfloat16>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<__nv_bfloat16 *>(out));
+    return chain_launch(true, k_linear_sum<float>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<float *>(out));
 }
 
 }  // namespace sdm

@@ -2,6 +2,7 @@
 // row's threads, column sums of blocks' partials.
 #pragma once
 
+#include "chain.cuh"
 #include "sdm_internal.cuh"
 
 namespace sdm {
@@ -238,6 +239,7 @@ __device__ __forceinline__ void norm_cols(int block, const float *part, int part
 }
 __global__ void __launch_bounds__(kNormColThreads *kNormColSlices)
     k_norm_cols(const float *part, int parts, int n, float *dw, float *db) {
+    chain_wait();                                        // (where it is chained to what makes the partials)
     norm_cols(blockIdx.x, part, parts, n, dw, db);
 }
 inline unsigned norm_col_blocks(int n) { return (2 * n + kNormColThreads - 1) / kNormColThreads; }
