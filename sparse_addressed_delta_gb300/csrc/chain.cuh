@@ -1,6 +1,11 @@
 // Launches of one call that follow each other on a stream: a kernel is launched while the one before it ends (programmatic
 // dependent launch) and waits for its end itself, so its blocks' start is hidden behind it. Only ever behind a kernel
 // of the same call, so that the inputs, which no kernel of the call writes, may be read before the wait.
+//
+// A kernel that needs nothing of the one before it, and writes nothing that one reads, runs beside it: its last block waits
+// at its end, so that when it has ended the other has (all blocks would hold their SMs until then). Whatever ended before
+// the other passed its own wait at its start, or before a chain of such kernels began, has ended for it too, as nobody
+// lets the next launch start before that; it reads what those wrote past L1 (__ldcg).
 #pragma once
 
 #include <utility>
@@ -14,8 +19,18 @@ __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait
 // the next launch may start its blocks as SMs become free
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+enum class Chain { alone, behind, beside };
+// at a kernel's start and end
+__device__ __forceinline__ void chain_begin(Chain c) {
+    if (c != Chain::beside) chain_wait();
+    chain_next();
+}
+__device__ __forceinline__ void chain_end(Chain c) {
+    if (c == Chain::beside && blockIdx.x == gridDim.x - 1) chain_wait();
+}
+
 template <typename... P, typename... A>
-cudaError_t chain_launch(bool chained, void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A &&...args) {
+cudaError_t chain_launch(Chain chain, void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A &&...args) {
     cudaLaunchAttribute attribute{};
     attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attribute.val.programmaticStreamSerializationAllowed = 1;
@@ -25,7 +40,7 @@ cudaError_t chain_launch(bool chained, void (*kern)(P...), dim3 grid, unsigned t
     config.dynamicSmemBytes = smem;
     config.stream = st;
     config.attrs = &attribute;
-    config.numAttrs = chained ? 1 : 0;
+    config.numAttrs = chain == Chain::alone ? 0 : 1;
     return cudaLaunchKernelEx(&config, kern, std::forward<A>(args)...);
 }
 

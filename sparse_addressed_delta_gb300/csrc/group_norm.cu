@@ -775,8 +775,8 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
         k_group_stats<T, VEC><<<grid, kGroupThreads, smem, st>>>(s, x, part);
         float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
         const long long warps = s.N * s.G;
-        chain_launch(true, k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
-        chain_launch(true, k_group_apply<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
+        chain_launch(Chain::behind, k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
+        chain_launch(Chain::behind, k_group_apply<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
     });
 }
 
@@ -800,7 +800,7 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
             };
             if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>);
             else go(k_group_row_bwd<T, VEC, NV, false, ACT>);
-            if (sums) chain_launch(true, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
+            if (sums) chain_launch(Chain::behind, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
             return;
         }
         const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
@@ -810,8 +810,8 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
         float2 *split_terms = terms + s.N * s.G;
         k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
         const int blocks = (int)((s.N * s.G + kGroupTermWarps - 1) / kGroupTermWarps);
-        chain_launch(true, k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
-        chain_launch(true, k_group_apply_bwd<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
+        chain_launch(Chain::behind, k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
+        chain_launch(Chain::behind, k_group_apply_bwd<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
     });
 }
 

@@ -39,6 +39,7 @@ struct CarryArgs {
     long long heads[2], seqs[2];         // of the laid keys and values, 0: broadcast
     int kshare, vshare, K, V;
     float to;
+    Chain chain;
 };
 
 template <int KP, int NP, bool REV>
@@ -84,9 +85,8 @@ __global__ void __launch_bounds__(kCarThreads, 1)
         pw[tid] = x;
         if (REV ? tid > 0 : tid < C) weight[REV ? tid - 1 : C - 1 - tid] = a.to * x;
     }
-    chain_wait();
-    if (tid == 0) *dead = a.status->code != 0;                     // an earlier kernel of this call gave up
-    chain_next();
+    chain_begin(a.chain);
+    if (tid == 0) *dead = __ldcg(&a.status->code) != 0;            // an earlier kernel of this call gave up
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kCarThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == kCarWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
+    chain_end(a.chain);
 }
 
 // starts [segs]: the state itself, then each segment's first state from the one before and what the carry left
@@ -240,8 +241,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
         return t < ntok ? t : ntok;
     };
     const float decay = g[h];
-    chain_wait();
-    chain_next();
+    chain_begin(Chain::behind);
     float4 s = first ? make_float4(first[i], first[i + 1], first[i + 2], first[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<float4 *>(starts + i) = s;
     // what the segments add is fetched eight at a time: one by one each waits for memory (16 segments 10 us)
@@ -263,34 +263,34 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Lin
 }
 
 template <int KP, int NP, bool REV>
-cudaError_t carry(const LinearDims &d, const CarryArgs &a, const CUtensorMap *m, bool chained, cudaStream_t st) {
+cudaError_t carry(const LinearDims &d, const CarryArgs &a, const CUtensorMap *m, Chain chain, cudaStream_t st) {
     using L = LinCarry<KP, NP>;
     set_kernel_smem(k_linear_carry<KP, NP, REV>, L::BYTES);
     const long long blocks = (long long)d.B * d.H * linear_tiles(a.V) * (d.segs - 1);
-    return chain_launch(chained, k_linear_carry<KP, NP, REV>, (unsigned)blocks, kCarThreads, L::BYTES, st, m[0], m[1], d, a);
+    return chain_launch(chain, k_linear_carry<KP, NP, REV>, (unsigned)blocks, kCarThreads, L::BYTES, st, m[0], m[1], d, a);
 }
 
 }  // namespace
 
 // k, v: those of a pass along the state's rows (p.sv = 1)
 cudaError_t launch_linear_carry(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid &k, const LinearLaid &v,
-                                float *starts, void *status, bool chained, cudaStream_t st) {
+                                float *starts, void *status, Chain chain, cudaStream_t st) {
     const int np = d.dtype == SDM_F32 ? 3 : 1;
-    const CarryArgs a{in.g, in.valid, starts, static_cast<DevStatus *>(status), {k.s[2], v.s[2]}, {k.s[0], v.s[0]}, p.k.share, p.v.share, p.K, p.V, p.to};
+    const CarryArgs a{in.g, in.valid, starts, static_cast<DevStatus *>(status), {k.s[2], v.s[2]}, {k.s[0], v.s[0]}, p.k.share, p.v.share, p.K, p.V, p.to, chain};
     CUtensorMap m[2];
     cudaError_t e = tc_tensor_map(m, k.p, k.s, np * d.B, d.T, k.heads, k.width);
     if (e == cudaSuccess) e = tc_tensor_map(m + 1, v.p, v.s, np * d.B, d.T, v.heads, v.width);
     if (e != cudaSuccess) return e;
     auto go = [&](auto kp, auto planes) {
         constexpr int KP = decltype(kp)::value, NP = decltype(planes)::value;
-        return p.reverse ? carry<KP, NP, true>(d, a, m, chained, st) : carry<KP, NP, false>(d, a, m, chained, st);
+        return p.reverse ? carry<KP, NP, true>(d, a, m, chain, st) : carry<KP, NP, false>(d, a, m, chain, st);
     };
     using std::integral_constant;
     if (np == 1) e = p.K > 64 ? go(integral_constant<int, 128>{}, integral_constant<int, 1>{}) : go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
     else e = p.K > 64 ? go(integral_constant<int, 128>{}, integral_constant<int, 3>{}) : go(integral_constant<int, 64>{}, integral_constant<int, 3>{});
     if (e != cudaSuccess) return e;
     const long long blocks = (linear_states(d) / 4 + 255) / 256;
-    return chain_launch(true, k_linear_join, (unsigned)blocks, 256, 0, st, d, in.g, in.valid, p.first, p.reverse, starts);
+    return chain_launch(Chain::behind, k_linear_join, (unsigned)blocks, 256, 0, st, d, in.g, in.valid, p.first, p.reverse, starts);
 }
 
 }  // namespace sdm

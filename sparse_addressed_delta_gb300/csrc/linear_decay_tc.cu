@@ -47,6 +47,7 @@ struct DecayArgs {
     DevStatus *status;
     long long heads[4], seqs[4];         // q, k, v, grad: strides of the laid operands, 0: broadcast
     int share, kblocks;
+    Chain chain;
 };
 
 template <int NP>
@@ -100,9 +101,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (tid == C) pw[0] = 1.f;
         pair[tid] = tid < C ? 0.f : (float)n * x;
     }
-    chain_wait();
-    if (tid == 0) *dead = a.status->code != 0;                     // an earlier kernel of this call gave up
-    chain_next();
+    chain_begin(a.chain);
+    if (tid == 0) *dead = __ldcg(&a.status->code) != 0;            // an earlier kernel of this call gave up
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const float *begin = a.starts + seg * states + own;
 #pragma unroll
         for (int i = 0; i < HD; ++i) {
-            S[i] = mine && k0 + kk + i < d.Dk && nch > 0 ? begin[(long long)i * d.Dv] : 0.f;
+            S[i] = mine && k0 + kk + i < d.Dk && nch > 0 ? __ldcg(begin + (long long)i * d.Dv) : 0.f;
             G[i] = 0.f;
         }
         auto arrive = [&](int which) {
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < HD; ++i)
-                    if (k0 + kk + i < d.Dk) sum = fmaf(G[i], end[(long long)i * d.Dv], sum);
+                    if (k0 + kk + i < d.Dk) sum = fmaf(G[i], __ldcg(end + (long long)i * d.Dv), sum);
                 add(sum);
             }
         }
@@ -324,33 +324,34 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int i = 0; i < kDecWarps; ++i) s += sums[i];
         a.part[blockIdx.x] = s;
     }
+    chain_end(a.chain);
 }
 
 // a head's parts of all sequences, in a fixed order; a warp a head
-__global__ void __launch_bounds__(32) k_linear_decay_sum(const double *part, int B, int H, int each, float *out) {
-    chain_wait();
-    chain_next();
+__global__ void __launch_bounds__(32) k_linear_decay_sum(const double *part, int B, int H, int each, float *out, Chain chain) {
+    chain_begin(chain);
     const int h = blockIdx.x;
     double s = 0.0;
-    for (long long i = threadIdx.x; i < (long long)B * each; i += 32) s += part[(i / each * H + h) * each + i % each];
+    for (long long i = threadIdx.x; i < (long long)B * each; i += 32) s += __ldcg(part + (i / each * H + h) * each + i % each);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
     if (threadIdx.x == 0) out[h] = (float)s;
+    chain_end(chain);
 }
 
 template <int NP>
 cudaError_t decay(const LinearDims &d, const DecayArgs &a, const CUtensorMap *m, cudaStream_t st) {
     using L = LinDecay<NP>;
     set_kernel_smem(k_linear_decay<NP>, L::BYTES);
-    return chain_launch(true, k_linear_decay<NP>, (unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
+    return chain_launch(a.chain, k_linear_decay<NP>, (unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearLaid (&laid)[4], const float *starts, const float *ends,
-                                double *part, float *grad_decay, void *status, cudaStream_t st) {
+                                double *part, void *status, Chain chain, cudaStream_t st) {
     const int np = d.dtype == SDM_F32 ? 3 : 1;
-    DecayArgs a{in.g, in.valid, starts, ends, part, static_cast<DevStatus *>(status), {}, {}, d.H / d.Hk, linear_decay_blocks(d)};
+    DecayArgs a{in.g, in.valid, starts, ends, part, static_cast<DevStatus *>(status), {}, {}, d.H / d.Hk, linear_decay_blocks(d), chain};
     CUtensorMap m[4];
     for (int i = 0; i < 4; ++i) {
         const cudaError_t e = tc_tensor_map(m + i, laid[i].p, laid[i].s, np * d.B, d.T, laid[i].heads, laid[i].width);
@@ -358,9 +359,11 @@ cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const L
         a.seqs[i] = laid[i].s[0];
         a.heads[i] = laid[i].s[2];
     }
-    const cudaError_t e = np == 3 ? decay<3>(d, a, m, st) : decay<1>(d, a, m, st);
-    if (e != cudaSuccess) return e;
-    return chain_launch(true, k_linear_decay_sum, d.H, 32, 0, st, part, d.B, d.H, a.kblocks * linear_tiles(d.Dv) * d.segs, grad_decay);
+    return np == 3 ? decay<3>(d, a, m, st) : decay<1>(d, a, m, st);
+}
+
+cudaError_t launch_linear_decay_sum(const LinearDims &d, const double *part, float *grad_decay, Chain chain, cudaStream_t st) {
+    return chain_launch(chain, k_linear_decay_sum, d.H, 32, 0, st, part, d.B, d.H, linear_decay_blocks(d) * linear_tiles(d.Dv) * d.segs, grad_decay, chain);
 }
 
 }  // namespace sdm

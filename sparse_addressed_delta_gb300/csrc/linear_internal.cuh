@@ -105,25 +105,26 @@ struct LinearLay {
 };
 // n > 0 of them; clears the status block too
 cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, DevStatus *status, cudaStream_t st);
-// (chained: behind another kernel of the call)
 cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts,
-                               void *status, bool chained, cudaStream_t st);
+                               void *status, Chain chain, cudaStream_t st);
 // A sequence in segments (d.segs > 1): a first launch takes every segment but the pass's last from a state of zeros to
 // what it adds, a join makes the states they begin with of that, and the scan runs all at once. k, v: the laid operands
 // of a pass along the state's rows (sv = 1).
 cudaError_t launch_linear_carry(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid &k, const LinearLaid &v, float *starts,
-                                void *status, bool chained, cudaStream_t st);
+                                void *status, Chain chain, cudaStream_t st);
 
 // up to kLinearStepTokens tokens (any number, but slowly)
 cudaError_t launch_linear_step(const LinearDims &d, const LinearIn &in, const void *q, const void *k, const void *v, float *state, void *o,
                                cudaStream_t st);
 // out [B, T, Hk, width] = the sum over a key head's heads, and over `blocks` parts, of part [blocks][B, T, H, width]
-cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, cudaStream_t st);
+cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, Chain chain, cudaStream_t st);
 // grad_decay [H] from the laid q, k, v and readings' gradient, the segments' first states and the gradients of the
 // states they end with (from the last one; one segment: may be null)
 inline int linear_decay_blocks(const LinearDims &d) { return (d.Dk + 63) / 64; }   // of Dk
 inline long long linear_decay_parts(const LinearDims &d) { return (long long)d.B * d.H * d.segs * linear_decay_blocks(d) * linear_tiles(d.Dv); }
 cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const LinearLaid (&laid)[4], const float *starts, const float *ends,
-                                double *part, float *grad_decay, void *status, cudaStream_t st);
+                                double *part, void *status, Chain chain, cudaStream_t st);
+// behind it: the parts' sums
+cudaError_t launch_linear_decay_sum(const LinearDims &d, const double *part, float *grad_decay, Chain chain, cudaStream_t st);
 
 }  // namespace sdm

@@ -58,6 +58,7 @@ struct LinArgs {
     long long heads[3];                  // head strides of the laid operands, 0: broadcast
     long long seqs[3];
     bool column;                         // columns with NaN or infinity are taken again (linear_column)
+    Chain chain;
 };
 
 // One column of a segment by one warp, token by token from the state it begins with; the readings of tokens from
@@ -148,9 +149,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     for (int i = tid; i < 3 * TILE / 16; i += kLinThreads)
         *reinterpret_cast<uint4 *>(smem + L::Z + i / (TILE / 16) * L::PLANE + i % (TILE / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
-    chain_wait();
-    if (tid == 0) *dead = a.status->code != 0;                     // an earlier kernel of this call gave up
-    chain_next();
+    chain_begin(a.chain);
+    if (tid == 0) *dead = __ldcg(&a.status->code) != 0;            // an earlier kernel of this call gave up
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -168,13 +168,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (p.sk == 1 && ((uintptr_t)begin & 15) == 0) {           // transposed: K runs along the row
 #pragma unroll
             for (int i = 0; i < HD / 4; ++i) {
-                const float4 x = begin && mine && kk + 4 * i < K ? *reinterpret_cast<const float4 *>(begin + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 x = begin && mine && kk + 4 * i < K ? __ldcg(reinterpret_cast<const float4 *>(begin + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 S[2 * i] = make_float2(x.x, x.y);
                 S[2 * i + 1] = make_float2(x.z, x.w);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < HD; ++i) reinterpret_cast<float *>(S)[i] = begin && mine && kk + i < K ? begin[i * p.sk] : 0.f;
+            for (int i = 0; i < HD; ++i) reinterpret_cast<float *>(S)[i] = begin && mine && kk + i < K ? __ldcg(begin + i * p.sk) : 0.f;
         }
         auto planes_of_s = [&] {
 #pragma unroll
@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tc_fence_before();
     const bool bad = __syncthreads_or(first >= 0);
     if (warp == kLinWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
+    chain_end(a.chain);
     if (*dead) return;
     {
         if (bad && a.column) {
@@ -513,20 +514,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 }
 
 template <int KP, int NP, bool REV, typename OT>
-cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, bool chained, cudaStream_t st) {
+cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, Chain chain, cudaStream_t st) {
     auto kern = k_linear_scan<KP, NP, REV, OT>;
     using L = LinScan<KP, NP>;
     set_kernel_smem(kern, L::BYTES);
     const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * d.segs;
-    return chain_launch(chained, kern, (unsigned)blocks, kLinThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
+    return chain_launch(chain, kern, (unsigned)blocks, kLinThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
 }
 
 template <int KP, int NP>
-cudaError_t scan_of(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, bool chained, cudaStream_t st) {
+cudaError_t scan_of(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, Chain chain, cudaStream_t st) {
     using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
     if constexpr (NP == 1)
-        if (a.p.out_f32) return a.p.reverse ? scan<KP, NP, true, float>(d, a, m, chained, st) : scan<KP, NP, false, float>(d, a, m, chained, st);
-    return a.p.reverse ? scan<KP, NP, true, IT>(d, a, m, chained, st) : scan<KP, NP, false, IT>(d, a, m, chained, st);
+        if (a.p.out_f32) return a.p.reverse ? scan<KP, NP, true, float>(d, a, m, chain, st) : scan<KP, NP, false, float>(d, a, m, chain, st);
+    return a.p.reverse ? scan<KP, NP, true, IT>(d, a, m, chain, st) : scan<KP, NP, false, IT>(d, a, m, chain, st);
 }
 
 // the operands as the tensor copies take them: float32 ones as three bfloat16 planes, the others contiguous
@@ -568,9 +569,9 @@ __global__ void __launch_bounds__(256) k_linear_lay(const __grid_constant__ LayT
 }  // namespace
 
 cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts, void *status,
-                               bool chained, cudaStream_t st) {
+                               Chain chain, cudaStream_t st) {
     const int np = d.dtype == SDM_F32 ? 3 : 1;
-    LinArgs a{p, in.g, in.valid, starts, static_cast<DevStatus *>(status), {}, {}, p.last != nullptr && !p.reverse};
+    LinArgs a{p, in.g, in.valid, starts, static_cast<DevStatus *>(status), {}, {}, p.last != nullptr && !p.reverse, chain};
     CUtensorMap m[4];
     for (int i = 0; i < 3; ++i) {
         const cudaError_t e = tc_tensor_map(m + i, laid[i].p, laid[i].s, np * d.B, d.T, laid[i].heads, laid[i].width);
@@ -585,8 +586,8 @@ cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const L
         if (e != cudaSuccess) return e;
     }
     const bool wide = p.K > 64;
-    if (np == 1) return wide ? scan_of<128, 1>(d, a, m, chained, st) : scan_of<64, 1>(d, a, m, chained, st);
-    return wide ? scan_of<128, 3>(d, a, m, chained, st) : scan_of<64, 3>(d, a, m, chained, st);
+    if (np == 1) return wide ? scan_of<128, 1>(d, a, m, chain, st) : scan_of<64, 1>(d, a, m, chain, st);
+    return wide ? scan_of<128, 3>(d, a, m, chain, st) : scan_of<64, 3>(d, a, m, chain, st);
 }
 
 cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, DevStatus *status, cudaStream_t st) {

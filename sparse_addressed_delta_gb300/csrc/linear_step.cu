@@ -122,11 +122,10 @@ cudaError_t launch_step(const LinearDims &d, const LinearIn &in, const void *q, 
 // 8192 tokens, 32 heads of 128 in pairs: 27 us, 6.2 TB/s.
 constexpr int kSumRows = 4;
 template <typename T>
-__global__ void __launch_bounds__(256) k_linear_sum(const float *part, long long rows, int group, int blocks, int width, T *out) {
-    chain_wait();
-    chain_next();
+__global__ void __launch_bounds__(256) k_linear_sum(const float *part, long long rows, int group, int blocks, int width, T *out, Chain chain) {
+    chain_begin(chain);
     const int pieces = width / 4, rpb = 256 / pieces, sub = threadIdx.x / pieces, c = threadIdx.x % pieces * 4;
-    if (sub >= rpb) return;
+    if (sub >= rpb) return;                              // (not all of a block)
     const long long row = (long long)blockIdx.x * rpb * kSumRows + sub, plane = rows * group * width;
     float4 s[kSumRows] = {};
     for (int g = 0; g < group; ++g)
@@ -135,7 +134,7 @@ __global__ void __launch_bounds__(256) k_linear_sum(const float *part, long long
 #pragma unroll
             for (int i = 0; i < kSumRows; ++i)
                 if (row + i * rpb < rows)
-                    x[i] = __ldcs(reinterpret_cast<const float4 *>(part + m * plane + ((row + i * rpb) * group + g) * width + c));
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(part + m * plane + ((row + i * rpb) * group + g) * width + c));
 #pragma unroll
             for (int i = 0; i < kSumRows; ++i) {
                 s[i].x += x[i].x; s[i].y += x[i].y; s[i].z += x[i].z; s[i].w += x[i].w;
@@ -147,6 +146,7 @@ __global__ void __launch_bounds__(256) k_linear_sum(const float *part, long long
             const float y[4] = {s[i].x, s[i].y, s[i].z, s[i].w};
             store_vec<T, 4>(out + (row + i * rpb) * width + c, y);
         }
+    chain_end(chain);
 }
 
 }  // namespace
@@ -156,12 +156,12 @@ cudaError_t launch_linear_step(const LinearDims &d, const LinearIn &in, const vo
     return d.dtype == SDM_BF16 ? launch_step<__nv_bfloat16>(d, in, q, k, v, state, o, st) : launch_step<float>(d, in, q, k, v, state, o, st);
 }
 
-cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, cudaStream_t st) {
+cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks, int width, void *out, Chain chain, cudaStream_t st) {
     const long long rows = (long long)d.B * d.T * d.Hk, each = 256 / (width / 4) * kSumRows, grid = (rows + each - 1) / each;
     const int group = d.H / d.Hk;
     if (d.dtype == SDM_BF16)
-        return chain_launch(true, k_linear_sum<__nv_bfloat16>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<__nv_bfloat16 *>(out));
-    return chain_launch(true, k_linear_sum<float>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<float *>(out));
+        return chain_launch(chain, k_linear_sum<__nv_bfloat16>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<__nv_bfloat16 *>(out), chain);
+    return chain_launch(chain, k_linear_sum<float>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<float *>(out), chain);
 }
 
 }  // namespace sdm
