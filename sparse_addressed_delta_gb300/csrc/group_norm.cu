@@ -18,8 +18,17 @@ namespace sdm {
 namespace {
 
 constexpr int kGroupThreads = 256, kGroupSm = 3, kGroupBatch = 8, kGroupMaxCols = 16384, kGroupRowCols = 8192;
-// an SM's threads of the forward over rows, 128 registers each (1024 of 64: 145 us for 32768 x 4096 bfloat16 where this took 123)
-constexpr int kGroupRowThreads = 512;
+// An SM's threads over rows, in blocks of several rows (rows as wide as a block and wider: 512, 16384 x 4096 bfloat16 in one
+// group 61 us, one block of 256 113). With the activation the issue of instructions bounds them and more threads help as long
+// as they fit the registers, without it memory does and fewer rows at once are read in better order. 32768 x 4096 in 32
+// groups, forward: bfloat16 with silu 640 / 512 / 384 threads 95 / 89 / 101 us, without 98 / 98 / 85; half as many of float32 89 /
+// 99 / 122 and 88 / 88 / 90. Backward: bfloat16 with silu 512 / 384 / 256 threads (up to 168 registers each, so 512 end in
+// a second wave) 150 / 138 / 161 us, without 146 / 142 / 132; float32 176 / 133 / 178 and 131 / 129 / 131.
+template <typename T>
+constexpr int group_row_threads(bool block, bool act) {
+    return block ? 512 : !act ? 384 : sizeof(T) == 4 ? 640 : 512;
+}
+int group_back_threads(bool block, bool act) { return block ? 512 : act ? 384 : 256; }
 
 // The sigmoid. bfloat16: by the approximate exponential and reciprocal instructions, within 2^-20 of it where it is not
 // negligible, far inside the results' rounding of 2^-8; the exact ones would bound the kernel (25 instructions an
@@ -197,7 +206,7 @@ __device__ __forceinline__ void store_pairs(T *row, int t, int tpr, int c, const
 }
 
 template <typename T, int VEC, int NV, bool BLOCK, bool ACT>
-__global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock, kGroupRowThreads / (BLOCK ? 512 : kNormBlock))
+__global__ void __launch_bounds__(BLOCK ? 512 : kNormBlock, group_row_threads<T>(BLOCK, ACT) / (BLOCK ? 512 : kNormBlock))
     k_group_row(const __grid_constant__ GroupShape s, const T *x, int tpr, T *y, float2 *stats) {
     constexpr int E = VEC * NV, ST = kNormStages<T>;
     extern __shared__ __align__(16) unsigned char ring_smem[];
@@ -723,8 +732,8 @@ struct GroupBack {
     bool same;
     long long blocks, parts;
 };
-GroupBack group_back(const NormGeom &g, long long N, int G) {
-    const int per_sm = g.threads >= 512 ? 1 : 512 / g.threads;
+GroupBack group_back(const NormGeom &g, long long N, int G, bool act) {
+    const int per_sm = group_back_threads(g.block, act) / g.threads;
     const long long few = N * G / g.rpb / kNormRowsBlock;
     const long long fill = (long long)kRefSms * per_sm, most = few > kRefSms ? few : kRefSms, cap = fill < most ? fill : most;
     if (N < g.rpb) {
@@ -761,7 +770,7 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
             const size_t smem = GroupRing<T, VEC, NV, 1, false>::bytes(g.threads);
             auto go = [&](auto kern) {
                 group_smem(kern, smem);
-                const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (kGroupRowThreads / g.threads));
+                const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (group_row_threads<T>(g.block, ACT) / g.threads));
                 kern<<<(unsigned)grid, g.threads, smem, st>>>(s, x, g.tpr, y, stats);
             };
             if (g.block) go(k_group_row<T, VEC, NV, true, ACT>);
@@ -791,7 +800,7 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
             const NormGeom g = norm_geom(each, VEC, true);
             constexpr int NV = 16 / VEC;
             const size_t smem = GroupRing<T, VEC, NV, 2, true>::bytes(g.threads);
-            const GroupBack to = group_back(g, s.N, s.G);
+            const GroupBack to = group_back(g, s.N, s.G, ACT);
             const size_t cols = g.block ? 0 : (size_t)2 * kNormBlock * 16 * 4;
             auto go = [&](auto kern) {
                 const size_t bytes = smem > cols ? smem : cols;
@@ -834,9 +843,9 @@ size_t group_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 size_t group_part_bytes(long long N, long long L, int C, int G, bool back) {
     if (group_rows(L, C / G)) {
         if (!back) return 0;
-        // every vector width has the same blocks
+        // every vector width has the same blocks, without an activation there are no more of them
         const NormGeom g = norm_geom(C / G, 1, true);
-        return group_up((size_t)group_back(g, N, G).parts * 2 * C * 4);
+        return group_up((size_t)group_back(g, N, G, true).parts * 2 * C * 4);
     }
     const size_t pieces = (size_t)N * group_splits(N, L);
     // (a forward that keeps no statistics: those of the whole samples behind the splits')

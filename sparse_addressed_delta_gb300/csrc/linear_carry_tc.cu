@@ -7,8 +7,8 @@
 // three planes with six of their products (NP = 3). Warps 0..15 compute (lanes 32 (warp % 4).., quarter warp / 4 of the
 // tokens and of the columns), warp 16 issues the products, warp 17 loads.
 //
-// Bound by the issue of instructions (72 % of its cycles): splitting the decayed keys in three planes and adding a product to
-// the state, 0.86 us a chunk, near the copies' own time. 16384 tokens, 32 heads of 128 x 128, three of four segments:
+// Bound by the threads' work (the issue of instructions is busy 59 % of its cycles, the tensor pipe 47 %): splitting the decayed
+// keys in three planes and adding a product to the state, 0.86 us a chunk, near the copies' own time. 16384 tokens, 32 heads of 128 x 128, three of four segments:
 // 55 us on 96 SMs, where the copies alone, as deep, take 42 (4.7 TB/s). Warps that take even and odd chunks instead of
 // quarters of each 65.6 (63 then), the copies awaited one after the other 80.
 #include <type_traits>
