@@ -18,6 +18,7 @@ namespace sdm {
 namespace {
 
 constexpr int kGroupThreads = 256, kGroupSm = 3, kGroupBatch = 8, kGroupMaxCols = 16384, kGroupRowCols = 8192;
+constexpr int kSmallMany = 4, kSmallBack = 2, kSmallBlocks = 2 * kRefSms;   // vectors a thread of small samples; the backward's blocks
 // An SM's threads over rows, in blocks of several rows (rows as wide as a block and wider: 512, 16384 x 4096 bfloat16 in one
 // group 61 us, one block of 256 113). With the activation the issue of instructions bounds them and more threads help as long
 // as they fit the registers, without it memory does and fewer rows at once are read in better order. 32768 x 4096 in 32
@@ -409,6 +410,13 @@ struct Piece {
     }
 };
 
+template <typename T, int VEC>
+__device__ __forceinline__ void load_params(const void *p, bool f32, float fill, int c0, float (&o)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+        o[j] = !p ? fill : f32 ? static_cast<const float *>(p)[c0 + j] : to_f32(static_cast<const T *>(p)[c0 + j]);
+}
+
 // part [N][splits][G]: mean and sum of squares around it
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const __grid_constant__ GroupShape s, const T *x, float2 *part) {
@@ -486,13 +494,6 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_join(const __grid_const
         return Moments{(float)(s.per + (k < s.more)) * c, e.x, e.y};
     });
     if ((threadIdx.x & 31) == 0) joined[i] = make_float2(a.x, 1.f / sqrtf(a.y / all + s.eps));
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void load_params(const void *p, bool f32, float fill, int c0, float (&o)[VEC]) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-        o[j] = !p ? fill : f32 ? static_cast<const float *>(p)[c0 + j] : to_f32(static_cast<const T *>(p)[c0 + j]);
 }
 
 template <typename T, int VEC, bool ACT>
@@ -697,6 +698,181 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
     }
 }
 
+// ---- small samples ------------------------------------------------------------------------------
+
+// Samples of a few vectors: a block takes several whole ones into registers, MANY vectors a thread, so that they are read
+// once and one launch does all. A thread's vectors lie at the same channels in every turn.
+template <typename T, int VEC, int MANY>
+struct Small {
+    int cv, vectors, ev, all;            // vectors of a position, of a sample, of a group's channels; of the block's samples
+    long long from[MANY];                // this thread's, from the block's first sample on, in x
+    int at[MANY];                        // sample of the block and group, (.. G + g); -1: none
+    __device__ Small(const GroupShape &s, int samples)
+        : cv(s.C / VEC), vectors((int)s.L * cv), ev(cv / s.G), all(samples * vectors) {
+#pragma unroll
+        for (int k = 0; k < MANY; ++k) {
+            const int i = (int)threadIdx.x + k * kGroupThreads, n = i / vectors, v = i % vectors;
+            from[k] = (n * s.L + v / cv) * s.xs + v % cv * VEC;
+            at[k] = i < all ? n * s.G + v % cv / ev : -1;
+        }
+    }
+    // a sample's group, e-th vector
+    __device__ __forceinline__ int entry(int n, int g, int e) const { return n * vectors + e / ev * cv + g * ev + e % ev; }
+};
+
+template <typename T, int VEC, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads, 2) k_group_small(const __grid_constant__ GroupShape s, const T *x, int samples, T *y, float2 *stats) {
+    extern __shared__ float2 acc[];                      // [vectors] mean and squares around it; [samples][G] mean and rstd
+    const Small<T, VEC, kSmallMany> m(s, samples);
+    float2 *joined = acc + m.all;
+    const float all = (float)s.L * (float)(s.C / s.G);
+    for (long long n0 = (long long)blockIdx.x * samples; n0 < s.N; n0 += (long long)gridDim.x * samples) {
+        const T *base = x + n0 * s.L * s.xs;
+        const int live = (int)(s.N - n0 < samples ? s.N - n0 : samples) * s.G;
+        Vec<T, VEC> raw[kSmallMany];
+#pragma unroll
+        for (int k = 0; k < kSmallMany; ++k)
+            raw[k] = m.at[k] >= 0 && m.at[k] < live ? __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + m.from[k])) : Vec<T, VEC>{};
+#pragma unroll
+        for (int k = 0; k < kSmallMany; ++k) {
+            float v[VEC], mean = 0.f, q = 0.f;
+            unpack<T, VEC>(raw[k], v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) mean += v[j];
+            mean *= 1.f / VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) q = fmaf(v[j] - mean, v[j] - mean, q);
+            if (m.at[k] >= 0) acc[threadIdx.x + k * kGroupThreads] = make_float2(mean, VEC > 1 ? q : 0.f);
+        }
+        __syncthreads();
+        for (int p0 = 0; p0 < live; p0 += kGroupThreads / 8) {
+            const int p = p0 + (int)(threadIdx.x >> 3), n = p / s.G, g = p % s.G;
+            const float2 a = join_parts<8>(p < live ? (int)s.L * m.ev : 0, all, [&](int e) {
+                const float2 part = acc[m.entry(n, g, e)];
+                return Moments{(float)VEC, part.x, part.y};
+            });
+            if (p < live && (threadIdx.x & 7) == 0) {
+                joined[p] = make_float2(a.x, 1.f / sqrtf(a.y / all + s.eps));
+                if (stats) stats[n0 * s.G + p] = joined[p];
+            }
+        }
+        __syncthreads();
+        T *out = y + n0 * s.L * s.C;
+#pragma unroll
+        for (int k = 0; k < kSmallMany; ++k) {
+            if (m.at[k] < 0 || m.at[k] >= live) continue;
+            const int i = threadIdx.x + k * kGroupThreads;
+            const float2 a = joined[m.at[k]];
+            float v[VEC], w[VEC], b[VEC];
+            unpack<T, VEC>(raw[k], v);
+            load_params<T, VEC>(s.w, s.wf32, 1.f, i % m.cv * VEC, w);
+            load_params<T, VEC>(s.b, s.wf32, 0.f, i % m.cv * VEC, b);
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) {
+                constexpr bool TWO = VEC > 1;
+                float2 z = mul2(add2(make_float2(v[j], TWO ? v[j + 1] : 0.f), both(-a.x)), both(a.y));
+                z = activate<T, ACT>(fma2(z, make_float2(w[j], TWO ? w[j + 1] : 0.f), make_float2(b[j], TWO ? b[j + 1] : 0.f)));
+                v[j] = z.x;
+                if constexpr (TWO) v[j + 1] = z.y;
+            }
+            store_vec<T, VEC>(out + (long long)i * VEC, v);
+        }
+    }
+}
+
+// part [blocks][2][C], where it is wanted: column sums of dz xhat and of dz
+template <typename T, int VEC, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads, 2)
+    k_group_small_bwd(const __grid_constant__ GroupShape s, const T *dy, const T *x, int samples, const float2 *stats, T *dx, float *part) {
+    // [vectors] terms, [samples][G] their means; in the end [2][vectors][VEC], sums
+    extern __shared__ __align__(16) float2 terms[];
+    chain_next();
+    const Small<T, VEC, kSmallBack> m(s, samples);
+    float2 *means = terms + m.all;
+    const float count = (float)s.L * (float)(s.C / s.G);
+    float sw[kSmallBack][VEC], sb[kSmallBack][VEC];
+#pragma unroll
+    for (int k = 0; k < kSmallBack; ++k)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sw[k][j] = sb[k][j] = 0.f;
+    for (long long n0 = (long long)blockIdx.x * samples; n0 < s.N; n0 += (long long)gridDim.x * samples) {
+        const T *base = x + n0 * s.L * s.xs, *gbase = dy + n0 * s.L * s.gs;
+        const int live = (int)(s.N - n0 < samples ? s.N - n0 : samples) * s.G;
+        float h[kSmallBack][VEC], d[kSmallBack][VEC];      // xhat and w dz
+        float2 a[kSmallBack];
+#pragma unroll
+        for (int k = 0; k < kSmallBack; ++k) {
+            const int i = threadIdx.x + k * kGroupThreads, v = i % m.vectors;
+            Vec<T, VEC> rx{}, rg{};
+            a[k] = both(0.f);
+            if (m.at[k] >= 0 && m.at[k] < live) {
+                rx = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + m.from[k]));
+                rg = __ldg(reinterpret_cast<const Vec<T, VEC> *>(gbase + (i / m.vectors * s.L + v / m.cv) * s.gs + v % m.cv * VEC));
+                a[k] = stats[n0 * s.G + m.at[k]];
+            }
+            unpack<T, VEC>(rx, h[k]);
+            unpack<T, VEC>(rg, d[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kSmallBack; ++k) {
+            const int i = threadIdx.x + k * kGroupThreads;
+            if (m.at[k] < 0) continue;
+            float w[VEC], b[VEC];
+            load_params<T, VEC>(s.w, s.wf32, 1.f, i % m.cv * VEC, w);
+            load_params<T, VEC>(s.b, s.wf32, 0.f, i % m.cv * VEC, b);
+            float2 mine = both(0.f);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                h[k][j] = (h[k][j] - a[k].x) * a[k].y;
+                const float t = back<T, ACT>(make_float2(d[k][j], 0.f), make_float2(fmaf(h[k][j], w[j], b[j]), 0.f)).x;
+                sw[k][j] = fmaf(t, h[k][j], sw[k][j]);
+                sb[k][j] += t;
+                d[k][j] = t * w[j];
+                mine = fma2(make_float2(1.f, h[k][j]), both(d[k][j]), mine);
+            }
+            terms[i] = mine;
+        }
+        __syncthreads();
+        for (int p0 = 0; p0 < live; p0 += kGroupThreads / 8) {
+            const int p = p0 + (int)(threadIdx.x >> 3), n = p / s.G, g = p % s.G;
+            float2 t = both(0.f);
+            if (p < live)
+                for (int e = threadIdx.x & 7; e < (int)s.L * m.ev; e += 8) t = add2(t, terms[m.entry(n, g, e)]);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) t = add2(t, make_float2(__shfl_xor_sync(~0u, t.x, o), __shfl_xor_sync(~0u, t.y, o)));
+            if (p < live && (threadIdx.x & 7) == 0) means[p] = make_float2(t.x / count, t.y / count);
+        }
+        __syncthreads();
+        T *out = dx + n0 * s.L * s.C;
+#pragma unroll
+        for (int k = 0; k < kSmallBack; ++k) {
+            if (m.at[k] < 0 || m.at[k] >= live) continue;
+            const float2 t = means[m.at[k]];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) d[k][j] = a[k].y * fmaf(-h[k][j], t.y, d[k][j] - t.x);
+            store_vec<T, VEC>(out + (long long)(threadIdx.x + k * kGroupThreads) * VEC, d[k]);
+        }
+    }
+    if (!part) return;
+    float *cols = reinterpret_cast<float *>(terms);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSmallBack; ++k) {
+        const int i = threadIdx.x + k * kGroupThreads;
+        if (m.at[k] < 0) continue;
+        store_vec<float, VEC>(cols + (long long)i * VEC, sw[k]);
+        store_vec<float, VEC>(cols + (long long)(m.all + i) * VEC, sb[k]);
+    }
+    __syncthreads();
+    float *out = part + (size_t)blockIdx.x * 2 * s.C;
+    for (int c = threadIdx.x; c < 2 * s.C; c += kGroupThreads) {
+        const float *from = cols + (c < s.C ? c : m.all * VEC + c - s.C);
+        float t = 0.f;
+        for (int i = 0; i < m.all * VEC; i += s.C) t += from[i];
+        out[c] = t;
+    }
+}
+
 // ---- which form, and its launches ---------------------------------------------------------------
 
 // Blocks of a sample: kGroupSm an SM in all, 8 positions at least each. kGroupSm 3, of 80 registers: 8 x 4096 x 512 bfloat16
@@ -724,6 +900,13 @@ long long group_grid(long long rows, int rpb, int G, long long most) {
 // form, one position a block: 1056 and 1130), 1024 x 8192 of 8 10 and 33 (64 and 82). The registers end at 8192 columns
 // (512 threads of 16 elements).
 bool group_rows(long long L, int each) { return L == 1 && each <= kGroupRowCols; }
+// Samples that a block of `many` vectors a thread takes whole, in one launch; 0: they are too large. Wherever they fit,
+// forward and backward: 31337 x 10 x 8 bfloat16 15 and 17 us (split, a block a sample: 754 and 482), 1000 x 8 x 512 15 and 18
+// (27 and 36), 300 x 9 x 40 4.6 and 7.0 (9.5 and 9.1).
+int group_small(long long N, long long L, int C, int vec, int many) {
+    const long long vectors = L * (C / vec), fit = many * kGroupThreads / (vectors ? vectors : 1), spread = (N + kSmallBlocks - 1) / kSmallBlocks;
+    return (int)(fit < spread ? fit : spread);
+}
 
 // The backward's blocks over rows, and how many partials of the column sums they leave. `same`: all rows of a block are
 // of one group and joined before they leave, as soon as there are samples enough for a block (32768 x 256 of 16 groups 29 us,
@@ -778,6 +961,12 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
             return;
         }
         const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+        if (const int samples = group_small(s.N, s.L, s.C, VEC, kSmallMany)) {
+            const size_t smem = (size_t)samples * ((size_t)s.L * cv + s.G) * 8;
+            const long long need = (s.N + samples - 1) / samples, most = 2 * kSmallBlocks;
+            k_group_small<T, VEC, ACT><<<(unsigned)(need < most ? need : most), kGroupThreads, smem, st>>>(s, x, samples, y, stats);
+            return;
+        }
         const unsigned grid = (unsigned)(s.N * s.splits);
         const size_t smem = (size_t)slots * cv * 8;
         group_smem(k_group_stats<T, VEC>, smem);
@@ -813,6 +1002,14 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
             return;
         }
         const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+        if (const int samples = group_small(s.N, s.L, s.C, VEC, kSmallBack)) {
+            const size_t vectors = (size_t)samples * s.L * cv, one = (vectors + (size_t)samples * s.G) * 8, two = vectors * VEC * 8;
+            const long long need = (s.N + samples - 1) / samples, blocks = need < kSmallBlocks ? need : kSmallBlocks;
+            k_group_small_bwd<T, VEC, ACT><<<(unsigned)blocks, kGroupThreads, one > two ? one : two, st>>>(s, dy, x, samples, stats, dx, sums ? part : nullptr);
+            if (sums)
+                chain_launch(Chain::behind, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)blocks, s.C, dw, db);
+            return;
+        }
         const unsigned grid = (unsigned)(s.N * s.splits);
         const size_t smem = (size_t)slots * cv * 8 + (slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0);
         group_smem(k_group_sums<T, VEC, ACT>, smem);
