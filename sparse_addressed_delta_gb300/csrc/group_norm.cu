@@ -4,11 +4,12 @@
 //   dz = dy act'(z);  dx = rstd (w dz - mean(w dz) - xhat mean(w dz xhat));  dw = sum dz xhat;  db = sum dz
 // All arithmetic is float32; y and dx are rounded once.
 //
-// Two forms. One position a sample (a token's heads): a group is a row of C / G elements, kept in registers, read
+// Three forms. One position a sample (a token's heads): a group is a row of C / G elements, kept in registers, read
 // once (k_group_row*): a row belongs to a part of a warp or to a block, blocks walk over the samples with a stride
-// that keeps every thread at its group, so weights and column sums stay in registers. More positions, or rows past
-// the registers: a sample's positions are split over blocks, each thread at its channels; a first launch makes every
-// split's statistics (or column sums), the second joins them and reads the rows again, from L2 where they fit.
+// that keeps every thread at its group, so weights and column sums stay in registers. Small samples: several of them
+// whole in a block's registers (k_group_small*). Else a sample's positions are split over blocks, each thread at its
+// channels: a first launch makes every split's statistics (or column sums and terms), the second joins them, the third
+// reads the rows again, from L2 where they fit.
 #include <type_traits>
 
 #include "norm_rows.cuh"
@@ -417,10 +418,13 @@ __device__ __forceinline__ void load_params(const void *p, bool f32, float fill,
         o[j] = !p ? fill : f32 ? static_cast<const float *>(p)[c0 + j] : to_f32(static_cast<const T *>(p)[c0 + j]);
 }
 
+// The vectors of the kernels below are parts of a group, or (OWN) groups end inside them: then every channel has a group, a
+// partial and statistics of its own. 4000 x 64 x 128 bfloat16 in 32 groups: @.
+
 // part [N][splits][G]: mean and sum of squares around it
-template <typename T, int VEC>
+template <typename T, int VEC, bool OWN>
 __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const __grid_constant__ GroupShape s, const T *x, float2 *part) {
-    extern __shared__ float2 acc[];                      // [slots][cv]
+    extern __shared__ float2 acc[];                      // [slots][cv], of channels (OWN) [slots][C]
     chain_next();
     const Piece p(s);
     const Spread sp(s.C, VEC);
@@ -428,6 +432,7 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const _
     const T *base = x + p.n * s.L * s.xs;
     for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += kGroupThreads) {
         Moments m{0.f, 0.f, 0.f};
+        float mean[OWN ? VEC : 1] = {}, m2[OWN ? VEC : 1] = {};
         if (slot >= 0 || sp.slots == 1) {
             const T *col = base + cv * VEC;
             for (long long r = p.from + (sp.slots > 1 ? slot : 0); r < p.to; r += (long long)sp.slots * kGroupBatch) {
@@ -441,8 +446,29 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const _
                     raw[i] = Vec<T, VEC>{};
                     if (at < p.to) {
                         raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(col + at * s.xs));
-                        count += VEC;
+                        count += OWN ? 1 : VEC;
                     }
+                }
+                if constexpr (OWN) {                               // as below, a channel at a time
+                    const float f = __fdividef(count, m.n + count), by = 1.f / count;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        float v[kGroupBatch], t = 0.f, q = 0.f;
+#pragma unroll
+                        for (int i = 0; i < kGroupBatch; ++i) {
+                            v[i] = to_f32(reinterpret_cast<const T *>(raw + i)[j]);
+                            t += v[i];
+                        }
+                        t *= by;
+#pragma unroll
+                        for (int i = 0; i < kGroupBatch; ++i)
+                            if (r + (long long)i * sp.slots < p.to) q = fmaf(v[i] - t, v[i] - t, q);
+                        const float d = m.n > 0.f ? t - mean[j] : 0.f;
+                        mean[j] = m.n > 0.f ? fmaf(d, f, mean[j]) : t;
+                        m2[j] += fmaf(d * d, m.n * f, q);
+                    }
+                    m.n += count;
+                    continue;
                 }
                 auto each_pair = [&](auto f) {
 #pragma unroll
@@ -463,19 +489,26 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_stats(const _
                 m.join(count, mean, q.x + q.y);
             }
         }
-        if (slot >= 0 || sp.slots == 1) acc[(sp.slots > 1 ? slot : 0) * sp.cv + cv] = make_float2(m.mean, m.m2);
+        if (slot >= 0 || sp.slots == 1) {
+            const int at = (sp.slots > 1 ? slot : 0) * sp.cv + cv;
+            if constexpr (OWN)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) acc[at * VEC + j] = make_float2(mean[j], m2[j]);
+            else acc[at] = make_float2(m.mean, m.m2);
+        }
         if (sp.slots > 1) break;
     }
     __syncthreads();
-    const int each = sp.cv / s.G;
+    constexpr int PART = OWN ? 1 : VEC;                            // channels of a partial
+    const int each = s.C / PART / s.G, line = s.C / PART;
     const long long rows = p.to - p.from;
     const float all = (float)rows * (float)(s.C / s.G);
     for (int g0 = 0; g0 < s.G; g0 += kGroupThreads / 8) {
         const int g = g0 + (threadIdx.x >> 3);
         const float2 a = join_parts<8>(g < s.G ? each * sp.slots : 0, all, [&](int i) {
             const int sl = i / each;
-            const float2 e = acc[sl * sp.cv + g * each + i % each];
-            return Moments{(float)((rows > sl ? (rows - sl + sp.slots - 1) / sp.slots : 0) * VEC), e.x, e.y};
+            const float2 e = acc[sl * line + g * each + i % each];
+            return Moments{(float)((rows > sl ? (rows - sl + sp.slots - 1) / sp.slots : 0) * PART), e.x, e.y};
         });
         if (g < s.G && (threadIdx.x & 7) == 0) part[((size_t)p.n * s.splits + p.split) * s.G + g] = a;
     }
@@ -496,8 +529,8 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_join(const __grid_const
     if ((threadIdx.x & 31) == 0) joined[i] = make_float2(a.x, 1.f / sqrtf(a.y / all + s.eps));
 }
 
-template <typename T, int VEC, bool ACT>
-__global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_apply(const __grid_constant__ GroupShape s, const T *x, const float2 *stats, T *y) {
+template <typename T, int VEC, bool OWN, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads, OWN ? 2 : kGroupSm) k_group_apply(const __grid_constant__ GroupShape s, const T *x, const float2 *stats, T *y) {
     const Piece p(s);
     const Spread sp(s.C, VEC);
     const int slot = sp.slots > 1 ? threadIdx.x / sp.cv : 0, each = s.C / s.G;
@@ -520,7 +553,9 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_apply(const _
         load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
         load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
         chain_wait();
-        const float2 a = stats[p.n * s.G + c0 / each];
+        float2 a[OWN ? VEC : 1];
+#pragma unroll
+        for (int j = 0; j < (OWN ? VEC : 1); ++j) a[j] = stats[p.n * s.G + (c0 + j) / each];
         for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * kGroupBatch) {
 #pragma unroll
             for (int i = 0; i < kGroupBatch; ++i) {
@@ -533,7 +568,8 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_apply(const _
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
                     float2 z = make_float2(v[j], j + 1 < VEC ? v[j + 1] : 0.f);
-                    z = mul2(add2(z, both(-a.x)), both(a.y));
+                    if constexpr (OWN) z = mul2(add2(z, make_float2(-a[j].x, -a[j + 1].x)), make_float2(a[j].y, a[j + 1].y));
+                    else z = mul2(add2(z, both(-a[0].x)), both(a[0].y));
                     z = activate<T, ACT>(fma2(z, make_float2(w[j], j + 1 < VEC ? w[j + 1] : 0.f), make_float2(b[j], j + 1 < VEC ? b[j + 1] : 0.f)));
                     v[j] = z.x;
                     if (j + 1 < VEC) v[j + 1] = z.y;
@@ -546,8 +582,8 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm) k_group_apply(const _
 
 // part [N][splits][2][C], where it is wanted: column sums of dz xhat and of dz; terms [N][splits][G]: sums over a group of
 // w dz and of w dz xhat
-template <typename T, int VEC, bool ACT>
-__global__ void __launch_bounds__(kGroupThreads, kGroupSm)
+template <typename T, int VEC, bool OWN, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads, OWN ? 2 : kGroupSm)
     k_group_sums(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, float *part, float2 *terms) {
     extern __shared__ __align__(16) float sums[];        // [slots][2][C] where there are several slots; then [slots][cv] a thread's terms
     chain_next();
@@ -560,7 +596,9 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
     if (slot < sp.slots)
         for (int cv = sp.slots > 1 ? threadIdx.x % sp.cv : threadIdx.x; cv < sp.cv; cv += sp.slots > 1 ? sp.cv : kGroupThreads) {
             const int c0 = cv * VEC;
-            const float2 a = stats[p.n * s.G + c0 / each];
+            float2 a[OWN ? VEC : 1];
+#pragma unroll
+            for (int j = 0; j < (OWN ? VEC : 1); ++j) a[j] = stats[p.n * s.G + (c0 + j) / each];
             float w[VEC], b[VEC], sw[VEC], sb[VEC];
             load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
             load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
@@ -586,7 +624,9 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
 #pragma unroll
                     for (int j = 0; j < VEC; j += 2) {   // where no position is, dy is 0
                         constexpr bool TWO = VEC > 1;
-                        float2 z = mul2(add2(make_float2(h[j], TWO ? h[j + 1] : 0.f), both(-a.x)), both(a.y));
+                        float2 z = make_float2(h[j], TWO ? h[j + 1] : 0.f);
+                        if constexpr (OWN) z = mul2(add2(z, make_float2(-a[j].x, -a[j + 1].x)), make_float2(a[j].y, a[j + 1].y));
+                        else z = mul2(add2(z, both(-a[0].x)), both(a[0].y));
                         const float2 t = back<T, ACT>(make_float2(d[j], TWO ? d[j + 1] : 0.f),
                                                       fma2(z, make_float2(w[j], TWO ? w[j + 1] : 0.f), make_float2(b[j], TWO ? b[j + 1] : 0.f)));
                         sw[j] = fmaf(t.x, z.x, sw[j]);
@@ -600,21 +640,23 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
             }
             float2 mine = both(0.f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) mine = fma2(make_float2(sb[j], sw[j]), both(w[j]), mine);
+            for (int j = 0; j < VEC; ++j)
+                if constexpr (OWN) pairs[slot * s.C + c0 + j] = make_float2(sb[j] * w[j], sw[j] * w[j]);
+                else mine = fma2(make_float2(sb[j], sw[j]), both(w[j]), mine);
             if (out) {
                 float *to = (sp.slots > 1 ? sums + (size_t)slot * 2 * s.C : out) + c0;
                 store_vec<float, VEC>(to, sw);
                 store_vec<float, VEC>(to + s.C, sb);
             }
-            pairs[slot * sp.cv + cv] = mine;
+            if constexpr (!OWN) pairs[slot * sp.cv + cv] = mine;
         }
     __syncthreads();
-    const int wide = sp.cv / s.G;
+    const int line = OWN ? s.C : sp.cv, wide = line / s.G;
     for (int g0 = 0; g0 < s.G; g0 += kGroupThreads / 8) {
         const int g = g0 + (threadIdx.x >> 3);
         float2 a = both(0.f);
         if (g < s.G)
-            for (int i = threadIdx.x & 7; i < wide * sp.slots; i += 8) a = add2(a, pairs[i / wide * sp.cv + g * wide + i % wide]);
+            for (int i = threadIdx.x & 7; i < wide * sp.slots; i += 8) a = add2(a, pairs[i / wide * line + g * wide + i % wide]);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) a = add2(a, make_float2(__shfl_xor_sync(~0u, a.x, o), __shfl_xor_sync(~0u, a.y, o)));
         if (g < s.G && (threadIdx.x & 7) == 0) terms[((size_t)p.n * s.splits + p.split) * s.G + g] = a;
@@ -648,8 +690,8 @@ __global__ void __launch_bounds__(kGroupTermThreads) k_group_terms(const __grid_
     if ((threadIdx.x & 31) == 0) terms[i] = make_float2(a.x / count, a.y / count);
 }
 
-template <typename T, int VEC, bool ACT>
-__global__ void __launch_bounds__(kGroupThreads, kGroupSm)
+template <typename T, int VEC, bool OWN, bool ACT>
+__global__ void __launch_bounds__(kGroupThreads, OWN ? 2 : kGroupSm)
     k_group_apply_bwd(const __grid_constant__ GroupShape s, const T *dy, const T *x, const float2 *stats, const float2 *terms, T *dx) {
     const Piece p(s);
     const Spread sp(s.C, VEC);
@@ -663,7 +705,12 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
         load_params<T, VEC>(s.w, s.wf32, 1.f, c0, w);
         load_params<T, VEC>(s.b, s.wf32, 0.f, c0, b);
         chain_wait();
-        const float2 a = stats[p.n * s.G + c0 / each], m = terms[p.n * s.G + c0 / each];
+        float2 a[OWN ? VEC : 1], m[OWN ? VEC : 1];
+#pragma unroll
+        for (int j = 0; j < (OWN ? VEC : 1); ++j) {
+            a[j] = stats[p.n * s.G + (c0 + j) / each];
+            m[j] = __ldcg(terms + p.n * s.G + (c0 + j) / each);
+        }
         constexpr int BATCH = 4;
         for (long long r = p.from + slot; r < p.to; r += (long long)sp.slots * BATCH) {
             Vec<T, VEC> rx[BATCH], rg[BATCH];
@@ -686,9 +733,12 @@ __global__ void __launch_bounds__(kGroupThreads, kGroupSm)
                 for (int j = 0; j < VEC; j += 2) {
                     constexpr bool TWO = VEC > 1;
                     const float2 wj = make_float2(w[j], TWO ? w[j + 1] : 0.f);
-                    const float2 z = mul2(add2(make_float2(h[j], TWO ? h[j + 1] : 0.f), both(-a.x)), both(a.y));
+                    constexpr int J = OWN ? 1 : 0;                 // (the pair's statistics: their own or the vector's)
+                    const float2 a0 = a[J * j], a1 = a[J * (j + 1)], m0 = m[J * j], m1 = m[J * (j + 1)];
+                    const float2 rstd = make_float2(a0.y, a1.y);
+                    const float2 z = mul2(add2(make_float2(h[j], TWO ? h[j + 1] : 0.f), make_float2(-a0.x, -a1.x)), rstd);
                     float2 t = mul2(back<T, ACT>(make_float2(d[j], TWO ? d[j + 1] : 0.f), fma2(z, wj, make_float2(b[j], TWO ? b[j + 1] : 0.f))), wj);
-                    t = mul2(both(a.y), fma2(z, both(-m.y), add2(t, both(-m.x))));
+                    t = mul2(rstd, fma2(z, make_float2(-m0.y, -m1.y), add2(t, make_float2(-m0.x, -m1.x))));
                     d[j] = t.x;
                     if constexpr (TWO) d[j + 1] = t.y;
                 }
@@ -942,8 +992,46 @@ void group_by_vec(int vec, F f) {
     f(std::integral_constant<int, 1>{});
 }
 
+// Whether channels have statistics of their own, so that the loads are wide: a block's end costs more then, so it pays from 16
+// rows a thread on. Forward and backward, so and by narrow vectors: 24 rows, 2 x 16384 x 640 bfloat16 in 32 groups 47 and 88 us
+// (63 and 96), 8 x 4096 x 320 float32 37 and 72 (73 and 106); 12 rows, the latter in bfloat16 28 and 46 (25 and 40); 4 rows,
+// 8 x 4096 x 128 20 and 28 (14 and 18).
+bool group_own(const GroupShape &s, int vec) {
+    const int cv = s.C / vec;
+    return s.per >= 16LL * (cv < kGroupThreads ? kGroupThreads / cv : 1);
+}
+
+template <typename T, int VEC, bool OWN, bool ACT>
+void group_forward_split(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, cudaStream_t st) {
+    const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+    const unsigned grid = (unsigned)(s.N * s.splits);
+    const size_t smem = (size_t)slots * cv * (OWN ? VEC : 1) * 8;
+    group_smem(k_group_stats<T, VEC, OWN>, smem);
+    k_group_stats<T, VEC, OWN><<<grid, kGroupThreads, smem, st>>>(s, x, part);
+    float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
+    const long long warps = s.N * s.G;
+    chain_launch(Chain::behind, k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
+    chain_launch(Chain::behind, k_group_apply<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
+}
+
+template <typename T, int VEC, bool OWN, bool ACT>
+void group_backward_split(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, float *dw, float *db, float *part, float2 *terms,
+                          cudaStream_t st) {
+    const bool sums = dw || db;
+    const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+    const unsigned grid = (unsigned)(s.N * s.splits);
+    const size_t smem = (size_t)slots * cv * (OWN ? VEC : 1) * 8 + (slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0);
+    group_smem(k_group_sums<T, VEC, OWN, ACT>, smem);
+    float2 *split_terms = terms + s.N * s.G;
+    k_group_sums<T, VEC, OWN, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
+    const int blocks = (int)((s.N * s.G + kGroupTermWarps - 1) / kGroupTermWarps);
+    chain_launch(Chain::behind, k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
+    chain_launch(Chain::behind, k_group_apply_bwd<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
+}
+
+// vec: of vectors that are parts of groups; wide: 16-byte vectors that are not would do
 template <typename T, bool ACT>
-void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, int vec, cudaStream_t st) {
+void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, int vec, bool wide, cudaStream_t st) {
     const int each = s.C / s.G;
     group_by_vec<T>(vec, [&](auto v) {
         constexpr int VEC = decltype(v)::value;
@@ -960,27 +1048,22 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
             else go(k_group_row<T, VEC, NV, false, ACT>);
             return;
         }
-        const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+        const int cv = s.C / VEC;
         if (const int samples = group_small(s.N, s.L, s.C, VEC, kSmallMany)) {
             const size_t smem = (size_t)samples * ((size_t)s.L * cv + s.G) * 8;
             const long long need = (s.N + samples - 1) / samples, most = 2 * kSmallBlocks;
             k_group_small<T, VEC, ACT><<<(unsigned)(need < most ? need : most), kGroupThreads, smem, st>>>(s, x, samples, y, stats);
             return;
         }
-        const unsigned grid = (unsigned)(s.N * s.splits);
-        const size_t smem = (size_t)slots * cv * 8;
-        group_smem(k_group_stats<T, VEC>, smem);
-        k_group_stats<T, VEC><<<grid, kGroupThreads, smem, st>>>(s, x, part);
-        float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
-        const long long warps = s.N * s.G;
-        chain_launch(Chain::behind, k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
-        chain_launch(Chain::behind, k_group_apply<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
+        constexpr int V16 = 16 / (int)sizeof(T);
+        if (VEC < V16 && wide && group_own(s, V16)) group_forward_split<T, V16, true, ACT>(s, x, y, stats, part, st);
+        else group_forward_split<T, VEC, false, ACT>(s, x, y, stats, part, st);
     });
 }
 
 template <typename T, bool ACT>
 void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, float *dw, float *db, float *part, float2 *terms, int vec,
-                    cudaStream_t st) {
+                    bool wide, cudaStream_t st) {
     const int each = s.C / s.G;
     const bool sums = dw || db;
     group_by_vec<T>(vec, [&](auto v) {
@@ -1001,7 +1084,7 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
             if (sums) chain_launch(Chain::behind, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
             return;
         }
-        const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
+        const int cv = s.C / VEC;
         if (const int samples = group_small(s.N, s.L, s.C, VEC, kSmallBack)) {
             const size_t vectors = (size_t)samples * s.L * cv, one = (vectors + (size_t)samples * s.G) * 8, two = vectors * VEC * 8;
             const long long need = (s.N + samples - 1) / samples, blocks = need < kSmallBlocks ? need : kSmallBlocks;
@@ -1010,14 +1093,9 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
                 chain_launch(Chain::behind, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)blocks, s.C, dw, db);
             return;
         }
-        const unsigned grid = (unsigned)(s.N * s.splits);
-        const size_t smem = (size_t)slots * cv * 8 + (slots > 1 ? (size_t)slots * 2 * s.C * 4 : 0);
-        group_smem(k_group_sums<T, VEC, ACT>, smem);
-        float2 *split_terms = terms + s.N * s.G;
-        k_group_sums<T, VEC, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
-        const int blocks = (int)((s.N * s.G + kGroupTermWarps - 1) / kGroupTermWarps);
-        chain_launch(Chain::behind, k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
-        chain_launch(Chain::behind, k_group_apply_bwd<T, VEC, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
+        constexpr int V16 = 16 / (int)sizeof(T);
+        if (VEC < V16 && wide && group_own(s, V16)) group_backward_split<T, V16, true, ACT>(s, dy, x, stats, dx, dw, db, part, terms, st);
+        else group_backward_split<T, VEC, false, ACT>(s, dy, x, stats, dx, dw, db, part, terms, st);
     });
 }
 
@@ -1092,11 +1170,12 @@ int sdm_group_norm(const void *x, long long x_stride, long long N, long long L, 
     GroupShape s{N, L, x_stride, 0, C, G, weight_dtype == SDM_F32, eps, weight, bias};
     s.split(group_splits(N, L));
     const int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, C, x, y, y);
+    const bool wide = norm_vec(dtype == SDM_BF16 ? 2 : 4, C, x_stride, C, x, y, y) == (dtype == SDM_BF16 ? 8 : 4);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto type, auto act) {
         using T = decltype(type);
         group_forward<T, decltype(act)::value>(s, static_cast<const T *>(x), static_cast<T *>(y), reinterpret_cast<float2 *>(stats),
-                                               static_cast<float2 *>(workspace), vec, st);
+                                               static_cast<float2 *>(workspace), vec, wide, st);
     };
     const bool silu = activation == SDM_ACT_SILU;
     if (dtype == SDM_BF16) silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});
@@ -1132,13 +1211,14 @@ int sdm_group_norm_backward(const void *grad, long long grad_stride, const void 
     }
     GroupShape s{N, L, x_stride, grad_stride, C, G, weight_dtype == SDM_F32, 0.f, weight, bias};
     s.split(group_splits(N, L));
-    int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, grad_stride, x, grad, grad_x);
+    const int vec = norm_vec(dtype == SDM_BF16 ? 2 : 4, C / G, x_stride, grad_stride, x, grad, grad_x);
+    const bool wide = norm_vec(dtype == SDM_BF16 ? 2 : 4, C, x_stride, grad_stride, x, grad, grad_x) == (dtype == SDM_BF16 ? 8 : 4);
     auto part = static_cast<float *>(workspace);
     auto terms = rows ? nullptr : reinterpret_cast<float2 *>(static_cast<unsigned char *>(workspace) + group_part_bytes(N, L, C, G, true));
     auto go = [&](auto type, auto act) {
         using T = decltype(type);
         group_backward<T, decltype(act)::value>(s, static_cast<const T *>(grad), static_cast<const T *>(x), reinterpret_cast<const float2 *>(stats),
-                                                static_cast<T *>(grad_x), grad_weight, grad_bias, part, terms, vec, st);
+                                                static_cast<T *>(grad_x), grad_weight, grad_bias, part, terms, vec, wide, st);
     };
     const bool silu = activation == SDM_ACT_SILU;
     if (dtype == SDM_BF16) silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});

@@ -146,6 +146,29 @@ def test_group_norm_splits(shape, groups, act, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("shape,groups", [((3, 300, 128), 32), ((2, 500, 640), 32), ((1, 130, 2056), 8), ((2, 40, 16384), 4096), ((2, 333, 36), 4),
+                                          ((2, 90, 104), 104), ((700, 40, 24), 3), ((1, 3000, 8), 4), ((500, 60, 1032), 24), ((300, 60, 2056), 257), ((2, 9000, 648), 72)], ids=str)
+def test_group_norm_groups_that_end_inside_vectors(shape, groups, act, dtype):
+    """Groups of a few channels, odd ones and single ones, where 16 bytes of a position hold several or parts of them."""
+    x, w, b, dy = tg.draw(shape, dtype, seed=sum(shape))
+    tg.check(x, groups, w, b, dy, act, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,groups", [((31337, 10, 8), 1), ((1500, 6, 40), 5), ((3, 4, 96), 12), ((611, 16, 64), 64), ((305, 2, 510), 6), ((1, 2, 4), 2)],
+                         ids=str)
+def test_group_norm_small_samples(shape, groups, dtype):
+    """Several samples a block, more of them than the blocks take in one turn, the last turn not full."""
+    x, w, b, dy = tg.draw(shape, dtype, seed=sum(shape))
+    tg.check(x, groups, w, b, dy, "silu", dtype)
+    wide = torch.zeros(shape[:-1] + (shape[-1] + 8,), dtype=x.dtype, device="cuda")
+    wide[..., :shape[-1]] = x
+    wide[..., shape[-1]:] = torch.nan
+    assert torch.equal(sdm.group_norm(wide[..., :shape[-1]], groups, w, b), sdm.group_norm(x, groups, w, b))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_group_norm_of_repeated_positions(dtype):
     """One row for all positions and samples (a stride of zero), and parameters and gradients at odd addresses."""
     x, w, b, dy = tg.draw((3, 50, 64), dtype, seed=49)
