@@ -419,7 +419,7 @@ __device__ __forceinline__ void load_params(const void *p, bool f32, float fill,
 }
 
 // The vectors of the kernels below are parts of a group, or (OWN) groups end inside them: then every channel has a group, a
-// partial and statistics of its own. 4000 x 64 x 128 bfloat16 in 32 groups: @.
+// partial and statistics of its own.
 
 // part [N][splits][G]: mean and sum of squares around it
 template <typename T, int VEC, bool OWN>
@@ -1037,15 +1037,17 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
         constexpr int VEC = decltype(v)::value;
         if (group_rows(s.L, each)) {
             const NormGeom g = norm_geom(each, VEC, true);
-            constexpr int NV = 16 / VEC;
-            const size_t smem = GroupRing<T, VEC, NV, 1, false>::bytes(g.threads);
-            auto go = [&](auto kern) {
+            auto go = [&](auto kern, size_t smem) {
                 group_smem(kern, smem);
                 const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (group_row_threads<T>(g.block, ACT) / g.threads));
                 kern<<<(unsigned)grid, g.threads, smem, st>>>(s, x, g.tpr, y, stats);
             };
-            if (g.block) go(k_group_row<T, VEC, NV, true, ACT>);
-            else go(k_group_row<T, VEC, NV, false, ACT>);
+            // rows of up to 8 elements, a thread each: 8 registers of them, not 16 (116871 x 128 bfloat16 in 16 groups 14 us
+            // forward and 41 backward, 20 and 43 with 16; 120216 x 256 float32 in 32 57 and 132, 75 and 137)
+            constexpr int NV = 16 / VEC, HALF = 8 / VEC;
+            if (g.block) go(k_group_row<T, VEC, NV, true, ACT>, GroupRing<T, VEC, NV, 1, false>::bytes(g.threads));
+            else if (each <= 8) go(k_group_row<T, VEC, HALF, false, ACT>, GroupRing<T, VEC, HALF, 1, false>::bytes(g.threads));
+            else go(k_group_row<T, VEC, NV, false, ACT>, GroupRing<T, VEC, NV, 1, false>::bytes(g.threads));
             return;
         }
         const int cv = s.C / VEC;
@@ -1070,17 +1072,17 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
         constexpr int VEC = decltype(v)::value;
         if (group_rows(s.L, each)) {
             const NormGeom g = norm_geom(each, VEC, true);
-            constexpr int NV = 16 / VEC;
-            const size_t smem = GroupRing<T, VEC, NV, 2, true>::bytes(g.threads);
             const GroupBack to = group_back(g, s.N, s.G, ACT);
             const size_t cols = g.block ? 0 : (size_t)2 * kNormBlock * 16 * 4;
-            auto go = [&](auto kern) {
+            auto go = [&](auto kern, size_t smem) {
                 const size_t bytes = smem > cols ? smem : cols;
                 group_smem(kern, bytes);
                 kern<<<(unsigned)to.blocks, g.threads, bytes, st>>>(s, dy, x, g.tpr, to.same, stats, dx, sums ? part : nullptr);
             };
-            if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>);
-            else go(k_group_row_bwd<T, VEC, NV, false, ACT>);
+            constexpr int NV = 16 / VEC, HALF = 8 / VEC;
+            if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
+            else if (each <= 8) go(k_group_row_bwd<T, VEC, HALF, false, ACT>, GroupRing<T, VEC, HALF, 2, true>::bytes(g.threads));
+            else go(k_group_row_bwd<T, VEC, NV, false, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
             if (sums) chain_launch(Chain::behind, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
             return;
         }
