@@ -139,7 +139,7 @@ size_t linear_saved(const LinearDims &d) { return up(d.segs * (size_t)linear_sta
 
 // q, k, v (and with grad the readings' gradient) as the tensor copies take them; clears the status block
 cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char *ws, const void *const (&src)[4], LinearLaid (&laid)[4],
-                       Chain &chain, cudaStream_t st) {
+                       cudaStream_t st) {
     LinearLay lay[4];
     int n = 0;
     for (int i = 0; i < 4 && src[i]; ++i) {
@@ -150,8 +150,7 @@ cudaError_t linear_lay(const LinearDims &d, const LinearLayout &l, unsigned char
         lay[n++] = LinearLay{src[i], {s[0], s[1], s[2]}, heads, width, ws + l.laid[i]};
         laid[i] = LinearLaid{ws + l.laid[i], {(long long)d.T * heads * width, (long long)heads * width, width}, heads, width};
     }
-    chain = n ? Chain::behind : Chain::alone;
-    return n ? launch_linear_lay(d, lay, n, reinterpret_cast<DevStatus *>(ws), st) : linear_clear(ws, kAlign, st);
+    return launch_linear_lay(d, lay, n, reinterpret_cast<DevStatus *>(ws), st);
 }
 
 LinearOperand operand(const void *p, const long long *s, int share) { return LinearOperand{p, {s[0], s[1], s[2]}, share}; }
@@ -184,14 +183,13 @@ int linear_forward(const sdm_linear_shape *shape, float *state, const void *q, c
     if (rc != SDM_OK) return rc;
     auto ws = static_cast<unsigned char *>(workspace);
     LinearLaid laid[4];
-    Chain chain = Chain::alone;
     cudaError_t e = cudaSuccess;
     if (save && d.segs == 1)
         e = cudaMemcpyAsync(saved, state, (size_t)linear_states(d) * 4, cudaMemcpyDeviceToDevice, st);
-    if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, nullptr}, laid, chain, st);
+    if (e == cudaSuccess) e = linear_lay(d, l, ws, {q, k, v, nullptr}, laid, st);
     float *starts = save ? static_cast<float *>(saved) : reinterpret_cast<float *>(ws + l.starts);
-    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, p, in, laid[1], laid[2], starts, ws, chain, st);
-    if (e == cudaSuccess) e = launch_linear_scan(d, p, in, {laid[0], laid[1], laid[2]}, starts, ws, d.segs > 1 ? Chain::behind : chain, st);
+    if (e == cudaSuccess && d.segs > 1) e = launch_linear_carry(d, p, in, laid[1], laid[2], starts, ws, Chain::behind, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, p, in, {laid[0], laid[1], laid[2]}, starts, ws, Chain::behind, st);
     return linear_status(e);
 }
 
@@ -272,15 +270,14 @@ int sdm_linear_attention_backward(const sdm_linear_shape *shape, const void *q, 
     const LinearPass pk{ov, og, oq, d.Dv, d.Dk, tiles, true, d.scale, 1.f, d.scale, grad_final_state, nullptr, 1, d.Dv, dk, parts};
     const LinearPass pv{ok, oq, og, d.Dk, d.Dv, 1, true, d.scale, 1.f, d.scale, grad_final_state, grad_state, d.Dv, 1, grad_v, false};
     LinearLaid laid[4];
-    Chain chain = Chain::alone;
     const bool cut = d.segs > 1, decay = grad_log_decay != nullptr;
     auto part = reinterpret_cast<double *>(ws + l.decay);
-    cudaError_t e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, chain, st);
+    cudaError_t e = linear_lay(d, l, ws, {q, k, v, grad_readings}, laid, st);
     float *ends = reinterpret_cast<float *>(ws + l.starts);
     // The scans and the decays' gradient need only the segments' ends, and no other launch's results: they run beside each
     // other, as do the carry and dq's scan, and the sums of dq and what comes after them, so that a launch's idle SMs
     // have work (2 x 4096 tokens of 32 heads: 64 heads in two segments leave 24 of 152 idle; training 590 -> 534 us).
-    if (e == cudaSuccess) e = launch_linear_scan(d, pq, in, {laid[3], laid[2], laid[1]}, first, ws, chain, st);
+    if (e == cudaSuccess) e = launch_linear_scan(d, pq, in, {laid[3], laid[2], laid[1]}, first, ws, Chain::behind, st);
     if (e == cudaSuccess && cut) e = launch_linear_carry(d, pv, in, laid[0], laid[3], ends, ws, Chain::beside, st);
     if (e == cudaSuccess) e = launch_linear_scan(d, pk, in, {laid[2], laid[3], laid[0]}, ends, ws, cut ? Chain::behind : Chain::beside, st);
     if (e == cudaSuccess && decay) e = launch_linear_decay(d, in, laid, first, cut ? ends : grad_final_state, part, ws, Chain::beside, st);

@@ -103,7 +103,7 @@ struct LinearLay {
     int heads, width;
     void *dst;
 };
-// n > 0 of them; clears the status block too
+// n of them, or none; clears the status block too
 cudaError_t launch_linear_lay(const LinearDims &d, const LinearLay *lay, int n, DevStatus *status, cudaStream_t st);
 cudaError_t launch_linear_scan(const LinearDims &d, const LinearPass &p, const LinearIn &in, const LinearLaid (&laid)[3], const float *starts,
                                void *status, Chain chain, cudaStream_t st);
