@@ -19,7 +19,7 @@ __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait
 // the next launch may start its blocks as SMs become free
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-enum class Chain { alone, behind, beside };
+enum class Chain { behind, beside };
 // at a kernel's start and end
 __device__ __forceinline__ void chain_begin(Chain c) {
     if (c != Chain::beside) chain_wait();
@@ -30,7 +30,7 @@ __device__ __forceinline__ void chain_end(Chain c) {
 }
 
 template <typename... P, typename... A>
-cudaError_t chain_launch(Chain chain, void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A &&...args) {
+cudaError_t chain_launch(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A &&...args) {
     cudaLaunchAttribute attribute{};
     attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attribute.val.programmaticStreamSerializationAllowed = 1;
@@ -40,7 +40,7 @@ cudaError_t chain_launch(Chain chain, void (*kern)(P...), dim3 grid, unsigned th
     config.dynamicSmemBytes = smem;
     config.stream = st;
     config.attrs = &attribute;
-    config.numAttrs = chain == Chain::alone ? 0 : 1;
+    config.numAttrs = 1;
     return cudaLaunchKernelEx(&config, kern, std::forward<A>(args)...);
 }
 

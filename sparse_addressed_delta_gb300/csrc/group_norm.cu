@@ -1010,8 +1010,8 @@ void group_forward_split(const GroupShape &s, const T *x, T *y, float2 *stats, f
     k_group_stats<T, VEC, OWN><<<grid, kGroupThreads, smem, st>>>(s, x, part);
     float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
     const long long warps = s.N * s.G;
-    chain_launch(Chain::behind, k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
-    chain_launch(Chain::behind, k_group_apply<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
+    chain_launch(k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
+    chain_launch(k_group_apply<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
 }
 
 template <typename T, int VEC, bool OWN, bool ACT>
@@ -1025,8 +1025,8 @@ void group_backward_split(const GroupShape &s, const T *dy, const T *x, const fl
     float2 *split_terms = terms + s.N * s.G;
     k_group_sums<T, VEC, OWN, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
     const int blocks = (int)((s.N * s.G + kGroupTermWarps - 1) / kGroupTermWarps);
-    chain_launch(Chain::behind, k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
-    chain_launch(Chain::behind, k_group_apply_bwd<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
+    chain_launch(k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
+    chain_launch(k_group_apply_bwd<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
 }
 
 // vec: of vectors that are parts of groups; wide: 16-byte vectors that are not would do
@@ -1083,7 +1083,7 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
             if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
             else if (each <= 8) go(k_group_row_bwd<T, VEC, HALF, false, ACT>, GroupRing<T, VEC, HALF, 2, true>::bytes(g.threads));
             else go(k_group_row_bwd<T, VEC, NV, false, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
-            if (sums) chain_launch(Chain::behind, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
+            if (sums) chain_launch(k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
             return;
         }
         const int cv = s.C / VEC;
@@ -1092,7 +1092,7 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
             const long long need = (s.N + samples - 1) / samples, blocks = need < kSmallBlocks ? need : kSmallBlocks;
             k_group_small_bwd<T, VEC, ACT><<<(unsigned)blocks, kGroupThreads, one > two ? one : two, st>>>(s, dy, x, samples, stats, dx, sums ? part : nullptr);
             if (sums)
-                chain_launch(Chain::behind, k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)blocks, s.C, dw, db);
+                chain_launch(k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)blocks, s.C, dw, db);
             return;
         }
         constexpr int V16 = 16 / (int)sizeof(T);

@@ -267,7 +267,7 @@ cudaError_t carry(const LinearDims &d, const CarryArgs &a, const CUtensorMap *m,
     using L = LinCarry<KP, NP>;
     set_kernel_smem(k_linear_carry<KP, NP, REV>, L::BYTES);
     const long long blocks = (long long)d.B * d.H * linear_tiles(a.V) * (d.segs - 1);
-    return chain_launch(chain, k_linear_carry<KP, NP, REV>, (unsigned)blocks, kCarThreads, L::BYTES, st, m[0], m[1], d, a);
+    return chain_launch(k_linear_carry<KP, NP, REV>, (unsigned)blocks, kCarThreads, L::BYTES, st, m[0], m[1], d, a);
 }
 
 }  // namespace
@@ -290,7 +290,7 @@ cudaError_t launch_linear_carry(const LinearDims &d, const LinearPass &p, const 
     else e = p.K > 64 ? go(integral_constant<int, 128>{}, integral_constant<int, 3>{}) : go(integral_constant<int, 64>{}, integral_constant<int, 3>{});
     if (e != cudaSuccess) return e;
     const long long blocks = (linear_states(d) / 4 + 255) / 256;
-    return chain_launch(Chain::behind, k_linear_join, (unsigned)blocks, 256, 0, st, d, in.g, in.valid, p.first, p.reverse, starts);
+    return chain_launch(k_linear_join, (unsigned)blocks, 256, 0, st, d, in.g, in.valid, p.first, p.reverse, starts);
 }
 
 }  // namespace sdm

@@ -343,7 +343,7 @@ template <int NP>
 cudaError_t decay(const LinearDims &d, const DecayArgs &a, const CUtensorMap *m, cudaStream_t st) {
     using L = LinDecay<NP>;
     set_kernel_smem(k_linear_decay<NP>, L::BYTES);
-    return chain_launch(a.chain, k_linear_decay<NP>, (unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
+    return chain_launch(k_linear_decay<NP>, (unsigned)linear_decay_parts(d), kDecThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
 }
 
 }  // namespace
@@ -363,7 +363,7 @@ cudaError_t launch_linear_decay(const LinearDims &d, const LinearIn &in, const L
 }
 
 cudaError_t launch_linear_decay_sum(const LinearDims &d, const double *part, float *grad_decay, Chain chain, cudaStream_t st) {
-    return chain_launch(chain, k_linear_decay_sum, d.H, 32, 0, st, part, d.B, d.H, linear_decay_blocks(d) * linear_tiles(d.Dv) * d.segs, grad_decay, chain);
+    return chain_launch(k_linear_decay_sum, d.H, 32, 0, st, part, d.B, d.H, linear_decay_blocks(d) * linear_tiles(d.Dv) * d.segs, grad_decay, chain);
 }
 
 }  // namespace sdm

@@ -519,7 +519,7 @@ cudaError_t scan(const LinearDims &d, const LinArgs &a, const CUtensorMap *m, Ch
     using L = LinScan<KP, NP>;
     set_kernel_smem(kern, L::BYTES);
     const long long blocks = (long long)d.B * d.H * linear_tiles(a.p.V) * a.p.blocks * d.segs;
-    return chain_launch(chain, kern, (unsigned)blocks, kLinThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
+    return chain_launch(kern, (unsigned)blocks, kLinThreads, L::BYTES, st, m[0], m[1], m[2], m[3], d, a);
 }
 
 template <int KP, int NP>

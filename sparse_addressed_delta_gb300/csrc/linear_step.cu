@@ -160,8 +160,8 @@ cudaError_t launch_linear_sum(const LinearDims &d, const float *part, int blocks
     const long long rows = (long long)d.B * d.T * d.Hk, each = 256 / (width / 4) * kSumRows, grid = (rows + each - 1) / each;
     const int group = d.H / d.Hk;
     if (d.dtype == SDM_BF16)
-        return chain_launch(chain, k_linear_sum<__nv_bfloat16>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<__nv_bfloat16 *>(out), chain);
-    return chain_launch(chain, k_linear_sum<float>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<float *>(out), chain);
+        return chain_launch(k_linear_sum<__nv_bfloat16>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<__nv_bfloat16 *>(out), chain);
+    return chain_launch(k_linear_sum<float>, (unsigned)grid, 256, 0, st, part, rows, group, blocks, width, static_cast<float *>(out), chain);
 }
 
 }  // namespace sdm
