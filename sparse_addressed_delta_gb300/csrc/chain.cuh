@@ -1,6 +1,8 @@
 // Launches of one call that follow each other on a stream: a kernel is launched while the one before it ends (programmatic
 // dependent launch) and waits for its end itself, so its blocks' start is hidden behind it. Only ever behind a kernel
-// of the same call, so that the inputs, which no kernel of the call writes, may be read before the wait.
+// of the same call, so that the inputs, which no kernel of the call writes, may be read before the wait. What the launch
+// before wrote is read behind the wait and never through the read-only path (__ldg): that holds for memory that nobody
+// writes while the reading kernel lives, and a chained kernel lives from before the wait on.
 //
 // A kernel that needs nothing of the one before it, and writes nothing that one reads, runs beside it: its last block waits
 // at its end, so that when it has ended the other has (all blocks would hold their SMs until then). Whatever ended before

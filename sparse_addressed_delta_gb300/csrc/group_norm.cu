@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_join(const __grid_const
     const float c = (float)(s.C / s.G), all = (float)s.L * c;
     const float2 *at = part + i / s.G * s.splits * s.G + i % s.G;
     const float2 a = join_parts<32>(s.splits, all, [&](int k) {
-        const float2 e = __ldg(at + (size_t)k * s.G);
+        const float2 e = __ldcg(at + (size_t)k * s.G);
         return Moments{(float)(s.per + (k < s.more)) * c, e.x, e.y};
     });
     if ((threadIdx.x & 31) == 0) joined[i] = make_float2(a.x, 1.f / sqrtf(a.y / all + s.eps));
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kGroupTermThreads) k_group_terms(const __grid_
     const float2 *at = part + i / s.G * s.splits * s.G + i % s.G;
     float2 a = both(0.f);
 #pragma unroll 4
-    for (int k = threadIdx.x & 31; k < s.splits; k += 32) a = add2(a, __ldg(at + (size_t)k * s.G));
+    for (int k = threadIdx.x & 31; k < s.splits; k += 32) a = add2(a, __ldcg(at + (size_t)k * s.G));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = add2(a, make_float2(__shfl_xor_sync(~0u, a.x, o), __shfl_xor_sync(~0u, a.y, o)));
     const float count = (float)s.L * (float)(s.C / s.G);

@@ -214,7 +214,7 @@ __device__ __forceinline__ void norm_cols(int block, const float *part, int part
     float s = 0.f, low = 0.f;
     if (c < 2 * n)
 #pragma unroll 8
-        for (int p = ty; p < parts; p += kNormColSlices) s = add_exact(s, __ldg(part + (size_t)p * 2 * n + c), low);
+        for (int p = ty; p < parts; p += kNormColSlices) s = add_exact(s, __ldcg(part + (size_t)p * 2 * n + c), low);
     sh[ty][tx] = s;
     lost[ty][tx] = low;
     __syncthreads();
