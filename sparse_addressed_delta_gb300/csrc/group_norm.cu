@@ -418,6 +418,9 @@ __device__ __forceinline__ void load_params(const void *p, bool f32, float fill,
         o[j] = !p ? fill : f32 ? static_cast<const float *>(p)[c0 + j] : to_f32(static_cast<const T *>(p)[c0 + j]);
 }
 
+// The result may be x, or x's gradient y's: what a kernel overwrites itself it reads by plain loads (a read-only
+// one may be moved behind the store), each vector before it stores there and no other thread's.
+
 // The vectors of the kernels below are parts of a group, or (OWN) groups end inside them: then every channel has a group, a
 // partial and statistics of its own.
 
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(kGroupThreads, OWN ? 2 : kGroupSm) k_group_app
 #pragma unroll
         for (int i = 0; i < kGroupBatch; ++i) {
             const long long at = r + (long long)i * sp.slots;
-            if (at < p.to) raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0));
+            if (at < p.to) raw[i] = *reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0);
         }
     };
     for (int cv = cv0; cv < sp.cv; cv += wide) {
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(kGroupThreads, OWN ? 2 : kGroupSm) k_group_app
                 float v[VEC];
                 unpack<T, VEC>(raw[i], v);
                 const long long next = at + (long long)sp.slots * kGroupBatch;
-                if (next < p.to) raw[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + next * s.xs + c0));
+                if (next < p.to) raw[i] = *reinterpret_cast<const Vec<T, VEC> *>(base + next * s.xs + c0);
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
                     float2 z = make_float2(v[j], j + 1 < VEC ? v[j + 1] : 0.f);
@@ -718,8 +721,8 @@ __global__ void __launch_bounds__(kGroupThreads, OWN ? 2 : kGroupSm)
             for (int i = 0; i < BATCH; ++i) {
                 const long long at = r + (long long)i * sp.slots;
                 if (at < p.to) {
-                    rx[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0));
-                    rg[i] = __ldg(reinterpret_cast<const Vec<T, VEC> *>(gbase + at * s.gs + c0));
+                    rx[i] = *reinterpret_cast<const Vec<T, VEC> *>(base + at * s.xs + c0);
+                    rg[i] = *reinterpret_cast<const Vec<T, VEC> *>(gbase + at * s.gs + c0);
                 }
             }
 #pragma unroll
@@ -782,7 +785,7 @@ __global__ void __launch_bounds__(kGroupThreads, 2) k_group_small(const __grid_c
         Vec<T, VEC> raw[kSmallMany];
 #pragma unroll
         for (int k = 0; k < kSmallMany; ++k)
-            raw[k] = m.at[k] >= 0 && m.at[k] < live ? __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + m.from[k])) : Vec<T, VEC>{};
+            raw[k] = m.at[k] >= 0 && m.at[k] < live ? *reinterpret_cast<const Vec<T, VEC> *>(base + m.from[k]) : Vec<T, VEC>{};
 #pragma unroll
         for (int k = 0; k < kSmallMany; ++k) {
             float v[VEC], mean = 0.f, q = 0.f;
@@ -856,8 +859,8 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
             Vec<T, VEC> rx{}, rg{};
             a[k] = both(0.f);
             if (m.at[k] >= 0 && m.at[k] < live) {
-                rx = __ldg(reinterpret_cast<const Vec<T, VEC> *>(base + m.from[k]));
-                rg = __ldg(reinterpret_cast<const Vec<T, VEC> *>(gbase + (i / m.vectors * s.L + v / m.cv) * s.gs + v % m.cv * VEC));
+                rx = *reinterpret_cast<const Vec<T, VEC> *>(base + m.from[k]);
+                rg = *reinterpret_cast<const Vec<T, VEC> *>(gbase + (i / m.vectors * s.L + v / m.cv) * s.gs + v % m.cv * VEC);
                 a[k] = stats[n0 * s.G + m.at[k]];
             }
             unpack<T, VEC>(rx, h[k]);

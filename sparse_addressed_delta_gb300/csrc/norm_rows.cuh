@@ -116,13 +116,13 @@ struct RowRing {
     }
 };
 
-// the thread's pieces of a row (0 past its end), straight to registers
+// the thread's pieces of a row (0 past its end), straight to registers (the row may be the result's: no read-only loads)
 template <typename T, int VEC, int NV>
 __device__ __forceinline__ void load_row(const T *row, int t, int tpr, int n, float *o) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * VEC;
-        const Vec<T, VEC> r = c < n ? __ldg(reinterpret_cast<const Vec<T, VEC> *>(row + c)) : Vec<T, VEC>{};
+        const Vec<T, VEC> r = c < n ? *reinterpret_cast<const Vec<T, VEC> *>(row + c) : Vec<T, VEC>{};
         unpack<T, VEC>(r, o + i * VEC);
     }
 }

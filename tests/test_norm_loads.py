@@ -31,3 +31,9 @@ def test_behind_another_launch(name):
     """These begin while the launch that writes what they read still runs."""
     text = body(name)
     assert "__ldcg(" in text and "__ldg(" not in text
+
+
+@pytest.mark.parametrize("name", ["k_group_apply", "k_group_apply_bwd", "k_group_small", "k_group_small_bwd", "load_row"])
+def test_of_what_the_kernel_may_overwrite(name):
+    """y may be x, and x's gradient y's: such a kernel stores where it has read."""
+    assert "__ldg(" not in body(name)
