@@ -39,6 +39,17 @@ std::atomic<long long> g_wait_limit{kSpinLimit};
 
 long long wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
 
+void raise_kernel_smem(const void *kern, size_t bytes) {
+    static std::mutex mu;
+    auto enough = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kern) == cudaSuccess && (size_t)a.maxDynamicSharedSizeBytes >= bytes;
+    };
+    if (enough()) return;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!enough()) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 int set_error(int code, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);

@@ -446,11 +446,14 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 
 __host__ __device__ __forceinline__ int goff_stride(int CW) { return CW + 4; }
 
-// Dynamic shared memory limit of a kernel (the driver keeps choosing the carveout: forcing the
-// largest one measured slower for the pipelined Phase 2, whose gather uses the L1 that is left)
+// Room for `bytes` of dynamic shared memory in a kernel's limit, which belongs to the kernel and so to every host thread:
+// it is only ever raised, so that no call lowers it between another one's setting of it and that one's launch. (The
+// driver keeps choosing the carveout: forcing the largest one measured slower for the pipelined Phase 2, whose gather
+// uses the L1 that is left.)
+void raise_kernel_smem(const void *kern, size_t bytes);
 template <typename K>
 inline void set_kernel_smem(K kern, size_t bytes) {
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    raise_kernel_smem(reinterpret_cast<const void *>(kern), bytes);
 }
 // a group with at least kHotGroup members is summed by a whole warp in the pipelined DW
 constexpr int kHotGroup = 16;
