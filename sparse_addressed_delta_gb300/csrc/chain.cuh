@@ -43,7 +43,9 @@ cudaError_t chain_launch(void (*kern)(P...), dim3 grid, unsigned threads, size_t
     config.stream = st;
     config.attrs = &attribute;
     config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, kern, std::forward<A>(args)...);
+    const cudaError_t e = cudaLaunchKernelEx(&config, kern, std::forward<A>(args)...);
+    if (e != cudaSuccess) cudaGetLastError();            // returned here, not found again by the next call
+    return e;
 }
 
 }  // namespace sdm

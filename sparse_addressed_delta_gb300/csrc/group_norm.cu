@@ -986,13 +986,15 @@ void group_smem(K kern, size_t bytes) {
     if (bytes > 40 * 1024) set_kernel_smem(kern, bytes);
 }
 
+// The launches below return the first error, and none follows a launch that failed: it would read what that one has not
+// written.
 template <typename T, typename F>
-void group_by_vec(int vec, F f) {
+cudaError_t group_by_vec(int vec, F f) {
     constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
     if (vec == V16) return f(std::integral_constant<int, V16>{});
     if constexpr (V4 > 1)
         if (vec == V4) return f(std::integral_constant<int, V4>{});
-    f(std::integral_constant<int, 1>{});
+    return f(std::integral_constant<int, 1>{});
 }
 
 // Whether channels have statistics of their own, so that the loads are wide: a block's end costs more then, so it pays from 16
@@ -1005,20 +1007,23 @@ bool group_own(const GroupShape &s, int vec) {
 }
 
 template <typename T, int VEC, bool OWN, bool ACT>
-void group_forward_split(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, cudaStream_t st) {
+cudaError_t group_forward_split(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, cudaStream_t st) {
     const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
     const unsigned grid = (unsigned)(s.N * s.splits);
     const size_t smem = (size_t)slots * cv * (OWN ? VEC : 1) * 8;
     group_smem(k_group_stats<T, VEC, OWN>, smem);
     k_group_stats<T, VEC, OWN><<<grid, kGroupThreads, smem, st>>>(s, x, part);
+    cudaError_t e = cudaGetLastError();
     float2 *joined = stats ? stats : part + (size_t)s.N * s.splits * s.G;
     const long long warps = s.N * s.G;
-    chain_launch(k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
-    chain_launch(k_group_apply<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
+    if (e == cudaSuccess)
+        e = chain_launch(k_group_join, (unsigned)((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)), kGroupThreads, 0, st, s, part, joined);
+    if (e == cudaSuccess) e = chain_launch(k_group_apply<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, x, joined, y);
+    return e;
 }
 
 template <typename T, int VEC, bool OWN, bool ACT>
-void group_backward_split(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, float *dw, float *db, float *part, float2 *terms,
+cudaError_t group_backward_split(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, float *dw, float *db, float *part, float2 *terms,
                           cudaStream_t st) {
     const bool sums = dw || db;
     const int cv = s.C / VEC, slots = cv < kGroupThreads ? kGroupThreads / cv : 1;
@@ -1027,16 +1032,19 @@ void group_backward_split(const GroupShape &s, const T *dy, const T *x, const fl
     group_smem(k_group_sums<T, VEC, OWN, ACT>, smem);
     float2 *split_terms = terms + s.N * s.G;
     k_group_sums<T, VEC, OWN, ACT><<<grid, kGroupThreads, smem, st>>>(s, dy, x, stats, sums ? part : nullptr, split_terms);
+    cudaError_t e = cudaGetLastError();
     const int blocks = (int)((s.N * s.G + kGroupTermWarps - 1) / kGroupTermWarps);
-    chain_launch(k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
-    chain_launch(k_group_apply_bwd<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
+    if (e == cudaSuccess)
+        e = chain_launch(k_group_terms, blocks + (sums ? norm_col_blocks(s.C) : 0), kGroupTermThreads, 0, st, s, split_terms, terms, blocks, part, dw, db);
+    if (e == cudaSuccess) e = chain_launch(k_group_apply_bwd<T, VEC, OWN, ACT>, grid, kGroupThreads, 0, st, s, dy, x, stats, terms, dx);
+    return e;
 }
 
 // vec: of vectors that are parts of groups; wide: 16-byte vectors that are not would do
 template <typename T, bool ACT>
-void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, int vec, bool wide, cudaStream_t st) {
+cudaError_t group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 *part, int vec, bool wide, cudaStream_t st) {
     const int each = s.C / s.G;
-    group_by_vec<T>(vec, [&](auto v) {
+    return group_by_vec<T>(vec, [&](auto v) {
         constexpr int VEC = decltype(v)::value;
         if (group_rows(s.L, each)) {
             const NormGeom g = norm_geom(each, VEC, true);
@@ -1044,34 +1052,38 @@ void group_forward(const GroupShape &s, const T *x, T *y, float2 *stats, float2 
                 group_smem(kern, smem);
                 const long long grid = group_grid(s.N * s.G, g.rpb, s.G, (long long)kRefSms * (group_row_threads<T>(g.block, ACT) / g.threads));
                 kern<<<(unsigned)grid, g.threads, smem, st>>>(s, x, g.tpr, y, stats);
+                return cudaGetLastError();
             };
             // rows of up to 8 elements, a thread each: 8 registers of them, not 16 (116871 x 128 bfloat16 in 16 groups 14 us
             // forward and 41 backward, 20 and 43 with 16; 120216 x 256 float32 in 32 57 and 132, 75 and 137)
             constexpr int NV = 16 / VEC, HALF = 8 / VEC;
-            if (g.block) go(k_group_row<T, VEC, NV, true, ACT>, GroupRing<T, VEC, NV, 1, false>::bytes(g.threads));
-            else if (each <= 8) go(k_group_row<T, VEC, HALF, false, ACT>, GroupRing<T, VEC, HALF, 1, false>::bytes(g.threads));
-            else go(k_group_row<T, VEC, NV, false, ACT>, GroupRing<T, VEC, NV, 1, false>::bytes(g.threads));
-            return;
+            if (g.block) return go(k_group_row<T, VEC, NV, true, ACT>, GroupRing<T, VEC, NV, 1, false>::bytes(g.threads));
+            if (each <= 8) return go(k_group_row<T, VEC, HALF, false, ACT>, GroupRing<T, VEC, HALF, 1, false>::bytes(g.threads));
+            return go(k_group_row<T, VEC, NV, false, ACT>, GroupRing<T, VEC, NV, 1, false>::bytes(g.threads));
         }
         const int cv = s.C / VEC;
         if (const int samples = group_small(s.N, s.L, s.C, VEC, kSmallMany)) {
             const size_t smem = (size_t)samples * ((size_t)s.L * cv + s.G) * 8;
             const long long need = (s.N + samples - 1) / samples, most = 2 * kSmallBlocks;
             k_group_small<T, VEC, ACT><<<(unsigned)(need < most ? need : most), kGroupThreads, smem, st>>>(s, x, samples, y, stats);
-            return;
+            return cudaGetLastError();
         }
         constexpr int V16 = 16 / (int)sizeof(T);
-        if (VEC < V16 && wide && group_own(s, V16)) group_forward_split<T, V16, true, ACT>(s, x, y, stats, part, st);
-        else group_forward_split<T, VEC, false, ACT>(s, x, y, stats, part, st);
+        if (VEC < V16 && wide && group_own(s, V16)) return group_forward_split<T, V16, true, ACT>(s, x, y, stats, part, st);
+        return group_forward_split<T, VEC, false, ACT>(s, x, y, stats, part, st);
     });
 }
 
 template <typename T, bool ACT>
-void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, float *dw, float *db, float *part, float2 *terms, int vec,
+cudaError_t group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *stats, T *dx, float *dw, float *db, float *part, float2 *terms, int vec,
                     bool wide, cudaStream_t st) {
     const int each = s.C / s.G;
     const bool sums = dw || db;
-    group_by_vec<T>(vec, [&](auto v) {
+    auto columns = [&](cudaError_t e, long long parts) {
+        if (e != cudaSuccess || !sums) return e;
+        return chain_launch(k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)parts, s.C, dw, db);
+    };
+    return group_by_vec<T>(vec, [&](auto v) {
         constexpr int VEC = decltype(v)::value;
         if (group_rows(s.L, each)) {
             const NormGeom g = norm_geom(each, VEC, true);
@@ -1081,26 +1093,23 @@ void group_backward(const GroupShape &s, const T *dy, const T *x, const float2 *
                 const size_t bytes = smem > cols ? smem : cols;
                 group_smem(kern, bytes);
                 kern<<<(unsigned)to.blocks, g.threads, bytes, st>>>(s, dy, x, g.tpr, to.same, stats, dx, sums ? part : nullptr);
+                return columns(cudaGetLastError(), to.parts);
             };
             constexpr int NV = 16 / VEC, HALF = 8 / VEC;
-            if (g.block) go(k_group_row_bwd<T, VEC, NV, true, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
-            else if (each <= 8) go(k_group_row_bwd<T, VEC, HALF, false, ACT>, GroupRing<T, VEC, HALF, 2, true>::bytes(g.threads));
-            else go(k_group_row_bwd<T, VEC, NV, false, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
-            if (sums) chain_launch(k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)to.parts, s.C, dw, db);
-            return;
+            if (g.block) return go(k_group_row_bwd<T, VEC, NV, true, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
+            if (each <= 8) return go(k_group_row_bwd<T, VEC, HALF, false, ACT>, GroupRing<T, VEC, HALF, 2, true>::bytes(g.threads));
+            return go(k_group_row_bwd<T, VEC, NV, false, ACT>, GroupRing<T, VEC, NV, 2, true>::bytes(g.threads));
         }
         const int cv = s.C / VEC;
         if (const int samples = group_small(s.N, s.L, s.C, VEC, kSmallBack)) {
             const size_t vectors = (size_t)samples * s.L * cv, one = (vectors + (size_t)samples * s.G) * 8, two = vectors * VEC * 8;
             const long long need = (s.N + samples - 1) / samples, blocks = need < kSmallBlocks ? need : kSmallBlocks;
             k_group_small_bwd<T, VEC, ACT><<<(unsigned)blocks, kGroupThreads, one > two ? one : two, st>>>(s, dy, x, samples, stats, dx, sums ? part : nullptr);
-            if (sums)
-                chain_launch(k_norm_cols, norm_col_blocks(s.C), kNormColThreads * kNormColSlices, 0, st, part, (int)blocks, s.C, dw, db);
-            return;
+            return columns(cudaGetLastError(), blocks);
         }
         constexpr int V16 = 16 / (int)sizeof(T);
-        if (VEC < V16 && wide && group_own(s, V16)) group_backward_split<T, V16, true, ACT>(s, dy, x, stats, dx, dw, db, part, terms, st);
-        else group_backward_split<T, VEC, false, ACT>(s, dy, x, stats, dx, dw, db, part, terms, st);
+        if (VEC < V16 && wide && group_own(s, V16)) return group_backward_split<T, V16, true, ACT>(s, dy, x, stats, dx, dw, db, part, terms, st);
+        return group_backward_split<T, VEC, false, ACT>(s, dy, x, stats, dx, dw, db, part, terms, st);
     });
 }
 
@@ -1179,13 +1188,12 @@ int sdm_group_norm(const void *x, long long x_stride, long long N, long long L, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto type, auto act) {
         using T = decltype(type);
-        group_forward<T, decltype(act)::value>(s, static_cast<const T *>(x), static_cast<T *>(y), reinterpret_cast<float2 *>(stats),
+        return group_forward<T, decltype(act)::value>(s, static_cast<const T *>(x), static_cast<T *>(y), reinterpret_cast<float2 *>(stats),
                                                static_cast<float2 *>(workspace), vec, wide, st);
     };
     const bool silu = activation == SDM_ACT_SILU;
-    if (dtype == SDM_BF16) silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});
-    else silu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
-    return group_status(what, cudaGetLastError());
+    if (dtype == SDM_BF16) return group_status(what, silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{}));
+    return group_status(what, silu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{}));
 }
 
 size_t sdm_group_norm_backward_workspace_bytes(long long N, long long L, int C, int G) {
@@ -1222,13 +1230,12 @@ int sdm_group_norm_backward(const void *grad, long long grad_stride, const void 
     auto terms = rows ? nullptr : reinterpret_cast<float2 *>(static_cast<unsigned char *>(workspace) + group_part_bytes(N, L, C, G, true));
     auto go = [&](auto type, auto act) {
         using T = decltype(type);
-        group_backward<T, decltype(act)::value>(s, static_cast<const T *>(grad), static_cast<const T *>(x), reinterpret_cast<const float2 *>(stats),
+        return group_backward<T, decltype(act)::value>(s, static_cast<const T *>(grad), static_cast<const T *>(x), reinterpret_cast<const float2 *>(stats),
                                                 static_cast<T *>(grad_x), grad_weight, grad_bias, part, terms, vec, wide, st);
     };
     const bool silu = activation == SDM_ACT_SILU;
-    if (dtype == SDM_BF16) silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});
-    else silu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
-    return group_status(what, cudaGetLastError());
+    if (dtype == SDM_BF16) return group_status(what, silu ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{}));
+    return group_status(what, silu ? go(float{}, std::true_type{}) : go(float{}, std::false_type{}));
 }
 
 }  // extern "C"

@@ -261,7 +261,7 @@ int norm_status(cudaError_t e) {
 }
 
 template <typename T, int VEC, int E, bool HULL>
-void norm_launch(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
+cudaError_t norm_launch(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
                  const void *b, bool wf32, float eps, T *y, float2 *stats, cudaStream_t st) {
     const size_t smem = kNormStages<T> * RowRing<T, VEC, E / VEC, 1, false, HULL>::stage_bytes(n, g.threads, g.rpb);
     const long long need = (rows + g.rpb - 1) / g.rpb;
@@ -274,35 +274,36 @@ void norm_launch(const NormGeom &g, const T *x, long long xs, long long rows, in
         const long long most = (long long)kRefSms * (per_sm > 1 ? per_sm : 1);
         const unsigned grid = (unsigned)(need < most ? need : most);
         kern<<<grid, g.threads, smem, st>>>(x, xs, rows, n, g.tpr, w, b, wf32, eps, y, stats);
+        return cudaGetLastError();
     };
-    if (g.block) go(k_norm<T, VEC, E / VEC, true, HULL>);
-    else go(k_norm<T, VEC, E / VEC, false, HULL>);
+    if (g.block) return go(k_norm<T, VEC, E / VEC, true, HULL>);
+    return go(k_norm<T, VEC, E / VEC, false, HULL>);
 }
 
 template <typename T>
-void norm_forward(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
+cudaError_t norm_forward(const NormGeom &g, const T *x, long long xs, long long rows, int n, const void *w,
                   const void *b, bool wf32, float eps, T *y, float2 *stats, cudaStream_t st) {
     constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
     auto go = [&](auto vec) {
         constexpr int VEC = decltype(vec)::value;
         auto with = [&](auto hull) {
             constexpr bool HULL = decltype(hull)::value;
-            if (g.e == 32) norm_launch<T, VEC, 32, HULL>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
-            else norm_launch<T, VEC, 16, HULL>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
+            if (g.e == 32) return norm_launch<T, VEC, 32, HULL>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
+            return norm_launch<T, VEC, 16, HULL>(g, x, xs, rows, n, w, b, wf32, eps, y, stats, st);
         };
         // wide rows of bfloat16 pairs fare better by their own pieces (8192 x 8190: 97 us, 117 by hulls)
         if constexpr (VEC < V16)
             if (g.hull && !(VEC == 2 && g.e == 32)) return with(std::true_type{});
-        with(std::false_type{});
+        return with(std::false_type{});
     };
     if (g.vec == V16) return go(std::integral_constant<int, V16>{});
     if constexpr (V4 > 1)
         if (g.vec == V4) return go(std::integral_constant<int, V4>{});
-    go(std::integral_constant<int, 1>{});
+    return go(std::integral_constant<int, 1>{});
 }
 
 template <typename T, int VEC>
-void norm_bwd_launch(const NormGeom &g, int grid, const T *dy, long long ds, const T *x,
+cudaError_t norm_bwd_launch(const NormGeom &g, int grid, const T *dy, long long ds, const T *x,
                      long long xs, long long rows, int n, const void *w, bool wf32,
                      const float2 *stats, T *dx, float *part, cudaStream_t st) {
     constexpr int NV = 16 / VEC;
@@ -310,21 +311,22 @@ void norm_bwd_launch(const NormGeom &g, int grid, const T *dy, long long ds, con
     auto go = [&](auto kern, size_t smem) {
         set_kernel_smem(kern, smem);
         kern<<<grid, g.threads, smem, st>>>(dy, ds, x, xs, rows, n, g.tpr, w, wf32, stats, dx, part);
+        return cudaGetLastError();
     };
     if (n > kNormRegCols) return go(k_norm_bwd<T, VEC, NV, true, true, false>, sums);
     auto with = [&](auto hull) {
         constexpr bool HULL = decltype(hull)::value;
         const size_t ring = kNormStages<T> * RowRing<T, VEC, NV, 2, true, HULL>::stage_bytes(n, g.threads, g.rpb);
-        if (g.block) go(k_norm_bwd<T, VEC, NV, true, false, HULL>, ring);
-        else go(k_norm_bwd<T, VEC, NV, false, false, HULL>, ring > sums ? ring : sums);
+        if (g.block) return go(k_norm_bwd<T, VEC, NV, true, false, HULL>, ring);
+        return go(k_norm_bwd<T, VEC, NV, false, false, HULL>, ring > sums ? ring : sums);
     };
     if constexpr (VEC * sizeof(T) < 16)
         if (g.hull) return with(std::true_type{});
-    with(std::false_type{});
+    return with(std::false_type{});
 }
 
 template <typename T>
-void norm_backward(const NormGeom &g, int grid, const T *dy, long long ds, const T *x, long long xs,
+cudaError_t norm_backward(const NormGeom &g, int grid, const T *dy, long long ds, const T *x, long long xs,
                    long long rows, int n, const void *w, bool wf32, const float2 *stats, T *dx,
                    float *part, cudaStream_t st) {
     constexpr int V16 = 16 / (int)sizeof(T), V4 = 4 / (int)sizeof(T);
@@ -333,7 +335,7 @@ void norm_backward(const NormGeom &g, int grid, const T *dy, long long ds, const
     if constexpr (V4 > 1)
         if (g.vec == V4)
             return norm_bwd_launch<T, V4>(g, grid, dy, ds, x, xs, rows, n, w, wf32, stats, dx, part, st);
-    norm_bwd_launch<T, 1>(g, grid, dy, ds, x, xs, rows, n, w, wf32, stats, dx, part, st);
+    return norm_bwd_launch<T, 1>(g, grid, dy, ds, x, xs, rows, n, w, wf32, stats, dx, part, st);
 }
 
 }  // namespace
@@ -359,12 +361,10 @@ int sdm_layer_norm(const void *x, long long rows, int n, long long x_stride, con
     auto s2 = reinterpret_cast<float2 *>(stats);
     const bool wf32 = weight_dtype == SDM_F32;
     if (dtype == SDM_BF16)
-        norm_forward(g, static_cast<const __nv_bfloat16 *>(x), x_stride, rows, n, weight, bias, wf32,
-                     eps, static_cast<__nv_bfloat16 *>(y), s2, st);
-    else
-        norm_forward(g, static_cast<const float *>(x), x_stride, rows, n, weight, bias, wf32, eps,
-                     static_cast<float *>(y), s2, st);
-    return norm_status(cudaGetLastError());
+        return norm_status(norm_forward(g, static_cast<const __nv_bfloat16 *>(x), x_stride, rows, n, weight, bias, wf32,
+                                        eps, static_cast<__nv_bfloat16 *>(y), s2, st));
+    return norm_status(norm_forward(g, static_cast<const float *>(x), x_stride, rows, n, weight, bias, wf32, eps,
+                                    static_cast<float *>(y), s2, st));
 }
 
 size_t sdm_layer_norm_workspace_bytes(long long rows, int n) {
@@ -404,19 +404,19 @@ int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void 
     float *part = sums ? static_cast<float *>(workspace) : nullptr;
     auto s2 = reinterpret_cast<const float2 *>(stats);
     const bool wf32 = weight_dtype == SDM_F32;
+    cudaError_t e = cudaSuccess;
     if (rows > 0) {
         if (dtype == SDM_BF16)
-            norm_backward(g, grid, static_cast<const __nv_bfloat16 *>(grad), grad_stride,
+            e = norm_backward(g, grid, static_cast<const __nv_bfloat16 *>(grad), grad_stride,
                           static_cast<const __nv_bfloat16 *>(x), x_stride, rows, n, weight, wf32, s2,
                           static_cast<__nv_bfloat16 *>(grad_x), part, st);
         else
-            norm_backward(g, grid, static_cast<const float *>(grad), grad_stride,
+            e = norm_backward(g, grid, static_cast<const float *>(grad), grad_stride,
                           static_cast<const float *>(x), x_stride, rows, n, weight, wf32, s2,
                           static_cast<float *>(grad_x), part, st);
     }
-    if (sums)
-        k_norm_cols<<<(2 * n + kNormColThreads - 1) / kNormColThreads, kNormColThreads * kNormColSlices,
-                      0, st>>>(part, grid, n, grad_weight, grad_bias);
+    if (e != cudaSuccess || !sums) return norm_status(e);   // (the sums would read what was not written)
+    k_norm_cols<<<norm_col_blocks(n), kNormColThreads * kNormColSlices, 0, st>>>(part, grid, n, grad_weight, grad_bias);
     return norm_status(cudaGetLastError());
 }
 
