@@ -577,7 +577,8 @@ int sdm_layer_norm_backward(const void *grad, long long grad_stride, const void 
  *   stats   [N, G, 2] float32 (mean, rstd) for the backward, or NULL; 8-byte aligned
  *   workspace  sdm_group_norm_workspace_bytes(N, L, C, G) bytes, 256-byte aligned; may be NULL for L = 1 and groups of
  *           up to 8192 channels
- * N and L may be 0. Deterministic. */
+ * N and L may be 0. N G and L are below 2^31; N is at most 2^31 - 2^20 for L = 1 and groups of up to 8192 channels, else
+ * 2^23. Deterministic. */
 enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1 };
 size_t sdm_group_norm_workspace_bytes(long long N, long long L, int C, int G);
 int sdm_group_norm(const void *x, long long x_stride, long long N, long long L, int C, int G,

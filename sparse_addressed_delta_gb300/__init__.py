@@ -1225,8 +1225,9 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     statistics of a sample's group over all its positions and C / groups neighbouring channels; then y = z, or with
     ``activation`` "silu" z / (1 + exp(-z)); in float32, rounded once to x's dtype (float32 or bfloat16). weight and
     bias [C], float32 or x's dtype, each optional. The first dimension is the samples': a norm of every token's heads
-    takes [tokens, C] with the heads as groups. Positions may be strided; the result is contiguous. What is allocated
-    here belongs to ``stream`` (None: the current one)."""
+    takes [tokens, C] with the heads as groups (up to 2^31 - 2^20 tokens; samples of several positions, or of groups wider than
+    8192 channels, are up to 2^23). Positions may be strided; the result is contiguous. What is allocated here belongs to
+    ``stream`` (None: the current one)."""
     if stream is not None:
         return _on(stream, group_norm, x, groups, weight, bias, activation=activation, eps=eps, out=out, workspace=workspace)
     if out is None and workspace is None:

@@ -1122,8 +1122,12 @@ int group_check(const char *what, long long N, long long L, int C, int G, long l
         return set_error(SDM_ERR_INVALID, "%s: N and L must be >= 0, C a multiple of G >= 1 and the stride >= 0, got %lld, %lld, %d, %d, %lld",
                          what, N, L, C, G, xs);
     if (C > kGroupMaxCols) return set_error(SDM_ERR_UNSUPPORTED, "%s: at most %d channels, got %d", what, kGroupMaxCols, C);
-    if (N > (1LL << 31) / 256 || L >= (1LL << 31) || N * G >= (1LL << 31))
-        return set_error(SDM_ERR_UNSUPPORTED, "%s: N must be at most 2^23, N G and L below 2^31", what);
+    // Rows in registers count samples in an int and run up to five steps past the last (a step: the rows at once, 5 blocks of
+    // 128 an SM at most); the other forms keep partials of every sample in the workspace.
+    const bool rows = group_rows(L, C / G);
+    if (N && L && (N > (rows ? (1LL << 31) - (1 << 20) : 1LL << 23) || L >= (1LL << 31) || N * G >= (1LL << 31)))
+        return set_error(SDM_ERR_UNSUPPORTED, "%s: N G and L must be below 2^31, N at most 2^31 - 2^20 for one position a sample and groups of up to "
+                         "%d channels, else 2^23, got %lld, %lld, %d", what, kGroupRowCols, N, L, G);
     return SDM_OK;
 }
 
@@ -1141,6 +1145,7 @@ size_t group_part_bytes(long long N, long long L, int C, int G, bool back) {
     return group_up(pieces * (back ? (size_t)2 * C * 4 : (size_t)G * 8) + (back ? 0 : (size_t)N * G * 8));
 }
 size_t group_bytes(long long N, long long L, int C, int G, bool back) {
+    if (N == 0 || L == 0) return kAlign;
     const bool terms = back && !group_rows(L, C / G);
     return group_part_bytes(N, L, C, G, back) + (terms ? group_up((size_t)N * (1 + group_splits(N, L)) * G * 8) : 0) + kAlign;
 }
