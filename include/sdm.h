@@ -599,7 +599,7 @@ int sdm_group_norm_backward(const void *grad, long long grad_stride, const void 
 
 /* Testing aid: the number of polls after which a kernel's bounded wait for its own bulk copies
  * gives up (default 2^22, seconds at most), for calls queued after this one, process-wide;
- * polls < 1 restores the default. A kernel whose wait gives up sets SDM_ERR_TIMEOUT in the
+ * 1: at once, whether or not the copy has landed; polls < 1 restores the default. A kernel whose wait gives up sets SDM_ERR_TIMEOUT in the
  * device status, waits (with the default limit) for the copies it has in flight, and returns
  * early, leaving that call's bank and readings incomplete. Returns the previous limit. The
  * pages have no counterpart: this exists so that the give-up path can be exercised without

@@ -205,8 +205,8 @@ def version() -> str:
 
 def set_wait_limit(polls: int) -> int:
     """Testing aid: the number of polls after which a kernel's bounded wait for its own copies
-    gives up, for calls queued from now on (process-wide; polls < 1 restores the default).
-    Returns the previous limit."""
+    gives up (1: at once, whether or not they have landed), for calls queued from now on
+    (process-wide; polls < 1 restores the default). Returns the previous limit."""
     return int(library().sdm_set_wait_limit(int(polls)))
 
 

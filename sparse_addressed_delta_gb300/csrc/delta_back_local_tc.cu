@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool all = i == B_PL || i == B_D1 || i == B_PA || i == B_S0;
             mbar_init(bar + i, all ? kWarps : i == B_TFREE ? kWarps + 1 : i >= B_BFREE && i < B_PL ? 4 : 1);
         }
-        *dead = 0;
+        *dead = tc_gives_up(d.spin);
         fence_mbar_init();
     }
     if (warp == kWarps) {

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = B_S; i < B_E; ++i) mbar_init(bar + i, kTcWarps / 2);
         for (int i = B_E; i < B_COUNT; ++i) mbar_init(bar + i, i == B_GRAD ? kTcWarps : 1);
-        *dead = SEG && !CARRY && w.status->code != 0;              // an earlier kernel of this call gave up
+        *dead = tc_gives_up(d.spin) || (SEG && !CARRY && w.status->code != 0);   // an earlier kernel of this call gave up
         fence_mbar_init();
     }
     if (warp == kTcWarps) {

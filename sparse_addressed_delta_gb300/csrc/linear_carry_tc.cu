@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kCarThreads, 1)
         if (REV ? tid > 0 : tid < C) weight[REV ? tid - 1 : C - 1 - tid] = a.to * x;
     }
     chain_begin(a.chain);
-    if (tid == 0) *dead = __ldcg(&a.status->code) != 0;            // an earlier kernel of this call gave up
+    if (tid == 0) *dead = tc_gives_up(d.spin) || __ldcg(&a.status->code) != 0;   // an earlier kernel of this call gave up
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         pair[tid] = tid < C ? 0.f : (float)n * x;
     }
     chain_begin(a.chain);
-    if (tid == 0) *dead = __ldcg(&a.status->code) != 0;            // an earlier kernel of this call gave up
+    if (tid == 0) *dead = tc_gives_up(d.spin) || __ldcg(&a.status->code) != 0;   // an earlier kernel of this call gave up
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         *reinterpret_cast<uint4 *>(smem + L::Z + i / (TILE / 16) * L::PLANE + i % (TILE / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     chain_begin(a.chain);
-    if (tid == 0) *dead = __ldcg(&a.status->code) != 0;            // an earlier kernel of this call gave up
+    if (tid == 0) *dead = tc_gives_up(d.spin) || __ldcg(&a.status->code) != 0;   // an earlier kernel of this call gave up
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -431,10 +431,11 @@ __device__ __forceinline__ bool mbar_try_wait(unsigned long long *bar, unsigned 
         : "memory");
     return ok != 0;
 }
-// Waits for the phase of `parity` to complete; false if it did not within `limit` polls.
+// Waits for the phase of `parity` to complete; false from the poll number `limit` on, which looks no more: with a limit of
+// one the wait gives up whether the phase has completed or not (one try_wait may itself wait until it has).
 __device__ __forceinline__ bool mbar_wait_bounded(unsigned long long *bar, unsigned parity,
                                                   long long limit = kSpinLimit) {
-    for (long long it = 0; it < limit; ++it)
+    for (long long it = 1; it < limit; ++it)
         if (mbar_try_wait(bar, parity)) return true;
     return false;
 }

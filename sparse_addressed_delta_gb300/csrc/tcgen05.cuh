@@ -169,11 +169,14 @@ __device__ __forceinline__ bool mbar_test_wait(unsigned long long *bar, unsigned
     return ok != 0;
 }
 
+// What a block's `*dead` begins with: with a limit of one it has given up, whatever its waits' looks find. (Asked in each wait
+// it takes the 16384 tokens below 195 us.)
+__device__ __forceinline__ bool tc_gives_up(long long limit) { return limit < 2; }
 // Waits for a phase of `bar`, at most `limit` polls; gives up at once when another thread of the
 // block has. Returns whether the phase completed.
 __device__ __forceinline__ bool tc_wait(unsigned long long *bar, unsigned parity, volatile int *dead,
                                         long long limit) {
-    // one look first: a try_wait may wait by itself, and a limit of one poll is to give up at once
+    // one look by test_wait first: with try_wait alone linear attention of 16384 tokens takes 198 us for 192
     if (mbar_test_wait(bar, parity)) return true;
     for (long long i = 1; i < limit; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
