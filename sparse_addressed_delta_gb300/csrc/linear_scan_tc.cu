@@ -197,71 +197,65 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         int unit0, unit1;
         {
             constexpr int UNITS = 2 * KP / 8;                      // 32 or 16
-            {
-                // warps of lanes 64..: 3 of each 4; without pairs: 3; off the diagonal: 1; on it: none
-                const bool other = (warp & 3) >= 2;
-                const int none = REV ? (warp & 3) == 0 && part >= 2 : (warp & 3) == 1 && part < 2;
-                const int off = REV ? (warp & 3) == 1 && part < 2 : (warp & 3) == 0 && part >= 2;
-                const int at_other = part * 2 + (warp & 1), at_rest = part & 1;
-                const int from = other ? 3 * at_other : none ? 24 + 3 * at_rest : off ? 30 + at_rest : 32, many = other || none ? 3 : off ? 1 : 0;
-                unit0 = from * UNITS / 32;
-                unit1 = (from + many) * UNITS / 32;
-            }
+            // warps of lanes 64..: 3 of each 4; without pairs: 3; off the diagonal: 1; on it: none
+            const bool other = (warp & 3) >= 2;
+            const int none = REV ? (warp & 3) == 0 && part >= 2 : (warp & 3) == 1 && part < 2;
+            const int off = REV ? (warp & 3) == 1 && part < 2 : (warp & 3) == 0 && part >= 2;
+            const int at_other = part * 2 + (warp & 1), at_rest = part & 1;
+            const int from = other ? 3 * at_other : none ? 24 + 3 * at_rest : off ? 30 + at_rest : 32, many = other || none ? 3 : off ? 1 : 0;
+            unit0 = from * UNITS / 32;
+            unit1 = (from + many) * UNITS / 32;
         }
         auto local = [&](int it) {
             const int n = chunk_at(it), nt = ntok - n * C < C ? ntok - n * C : C;
             if (!tc_warp_wait(bar + B_FULL + it % ST, it / ST & 1, dead, d.spin)) return false;
-            {
-                const unsigned char *src = smem + it % ST * L::STAGE + L::K;
-                auto one = [&](int i) {
-                    const int row = 32 * (i & 1) + lane, piece = i >> 1, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
-                    const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
-                    float2 x[4];
-                    load_piece<NP, KT * TILE>(src + off, x);
-                    scale_piece(x, w, smem + L::KX + off, L::PLANE);
-                };
-                if (unit1 - unit0 == 3) {                          // side by side: one takes 500 cycles by itself
+            const unsigned char *src = smem + it % ST * L::STAGE + L::K;
+            auto one = [&](int i) {
+                const int row = 32 * (i & 1) + lane, piece = i >> 1, off = (piece >> 3) * TILE + tc_at(row, piece & 7);
+                const float w = row < nt ? p.to * pw[REV ? row + 1 : nt - 1 - row] : 0.f;
+                float2 x[4];
+                load_piece<NP, KT * TILE>(src + off, x);
+                scale_piece(x, w, smem + L::KX + off, L::PLANE);
+            };
+            if (unit1 - unit0 == 3) {                          // side by side: one takes 500 cycles by itself
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) one(unit0 + i);
-                } else {
-                    for (int i = unit0; i < unit1; ++i) one(i);
-                }
+                for (int i = 0; i < 3; ++i) one(unit0 + i);
+            } else {
+                for (int i = unit0; i < unit1; ++i) one(i);
             }
             if ((warp & 3) < 2 && ahead >= -46) {
                 if (!tc_warp_wait(bar + B_P, it & 1, dead, d.spin)) return false;
                 tc_fence_after();
-                {
-                    const int row = lane0 + lane;
-                    float2 x[8];
-                    tc_load16(at + L::P + 16 * part, reinterpret_cast<float(&)[16]>(x));
-                    if (ahead >= 0) {                              // e^{L apart} = e^{L least} e^{L rest}, all of it before the diagonal
-                        const float w = pair[C + (REV ? row - 16 * part - 15 : 16 * part - row)];
+                const int row = lane0 + lane;
+                float2 x[8];
+                tc_load16(at + L::P + 16 * part, reinterpret_cast<float(&)[16]>(x));
+                if (ahead >= 0) {                              // e^{L apart} = e^{L least} e^{L rest}, all of it before the diagonal
+                    const float w = pair[C + (REV ? row - 16 * part - 15 : 16 * part - row)];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            x[i] = mul2(mul2(x[i], make_float2(w, w)), REV ? make_float2(pw[15 - 2 * i], pw[14 - 2 * i]) : make_float2(pw[2 * i], pw[2 * i + 1]));
-                    } else {
-                        const int apart = REV ? row - 16 * part : 16 * part - row;   // of column 0; the others' step by step
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = mul2(mul2(x[i], make_float2(w, w)), REV ? make_float2(pw[15 - 2 * i], pw[14 - 2 * i]) : make_float2(pw[2 * i], pw[2 * i + 1]));
+                } else {
+                    const int apart = REV ? row - 16 * part : 16 * part - row;   // of column 0; the others' step by step
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int a0 = REV ? apart - 2 * i : apart + 2 * i, a1 = REV ? a0 - 1 : a0 + 1;
-                            const float2 y = mul2(x[i], make_float2(pair[C + a0], pair[C + a1]));
-                            x[i] = make_float2(a0 >= 0 ? y.x : 0.f, a1 >= 0 ? y.y : 0.f);   // (a NaN past the diagonal stays out)
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        const int a0 = REV ? apart - 2 * i : apart + 2 * i, a1 = REV ? a0 - 1 : a0 + 1;
+                        const float2 y = mul2(x[i], make_float2(pair[C + a0], pair[C + a1]));
+                        x[i] = make_float2(a0 >= 0 ? y.x : 0.f, a1 >= 0 ? y.y : 0.f);   // (a NaN past the diagonal stays out)
                     }
-                    unsigned pl[3][8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        unsigned s[3];
-                        split3(x[e].x, x[e].y, s);
-                        pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
-                    }
-#pragma unroll
-                    for (int m = 0; m < 3; ++m)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            *reinterpret_cast<uint4 *>(smem + L::Z + m * L::PLANE + tc_at(row, 2 * part + c)) =
-                                make_uint4(pl[m][4 * c], pl[m][4 * c + 1], pl[m][4 * c + 2], pl[m][4 * c + 3]);
                 }
+                unsigned pl[3][8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    unsigned s[3];
+                    split3(x[e].x, x[e].y, s);
+                    pl[0][e] = s[0]; pl[1][e] = s[1]; pl[2][e] = s[2];
+                }
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<uint4 *>(smem + L::Z + m * L::PLANE + tc_at(row, 2 * part + c)) =
+                            make_uint4(pl[m][4 * c], pl[m][4 * c + 1], pl[m][4 * c + 2], pl[m][4 * c + 3]);
             }
             fence_proxy_async_smem();
             arrive(B_ZK);
@@ -298,57 +292,55 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             arrive(B_UF);
             if (it + 1 < nch && !(ok = local(it + 1))) break;
-            {
-                ok = tc_warp_wait(bar + B_O, par, dead, d.spin);
-                if (!ok) break;
-                tc_fence_after();
-                if constexpr (sizeof(OT) == 2) {
-                    // in the place of the chunk's V, which warp 18 stores
-                    unsigned char *to = smem + it % ST * L::STAGE + L::V;
-                    float y[2][8], z[2][8];                        // 16 lanes of columns each
-                    tc_load_frag16(at + L::OA + 16 * part, at + L::OB + 16 * part, y[0], z[0]);
-                    tc_load_frag16(at + (16u << 16) + L::OA + 16 * part, at + (16u << 16) + L::OB + 16 * part, y[1], z[1]);
-                    arrive(B_OF);
+            ok = tc_warp_wait(bar + B_O, par, dead, d.spin);
+            if (!ok) break;
+            tc_fence_after();
+            if constexpr (sizeof(OT) == 2) {
+                // in the place of the chunk's V, which warp 18 stores
+                unsigned char *to = smem + it % ST * L::STAGE + L::V;
+                float y[2][8], z[2][8];                        // 16 lanes of columns each
+                tc_load_frag16(at + L::OA + 16 * part, at + L::OB + 16 * part, y[0], z[0]);
+                tc_load_frag16(at + (16u << 16) + L::OA + 16 * part, at + (16u << 16) + L::OB + 16 * part, y[1], z[1]);
+                arrive(B_OF);
 #pragma unroll
-                    for (int l = 0; l < 2; ++l) {
-                        if (nt == C) {
+                for (int l = 0; l < 2; ++l) {
+                    if (nt == C) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) z[l][i] = fmaf(reads[(i >> 2) * 2 + (i & 1)], y[l][i], z[l][i]);
-                        } else {
+                        for (int i = 0; i < 8; ++i) z[l][i] = fmaf(reads[(i >> 2) * 2 + (i & 1)], y[l][i], z[l][i]);
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int t = 16 * part + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
-                                z[l][i] = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[l][i], z[l][i]) : 0.f;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const int t = 16 * part + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                            z[l][i] = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[l][i], z[l][i]) : 0.f;
                         }
-                        unsigned r[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[l][2 * i], z[l][2 * i + 1]);
-                        const int c = ocol + 2 * l;
-                        stsm4t(smem_u32(to) + (c >> 3) * TILE + tc_at(orow, c & 7), r);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar + B_OUT);
-                } else {
-                    float x[16], y[16];
-                    tc_load16(at + L::OA + 16 * part, y);
-                    tc_load16(at + L::OB + 16 * part, x);
-                    arrive(B_OF);
-                    float *out = static_cast<float *>(p.out) + ((((long long)kb * d.B + b) * d.T + n * C + 16 * part) * d.H + h) * p.V + col;
-                    const int left = d.T - n * C - 16 * part;
+                    unsigned r[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int t = 16 * part + i;
-                        const float r = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[i], x[i]) : 0.f;
-                        if (mine && i < left) *out = r;
-                        out += (long long)d.H * p.V;
-                    }
+                    for (int i = 0; i < 4; ++i) r[i] = pack_bf16(z[l][2 * i], z[l][2 * i + 1]);
+                    const int c = ocol + 2 * l;
+                    stsm4t(smem_u32(to) + (c >> 3) * TILE + tc_at(orow, c & 7), r);
                 }
-                if (it + 1 < nch) {
-                    planes_of_s();
-                    arrive(B_S);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + B_OUT);
+            } else {
+                float x[16], y[16];
+                tc_load16(at + L::OA + 16 * part, y);
+                tc_load16(at + L::OB + 16 * part, x);
+                arrive(B_OF);
+                float *out = static_cast<float *>(p.out) + ((((long long)kb * d.B + b) * d.T + n * C + 16 * part) * d.H + h) * p.V + col;
+                const int left = d.T - n * C - 16 * part;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int t = 16 * part + i;
+                    const float r = t < nt ? fmaf(p.from * pw[REV ? nt - 1 - t : t + 1], y[i], x[i]) : 0.f;
+                    if (mine && i < left) *out = r;
+                    out += (long long)d.H * p.V;
                 }
+            }
+            if (it + 1 < nch) {
+                planes_of_s();
+                arrive(B_S);
             }
         }
         reinterpret_cast<int *>(smem + L::BAD)[part * 128 + lane0 + lane] = first;
@@ -398,29 +390,27 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         add = true;
                     }
             tc_commit_to(one, bar + B_U);
-            {
-                if (ST > 1 && it + 1 < nch) {
-                    ok = tc_warp_wait(bar + B_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(it + 1);
-                }
-                ok = tc_warp_wait(bar + B_S, par, dead, d.spin);
+            if (ST > 1 && it + 1 < nch) {
+                ok = tc_warp_wait(bar + B_FULL + (it + 1) % ST, (it + 1) / ST & 1, dead, d.spin);
                 if (!ok) break;
                 tc_fence_after();
-                add = false;
-#pragma unroll
-                for (int sum = 2; sum >= 0; --sum)
-#pragma unroll
-                    for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
-#pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            tc_mma_ts(one, tu + L::OA, tu + L::SP + (sum - m) * (KP / 2) + 8 * ks,
-                                      qd + (m * KT * TILE + (ks >> 2) * TILE + 32 * (ks & 3)) / 16, tc_idesc<false>(C), add);
-                            add = true;
-                        }
-                tc_commit_to(one, bar + B_O);
+                scores(it + 1);
             }
+            ok = tc_warp_wait(bar + B_S, par, dead, d.spin);
+            if (!ok) break;
+            tc_fence_after();
+            add = false;
+#pragma unroll
+            for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                for (int m = sum < NP - 1 ? sum : NP - 1; m >= 0; --m)
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        tc_mma_ts(one, tu + L::OA, tu + L::SP + (sum - m) * (KP / 2) + 8 * ks,
+                                  qd + (m * KT * TILE + (ks >> 2) * TILE + 32 * (ks & 3)) / 16, tc_idesc<false>(C), add);
+                        add = true;
+                    }
+            tc_commit_to(one, bar + B_O);
             tc_commit_to(one, bar + B_EMPTY + it % ST);
             if (ST == 1 && it + 1 < nch) {
                 ok = tc_warp_wait(bar + B_FULL, (it + 1) & 1, dead, d.spin);
@@ -479,30 +469,28 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (warp == kLinWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
     chain_end(a.chain);
     if (*dead) return;
-    {
-        if (bad && a.column) {
-            const int *at = reinterpret_cast<int *>(smem + L::BAD);
-            const float *begin = d.segs > 1 ? a.starts + seg * states : p.first;
-            for (int c = warp; c < 128; c += kLinThreads / 32) {
-                const int n = at[c], col = v0 + c;
-                // a value's NaN leaves no row of the update finite
-                if (n < 0 || col >= p.V || at[128 + c] != n || at[256 + c] != n || at[384 + c] != n) continue;
-                const int t1 = (n0 + n) * C, t2 = t1 + C < ntok ? t1 + C : ntok;
-                using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
-                linear_column<IT>(d, p, linear_power(a.g[h], 1), b, h, col, n0 * C, t1, t2, begin ? begin + own + col * p.sv : nullptr);
-            }
-            __syncthreads();
+    if (bad && a.column) {
+        const int *at = reinterpret_cast<int *>(smem + L::BAD);
+        const float *begin = d.segs > 1 ? a.starts + seg * states : p.first;
+        for (int c = warp; c < 128; c += kLinThreads / 32) {
+            const int n = at[c], col = v0 + c;
+            // a value's NaN leaves no row of the update finite
+            if (n < 0 || col >= p.V || at[128 + c] != n || at[256 + c] != n || at[384 + c] != n) continue;
+            const int t1 = (n0 + n) * C, t2 = t1 + C < ntok ? t1 + C : ntok;
+            using IT = std::conditional_t<NP == 1, __nv_bfloat16, float>;
+            linear_column<IT>(d, p, linear_power(a.g[h], 1), b, h, col, n0 * C, t1, t2, begin ? begin + own + col * p.sv : nullptr);
         }
-        // Results behind the last chunk are 0: 16 bytes a thread, by all the sequence's segments in turn (one value a
-        // thread by its last one: 4 of the 14 us of two sequences of up to 1003 tokens).
-        constexpr int PIECE = 16 / (int)sizeof(OT);
-        const int pieces = (p.V - v0 < 128 ? p.V - v0 : 128) / PIECE, rows = kLinThreads / pieces, row = tid / pieces;
-        const long long step = (long long)d.H * p.V;
-        OT *out = static_cast<OT *>(p.out) + (((long long)kb * d.B + b) * d.T * d.H + h) * p.V + v0 + tid % pieces * PIECE;
-        if (row < rows)
-            for (long long t = (long long)chunks * C + (long long)seg * rows + row; t < d.T; t += (long long)rows * d.segs)
-                *reinterpret_cast<uint4 *>(out + t * step) = make_uint4(0, 0, 0, 0);
+        __syncthreads();
     }
+    // Results behind the last chunk are 0: 16 bytes a thread, by all the sequence's segments in turn (one value a
+    // thread by its last one: 4 of the 14 us of two sequences of up to 1003 tokens).
+    constexpr int PIECE = 16 / (int)sizeof(OT);
+    const int pieces = (p.V - v0 < 128 ? p.V - v0 : 128) / PIECE, rows = kLinThreads / pieces, row = tid / pieces;
+    const long long step = (long long)d.H * p.V;
+    OT *out = static_cast<OT *>(p.out) + (((long long)kb * d.B + b) * d.T * d.H + h) * p.V + v0 + tid % pieces * PIECE;
+    if (row < rows)
+        for (long long t = (long long)chunks * C + (long long)seg * rows + row; t < d.T; t += (long long)rows * d.segs)
+            *reinterpret_cast<uint4 *>(out + t * step) = make_uint4(0, 0, 0, 0);
     float *end = seg + 1 == d.segs ? p.last : nullptr;
     if (warp < kLinWarps && end) {
         const int kk = (warp >> 2) * HD, col = v0 + 32 * (warp & 3) + lane;
