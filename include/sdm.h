@@ -481,8 +481,8 @@ int sdm_gated_delta_backward(const sdm_delta_shape *shape, const void *q, const 
  * decays by the head's own factor at every token, the key writes its value, the query reads:
  *     S = exp(g) S + k v^T;  o = scale S^T q
  *   B  sequences, T  tokens (both may be 0), H  value heads, Hk  key heads (H a multiple of Hk: value head h
- *   reads key head h / (H / Hk)); Dk, Dv  head widths, multiples of 16, Dk up to 128 and Dv up to 512; dtype SDM_F32 or SDM_BF16 of q, k, v, the readings and their gradients; the state and the decays
- *   are float32. Strides are in elements, for (sequence, token, head); the last dimension is contiguous.
+ *   reads key head h / (H / Hk)); Dk, Dv  head widths, multiples of 16, Dk up to 128 and Dv up to 512; dtype SDM_F32 or
+ *   SDM_BF16 of q, k, v, the readings and their gradients; the state and the decays are float32. Strides are in elements, for (sequence, token, head); the last dimension is contiguous.
  *   Strides must be multiples of 16 bytes, addresses 16-byte aligned; a stride of 0 (a broadcast input) is fine.
  *
  *   state        [B, H, Dk, Dv] float32, advanced in place
@@ -529,7 +529,7 @@ int sdm_linear_attention_save(const sdm_linear_shape *shape, float *state, const
  *                     grad_final_state itself)
  *   grad_q, grad_k    [B, T, Hk, Dk] dtype, heads that share a key head added in float32 in head order
  *   grad_v            [B, T, H, Dv] dtype
- *   grad_log_decay    [H] float32, summed over the sequences in order; NULL where the decays are fixed
+ *   grad_log_decay    [H] float32, summed over the sequences in a fixed order; NULL where the decays are fixed
  * all contiguous and written whole. workspace: sdm_linear_attention_backward_workspace_bytes(shape) bytes,
  * 256-byte aligned. */
 size_t sdm_linear_attention_backward_workspace_bytes(const sdm_linear_shape *shape);

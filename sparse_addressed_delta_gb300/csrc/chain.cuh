@@ -7,7 +7,8 @@
 // A kernel that needs nothing of the one before it, and writes nothing that one reads, runs beside it: its last block waits
 // at its end, so that when it has ended the other has (all blocks would hold their SMs until then). Whatever ended before
 // the other passed its own wait at its start, or before a chain of such kernels began, has ended for it too, as nobody
-// lets the next launch start before that; it reads what those wrote past L1 (__ldcg).
+// lets the next launch start before that; it reads what those wrote past L1 (__ldcg, tensor copies). Documented is what the
+// launch that waits sees; for the one beside it this rests on an ended launch's writes being in L2, where it reads them.
 #pragma once
 
 #include <utility>

@@ -949,9 +949,9 @@ long long group_grid(long long rows, int rpb, int G, long long most) {
     return unit * (need < fit ? need : fit > 1 ? fit : 1);
 }
 
-// Rows in registers wherever they fit: 32768 x 4096 bfloat16 of 32 groups with silu 89 us forward and 75 backward (the split
-// form, one position a block: 1056 and 1130), 1024 x 8192 of 8 10 and 33 (64 and 82). The registers end at 8192 columns
-// (512 threads of 16 elements).
+// Rows in registers wherever they fit: 32768 x 4096 bfloat16 of 32 groups with silu 87 us forward and 136 backward (the split
+// form, one position a block: 365 and 464), half as many 46 and 72 (188 and 242), 1024 x 8192 of 8 10 and 32 (31 and 80). The
+// registers end at 8192 columns (512 threads of 16 elements).
 bool group_rows(long long L, int each) { return L == 1 && each <= kGroupRowCols; }
 // Samples that a block of `many` vectors a thread takes whole, in one launch; 0: they are too large. Wherever they fit,
 // forward and backward: 31337 x 10 x 8 bfloat16 15 and 17 us (split, a block a sample: 754 and 482), 1000 x 8 x 512 15 and 18

@@ -13,8 +13,10 @@
 namespace sdm {
 
 constexpr int kLinearMaxDk = 128, kLinearMaxDv = 512;
-// Up to this many tokens go one by one. 8 tokens so and 9 in a chunk (128 x 128 bfloat16): 16 heads 5.4 and 12.5 us, 256
-// 11.8 and 20.9, 2048 101 and 130 (7 us a token more: they cross at 12); float32, 16 heads 5.2 and 18.7.
+// Up to this many tokens go one by one. 12 tokens so and 13 in a chunk (128 x 128 bfloat16, in a graph): 2048 heads 135 and 133
+// us (7.8 us a token more), 256 heads 15.2 and 19.0 (0.84 more), 16 heads 7.1 and 10.1 (0.4 more); float32, 16 heads 7.0 and
+// 13.9. By the number of tokens alone, so that a sequence's results do not go by the batch it stands in: few heads would
+// cross at 17 to 19 tokens.
 constexpr int kLinearStepTokens = 12;
 // A log-decay below this is taken as this: exp(-110) is 0 in float32, so the state is forgotten whole, and
 // -inf (a hard reset at every token) has no 0 x inf among its powers.
